@@ -44,6 +44,9 @@ EXPORTED_SYMBOLS = (
 RMSNORM_EXPORTED_SYMBOLS = ("bi_rmsnorm_create", "bi_rmsnorm_run", "bi_rmsnorm_get_config", "bi_rmsnorm_destroy")
 # every symbol include/bi_prenorm.h declares
 PRENORM_EXPORTED_SYMBOLS = ("bi_prenorm_create", "bi_prenorm_run", "bi_prenorm_get_config", "bi_prenorm_destroy")
+# every symbol include/bi_qkrope.h declares
+QKROPE_EXPORTED_SYMBOLS = ("bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",
+                           "bi_qkrope_destroy")
 # every symbol include/bi_attention.h declares
 ATTENTION_EXPORTED_SYMBOLS = ("bi_attention_create", "bi_attention_run", "bi_attention_workspace_size",
                               "bi_attention_get_device_error", "bi_attention_get_config", "bi_attention_destroy")
@@ -84,6 +87,11 @@ class bi_attention_config(ctypes.Structure):
                                               "ring_stages")]
 
 
+class bi_qkrope_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "page_size", "rot_dim",
+                                              "interleaved", "threads", "tokens_per_block")]
+
+
 class bi_prenorm_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("K", "N", "chunk", "splits", "tile_rows")]
 
@@ -122,10 +130,15 @@ def _load() -> ctypes.CDLL:
     L.bi_prenorm_run.argtypes = [P, P, I64, P, P, P]
     L.bi_prenorm_get_config.argtypes = [P, ctypes.POINTER(bi_prenorm_config)]
     L.bi_prenorm_destroy.argtypes = [P]
+    L.bi_qkrope_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, I64, ctypes.c_int32, ctypes.c_float]
+    L.bi_qkrope_run.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, P, P, I64, P, I64, I64, P, P]
+    L.bi_qkrope_get_device_error.argtypes = [P, P]
+    L.bi_qkrope_get_config.argtypes = [P, ctypes.POINTER(bi_qkrope_config)]
+    L.bi_qkrope_destroy.argtypes = [P]
     for n in ("bi_gemm_create", "bi_gemm_create_ex", "bi_gemm_run", "bi_gemm_run_noalloc", "bi_gemm_run_gathered",
               "bi_gemm_get_device_error",
               "bi_gemm_destroy", "bi_gemm_get_config", "bi_gemm_workspace_size", "bi_gemm_version") + \
-            RMSNORM_EXPORTED_SYMBOLS + ATTENTION_EXPORTED_SYMBOLS + PRENORM_EXPORTED_SYMBOLS:
+            RMSNORM_EXPORTED_SYMBOLS + ATTENTION_EXPORTED_SYMBOLS + PRENORM_EXPORTED_SYMBOLS + QKROPE_EXPORTED_SYMBOLS:
         getattr(L, n).restype = I32
     return L
 
@@ -270,6 +283,41 @@ def bi_attention_get_device_error(h: int, stream: int = 0) -> int:
 
 def bi_attention_destroy(h: int) -> None:
     _check(library().bi_attention_destroy(ctypes.c_void_p(h)), "bi_attention_destroy")
+
+
+def bi_qkrope_create(num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, rot_dim: int,
+                     interleaved: bool, eps: float) -> int:
+    """Returns the handle (an opaque integer); raises BiGemmError on refusal."""
+    h = ctypes.c_void_p()
+    _check(library().bi_qkrope_create(ctypes.byref(h), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                      int(page_size), int(rot_dim), int(bool(interleaved)), float(eps)),
+           "bi_qkrope_create")
+    return h.value
+
+
+def bi_qkrope_run(h: int, qkv: int, T: int, qkv_stride: int, gq: int | None, gk: int | None, cos_sin: int,
+                  num_positions: int, q_seq: int, q_pos: int, k_cache: int, v_cache: int, num_pages: int,
+                  page_table: int, num_seqs: int, max_pages: int, q_out: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    V = ctypes.c_void_p
+    rc = library().bi_qkrope_run(V(h), V(qkv), int(T), int(qkv_stride), V(gq), V(gk), V(cos_sin), int(num_positions),
+                                 V(q_seq), V(q_pos), V(k_cache), V(v_cache), int(num_pages), V(page_table),
+                                 int(num_seqs), int(max_pages), V(q_out), V(stream))
+    _check(rc, "bi_qkrope_run")
+
+
+def bi_qkrope_get_device_error(h: int, stream: int = 0) -> int:
+    return library().bi_qkrope_get_device_error(ctypes.c_void_p(h), ctypes.c_void_p(stream))
+
+
+def bi_qkrope_get_config(h: int) -> dict:
+    c = bi_qkrope_config()
+    _check(library().bi_qkrope_get_config(ctypes.c_void_p(h), ctypes.byref(c)), "bi_qkrope_get_config")
+    return {n: getattr(c, n) for n, _ in bi_qkrope_config._fields_}
+
+
+def bi_qkrope_destroy(h: int) -> None:
+    _check(library().bi_qkrope_destroy(ctypes.c_void_p(h)), "bi_qkrope_destroy")
 
 
 def bi_prenorm_create(K: int, N: int, eps: float, chunk: int = 0) -> int:
@@ -534,6 +582,101 @@ class BiAttention:
             pass
 
 
+def _check_cache(k_cache, v_cache, page_table, page_size: int, Hkv: int, D: int, dev) -> None:
+    """The paged cache of one layer: k_cache, v_cache [pages, page_size, Hkv, D] bf16, page_table
+    [num_seqs, max_pages] int32, all contiguous on `dev`."""
+    import torch
+    if k_cache.dim() != 4 or tuple(k_cache.shape[1:]) != (page_size, Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache, v_cache must be [pages, page_size, num_kv_heads, head_dim]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [num_seqs, max_pages]")
+    for name, tns, dt in (("k_cache", k_cache, torch.bfloat16), ("v_cache", v_cache, torch.bfloat16),
+                          ("page_table", page_table, torch.int32)):
+        if tns.dtype != dt or not tns.is_contiguous() or tns.device != dev:
+            raise ValueError(f"{name} must be a contiguous {dt} tensor on {dev}")
+
+
+def _check_int32(dev, shape, **tensors) -> None:
+    import torch
+    for name, tns in tensors.items():
+        if tns.dtype != torch.int32 or not tns.is_contiguous() or tns.device != dev or tuple(tns.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
+
+
+class BiQkRope:
+    """Per-head RMSNorm of queries and keys, rotation by position and append to the paged cache
+    in one pass, on torch tensors (include/bi_qkrope.h has the definition and the conventions).
+
+    qkv [T, (Hq + 2 Hkv) D] bf16 (rows may be strided); gq, gk [D] bf16, or both None for no norm;
+    cos_sin [positions, rot_dim] fp32, the cosines of a position's rot_dim / 2 angles, then their
+    sines; q_seq, q_pos int32 [T] (request and position of each token); caches and page table as in
+    BiAttention.  Returns q [T, Hq, D]; keys and values go to their slots of the caches.
+    """
+
+    def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, rot_dim: int | None = None,
+                 eps: float = 1e-6, interleaved: bool = False):
+        self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
+        self.rot_dim = int(rot_dim) if rot_dim is not None else self.D
+        self.handle = bi_qkrope_create(self.Hq, self.Hkv, self.D, self.page_size, self.rot_dim, interleaved, eps)
+
+    @property
+    def config(self) -> dict:
+        return bi_qkrope_get_config(self.handle)
+
+    def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
+        import torch
+        dev = qkv.device
+        T, width = int(qkv.shape[0]), (self.Hq + 2 * self.Hkv) * self.D
+        if qkv.dim() != 2 or qkv.shape[1] != width or qkv.dtype != torch.bfloat16 or not qkv.is_cuda:
+            raise ValueError("qkv must be a bf16 CUDA tensor [T, (num_q_heads + 2 num_kv_heads) head_dim]")
+        if qkv.stride(1) != 1 or (T > 1 and qkv.stride(0) < width):
+            raise ValueError("qkv rows must be contiguous and must not overlap")
+        if (gq is None) != (gk is None):
+            raise ValueError("gq and gk: both norm weights or neither")
+        for name, g in (("gq", gq), ("gk", gk)):
+            if g is not None and (tuple(g.shape) != (self.D,) or g.dtype != torch.bfloat16 or g.device != dev or
+                                  not g.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous bf16 tensor [head_dim] on {dev}")
+        if cos_sin.dim() != 2 or cos_sin.shape[1] != self.rot_dim or cos_sin.dtype != torch.float32 or \
+                cos_sin.device != dev or not cos_sin.is_contiguous():
+            raise ValueError(f"cos_sin must be a contiguous fp32 tensor [positions, rot_dim] on {dev}")
+        _check_int32(dev, (T,), q_seq=q_seq, q_pos=q_pos)
+        _check_cache(k_cache, v_cache, page_table, self.page_size, self.Hkv, self.D, dev)
+        if q_out is None:
+            q_out = torch.empty((T, self.Hq, self.D), dtype=torch.bfloat16, device=dev)
+        if tuple(q_out.shape) != (T, self.Hq, self.D) or q_out.dtype != torch.bfloat16 or q_out.device != dev or \
+                not q_out.is_contiguous():
+            raise ValueError(f"q_out must be a contiguous bf16 tensor [T, num_q_heads, head_dim] on {dev}")
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        bi_qkrope_run(self.handle, qkv.data_ptr(), T, int(qkv.stride(0)) if T > 1 else width,
+                      None if gq is None else gq.data_ptr(), None if gk is None else gk.data_ptr(),
+                      cos_sin.data_ptr(), int(cos_sin.shape[0]), q_seq.data_ptr(), q_pos.data_ptr(),
+                      k_cache.data_ptr(), v_cache.data_ptr(), int(k_cache.shape[0]), page_table.data_ptr(),
+                      int(page_table.shape[0]), int(page_table.shape[1]), q_out.data_ptr(), s)
+        return q_out
+
+    __call__ = run
+
+    def device_error(self, stream=None) -> int:
+        s = 0
+        if stream is not None:
+            s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return bi_qkrope_get_device_error(self.handle, s)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            bi_qkrope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 class BiPreNorm:
     """mHC pre-norm projection y = RMSNorm(x) . W (fp32 out) on torch tensors: x [M, K] bf16,
     W [K, N] bf16 (a norm weight folded into W's rows)."""
@@ -580,6 +723,8 @@ class BiPreNorm:
 
 
 __all__ = [
+    "BiQkRope", "bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",
+    "bi_qkrope_destroy", "bi_qkrope_config", "QKROPE_EXPORTED_SYMBOLS",
     "BiPreNorm", "bi_prenorm_create", "bi_prenorm_run", "bi_prenorm_get_config", "bi_prenorm_destroy",
     "bi_prenorm_config", "PRENORM_EXPORTED_SYMBOLS",
     "BiAttention", "bi_attention_create", "bi_attention_run", "bi_attention_get_config", "bi_attention_workspace_size",

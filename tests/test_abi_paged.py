@@ -1,0 +1,56 @@
+"""Host-side checks of the entry points around the paged cache that need no GPU: every declared
+symbol is exported, the binding's structures match the headers, and bad arguments are refused with
+the documented codes before any CUDA call."""
+import ctypes
+
+import pytest
+
+import invariant_bi_gemm_gb300 as bg
+from invariant_bi_gemm_gb300 import build as bgbuild
+from test_abi import _declared, _structs
+
+INVALID, UNSUPPORTED = bg.BI_GEMM_ERR_INVALID_ARG, bg.BI_GEMM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("header,names", [("bi_qkrope.h", bg.QKROPE_EXPORTED_SYMBOLS)])
+def test_header_symbols_exported(header, names):
+    declared = _declared(header)
+    assert set(declared) == set(names)
+    L = ctypes.CDLL(bgbuild.lib_path("libbi_gemm.so"))
+    for name in declared:
+        assert hasattr(L, name), name
+
+
+@pytest.mark.parametrize("header,name", [("bi_qkrope.h", "bi_qkrope_config")])
+def test_binding_structs_match_the_headers(header, name):
+    assert [n for _, n in _structs(header)[name]] == [n for n, _ in getattr(bg, name)._fields_]
+    assert all(t == "int32_t" for t, _ in _structs(header)[name])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,rot,inter,eps,want", [
+    (32, 8, 128, 16, 128, 0, -1.0, INVALID),
+    (32, 8, 128, 16, 128, 0, float("nan"), INVALID),
+    (32, 8, 128, 16, 128, 2, 1e-6, INVALID),
+    (32, 8, 128, 0, 128, 0, 1e-6, INVALID),
+    (0, 8, 128, 16, 128, 0, 1e-6, INVALID),
+    (32, 8, 128, 16, 0, 0, 1e-6, INVALID),
+    (32, 8, 96, 16, 96, 0, 1e-6, UNSUPPORTED),         # head dim
+    (32, 8, 64, 16, 128, 0, 1e-6, UNSUPPORTED),        # rot_dim > head_dim
+    (32, 8, 128, 16, 24, 0, 1e-6, UNSUPPORTED),        # rot_dim % 16
+    (4000, 80, 128, 16, 128, 0, 1e-6, UNSUPPORTED),    # heads
+    (32, 8, 128, (1 << 20) + 1, 128, 0, 1e-6, UNSUPPORTED),
+])
+def test_qkrope_create_refuses_before_touching_cuda(Hq, Hkv, D, page, rot, inter, eps, want):
+    h = ctypes.c_void_p()
+    assert bg.library().bi_qkrope_create(ctypes.byref(h), Hq, Hkv, D, page, rot, inter, eps) == want
+    assert h.value is None
+
+
+def test_qkrope_null_arguments():
+    L = bg.library()
+    assert L.bi_qkrope_create(None, 32, 8, 128, 16, 128, 0, 1e-6) == INVALID
+    assert L.bi_qkrope_run(None, None, 1, 6144, None, None, None, 1, None, None, None, None, 1, None, 1, 1, None,
+                           None) == INVALID
+    assert L.bi_qkrope_get_device_error(None, None) == INVALID
+    assert L.bi_qkrope_get_config(None, None) == INVALID
+    assert L.bi_qkrope_destroy(None) == bg.BI_GEMM_OK
