@@ -44,6 +44,9 @@ EXPORTED_SYMBOLS = (
 RMSNORM_EXPORTED_SYMBOLS = ("bi_rmsnorm_create", "bi_rmsnorm_run", "bi_rmsnorm_get_config", "bi_rmsnorm_destroy")
 # every symbol include/bi_prenorm.h declares
 PRENORM_EXPORTED_SYMBOLS = ("bi_prenorm_create", "bi_prenorm_run", "bi_prenorm_get_config", "bi_prenorm_destroy")
+# every symbol include/bi_prompt.h declares
+PROMPT_EXPORTED_SYMBOLS = ("bi_prompt_create", "bi_prompt_run", "bi_prompt_workspace_size",
+                           "bi_prompt_get_device_error", "bi_prompt_get_config", "bi_prompt_destroy")
 # every symbol include/bi_qkrope.h declares
 QKROPE_EXPORTED_SYMBOLS = ("bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",
                            "bi_qkrope_destroy")
@@ -92,6 +95,11 @@ class bi_qkrope_config(ctypes.Structure):
                                               "interleaved", "threads", "tokens_per_block")]
 
 
+class bi_prompt_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "page_size", "tile_positions",
+                                              "block_positions", "stages", "threads", "max_ctas", "tma_pages")]
+
+
 class bi_prenorm_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("K", "N", "chunk", "splits", "tile_rows")]
 
@@ -135,10 +143,17 @@ def _load() -> ctypes.CDLL:
     L.bi_qkrope_get_device_error.argtypes = [P, P]
     L.bi_qkrope_get_config.argtypes = [P, ctypes.POINTER(bi_qkrope_config)]
     L.bi_qkrope_destroy.argtypes = [P]
+    L.bi_prompt_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, ctypes.c_float]
+    L.bi_prompt_run.argtypes = [P, P, I64, P, P, I64, P, P, I64, P, I64, I64, P, P]
+    L.bi_prompt_workspace_size.argtypes = [P, I64, I64, ctypes.POINTER(ctypes.c_uint64)]
+    L.bi_prompt_get_device_error.argtypes = [P, P]
+    L.bi_prompt_get_config.argtypes = [P, ctypes.POINTER(bi_prompt_config)]
+    L.bi_prompt_destroy.argtypes = [P]
     for n in ("bi_gemm_create", "bi_gemm_create_ex", "bi_gemm_run", "bi_gemm_run_noalloc", "bi_gemm_run_gathered",
               "bi_gemm_get_device_error",
               "bi_gemm_destroy", "bi_gemm_get_config", "bi_gemm_workspace_size", "bi_gemm_version") + \
-            RMSNORM_EXPORTED_SYMBOLS + ATTENTION_EXPORTED_SYMBOLS + PRENORM_EXPORTED_SYMBOLS + QKROPE_EXPORTED_SYMBOLS:
+            RMSNORM_EXPORTED_SYMBOLS + ATTENTION_EXPORTED_SYMBOLS + PRENORM_EXPORTED_SYMBOLS + QKROPE_EXPORTED_SYMBOLS + \
+            PROMPT_EXPORTED_SYMBOLS:
         getattr(L, n).restype = I32
     return L
 
@@ -318,6 +333,42 @@ def bi_qkrope_get_config(h: int) -> dict:
 
 def bi_qkrope_destroy(h: int) -> None:
     _check(library().bi_qkrope_destroy(ctypes.c_void_p(h)), "bi_qkrope_destroy")
+
+
+def bi_prompt_create(num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, scale: float) -> int:
+    """Returns the handle (an opaque integer); raises BiGemmError on refusal."""
+    h = ctypes.c_void_p()
+    _check(library().bi_prompt_create(ctypes.byref(h), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                      int(page_size), float(scale)), "bi_prompt_create")
+    return h.value
+
+
+def bi_prompt_run(h: int, q: int, T: int, q_start: int, q_pos0: int, num_seqs: int, k_cache: int, v_cache: int,
+                  num_pages: int, page_table: int, max_pages: int, max_pos: int, o: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_prompt_run(h, q, T, q_start, q_pos0, num_seqs, k_cache, v_cache, num_pages, page_table,
+                                   max_pages, max_pos, o, stream), "bi_prompt_run")
+
+
+def bi_prompt_workspace_size(h: int, T: int, num_seqs: int) -> int:
+    b = ctypes.c_uint64()
+    _check(library().bi_prompt_workspace_size(ctypes.c_void_p(h), int(T), int(num_seqs), ctypes.byref(b)),
+           "bi_prompt_workspace_size")
+    return b.value
+
+
+def bi_prompt_get_device_error(h: int, stream: int = 0) -> int:
+    return library().bi_prompt_get_device_error(ctypes.c_void_p(h), ctypes.c_void_p(stream))
+
+
+def bi_prompt_get_config(h: int) -> dict:
+    c = bi_prompt_config()
+    _check(library().bi_prompt_get_config(ctypes.c_void_p(h), ctypes.byref(c)), "bi_prompt_get_config")
+    return {n: getattr(c, n) for n, _ in bi_prompt_config._fields_}
+
+
+def bi_prompt_destroy(h: int) -> None:
+    _check(library().bi_prompt_destroy(ctypes.c_void_p(h)), "bi_prompt_destroy")
 
 
 def bi_prenorm_create(K: int, N: int, eps: float, chunk: int = 0) -> int:
@@ -677,6 +728,72 @@ class BiQkRope:
             pass
 
 
+class BiPromptAttention:
+    """Batch-invariant causal attention of packed prompts, or of chunks of them behind a cached
+    context, over the paged KV cache of BiAttention, on torch tensors (include/bi_prompt.h).
+
+    q [T, Hq, D] bf16, the sequences one after the other; q_start int32 [num_seqs + 1], the first row
+    of each and the end of the last; q_pos0 int32 [num_seqs], the position of each first row (0 for
+    a whole prompt); caches and page table as in BiAttention, holding the calls' own keys and values.
+    max_pos: an upper bound of every position.  Returns o [T, Hq, D]; rows outside the sequences are
+    left as they were (undefined in a new o).
+    """
+
+    def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int,
+                 scale: float | None = None):
+        self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
+        self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
+        self.handle = bi_prompt_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale)
+
+    @property
+    def config(self) -> dict:
+        return bi_prompt_get_config(self.handle)
+
+    def run(self, q, q_start, q_pos0, k_cache, v_cache, page_table, max_pos: int, o=None, stream=None):
+        import torch
+        dev = q.device
+        if q.dim() != 3 or q.shape[1] != self.Hq or q.shape[2] != self.D or q.dtype != torch.bfloat16 or \
+                not q.is_cuda or not q.is_contiguous():
+            raise ValueError("q must be a contiguous bf16 CUDA tensor [T, num_q_heads, head_dim]")
+        _check_cache(k_cache, v_cache, page_table, self.page_size, self.Hkv, self.D, dev)
+        T, B = int(q.shape[0]), int(page_table.shape[0])
+        _check_int32(dev, (B + 1,), q_start=q_start)
+        _check_int32(dev, (B,), q_pos0=q_pos0)
+        if o is None:
+            o = torch.empty_like(q)
+        if o.shape != q.shape or o.dtype != torch.bfloat16 or o.device != dev or not o.is_contiguous():
+            raise ValueError("o must be a contiguous bf16 tensor shaped like q")
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        bi_prompt_run(self.handle, q.data_ptr(), T, q_start.data_ptr(), q_pos0.data_ptr(), B, k_cache.data_ptr(),
+                      v_cache.data_ptr(), int(k_cache.shape[0]), page_table.data_ptr(), int(page_table.shape[1]),
+                      int(max_pos), o.data_ptr(), s)
+        return o
+
+    __call__ = run
+
+    def device_error(self, stream=None) -> int:
+        s = 0
+        if stream is not None:
+            s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return bi_prompt_get_device_error(self.handle, s)
+
+    def workspace_size(self, T: int, num_seqs: int) -> int:
+        return bi_prompt_workspace_size(self.handle, T, num_seqs)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            bi_prompt_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 class BiPreNorm:
     """mHC pre-norm projection y = RMSNorm(x) . W (fp32 out) on torch tensors: x [M, K] bf16,
     W [K, N] bf16 (a norm weight folded into W's rows)."""
@@ -723,6 +840,8 @@ class BiPreNorm:
 
 
 __all__ = [
+    "BiPromptAttention", "bi_prompt_create", "bi_prompt_run", "bi_prompt_workspace_size", "bi_prompt_get_device_error",
+    "bi_prompt_get_config", "bi_prompt_destroy", "bi_prompt_config", "PROMPT_EXPORTED_SYMBOLS",
     "BiQkRope", "bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",
     "bi_qkrope_destroy", "bi_qkrope_config", "QKROPE_EXPORTED_SYMBOLS",
     "BiPreNorm", "bi_prenorm_create", "bi_prenorm_run", "bi_prenorm_get_config", "bi_prenorm_destroy",

@@ -1,0 +1,979 @@
+// bi_prompt.cu — batch-invariant causal attention of packed prompts over a paged KV cache, sm_103a.
+// Implements include/bi_prompt.h.
+//
+// Mathematics: per query row, over blocks of 128 keys in ascending order, with s the scores times
+// scale log2(e) and m a running reference of their maximum:
+//     P = 2^(s - m),   l += sum P,   O += bf16(P) V;     when m rises, l and O shrink by 2^(m_old - m)
+// and o = O / l.  One pass over keys and values; scores and weights never leave the SM.  m rises only
+// when a block's maximum passes it by more than 8 (a weight is then at most 2^8, and the product's
+// relative rounding is the same), so O is rescaled rarely.  The rule looks at the row alone.
+//
+// Bound: the tensor cores, 4 D operations per query row and key, beside 16-bit operands that stay on
+// chip.  Tile: 128 rows = 128 / G positions x the G query heads of a KV head, so a block of keys is
+// loaded once for all its heads and a short chunk still fills rows.  A unit is two tiles (256 / G
+// positions) that share every key and value block and take turns: while one tile's softmax runs,
+// the tensor cores work for the other.  Tiles and blocks are cut at multiples of their size in the
+// request's own positions, so a row's arithmetic never depends on the chunk it came in.
+//
+// Warps (384 threads, one block per SM, persistent; units, longest first, from a counter):
+//   0       producer: takes units, loads the tiles' queries (TMA box: 64 dims x G heads x positions)
+//           and the ring of key and value blocks (K0, V0, K1, V1, ...), page by page
+//   1       issues the MMAs:  S = Q K^T (both operands in shared memory), O += P V (P in TMEM)
+//   2, 3    clean the value blocks on the diagonal: rows a query must not see meet weights of zero,
+//           and zero times a value that is not finite is not zero.  Those values become zeros; for
+//           the rows that do see them, the epilogue adds them back (bad_v)
+//   4 - 11  softmax, a warpgroup per tile, a thread per row: S from TMEM, P to TMEM over S's columns
+// TMEM (512 columns): S0 / P0, S1 / P1 (128 each), O0, O1 (D each).
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include "../../include/bi_prompt.h"
+#include "attn_ptx.cuh"
+
+#ifndef BI_GEMM_API
+#define BI_GEMM_API extern "C" __attribute__((visibility("default")))
+#endif
+
+namespace biprompt {
+
+using namespace biattn_tc;
+
+constexpr int kThreads = 384;
+constexpr int kUnitRows = 256;            // query rows of a unit: two tiles of 128
+constexpr int kBins = 2048;               // plan: units are sorted by key blocks, up to this many
+constexpr int kUnitSlots = 2;             // units handed from the producer to the other warps
+constexpr int kUnitReaders = 11;          // warps 1 .. 11
+constexpr float kSlack = 8.0f;            // how far (log2) a maximum may pass its reference
+
+struct Params {
+  const int32_t* q_start;
+  const int32_t* q_pos0;
+  uint16_t* o;
+  int32_t* cum;             // [B + 1] tiles of the sequences before b
+  int2* rec;                // [tiles] (sequence, tile of its request), longest first
+  uint32_t* counter;        // [2]: tiles planned, units taken
+  uint32_t* status;
+  Cache c;
+  int64_t T, B, cap_tiles;
+  int32_t max_pos, Hq;
+  int32_t stall;            // failure injection (test controls only): this block loads nothing
+  uint64_t timeout_ns;
+  float scale_log2;
+};
+
+// A unit as the roles see it.
+struct Unit {
+  int32_t row0;        // token row of the unit's position `base` (negative where the chunk starts later)
+  int32_t base;        // first position
+  int32_t first, last; // positions of the chunk
+  int32_t b, kh;
+  int32_t nb[2];       // key blocks of each tile (0: none of its rows belong to the chunk)
+};
+
+template <int D_, int G_>
+struct Cfg {
+  static constexpr int D = D_, G = G_;
+  static constexpr int P = 128 / G;                       // positions per tile
+  static constexpr int UP = kUnitRows / G;                // positions per unit
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE_BYTES = 128 * D * 2;
+  static constexpr int STAGE_BYTES = kBlockPos * D * 2;
+  static constexpr int STAGES = D == 128 ? 5 : 8;
+  static constexpr int OFF_RING = 2 * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE_BYTES;
+  // ring full, empty, cleaned; unit full, empty; Q full, empty; S full, P full, O done (per tile); drain
+  static constexpr int NUM_BARS = 3 * STAGES + 2 * kUnitSlots + 2 + 6 + 1;
+  static constexpr int OFF_UNIT = OFF_BAR + 8 * NUM_BARS;
+  static constexpr int OFF_MISC = OFF_UNIT + kUnitSlots * int(sizeof(Unit));
+  static constexpr int SMEM = OFF_MISC + 32 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr uint32_t IDESC_QK = idesc_bf16(128, kBlockPos, false, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
+};
+
+// ------------------------------------------------------------------ plan
+
+// Tiles of sequence b: its first tile and how many (0 where its inputs cannot be served).
+__device__ __forceinline__ int32_t tiles_of(const Params& p, int64_t b, int32_t up, int32_t* first) {
+  const int32_t s = p.q_start[b], e = p.q_start[b + 1], pos0 = p.q_pos0[b];
+  const int64_t n = int64_t(e) - s, last = int64_t(pos0) + n - 1;
+  *first = 0;
+  if (s < 0 || n < 0 || e > p.T || pos0 < 0 || last / p.c.page_size >= p.c.max_pages) {
+    if (n != 0 || s < 0 || e > p.T) atomicOr(p.status, kErrInput);
+    return 0;
+  }
+  if (n == 0) return 0;
+  if (last > p.max_pos) {
+    atomicOr(p.status, kErrBound);
+    return 0;
+  }
+  *first = pos0 / up;
+  return int32_t(last / up) - *first + 1;
+}
+
+// One block: tiles per sequence, then every tile's record, sorted by its key blocks (descending; the
+// order among equals is not fixed and decides no bit).
+__global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) {
+  __shared__ int32_t warp_sums[32];
+  __shared__ int32_t carry;
+  __shared__ int32_t bins[kBins];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) carry = 0;
+  for (int i = tid; i < kBins; i += 1024) bins[i] = 0;
+  __syncthreads();
+  for (int64_t base = 0; base < p.B; base += 1024) {
+    const int64_t b = base + tid;
+    int32_t first, n = b < p.B ? tiles_of(p, b, up, &first) : 0;
+    int32_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int32_t w = warp_sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
+      }
+      warp_sums[lane] = w;
+    }
+    __syncthreads();
+    const int32_t incl = carry + x + (warp > 0 ? warp_sums[warp - 1] : 0);
+    if (b < p.B) p.cum[b] = incl - n;
+    __syncthreads();
+    if (tid == 1023) carry = incl;
+    __syncthreads();
+  }
+  if (tid == 0) p.cum[p.B] = carry;
+  // Ascending q_start gives at most cap_tiles; a table that descends and climbs again may claim more.
+  int32_t total = carry;
+  if (total > p.cap_tiles) {
+    if (tid == 0) atomicOr(p.status, kErrInput);
+    total = int32_t(p.cap_tiles);
+  }
+  __syncthreads();
+  auto tile_of = [&](int32_t i, int32_t* b) {
+    int64_t lo = 0, hi = p.B;                 // the last sequence whose tiles start at or before i
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (p.cum[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    *b = int32_t(lo);
+    return p.q_pos0[lo] / up + (i - p.cum[lo]);
+  };
+  auto bin_of = [&](int32_t tile) { return kBins - 1 - min(kBins - 1, int32_t(int64_t(tile) * up / kBlockPos)); };
+  for (int32_t i = tid; i < total; i += 1024) {
+    int32_t b;
+    atomicAdd(&bins[bin_of(tile_of(i, &b))], 1);
+  }
+  __syncthreads();
+  {                                           // exclusive scan of the bins, two per thread
+    const int32_t a0 = bins[2 * tid], a1 = bins[2 * tid + 1];
+    int32_t x = a0 + a1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int32_t w = warp_sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
+      }
+      warp_sums[lane] = w;
+    }
+    __syncthreads();
+    const int32_t ex = x - a0 - a1 + (warp > 0 ? warp_sums[warp - 1] : 0);
+    bins[2 * tid] = ex;
+    bins[2 * tid + 1] = ex + a0;
+    __syncthreads();
+  }
+  for (int32_t i = tid; i < total; i += 1024) {
+    int32_t b;
+    const int32_t tile = tile_of(i, &b);
+    p.rec[atomicAdd(&bins[bin_of(tile)], 1)] = make_int2(b, tile);
+  }
+  if (tid == 0) {
+    p.counter[0] = uint32_t(total);
+    p.counter[1] = 0u;
+  }
+}
+
+// ------------------------------------------------------------------ attention
+
+template <class C, bool kTma>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv, const Params p) {
+  constexpr int D = C::D, G = C::G, NS = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full = [&](uint32_t s) { return bar0 + 8 * s; };
+  auto empty = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
+  auto clean = [&](uint32_t s) { return bar0 + 8 * (2 * NS + s); };
+  const uint32_t ubar = bar0 + 8 * (3 * NS);
+  auto unit_full = [&](uint32_t s) { return ubar + 8 * s; };
+  auto unit_empty = [&](uint32_t s) { return ubar + 8 * (kUnitSlots + s); };
+  const uint32_t q_full = ubar + 8 * (2 * kUnitSlots), q_empty = q_full + 8;
+  auto s_full = [&](int i) { return q_empty + 8 + 8 * i; };
+  auto p_full = [&](int i) { return q_empty + 24 + 8 * i; };
+  auto o_done = [&](int i) { return q_empty + 40 + 8 * i; };
+  const uint32_t drain = q_empty + 56;
+  Unit* units = reinterpret_cast<Unit*>(smem + C::OFF_UNIT);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  uint32_t* tmem_slot = misc;
+  volatile uint32_t* abort = misc + 1;
+  // [4]: the number (from 1) of the unit, one in four, that last met values on the diagonal that are
+  // not finite; no slot is written again before every warp has left that unit
+  volatile uint32_t* bad_v = misc + 2;
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), 3);             // the MMAs' commit and the two cleaning warps
+      ptx::mbar_init(clean(s), 2);
+    }
+    for (int s = 0; s < kUnitSlots; ++s) {
+      ptx::mbar_init(unit_full(s), 1);
+      ptx::mbar_init(unit_empty(s), kUnitReaders);
+    }
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(s_full(i), 1);
+      ptx::mbar_init(p_full(i), 4);
+      ptx::mbar_init(o_done(i), 1);
+    }
+    ptx::mbar_init(drain, 1);
+    for (int i = 1; i < 6; ++i) misc[i] = 0u;
+    ptx::fence_barrier_init();
+    ptx::prefetch_tensormap(&tmq);
+    if (kTma) {
+      ptx::prefetch_tensormap(&tmk);
+      ptx::prefetch_tensormap(&tmv);
+    }
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  ptx::grid_dependency_wait();   // the plan (and what ran before it) is complete and visible
+  ptx::launch_dependents();
+  const Sync sy{abort, p.status, p.timeout_ns};
+
+  // The next unit, handed over by the producer; false at the end (or after a wait gave up).
+  uint32_t un = 0;               // units seen
+  auto next_unit = [&](Unit& u) {
+    const uint32_t s = un % kUnitSlots, ph = (un / kUnitSlots) & 1u;
+    bool ok = true;
+    if (lane == 0) ok = wait_bar(unit_full(s), ph, sy);
+    ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+    if (!ok) return false;
+    (void)ptx::mbar_try_wait(unit_full(s), ph);   // (complete: every lane observes it)
+    u = units[s];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(unit_empty(s));
+    ++un;
+    return u.b >= 0;
+  };
+
+  if (warp < 4) {
+    ptx::setmaxnreg_dec<80>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      const int32_t total = int32_t(p.counter[0]);
+      bool ok = true, bad = false;
+      uint32_t seq = 0, nun = 0;               // ring loads issued, units handed out
+      uint32_t q_issued = 0;                   // units whose queries were loaded
+      uint32_t late = 0;                       // row copies: loads not yet announced
+      auto announce = [&](uint32_t keep) {     // (row copies) loads up to seq - keep have landed
+        while (late > keep) {
+          if (keep == 1) ptx::cp_async_wait<1>();
+          else ptx::cp_async_wait<0>();
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(full((seq - late) % NS));
+          --late;
+        }
+      };
+      while (ok) {
+        uint32_t id = 0;
+        if (lane == 0) id = atomicAdd(p.counter + 1, 1u);
+        id = __shfl_sync(0xFFFFFFFFu, id, 0);
+        Unit u;
+        u.b = -1;
+        u.row0 = u.base = u.first = u.last = u.kh = u.nb[0] = u.nb[1] = 0;
+        const int64_t rank = int64_t(id) / p.c.Hkv;
+        if (rank < total) {
+          const int2 r = p.rec[rank];
+          u.b = r.x;
+          u.kh = int32_t(int64_t(id) - rank * p.c.Hkv);
+          const int32_t s = p.q_start[r.x];
+          u.first = p.q_pos0[r.x];
+          u.last = u.first + (p.q_start[r.x + 1] - s) - 1;
+          u.base = r.y * C::UP;
+          u.row0 = s + (u.base - u.first);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int32_t t0 = u.base + i * C::P, t1 = t0 + C::P - 1;
+            u.nb[i] = t1 >= u.first && t0 <= u.last ? t0 / kBlockPos + 1 : 0;
+          }
+          if (u.nb[0] == 0 && u.nb[1] == 0) continue;     // (only from a q_start that descends)
+        }
+        const uint32_t us = nun % kUnitSlots;
+        if (nun >= kUnitSlots) {
+          if (lane == 0) ok = wait_bar(unit_empty(us), (nun / kUnitSlots - 1) & 1u, sy);
+          ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          units[us] = u;
+          ptx::mbar_arrive(unit_full(us));
+        }
+        ++nun;
+        if (u.b < 0) break;
+        const int32_t nb = max(u.nb[0], u.nb[1]);
+        const int32_t* trow = p.c.table + int64_t(u.b) * p.c.max_pages;
+        int32_t page = 0;
+        int64_t off[4];
+        for (int32_t i = 0; i < 2 * nb && ok; ++i) {      // K0, V0, K1, V1, ...
+          const int32_t pos0 = (i >> 1) * kBlockPos;
+          if ((i & 1) == 0) {
+            if constexpr (kTma) page = block_page(p.c, trow, pos0, u.last, lane, &bad);
+            else block_rows(p.c, trow, pos0, u.last, D, lane, off, &bad);
+          }
+          const uint32_t s = seq % NS;
+          if (seq >= uint32_t(NS)) {
+            if (!kTma) announce(0);                       // nothing of ours may hold the wait up
+            if (lane == 0) ok = wait_bar(empty(s), (seq / NS - 1) & 1u, sy);
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+          }
+          if (int(blockIdx.x) == p.stall) continue;
+          const uint32_t dst = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
+          if constexpr (kTma) {
+            load_block_tma<D>(dst, full(s), (i & 1) ? &tmv : &tmk, p.c, page, pos0, u.kh, lane);
+            ++seq;
+          } else {
+            load_block_rows<D>(dst, (i & 1) ? p.c.vc : p.c.kc, off, u.kh, lane);
+            ptx::cp_async_commit();
+            ++seq;
+            ++late;
+            announce(1);
+          }
+          if (i == 0) {                                   // the queries behind the first key block
+            if (q_issued > 0) {
+              if (lane == 0) ok = wait_bar(q_empty, (q_issued - 1) & 1u, sy);
+              ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+              if (!ok) break;
+            }
+            if (lane == 0) {
+              ptx::mbar_arrive_expect_tx(q_full, uint32_t((u.nb[0] > 0) + (u.nb[1] > 0)) * C::TILE_BYTES);
+              for (int t = 0; t < 2; ++t)
+                if (u.nb[t] > 0)
+                  for (int hh = 0; hh < C::HALVES; ++hh)
+                    tma_load_3d(sbase + uint32_t(t * C::TILE_BYTES + hh * 128 * 128), &tmq, q_full, hh * 64,
+                                u.kh * G, u.row0 + t * C::P);
+            }
+            ++q_issued;
+          }
+        }
+        if (!kTma) announce(0);
+      }
+      if (bad) atomicOr(p.status, kErrPage);
+      // no copy of ours may be in flight when the block leaves (bounded)
+      if (!kTma) ptx::cp_async_wait<0>();
+      if (lane == 0) {
+        volatile uint32_t none = 0;
+        const Sync end{&none, p.status, p.timeout_ns};
+        if (kTma)
+          for (uint32_t k = 0; k < uint32_t(NS) && k < seq; ++k)
+            wait_bar(full((seq - 1 - k) % NS), ((seq - 1 - k) / NS) & 1u, end);
+        if (q_issued > 0) wait_bar(q_full, (q_issued - 1) & 1u, end);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer (lane 0 issues)
+      Unit u;
+      uint32_t seq = 0, nu = 0, cleaned = 0, np[2] = {0, 0};
+      bool ok = true, issued = false;
+      while (ok && next_unit(u)) {
+        if (lane == 0) {
+          const int32_t nb = max(u.nb[0], u.nb[1]);
+          const int32_t dirty = (u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1;   // cleaned from this block on
+          auto qk = [&](int i, uint32_t s) {
+            const uint32_t qa = sbase + uint32_t(i * C::TILE_BYTES);
+            const uint32_t ka = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t o = uint32_t((k >> 2) * 128 * 128 + (k & 3) * 32);
+              ptx::mma_bf16(tmem + uint32_t(i * 128), sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024),
+                            C::IDESC_QK, k ? 1u : 0u);
+            }
+            ptx::tc_commit(s_full(i));
+            issued = true;
+          };
+          ok = wait_bar(q_full, nu & 1u, sy) && wait_bar(full(seq % NS), (seq / NS) & 1u, sy);
+          if (ok) {
+            ptx::tc_fence_after();
+            for (int i = 0; i < 2; ++i)
+              if (u.nb[i] > 0) qk(i, seq % NS);
+            ptx::tc_commit(empty(seq % NS));
+            if (nb == 1) ptx::tc_commit(q_empty);
+          }
+          for (int32_t j = 0; j < nb && ok; ++j) {
+            const uint32_t vs = seq + 1, ks = seq + 2;           // this block's values, the next one's keys
+            ok = wait_bar(full(vs % NS), (vs / NS) & 1u, sy);
+            if (ok && j >= dirty) {
+              ok = wait_bar(clean(vs % NS), (cleaned >> (vs % NS)) & 1u, sy);
+              cleaned ^= 1u << (vs % NS);
+            }
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (j >= u.nb[i]) continue;
+              ok = wait_bar(p_full(i), np[i] & 1u, sy);
+              if (!ok) break;
+              ++np[i];
+              ptx::tc_fence_after();
+              const uint32_t va = sbase + uint32_t(C::OFF_RING) + (vs % NS) * uint32_t(C::STAGE_BYTES);
+#pragma unroll
+              for (int k = 0; k < kBlockPos / 16; ++k)
+                mma_bf16_ta(tmem + uint32_t(256 + i * D), tmem + uint32_t(i * 128 + k * 8),
+                            sdesc_sw128(va + uint32_t(k * 16 * 128), kBlockPos * 128, 1024), C::IDESC_PV,
+                            (j | k) ? 1u : 0u);
+              issued = true;
+              if (j + 1 == u.nb[i]) ptx::tc_commit(o_done(i));
+              else if ((ok = wait_bar(full(ks % NS), (ks / NS) & 1u, sy))) {
+                ptx::tc_fence_after();
+                qk(i, ks % NS);
+              }
+            }
+            if (!ok) break;
+            ptx::tc_commit(empty(vs % NS));
+            if (j + 1 < nb) {
+              ptx::tc_commit(empty(ks % NS));
+              if (j + 2 == nb) ptx::tc_commit(q_empty);
+            }
+            seq += 2;
+          }
+          ++nu;
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+      }
+      if (lane == 0 && issued) {     // no MMA of ours may be in flight when TMEM is released
+        volatile uint32_t none = 0;
+        const Sync end{&none, p.status, p.timeout_ns};
+        ptx::tc_commit(drain);
+        wait_bar(drain, 0u, end);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ cleaning of the diagonal's values
+      const int hid = (warp - 2) * 32 + lane;      // 64 threads
+      Unit u;
+      uint32_t seq = 0, nu = 0;
+      bool ok = true;
+      while (ok && next_unit(u)) {
+        const int32_t nb = max(u.nb[0], u.nb[1]);
+        const int32_t dirty = (u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1;
+        bool found = false;
+        // Every load is waited for in turn and released, so that a parity is never a lap off.
+        for (int32_t x = 0; x < 2 * nb && ok; ++x) {
+          const uint32_t vs = seq + uint32_t(x);
+          ok = wait_bar(full(vs % NS), (vs / NS) & 1u, sy);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const int32_t j = x >> 1;
+          if ((x & 1) == 0 || j < dirty) {
+            if (lane == 0) ptx::mbar_arrive(empty(vs % NS));
+            continue;
+          }
+          const uint32_t va = sbase + uint32_t(C::OFF_RING) + (vs % NS) * uint32_t(C::STAGE_BYTES);
+          // (the swizzle only moves 16-byte chunks inside a row)
+          for (int e = hid; e < C::STAGE_BYTES / 16; e += 64) {
+            const uint32_t a = va + uint32_t(e) * 16;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(a));
+            bool hit = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, hit = true;
+              if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu, hit = true;
+            }
+            if (hit) {
+              ptx::st_shared_v4(a, w[0], w[1], w[2], w[3]);
+              found |= j * kBlockPos + (e / 8) % kBlockPos <= u.last;   // (unused slots: nobody sees them)
+            }
+          }
+          if (__any_sync(0xFFFFFFFFu, found) && lane == 0) bad_v[nu & 3u] = nu + 1;
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(clean(vs % NS));
+            ptx::mbar_arrive(empty(vs % NS));
+          }
+        }
+        seq += 2 * uint32_t(nb);
+        ++nu;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax: a thread per query row
+    ptx::setmaxnreg_inc<208>();
+    const int i = (warp - 4) >> 2;                 // tile
+    const int r = tid - 128 - i * 128;             // row of the tile = TMEM lane
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + uint32_t(i * 128), to = tmem + lane_base + uint32_t(256 + i * D);
+    uint32_t ns = 0, nt = 0;                       // blocks and units of this tile
+    Unit u;
+    bool ok = true;
+    while (ok && next_unit(u)) {
+      const int32_t nb = i ? u.nb[1] : u.nb[0];
+      if (nb == 0) continue;
+      const int32_t pos = u.base + i * C::P + r / G;
+      float m = -INFINITY, l = 0.0f;
+      for (int32_t j = 0; j < nb; ++j) {
+        ok = wait_bar(s_full(i), ns & 1u, sy);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        ++ns;
+        ptx::tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(ts + uint32_t(c * 32), s[c]);
+        ptx::tmem_wait_ld();
+        if (j + 1 == nb) {                         // the diagonal: keys behind the row's position
+          const int32_t lim = pos - j * kBlockPos;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e > lim) s[c][e] = 0xFF800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+        }
+        const float mb = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), p.scale_log2);
+        float f = 1.0f;
+        if (mb > m + kSlack || m == -INFINITY) {
+          f = m == -INFINITY ? 1.0f : ex2(__fsub_rn(m, mb));      // (nothing to shrink yet)
+          m = mb;
+          l = __fmul_rn(l, f);
+        }
+        // P V of the block before is complete: this block's S was issued behind it
+        if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld_32x32b_x32(to + uint32_t(c), o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), f));
+            tmem_st_x32(to + uint32_t(c), o);
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;   // a row of -infinity so far: weights of zero
+        float ls[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          ls[c] = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float w0 = ex2(__fmaf_rn(__uint_as_float(s[c][e]), p.scale_log2, -ref));
+            const float w1 = ex2(__fmaf_rn(__uint_as_float(s[c][e + 1]), p.scale_log2, -ref));
+            ls[c] = __fadd_rn(ls[c], w0);
+            ls[c] = __fadd_rn(ls[c], w1);
+            pk[e >> 1] = ptx::pack_bf16x2(w0, w1);
+          }
+          tmem_st_x16(ts + uint32_t(c * 16), pk);
+        }
+        l = __fadd_rn(l, __fadd_rn(__fadd_rn(ls[0], ls[1]), __fadd_rn(ls[2], ls[3])));
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full(i));
+      }
+      if (!ok) break;
+      ok = wait_bar(o_done(i), nt & 1u, sy);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      ++nt;
+      ptx::tc_fence_after();
+      const bool store = pos >= u.first && pos <= u.last;
+      const bool dirty = bad_v[(un - 1) & 3u] == un;      // (written before the values' MMA)
+      uint16_t* orow = p.o + ((int64_t(u.row0) + i * C::P + r / G) * p.Hq + u.kh * G + r % G) * D;
+      const float rl = __fdiv_rn(1.0f, l);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        ptx::tmem_ld_32x32b_x32(to + uint32_t(c), o);
+        ptx::tmem_wait_ld();
+        if (dirty && store) {
+          // values on the diagonal that are not finite: a weight is positive, so each stands for itself
+          const int32_t d0 = ((u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1) * kBlockPos;
+          for (int32_t k = d0; k <= pos; ++k) {
+            const int64_t page = p.c.table[int64_t(u.b) * p.c.max_pages + k / p.c.page_size];
+            if (page < 0 || page >= p.c.num_pages) continue;
+            const uint16_t* v = p.c.vc + ((page * p.c.page_size + k % p.c.page_size) * p.c.Hkv + u.kh) * D + c;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((v[e] & 0x7F80u) == 0x7F80u)
+                o[e] = __float_as_uint(__fadd_rn(__uint_as_float(o[e]), __uint_as_float(uint32_t(v[e]) << 16)));
+          }
+        }
+        if (store) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = ptx::pack_bf16x2(__fmul_rn(__uint_as_float(o[e + 2 * k]), rl),
+                                      __fmul_rn(__uint_as_float(o[e + 2 * k + 1]), rl));
+            ptx::st_global_v4(orow + c + e, w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      ptx::tc_fence_before();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+struct KernelInfo {
+  const void* tma = nullptr;
+  const void* rows = nullptr;
+  int smem = 0, stages = 0, up = 0;
+};
+
+template <int D, int G>
+KernelInfo info() {
+  using C = Cfg<D, G>;
+  KernelInfo k;
+  k.tma = reinterpret_cast<const void*>(&prompt_kernel<C, true>);
+  k.rows = reinterpret_cast<const void*>(&prompt_kernel<C, false>);
+  k.smem = C::SMEM;
+  k.stages = C::STAGES;
+  k.up = C::UP;
+  return k;
+}
+
+inline KernelInfo select(int D, int G) {
+  if (D == 128) {
+    switch (G) {
+      case 1: return info<128, 1>();
+      case 2: return info<128, 2>();
+      case 4: return info<128, 4>();
+      case 8: return info<128, 8>();
+    }
+  } else if (D == 64) {
+    switch (G) {
+      case 1: return info<64, 1>();
+      case 2: return info<64, 2>();
+      case 4: return info<64, 4>();
+      case 8: return info<64, 8>();
+    }
+  }
+  return KernelInfo{};
+}
+
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// [rows, H, D] bf16 as a 3-D tensor; boxes of 64 dims x `heads` x `box` rows, zero fill outside.
+bool encode(CUtensorMap* m, const void* base, int64_t rows, int H, int D, int heads, int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(H) * D * 2};
+  cuuint32_t b[3] = {64, cuuint32_t(heads), cuuint32_t(box)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, b, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace biprompt
+
+struct bi_prompt {
+  int Hq = 0, Hkv = 0, D = 0, G = 0, page_size = 0;
+  float scale = 0.0f;
+  int device = 0, num_sms = 0;
+  biprompt::KernelInfo kern;
+  uint32_t* d_status = nullptr;
+  void* ws = nullptr;
+  size_t ws_bytes = 0;
+};
+
+namespace {
+
+struct PromptWs {
+  size_t counter, cum, rec, total;
+  int64_t cap_tiles;
+};
+
+PromptWs prompt_layout(const bi_prompt* h, int64_t T, int64_t B) {
+  PromptWs w;
+  w.cap_tiles = T / h->kern.up + 2 * B;     // a sequence of n tokens touches at most n / up + 2 units
+  w.counter = 0;
+  w.cum = 256;
+  w.rec = w.cum + biprompt::align256(size_t(B + 1) * sizeof(int32_t));
+  w.total = w.rec + biprompt::align256(size_t(w.cap_tiles) * sizeof(int2));
+  return w;
+}
+
+}  // namespace
+
+BI_GEMM_API int bi_prompt_create(bi_prompt_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                                 int64_t page_size, float scale) {
+  if (!out) return BI_GEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!std::isfinite(scale) || scale <= 0.0f) return BI_GEMM_ERR_INVALID_ARG;
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0) return BI_GEMM_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0 || num_q_heads > 4096 || page_size > (1 << 20) ||
+      (head_dim != 64 && head_dim != 128))
+    return BI_GEMM_ERR_UNSUPPORTED;
+  const int64_t G = num_q_heads / num_kv_heads;
+  if (G > 8) return BI_GEMM_ERR_UNSUPPORTED;
+  const biprompt::KernelInfo k = biprompt::select(int(head_dim), int(G));
+  if (!k.tma) return BI_GEMM_ERR_UNSUPPORTED;
+  int dev = 0, major = 0, minor = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (major != 10 || minor != 3) return BI_GEMM_ERR_UNSUPPORTED;
+  if (!biprompt::encode_fn() ||
+      cudaFuncSetAttribute(k.tma, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
+      cudaFuncSetAttribute(k.rows, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  bi_prompt* h = new (std::nothrow) bi_prompt();
+  if (!h) return BI_GEMM_ERR_OOM;
+  h->Hq = int(num_q_heads);
+  h->Hkv = int(num_kv_heads);
+  h->D = int(head_dim);
+  h->G = int(G);
+  h->page_size = int(page_size);
+  h->scale = scale;
+  h->device = dev;
+  h->num_sms = sms;
+  h->kern = k;
+  if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
+      cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
+    cudaGetLastError();
+    if (h->d_status) cudaFree(h->d_status);
+    delete h;
+    return BI_GEMM_ERR_CUDA;
+  }
+  *out = h;
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_prompt_workspace_size(bi_prompt_t h, int64_t T, int64_t num_seqs, uint64_t* bytes) {
+  if (!h || !bytes || T < 0 || num_seqs < 0) return BI_GEMM_ERR_INVALID_ARG;
+  *bytes = T == 0 || num_seqs == 0 ? 0 : uint64_t(prompt_layout(h, T, num_seqs).total);
+  return BI_GEMM_OK;
+}
+
+namespace {
+
+// bi_prompt_run with the failure injection of the test controls (stall: that block loads no keys) and
+// the limit of the waits.
+int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, const int32_t* q_pos0, int64_t B,
+               const void* k_cache, const void* v_cache, int64_t num_pages, const int32_t* page_table,
+               int64_t max_pages, int64_t max_pos, void* o, void* stream, int32_t stall, uint64_t timeout_ns) {
+  if (!h || T < 0 || B < 0 || num_pages < 0 || max_pages < 0 || max_pos < 0) return BI_GEMM_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return BI_GEMM_OK;
+  // row coordinates, unit numbers and positions are 32-bit
+  if (T > (int64_t(1) << 28) || B > (int64_t(1) << 24) || max_pos >= (int64_t(1) << 30) ||
+      (T / h->kern.up + 2 * B) * h->Hkv >= (int64_t(1) << 31))
+    return BI_GEMM_ERR_UNSUPPORTED;
+  if (!q || !q_start || !q_pos0 || !k_cache || !v_cache || !page_table || !o) return BI_GEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(q_start) | reinterpret_cast<uintptr_t>(q_pos0) |
+       reinterpret_cast<uintptr_t>(page_table)) & 3u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
+  CUtensorMap tmq, tmk, tmv;
+  std::memset(&tmk, 0, sizeof(tmk));
+  std::memset(&tmv, 0, sizeof(tmv));
+  if (!biprompt::encode(&tmq, q, T, h->Hq, h->D, h->G, 128 / h->G)) return BI_GEMM_ERR_CUDA;
+  // TMA boxes need whole pages and row coordinates (one page past the end included) of 32 bits;
+  // otherwise rows are copied: the same bits.
+  const int64_t rows = num_pages * h->page_size;
+  const int box = std::min(h->page_size, biattn_tc::kBlockPos);
+  const bool tma = biattn_tc::tma_page_size(h->page_size) && num_pages > 0 &&
+                   rows + h->page_size < (int64_t(1) << 31) &&
+                   biprompt::encode(&tmk, k_cache, rows, h->Hkv, h->D, 1, box) &&
+                   biprompt::encode(&tmv, v_cache, rows, h->Hkv, h->D, 1, box);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const PromptWs w = prompt_layout(h, T, B);
+  if (w.total > h->ws_bytes) {
+    if (h->ws) cudaFreeAsync(h->ws, st);
+    h->ws = nullptr;
+    h->ws_bytes = 0;
+    void* ws = nullptr;
+    if (cudaMallocAsync(&ws, w.total, st) != cudaSuccess) {
+      cudaGetLastError();
+      return BI_GEMM_ERR_OOM;
+    }
+    h->ws = ws;
+    h->ws_bytes = w.total;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  biprompt::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.q_start = q_start;
+  p.q_pos0 = q_pos0;
+  p.o = static_cast<uint16_t*>(o);
+  p.counter = reinterpret_cast<uint32_t*>(ws + w.counter);
+  p.cum = reinterpret_cast<int32_t*>(ws + w.cum);
+  p.rec = reinterpret_cast<int2*>(ws + w.rec);
+  p.status = h->d_status;
+  p.c.kc = static_cast<const uint16_t*>(k_cache);
+  p.c.vc = static_cast<const uint16_t*>(v_cache);
+  p.c.table = page_table;
+  p.c.num_pages = num_pages;
+  p.c.max_pages = max_pages;
+  p.c.Hkv = h->Hkv;
+  p.c.page_size = h->page_size;
+  p.T = T;
+  p.B = B;
+  p.cap_tiles = w.cap_tiles;
+  p.max_pos = int32_t(max_pos);
+  p.Hq = h->Hq;
+  p.stall = stall;
+  p.timeout_ns = timeout_ns;
+  p.scale_log2 = h->scale * 1.4426950408889634f;   // log2(e)
+  int32_t up = h->kern.up;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  void* pargs[2] = {&p, &up};
+  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&biprompt::plan_kernel), pargs);
+  if (e == cudaSuccess) {
+    void* args[4] = {&tmq, &tmk, &tmv, &p};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(w.cap_tiles * h->Hkv, h->num_sms)));
+    cfg.blockDim = dim3(biprompt::kThreads);
+    cfg.dynamicSmemBytes = size_t(h->kern.smem);
+    e = cudaLaunchKernelExC(&cfg, tma ? h->kern.tma : h->kern.rows, args);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  return BI_GEMM_OK;
+}
+
+}  // namespace
+
+BI_GEMM_API int bi_prompt_run(bi_prompt_t h, const void* q, int64_t T, const int32_t* q_start, const int32_t* q_pos0,
+                              int64_t num_seqs, const void* k_cache, const void* v_cache, int64_t num_pages,
+                              const int32_t* page_table, int64_t max_pages, int64_t max_pos, void* o, void* stream) {
+  return prompt_run(h, q, T, q_start, q_pos0, num_seqs, k_cache, v_cache, num_pages, page_table, max_pages, max_pos, o,
+                    stream, -1, biattn_tc::kTimeoutNs);
+}
+
+BI_GEMM_API int bi_prompt_get_device_error(bi_prompt_t h, void* stream) {
+  if (!h) return BI_GEMM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t s = 0;
+  if (cudaMemcpyAsync(&s, h->d_status, sizeof(s), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (s == 0) return BI_GEMM_OK;
+  if (cudaMemsetAsync(h->d_status, 0, sizeof(uint32_t), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  return (s & biattn_tc::kErrTimeout) ? BI_GEMM_ERR_TIMEOUT : BI_GEMM_ERR_INVALID_ARG;
+}
+
+BI_GEMM_API int bi_prompt_get_config(bi_prompt_t h, bi_prompt_config* c) {
+  if (!h || !c) return BI_GEMM_ERR_INVALID_ARG;
+  c->num_q_heads = h->Hq;
+  c->num_kv_heads = h->Hkv;
+  c->head_dim = h->D;
+  c->page_size = h->page_size;
+  c->tile_positions = h->kern.up;
+  c->block_positions = biattn_tc::kBlockPos;
+  c->stages = h->kern.stages;
+  c->threads = biprompt::kThreads;
+  c->max_ctas = h->num_sms;
+  c->tma_pages = biattn_tc::tma_page_size(h->page_size) ? 1 : 0;
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_prompt_destroy(bi_prompt_t h) {
+  if (!h) return BI_GEMM_OK;
+  if (h->ws) cudaFree(h->ws);
+  if (h->d_status) cudaFree(h->d_status);
+  delete h;
+  return BI_GEMM_OK;
+}

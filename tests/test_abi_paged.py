@@ -12,7 +12,8 @@ from test_abi import _declared, _structs
 INVALID, UNSUPPORTED = bg.BI_GEMM_ERR_INVALID_ARG, bg.BI_GEMM_ERR_UNSUPPORTED
 
 
-@pytest.mark.parametrize("header,names", [("bi_qkrope.h", bg.QKROPE_EXPORTED_SYMBOLS)])
+@pytest.mark.parametrize("header,names", [("bi_qkrope.h", bg.QKROPE_EXPORTED_SYMBOLS),
+                                          ("bi_prompt.h", bg.PROMPT_EXPORTED_SYMBOLS)])
 def test_header_symbols_exported(header, names):
     declared = _declared(header)
     assert set(declared) == set(names)
@@ -21,7 +22,7 @@ def test_header_symbols_exported(header, names):
         assert hasattr(L, name), name
 
 
-@pytest.mark.parametrize("header,name", [("bi_qkrope.h", "bi_qkrope_config")])
+@pytest.mark.parametrize("header,name", [("bi_qkrope.h", "bi_qkrope_config"), ("bi_prompt.h", "bi_prompt_config")])
 def test_binding_structs_match_the_headers(header, name):
     assert [n for _, n in _structs(header)[name]] == [n for n, _ in getattr(bg, name)._fields_]
     assert all(t == "int32_t" for t, _ in _structs(header)[name])
@@ -54,3 +55,31 @@ def test_qkrope_null_arguments():
     assert L.bi_qkrope_get_device_error(None, None) == INVALID
     assert L.bi_qkrope_get_config(None, None) == INVALID
     assert L.bi_qkrope_destroy(None) == bg.BI_GEMM_OK
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,scale,want", [
+    (32, 8, 128, 16, 0.0, INVALID),
+    (32, 8, 128, 16, float("nan"), INVALID),
+    (32, 8, 128, 0, 0.1, INVALID),
+    (32, -8, 128, 16, 0.1, INVALID),
+    (30, 8, 128, 16, 0.1, UNSUPPORTED),        # heads not a multiple
+    (24, 8, 128, 16, 0.1, UNSUPPORTED),        # group of 3
+    (32, 2, 128, 16, 0.1, UNSUPPORTED),        # group of 16
+    (32, 8, 96, 16, 0.1, UNSUPPORTED),
+    (32, 8, 128, (1 << 20) + 1, 0.1, UNSUPPORTED),
+])
+def test_prompt_create_refuses_before_touching_cuda(Hq, Hkv, D, page, scale, want):
+    h = ctypes.c_void_p()
+    assert bg.library().bi_prompt_create(ctypes.byref(h), Hq, Hkv, D, page, scale) == want
+    assert h.value is None
+
+
+def test_prompt_null_arguments():
+    L = bg.library()
+    b = ctypes.c_uint64()
+    assert L.bi_prompt_create(None, 32, 8, 128, 16, 0.1) == INVALID
+    assert L.bi_prompt_run(None, None, 1, None, None, 1, None, None, 1, None, 1, 0, None, None) == INVALID
+    assert L.bi_prompt_workspace_size(None, 1, 1, ctypes.byref(b)) == INVALID
+    assert L.bi_prompt_get_device_error(None, None) == INVALID
+    assert L.bi_prompt_get_config(None, None) == INVALID
+    assert L.bi_prompt_destroy(None) == bg.BI_GEMM_OK
