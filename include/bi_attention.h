@@ -96,6 +96,34 @@ int bi_attention_run(bi_attention_t h, const void* q, int64_t T, const int32_t* 
 /* Workspace bytes a run with T tokens and the bound max_pos needs. */
 int bi_attention_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, uint64_t* bytes);
 
+/* bi_attention_run for a batch whose tokens come in groups with a common prefix (a system prompt,
+ * samples of one prompt, a forked cache): group g is the tokens group_start[g] .. group_start[g + 1]
+ * - 1, whose requests agree on positions 0 .. group_len[g] - 1, and agree by naming the same pages
+ * for them.  A split that lies in the prefix before the token's own split is computed once for all
+ * tokens of the group (tensor cores, one load of its keys and values) instead of once per token.
+ *
+ * o has the bits of bi_attention_run on the same tokens: sharing changes no result, so a request's
+ * output does not depend on whether, or with whom, it shares.  Tokens of a group may differ in
+ * position and share fewer splits than others; a group may hold several tokens of one request; a
+ * group_len of 0, a group of one token and tokens outside every group (before group_start[0], from
+ * group_start[num_groups] on) are served as in bi_attention_run.
+ *
+ * group_start int32 [num_groups + 1], ascending, and group_len int32 [num_groups]: DEVICE pointers,
+ * 4-byte aligned.  Caught by the kernels, as BI_GEMM_ERR_INVALID_ARG from
+ * bi_attention_get_device_error with the group's outputs undefined: a group_start that descends or
+ * leaves [0, T], a negative group_len, page tables that differ within a shared split.  num_groups
+ * >= 0; all else as bi_attention_run.  Queues four kernels: a plan, the groups' units, the other
+ * units, the merge. */
+int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
+                            const int32_t* q_pos, const void* k_cache, const void* v_cache,
+                            int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
+                            int64_t max_pages, int64_t max_pos, const int32_t* group_start,
+                            const int32_t* group_len, int64_t num_groups, void* o, void* stream);
+
+/* Workspace bytes of a run_shared with T tokens, the bound max_pos and num_groups groups. */
+int bi_attention_shared_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, int64_t num_groups,
+                                       uint64_t* bytes);
+
 /* Synchronise `stream`; BI_GEMM_ERR_TIMEOUT if a bounded wait expired, else
  * BI_GEMM_ERR_INVALID_ARG if a kernel caught a bad input, since the last call (the status is then
  * cleared); BI_GEMM_ERR_CUDA if synchronisation failed; else BI_GEMM_OK. */

@@ -52,7 +52,8 @@ QKROPE_EXPORTED_SYMBOLS = ("bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_d
                            "bi_qkrope_destroy")
 # every symbol include/bi_attention.h declares
 ATTENTION_EXPORTED_SYMBOLS = ("bi_attention_create", "bi_attention_run", "bi_attention_workspace_size",
-                              "bi_attention_get_device_error", "bi_attention_get_config", "bi_attention_destroy")
+                              "bi_attention_get_device_error", "bi_attention_get_config", "bi_attention_destroy",
+                              "bi_attention_run_shared", "bi_attention_shared_workspace_size")
 
 
 class BiGemmError(RuntimeError):
@@ -131,6 +132,8 @@ def _load() -> ctypes.CDLL:
     L.bi_attention_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, ctypes.c_float, I64]
     L.bi_attention_run.argtypes = [P, P, I64, P, P, P, P, I64, P, I64, I64, I64, P, P]
     L.bi_attention_workspace_size.argtypes = [P, I64, I64, ctypes.POINTER(ctypes.c_uint64)]
+    L.bi_attention_run_shared.argtypes = [P, P, I64, P, P, P, P, I64, P, I64, I64, I64, P, P, I64, P, P]
+    L.bi_attention_shared_workspace_size.argtypes = [P, I64, I64, I64, ctypes.POINTER(ctypes.c_uint64)]
     L.bi_attention_get_device_error.argtypes = [P, P]
     L.bi_attention_get_config.argtypes = [P, ctypes.POINTER(bi_attention_config)]
     L.bi_attention_destroy.argtypes = [P]
@@ -277,6 +280,22 @@ def bi_attention_run(h: int, q: int, T: int, q_seq: int, q_pos: int, k_cache: in
     rc = library().bi_attention_run(V(h), V(q), int(T), V(q_seq), V(q_pos), V(k_cache), V(v_cache), int(num_pages),
                                      V(page_table), int(num_seqs), int(max_pages), int(max_pos), V(o), V(stream))
     _check(rc, "bi_attention_run")
+
+
+def bi_attention_run_shared(h: int, q: int, T: int, q_seq: int, q_pos: int, k_cache: int, v_cache: int,
+                            num_pages: int, page_table: int, num_seqs: int, max_pages: int, max_pos: int,
+                            group_start: int, group_len: int, num_groups: int, o: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_attention_run_shared(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs,
+                                             max_pages, max_pos, group_start, group_len, num_groups, o, stream),
+           "bi_attention_run_shared")
+
+
+def bi_attention_shared_workspace_size(h: int, T: int, max_pos: int, num_groups: int) -> int:
+    b = ctypes.c_uint64()
+    _check(library().bi_attention_shared_workspace_size(ctypes.c_void_p(h), int(T), int(max_pos), int(num_groups),
+                                                        ctypes.byref(b)), "bi_attention_shared_workspace_size")
+    return b.value
 
 
 def bi_attention_get_config(h: int) -> dict:
@@ -618,8 +637,41 @@ class BiAttention:
             s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         return bi_attention_get_device_error(self.handle, s)
 
+    def run_shared(self, q, q_seq, q_pos, k_cache, v_cache, page_table, max_pos: int, group_start, group_len,
+                   o=None, stream=None):
+        """run() for tokens in groups that share a prefix: group g is the tokens group_start[g] ..
+        group_start[g + 1] - 1 (int32 [groups + 1], ascending), whose requests name the same pages
+        for positions 0 .. group_len[g] - 1 (int32 [groups]).  The prefix is read once per group;
+        the result has the bits of run()."""
+        import torch
+        dev = q.device
+        T = int(q.shape[0])
+        if q.dim() != 3 or q.shape[1] != self.Hq or q.shape[2] != self.D or q.dtype != torch.bfloat16 or \
+                not q.is_cuda or not q.is_contiguous():
+            raise ValueError("q must be a contiguous bf16 CUDA tensor [T, num_q_heads, head_dim]")
+        _check_cache(k_cache, v_cache, page_table, self.page_size, self.Hkv, self.D, dev)
+        _check_int32(dev, (T,), q_seq=q_seq, q_pos=q_pos)
+        groups = int(group_len.shape[0])
+        _check_int32(dev, (groups,), group_len=group_len)
+        _check_int32(dev, (groups + 1,), group_start=group_start)
+        if o is None:
+            o = torch.empty_like(q)
+        if o.shape != q.shape or o.dtype != torch.bfloat16 or o.device != dev or not o.is_contiguous():
+            raise ValueError("o must be a contiguous bf16 tensor shaped like q")
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        bi_attention_run_shared(self.handle, q.data_ptr(), T, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(),
+                                v_cache.data_ptr(), int(k_cache.shape[0]), page_table.data_ptr(),
+                                int(page_table.shape[0]), int(page_table.shape[1]), int(max_pos),
+                                group_start.data_ptr(), group_len.data_ptr(), groups, o.data_ptr(), s)
+        return o
+
     def workspace_size(self, T: int, max_pos: int) -> int:
         return bi_attention_workspace_size(self.handle, T, max_pos)
+
+    def shared_workspace_size(self, T: int, max_pos: int, num_groups: int) -> int:
+        return bi_attention_shared_workspace_size(self.handle, T, max_pos, num_groups)
 
     def close(self) -> None:
         if getattr(self, "handle", None):
@@ -847,7 +899,8 @@ __all__ = [
     "BiPreNorm", "bi_prenorm_create", "bi_prenorm_run", "bi_prenorm_get_config", "bi_prenorm_destroy",
     "bi_prenorm_config", "PRENORM_EXPORTED_SYMBOLS",
     "BiAttention", "bi_attention_create", "bi_attention_run", "bi_attention_get_config", "bi_attention_workspace_size",
-    "bi_attention_get_device_error", "bi_attention_destroy", "bi_attention_config", "ATTENTION_EXPORTED_SYMBOLS",
+    "bi_attention_get_device_error", "bi_attention_destroy", "bi_attention_config", "bi_attention_run_shared",
+    "bi_attention_shared_workspace_size", "ATTENTION_EXPORTED_SYMBOLS",
     "BiRmsNorm", "bi_rmsnorm_create", "bi_rmsnorm_run", "bi_rmsnorm_get_config", "bi_rmsnorm_destroy",
     "bi_rmsnorm_config", "RMSNORM_EXPORTED_SYMBOLS",
     "BiGemm", "BiGemmError", "bi_gemm_create", "bi_gemm_run", "bi_gemm_run_noalloc", "bi_gemm_get_device_error",

@@ -71,7 +71,7 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 // tcgen05 instruction descriptor (kind::f16): D = f32, A = B = bf16.
-constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
+constexpr __host__ __device__ uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn_major ? 1u << 15 : 0u) | (b_mn_major ? 1u << 16 : 0u) |
          (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }

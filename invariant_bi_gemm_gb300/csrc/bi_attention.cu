@@ -1209,6 +1209,8 @@ bool encode_cache(CUtensorMap* m, const void* base, int64_t rows, int Hkv, int D
 
 }  // namespace biattn
 
+#include "bi_attention_shared.cuh"
+
 struct bi_attention {
   int Hq = 0, Hkv = 0, D = 0, G = 0, page_size = 0, split = 0;
   float scale = 0.0f;
@@ -1225,6 +1227,7 @@ struct bi_attention {
   int nstage4 = 0, tma4_ctas = 0, tma4_ctas_inline = 0;
   size_t tma4_smem = 0;
   biattn::KernelInfo kern;
+  biattn::SharedInfo shared;
   uint32_t* d_status = nullptr;
   void* ws = nullptr;
   size_t ws_bytes = 0;
@@ -1372,6 +1375,15 @@ BI_GEMM_API int bi_attention_create(bi_attention_t* out, int64_t num_q_heads, in
   h->max_ctas = per_sm * sms;
   h->smem = smem;
   h->kern = k;
+  h->shared = biattn::select_shared(h->D, h->G);
+  if (cudaFuncSetAttribute(h->shared.tma, cudaFuncAttributeMaxDynamicSharedMemorySize, h->shared.smem) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(h->shared.rows, cudaFuncAttributeMaxDynamicSharedMemorySize, h->shared.smem) !=
+          cudaSuccess) {
+    cudaGetLastError();
+    delete h;
+    return BI_GEMM_ERR_CUDA;
+  }
   if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
     cudaGetLastError();
@@ -1537,6 +1549,177 @@ BI_GEMM_API int bi_attention_run(bi_attention_t h, const void* q, int64_t T, con
                                  int64_t max_pages, int64_t max_pos, void* o, void* stream) {
   return attention_run(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages, max_pos,
                        o, stream, -1, biattn::kTimeoutNs);
+}
+
+namespace {
+
+struct SharedWs {
+  WsLayout base;
+  size_t nsh, srec, count, total;
+  int64_t cap;      // unit records: a group of n tokens has at most n / (tokens of a unit) + 1 rows of units
+  int32_t cols;
+};
+
+SharedWs shared_layout(const bi_attention* h, int64_t T, int64_t max_pos, int64_t num_groups) {
+  SharedWs w;
+  w.base = layout_of(h, T, max_pos);
+  w.cols = h->split <= 512 ? 128 : 64;      // (blocks of a split) x columns fit the 512 of tensor memory
+  w.cap = (T / (w.cols / h->G) + num_groups) * (max_pos / h->split);
+  w.nsh = w.base.total;
+  w.srec = w.nsh + biattn::align256(size_t(T) * sizeof(int32_t));
+  w.count = w.srec + biattn::align256(size_t(w.cap) * sizeof(int4));
+  w.total = w.count + 256;
+  return w;
+}
+
+}  // namespace
+
+BI_GEMM_API int bi_attention_shared_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, int64_t num_groups,
+                                                   uint64_t* bytes) {
+  if (!h || !bytes || T < 0 || max_pos < 0 || num_groups < 0) return BI_GEMM_ERR_INVALID_ARG;
+  *bytes = T == 0 ? 0 : uint64_t(shared_layout(h, T, max_pos, num_groups).total);
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
+                                        const int32_t* q_pos, const void* k_cache, const void* v_cache,
+                                        int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
+                                        int64_t max_pages, int64_t max_pos, const int32_t* group_start,
+                                        const int32_t* group_len, int64_t num_groups, void* o, void* stream) {
+  if (!h || T < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || max_pos < 0 || num_groups < 0)
+    return BI_GEMM_ERR_INVALID_ARG;
+  // without a group, or a bound that leaves no whole split before a token's own, nothing is shared
+  if (T == 0 || num_groups == 0 || max_pos < h->split)
+    return bi_attention_run(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages,
+                            max_pos, o, stream);
+  if (T > (int64_t(1) << 24) || max_pos >= (int64_t(1) << 30) || num_groups > (int64_t(1) << 24) ||
+      T * h->Hkv * (max_pos / h->split + 1) >= (int64_t(1) << 31))   // unit indices are int32
+    return BI_GEMM_ERR_UNSUPPORTED;
+  const SharedWs w = shared_layout(h, T, max_pos, num_groups);
+  if (w.cap * h->Hkv >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  if (!q || !q_seq || !q_pos || !k_cache || !v_cache || !page_table || !o || !group_start || !group_len)
+    return BI_GEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(k_cache) |
+       reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(q_seq) | reinterpret_cast<uintptr_t>(q_pos) |
+       reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(group_start) |
+       reinterpret_cast<uintptr_t>(group_len)) & 3u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
+  const int64_t rows = num_pages * h->page_size;
+  const int32_t per = w.cols / h->G;        // tokens of a unit
+  CUtensorMap tmq, tmk, tmv, smk, smv;
+  if (!biattn::encode_rows(&tmq, q, T, h->Hq, h->D, h->G, per)) return BI_GEMM_ERR_CUDA;
+  // The own units run as in bi_attention_run (its choice between three and four blocks per SM needs
+  // the unit count, which only the device knows here: three); the groups' units load pages as TMA
+  // boxes where a block is whole pages.  All give the same bits.
+  const bool in_range = num_pages > 0 && rows + h->page_size < (int64_t(1) << 31);
+  const bool use_tma = h->tma && in_range &&
+                       biattn::encode_cache(&tmk, k_cache, rows, h->Hkv, h->D, h->page_size) &&
+                       biattn::encode_cache(&tmv, v_cache, rows, h->Hkv, h->D, h->page_size);
+  std::memset(&smk, 0, sizeof(smk));
+  std::memset(&smv, 0, sizeof(smv));
+  const int box = std::min(h->page_size, biattn_tc::kBlockPos);
+  const bool shared_tma = biattn_tc::tma_page_size(h->page_size) && in_range &&
+                          biattn::encode_rows(&smk, k_cache, rows, h->Hkv, h->D, 1, box) &&
+                          biattn::encode_rows(&smv, v_cache, rows, h->Hkv, h->D, 1, box);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (w.total > h->ws_bytes) {
+    if (h->ws) cudaFreeAsync(h->ws, st);
+    h->ws = nullptr;
+    h->ws_bytes = 0;
+    void* ws = nullptr;
+    if (cudaMallocAsync(&ws, w.total, st) != cudaSuccess) {
+      cudaGetLastError();
+      return BI_GEMM_ERR_OOM;
+    }
+    h->ws = ws;
+    h->ws_bytes = w.total;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  biattn::SharedParams sp;
+  std::memset(&sp, 0, sizeof(sp));
+  biattn::Params& p = sp.a;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_seq = q_seq;
+  p.q_pos = q_pos;
+  p.kc = static_cast<const uint16_t*>(k_cache);
+  p.vc = static_cast<const uint16_t*>(v_cache);
+  p.table = page_table;
+  p.o = static_cast<uint16_t*>(o);
+  p.cum = reinterpret_cast<int32_t*>(ws + w.base.cum);
+  p.urec = reinterpret_cast<int4*>(ws + w.base.urec);
+  p.part = reinterpret_cast<float*>(ws + w.base.part);
+  p.ml = reinterpret_cast<float*>(ws + w.base.ml);
+  p.status = h->d_status;
+  p.T = T;
+  p.num_pages = num_pages;
+  p.B = num_seqs;
+  p.max_pages = max_pages;
+  p.Hq = h->Hq;
+  p.Hkv = h->Hkv;
+  p.page_size = h->page_size;
+  p.split = h->split;
+  p.max_splits = int32_t(max_pos / h->split + 1);
+  p.max_pos = int32_t(max_pos);
+  p.c = h->scale * 1.4426950408889634f;   // log2(e)
+  p.nstage = h->nstage;
+  p.stall_block = -1;
+  p.timeout_ns = biattn::kTimeoutNs;
+  sp.group_start = group_start;
+  sp.group_len = group_len;
+  sp.nsh = reinterpret_cast<int32_t*>(ws + w.nsh);
+  sp.srec = reinterpret_cast<int4*>(ws + w.srec);
+  sp.count = reinterpret_cast<int32_t*>(ws + w.count);
+  sp.c.kc = p.kc;
+  sp.c.vc = p.vc;
+  sp.c.table = page_table;
+  sp.c.num_pages = num_pages;
+  sp.c.max_pages = max_pages;
+  sp.c.Hkv = h->Hkv;
+  sp.c.page_size = h->page_size;
+  sp.num_groups = num_groups;
+  sp.cap = w.cap;
+  sp.cols = w.cols;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto launch = [&](const void* fn, int64_t grid, int threads, size_t smem, void** args) {
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess;
+  };
+  void* plan_args[1] = {&sp};
+  void* shared_args[4] = {&tmq, &smk, &smv, &sp};
+  void* own_args[1] = {&p};
+  void* own_tma_args[3] = {&tmk, &tmv, &p};
+  const int64_t units = T * h->Hkv * int64_t(p.max_splits);
+  const bool ok =
+      launch(reinterpret_cast<const void*>(&biattn::plan_shared_kernel), 1, 1024, 0, plan_args) &&
+      launch(shared_tma ? h->shared.tma : h->shared.rows, std::min<int64_t>(w.cap * h->Hkv, h->num_sms),
+             biattn::kSharedThreads, size_t(h->shared.smem), shared_args) &&
+      (use_tma ? launch(h->kern.tma, std::min<int64_t>(units, h->tma_ctas), h->kern.tma_threads, h->tma_smem,
+                        own_tma_args)
+               : launch(h->kern.fn, std::min<int64_t>(units, h->max_ctas), biattn::kThreads, h->smem, own_args)) &&
+      launch((p.max_splits + 3) / 4 <= 4 ? h->kern.merge : h->kern.merge_long, T * h->Hkv * h->kern.merge_slices,
+             biattn::kMergeThreads, 0, own_args);
+  if (!ok) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  return BI_GEMM_OK;
 }
 
 BI_GEMM_API int bi_attention_get_device_error(bi_attention_t h, void* stream) {

@@ -83,3 +83,11 @@ def test_prompt_null_arguments():
     assert L.bi_prompt_get_device_error(None, None) == INVALID
     assert L.bi_prompt_get_config(None, None) == INVALID
     assert L.bi_prompt_destroy(None) == bg.BI_GEMM_OK
+
+
+def test_shared_attention_null_arguments():
+    L = bg.library()
+    b = ctypes.c_uint64()
+    assert L.bi_attention_run_shared(None, None, 1, None, None, None, None, 1, None, 1, 1, 0, None, None, 1, None,
+                                     None) == INVALID
+    assert L.bi_attention_shared_workspace_size(None, 1, 1, 1, ctypes.byref(b)) == INVALID

@@ -1,0 +1,247 @@
+"""Decode attention over groups that share a prefix (bi_attention_run_shared) on the GPU: for every
+call the bits of bi_attention_run on the same tokens (whose values the decode attention's tests hold
+to the oracle), and fp64 attention for one call of each head dimension; groups of all sizes and
+lengths, several tokens of one request, page and split sizes, values that are not finite, zeros of
+both signs; bad groups; streams and graphs."""
+import numpy as np
+import pytest
+import torch
+
+import invariant_bi_gemm_gb300 as bg
+from invariant_bi_gemm_gb300 import BiAttention
+
+pytestmark = pytest.mark.gpu
+
+
+class Groups:
+    """groups: [(prefix, [own tokens of each request])]; pages of the prefix's whole pages in common,
+    its rest copied; one query token per request at its last position; `more`: further (request,
+    position) tokens placed at the end, outside every group."""
+
+    def __init__(self, groups, Hq, Hkv, D, page, seed=3, more=()):
+        g = torch.Generator().manual_seed(seed)
+        rn = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)
+        tables, lens, start, share = [], [], [0], []
+        pages_k, pages_v = [], []
+        order_at = 0
+
+        def add(k, v):
+            """Pages holding rows k, v; returns their ids."""
+            nonlocal order_at
+            n = -(-k.shape[0] // page)
+            ids = list(range(order_at, order_at + n))
+            order_at += n
+            for i in range(n):
+                for dst, src in ((pages_k, k), (pages_v, v)):
+                    pg = torch.full((page, Hkv, D), float("nan"), dtype=torch.bfloat16)
+                    part = src[i * page:(i + 1) * page]
+                    pg[:len(part)] = part
+                    dst.append(pg)
+            return ids
+
+        for prefix, owns in groups:
+            k, v = rn(prefix, Hkv, D), rn(prefix, Hkv, D)
+            whole = prefix // page
+            common = add(k[:whole * page], v[:whole * page])
+            for own in owns:
+                mk, mv = rn(own, Hkv, D), rn(own, Hkv, D)
+                rest = add(torch.cat([k[whole * page:], mk]), torch.cat([v[whole * page:], mv]))
+                tables.append(common + rest)
+                lens.append(prefix + own)
+            start.append(start[-1] + len(owns))
+            share.append(whole * page)
+        perm = torch.randperm(order_at + 2, generator=g)
+        self.kc = torch.full((order_at + 2, page, Hkv, D), float("nan"), dtype=torch.bfloat16)
+        self.vc = self.kc.clone()
+        self.kc[perm[:order_at]], self.vc[perm[:order_at]] = torch.stack(pages_k), torch.stack(pages_v)
+        self.table = torch.full((len(tables), max(map(len, tables))), -1, dtype=torch.int32)
+        for b, ids in enumerate(tables):
+            self.table[b, :len(ids)] = perm[torch.tensor(ids, dtype=torch.long)].to(torch.int32)
+        tokens = [(b, n - 1) for b, n in enumerate(lens)] + list(more)
+        self.q_seq = torch.tensor([b for b, _ in tokens], dtype=torch.int32)
+        self.q_pos = torch.tensor([p for _, p in tokens], dtype=torch.int32)
+        self.q = rn(len(tokens), Hq, D)
+        self.start, self.len = torch.tensor(start, dtype=torch.int32), torch.tensor(share, dtype=torch.int32)
+        self.max_pos = int(self.q_pos.max())
+
+    def args(self):
+        return [x.cuda() for x in (self.q, self.q_seq, self.q_pos, self.kc, self.vc, self.table)] + [self.max_pos]
+
+    def both(self, h):
+        a = self.args()
+        plain = h.run(*a)
+        assert h.device_error() == 0
+        shared = h.run_shared(*a, self.start.cuda(), self.len.cuda())
+        assert h.device_error() == 0
+        return bits(plain), bits(shared)
+
+
+def bits(x):
+    return x.view(torch.int16)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,split", [
+    (32, 8, 128, 16, 0), (32, 8, 128, 16, 128), (32, 8, 128, 64, 1024), (8, 1, 128, 32, 256), (4, 4, 128, 8, 512),
+    (16, 8, 128, 128, 384), (16, 2, 64, 16, 0), (8, 8, 64, 32, 256), (8, 4, 64, 8, 1024), (16, 4, 64, 256, 128),
+    (32, 8, 128, 5, 0), (16, 2, 64, 12, 128), (4, 4, 64, 1, 256), (8, 1, 128, 7, 640),
+])
+def test_bits_of_run(Hq, Hkv, D, page, split):
+    """Groups of one, few and many tokens, prefixes below, at and above split borders, own tails over a
+    border, and tokens in no group."""
+    s = split or 512
+    groups = [(2 * s + 37, [1, 5, s + 3, 40]), (s - 1, [1, 2]), (s, [1, 2, 3]), (3 * s, [7]),
+              (s + page, [1 + 3 * i for i in range(37)]), (10, [4, 5])]
+    gr = Groups(groups, Hq, Hkv, D, page, more=[(0, 2 * s + 30), (3, 5)])
+    h = BiAttention(Hq, Hkv, D, page, split_size=split)
+    plain, shared = gr.both(h)
+    assert torch.equal(plain, shared)
+    h.close()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (16, 2, 64)])
+def test_long_prefix_and_fp64(Hq, Hkv, D):
+    gr = Groups([(9000, [1 + 17 * i for i in range(70)])], Hq, Hkv, D, 16)
+    h = BiAttention(Hq, Hkv, D, 16)
+    plain, shared = gr.both(h)
+    assert torch.equal(plain, shared)
+    o = shared.view(torch.bfloat16).double().cpu()
+    for t in (0, 31, 69):
+        L = int(gr.q_pos[t]) + 1
+        slot = gr.table[t, torch.arange(L) // 16].long() * 16 + torch.arange(L) % 16
+        k, v = (x.view(-1, Hkv, D)[slot].double().repeat_interleave(Hq // Hkv, 1) for x in (gr.kc, gr.vc))
+        sc = torch.einsum("hd,lhd->hl", gr.q[t].double(), k) * D**-0.5
+        w = torch.softmax(sc, 1)
+        val, a = torch.einsum("hl,lhd->hd", w, v), torch.einsum("hl,lhd->hd", w, v.abs())
+        u = 2.0**-24       # the decode attention's bound
+        tol = 2.0**-8 * val.abs() + (4 * (D + 8) * u * sc.abs().amax(1, keepdim=True) + 2 * (L + 32) * u) * a
+        assert bool(((o[t] - val).abs() <= tol).all())
+    h.close()
+
+
+def test_tokens_of_one_request_and_positions_inside_the_prefix():
+    """A group may hold a chunk of a request and tokens whose position lies inside the prefix: each
+    shares the splits before its own."""
+    Hq, Hkv, D = 16, 4, 128
+    base = Groups([(2000, [10, 20])], Hq, Hkv, D, 16)
+    tokens = [(0, p) for p in (3, 511, 512, 700, 1023, 1024, 1999, 2009)] + [(1, p) for p in (1, 600, 1500, 2019)]
+    base.q_seq = torch.tensor([b for b, _ in tokens], dtype=torch.int32)
+    base.q_pos = torch.tensor([p for _, p in tokens], dtype=torch.int32)
+    base.q = torch.randn(12, Hq, D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    base.start = torch.tensor([0, 12], dtype=torch.int32)
+    h = BiAttention(Hq, Hkv, D, 16)
+    plain, shared = base.both(h)
+    assert torch.equal(plain, shared)
+    h.close()
+
+
+def test_zeros_infinities_and_nan():
+    """Zeros of both signs as queries, keys and values; infinities and NaN in the prefix: the bits of
+    run (any NaN for a NaN)."""
+    Hq, Hkv, D = 8, 2, 64
+    gr = Groups([(1100, [3, 4, 5])], Hq, Hkv, D, 16)
+    gr.q[0, 0] = 0.0
+    gr.q[1, 1] = -0.0
+    flat_k, flat_v = gr.kc.view(-1, Hkv, D), gr.vc.view(-1, Hkv, D)
+    slot = lambda p: int(gr.table[0, p // 16]) * 16 + p % 16
+    for p in range(1100 // 16 * 16):
+        flat_v[slot(p), 0, 3] = -0.0
+        flat_v[slot(p), 0, 4] = 0.0
+    flat_k[slot(100), 1, 5] = float("inf")
+    flat_v[slot(700), 0, 9] = float("-inf")
+    flat_v[slot(701), 0, 10] = float("nan")
+    h = BiAttention(Hq, Hkv, D, 16)
+    plain, shared = (x.view(torch.bfloat16) for x in gr.both(h))
+    assert torch.equal(plain.isnan(), shared.isnan())
+    fine = ~plain.isnan()
+    assert torch.equal(bits(plain[fine]), bits(shared[fine]))
+    assert bool(plain.isnan().any()) and bool(plain.isinf().any())
+    h.close()
+
+
+def test_independent_of_grouping():
+    """The same 20 tokens as one group, as groups of 7, 1 and 12, and with a shorter common length."""
+    gr = Groups([(3000, [1 + 9 * i for i in range(20)])], 32, 8, 128, 16)
+    h = BiAttention(32, 8, 128, 16)
+    want, got = gr.both(h)
+    assert torch.equal(want, got)
+    for start, lens in (([0, 7, 8, 20], [2992, 2992, 2992]), ([0, 20], [1024]), ([0, 20], [0]), ([3, 11], [2000]),
+                        ([0, 0, 20, 20], [5, 2992, 7])):
+        gr.start, gr.len = torch.tensor(start, dtype=torch.int32), torch.tensor(lens, dtype=torch.int32)
+        assert torch.equal(gr.both(h)[1], want), start
+    h.close()
+
+
+@pytest.mark.parametrize("what", ["descending", "past the end", "negative length", "other pages", "position", "page"])
+def test_bad_groups_are_reported(what):
+    gr = Groups([(1100, [3, 40, 5]), (1500, [1, 2])], 8, 2, 64, 16)
+    h = BiAttention(8, 2, 64, 16)
+    good = gr.both(h)[0]
+    start, length, mp = gr.start.clone(), gr.len.clone(), gr.max_pos
+    table, pos = gr.table.clone(), gr.q_pos.clone()
+    if what == "descending":
+        gr.start[1] = 6
+    elif what == "past the end":
+        gr.start[2] = 9
+    elif what == "negative length":
+        gr.len[1] = -1
+    elif what == "other pages":
+        gr.table[1, 5] = gr.table[1, 6]
+    elif what == "position":
+        gr.q_pos[4] = -1
+    else:
+        gr.table[3:, 2] = -1
+    a = gr.args()
+    o = h.run_shared(*a, gr.start.cuda(), gr.len.cuda())
+    assert h.device_error() == bg.BI_GEMM_ERR_INVALID_ARG and h.device_error() == 0
+    if what in ("past the end", "negative length", "page"):
+        assert torch.equal(bits(o)[:3], good[:3])
+    gr.start, gr.len, gr.table, gr.q_pos = start, length, table, pos
+    assert torch.equal(gr.both(h)[1], good)
+    h.close()
+
+
+def test_refusals_and_empty_calls():
+    gr = Groups([(600, [3, 4])], 8, 2, 64, 16)
+    h = BiAttention(8, 2, 64, 16)
+    a, s, n = gr.args(), gr.start.cuda(), gr.len.cuda()
+    want = bits(h.run(*a))
+    for bad in ((s[:1], n), (s.long(), n), (s, n.cpu()), (s, n.float())):
+        with pytest.raises(ValueError):
+            h.run_shared(*a, *bad)
+    with pytest.raises(bg.BiGemmError):
+        h.run_shared(*a[:-1], -1, s, n)
+    assert torch.equal(bits(h.run_shared(*a, s[:1], n[:0])), want)          # no group
+    empty = [a[0][:0], a[1][:0], a[2][:0]] + a[3:]
+    assert h.run_shared(*empty, torch.zeros(2, dtype=torch.int32, device="cuda"), n).shape[0] == 0
+    assert h.shared_workspace_size(2, 600, 1) > h.workspace_size(2, 600)
+    h.close()
+
+
+def test_repeat_stream_and_graph():
+    gr = Groups([(2600, [1 + 11 * i for i in range(40)]), (700, [2, 3])], 32, 8, 128, 16)
+    h = BiAttention(32, 8, 128, 16)
+    want, got = gr.both(h)
+    assert torch.equal(want, got)
+    a, s, n = gr.args(), gr.start.cuda(), gr.len.cuda()
+    for _ in range(20):
+        assert torch.equal(bits(h.run_shared(*a, s, n)), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = h.run_shared(*a, s, n)
+    side.synchronize()
+    assert torch.equal(bits(got), want)
+    out = torch.zeros_like(a[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h.run_shared(*a, s, n, o=out)
+    a[2].copy_(a[2] - 1)                       # replayed with other positions and queries
+    a[0].copy_(a[0].flip(0).contiguous())
+    other = BiAttention(32, 8, 128, 16)
+    want2 = bits(other.run(*a))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), want2)
+    assert h.device_error() == 0 and other.device_error() == 0
+    h.close()
+    other.close()
