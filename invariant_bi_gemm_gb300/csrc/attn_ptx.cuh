@@ -3,6 +3,9 @@
 #pragma once
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <mutex>
 
 #include "ptx.cuh"
 
@@ -24,6 +27,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// As tma_load_3d, five dimensions.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
 
@@ -59,10 +72,42 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Three-input maximum (a NaN is passed over), and packed pairs of fp32 in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start, leading / stride byte offsets, version 1.
@@ -108,11 +153,30 @@ struct Cache {
   int32_t Hkv, page_size;
 };
 
-// One 128-position block of one KV head goes to shared memory as D / 64 column halves of 128 rows
-// of 128 bytes, 128-byte swizzled (16-byte chunk c of row r at chunk c ^ (r % 8)), whoever writes it:
+// One 128-position block of one KV head goes to shared memory as 16 groups of 8 rows, a group as its
+// D / 64 column halves of 8 rows of 128 bytes, 128-byte swizzled (16-byte chunk c of row r at chunk
+// c ^ (r % 8)).  So a page of any multiple of 8 rows is one TMA box (64 x 8 x halves x groups of the
+// cache seen as [Hkv][groups][halves][8][64]): a box costs its issue about 48 clocks, whatever it
+// holds, and with a box per page and half, pages of 16 positions had bounded the prompt kernel.
+template <int D>
+struct BlockLayout {
+  static constexpr uint32_t GROUP = D / 64 * 1024;            // bytes of 8 rows
+  static constexpr uint32_t HALF = 1024;                      // between the halves of a group
+  // 16-byte chunk c of row r
+  __device__ static uint32_t chunk(int r, int c) {
+    return uint32_t(r >> 3) * GROUP + uint32_t(c >> 3) * HALF + uint32_t((r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+  }
+  // descriptors of the block at `a`: rows as the MMA's rows or columns, k step of 16 dimensions ...
+  __device__ static uint64_t by_row(uint32_t a, int k) {
+    return sdesc_sw128(a + uint32_t(k >> 2) * HALF + uint32_t(k & 3) * 32, 16, GROUP);
+  }
+  // ... or dimensions as rows or columns, k step of 16 positions
+  __device__ static uint64_t by_dim(uint32_t a, int k) { return sdesc_sw128(a + uint32_t(k) * 2 * GROUP, HALF, GROUP); }
+};
+
 // `pg` holds lane l's page of the block (pages of min(page_size, 128) rows; -1: zeros), from
-// block_page.  TMA: lane l issues its page's boxes; a page outside the cache loads a box from past
-// the cache's end, which TMA fills with zeros.
+// block_page.  TMA: lane l issues its page's box; a page outside the cache loads a box from past the
+// cache's end, which TMA fills with zeros.
 __device__ __forceinline__ int32_t block_page(const Cache& c, const int32_t* row, int32_t pos0, int32_t last, int lane,
                                               bool* bad) {
   const int32_t step = c.page_size < kBlockPos ? c.page_size : kBlockPos;
@@ -135,9 +199,7 @@ __device__ __forceinline__ void load_block_tma(uint32_t dst, uint32_t bar, const
   if (lane * step < kBlockPos) {
     const int32_t row = page >= 0 ? page * c.page_size + (pos0 + lane * step) % c.page_size
                                   : int32_t(c.num_pages * c.page_size);
-#pragma unroll
-    for (int hh = 0; hh < D / 64; ++hh)
-      tma_load_3d(dst + uint32_t(hh * kBlockPos * 128 + lane * step * 128), m, bar, hh * 64, kh, row);
+    tma_load_5d(dst + uint32_t(lane * step / 8) * BlockLayout<D>::GROUP, m, bar, 0, 0, 0, row / 8, kh);
   }
 }
 
@@ -171,7 +233,7 @@ __device__ __forceinline__ void load_block_rows(uint32_t dst, const uint16_t* ba
       const int rl = i * RPI + sub;
       const int64_t o = __shfl_sync(0xFFFFFFFFu, off[k], rl);
       const int r = 32 * k + rl;
-      ptx::cp_async_16(dst + uint32_t((ch >> 3) * kBlockPos * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+      ptx::cp_async_16(dst + BlockLayout<D>::chunk(r, ch),
                        o >= 0 ? base + o + int64_t(kh) * D + ch * 8 : base, o >= 0 ? 16u : 0u);
     }
   }
@@ -179,5 +241,44 @@ __device__ __forceinline__ void load_block_rows(uint32_t dst, const uint16_t* ba
 
 // Page sizes whose blocks are whole TMA boxes: powers of two from 8 (one 1024-byte swizzle atom) up.
 inline bool tma_page_size(int64_t ps) { return ps >= 8 && (ps & (ps - 1)) == 0; }
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+inline bool encode_bf16(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                        const cuuint32_t* box) {
+  auto fn = encode_fn();
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), dims, strides, box,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows [T, H, D]: boxes of 64 dims x `heads` x `tokens`, zero fill outside.
+inline bool encode_queries(CUtensorMap* m, const void* q, int64_t T, int H, int D, int heads, int tokens) {
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
+  const cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(H) * D * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(heads), cuuint32_t(tokens)};
+  return encode_bf16(m, q, 3, dims, strides, box);
+}
+
+// A cache of `rows` = pages x page_size rows for load_block_tma.
+inline bool encode_pages(CUtensorMap* m, const void* cache, int64_t rows, int Hkv, int D, int page_size) {
+  const cuuint64_t pitch = cuuint64_t(Hkv) * D * 2;
+  const cuuint64_t dims[5] = {64, 8, cuuint64_t(D / 64), cuuint64_t(rows / 8), cuuint64_t(Hkv)};
+  const cuuint64_t strides[4] = {pitch, 128, 8 * pitch, cuuint64_t(D) * 2};
+  const cuuint32_t box[5] = {64, 8, cuuint32_t(D / 64), cuuint32_t((page_size < kBlockPos ? page_size : kBlockPos) / 8), 1};
+  return encode_bf16(m, cache, 5, dims, strides, box);
+}
 
 }  // namespace biattn_tc

@@ -1615,7 +1615,7 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
   const int64_t rows = num_pages * h->page_size;
   const int32_t per = w.cols / h->G;        // tokens of a unit
   CUtensorMap tmq, tmk, tmv, smk, smv;
-  if (!biattn::encode_rows(&tmq, q, T, h->Hq, h->D, h->G, per)) return BI_GEMM_ERR_CUDA;
+  if (!biattn_tc::encode_queries(&tmq, q, T, h->Hq, h->D, h->G, per)) return BI_GEMM_ERR_CUDA;
   // The own units run as in bi_attention_run (its choice between three and four blocks per SM needs
   // the unit count, which only the device knows here: three); the groups' units load pages as TMA
   // boxes where a block is whole pages.  All give the same bits.
@@ -1625,10 +1625,9 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
                        biattn::encode_cache(&tmv, v_cache, rows, h->Hkv, h->D, h->page_size);
   std::memset(&smk, 0, sizeof(smk));
   std::memset(&smv, 0, sizeof(smv));
-  const int box = std::min(h->page_size, biattn_tc::kBlockPos);
   const bool shared_tma = biattn_tc::tma_page_size(h->page_size) && in_range &&
-                          biattn::encode_rows(&smk, k_cache, rows, h->Hkv, h->D, 1, box) &&
-                          biattn::encode_rows(&smv, v_cache, rows, h->Hkv, h->D, 1, box);
+                          biattn_tc::encode_pages(&smk, k_cache, rows, h->Hkv, h->D, h->page_size) &&
+                          biattn_tc::encode_pages(&smv, v_cache, rows, h->Hkv, h->D, h->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (w.total > h->ws_bytes) {
     if (h->ws) cudaFreeAsync(h->ws, st);

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t o = uint32_t((k >> 2) * 128 * 128 + (k & 3) * 32);
-              ptx::mma_bf16(tmem + uint32_t(b * sp.cols), tc::sdesc_sw128(ka + o, 16, 1024),
+              ptx::mma_bf16(tmem + uint32_t(b * sp.cols), tc::BlockLayout<D>::by_row(ka, k),
                             tc::sdesc_sw128(sbase + o, 16, 1024), id_qk, k ? 1u : 0u);
             }
             issued = true;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               const uint32_t od = tmem + uint32_t(i ? x.c0 : 0);
 #pragma unroll
               for (int k = 0; k < tc::kBlockPos / 16; ++k) {
-                const uint64_t vd = tc::sdesc_sw128(va + uint32_t(k * 16 * 128), tc::kBlockPos * 128, 1024);
+                const uint64_t vd = tc::BlockLayout<D>::by_dim(va, k);
                 ptx::mma_bf16(od, vd, tc::sdesc_sw128(ph + uint32_t(k * 16 * 128), 16, 1024), id_pv, (b | k) ? 1u : 0u);
                 ptx::mma_bf16(od, vd, tc::sdesc_sw128(pl + uint32_t(k * 16 * 128), 16, 1024), id_pv, 1u);
               }
@@ -601,19 +601,6 @@ inline SharedInfo select_shared(int D, int G) {
     }
   }
   return SharedInfo{};
-}
-
-// [rows, H, D] bf16 as a 3-D tensor; boxes of 64 dims x `heads` x `box` rows, zero fill outside.
-bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int H, int D, int heads, int box) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(rows)};
-  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(H) * D * 2};
-  cuuint32_t b[3] = {64, cuuint32_t(heads), cuuint32_t(box)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, b, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace biattn

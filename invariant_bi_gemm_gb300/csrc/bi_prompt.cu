@@ -26,13 +26,11 @@
 // TMEM (512 columns): S0 / P0, S1 / P1 (128 each), O0, O1 (D each).
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 #include <new>
 
 #include "../../include/bi_prompt.h"
@@ -419,73 +417,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer (lane 0 issues)
+      // ------------------------------------------------------------ MMA issuer
+      // The tensor pipe holds about four MMAs (256 clocks) beside the one that runs, so whatever lies
+      // between two batches of eight has to be short: ring stages and phases are counted, not divided
+      // out, descriptors are added up from constants, and the whole warp walks the waits (one lane,
+      // chosen once, issues), which keeps all of it in uniform registers.
+      const bool lead = elect_one();
+      const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + C::TILE_BYTES, 16, 1024)};
+      const uint64_t kd0 = BlockLayout<D>::by_row(sbase + C::OFF_RING, 0);
+      const uint64_t vd0 = BlockLayout<D>::by_dim(sbase + C::OFF_RING, 0);
+      constexpr uint64_t kStep = C::STAGE_BYTES >> 4;
       Unit u;
-      uint32_t seq = 0, nu = 0, cleaned = 0, np[2] = {0, 0};
+      uint32_t st = 0, ph = 0;                // stage and phase of the next load to consume
+      uint32_t nu = 0, cleaned = 0, np[2] = {0, 0};
       bool ok = true, issued = false;
-      while (ok && next_unit(u)) {
-        if (lane == 0) {
-          const int32_t nb = max(u.nb[0], u.nb[1]);
-          const int32_t dirty = (u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1;   // cleaned from this block on
-          auto qk = [&](int i, uint32_t s) {
-            const uint32_t qa = sbase + uint32_t(i * C::TILE_BYTES);
-            const uint32_t ka = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
+      auto advance = [&]() {
+        if (++st == uint32_t(NS)) st = 0, ph ^= 1u;
+      };
+      auto qk = [&](int i, uint32_t s) {
+        if (lead) {
+          const uint64_t kd = kd0 + s * kStep;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t o = uint32_t((k >> 2) * 128 * 128 + (k & 3) * 32);
-              ptx::mma_bf16(tmem + uint32_t(i * 128), sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024),
-                            C::IDESC_QK, k ? 1u : 0u);
-            }
-            ptx::tc_commit(s_full(i));
-            issued = true;
-          };
-          ok = wait_bar(q_full, nu & 1u, sy) && wait_bar(full(seq % NS), (seq / NS) & 1u, sy);
-          if (ok) {
-            ptx::tc_fence_after();
-            for (int i = 0; i < 2; ++i)
-              if (u.nb[i] > 0) qk(i, seq % NS);
-            ptx::tc_commit(empty(seq % NS));
-            if (nb == 1) ptx::tc_commit(q_empty);
+          for (int k = 0; k < D / 16; ++k)
+            ptx::mma_bf16(tmem + uint32_t(i * 128), qd[i] + uint64_t(((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
+                          kd + uint64_t(((k >> 2) * BlockLayout<D>::HALF + (k & 3) * 32) >> 4), C::IDESC_QK, k ? 1u : 0u);
+          ptx::tc_commit(s_full(i));
+        }
+      };
+      while (ok && next_unit(u)) {
+        const int32_t nb0 = u.nb[0], nb1 = u.nb[1], nb = max(nb0, nb1);
+        const int32_t dirty = (nb0 > 0 ? nb0 : nb1) - 1;             // cleaned from this block on
+        ok = wait_bar(q_full, nu & 1u, sy) && wait_bar(full(st), ph, sy);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        issued = true;
+        if (nb0 > 0) qk(0, st);
+        if (nb1 > 0) qk(1, st);
+        if (lead) {
+          ptx::tc_commit(empty(st));
+          if (nb == 1) ptx::tc_commit(q_empty);
+        }
+        advance();
+        for (int32_t j = 0; j < nb; ++j) {
+          const uint32_t vs = st, vph = ph;                          // this block's values
+          advance();
+          const uint32_t ks = st, kph = ph;                          // the next block's keys
+          const bool more = j + 1 < nb;
+          ok = wait_bar(full(vs), vph, sy);
+          if (j >= dirty) {
+            ok = ok && wait_bar(clean(vs), (cleaned >> vs) & 1u, sy);
+            cleaned ^= 1u << vs;
           }
-          for (int32_t j = 0; j < nb && ok; ++j) {
-            const uint32_t vs = seq + 1, ks = seq + 2;           // this block's values, the next one's keys
-            ok = wait_bar(full(vs % NS), (vs / NS) & 1u, sy);
-            if (ok && j >= dirty) {
-              ok = wait_bar(clean(vs % NS), (cleaned >> (vs % NS)) & 1u, sy);
-              cleaned ^= 1u << (vs % NS);
-            }
-            for (int i = 0; i < 2 && ok; ++i) {
-              if (j >= u.nb[i]) continue;
-              ok = wait_bar(p_full(i), np[i] & 1u, sy);
-              if (!ok) break;
-              ++np[i];
-              ptx::tc_fence_after();
-              const uint32_t va = sbase + uint32_t(C::OFF_RING) + (vs % NS) * uint32_t(C::STAGE_BYTES);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int32_t nbi = i ? nb1 : nb0;
+            if (j >= nbi) continue;
+            ok = ok && wait_bar(p_full(i), np[i] & 1u, sy);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            ++np[i];
+            ptx::tc_fence_after();
+            if (lead) {
+              const uint64_t vd = vd0 + vs * kStep;
 #pragma unroll
               for (int k = 0; k < kBlockPos / 16; ++k)
                 mma_bf16_ta(tmem + uint32_t(256 + i * D), tmem + uint32_t(i * 128 + k * 8),
-                            sdesc_sw128(va + uint32_t(k * 16 * 128), kBlockPos * 128, 1024), C::IDESC_PV,
-                            (j | k) ? 1u : 0u);
-              issued = true;
-              if (j + 1 == u.nb[i]) ptx::tc_commit(o_done(i));
-              else if ((ok = wait_bar(full(ks % NS), (ks / NS) & 1u, sy))) {
-                ptx::tc_fence_after();
-                qk(i, ks % NS);
-              }
+                            vd + uint64_t((k * 2 * BlockLayout<D>::GROUP) >> 4), C::IDESC_PV, (j | k) ? 1u : 0u);
+              if (j + 1 == nbi) ptx::tc_commit(o_done(i));
             }
-            if (!ok) break;
-            ptx::tc_commit(empty(vs % NS));
-            if (j + 1 < nb) {
-              ptx::tc_commit(empty(ks % NS));
-              if (j + 2 == nb) ptx::tc_commit(q_empty);
+            if (j + 1 < nbi) {
+              ok = wait_bar(full(ks), kph, sy);
+              ok = __all_sync(0xFFFFFFFFu, ok);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              qk(i, ks);
             }
-            seq += 2;
           }
-          ++nu;
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (lead) {
+            ptx::tc_commit(empty(vs));
+            if (more) ptx::tc_commit(empty(ks));
+            if (j + 2 == nb) ptx::tc_commit(q_empty);
+          }
+          if (more) advance();
         }
-        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        ++nu;
       }
-      if (lane == 0 && issued) {     // no MMA of ours may be in flight when TMEM is released
+      if (lead && issued) {          // no MMA of ours may be in flight when TMEM is released
         volatile uint32_t none = 0;
         const Sync end{&none, p.status, p.timeout_ns};
         ptx::tc_commit(drain);
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (hit) {
               ptx::st_shared_v4(a, w[0], w[1], w[2], w[3]);
-              found |= j * kBlockPos + (e / 8) % kBlockPos <= u.last;   // (unused slots: nobody sees them)
+              found |= j * kBlockPos + e / (8 * C::HALVES * 8) * 8 + (e / 8) % 8 <= u.last;   // (unused slots: nobody sees them)
             }
           }
           if (__any_sync(0xFFFFFFFFu, found) && lane == 0) bad_v[nu & 3u] = nu + 1;
@@ -577,14 +597,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e > lim) s[c][e] = 0xFF800000u;
         }
-        float mx[4];
+        // eight chains of three-input maxima
+        float mx[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
+        for (int k = 0; k < 8; ++k) mx[k] = __uint_as_float(s[k >> 1][(k & 1) * 16]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
-        }
-        const float mb = __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), p.scale_log2);
+        for (int e = 1; e < 15; e += 2)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mx[k] = max3(mx[k], __uint_as_float(s[k >> 1][(k & 1) * 16 + e]),
+                         __uint_as_float(s[k >> 1][(k & 1) * 16 + e + 1]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(s[k >> 1][(k & 1) * 16 + 15]));
+        const float mb = __fmul_rn(max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])),
+                                   p.scale_log2);
         float f = 1.0f;
         if (mb > m + kSlack || m == -INFINITY) {
           f = m == -INFINITY ? 1.0f : ex2(__fsub_rn(m, mb));      // (nothing to shrink yet)
@@ -604,22 +630,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;   // a row of -infinity so far: weights of zero
-        float ls[4];
+        const uint64_t sc2 = pair(p.scale_log2, p.scale_log2), ref2 = pair(-ref, -ref);
+        uint64_t ls[4] = {0, 0, 0, 0};             // four pairs of partial sums
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
-          ls[c] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float w0 = ex2(__fmaf_rn(__uint_as_float(s[c][e]), p.scale_log2, -ref));
-            const float w1 = ex2(__fmaf_rn(__uint_as_float(s[c][e + 1]), p.scale_log2, -ref));
-            ls[c] = __fadd_rn(ls[c], w0);
-            ls[c] = __fadd_rn(ls[c], w1);
+            const uint64_t x = fma2(pair(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), sc2, ref2);
+            float w0, w1;
+            unpair(x, w0, w1);
+            w0 = ex2(w0);
+            w1 = ex2(w1);
+            ls[(e >> 1) & 3] = add2(ls[(e >> 1) & 3], pair(w0, w1));
             pk[e >> 1] = ptx::pack_bf16x2(w0, w1);
           }
           tmem_st_x16(ts + uint32_t(c * 16), pk);
         }
-        l = __fadd_rn(l, __fadd_rn(__fadd_rn(ls[0], ls[1]), __fadd_rn(ls[2], ls[3])));
+        float l0, l1;
+        unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), l0, l1);
+        l = __fadd_rn(l, __fadd_rn(l0, l1));
         tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -712,32 +742,6 @@ inline KernelInfo select(int D, int G) {
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// [rows, H, D] bf16 as a 3-D tensor; boxes of 64 dims x `heads` x `box` rows, zero fill outside.
-bool encode(CUtensorMap* m, const void* base, int64_t rows, int H, int D, int heads, int box) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(rows)};
-  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(H) * D * 2};
-  cuuint32_t b[3] = {64, cuuint32_t(heads), cuuint32_t(box)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, b, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace biprompt
 
 struct bi_prompt {
@@ -791,7 +795,7 @@ BI_GEMM_API int bi_prompt_create(bi_prompt_t* out, int64_t num_q_heads, int64_t 
     return BI_GEMM_ERR_CUDA;
   }
   if (major != 10 || minor != 3) return BI_GEMM_ERR_UNSUPPORTED;
-  if (!biprompt::encode_fn() ||
+  if (!biattn_tc::encode_fn() ||
       cudaFuncSetAttribute(k.tma, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
       cudaFuncSetAttribute(k.rows, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) {
     cudaGetLastError();
@@ -854,15 +858,14 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
   CUtensorMap tmq, tmk, tmv;
   std::memset(&tmk, 0, sizeof(tmk));
   std::memset(&tmv, 0, sizeof(tmv));
-  if (!biprompt::encode(&tmq, q, T, h->Hq, h->D, h->G, 128 / h->G)) return BI_GEMM_ERR_CUDA;
+  if (!biattn_tc::encode_queries(&tmq, q, T, h->Hq, h->D, h->G, 128 / h->G)) return BI_GEMM_ERR_CUDA;
   // TMA boxes need whole pages and row coordinates (one page past the end included) of 32 bits;
   // otherwise rows are copied: the same bits.
   const int64_t rows = num_pages * h->page_size;
-  const int box = std::min(h->page_size, biattn_tc::kBlockPos);
   const bool tma = biattn_tc::tma_page_size(h->page_size) && num_pages > 0 &&
                    rows + h->page_size < (int64_t(1) << 31) &&
-                   biprompt::encode(&tmk, k_cache, rows, h->Hkv, h->D, 1, box) &&
-                   biprompt::encode(&tmv, v_cache, rows, h->Hkv, h->D, 1, box);
+                   biattn_tc::encode_pages(&tmk, k_cache, rows, h->Hkv, h->D, h->page_size) &&
+                   biattn_tc::encode_pages(&tmv, v_cache, rows, h->Hkv, h->D, h->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const PromptWs w = prompt_layout(h, T, B);
   if (w.total > h->ws_bytes) {
