@@ -72,6 +72,10 @@ __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void ld_shared_v4(uint32_t a, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -174,33 +178,31 @@ struct BlockLayout {
   __device__ static uint64_t by_dim(uint32_t a, int k) { return sdesc_sw128(a + uint32_t(k) * 2 * GROUP, HALF, GROUP); }
 };
 
-// `pg` holds lane l's page of the block (pages of min(page_size, 128) rows; -1: zeros), from
-// block_page.  TMA: lane l issues its page's box; a page outside the cache loads a box from past the
-// cache's end, which TMA fills with zeros.
-__device__ __forceinline__ int32_t block_page(const Cache& c, const int32_t* row, int32_t pos0, int32_t last, int lane,
-                                              bool* bad) {
+// TMA: lane l issues the box of the block's l-th page (of min(page_size, 128) rows).  block_box gives
+// its first group in the cache, ahead of the wait for the ring: the page at or behind `last` and a page
+// outside the cache (which sets *bad) load a box from past the cache's end, which TMA fills with zeros.
+__device__ __forceinline__ int32_t block_box(const Cache& c, const int32_t* row, int32_t pos0, int32_t last, int lane,
+                                             bool* bad) {
   const int32_t step = c.page_size < kBlockPos ? c.page_size : kBlockPos;
   const int32_t pos = pos0 + lane * step;
-  if (lane * step >= kBlockPos || pos > last) return -1;
+  const int32_t past = int32_t(c.num_pages * c.page_size / 8);
+  if (lane * step >= kBlockPos || pos > last) return past;
   const int32_t page = row[pos / c.page_size];
   if (page < 0 || page >= c.num_pages) {
     *bad = true;
-    return -1;
+    return past;
   }
-  return page;
+  return (page * c.page_size + pos % c.page_size) / 8;
 }
 
 template <int D>
 __device__ __forceinline__ void load_block_tma(uint32_t dst, uint32_t bar, const CUtensorMap* m, const Cache& c,
-                                               int32_t page, int32_t pos0, int32_t kh, int lane) {
+                                               int32_t box, int32_t kh, int lane) {
   const int32_t step = c.page_size < kBlockPos ? c.page_size : kBlockPos;
   if (lane == 0) ptx::mbar_arrive_expect_tx(bar, uint32_t(kBlockPos * D * 2));
   __syncwarp();
-  if (lane * step < kBlockPos) {
-    const int32_t row = page >= 0 ? page * c.page_size + (pos0 + lane * step) % c.page_size
-                                  : int32_t(c.num_pages * c.page_size);
-    tma_load_5d(dst + uint32_t(lane * step / 8) * BlockLayout<D>::GROUP, m, bar, 0, 0, 0, row / 8, kh);
-  }
+  if (lane * step < kBlockPos)
+    tma_load_5d(dst + uint32_t(lane * (step / 8)) * BlockLayout<D>::GROUP, m, bar, 0, 0, 0, box, kh);
 }
 
 // Any page size: lane l owns rows l, l + 32, l + 64, l + 96 of the block; off[k] = the row's element

@@ -296,13 +296,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           const int32_t pos0 = base + b * tc::kBlockPos;
           const uint32_t s = seq % NS, dst = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
           if constexpr (kTma) {
-            const int32_t page = tc::block_page(sp.c, trow, pos0, last, lane, &bad);
+            const int32_t box = tc::block_box(sp.c, trow, pos0, last, lane, &bad);
             if (seq >= uint32_t(NS)) {
               if (lane == 0) ok = tc::wait_bar(empty(s), (seq / NS - 1) & 1u, sy);
               ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
               if (!ok) break;
             }
-            tc::load_block_tma<D>(dst, full(s), i < nblk ? &tmk : &tmv, sp.c, page, pos0, x.kh, lane);
+            tc::load_block_tma<D>(dst, full(s), i < nblk ? &tmk : &tmv, sp.c, box, x.kh, lane);
           } else {
             int64_t off[4];
             tc::block_rows(sp.c, trow, pos0, last, D, lane, off, &bad);

@@ -16,10 +16,11 @@
 // request's own positions, so a row's arithmetic never depends on the chunk it came in.
 //
 // Warps (384 threads, one block per SM, persistent; units, longest first, from a counter):
-//   0       producer: takes units, loads the tiles' queries (TMA box: 64 dims x G heads x positions)
-//           and the ring of key and value blocks (K0, V0, K1, V1, ...), page by page
+//   0       takes units, loads the tiles' queries (TMA box: 64 dims x G heads x positions) and the
+//           key blocks, page by page, into the ring (K0, V0, K1, V1, ...)
 //   1       issues the MMAs:  S = Q K^T (both operands in shared memory), O += P V (P in TMEM)
-//   2, 3    clean the value blocks on the diagonal: rows a query must not see meet weights of zero,
+//   2       loads the value blocks (two warps, since a box takes about 48 clocks to issue)
+//   3       cleans the value blocks on the diagonal: rows a query must not see meet weights of zero,
 //           and zero times a value that is not finite is not zero.  Those values become zeros; for
 //           the rows that do see them, the epilogue adds them back (bad_v)
 //   4 - 11  softmax, a warpgroup per tile, a thread per row: S from TMEM, P to TMEM over S's columns
@@ -250,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(full(s), 1);
-      ptx::mbar_init(empty(s), 3);             // the MMAs' commit and the two cleaning warps
-      ptx::mbar_init(clean(s), 2);
+      ptx::mbar_init(empty(s), 2);             // the MMAs' commit and the cleaning warp
+      ptx::mbar_init(clean(s), 1);
     }
     for (int s = 0; s < kUnitSlots; ++s) {
       ptx::mbar_init(unit_full(s), 1);
@@ -303,26 +304,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     ptx::setmaxnreg_dec<80>();
-    if (warp == 0) {
-      // ------------------------------------------------------------ producer
-      const int32_t total = int32_t(p.counter[0]);
-      bool ok = true, bad = false;
-      uint32_t seq = 0, nun = 0;               // ring loads issued, units handed out
-      uint32_t q_issued = 0;                   // units whose queries were loaded
-      uint32_t late = 0;                       // row copies: loads not yet announced
-      auto announce = [&](uint32_t keep) {     // (row copies) loads up to seq - keep have landed
-        while (late > keep) {
-          if (keep == 1) ptx::cp_async_wait<1>();
-          else ptx::cp_async_wait<0>();
+    bool bad = false;                        // (loading warps) a page outside the cache
+    uint32_t late = 0, late_at = 0;          // (row copies) a load not yet announced, its ring number
+    auto announce = [&]() {
+      if (late) {
+        ptx::cp_async_wait<0>();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full(late_at % NS));
+        late = 0;
+      }
+    };
+    // Block j of a unit's keys or values as load number `n` of the ring; false once a wait gave up.
+    auto load = [&](bool values, const Unit& u, const int32_t* trow, int32_t j, uint32_t n) {
+      const uint32_t s = n % NS, dst = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
+      int32_t box = 0;
+      int64_t off[4];
+      if constexpr (kTma) box = block_box(p.c, trow, j * kBlockPos, u.last, lane, &bad);
+      else block_rows(p.c, trow, j * kBlockPos, u.last, D, lane, off, &bad);
+      if (n >= uint32_t(NS)) {
+        if constexpr (!kTma) {                 // nothing of ours may hold the wait up
+          if (!__all_sync(0xFFFFFFFFu, ptx::mbar_try_wait(empty(s), (n / NS - 1) & 1u))) announce();
+        }
+        const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(empty(s), (n / NS - 1) & 1u, sy));
+        if (!ok) return false;
+      }
+      if (int(blockIdx.x) == p.stall) return true;
+      if constexpr (kTma) {
+        load_block_tma<D>(dst, full(s), values ? &tmv : &tmk, p.c, box, u.kh, lane);
+      } else {
+        load_block_rows<D>(dst, values ? p.c.vc : p.c.kc, off, u.kh, lane);
+        ptx::cp_async_commit();
+        if (late) {                            // (the load before this one has had a block's time)
+          ptx::cp_async_wait<1>();
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(full((seq - late) % NS));
-          --late;
+          if (lane == 0) ptx::mbar_arrive(full(late_at % NS));
         }
-      };
+        late = 1, late_at = n;
+      }
+      return true;
+    };
+    if (warp == 0) {
+      // ------------------------------------------------------------ units, queries, keys
+      const int32_t total = int32_t(p.counter[0]);
+      bool ok = true;
+      uint32_t seq = 0, nun = 0;               // ring loads and units so far
+      uint32_t id = 0;
+      if (lane == 0) id = atomicAdd(p.counter + 1, 1u);
       while (ok) {
-        uint32_t id = 0;
-        if (lane == 0) id = atomicAdd(p.counter + 1, 1u);
         id = __shfl_sync(0xFFFFFFFFu, id, 0);
         Unit u;
         u.b = -1;
@@ -342,56 +372,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t t0 = u.base + i * C::P, t1 = t0 + C::P - 1;
             u.nb[i] = t1 >= u.first && t0 <= u.last ? t0 / kBlockPos + 1 : 0;
           }
-          if (u.nb[0] == 0 && u.nb[1] == 0) continue;     // (only from a q_start that descends)
+          if (lane == 0) id = atomicAdd(p.counter + 1, 1u);       // the next one, ahead of its use
+          if (u.nb[0] == 0 && u.nb[1] == 0) continue;             // (only from a q_start that descends)
         }
         const uint32_t us = nun % kUnitSlots;
         if (nun >= kUnitSlots) {
-          if (lane == 0) ok = wait_bar(unit_empty(us), (nun / kUnitSlots - 1) & 1u, sy);
-          ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(unit_empty(us), (nun / kUnitSlots - 1) & 1u, sy));
           if (!ok) break;
         }
         if (lane == 0) {
           units[us] = u;
           ptx::mbar_arrive(unit_full(us));
         }
-        ++nun;
         if (u.b < 0) break;
         const int32_t nb = max(u.nb[0], u.nb[1]);
         const int32_t* trow = p.c.table + int64_t(u.b) * p.c.max_pages;
-        int32_t page = 0;
-        int64_t off[4];
-        for (int32_t i = 0; i < 2 * nb && ok; ++i) {      // K0, V0, K1, V1, ...
-          const int32_t pos0 = (i >> 1) * kBlockPos;
-          if ((i & 1) == 0) {
-            if constexpr (kTma) page = block_page(p.c, trow, pos0, u.last, lane, &bad);
-            else block_rows(p.c, trow, pos0, u.last, D, lane, off, &bad);
-          }
-          const uint32_t s = seq % NS;
-          if (seq >= uint32_t(NS)) {
-            if (!kTma) announce(0);                       // nothing of ours may hold the wait up
-            if (lane == 0) ok = wait_bar(empty(s), (seq / NS - 1) & 1u, sy);
-            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        for (int32_t j = 0; j < nb && ok; ++j, seq += 2) {
+          ok = load(false, u, trow, j, seq);
+          if (ok && j == 0) {                                     // the queries behind the first key block
+            if (nun > 0) ok = __all_sync(0xFFFFFFFFu, wait_bar(q_empty, (nun - 1) & 1u, sy));
             if (!ok) break;
-          }
-          if (int(blockIdx.x) == p.stall) continue;
-          const uint32_t dst = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
-          if constexpr (kTma) {
-            load_block_tma<D>(dst, full(s), (i & 1) ? &tmv : &tmk, p.c, page, pos0, u.kh, lane);
-            ++seq;
-          } else {
-            load_block_rows<D>(dst, (i & 1) ? p.c.vc : p.c.kc, off, u.kh, lane);
-            ptx::cp_async_commit();
-            ++seq;
-            ++late;
-            announce(1);
-          }
-          if (i == 0) {                                   // the queries behind the first key block
-            if (q_issued > 0) {
-              if (lane == 0) ok = wait_bar(q_empty, (q_issued - 1) & 1u, sy);
-              ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-              if (!ok) break;
-            }
-            if (lane == 0) {
+            if (lane == 0 && int(blockIdx.x) != p.stall) {
               ptx::mbar_arrive_expect_tx(q_full, uint32_t((u.nb[0] > 0) + (u.nb[1] > 0)) * C::TILE_BYTES);
               for (int t = 0; t < 2; ++t)
                 if (u.nb[t] > 0)
@@ -399,23 +400,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(sbase + uint32_t(t * C::TILE_BYTES + hh * 128 * 128), &tmq, q_full, hh * 64,
                                 u.kh * G, u.row0 + t * C::P);
             }
-            ++q_issued;
           }
         }
-        if (!kTma) announce(0);
+        announce();
+        ++nun;
       }
       if (bad) atomicOr(p.status, kErrPage);
-      // no copy of ours may be in flight when the block leaves (bounded)
-      if (!kTma) ptx::cp_async_wait<0>();
-      if (lane == 0) {
-        volatile uint32_t none = 0;
-        const Sync end{&none, p.status, p.timeout_ns};
-        if (kTma)
-          for (uint32_t k = 0; k < uint32_t(NS) && k < seq; ++k)
-            wait_bar(full((seq - 1 - k) % NS), ((seq - 1 - k) / NS) & 1u, end);
-        if (q_issued > 0) wait_bar(q_full, (q_issued - 1) & 1u, end);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ values
+      Unit u;
+      uint32_t seq = 1;
+      bool ok = true;
+      while (ok && next_unit(u)) {
+        const int32_t nb = max(u.nb[0], u.nb[1]);
+        const int32_t* trow = p.c.table + int64_t(u.b) * p.c.max_pages;
+        for (int32_t j = 0; j < nb && ok; ++j, seq += 2) ok = load(true, u, trow, j, seq);
+        announce();
       }
-      __syncwarp();
+      if (bad) atomicOr(p.status, kErrPage);
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       // The tensor pipe holds about four MMAs (256 clocks) beside the one that runs, so whatever lies
@@ -485,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_bf16_ta(tmem + uint32_t(256 + i * D), tmem + uint32_t(i * 128 + k * 8),
                             vd + uint64_t((k * 2 * BlockLayout<D>::GROUP) >> 4), C::IDESC_PV, (j | k) ? 1u : 0u);
               if (j + 1 == nbi) ptx::tc_commit(o_done(i));
+              if (i == 1 || j >= nb1) ptx::tc_commit(empty(vs));
             }
             if (j + 1 < nbi) {
               ok = wait_bar(full(ks), kph, sy);
@@ -497,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           if (lead) {
-            ptx::tc_commit(empty(vs));
             if (more) ptx::tc_commit(empty(ks));
             if (j + 2 == nb) ptx::tc_commit(q_empty);
           }
@@ -514,19 +516,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ------------------------------------------------------------ cleaning of the diagonal's values
-      const int hid = (warp - 2) * 32 + lane;      // 64 threads
       Unit u;
       uint32_t seq = 0, nu = 0;
       bool ok = true;
       while (ok && next_unit(u)) {
         const int32_t nb = max(u.nb[0], u.nb[1]);
         const int32_t dirty = (u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1;
-        bool found = false;
         // Every load is waited for in turn and released, so that a parity is never a lap off.
         for (int32_t x = 0; x < 2 * nb && ok; ++x) {
           const uint32_t vs = seq + uint32_t(x);
-          ok = wait_bar(full(vs % NS), (vs / NS) & 1u, sy);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = __all_sync(0xFFFFFFFFu, wait_bar(full(vs % NS), (vs / NS) & 1u, sy));
           if (!ok) break;
           const int32_t j = x >> 1;
           if ((x & 1) == 0 || j < dirty) {
@@ -534,27 +533,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           const uint32_t va = sbase + uint32_t(C::OFF_RING) + (vs % NS) * uint32_t(C::STAGE_BYTES);
-          // (the swizzle only moves 16-byte chunks inside a row)
-          for (int e = hid; e < C::STAGE_BYTES / 16; e += 64) {
-            const uint32_t a = va + uint32_t(e) * 16;
+          // magnitudes from 0x7F80 on are infinities and NaN
+          uint32_t top = 0;
+#pragma unroll 8
+          for (int e = lane; e < C::STAGE_BYTES / 16; e += 32) {
             uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(a));
-            bool hit = false;
+            ld_shared_v4(va + uint32_t(e) * 16, w);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, hit = true;
-              if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu, hit = true;
-            }
-            if (hit) {
-              ptx::st_shared_v4(a, w[0], w[1], w[2], w[3]);
-              found |= j * kBlockPos + e / (8 * C::HALVES * 8) * 8 + (e / 8) % 8 <= u.last;   // (unused slots: nobody sees them)
-            }
+            for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
           }
-          if (__any_sync(0xFFFFFFFFu, found) && lane == 0) bad_v[nu & 3u] = nu + 1;
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
+          const bool hit = (top & 0xFFFFu) >= 0x7F80u || (top >> 16) >= 0x7F80u;
+          if (__any_sync(0xFFFFFFFFu, hit)) {
+            bool found = false;
+            for (int e = lane; e < C::STAGE_BYTES / 16; e += 32) {
+              uint32_t w[4];
+              ld_shared_v4(va + uint32_t(e) * 16, w);
+              bool here = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u, here = true;
+                if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu, here = true;
+              }
+              if (here) {
+                ptx::st_shared_v4(va + uint32_t(e) * 16, w[0], w[1], w[2], w[3]);
+                // (the swizzle only moves chunks inside a row; unused slots are seen by nobody)
+                found |= j * kBlockPos + e / (64 * C::HALVES) * 8 + (e / 8) % 8 <= u.last;
+              }
+            }
+            if (__any_sync(0xFFFFFFFFu, found) && lane == 0) bad_v[nu & 3u] = nu + 1;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+          }
           if (lane == 0) {
             ptx::mbar_arrive(clean(vs % NS));
             ptx::mbar_arrive(empty(vs % NS));
@@ -700,6 +709,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (*abort) {                      // a wait gave up: let every copy in flight land before the block leaves
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 2000000ull) {
+    }
+  }
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
