@@ -419,18 +419,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     float* red = reinterpret_cast<float*>(pbuf);         // [4][64], while the weights' buffer is free
     const uint32_t pb = sbase + uint32_t(C::OFF_P + i * C::P_BYTES) + uint32_t(pos * 128);
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory"); };
-    auto group_or = [&](bool x) {
-      uint32_t r;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t"
-          "setp.ne.u32 p, %1, 0;\n\t"
-          "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
-          "selp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(r)
-          : "r"(uint32_t(x)), "r"(1 + i)
-          : "memory");
-      return r != 0;
-    };
     uint32_t nu = 0, np = 0;
     bool ok = true;
     for (int32_t u = int32_t(blockIdx.x); u < units && ok; u += int32_t(gridDim.x), ++nu) {
@@ -558,7 +546,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         }
       }
       // The scratch is the next unit's weights' buffer; the warps of the group go on or stop together.
-      ok = !group_or(!ok);
+      ok = !tc::bar_or(1 + i, !ok);
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(o_free);

@@ -85,9 +85,12 @@ struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE_BYTES = 128 * D * 2;
   static constexpr int STAGE_BYTES = kBlockPos * D * 2;
-  static constexpr int STAGES = D == 128 ? 5 : 8;
+  // (five stages and no room for the outputs were 0 to 5 % faster between units, but stores of rows
+  // by their threads, 32 lines an instruction, held each unit up for 6000 clocks)
+  static constexpr int STAGES = D == 128 ? 4 : 8;
   static constexpr int OFF_RING = 2 * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE_BYTES;
+  static constexpr int OFF_OUT = OFF_RING + STAGES * STAGE_BYTES;   // per tile, 64 of the output's dimensions
+  static constexpr int OFF_BAR = OFF_OUT + 2 * 128 * 128;
   // ring full, empty, cleaned; unit full, empty; Q full, empty; S full, P full, O done (per tile); drain
   static constexpr int NUM_BARS = 3 * STAGES + 2 * kUnitSlots + 2 + 6 + 1;
   static constexpr int OFF_UNIT = OFF_BAR + 8 * NUM_BARS;
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) 
 template <class C, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                  const __grid_constant__ CUtensorMap tmv, const Params p) {
+                  const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, const Params p) {
   constexpr int D = C::D, G = C::G, NS = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -269,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 1; i < 6; ++i) misc[i] = 0u;
     ptx::fence_barrier_init();
     ptx::prefetch_tensormap(&tmq);
+    ptx::prefetch_tensormap(&tmo);
     if (kTma) {
       ptx::prefetch_tensormap(&tmk);
       ptx::prefetch_tensormap(&tmv);
@@ -580,10 +584,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = tid - 128 - i * 128;             // row of the tile = TMEM lane
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + uint32_t(i * 128), to = tmem + lane_base + uint32_t(256 + i * D);
+    const uint32_t out_row = sbase + uint32_t(C::OFF_OUT + i * 128 * 128 + r * 128);
+    auto tile_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory"); };
     uint32_t ns = 0, nt = 0;                       // blocks and units of this tile
     Unit u;
     bool ok = true;
-    while (ok && next_unit(u)) {
+    // The tile's four warps meet at named barriers, so they start and finish units together or not at all.
+    while (true) {
+      ok = next_unit(u);
+      if (bar_or(1 + i, !ok)) break;
       const int32_t nb = i ? u.nb[1] : u.nb[0];
       if (nb == 0) continue;
       const int32_t pos = u.base + i * C::P + r / G;
@@ -664,16 +673,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(p_full(i));
       }
-      if (!ok) break;
-      ok = wait_bar(o_done(i), nt & 1u, sy);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
+      if (ok) ok = wait_bar(o_done(i), nt & 1u, sy);
+      if (bar_or(1 + i, !ok)) break;
       ++nt;
       ptx::tc_fence_after();
       const bool store = pos >= u.first && pos <= u.last;
       const bool dirty = bad_v[(un - 1) & 3u] == un;      // (written before the values' MMA)
       uint16_t* orow = p.o + ((int64_t(u.row0) + i * C::P + r / G) * p.Hq + u.kh * G + r % G) * D;
       const float rl = __fdiv_rn(1.0f, l);
+      // A whole tile leaves through shared memory as two TMA boxes (64 dims x G heads x positions); the
+      // tile at an end of the chunk row by row.
+      const int32_t t0 = u.base + i * C::P;
+      const bool whole = t0 >= u.first && t0 + C::P - 1 <= u.last;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -692,20 +703,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[e] = __float_as_uint(__fadd_rn(__uint_as_float(o[e]), __uint_as_float(uint32_t(v[e]) << 16)));
           }
         }
-        if (store) {
+        uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = ptx::pack_bf16x2(__fmul_rn(__uint_as_float(o[e + 2 * k]), rl),
-                                      __fmul_rn(__uint_as_float(o[e + 2 * k + 1]), rl));
-            ptx::st_global_v4(orow + c + e, w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 16; ++k)
+          w[k] = ptx::pack_bf16x2(__fmul_rn(__uint_as_float(o[2 * k]), rl), __fmul_rn(__uint_as_float(o[2 * k + 1]), rl));
+        if (whole) {
+          if ((c & 32) == 0) {                  // the box before this one has been read
+            if (r == 0) ptx::bulk_wait_read<0>();
+            tile_sync();
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ptx::st_shared_v4(out_row + uint32_t((((c & 32) / 8 + k) ^ (r & 7)) << 4), w[4 * k], w[4 * k + 1],
+                              w[4 * k + 2], w[4 * k + 3]);
+          if ((c & 32) != 0) {
+            ptx::fence_proxy_async_smem();
+            tile_sync();
+            if (r == 0) {
+              tma_store_3d(&tmo, sbase + uint32_t(C::OFF_OUT + i * 128 * 128), c - 32, u.kh * G, u.row0 + i * C::P);
+              ptx::bulk_commit();
+            }
+          }
+        } else if (store) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ptx::st_global_v4(orow + c + 8 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       }
       ptx::tc_fence_before();
     }
+    if (r == 0) bulk_wait_all();                   // the outputs are written
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -869,10 +895,12 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
     return BI_GEMM_ERR_CUDA;
   }
   if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
-  CUtensorMap tmq, tmk, tmv;
+  CUtensorMap tmq, tmk, tmv, tmo;
   std::memset(&tmk, 0, sizeof(tmk));
   std::memset(&tmv, 0, sizeof(tmv));
-  if (!biattn_tc::encode_queries(&tmq, q, T, h->Hq, h->D, h->G, 128 / h->G)) return BI_GEMM_ERR_CUDA;
+  if (!biattn_tc::encode_queries(&tmq, q, T, h->Hq, h->D, h->G, 128 / h->G) ||
+      !biattn_tc::encode_queries(&tmo, o, T, h->Hq, h->D, h->G, 128 / h->G))
+    return BI_GEMM_ERR_CUDA;
   // TMA boxes need whole pages and row coordinates (one page past the end included) of 32 bits;
   // otherwise rows are copied: the same bits.
   const int64_t rows = num_pages * h->page_size;
@@ -933,7 +961,7 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
   void* pargs[2] = {&p, &up};
   cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&biprompt::plan_kernel), pargs);
   if (e == cudaSuccess) {
-    void* args[4] = {&tmq, &tmk, &tmv, &p};
+    void* args[5] = {&tmq, &tmk, &tmv, &tmo, &p};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(w.cap_tiles * h->Hkv, h->num_sms)));
     cfg.blockDim = dim3(biprompt::kThreads);
     cfg.dynamicSmemBytes = size_t(h->kern.smem);
