@@ -425,91 +425,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       // The tensor pipe holds about four MMAs (256 clocks) beside the one that runs, so whatever lies
-      // between two batches of eight has to be short: ring stages and phases are counted, not divided
-      // out, descriptors are added up from constants, and the whole warp walks the waits (one lane,
-      // chosen once, issues), which keeps all of it in uniform registers.
+      // between two batches of eight has to be shorter than that: one lane does it all, ring stages and
+      // phases are counted, descriptors are added up from constants, and every wait stands where the
+      // pipe has work left (the next block's values are awaited before tile 1's scores are issued, so
+      // that only tile 0's weights are awaited at the turn of the loop).
       const bool lead = elect_one();
-      const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + C::TILE_BYTES, 16, 1024)};
-      const uint64_t kd0 = BlockLayout<D>::by_row(sbase + C::OFF_RING, 0);
-      const uint64_t vd0 = BlockLayout<D>::by_dim(sbase + C::OFF_RING, 0);
-      constexpr uint64_t kStep = C::STAGE_BYTES >> 4;
-      Unit u;
-      uint32_t st = 0, ph = 0;                // stage and phase of the next load to consume
-      uint32_t nu = 0, cleaned = 0, np[2] = {0, 0};
-      bool ok = true, issued = false;
-      auto advance = [&]() {
-        if (++st == uint32_t(NS)) st = 0, ph ^= 1u;
-      };
-      auto qk = [&](int i, uint32_t s) {
-        if (lead) {
+      bool issued = false;
+      if (lead) {
+        const uint64_t qd[2] = {sdesc_sw128(sbase, 16, 1024), sdesc_sw128(sbase + C::TILE_BYTES, 16, 1024)};
+        const uint64_t kd0 = BlockLayout<D>::by_row(sbase + C::OFF_RING, 0);
+        const uint64_t vd0 = BlockLayout<D>::by_dim(sbase + C::OFF_RING, 0);
+        constexpr uint64_t kStep = C::STAGE_BYTES >> 4;
+        uint32_t st = 0, ph = 0;              // stage and phase of the next load to consume
+        uint32_t nu = 0, cleaned = 0, np[2] = {0, 0};
+        auto advance = [&]() {
+          if (++st == uint32_t(NS)) st = 0, ph ^= 1u;
+        };
+        auto qk = [&](int i, uint32_t s) {
           const uint64_t kd = kd0 + s * kStep;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             ptx::mma_bf16(tmem + uint32_t(i * 128), qd[i] + uint64_t(((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4),
                           kd + uint64_t(((k >> 2) * BlockLayout<D>::HALF + (k & 3) * 32) >> 4), C::IDESC_QK, k ? 1u : 0u);
           ptx::tc_commit(s_full(i));
-        }
-      };
-      while (ok && next_unit(u)) {
-        const int32_t nb0 = u.nb[0], nb1 = u.nb[1], nb = max(nb0, nb1);
-        const int32_t dirty = (nb0 > 0 ? nb0 : nb1) - 1;             // cleaned from this block on
-        ok = wait_bar(q_full, nu & 1u, sy) && wait_bar(full(st), ph, sy);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        issued = true;
-        if (nb0 > 0) qk(0, st);
-        if (nb1 > 0) qk(1, st);
-        if (lead) {
+        };
+        auto pv = [&](int i, uint32_t s, bool first) {
+          const uint64_t vd = vd0 + s * kStep;
+#pragma unroll
+          for (int k = 0; k < kBlockPos / 16; ++k)
+            mma_bf16_ta(tmem + uint32_t(256 + i * D), tmem + uint32_t(i * 128 + k * 8),
+                        vd + uint64_t((k * 2 * BlockLayout<D>::GROUP) >> 4), C::IDESC_PV, (first && k == 0) ? 0u : 1u);
+        };
+        auto values_ready = [&](uint32_t s, uint32_t phase, bool dirty) {
+          if (!wait_bar(full(s), phase, sy)) return false;
+          if (dirty) {
+            if (!wait_bar(clean(s), (cleaned >> s) & 1u, sy)) return false;
+            cleaned ^= 1u << s;
+          }
+          return true;
+        };
+        // One unit; false once a wait gave up.
+        auto unit = [&](const int32_t nb0, const int32_t nb1) {
+          const int32_t nb = max(nb0, nb1);
+          const int32_t dirty = (nb0 > 0 ? nb0 : nb1) - 1;           // cleaned from this block on
+          if (!wait_bar(q_full, nu & 1u, sy) || !wait_bar(full(st), ph, sy)) return false;
+          ptx::tc_fence_after();
+          issued = true;
+          if (nb0 > 0) qk(0, st);
+          if (nb1 > 0) qk(1, st);
           ptx::tc_commit(empty(st));
           if (nb == 1) ptx::tc_commit(q_empty);
-        }
-        advance();
-        for (int32_t j = 0; j < nb; ++j) {
-          const uint32_t vs = st, vph = ph;                          // this block's values
           advance();
-          const uint32_t ks = st, kph = ph;                          // the next block's keys
-          const bool more = j + 1 < nb;
-          ok = wait_bar(full(vs), vph, sy);
-          if (j >= dirty) {
-            ok = ok && wait_bar(clean(vs), (cleaned >> vs) & 1u, sy);
-            cleaned ^= 1u << vs;
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int32_t nbi = i ? nb1 : nb0;
-            if (j >= nbi) continue;
-            ok = ok && wait_bar(p_full(i), np[i] & 1u, sy);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            ++np[i];
-            ptx::tc_fence_after();
-            if (lead) {
-              const uint64_t vd = vd0 + vs * kStep;
-#pragma unroll
-              for (int k = 0; k < kBlockPos / 16; ++k)
-                mma_bf16_ta(tmem + uint32_t(256 + i * D), tmem + uint32_t(i * 128 + k * 8),
-                            vd + uint64_t((k * 2 * BlockLayout<D>::GROUP) >> 4), C::IDESC_PV, (j | k) ? 1u : 0u);
-              if (j + 1 == nbi) ptx::tc_commit(o_done(i));
-              if (i == 1 || j >= nb1) ptx::tc_commit(empty(vs));
-            }
-            if (j + 1 < nbi) {
-              ok = wait_bar(full(ks), kph, sy);
-              ok = __all_sync(0xFFFFFFFFu, ok);
-              if (!ok) break;
+          if (!values_ready(st, ph, dirty == 0)) return false;
+          for (int32_t j = 0; j < nb; ++j) {
+            const uint32_t vs = st;                                  // this block's values
+            advance();
+            const uint32_t ks = st, kph = ph;                        // the next block's keys
+            const bool more = j + 1 < nb;
+            if (more) advance();
+            const uint32_t v2 = st, v2ph = ph;                       // and values
+            if (j < nb0) {
+              if (!wait_bar(p_full(0), np[0]++ & 1u, sy)) return false;
               ptx::tc_fence_after();
-              qk(i, ks);
+              pv(0, vs, j == 0);
+              if (j + 1 == nb0) ptx::tc_commit(o_done(0));
+              if (j >= nb1) ptx::tc_commit(empty(vs));
+            }
+            if (more) {
+              if (!wait_bar(full(ks), kph, sy)) return false;
+              ptx::tc_fence_after();
+              if (j + 1 < nb0) qk(0, ks);
+            }
+            if (j < nb1) {
+              if (!wait_bar(p_full(1), np[1]++ & 1u, sy)) return false;
+              ptx::tc_fence_after();
+              pv(1, vs, j == 0);
+              if (j + 1 == nb1) ptx::tc_commit(o_done(1));
+              ptx::tc_commit(empty(vs));
+            }
+            if (more) {
+              if (!values_ready(v2, v2ph, j + 1 >= dirty)) return false;
+              if (j + 1 < nb1) qk(1, ks);
+              ptx::tc_commit(empty(ks));
+              if (j + 2 == nb) ptx::tc_commit(q_empty);
             }
           }
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          if (lead) {
-            if (more) ptx::tc_commit(empty(ks));
-            if (j + 2 == nb) ptx::tc_commit(q_empty);
-          }
-          if (more) advance();
+          ++nu;
+          return true;
+        };
+        while (true) {
+          const uint32_t us = un % kUnitSlots;
+          if (!wait_bar(unit_full(us), (un / kUnitSlots) & 1u, sy)) break;
+          const int32_t b = units[us].b, nb0 = units[us].nb[0], nb1 = units[us].nb[1];
+          ptx::mbar_arrive(unit_empty(us));
+          ++un;
+          if (b < 0 || !unit(nb0, nb1)) break;
         }
-        ++nu;
       }
       if (lead && issued) {          // no MMA of ours may be in flight when TMEM is released
         volatile uint32_t none = 0;
