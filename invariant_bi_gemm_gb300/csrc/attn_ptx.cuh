@@ -248,20 +248,24 @@ __device__ __forceinline__ void block_rows(const Cache& c, const int32_t* row, i
   }
 }
 
+// Eight lanes copy 128 bytes of a row, so an instruction takes four rows and a row's offset is fetched
+// from its lane once for both of its halves.
 template <int D>
 __device__ __forceinline__ void load_block_rows(uint32_t dst, const uint16_t* base, const int64_t (&off)[4],
                                                 int32_t kh, int lane) {
-  constexpr int CH = D / 8, RPI = 32 / CH;      // chunks per row, rows per step of the warp
-  const int ch = lane % CH, sub = lane / CH;
+  const int sub = lane >> 3, ch = lane & 7;
+  const uint16_t* src0 = base + int64_t(kh) * D + ch * 8;
+  const uint32_t even = BlockLayout<D>::chunk(sub, ch), odd = BlockLayout<D>::chunk(sub + 4, ch);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-#pragma unroll 4
-    for (int i = 0; i < 32 / RPI; ++i) {
-      const int rl = i * RPI + sub;
-      const int64_t o = __shfl_sync(0xFFFFFFFFu, off[k], rl);
-      const int r = 32 * k + rl;
-      ptx::cp_async_16(dst + BlockLayout<D>::chunk(r, ch),
-                       o >= 0 ? base + o + int64_t(kh) * D + ch * 8 : base, o >= 0 ? 16u : 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, off[k], 4 * i + sub);
+      const uint32_t to = dst + uint32_t(4 * k + (i >> 1)) * BlockLayout<D>::GROUP + ((i & 1) ? odd : even);
+      const uint16_t* src = o >= 0 ? src0 + o : base;
+      const uint32_t bytes = o >= 0 ? 16u : 0u;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) ptx::cp_async_16(to + uint32_t(h) * BlockLayout<D>::HALF, src + h * 64, bytes);
     }
   }
 }

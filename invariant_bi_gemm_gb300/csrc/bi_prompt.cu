@@ -121,69 +121,25 @@ __device__ __forceinline__ int32_t tiles_of(const Params& p, int64_t b, int32_t 
   return int32_t(last / up) - *first + 1;
 }
 
-// One block: tiles per sequence, then every tile's record, sorted by its key blocks (descending; the
-// order among equals is not fixed and decides no bit).
+// One block: every tile's record, the sequences sorted by their last position's block (descending), a
+// sequence's tiles one after the other from its last: side by side run units of the same keys, and the
+// shortest come last.  (The order among sequences of one length is not fixed and decides no bit.)
 __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) {
   __shared__ int32_t warp_sums[32];
-  __shared__ int32_t carry;
   __shared__ int32_t bins[kBins];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) carry = 0;
   for (int i = tid; i < kBins; i += 1024) bins[i] = 0;
   __syncthreads();
-  for (int64_t base = 0; base < p.B; base += 1024) {
-    const int64_t b = base + tid;
-    int32_t first, n = b < p.B ? tiles_of(p, b, up, &first) : 0;
-    int32_t x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      int32_t w = warp_sums[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
-        if (lane >= o) w += y;
-      }
-      warp_sums[lane] = w;
-    }
-    __syncthreads();
-    const int32_t incl = carry + x + (warp > 0 ? warp_sums[warp - 1] : 0);
-    if (b < p.B) p.cum[b] = incl - n;
-    __syncthreads();
-    if (tid == 1023) carry = incl;
-    __syncthreads();
-  }
-  if (tid == 0) p.cum[p.B] = carry;
-  // Ascending q_start gives at most cap_tiles; a table that descends and climbs again may claim more.
-  int32_t total = carry;
-  if (total > p.cap_tiles) {
-    if (tid == 0) atomicOr(p.status, kErrInput);
-    total = int32_t(p.cap_tiles);
-  }
-  __syncthreads();
-  auto tile_of = [&](int32_t i, int32_t* b) {
-    int64_t lo = 0, hi = p.B;                 // the last sequence whose tiles start at or before i
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (p.cum[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    *b = int32_t(lo);
-    return p.q_pos0[lo] / up + (i - p.cum[lo]);
-  };
   auto bin_of = [&](int32_t tile) { return kBins - 1 - min(kBins - 1, int32_t(int64_t(tile) * up / kBlockPos)); };
-  for (int32_t i = tid; i < total; i += 1024) {
-    int32_t b;
-    atomicAdd(&bins[bin_of(tile_of(i, &b))], 1);
+  for (int64_t b = tid; b < p.B; b += 1024) {
+    int32_t first;
+    const int32_t n = tiles_of(p, b, up, &first);
+    if (n > 0) atomicAdd(&bins[bin_of(first + n - 1)], n);
   }
   __syncthreads();
+  int32_t total;
   {                                           // exclusive scan of the bins, two per thread
     const int32_t a0 = bins[2 * tid], a1 = bins[2 * tid + 1];
     int32_t x = a0 + a1;
@@ -207,12 +163,22 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) 
     const int32_t ex = x - a0 - a1 + (warp > 0 ? warp_sums[warp - 1] : 0);
     bins[2 * tid] = ex;
     bins[2 * tid + 1] = ex + a0;
+    total = warp_sums[31];
     __syncthreads();
   }
-  for (int32_t i = tid; i < total; i += 1024) {
-    int32_t b;
-    const int32_t tile = tile_of(i, &b);
-    p.rec[atomicAdd(&bins[bin_of(tile)], 1)] = make_int2(b, tile);
+  // Ascending q_start gives at most cap_tiles; a table that descends and climbs again may claim more.
+  if (total < 0 || total > p.cap_tiles) {
+    if (tid == 0) atomicOr(p.status, kErrInput);
+    total = int32_t(p.cap_tiles);
+  }
+  for (int64_t b = warp; b < p.B; b += 32) {
+    int32_t first, at = 0;
+    const int32_t n = tiles_of(p, b, up, &first);
+    if (n == 0) continue;
+    if (lane == 0) at = atomicAdd(&bins[bin_of(first + n - 1)], n);
+    at = __shfl_sync(0xFFFFFFFFu, at, 0);
+    for (int32_t k = lane; k < n; k += 32)
+      if (at + k >= 0 && at + k < p.cap_tiles) p.rec[at + k] = make_int2(int32_t(b), first + n - 1 - k);
   }
   if (tid == 0) {
     p.counter[0] = uint32_t(total);
@@ -456,12 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_bf16_ta(tmem + uint32_t(256 + i * D), tmem + uint32_t(i * 128 + k * 8),
                         vd + uint64_t((k * 2 * BlockLayout<D>::GROUP) >> 4), C::IDESC_PV, (first && k == 0) ? 0u : 1u);
         };
-        auto values_ready = [&](uint32_t s, uint32_t phase, bool dirty) {
-          if (!wait_bar(full(s), phase, sy)) return false;
-          if (dirty) {
-            if (!wait_bar(clean(s), (cleaned >> s) & 1u, sy)) return false;
-            cleaned ^= 1u << s;
-          }
+        auto values_clean = [&](uint32_t s) {
+          if (!wait_bar(clean(s), (cleaned >> s) & 1u, sy)) return false;
+          cleaned ^= 1u << s;
           return true;
         };
         // One unit; false once a wait gave up.
@@ -476,14 +439,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_commit(empty(st));
           if (nb == 1) ptx::tc_commit(q_empty);
           advance();
-          if (!values_ready(st, ph, dirty == 0)) return false;
+          if (kTma && !wait_bar(full(st), ph, sy)) return false;
           for (int32_t j = 0; j < nb; ++j) {
             const uint32_t vs = st;                                  // this block's values
+            if (!kTma && !wait_bar(full(st), ph, sy)) return false;  // (row copies come late)
             advance();
             const uint32_t ks = st, kph = ph;                        // the next block's keys
             const bool more = j + 1 < nb;
             if (more) advance();
             const uint32_t v2 = st, v2ph = ph;                       // and values
+            if (j >= dirty && !values_clean(vs)) return false;
             if (j < nb0) {
               if (!wait_bar(p_full(0), np[0]++ & 1u, sy)) return false;
               ptx::tc_fence_after();
@@ -504,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tc_commit(empty(vs));
             }
             if (more) {
-              if (!values_ready(v2, v2ph, j + 1 >= dirty)) return false;
+              if (kTma && !wait_bar(full(v2), v2ph, sy)) return false;
               if (j + 1 < nb1) qk(1, ks);
               ptx::tc_commit(empty(ks));
               if (j + 2 == nb) ptx::tc_commit(q_empty);
