@@ -17,11 +17,15 @@
 // Bound: for many tokens the tensor cores (6 D operations per query row and key, a third of them for
 // the weights' low part) and the softmax's instructions, for few the load of the prefix.
 //
-// Warps (384 threads, one block per SM): 0 loads (queries, then K1 .. K(n-1), K0, V0 .. V(n-1)
-// through a ring), 1 issues the MMAs, 2 and 3 check that the group's page tables agree, 4 - 11
-// softmax: two warpgroups, each half of the columns, a thread per position of a block.
+// Warps (640 threads, one block per SM): 0 loads (queries, then K1 .. K(n-1), K0, V0 .. V(n-1)
+// through a ring), 1 issues the MMAs, 2 and 3 check that the group's page tables agree, 4 - 19
+// softmax: four warpgroups, each a quarter of the columns, a thread per position of a block.  (Two
+// warpgroups with half of the columns each issued an instruction in 28 % of the clocks: their phases
+// are chains of dependent steps.)
 // TMEM: block b's scores at column 128 b (64 b for splits above 512); the value sums take block 0's
-// columns once its weights are out, so a unit's block 0 is the last whose scores are computed.
+// columns once its weights are out, so a unit's block 0 is the last whose scores are computed, and the
+// other blocks' scores of the next unit run beside the end of this one.  The weights of a block are
+// computed into registers while the block before still feeds the tensor cores from the one buffer.
 #pragma once
 
 #include "attn_ptx.cuh"
@@ -30,8 +34,9 @@ namespace biattn {
 
 namespace tc = biattn_tc;
 
-constexpr int kSharedThreads = 384;
-constexpr int kSharedStages = 4;
+constexpr int kSharedGroups = 4;              // softmax warpgroups
+constexpr int kSharedThreads = 128 + 128 * kSharedGroups;
+constexpr int kSharedStages = 3;
 constexpr int kMaxBlocks = 8;                 // blocks of a split: 1024 / 128
 
 struct SharedParams {
@@ -175,13 +180,14 @@ struct SharedCfg {
   static constexpr int NS = kSharedStages;
   static constexpr int STAGE_BYTES = tc::kBlockPos * D * 2;
   static constexpr int Q_BYTES = 128 * D * 2;
-  static constexpr int P_BYTES = 2 * tc::kBlockPos * 128;     // high and low parts: 128 positions x 64 columns
+  static constexpr int ATOM = tc::kBlockPos * 128;            // 128 positions x 64 columns of weights
   static constexpr int OFF_RING = Q_BYTES;
-  static constexpr int OFF_P = OFF_RING + NS * STAGE_BYTES;   // [2 warpgroups]
-  static constexpr int OFF_M = OFF_P + 2 * P_BYTES;           // [128] maxima
-  static constexpr int OFF_BAR = OFF_M + 128 * 4;
-  // ring full, empty; Q full, empty; scores of a block; weights full, free (per warpgroup); O free; drain
-  static constexpr int NUM_BARS = 2 * NS + 2 + kMaxBlocks + 4 + 2;
+  static constexpr int OFF_P = OFF_RING + NS * STAGE_BYTES;   // high parts of both halves, then low parts
+  static constexpr int OFF_M = OFF_P + 4 * ATOM;              // [4][32] the warpgroups' maxima
+  static constexpr int OFF_RED = OFF_M + 128 * 4;             // [4][4][32] their warps' maxima, then sums
+  static constexpr int OFF_BAR = OFF_RED + 4 * 4 * 32 * 4;
+  // ring full, empty; Q full, empty; scores of a block; weights full, free; O free; drain
+  static constexpr int NUM_BARS = 2 * NS + 2 + kMaxBlocks + 2 + 2;
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
@@ -202,9 +208,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   auto empty = [&](uint32_t s) { return bar0 + 8 * (NS + s); };
   const uint32_t q_full = bar0 + 8 * (2 * NS), q_empty = q_full + 8;
   auto s_full = [&](int b) { return q_empty + 8 + 8 * b; };
-  auto p_full = [&](int i) { return q_empty + 8 + 8 * (kMaxBlocks + i); };
-  auto p_free = [&](int i) { return q_empty + 8 + 8 * (kMaxBlocks + 2 + i); };
-  const uint32_t o_free = q_empty + 8 + 8 * (kMaxBlocks + 4), drain = o_free + 8;
+  const uint32_t p_full = q_empty + 8 + 8 * kMaxBlocks, p_free = p_full + 8, o_free = p_full + 16, drain = p_full + 24;
   float* msm = reinterpret_cast<float*>(smem + C::OFF_M);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort = misc + 1;
@@ -218,11 +222,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     ptx::mbar_init(q_full, 1);
     ptx::mbar_init(q_empty, 1);
     for (int b = 0; b < kMaxBlocks; ++b) ptx::mbar_init(s_full(b), 1);
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(p_full(i), 4);
-      ptx::mbar_init(p_free(i), 1);
-    }
-    ptx::mbar_init(o_free, 8);
+    ptx::mbar_init(p_full, 4 * kSharedGroups);
+    ptx::mbar_init(p_free, 1);
+    ptx::mbar_init(o_free, 4 * kSharedGroups);
     ptx::mbar_init(drain, 1);
     misc[1] = 0u;
     ptx::fence_barrier_init();
@@ -246,9 +248,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   const int32_t units = sp.count[0] * p.Hkv;
   const int nblk = p.split / tc::kBlockPos;
 
-  // A unit's record; columns and their halves (multiples of 16, the MMA's step in N).
+  // A unit's record; its columns (a multiple of 16, the MMA's step in N) and how many a warpgroup takes.
   struct U {
-    int32_t t0, n, s, src, kh, cols, c0;
+    int32_t t0, n, s, src, kh, cols, share;
   };
   auto unit = [&](int32_t u) {
     const int4 r = sp.srec[u / p.Hkv];
@@ -256,12 +258,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     x.t0 = r.x, x.n = r.y, x.s = r.z, x.src = r.w;
     x.kh = u % p.Hkv;
     x.cols = (x.n * G + 15) & ~15;
-    x.c0 = ((x.cols / 16 + 1) / 2) * 16;        // columns of warpgroup 0
+    x.share = (x.cols + 16 * kSharedGroups - 1) / (16 * kSharedGroups) * 16;
     return x;
   };
 
   if (warp < 4) {
-    ptx::setmaxnreg_dec<80>();
+    ptx::setmaxnreg_dec<56>();
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       bool ok = true, bad = false;
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       if (lane == 0) {
-        uint32_t seq = 0, nu = 0, np[2] = {0, 0};
+        uint32_t seq = 0, nu = 0, np = 0;
         bool ok = true, issued = false;
         for (int32_t u = int32_t(blockIdx.x); u < units && ok; u += int32_t(gridDim.x), ++nu) {
           const U x = unit(u);
@@ -360,28 +362,22 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             ptx::tc_commit(empty(seq % NS));
             if (i + 1 == nblk) ptx::tc_commit(q_empty);
           }
+          const uint32_t id_pv = tc::idesc_bf16(128, x.cols, true, true);
           for (int32_t b = 0; b < nblk && ok; ++b, ++seq) {
-            ok = tc::wait_bar(full(seq % NS), (seq / NS) & 1u, sy);
-            const uint32_t va = sbase + uint32_t(C::OFF_RING) + (seq % NS) * uint32_t(C::STAGE_BYTES);
-            for (int i = 0; i < 2 && ok; ++i) {
-              const int32_t nc = i ? x.cols - x.c0 : x.c0;
-              if (nc == 0) continue;
-              ok = tc::wait_bar(p_full(i), np[i] & 1u, sy);
-              if (!ok) break;
-              ++np[i];
-              ptx::tc_fence_after();
-              const uint32_t id_pv = tc::idesc_bf16(128, nc, true, true);
-              const uint32_t ph = sbase + uint32_t(C::OFF_P + i * C::P_BYTES), pl = ph + uint32_t(C::P_BYTES / 2);
-              const uint32_t od = tmem + uint32_t(i ? x.c0 : 0);
-#pragma unroll
-              for (int k = 0; k < tc::kBlockPos / 16; ++k) {
-                const uint64_t vd = tc::BlockLayout<D>::by_dim(va, k);
-                ptx::mma_bf16(od, vd, tc::sdesc_sw128(ph + uint32_t(k * 16 * 128), 16, 1024), id_pv, (b | k) ? 1u : 0u);
-                ptx::mma_bf16(od, vd, tc::sdesc_sw128(pl + uint32_t(k * 16 * 128), 16, 1024), id_pv, 1u);
-              }
-              ptx::tc_commit(p_free(i));
-            }
+            ok = tc::wait_bar(full(seq % NS), (seq / NS) & 1u, sy) && tc::wait_bar(p_full, np & 1u, sy);
             if (!ok) break;
+            ++np;
+            ptx::tc_fence_after();
+            const uint32_t va = sbase + uint32_t(C::OFF_RING) + (seq % NS) * uint32_t(C::STAGE_BYTES);
+            const uint64_t ph = tc::sdesc_sw128(sbase + C::OFF_P, C::ATOM, 1024);
+            const uint64_t pl = tc::sdesc_sw128(sbase + C::OFF_P + 2 * C::ATOM, C::ATOM, 1024);
+#pragma unroll
+            for (int k = 0; k < tc::kBlockPos / 16; ++k) {
+              const uint64_t vd = tc::BlockLayout<D>::by_dim(va, k), o = uint64_t(k * 16 * 128 >> 4);
+              ptx::mma_bf16(tmem, vd, ph + o, id_pv, (b | k) ? 1u : 0u);
+              ptx::mma_bf16(tmem, vd, pl + o, id_pv, 1u);
+            }
+            ptx::tc_commit(p_free);
             ptx::tc_commit(empty(seq % NS));
           }
         }
@@ -411,145 +407,162 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- softmax: a thread per position
-    ptx::setmaxnreg_inc<208>();
+    ptx::setmaxnreg_inc<104>();
     const int i = (warp - 4) >> 2, w4 = warp & 3;
     const int pos = w4 * 32 + lane;                      // position of a block = TMEM lane
     const uint32_t tl = tmem + (uint32_t(w4 * 32) << 16);
-    uint8_t* pbuf = smem + C::OFF_P + i * C::P_BYTES;
-    float* red = reinterpret_cast<float*>(pbuf);         // [4][64], while the weights' buffer is free
-    const uint32_t pb = sbase + uint32_t(C::OFF_P + i * C::P_BYTES) + uint32_t(pos * 128);
+    float* mine = msm + 32 * i;
+    float* red = reinterpret_cast<float*>(smem + C::OFF_RED) + 128 * i;      // [4][32]
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory"); };
+    // this position's row of the weights' buffer
+    const uint32_t prow = sbase + uint32_t(C::OFF_P + pos * 128);
     uint32_t nu = 0, np = 0;
     bool ok = true;
     for (int32_t u = int32_t(blockIdx.x); u < units && ok; u += int32_t(gridDim.x), ++nu) {
       const U x = unit(u);
-      const int32_t cb = i ? x.c0 : 0, nc = i ? x.cols - x.c0 : x.c0;
-      if (nc == 0) {                                     // the unit's phases still pass one by one
-        for (int32_t b = 0; b < nblk && ok; ++b) ok = __all_sync(0xFFFFFFFFu, tc::wait_bar(s_full(b), nu & 1u, sy));
-      } else {
-        // pass 1: each column's maximum (of the raw sums: the scaling is monotone)
-        float mx[2][32];
+      const int32_t cb = min(i * x.share, x.cols), nc = min(x.share, x.cols - cb);      // its columns: 0, 16 or 32
+      const uint32_t atom = prow + uint32_t((cb >> 6) * C::ATOM), ch0 = uint32_t(cb & 63) / 8;
+      // pass 1: each column's maximum (of the raw sums: the scaling is monotone)
+      {
+        float mx[32];
 #pragma unroll
-        for (int k = 0; k < 64; ++k) mx[k >> 5][k & 31] = -INFINITY;
+        for (int k = 0; k < 32; ++k) mx[k] = -INFINITY;
+#pragma unroll 1
         for (int32_t q = 0; q < nblk; ++q) {
           const int32_t b = q + 1 < nblk ? q + 1 : 0;
-          ok = tc::wait_bar(s_full(b), nu & 1u, sy);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = __all_sync(0xFFFFFFFFu, tc::wait_bar(s_full(b), nu & 1u, sy));
           if (!ok) break;
           ptx::tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k * 16 < nc) {
-              uint32_t s[16];
-              tmem_ld_x16(tl + uint32_t(b * sp.cols + cb + k * 16), s);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float& m = mx[k >> 1][(k & 1) * 16 + e];
-                m = fmaxf(m, __uint_as_float(s[e]));
-              }
-            }
-          }
-        }
-        if (ok) {
-          auto fmx = [](float a, float b) { return fmaxf(a, b); };
-          red[w4 * 64 + lane] = reduce_columns(mx[0], lane, fmx);
-          if (nc > 32) red[w4 * 64 + 32 + lane] = reduce_columns(mx[1], lane, fmx);
-        }
-        // (a warp that gave up still walks the barriers)
-        group_sync();
-        if (pos < nc)
-          msm[64 * i + pos] = __fmul_rn(fmaxf(fmaxf(red[pos], red[64 + pos]), fmaxf(red[128 + pos], red[192 + pos])), p.c);
-        group_sync();
-        // pass 2: weights, their sums, and their two bf16 parts for the value product
-        float ls[2][32];
-#pragma unroll
-        for (int k = 0; k < 64; ++k) ls[k >> 5][k & 31] = 0.0f;
-        for (int32_t b = 0; b < nblk && ok; ++b) {
-          if (b > 0) {
-            ok = tc::wait_bar(p_free(i), np & 1u, sy);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            ++np;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k * 16 < nc) {
-              uint32_t s[16], hi[8], lo[8];
-              tmem_ld_x16(tl + uint32_t(b * sp.cols + cb + k * 16), s);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 m = *reinterpret_cast<const float2*>(msm + 64 * i + k * 16 + e);
-                const float w0 = exp2f(__fsub_rn(__fmul_rn(__uint_as_float(s[e]), p.c), m.x));
-                const float w1 = exp2f(__fsub_rn(__fmul_rn(__uint_as_float(s[e + 1]), p.c), m.y));
-                float& l0 = ls[k >> 1][(k & 1) * 16 + e];
-                float& l1 = ls[k >> 1][(k & 1) * 16 + e + 1];
-                l0 = __fadd_rn(l0, w0);
-                l1 = __fadd_rn(l1, w1);
-                hi[e >> 1] = pack_bf16x2(w0, w1);
-                lo[e >> 1] = pack_bf16x2(__fsub_rn(w0, bf16_lo(hi[e >> 1])), __fsub_rn(w1, bf16_hi(hi[e >> 1])));
-              }
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a = pb + uint32_t(((2 * k + h) ^ (pos & 7)) << 4);
-                ptx::st_shared_v4(a, hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-                ptx::st_shared_v4(a + uint32_t(C::P_BYTES / 2), lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
-              }
-            }
-          }
-          ptx::tc_fence_before();
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(p_full(i));
-        }
-        if (ok) {
-          ok = tc::wait_bar(p_free(i), np & 1u, sy);     // the last block's product: the sums are complete
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (ok) ++np;
-        }
-        ptx::tc_fence_after();
-        if (ok) {
-          auto add = [](float a, float b) { return __fadd_rn(a, b); };
-          red[w4 * 64 + lane] = reduce_columns(ls[0], lane, add);
-          if (nc > 32) red[w4 * 64 + 32 + lane] = reduce_columns(ls[1], lane, add);
-        }
-        group_sync();
-        if (ok) {
-          const int32_t col = cb + pos, tok = col / G;
-          if (pos < nc && tok < x.n && sp.nsh[x.t0 + tok] > x.s) {
-            const float l = __fadd_rn(__fadd_rn(__fadd_rn(red[pos], red[64 + pos]), red[128 + pos]), red[192 + pos]);
-            const int64_t slot = (int64_t(x.t0 + tok) * p.Hkv + x.kh) * p.max_splits + x.s;
-            float* ml = p.ml + (slot * G + col % G) * 2;
-            ml[0] = msm[64 * i + pos];
-            ml[1] = l;
-          }
-          // value sums: thread = output dimension, a warp writes 32 of a column's at once
-          for (int32_t k = 0; k < nc; k += 16) {
-            uint32_t o[16];
-            tmem_ld_x16(tl + uint32_t(cb + k), o);
+          // (sixteen at a time: the last block's columns end where tensor memory does)
+          if (nc > 0) {
+            uint32_t s[16], s2[16];
+            tmem_ld_x16(tl + uint32_t(b * sp.cols + cb), s);
+            if (nc > 16) tmem_ld_x16(tl + uint32_t(b * sp.cols + cb + 16), s2);
             ptx::tmem_wait_ld();
-            const int32_t c16 = cb + k + (lane & 15);
-            const bool mine = c16 / G < x.n && sp.nsh[min(x.t0 + c16 / G, x.t0 + x.n - 1)] > x.s;
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, mine);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[e]));
+            if (nc > 16) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) mx[16 + e] = fmaxf(mx[16 + e], __uint_as_float(s2[e]));
+            }
+          }
+        }
+        if (ok && nc > 0) red[w4 * 32 + lane] = reduce_columns(mx, lane, [](float a, float b) { return fmaxf(a, b); });
+      }
+      // (a warp that gave up still walks the barriers)
+      group_sync();
+      if (pos < nc)
+        mine[pos] = __fmul_rn(fmaxf(fmaxf(red[pos], red[32 + pos]), fmaxf(red[64 + pos], red[96 + pos])), p.c);
+      group_sync();
+      // pass 2: weights, their sums, and their two bf16 parts for the value product
+      uint64_t ls[16];                                   // pairs of columns
+#pragma unroll
+      for (int k = 0; k < 16; ++k) ls[k] = 0;
+#pragma unroll 1
+      for (int32_t b = 0; b < nblk && ok; ++b) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (k * 16 < nc) {
+            uint32_t s[16];
+            tmem_ld_x16(tl + uint32_t(b * sp.cols + cb + k * 16), s);
+            ptx::tmem_wait_ld();
+            float w[16];
+            float low = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(mine + k * 16 + e);
+              // (mul and add on pairs came out fused, with one rounding where these have two)
+              w[e] = __fsub_rn(__fmul_rn(__uint_as_float(s[e]), p.c), m.x);
+              w[e + 1] = __fsub_rn(__fmul_rn(__uint_as_float(s[e + 1]), p.c), m.y);
+              w[e + 2] = __fsub_rn(__fmul_rn(__uint_as_float(s[e + 2]), p.c), m.z);
+              w[e + 3] = __fsub_rn(__fmul_rn(__uint_as_float(s[e + 3]), p.c), m.w);
+              low = tc::min3(low, tc::min3(w[e], w[e + 1], w[e + 2]), w[e + 3]);
+            }
+            // From -126 to 0 the instruction alone gives exp2f's bits (every float of the range was
+            // compared); a column past the unit's, with whatever is in it, at worst takes the other way.
+            if (__any_sync(0xFFFFFFFFu, low < -126.0f)) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = exp2f(w[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = tc::ex2(w[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int j = k * 8 + (e >> 1);
+              ls[j] = tc::add2(ls[j], tc::pair(w[e], w[e + 1]));
+              hi[j] = pack_bf16x2(w[e], w[e + 1]);
+              lo[j] = pack_bf16x2(__fsub_rn(w[e], bf16_lo(hi[j])), __fsub_rn(w[e + 1], bf16_hi(hi[j])));
+            }
+          }
+        }
+        if (b > 0) {                                     // the block before has been multiplied
+          ok = __all_sync(0xFFFFFFFFu, tc::wait_bar(p_free, np & 1u, sy));
+          if (!ok) break;
+          ++np;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k * 8 < nc) {
+            const uint32_t a = atom + (((ch0 + uint32_t(k)) ^ uint32_t(pos & 7)) << 4);
+            ptx::st_shared_v4(a, hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+            ptx::st_shared_v4(a + 2 * C::ATOM, lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+          }
+        }
+        ptx::tc_fence_before();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(p_full);
+      }
+      if (ok && nc > 0) {                                // the sums, while the last product runs
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) tc::unpair(ls[k], v[2 * k], v[2 * k + 1]);
+        red[w4 * 32 + lane] = reduce_columns(v, lane, [](float a, float b) { return __fadd_rn(a, b); });
+      }
+      group_sync();
+      const int64_t stride_t = int64_t(p.Hkv) * p.max_splits * G;            // rows of part between tokens
+      const int64_t row0 = ((int64_t(x.t0) * p.Hkv + x.kh) * p.max_splits + x.s) * G;
+      // which of the columns are tokens that share the split
+      const int32_t tok = (cb + lane) / G;
+      const uint32_t live =
+          __ballot_sync(0xFFFFFFFFu, lane < nc && tok < x.n && sp.nsh[x.t0 + min(tok, x.n - 1)] > x.s);
+      if (ok && w4 == 0 && ((live >> lane) & 1u)) {
+        const float l = __fadd_rn(__fadd_rn(__fadd_rn(red[lane], red[32 + lane]), red[64 + lane]), red[96 + lane]);
+        *reinterpret_cast<float2*>(p.ml + (row0 + tok * stride_t + (cb + lane) % G) * 2) = make_float2(mine[lane], l);
+      }
+      ok = ok && __all_sync(0xFFFFFFFFu, tc::wait_bar(p_free, np & 1u, sy));   // the last block's product
+      ++np;
+      ptx::tc_fence_after();
+      if (ok && nc > 0) {
+        // value sums: thread = output dimension, a warp writes 32 of a column's at once, tokens G
+        // columns at a time (a token's heads share the split or none does)
+        float* dst = p.part + (row0 + (cb / G) * stride_t) * D + pos;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (k * 16 < nc) {
+            uint32_t o[16];
+            tmem_ld_x16(tl + uint32_t(cb + k * 16), o);
+            ptx::tmem_wait_ld();
             if (pos < D) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if ((live >> e) & 1u) {
-                  const int32_t col = cb + k + e;
-                  const int64_t slot = (int64_t(x.t0 + col / G) * p.Hkv + x.kh) * p.max_splits + x.s;
-                  p.part[(slot * G + col % G) * D + pos] = __uint_as_float(o[e]);
+              for (int e = 0; e < 16; e += G) {
+                if ((live >> (k * 16 + e)) & 1u) {
+#pragma unroll
+                  for (int g = 0; g < G; ++g) dst[g * D] = __uint_as_float(o[e + g]);
                 }
+                dst += stride_t * D;
               }
             }
           }
         }
       }
-      // The scratch is the next unit's weights' buffer; the warps of the group go on or stop together.
+      // the warps of a group go on or stop together (they meet at its barrier)
       ok = !tc::bar_or(1 + i, !ok);
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(o_free);
+      if (lane == 0) tc::mbar_arrive_relaxed(o_free);
     }
   }
   ptx::tc_fence_before();
