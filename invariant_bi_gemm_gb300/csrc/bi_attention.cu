@@ -1616,9 +1616,9 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
   const int32_t per = w.cols / h->G;        // tokens of a unit
   CUtensorMap tmq, tmk, tmv, smk, smv;
   if (!biattn_tc::encode_queries(&tmq, q, T, h->Hq, h->D, h->G, per)) return BI_GEMM_ERR_CUDA;
-  // The own units run as in bi_attention_run (its choice between three and four blocks per SM needs
-  // the unit count, which only the device knows here: three); the groups' units load pages as TMA
-  // boxes where a block is whole pages.  All give the same bits.
+  // The own units run as in bi_attention_run (its choice between three and four blocks per SM, on the
+  // least that there can be: one for each token and KV head); the groups' units load pages as TMA boxes
+  // where a block is whole pages.  All give the same bits.
   const bool in_range = num_pages > 0 && rows + h->page_size < (int64_t(1) << 31);
   const bool use_tma = h->tma && in_range &&
                        biattn::encode_cache(&tmk, k_cache, rows, h->Hkv, h->D, h->page_size) &&
@@ -1705,15 +1705,18 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
   void* own_args[1] = {&p};
   void* own_tma_args[3] = {&tmk, &tmv, &p};
   const int64_t units = T * h->Hkv * int64_t(p.max_splits);
+  const bool use_tma4 = use_tma && h->tma4 && T * h->Hkv > h->tma_ctas && T * h->Hkv <= h->tma4_ctas;
+  if (use_tma4) p.nstage = h->nstage4;
   const bool ok =
       launch(reinterpret_cast<const void*>(&biattn::plan_shared_kernel), 1, 1024, 0, plan_args) &&
       launch(shared_tma ? h->shared.tma : h->shared.rows, std::min<int64_t>(w.cap * h->Hkv, h->num_sms),
              biattn::kSharedThreads, size_t(h->shared.smem), shared_args) &&
-      (use_tma ? launch(h->kern.tma, std::min<int64_t>(units, h->tma_ctas), h->kern.tma_threads, h->tma_smem,
-                        own_tma_args)
-               : launch(h->kern.fn, std::min<int64_t>(units, h->max_ctas), biattn::kThreads, h->smem, own_args)) &&
-      launch((p.max_splits + 3) / 4 <= 4 ? h->kern.merge : h->kern.merge_long, T * h->Hkv * h->kern.merge_slices,
-             biattn::kMergeThreads, 0, own_args);
+      (use_tma4  ? launch(h->kern.tma4, std::min<int64_t>(units, h->tma4_ctas), h->kern.tma_threads, h->tma4_smem,
+                          own_tma_args)
+       : use_tma ? launch(h->kern.tma, std::min<int64_t>(units, h->tma_ctas), h->kern.tma_threads, h->tma_smem,
+                          own_tma_args)
+                 : launch(h->kern.fn, std::min<int64_t>(units, h->max_ctas), biattn::kThreads, h->smem, own_args)) &&
+      launch(h->shared.merge, T * h->Hkv * h->shared.merge_slices, biattn::kWideThreads, 0, own_args);
   if (!ok) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;

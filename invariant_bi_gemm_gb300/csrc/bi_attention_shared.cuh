@@ -65,16 +65,18 @@ __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp
   for (int64_t t = tid; t < p.T; t += 1024) sp.nsh[t] = 0;
   __syncthreads();
   const int32_t G = p.Hq / p.Hkv, per = sp.cols / G;     // tokens of a unit
-  for (int64_t g = warp; g < sp.num_groups; g += 32) {
+  // a warp per group, or 32 / groups warps that share out its rows of units where there are few
+  const int wpg = sp.num_groups < 32 ? 32 / int(sp.num_groups) : 1, wi = warp % wpg;
+  for (int64_t g = warp / wpg; g < sp.num_groups; g += 32 / wpg) {
     const int32_t s = sp.group_start[g], e = sp.group_start[g + 1], len = sp.group_len[g];
     if (s < 0 || e < s || e > p.T || len < 0) {
       if (lane == 0) atomicOr(p.status, kErrInput);
       continue;
     }
     if (e - s < 2) continue;                             // (alone: its own units serve it as well)
-    for (int32_t t0 = s; t0 < e; t0 += per) {
+    for (int32_t t0 = s + wi * per; t0 < e; t0 += wpg * per) {
       const int32_t n = min(per, e - t0);
-      int32_t most = 0;
+      int32_t most = 0, first = 0;
       for (int32_t k = lane; k < n; k += 32) {
         const int32_t b = p.q_seq[t0 + k], pos = p.q_pos[t0 + k];
         // (the split that holds the token itself is always its own)
@@ -83,16 +85,19 @@ __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp
           x = min(len, pos) / p.split;
         sp.nsh[t0 + k] = x;
         most = max(most, x);
+        if (k == 0) first = x;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      first = __shfl_sync(0xFFFFFFFFu, first, 0);        // the first token's, which mostly shares all
       __syncwarp();
       int32_t at = 0;
       if (lane == 0) at = atomicAdd(&nrec, most);
       at = __shfl_sync(0xFFFFFFFFu, at, 0);
       for (int32_t sx = lane; sx < most; sx += 32) {
         int32_t src = t0;
-        while (sp.nsh[src] <= sx) ++src;                 // (ends: a token has `most`)
+        if (first <= sx)
+          while (sp.nsh[src] <= sx) ++src;               // (ends: a token has `most`)
         if (at + sx < sp.cap) sp.srec[at + sx] = make_int4(t0, n, sx, src);
         else atomicOr(p.status, kErrInput);              // (only from a group_start that descends)
       }
@@ -570,10 +575,91 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }
 
+// merge_kernel's arithmetic, output by output the same operations in the same order, for lists of many
+// splits: a thread holds an output pair for all four groups, so that a warp reads 256 bytes of a
+// split's sums at once (there four lanes share a pair, 64 bytes of each of four splits), and the
+// splits' factors are computed once per head, not per output.  256 tokens of 36 splits (32 heads of
+// 128, 150 MB of partial sums): 86 us with merge_kernel.
+constexpr int kWideThreads = 256, kWideChunk = 128, kWideBatch = 8;
+
+template <int D, int G>
+__global__ void __launch_bounds__(kWideThreads) merge_wide_kernel(const Params p) {
+  constexpr int kPairs = G * D / 2;
+  constexpr int kSlices = (kPairs + kWideThreads - 1) / kWideThreads;
+  __shared__ float fac[kWideChunk * G], wsum[kWideChunk * G], top[G];
+  const int64_t job = blockIdx.x / kSlices;              // token * Hkv + KV head
+  const int slice = int(blockIdx.x - job * kSlices), tid = int(threadIdx.x);
+  const int64_t t = job / p.Hkv;
+  const int32_t kh = int32_t(job - t * p.Hkv);
+  const int32_t b = __ldcg(p.q_seq + t), pos = __ldcg(p.q_pos + t);
+  ptx::grid_dependency_wait();   // every unit's partial results are complete and visible
+  if (b < 0 || b >= p.B || pos < 0 || int64_t(pos / p.page_size) >= p.max_pages || pos > p.max_pos) return;
+  const int32_t n = splits_of(pos, p.split);
+  if (n == 1) return;                                    // written directly
+  const int64_t slot0 = job * int64_t(p.max_splits);
+  const float2* ml = reinterpret_cast<const float2*>(p.ml) + slot0 * G;
+  for (int g = tid >> 5; g < G; g += kWideThreads / 32) {        // M, a warp per head
+    float m = -INFINITY;
+    for (int32_t s = tid & 31; s < n; s += 32) m = fmaxf(m, ml[int64_t(s) * G + g].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if ((tid & 31) == 0) top[g] = m;
+  }
+  __syncthreads();
+  const int pr = slice * kWideThreads + tid;
+  const bool valid = pr < kPairs;
+  const int g = valid ? pr / (D / 2) : 0, d = valid ? (pr % (D / 2)) * 2 : 0;
+  const float* pp = p.part + (slot0 * G + g) * D + d;
+  const int32_t c = (n + 3) / 4;                         // splits per group
+  float L = 0.0f, A0 = 0.0f, A1 = 0.0f, Ls = 0.0f, As0 = 0.0f, As1 = 0.0f;
+  int32_t left = c, group = 0;                           // of the current group
+  auto close = [&]() {                                   // the group's sums join those before it
+    Ls = group ? __fadd_rn(Ls, L) : L;
+    As0 = group ? __fadd_rn(As0, A0) : A0;
+    As1 = group ? __fadd_rn(As1, A1) : A1;
+    L = A0 = A1 = 0.0f;
+    ++group;
+    left = c;
+  };
+  for (int32_t c0 = 0; c0 < n; c0 += kWideChunk) {
+    const int32_t cn = min(kWideChunk, n - c0);
+    __syncthreads();
+    for (int i = tid; i < cn * G; i += kWideThreads) {
+      const float2 x = ml[int64_t(c0) * G + i];
+      const float f = exp2f(__fsub_rn(x.x, top[i % G]));
+      fac[i] = f;
+      wsum[i] = __fmul_rn(x.y, f);
+    }
+    __syncthreads();
+    if (!valid) continue;
+    for (int32_t s0 = 0; s0 < cn; s0 += kWideBatch) {
+      float2 v[kWideBatch];
+#pragma unroll
+      for (int k = 0; k < kWideBatch; ++k)
+        if (s0 + k < cn) v[k] = *reinterpret_cast<const float2*>(pp + int64_t(c0 + s0 + k) * G * D);
+#pragma unroll
+      for (int k = 0; k < kWideBatch; ++k) {
+        if (s0 + k < cn) {
+          const float f = fac[(s0 + k) * G + g];
+          L = __fadd_rn(L, wsum[(s0 + k) * G + g]);
+          A0 = __fadd_rn(A0, __fmul_rn(v[k].x, f));
+          A1 = __fadd_rn(A1, __fmul_rn(v[k].y, f));
+          if (--left == 0) close();
+        }
+      }
+    }
+  }
+  if (!valid) return;
+  if (left < c) close();
+  *reinterpret_cast<uint32_t*>(p.o + (t * p.Hq + int64_t(kh) * G + g) * D + d) =
+      pack_bf16x2(__fdiv_rn(As0, Ls), __fdiv_rn(As1, Ls));
+}
+
 struct SharedInfo {
   const void* tma = nullptr;
   const void* rows = nullptr;
-  int smem = 0;
+  const void* merge = nullptr;
+  int smem = 0, merge_slices = 1;
 };
 
 template <int D, int G>
@@ -582,6 +668,8 @@ SharedInfo shared_info() {
   k.tma = reinterpret_cast<const void*>(&shared_kernel<D, G, true>);
   k.rows = reinterpret_cast<const void*>(&shared_kernel<D, G, false>);
   k.smem = SharedCfg<D, G>::SMEM;
+  k.merge = reinterpret_cast<const void*>(&merge_wide_kernel<D, G>);
+  k.merge_slices = (G * D / 2 + kWideThreads - 1) / kWideThreads;
   return k;
 }
 
