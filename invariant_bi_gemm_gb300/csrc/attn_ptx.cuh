@@ -229,7 +229,7 @@ __device__ __forceinline__ int32_t block_box(const Cache& c, const int32_t* row,
   const int32_t pos = pos0 + lane * step;
   const int32_t past = int32_t(c.num_pages * c.page_size / 8);
   if (lane * step >= kBlockPos || pos > last) return past;
-  const int32_t page = row[pos / c.page_size];
+  const int32_t page = __ldcg(row + pos / c.page_size);
   if (page < 0 || page >= c.num_pages) {
     *bad = true;
     return past;
@@ -256,7 +256,7 @@ __device__ __forceinline__ void block_rows(const Cache& c, const int32_t* row, i
     const int32_t pos = pos0 + lane + 32 * k;
     off[k] = -1;
     if (pos <= last) {
-      const int64_t page = row[pos / c.page_size];
+      const int64_t page = __ldcg(row + pos / c.page_size);
       if (page >= 0 && page < c.num_pages)
         off[k] = (page * c.page_size + pos % c.page_size) * c.Hkv * D;
       else

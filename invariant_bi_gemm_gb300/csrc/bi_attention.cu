@@ -1709,13 +1709,13 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
   if (use_tma4) p.nstage = h->nstage4;
   const bool ok =
       launch(reinterpret_cast<const void*>(&biattn::plan_shared_kernel), 1, 1024, 0, plan_args) &&
-      launch(shared_tma ? h->shared.tma : h->shared.rows, std::min<int64_t>(w.cap * h->Hkv, h->num_sms),
-             biattn::kSharedThreads, size_t(h->shared.smem), shared_args) &&
       (use_tma4  ? launch(h->kern.tma4, std::min<int64_t>(units, h->tma4_ctas), h->kern.tma_threads, h->tma4_smem,
                           own_tma_args)
        : use_tma ? launch(h->kern.tma, std::min<int64_t>(units, h->tma_ctas), h->kern.tma_threads, h->tma_smem,
                           own_tma_args)
                  : launch(h->kern.fn, std::min<int64_t>(units, h->max_ctas), biattn::kThreads, h->smem, own_args)) &&
+      launch(shared_tma ? h->shared.tma : h->shared.rows, std::min<int64_t>(w.cap * h->Hkv, h->num_sms),
+             biattn::kSharedThreads, size_t(h->shared.smem), shared_args) &&
       launch(h->shared.merge, T * h->Hkv * h->shared.merge_slices, biattn::kWideThreads, 0, own_args);
   if (!ok) {
     cudaGetLastError();

@@ -51,17 +51,29 @@ struct SharedParams {
   int32_t cols;                // columns of a unit at most: 128, or 64 above splits of 512
 };
 
+constexpr int kPlanTokens = 1024;
+
 // One block: per token the splits that its group computes, the units of the groups, then the
 // records of all other units in the form that the attention kernels read.
 __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp) {
   __shared__ int32_t warp_sums[32];
   __shared__ int32_t carry;
   __shared__ int32_t nrec;
+  __shared__ int32_t spos[kPlanTokens], snsh[kPlanTokens];   // the first tokens' positions (-1: bad), shares
   const Params& p = sp.a;
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   if (tid == 0) carry = 0, nrec = 0;
+  // a token's position, -1 where it cannot be served
+  auto position = [&](int64_t t) {
+    const int32_t b = p.q_seq[t], pos = p.q_pos[t];
+    return b >= 0 && b < p.B && pos >= 0 && pos <= p.max_pos && int64_t(pos / p.page_size) < p.max_pages ? pos : -1;
+  };
+  // the thread's token of the first 1024: read once, ahead of everything that depends on the groups
+  const int32_t b0 = tid < p.T ? p.q_seq[tid] : -1, p0 = tid < p.T ? p.q_pos[tid] : -1;
+  spos[tid] = b0 >= 0 && b0 < p.B && p0 >= 0 && p0 <= p.max_pos && int64_t(p0 / p.page_size) < p.max_pages ? p0 : -1;
+  snsh[tid] = 0;
   for (int64_t t = tid; t < p.T; t += 1024) sp.nsh[t] = 0;
   __syncthreads();
   const int32_t G = p.Hq / p.Hkv, per = sp.cols / G;     // tokens of a unit
@@ -78,12 +90,11 @@ __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp
       const int32_t n = min(per, e - t0);
       int32_t most = 0, first = 0;
       for (int32_t k = lane; k < n; k += 32) {
-        const int32_t b = p.q_seq[t0 + k], pos = p.q_pos[t0 + k];
+        const int32_t pos = t0 + k < kPlanTokens ? spos[t0 + k] : position(t0 + k);
         // (the split that holds the token itself is always its own)
-        int32_t x = 0;
-        if (b >= 0 && b < p.B && pos >= 0 && pos <= p.max_pos && int64_t(pos / p.page_size) < p.max_pages)
-          x = min(len, pos) / p.split;
+        const int32_t x = pos < 0 ? 0 : min(len, pos) / p.split;
         sp.nsh[t0 + k] = x;
+        if (t0 + k < kPlanTokens) snsh[t0 + k] = x;
         most = max(most, x);
         if (k == 0) first = x;
       }
@@ -109,14 +120,14 @@ __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp
     const int64_t t = base + tid;
     int32_t n = 0, b = 0, pos = 0, sh = 0;
     if (t < p.T) {
-      b = p.q_seq[t];
-      pos = p.q_pos[t];
+      b = base == 0 ? b0 : p.q_seq[t];
+      pos = base == 0 ? p0 : p.q_pos[t];
       if (b < 0 || b >= p.B || pos < 0 || int64_t(pos / p.page_size) >= p.max_pages) {
         atomicOr(p.status, kErrInput);
       } else if (pos > p.max_pos) {
         atomicOr(p.status, kErrBound);
       } else {
-        sh = sp.nsh[t];
+        sh = base == 0 ? snsh[tid] : sp.nsh[t];
         n = (splits_of(pos, p.split) - sh) * p.Hkv;
       }
     }
@@ -247,18 +258,21 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
-  ptx::grid_dependency_wait();   // the plan is complete and visible
+  // No wait here: this grid is launched behind the own units' and may start once each of their blocks
+  // has passed its wait for the plan, so the plan (and what ran before it) is complete; its results are
+  // read from L2.  The two grids' units run side by side where there is room.  The wait at the end makes
+  // this grid end after the other, so that the merge, which waits for this one, waits for both.
   ptx::launch_dependents();
   const tc::Sync sy{abort, p.status, p.timeout_ns};
-  const int32_t units = sp.count[0] * p.Hkv;
+  const int32_t units = __ldcg(sp.count) * p.Hkv;
   const int nblk = p.split / tc::kBlockPos;
 
   // A unit's record; its columns (a multiple of 16, the MMA's step in N) and how many a warpgroup takes.
   struct U {
     int32_t t0, n, s, src, kh, cols, share;
   };
-  auto unit = [&](int32_t u) {
-    const int4 r = sp.srec[u / p.Hkv];
+  auto record = [&](int32_t u) { return u < units ? __ldcg(sp.srec + u / p.Hkv) : make_int4(0, 0, 0, 0); };
+  auto unit = [&](const int4 r, int32_t u) {
     U x;
     x.t0 = r.x, x.n = r.y, x.s = r.z, x.src = r.w;
     x.kh = u % p.Hkv;
@@ -283,8 +297,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           --late;
         }
       };
+      int4 rec = record(int32_t(blockIdx.x));
       for (int32_t u = int32_t(blockIdx.x); u < units && ok; u += int32_t(gridDim.x), ++nu) {
-        const U x = unit(u);
+        const U x = unit(rec, u);
+        rec = record(u + int32_t(gridDim.x));      // the next one's, ahead of its use
         if (nu > 0) {
           if (lane == 0) ok = tc::wait_bar(q_empty, (nu - 1) & 1u, sy);
           ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
@@ -296,7 +312,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             tc::tma_load_3d(sbase + uint32_t(hh * 128 * 128), &tmq, q_full, hh * 64, x.kh * G, x.t0);
         }
         ++q_issued;
-        const int32_t* trow = p.table + int64_t(p.q_seq[x.src]) * p.max_pages;
+        const int32_t* trow = p.table + int64_t(__ldcg(p.q_seq + x.src)) * p.max_pages;
         const int32_t base = x.s * p.split, last = base + p.split - 1;
         for (int32_t i = 0; i < 2 * nblk; ++i, ++seq) {
           const int32_t b = i < nblk ? (i + 1 < nblk ? i + 1 : 0) : i - nblk;
@@ -344,8 +360,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       if (lane == 0) {
         uint32_t seq = 0, nu = 0, np = 0;
         bool ok = true, issued = false;
+        int4 rec = record(int32_t(blockIdx.x));
         for (int32_t u = int32_t(blockIdx.x); u < units && ok; u += int32_t(gridDim.x), ++nu) {
-          const U x = unit(u);
+          const U x = unit(rec, u);
+          rec = record(u + int32_t(gridDim.x));      // the next one's, ahead of its use
           const uint32_t id_qk = tc::idesc_bf16(128, x.cols, false, false);
           ok = tc::wait_bar(q_full, nu & 1u, sy);
           for (int32_t i = 0; i < nblk && ok; ++i, ++seq) {
@@ -398,14 +416,16 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       // ------------------------------------------------------------ the group's tables agree
       const int hid = (warp - 2) * 32 + lane;
       bool differ = false;
+      int4 rec = record(int32_t(blockIdx.x));
       for (int32_t u = int32_t(blockIdx.x); u < units; u += int32_t(gridDim.x)) {
-        const U x = unit(u);
-        const int32_t* src = p.table + int64_t(p.q_seq[x.src]) * p.max_pages;
+        const U x = unit(rec, u);
+        rec = record(u + int32_t(gridDim.x));      // the next one's, ahead of its use
+        const int32_t* src = p.table + int64_t(__ldcg(p.q_seq + x.src)) * p.max_pages;
         const int32_t pg0 = x.s * p.split / p.page_size, pgs = ((x.s + 1) * p.split - 1) / p.page_size + 1 - pg0;
         for (int32_t k = x.kh; k < x.n; k += p.Hkv) {    // (the KV heads' units share the tokens out)
-          if (sp.nsh[x.t0 + k] <= x.s) continue;
-          const int32_t* row = p.table + int64_t(p.q_seq[x.t0 + k]) * p.max_pages;
-          for (int32_t i = hid; i < pgs; i += 64) differ |= row[pg0 + i] != src[pg0 + i];
+          if (__ldcg(sp.nsh + x.t0 + k) <= x.s) continue;
+          const int32_t* row = p.table + int64_t(__ldcg(p.q_seq + x.t0 + k)) * p.max_pages;
+          for (int32_t i = hid; i < pgs; i += 64) differ |= __ldcg(row + pg0 + i) != __ldcg(src + pg0 + i);
         }
       }
       if (differ) atomicOr(p.status, kErrInput);
@@ -423,8 +443,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t prow = sbase + uint32_t(C::OFF_P + pos * 128);
     uint32_t nu = 0, np = 0;
     bool ok = true;
+    int4 rec = record(int32_t(blockIdx.x));
     for (int32_t u = int32_t(blockIdx.x); u < units && ok; u += int32_t(gridDim.x), ++nu) {
-      const U x = unit(u);
+      const U x = unit(rec, u);
+      rec = record(u + int32_t(gridDim.x));      // the next one's, ahead of its use
       const int32_t cb = min(i * x.share, x.cols), nc = min(x.share, x.cols - cb);      // its columns: 0, 16 or 32
       const uint32_t atom = prow + uint32_t((cb >> 6) * C::ATOM), ch0 = uint32_t(cb & 63) / 8;
       // pass 1: each column's maximum (of the raw sums: the scaling is monotone)
@@ -532,7 +554,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       // which of the columns are tokens that share the split
       const int32_t tok = (cb + lane) / G;
       const uint32_t live =
-          __ballot_sync(0xFFFFFFFFu, lane < nc && tok < x.n && sp.nsh[x.t0 + min(tok, x.n - 1)] > x.s);
+          __ballot_sync(0xFFFFFFFFu, lane < nc && tok < x.n && __ldcg(sp.nsh + x.t0 + min(tok, x.n - 1)) > x.s);
       if (ok && w4 == 0 && ((live >> lane) & 1u)) {
         const float l = __fadd_rn(__fadd_rn(__fadd_rn(red[lane], red[32 + lane]), red[64 + lane]), red[96 + lane]);
         *reinterpret_cast<float2*>(p.ml + (row0 + tok * stride_t + (cb + lane) % G) * 2) = make_float2(mine[lane], l);
@@ -573,6 +595,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+  ptx::grid_dependency_wait();   // (see above)
 }
 
 // merge_kernel's arithmetic, output by output the same operations in the same order, for lists of many
