@@ -15,9 +15,9 @@
  * heads to the cache slot of (b, p), k_cache[page_table[b][p / page_size], p % page_size, kh, :]
  * and v_cache alike: the layout that bi_attention.h and bi_prompt.h read.
  *
- * Batch invariance: a head's elements are summed by D / 8 lanes, each its eight consecutive
- * elements in ascending order by fma, combined by a fixed xor butterfly; nothing else of the call
- * enters, so q_out[t] and the slot's contents are a function of qkv[t], the weights and p alone.
+ * Batch invariance: a head's squares are summed by D / 8 lanes, each its eight elements (fixed by
+ * rot_dim and the pairing) in two chains of fma, combined by a fixed xor butterfly; nothing else of
+ * the call enters, so q_out[t] and the slot's contents are a function of qkv[t], the weights and p.
  *
  * Conventions (as in bi_gemm.h, whose BI_GEMM_* return codes these functions use):
  *   - qkv bf16 [T, (Hq + 2 Hkv) D] with rows qkv_stride elements apart; gq, gk bf16 [D] (both, or

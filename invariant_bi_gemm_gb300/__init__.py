@@ -644,27 +644,18 @@ class BiAttention:
         for positions 0 .. group_len[g] - 1 (int32 [groups]).  The prefix is read once per group;
         the result has the bits of run()."""
         import torch
-        dev = q.device
-        T = int(q.shape[0])
-        if q.dim() != 3 or q.shape[1] != self.Hq or q.shape[2] != self.D or q.dtype != torch.bfloat16 or \
-                not q.is_cuda or not q.is_contiguous():
-            raise ValueError("q must be a contiguous bf16 CUDA tensor [T, num_q_heads, head_dim]")
-        _check_cache(k_cache, v_cache, page_table, self.page_size, self.Hkv, self.D, dev)
-        _check_int32(dev, (T,), q_seq=q_seq, q_pos=q_pos)
-        groups = int(group_len.shape[0])
-        _check_int32(dev, (groups,), group_len=group_len)
-        _check_int32(dev, (groups + 1,), group_start=group_start)
-        if o is None:
-            o = torch.empty_like(q)
-        if o.shape != q.shape or o.dtype != torch.bfloat16 or o.device != dev or not o.is_contiguous():
-            raise ValueError("o must be a contiguous bf16 tensor shaped like q")
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        bi_attention_run_shared(self.handle, q.data_ptr(), T, q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(),
-                                v_cache.data_ptr(), int(k_cache.shape[0]), page_table.data_ptr(),
-                                int(page_table.shape[0]), int(page_table.shape[1]), int(max_pos),
-                                group_start.data_ptr(), group_len.data_ptr(), groups, o.data_ptr(), s)
+        T, index, o = _check_queries(q, o, self.Hq, self.D)
+        pages, seqs, per = _check_cache(k_cache, v_cache, page_table, (self.page_size, self.Hkv, self.D), index)
+        groups, i32 = group_len.shape[0], torch.int32
+        _check_tensor("q_seq", q_seq, i32, (T,), index)
+        _check_tensor("q_pos", q_pos, i32, (T,), index)
+        _check_tensor("group_len", group_len, i32, (groups,), index)
+        _check_tensor("group_start", group_start, i32, (groups + 1,), index)
+        _check(library().bi_attention_run_shared(self.handle, q.data_ptr(), T, q_seq.data_ptr(), q_pos.data_ptr(),
+                                                 k_cache.data_ptr(), v_cache.data_ptr(), pages, page_table.data_ptr(),
+                                                 seqs, per, max_pos, group_start.data_ptr(), group_len.data_ptr(),
+                                                 groups, o.data_ptr(), _stream_of(stream, index)),
+               "bi_attention_run_shared")
         return o
 
     def workspace_size(self, T: int, max_pos: int) -> int:
@@ -685,25 +676,50 @@ class BiAttention:
             pass
 
 
-def _check_cache(k_cache, v_cache, page_table, page_size: int, Hkv: int, D: int, dev) -> None:
+def _stream_of(stream, index: int) -> int:
+    """The cudaStream_t of a stream argument; the device's current stream for None."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _check_tensor(name: str, t, dtype, shape, index: int) -> None:
+    """t: a contiguous tensor of this dtype and shape on CUDA device `index`.  (These checks are on
+    the path of a single token's step: plain attributes, no objects built unless something is wrong.)"""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
+
+
+def _check_cache(k_cache, v_cache, page_table, page_shape, index: int):
     """The paged cache of one layer: k_cache, v_cache [pages, page_size, Hkv, D] bf16, page_table
-    [num_seqs, max_pages] int32, all contiguous on `dev`."""
+    [num_seqs, max_pages] int32.  Returns (pages, num_seqs, max_pages)."""
     import torch
-    if k_cache.dim() != 4 or tuple(k_cache.shape[1:]) != (page_size, Hkv, D) or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache, v_cache must be [pages, page_size, num_kv_heads, head_dim]")
-    if page_table.dim() != 2:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1:] != page_shape:
+        raise ValueError(f"k_cache must be [pages, page_size, num_kv_heads, head_dim] = [pages, {page_shape}]")
+    _check_tensor("k_cache", k_cache, torch.bfloat16, shape, index)
+    _check_tensor("v_cache", v_cache, torch.bfloat16, shape, index)
+    table = page_table.shape
+    if len(table) != 2:
         raise ValueError("page_table must be [num_seqs, max_pages]")
-    for name, tns, dt in (("k_cache", k_cache, torch.bfloat16), ("v_cache", v_cache, torch.bfloat16),
-                          ("page_table", page_table, torch.int32)):
-        if tns.dtype != dt or not tns.is_contiguous() or tns.device != dev:
-            raise ValueError(f"{name} must be a contiguous {dt} tensor on {dev}")
+    _check_tensor("page_table", page_table, torch.int32, table, index)
+    return shape[0], table[0], table[1]
 
 
-def _check_int32(dev, shape, **tensors) -> None:
+def _check_queries(q, o, Hq: int, D: int):
+    """q [T, Hq, D] bf16 and o like it (made where it is None).  Returns (T, device index, o)."""
     import torch
-    for name, tns in tensors.items():
-        if tns.dtype != torch.int32 or not tns.is_contiguous() or tns.device != dev or tuple(tns.shape) != shape:
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {dev}")
+    shape, index = q.shape, q.get_device()
+    if len(shape) != 3 or shape[1] != Hq or shape[2] != D or index < 0:
+        raise ValueError("q must be a CUDA tensor [T, num_q_heads, head_dim]")
+    _check_tensor("q", q, torch.bfloat16, shape, index)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _check_tensor("o", o, torch.bfloat16, shape, index)
+    return shape[0], index, o
 
 
 class BiQkRope:
@@ -720,6 +736,7 @@ class BiQkRope:
                  eps: float = 1e-6, interleaved: bool = False):
         self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
         self.rot_dim = int(rot_dim) if rot_dim is not None else self.D
+        self._width, self._page_shape = (self.Hq + 2 * self.Hkv) * self.D, (self.page_size, self.Hkv, self.D)
         self.handle = bi_qkrope_create(self.Hq, self.Hkv, self.D, self.page_size, self.rot_dim, interleaved, eps)
 
     @property
@@ -728,36 +745,37 @@ class BiQkRope:
 
     def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
         import torch
-        dev = qkv.device
-        T, width = int(qkv.shape[0]), (self.Hq + 2 * self.Hkv) * self.D
-        if qkv.dim() != 2 or qkv.shape[1] != width or qkv.dtype != torch.bfloat16 or not qkv.is_cuda:
+        bf16, shape, index, width = torch.bfloat16, qkv.shape, qkv.get_device(), self._width
+        if len(shape) != 2 or shape[1] != width or qkv.dtype is not bf16 or index < 0:
             raise ValueError("qkv must be a bf16 CUDA tensor [T, (num_q_heads + 2 num_kv_heads) head_dim]")
-        if qkv.stride(1) != 1 or (T > 1 and qkv.stride(0) < width):
-            raise ValueError("qkv rows must be contiguous and must not overlap")
-        if (gq is None) != (gk is None):
-            raise ValueError("gq and gk: both norm weights or neither")
-        for name, g in (("gq", gq), ("gk", gk)):
-            if g is not None and (tuple(g.shape) != (self.D,) or g.dtype != torch.bfloat16 or g.device != dev or
-                                  not g.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous bf16 tensor [head_dim] on {dev}")
-        if cos_sin.dim() != 2 or cos_sin.shape[1] != self.rot_dim or cos_sin.dtype != torch.float32 or \
-                cos_sin.device != dev or not cos_sin.is_contiguous():
-            raise ValueError(f"cos_sin must be a contiguous fp32 tensor [positions, rot_dim] on {dev}")
-        _check_int32(dev, (T,), q_seq=q_seq, q_pos=q_pos)
-        _check_cache(k_cache, v_cache, page_table, self.page_size, self.Hkv, self.D, dev)
+        T, stride = shape[0], width
+        if not qkv.is_contiguous():
+            stride, inner = qkv.stride()
+            if inner != 1 or stride < width:
+                raise ValueError("qkv rows must be contiguous and must not overlap")
+        if gq is None or gk is None:
+            if gq is not gk:
+                raise ValueError("gq and gk: both norm weights or neither")
+            wq = wk = None
+        else:
+            _check_tensor("gq", gq, bf16, (self.D,), index)
+            _check_tensor("gk", gk, bf16, (self.D,), index)
+            wq, wk = gq.data_ptr(), gk.data_ptr()
+        angles = cos_sin.shape
+        if len(angles) != 2 or angles[1] != self.rot_dim:
+            raise ValueError("cos_sin must be [positions, rot_dim]")
+        _check_tensor("cos_sin", cos_sin, torch.float32, angles, index)
+        _check_tensor("q_seq", q_seq, torch.int32, (T,), index)
+        _check_tensor("q_pos", q_pos, torch.int32, (T,), index)
+        pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         if q_out is None:
-            q_out = torch.empty((T, self.Hq, self.D), dtype=torch.bfloat16, device=dev)
-        if tuple(q_out.shape) != (T, self.Hq, self.D) or q_out.dtype != torch.bfloat16 or q_out.device != dev or \
-                not q_out.is_contiguous():
-            raise ValueError(f"q_out must be a contiguous bf16 tensor [T, num_q_heads, head_dim] on {dev}")
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        bi_qkrope_run(self.handle, qkv.data_ptr(), T, int(qkv.stride(0)) if T > 1 else width,
-                      None if gq is None else gq.data_ptr(), None if gk is None else gk.data_ptr(),
-                      cos_sin.data_ptr(), int(cos_sin.shape[0]), q_seq.data_ptr(), q_pos.data_ptr(),
-                      k_cache.data_ptr(), v_cache.data_ptr(), int(k_cache.shape[0]), page_table.data_ptr(),
-                      int(page_table.shape[0]), int(page_table.shape[1]), q_out.data_ptr(), s)
+            q_out = torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device)
+        else:
+            _check_tensor("q_out", q_out, bf16, (T, self.Hq, self.D), index)
+        _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), angles[0],
+                                       q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                       pages, page_table.data_ptr(), seqs, per, q_out.data_ptr(),
+                                       _stream_of(stream, index)), "bi_qkrope_run")
         return q_out
 
     __call__ = run
@@ -795,6 +813,7 @@ class BiPromptAttention:
                  scale: float | None = None):
         self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
         self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
+        self._page_shape = (self.page_size, self.Hkv, self.D)
         self.handle = bi_prompt_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale)
 
     @property
@@ -803,24 +822,13 @@ class BiPromptAttention:
 
     def run(self, q, q_start, q_pos0, k_cache, v_cache, page_table, max_pos: int, o=None, stream=None):
         import torch
-        dev = q.device
-        if q.dim() != 3 or q.shape[1] != self.Hq or q.shape[2] != self.D or q.dtype != torch.bfloat16 or \
-                not q.is_cuda or not q.is_contiguous():
-            raise ValueError("q must be a contiguous bf16 CUDA tensor [T, num_q_heads, head_dim]")
-        _check_cache(k_cache, v_cache, page_table, self.page_size, self.Hkv, self.D, dev)
-        T, B = int(q.shape[0]), int(page_table.shape[0])
-        _check_int32(dev, (B + 1,), q_start=q_start)
-        _check_int32(dev, (B,), q_pos0=q_pos0)
-        if o is None:
-            o = torch.empty_like(q)
-        if o.shape != q.shape or o.dtype != torch.bfloat16 or o.device != dev or not o.is_contiguous():
-            raise ValueError("o must be a contiguous bf16 tensor shaped like q")
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        bi_prompt_run(self.handle, q.data_ptr(), T, q_start.data_ptr(), q_pos0.data_ptr(), B, k_cache.data_ptr(),
-                      v_cache.data_ptr(), int(k_cache.shape[0]), page_table.data_ptr(), int(page_table.shape[1]),
-                      int(max_pos), o.data_ptr(), s)
+        T, index, o = _check_queries(q, o, self.Hq, self.D)
+        pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
+        _check_tensor("q_start", q_start, torch.int32, (seqs + 1,), index)
+        _check_tensor("q_pos0", q_pos0, torch.int32, (seqs,), index)
+        _check(library().bi_prompt_run(self.handle, q.data_ptr(), T, q_start.data_ptr(), q_pos0.data_ptr(), seqs,
+                                       k_cache.data_ptr(), v_cache.data_ptr(), pages, page_table.data_ptr(), per,
+                                       max_pos, o.data_ptr(), _stream_of(stream, index)), "bi_prompt_run")
         return o
 
     __call__ = run

@@ -2,12 +2,13 @@
 // values to the paged cache, in one pass over the fused projection's output, for sm_103a.
 // Implements include/bi_qkrope.h.
 //
-// Bound: HBM bandwidth (every element read once, written once, about eight operations each); one
-// launch's latency for a few tokens.  A head of D elements belongs to D / 8 lanes, one 16-byte
-// load, one store and eight fp32 values each, so the norm's sum is a butterfly inside the warp and
-// a rotation partner D / 2 away is one shuffle.  A token has a power of two of such lane groups,
-// each with up to kHeads heads at a time in registers: their loads are issued before the token's
-// position is known, and its cosines, sines and the norm weights are read once for all of them.
+// Bound: HBM bandwidth (every element read once, written once) beside the instructions, about eight
+// operations an element; one launch's latency for a few tokens.  A head of D elements belongs to D / 8
+// lanes, eight elements each: two runs of four that are rotation partners (dimensions 4 j and
+// 4 j + rot / 2 on), or eight neighbours for an interleaved handle, so that a rotation needs no other
+// lane and its arithmetic goes two values an instruction.  A token has a power of two of such lane
+// groups, each with up to kHeads heads at a time in registers: their loads are issued before the
+// token's position is known, and its cosines, sines and the norm weights are read once for all of them.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -44,7 +45,7 @@ struct Params {
   int64_t T, stride, num_positions, num_pages, B, max_pages;
   int32_t Hq, Hkv, page_size, rot;
   int32_t groups_log2;      // lane groups per token
-  float D, eps;
+  float eps;
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -56,9 +57,30 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
-  x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
-  x[4] = bf16_lo(v.z), x[5] = bf16_hi(v.z), x[6] = bf16_lo(v.w), x[7] = bf16_hi(v.w);
+// Two fp32 values in a register pair, each rounded as by the scalar instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t widen(uint32_t w) { return pair(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pack_bf16x2(lo, hi);
 }
 
 template <int D, bool kInterleaved>
@@ -69,21 +91,29 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = int(threadIdx.x);
-  const int l = tid & (LANES - 1);                      // lane of the head: dimensions 8 l .. 8 l + 7
+  const int l = tid & (LANES - 1);                      // lane of the head
   const int groups = 1 << p.groups_log2;
   const int g = (tid / LANES) & (groups - 1);           // lane group of the token
   const int per_block = (kThreads / LANES) >> p.groups_log2;
   const int64_t t = int64_t(blockIdx.x) * per_block + ((tid / LANES) >> p.groups_log2);
   const bool live = t < p.T;                            // (whole lane groups: the shuffles stay inside them)
   const int H = p.Hq + 2 * p.Hkv;
+  // this lane's two runs of four dimensions, and whether they are rotated
+  const int half = p.rot >> 1, eighth = p.rot >> 3;
+  const bool turned = l < eighth;
+  const int da = kInterleaved || !turned ? 8 * l : 4 * l, db = kInterleaved || !turned ? da + 4 : da + half;
 
-  const uint16_t* row = p.qkv + (live ? t : 0) * p.stride + l * 8;
-  uint4 raw[kHeads];
+  const uint16_t* row = p.qkv + (live ? t : 0) * p.stride;
+  uint2 ra[kHeads], rb[kHeads];
   auto load = [&](int h0) {
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       const int h = h0 + k * groups;
-      raw[k] = live && h < H ? *reinterpret_cast<const uint4*>(row + int64_t(h) * D) : make_uint4(0, 0, 0, 0);
+      ra[k] = rb[k] = make_uint2(0, 0);
+      if (live && h < H) {
+        ra[k] = *reinterpret_cast<const uint2*>(row + h * D + da);
+        rb[k] = *reinterpret_cast<const uint2*>(row + h * D + db);
+      }
     }
   };
   load(g);
@@ -97,12 +127,11 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
             int64_t(pos / p.page_size) < p.max_pages;
   if (live && !ok) atomicOr(p.status, kErrInput);
   int64_t slot = 0;
-  float co[8], si[8];
-  // the rotation of this lane's dimensions: cosines and (signed) sines per element
-  const int half = p.rot >> 1;
-  const bool turned = 8 * l < p.rot;
+  // cosines and sines of the lane's pairs: of the four pairs (a, b) of its runs, or, interleaved, of each
+  // two neighbours, both alike and the sine with either sign
+  uint64_t co[kInterleaved ? 4 : 2], si[kInterleaved ? 4 : 2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) co[e] = 1.0f, si[e] = 0.0f;
+  for (int e = 0; e < (kInterleaved ? 4 : 2); ++e) co[e] = si[e] = 0;
   if (ok) {
     const int64_t page = p.table[int64_t(b) * p.max_pages + pos / p.page_size];
     if (page < 0 || page >= p.num_pages) {
@@ -111,69 +140,81 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
     }
     slot = page * p.page_size + pos % p.page_size;
     if (turned) {
-      const float* c = p.cs + int64_t(pos) * p.rot;
+      const float* c = p.cs + int64_t(pos) * p.rot + 4 * l;
+      const float4 cv = *reinterpret_cast<const float4*>(c);
+      const float4 sv = *reinterpret_cast<const float4*>(c + half);
       if constexpr (kInterleaved) {
-        const float4 cv = *reinterpret_cast<const float4*>(c + 4 * l);
-        const float4 sv = *reinterpret_cast<const float4*>(c + half + 4 * l);
-        const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) co[e] = cc[e >> 1], si[e] = (e & 1) ? ss[e >> 1] : -ss[e >> 1];
+        co[0] = pair(cv.x, cv.x), co[1] = pair(cv.y, cv.y), co[2] = pair(cv.z, cv.z), co[3] = pair(cv.w, cv.w);
+        si[0] = pair(-sv.x, sv.x), si[1] = pair(-sv.y, sv.y), si[2] = pair(-sv.z, sv.z), si[3] = pair(-sv.w, sv.w);
       } else {
-        const bool first = 8 * l < half;
-        const int i = 8 * l - (first ? 0 : half);
-#pragma unroll
-        for (int e4 = 0; e4 < 8; e4 += 4) {
-          const float4 cv = *reinterpret_cast<const float4*>(c + i + e4);
-          const float4 sv = *reinterpret_cast<const float4*>(c + half + i + e4);
-          co[e4] = cv.x, co[e4 + 1] = cv.y, co[e4 + 2] = cv.z, co[e4 + 3] = cv.w;
-          si[e4] = first ? -sv.x : sv.x, si[e4 + 1] = first ? -sv.y : sv.y;
-          si[e4 + 2] = first ? -sv.z : sv.z, si[e4 + 3] = first ? -sv.w : sv.w;
-        }
+        co[0] = pair(cv.x, cv.y), co[1] = pair(cv.z, cv.w);
+        si[0] = pair(sv.x, sv.y), si[1] = pair(sv.z, sv.w);
       }
     }
   }
-  // lane (of the warp) that holds the rotation partners of this lane's elements: half = 8 k, so
-  // they sit k lanes away in the same head
-  const int warp_lane = tid & 31;
-  const int partner = kInterleaved || !turned ? warp_lane : warp_lane + (8 * l < half ? half / 8 : -(half / 8));
+  uint2 wqa = make_uint2(0, 0), wqb = wqa, wka = wqa, wkb = wqa;
+  if (p.gq) {
+    wqa = *reinterpret_cast<const uint2*>(p.gq + da), wqb = *reinterpret_cast<const uint2*>(p.gq + db);
+    wka = *reinterpret_cast<const uint2*>(p.gk + da), wkb = *reinterpret_cast<const uint2*>(p.gk + db);
+  }
+  // The loop is uniform over a lane group, not over a warp: a shuffle names its group's lanes.
+  const uint32_t mask = LANES == 16 ? 0xFFFFu << (tid & 16) : 0xFFu << (tid & 24);
 
   for (int h0 = g;; h0 += kHeads * groups) {
-    // The loop is uniform over a lane group, not over a warp: a shuffle names its group's lanes.
-    const uint32_t mask = LANES == 16 ? 0xFFFFu << (warp_lane & 16) : 0xFFu << (warp_lane & 24);
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       const int h = h0 + k * groups;
       if (h >= H) break;
-      if (h >= p.Hq + p.Hkv) {
-        if (ok)
-          *reinterpret_cast<uint4*>(p.vc + (slot * p.Hkv + (h - p.Hq - p.Hkv)) * D + l * 8) = raw[k];
+      if (h >= p.Hq + p.Hkv) {                          // values: as they are
+        if (ok) {
+          uint16_t* dst = p.vc + (slot * p.Hkv + (h - p.Hq - p.Hkv)) * D;
+          *reinterpret_cast<uint2*>(dst + da) = ra[k];
+          *reinterpret_cast<uint2*>(dst + db) = rb[k];
+        }
         continue;
       }
       const bool key = h >= p.Hq;
-      float x[8];
-      widen(raw[k], x);
+      uint64_t x[4] = {widen(ra[k].x), widen(ra[k].y), widen(rb[k].x), widen(rb[k].y)};
       if (p.gq) {
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = __fmaf_rn(x[e], x[e], s);
+        uint64_t q2 = mul2(x[0], x[0]);
+        q2 = fma2(x[1], x[1], q2);
+        q2 = fma2(x[2], x[2], q2);
+        q2 = fma2(x[3], x[3], q2);
+        float s0, s1;
+        unpair(q2, s0, s1);
+        float s = __fadd_rn(s0, s1);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(mask, s, o));
-        const float r = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, p.D), p.eps));
-        float w[8];
-        widen(*reinterpret_cast<const uint4*>((key ? p.gk : p.gq) + l * 8), w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), w[e]);
+        const float r = __frsqrt_rn(__fmaf_rn(s, 1.0f / D, p.eps));     // (the product with 1 / D is exact)
+        const uint64_t r2 = pair(r, r);
+        x[0] = mul2(mul2(x[0], r2), widen(key ? wka.x : wqa.x));
+        x[1] = mul2(mul2(x[1], r2), widen(key ? wka.y : wqa.y));
+        x[2] = mul2(mul2(x[2], r2), widen(key ? wkb.x : wqb.x));
+        x[3] = mul2(mul2(x[3], r2), widen(key ? wkb.y : wqb.y));
       }
-      float y[8];
+      if (turned) {
+        if constexpr (kInterleaved) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float other = kInterleaved ? x[e ^ 1] : __shfl_sync(mask, x[e], partner);
-        y[e] = turned ? __fmaf_rn(x[e], co[e], __fmul_rn(other, si[e])) : x[e];
+          for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            unpair(x[e], lo, hi);
+            x[e] = fma2(x[e], co[e], mul2(pair(hi, lo), si[e]));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t a = x[e], c = x[e + 2];
+            float lo, hi;
+            unpair(mul2(c, si[e]), lo, hi);
+            x[e] = fma2(a, co[e], pair(-lo, -hi));
+            x[e + 2] = fma2(c, co[e], mul2(a, si[e]));
+          }
+        }
       }
       if (ok) {
         uint16_t* dst = key ? p.kc + (slot * p.Hkv + (h - p.Hq)) * D : p.q_out + (t * p.Hq + h) * D;
-        *reinterpret_cast<uint4*>(dst + l * 8) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                            pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        *reinterpret_cast<uint2*>(dst + da) = make_uint2(narrow(x[0]), narrow(x[1]));
+        *reinterpret_cast<uint2*>(dst + db) = make_uint2(narrow(x[2]), narrow(x[3]));
       }
     }
     if (h0 + kHeads * groups >= H) break;
@@ -288,7 +329,6 @@ BI_GEMM_API int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t
   p.page_size = h->page_size;
   p.rot = h->rot;
   p.groups_log2 = h->groups_log2;
-  p.D = float(h->D);
   p.eps = h->eps;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
