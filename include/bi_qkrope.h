@@ -52,8 +52,11 @@ typedef struct {
   int32_t num_q_heads, num_kv_heads, head_dim, page_size;
   int32_t rot_dim;            /* rotated dimensions of a head                              */
   int32_t interleaved;        /* 1: pairs (2 i, 2 i + 1); 0: pairs (i, i + rot_dim / 2)      */
-  int32_t threads;            /* threads per block                                          */
+  int32_t threads;            /* threads per block of the form for few tokens                */
   int32_t tokens_per_block;
+  int32_t ring_tokens;        /* the form for many tokens: tokens on their way per block (0:
+                                 rows too long for it), and its resident blocks              */
+  int32_t ring_ctas;
 } bi_qkrope_config;
 
 /* Create a handle.  Requirements: head_dim 64 or 128; rot_dim a multiple of 16, 16..head_dim;
@@ -72,8 +75,9 @@ int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride,
                   void* k_cache, void* v_cache, int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
                   int64_t max_pages, void* q_out, void* stream);
 
-/* Synchronise `stream`; BI_GEMM_ERR_INVALID_ARG if a kernel caught a bad input since the last call
- * (the status is then cleared); BI_GEMM_ERR_CUDA if synchronisation failed; else BI_GEMM_OK. */
+/* Synchronise `stream`; BI_GEMM_ERR_TIMEOUT if a bounded wait (2 s) expired, else
+ * BI_GEMM_ERR_INVALID_ARG if a kernel caught a bad input, since the last call (the status is then
+ * cleared); BI_GEMM_ERR_CUDA if synchronisation failed; else BI_GEMM_OK. */
 int bi_qkrope_get_device_error(bi_qkrope_t h, void* stream);
 
 int bi_qkrope_get_config(bi_qkrope_t h, bi_qkrope_config* c);

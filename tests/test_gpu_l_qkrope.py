@@ -69,9 +69,12 @@ def reference(a, Hq, Hkv, D, page, rot, interleaved):
     (5, 1, 1, 64, 1, 16, True, True, 0),
     (130, 40, 40, 128, 64, 96, False, True, 0),          # more heads than a block holds at once
     (9, 3, 1, 64, 12, 48, False, False, 24),
+    (6001, 16, 4, 64, 16, 64, False, True, 8),           # the form for many tokens
+    (5000, 8, 2, 128, 7, 64, True, True, 0),
+    (4001, 2, 1, 64, 32, 32, True, False, 0),
 ])
 def test_every_element(T, Hq, Hkv, D, page, rot, inter, norm, pad):
-    a = make(T, Hq, Hkv, D, page, rot, norm=norm, pad=pad)
+    a = make(T, Hq, Hkv, D, page, rot, norm=norm, pad=pad, far=2500)
     kc0, vc0 = a["k_cache"].clone(), a["v_cache"].clone()
     h = BiQkRope(Hq, Hkv, D, page, rot_dim=rot, eps=EPS, interleaved=inter)
     q = h.run(**a)
@@ -99,6 +102,29 @@ def test_token_independent_of_its_batch():
         b = dict(a, qkv=a["qkv"][t:t + 1], q_seq=a["q_seq"][t:t + 1], q_pos=a["q_pos"][t:t + 1])
         assert torch.equal(h.run(**b)[0].view(torch.int16), q[t].view(torch.int16))
     assert torch.equal(a["k_cache"].view(torch.int16), kc.view(torch.int16))
+    h.close()
+
+
+def test_token_independent_of_the_form():
+    """Tokens of a call large enough for the form for many tokens, alone and in calls on both sides of
+    the border between the forms: the same bits; bad tokens among them are reported and left out."""
+    h = BiQkRope(4, 2, 64, 16, eps=EPS)
+    border = 4 * h.config["ring_ctas"]
+    a = make(border + 3, 4, 2, 64, 16, 64, far=4000)
+    q = h.run(**a).clone()
+    kc = a["k_cache"].clone()
+    cut = lambda lo, hi: dict(a, qkv=a["qkv"][lo:hi], q_seq=a["q_seq"][lo:hi], q_pos=a["q_pos"][lo:hi])
+    for lo, hi in ((0, 1), (border, border + 3), (3, border + 2), (3, border + 3)):
+        assert torch.equal(h.run(**cut(lo, hi)).view(torch.int16), q[lo:hi].view(torch.int16)), (lo, hi)
+    assert torch.equal(a["k_cache"].view(torch.int16), kc.view(torch.int16)) and h.device_error() == 0
+    bad = dict(a, q_seq=a["q_seq"].clone())
+    bad["q_seq"][[5, border]] = -1
+    out = torch.full_like(q, 7.0)
+    h.run(**bad, q_out=out)
+    assert h.device_error() == bg.BI_GEMM_ERR_INVALID_ARG
+    keep = torch.ones(border + 3, dtype=torch.bool)
+    keep[[5, border]] = False
+    assert bool((out[~keep] == 7).all()) and torch.equal(out[keep].view(torch.int16), q[keep].view(torch.int16))
     h.close()
 
 
