@@ -112,8 +112,10 @@ int bi_attention_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, ui
  * 4-byte aligned.  Caught by the kernels, as BI_GEMM_ERR_INVALID_ARG from
  * bi_attention_get_device_error with the group's outputs undefined: a group_start that descends or
  * leaves [0, T], a negative group_len, page tables that differ within a shared split.  num_groups
- * >= 0; all else as bi_attention_run.  Queues four kernels: a plan, the groups' units, the other
- * units, the merge. */
+ * >= 0; all else as bi_attention_run, but for the workspace: run_shared has its own, grown by
+ * cudaMalloc (BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph that needs more than
+ * an earlier call of its size left; a graph stays valid when later calls grow it).  Queues four
+ * kernels: a plan, the tokens' own units, the groups' units beside them, the merge. */
 int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
                             const int32_t* q_pos, const void* k_cache, const void* v_cache,
                             int64_t num_pages, const int32_t* page_table, int64_t num_seqs,

@@ -59,7 +59,7 @@ def build(force: bool = False, verbose: bool = False) -> dict:
             continue
         tmp = out + f".tmp{os.getpid()}"
         cmd = [
-            nvcc(), "-std=c++17", "-O3", ARCH, "-lineinfo",
+            nvcc(), "-std=c++17", "-O3", ARCH, "-lineinfo", "--threads", "8",
             "-Xcompiler", "-fPIC,-fvisibility=hidden",
             "-Xlinker", "-Bsymbolic",
             "-shared", "-o", tmp, *[os.path.join(CSRC, s) for s in srcs],

@@ -6,7 +6,9 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <mutex>
+#include <vector>
 
+#include "../../include/bi_gemm.h"
 #include "ptx.cuh"
 
 namespace biattn_tc {
@@ -289,6 +291,47 @@ __device__ __forceinline__ void load_block_rows(uint32_t dst, const uint16_t* ba
 
 // Page sizes whose blocks are whole TMA boxes: powers of two from 8 (one 1024-byte swizzle atom) up.
 inline bool tma_page_size(int64_t ps) { return ps >= 8 && (ps & (ps - 1)) == 0; }
+
+// A handle's device scratch.  It grows to what a call needs, at least to twice what it was, and earlier
+// blocks live until the handle does: a graph captured with one of them may still be replayed.
+struct Workspace {
+  void* at = nullptr;
+  size_t bytes = 0;
+  std::vector<void*> earlier;
+
+  // A call being captured cannot allocate for good: it uses what earlier calls (or a reserve) left.
+  int need(size_t n, cudaStream_t st) {
+    if (n <= bytes) return BI_GEMM_OK;
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) {
+      cudaGetLastError();
+      return BI_GEMM_ERR_CUDA;
+    }
+    if (capturing != cudaStreamCaptureStatusNone) return BI_GEMM_ERR_SCRATCH_LIMIT;
+    const size_t size = n > 2 * bytes ? n : 2 * bytes;
+    void* p = nullptr;
+    if (cudaMalloc(&p, size) != cudaSuccess) {
+      cudaGetLastError();
+      return BI_GEMM_ERR_OOM;
+    }
+    try {
+      if (at) earlier.push_back(at);
+    } catch (...) {
+      cudaFree(p);
+      return BI_GEMM_ERR_OOM;
+    }
+    at = p;
+    bytes = size;
+    return BI_GEMM_OK;
+  }
+  void release() {
+    if (at) cudaFree(at);
+    for (void* p : earlier) cudaFree(p);
+    at = nullptr;
+    bytes = 0;
+    earlier.clear();
+  }
+};
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

@@ -1228,6 +1228,7 @@ struct bi_attention {
   size_t tma4_smem = 0;
   biattn::KernelInfo kern;
   biattn::SharedInfo shared;
+  biattn_tc::Workspace shared_ws;   // run_shared's own
   uint32_t* d_status = nullptr;
   void* ws = nullptr;
   size_t ws_bytes = 0;
@@ -1581,11 +1582,15 @@ BI_GEMM_API int bi_attention_shared_workspace_size(bi_attention_t h, int64_t T, 
   return BI_GEMM_OK;
 }
 
-BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
-                                        const int32_t* q_pos, const void* k_cache, const void* v_cache,
-                                        int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
-                                        int64_t max_pages, int64_t max_pos, const int32_t* group_start,
-                                        const int32_t* group_len, int64_t num_groups, void* o, void* stream) {
+namespace {
+
+// bi_attention_run_shared with the failure injection of the test controls (stall >= 0: that block of
+// the groups' kernel loads no keys) and the limit of the waits.
+int attention_run_shared(bi_attention* h, const void* q, int64_t T, const int32_t* q_seq, const int32_t* q_pos,
+                         const void* k_cache, const void* v_cache, int64_t num_pages, const int32_t* page_table,
+                         int64_t num_seqs, int64_t max_pages, int64_t max_pos, const int32_t* group_start,
+                         const int32_t* group_len, int64_t num_groups, void* o, void* stream, int32_t stall,
+                         uint64_t timeout_ns) {
   if (!h || T < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || max_pos < 0 || num_groups < 0)
     return BI_GEMM_ERR_INVALID_ARG;
   // without a group, or a bound that leaves no whole split before a token's own, nothing is shared
@@ -1629,19 +1634,8 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
                           biattn_tc::encode_pages(&smk, k_cache, rows, h->Hkv, h->D, h->page_size) &&
                           biattn_tc::encode_pages(&smv, v_cache, rows, h->Hkv, h->D, h->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (w.total > h->ws_bytes) {
-    if (h->ws) cudaFreeAsync(h->ws, st);
-    h->ws = nullptr;
-    h->ws_bytes = 0;
-    void* ws = nullptr;
-    if (cudaMallocAsync(&ws, w.total, st) != cudaSuccess) {
-      cudaGetLastError();
-      return BI_GEMM_ERR_OOM;
-    }
-    h->ws = ws;
-    h->ws_bytes = w.total;
-  }
-  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  if (const int rc = h->shared_ws.need(w.total, st)) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(h->shared_ws.at);
   biattn::SharedParams sp;
   std::memset(&sp, 0, sizeof(sp));
   biattn::Params& p = sp.a;
@@ -1670,7 +1664,8 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
   p.c = h->scale * 1.4426950408889634f;   // log2(e)
   p.nstage = h->nstage;
   p.stall_block = -1;
-  p.timeout_ns = biattn::kTimeoutNs;
+  p.timeout_ns = timeout_ns;
+  sp.stall = stall;
   sp.group_start = group_start;
   sp.group_len = group_len;
   sp.nsh = reinterpret_cast<int32_t*>(ws + w.nsh);
@@ -1724,6 +1719,17 @@ BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t
   return BI_GEMM_OK;
 }
 
+}  // namespace
+
+BI_GEMM_API int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
+                                        const int32_t* q_pos, const void* k_cache, const void* v_cache,
+                                        int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
+                                        int64_t max_pages, int64_t max_pos, const int32_t* group_start,
+                                        const int32_t* group_len, int64_t num_groups, void* o, void* stream) {
+  return attention_run_shared(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages,
+                              max_pos, group_start, group_len, num_groups, o, stream, -1, biattn::kTimeoutNs);
+}
+
 BI_GEMM_API int bi_attention_get_device_error(bi_attention_t h, void* stream) {
   if (!h) return BI_GEMM_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1760,6 +1766,7 @@ BI_GEMM_API int bi_attention_get_config(bi_attention_t h, bi_attention_config* c
 BI_GEMM_API int bi_attention_destroy(bi_attention_t h) {
   if (!h) return BI_GEMM_OK;
   if (h->ws) cudaFree(h->ws);
+  h->shared_ws.release();
   if (h->d_status) cudaFree(h->d_status);
   delete h;
   return BI_GEMM_OK;

@@ -48,6 +48,7 @@ struct SharedParams {
   int32_t* count;              // [1] records
   tc::Cache c;
   int64_t num_groups, cap;
+  int32_t stall;               // failure injection (test controls only): this block loads no keys
   int32_t cols;                // columns of a unit at most: 128, or 64 above splits of 512
 };
 
@@ -318,6 +319,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           const int32_t b = i < nblk ? (i + 1 < nblk ? i + 1 : 0) : i - nblk;
           const int32_t pos0 = base + b * tc::kBlockPos;
           const uint32_t s = seq % NS, dst = sbase + uint32_t(C::OFF_RING) + s * uint32_t(C::STAGE_BYTES);
+          if (int(blockIdx.x) == sp.stall) {
+            ok = __all_sync(0xFFFFFFFFu, tc::wait_bar(full(0), 0u, sy));   // (never)
+            break;
+          }
           if constexpr (kTma) {
             const int32_t box = tc::block_box(sp.c, trow, pos0, last, lane, &bad);
             if (seq >= uint32_t(NS)) {

@@ -15,10 +15,13 @@
 #include "bi_gemm.cu"
 #include "bi_rmsnorm.cu"
 #include "bi_attention.cu"
+#include "bi_prompt.cu"
+#include "bi_qkrope.cu"
 
 #include <cuda_bf16.h>
 
 #include "../../tests/include/bi_gemm_controls.h"
+#include "../../tests/include/bi_paged_controls.h"
 
 #define BI_CTL_API extern "C" __attribute__((visibility("default")))
 
@@ -193,3 +196,64 @@ BI_CTL_API int bi_ctl_attention_run_kernel(bi_attention_t h, const void* q, int6
   return attention_run(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages, max_pos, o,
                        stream, -1, biattn::kTimeoutNs, kernel);
 }
+
+// This library's own copies of the operators around the paged cache, and their failure injection.
+BI_CTL_API int bi_ctl_prompt_create(bi_prompt_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                                    int64_t page_size, float scale) {
+  return bi_prompt_create(out, num_q_heads, num_kv_heads, head_dim, page_size, scale);
+}
+
+BI_CTL_API int bi_ctl_prompt_run(bi_prompt_t h, const void* q, int64_t T, const int32_t* q_start,
+                                 const int32_t* q_pos0, int64_t num_seqs, const void* k_cache, const void* v_cache,
+                                 int64_t num_pages, const int32_t* page_table, int64_t max_pages, int64_t max_pos,
+                                 void* o, void* stream) {
+  return bi_prompt_run(h, q, T, q_start, q_pos0, num_seqs, k_cache, v_cache, num_pages, page_table, max_pages, max_pos,
+                       o, stream);
+}
+
+BI_CTL_API int bi_ctl_prompt_stall(bi_prompt_t h, const void* q, int64_t T, const int32_t* q_start,
+                                   const int32_t* q_pos0, int64_t num_seqs, const void* k_cache, const void* v_cache,
+                                   int64_t num_pages, const int32_t* page_table, int64_t max_pages, int64_t max_pos,
+                                   void* o, uint64_t timeout_ns, void* stream) {
+  if (timeout_ns == 0) return BI_GEMM_ERR_INVALID_ARG;
+  return prompt_run(h, q, T, q_start, q_pos0, num_seqs, k_cache, v_cache, num_pages, page_table, max_pages, max_pos, o,
+                    stream, 0, timeout_ns);
+}
+
+BI_CTL_API int bi_ctl_prompt_get_device_error(bi_prompt_t h, void* stream) {
+  return bi_prompt_get_device_error(h, stream);
+}
+
+BI_CTL_API int bi_ctl_prompt_destroy(bi_prompt_t h) { return bi_prompt_destroy(h); }
+
+BI_CTL_API int bi_ctl_attention_shared_stall(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
+                                             const int32_t* q_pos, const void* k_cache, const void* v_cache,
+                                             int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
+                                             int64_t max_pages, int64_t max_pos, const int32_t* group_start,
+                                             const int32_t* group_len, int64_t num_groups, void* o,
+                                             uint64_t timeout_ns, void* stream) {
+  if (timeout_ns == 0) return BI_GEMM_ERR_INVALID_ARG;
+  return attention_run_shared(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages,
+                              max_pos, group_start, group_len, num_groups, o, stream, 0, timeout_ns);
+}
+
+BI_CTL_API int bi_ctl_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                                    int64_t page_size, int64_t rot_dim, int32_t interleaved, float eps) {
+  return bi_qkrope_create(out, num_q_heads, num_kv_heads, head_dim, page_size, rot_dim, interleaved, eps);
+}
+
+BI_CTL_API int bi_ctl_qkrope_stall(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq,
+                                   const void* gk, const float* cos_sin, int64_t num_positions, const int32_t* q_seq,
+                                   const int32_t* q_pos, void* k_cache, void* v_cache, int64_t num_pages,
+                                   const int32_t* page_table, int64_t num_seqs, int64_t max_pages, void* q_out,
+                                   uint64_t timeout_ns, void* stream) {
+  if (timeout_ns == 0) return BI_GEMM_ERR_INVALID_ARG;
+  return qkrope_run(h, qkv, T, qkv_stride, gq, gk, cos_sin, num_positions, q_seq, q_pos, k_cache, v_cache, num_pages,
+                    page_table, num_seqs, max_pages, q_out, stream, 0, timeout_ns);
+}
+
+BI_CTL_API int bi_ctl_qkrope_get_device_error(bi_qkrope_t h, void* stream) {
+  return bi_qkrope_get_device_error(h, stream);
+}
+
+BI_CTL_API int bi_ctl_qkrope_destroy(bi_qkrope_t h) { return bi_qkrope_destroy(h); }

@@ -766,8 +766,7 @@ struct bi_prompt {
   int device = 0, num_sms = 0;
   biprompt::KernelInfo kern;
   uint32_t* d_status = nullptr;
-  void* ws = nullptr;
-  size_t ws_bytes = 0;
+  biattn_tc::Workspace ws;
 };
 
 namespace {
@@ -886,19 +885,8 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
                    biattn_tc::encode_pages(&tmv, v_cache, rows, h->Hkv, h->D, h->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const PromptWs w = prompt_layout(h, T, B);
-  if (w.total > h->ws_bytes) {
-    if (h->ws) cudaFreeAsync(h->ws, st);
-    h->ws = nullptr;
-    h->ws_bytes = 0;
-    void* ws = nullptr;
-    if (cudaMallocAsync(&ws, w.total, st) != cudaSuccess) {
-      cudaGetLastError();
-      return BI_GEMM_ERR_OOM;
-    }
-    h->ws = ws;
-    h->ws_bytes = w.total;
-  }
-  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  if (const int rc = h->ws.need(w.total, st)) return rc;
+  uint8_t* ws = static_cast<uint8_t*>(h->ws.at);
   biprompt::Params p;
   std::memset(&p, 0, sizeof(p));
   p.q_start = q_start;
@@ -993,7 +981,7 @@ BI_GEMM_API int bi_prompt_get_config(bi_prompt_t h, bi_prompt_config* c) {
 
 BI_GEMM_API int bi_prompt_destroy(bi_prompt_t h) {
   if (!h) return BI_GEMM_OK;
-  if (h->ws) cudaFree(h->ws);
+  h->ws.release();
   if (h->d_status) cudaFree(h->d_status);
   delete h;
   return BI_GEMM_OK;

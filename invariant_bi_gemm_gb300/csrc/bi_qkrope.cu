@@ -59,6 +59,8 @@ struct Params {
   int32_t groups_log2;      // lane groups per token
   int32_t ring;             // stages (tokens) of the ring, in the form for many tokens
   int32_t team_log2;        // and its warps per token
+  int32_t stall;            // failure injection (test controls only): this block of it loads nothing
+  uint64_t timeout_ns;      // limit of its waits
   float eps;
 };
 
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) qkrope_ring_kernel(const Par
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const biattn_tc::Sync sy{&gave_up, p.status, biattn_tc::kTimeoutNs};      // (every wait is bounded)
+  const biattn_tc::Sync sy{&gave_up, p.status, p.timeout_ns};      // (every wait is bounded)
   const int64_t step = gridDim.x;
   int s = 0;
   uint32_t ph = 0;                                      // stage and phase of the next token
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) qkrope_ring_kernel(const Par
         const int32_t at = __shfl_sync(0xFFFFFFFFu, pos, k);
         go = __all_sync(0xFFFFFFFFu, biattn_tc::wait_bar(empty + 8 * s, ph ^ 1u, sy));
         if (!go) break;
-        if (lane == 0) {
+        if (lane == 0 && int(blockIdx.x) != p.stall) {
           slots[s] = sl;
           const uint32_t dst = sbase + uint32_t(s) * stage_bytes;
           ptx::mbar_arrive_expect_tx(full + 8 * s, sl >= 0 ? stage_bytes : 0u);
@@ -442,11 +444,14 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
   return BI_GEMM_OK;
 }
 
-BI_GEMM_API int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq,
-                              const void* gk, const float* cos_sin, int64_t num_positions, const int32_t* q_seq,
-                              const int32_t* q_pos, void* k_cache, void* v_cache, int64_t num_pages,
-                              const int32_t* page_table, int64_t num_seqs, int64_t max_pages, void* q_out,
-                              void* stream) {
+namespace {
+
+// bi_qkrope_run with the failure injection of the test controls (stall >= 0: that block of the form for
+// many tokens loads nothing) and the limit of its waits.
+int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq, const void* gk,
+               const float* cos_sin, int64_t num_positions, const int32_t* q_seq, const int32_t* q_pos, void* k_cache,
+               void* v_cache, int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
+               void* q_out, void* stream, int32_t stall, uint64_t timeout_ns) {
   if (!h || T < 0 || num_positions < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || !gq != !gk)
     return BI_GEMM_ERR_INVALID_ARG;
   if (T == 0) return BI_GEMM_OK;
@@ -499,6 +504,8 @@ BI_GEMM_API int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t
   const bool ring = h->ring > 0 && T >= 4 * int64_t(h->ring_ctas);
   p.ring = h->ring;
   p.team_log2 = h->team_log2;
+  p.stall = stall;
+  p.timeout_ns = timeout_ns;
   cfg.gridDim = dim3(unsigned(ring ? h->ring_ctas : (T + h->per_block - 1) / h->per_block));
   cfg.blockDim = dim3(biqkr::kThreads + (ring ? 32 : 0));
   cfg.dynamicSmemBytes = ring ? h->ring_smem : 0;
@@ -514,6 +521,17 @@ BI_GEMM_API int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t
     return BI_GEMM_ERR_CUDA;
   }
   return BI_GEMM_OK;
+}
+
+}  // namespace
+
+BI_GEMM_API int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq,
+                              const void* gk, const float* cos_sin, int64_t num_positions, const int32_t* q_seq,
+                              const int32_t* q_pos, void* k_cache, void* v_cache, int64_t num_pages,
+                              const int32_t* page_table, int64_t num_seqs, int64_t max_pages, void* q_out,
+                              void* stream) {
+  return qkrope_run(h, qkv, T, qkv_stride, gq, gk, cos_sin, num_positions, q_seq, q_pos, k_cache, v_cache, num_pages,
+                    page_table, num_seqs, max_pages, q_out, stream, -1, biattn_tc::kTimeoutNs);
 }
 
 BI_GEMM_API int bi_qkrope_get_device_error(bi_qkrope_t h, void* stream) {

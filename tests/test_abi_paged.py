@@ -91,3 +91,13 @@ def test_shared_attention_null_arguments():
     assert L.bi_attention_run_shared(None, None, 1, None, None, None, None, 1, None, 1, 1, 0, None, None, 1, None,
                                      None) == INVALID
     assert L.bi_attention_shared_workspace_size(None, 1, 1, 1, ctypes.byref(b)) == INVALID
+
+
+def test_controls_symbols_exported():
+    declared = [n for n in _declared("bi_paged_controls.h") if n.startswith("bi_ctl_")]
+    assert len(declared) == 10
+    L = ctypes.CDLL(bgbuild.lib_path("libbi_gemm_controls.so"))
+    for name in declared:
+        assert hasattr(L, name), name
+    for name in bg.PROMPT_EXPORTED_SYMBOLS + bg.QKROPE_EXPORTED_SYMBOLS:
+        assert not hasattr(L, name), name

@@ -1,0 +1,252 @@
+"""The operators around the paged cache together on the GPU, as a serving loop uses them: a prompt's
+projection normalised, rotated and appended (BiQkRope), attended (BiPromptAttention), its cache forked
+for several samples and decoded behind the shared prefix (BiAttention.run_shared); caches past 32-bit
+offsets; handles on streams of their own at once; workspaces and graphs; and waits that run out."""
+import ctypes
+
+import pytest
+import torch
+
+import invariant_bi_gemm_gb300 as bg
+from gpu_util import Controls, stream_ptr
+from invariant_bi_gemm_gb300 import BiAttention, BiPromptAttention, BiQkRope
+from test_gpu_l_qkrope import make as make_rope
+from test_gpu_m_prompt import Pack
+from test_gpu_n_shared import Groups
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(x):
+    return x.view(torch.int16)
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def attention64(q, k, v, scale):
+    """q [n, H, D] at the last n positions of k, v [L, Hkv, D]: (value, sum of weights times |v|, largest score)."""
+    n, H, D = q.shape
+    L, G = k.shape[0], H // k.shape[1]
+    k, v = (x.double().repeat_interleave(G, 1) for x in (k, v))
+    s = torch.einsum("nhd,lhd->nhl", q.double(), k) * scale
+    seen = torch.arange(L, device=q.device)[None] <= torch.arange(L - n, L, device=q.device)[:, None]
+    s = s.masked_fill(~seen[:, None], -float("inf"))
+    w = torch.softmax(s, -1)
+    e = s.masked_fill(~seen[:, None], 0).abs().amax(-1, keepdim=True)
+    return torch.einsum("nhl,lhd->nhd", w, v), torch.einsum("nhl,lhd->nhd", w, v.abs()), e
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,n", [(32, 8, 128, 16, 1300), (16, 2, 64, 32, 700)])
+def test_prompt_then_forked_samples(Hq, Hkv, D, page, n):
+    """Each step against fp64 on the very caches it read (the bounds of the operators' own tests), for
+    a prompt in two chunks and three decode steps of four samples."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    samples, steps, width = 4, 3, (Hq + 2 * Hkv) * D
+    per = -(-(n + steps) // page)
+    pages = per + samples * 2 + 1
+    kc, vc = rn(pages, page, Hkv, D), rn(pages, page, Hkv, D)
+    rate = 10000.0 ** (-torch.arange(D // 2, device="cuda", dtype=torch.float64) / (D // 2))
+    ang = torch.arange(n + steps, device="cuda", dtype=torch.float64)[:, None] * rate
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    gq, gk = rn(D), rn(D)
+    rope, prompt, att = BiQkRope(Hq, Hkv, D, page), BiPromptAttention(Hq, Hkv, D, page), BiAttention(Hq, Hkv, D, page)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    mine = table[:per].view(1, per).contiguous()
+    flat = lambda c, row, length: c.view(-1, Hkv, D)[
+        row[torch.arange(length, device="cuda") // page].long() * page + torch.arange(length, device="cuda") % page]
+    u = 2.0**-24
+    done = 0
+    for m in (n - n // 3, n // 3):
+        q = rope.run(rn(m, width), gq, gk, cs, torch.zeros(m, dtype=torch.int32, device="cuda"),
+                     torch.arange(done, done + m, dtype=torch.int32, device="cuda"), kc, vc, mine)
+        o = prompt.run(q, i32(0, m), i32(done), kc, vc, mine, n - 1)
+        done += m
+        val, a, e = attention64(q, flat(kc, mine[0], done), flat(vc, mine[0], done), prompt.scale)
+        tol = 2.0**-8 * val.abs() + (2.0**-8 + 4 * (D + 8) * u * e + 2 * (done + 160) * u) * a
+        assert bool(((o.double() - val).abs() <= tol).all())
+    # the fork: whole pages in common, the last one copied
+    whole = n // page
+    tables = mine.repeat(samples, 1)
+    for b in range(samples):
+        own = table[per + 2 * b:per + 2 * b + per - whole]
+        if n % page:
+            kc[own[0].long()], vc[own[0].long()] = kc[mine[0, whole].long()], vc[mine[0, whole].long()]
+        tables[b, whole:] = own[:per - whole]
+    seqs = torch.arange(samples, dtype=torch.int32, device="cuda")
+    for t in range(steps):
+        pos = torch.full((samples,), n + t, dtype=torch.int32, device="cuda")
+        q = rope.run(rn(samples, width), gq, gk, cs, seqs, pos, kc, vc, tables)
+        args = (q, seqs, pos, kc, vc, tables, n + t)
+        o = att.run_shared(*args, i32(0, samples), i32(whole * page))
+        assert torch.equal(bits(o), bits(att.run(*args)))
+        for b in range(samples):
+            val, a, e = attention64(q[b:b + 1], flat(kc, tables[b], n + t + 1), flat(vc, tables[b], n + t + 1), att.scale)
+            tol = 2.0**-8 * val.abs() + (4 * (D + 8) * u * e + 2 * (n + t + 33) * u) * a
+            assert bool(((o[b:b + 1].double() - val).abs() <= tol).all())
+    for h in (rope, prompt, att):
+        assert h.device_error() == 0
+        h.close()
+
+
+@pytest.mark.parametrize("page", [16, 12])
+def test_caches_past_32_bit_offsets(page):
+    """Pages behind 2^32 bytes (and 2^31 elements) of a cache give the bits of the same pages near its
+    start, for both attentions, and take the appended keys and values."""
+    Hq, Hkv, D = 4, 4, 64
+    pages = ((1 << 32) // (Hkv * D * 2 * page)) + 400
+    kc = torch.empty(pages, page, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    n = 1400
+    per = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for c in (kc, vc):
+        c[:per] = torch.randn(per, page, Hkv, D, generator=g, device="cuda").to(torch.bfloat16)
+        c[pages - per:] = c[:per]
+    near = torch.arange(per, dtype=torch.int32, device="cuda").view(1, per)
+    far = near + (pages - per)
+    q = torch.randn(n, Hq, D, generator=g, device="cuda").to(torch.bfloat16)
+    prompt, att, rope = BiPromptAttention(Hq, Hkv, D, page), BiAttention(Hq, Hkv, D, page), BiQkRope(Hq, Hkv, D, page)
+    o = [prompt.run(q, i32(0, n), i32(0), kc, vc, t, n - 1) for t in (near, far)]
+    assert torch.equal(bits(o[0]), bits(o[1]))
+    two = [torch.cat([t, t]) for t in (near, far)]
+    pos, seq = i32(n - 1, n - 2), i32(0, 1)
+    s = [att.run_shared(q[:2].contiguous(), seq, pos, kc, vc, t, n - 1, i32(0, 2), i32(1024)) for t in two]
+    assert torch.equal(bits(s[0]), bits(s[1]))
+    assert torch.equal(bits(s[0]), bits(att.run(q[:2].contiguous(), seq, pos, kc, vc, two[0], n - 1)))
+    qkv = torch.randn(n, 3 * Hq * D, generator=g, device="cuda").to(torch.bfloat16)
+    cs = torch.rand(n, D, generator=g, device="cuda")
+    z, at = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    r = [rope.run(qkv, None, None, cs, z, at, kc, vc, t) for t in (near, far)]
+    assert torch.equal(bits(r[0]), bits(r[1]))
+    assert torch.equal(bits(kc[:per]), bits(kc[pages - per:])) and torch.equal(bits(vc[:per]), bits(vc[pages - per:]))
+    assert torch.equal(vc[:per].view(-1, Hkv, D)[:n], qkv.view(n, 3 * Hq, D)[:, 2 * Hq:])
+    for h in (prompt, att, rope):
+        assert h.device_error() == 0
+        h.close()
+
+
+def test_handles_on_streams_of_their_own_at_once():
+    """Two handles of each operator, each on a stream of its own, many calls in flight: the bits of calls one by one."""
+    pk = [Pack([(i, 300 + 40 * i, 90 * i)], 16, 4, 64, 16) for i in range(2)]
+    gr = [Groups([(1500, [1 + 7 * i for i in range(10 + 5 * k)])], 16, 4, 64, 16, seed=k) for k in range(2)]
+    ro = [make_rope(600 + 300 * k, 16, 4, 64, 16, 64, seed=k) for k in range(2)]
+    hs = [(BiPromptAttention(16, 4, 64, 16), BiAttention(16, 4, 64, 16), BiQkRope(16, 4, 64, 16)) for _ in range(2)]
+    pa, ga = [p.args() for p in pk], [x.args() + [x.start.cuda(), x.len.cuda()] for x in gr]
+    call = [lambda k: hs[k][0].run(*pa[k]), lambda k: hs[k][1].run_shared(*ga[k]), lambda k: hs[k][2].run(**ro[k])]
+    want = [[bits(f(k)).clone() for f in call] for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k] += [(j, call[j](k)) for j in range(3)]
+    torch.cuda.synchronize()
+    for k in range(2):
+        for j, o in got[k]:
+            assert torch.equal(bits(o), want[k][j])
+        for h in hs[k]:
+            assert h.device_error() == 0
+            h.close()
+
+
+def test_graphs_outlive_the_growth_of_their_workspace():
+    """A graph captured with a small workspace replays to the same bits after a larger eager call has
+    grown it; a capture that would have to grow it is refused and the handle goes on."""
+    small, large = Pack([(0, 60, 0)], 8, 2, 64, 16), Pack([(i, 200 + i, 0) for i in range(40)], 8, 2, 64, 16)
+    gs, gl = Groups([(600, [3, 4])], 8, 2, 64, 16), Groups([(3000, [1 + i for i in range(60)])], 8, 2, 64, 16)
+    prompt, att = BiPromptAttention(8, 2, 64, 16), BiAttention(8, 2, 64, 16)
+    runs = []
+    for h, x, y in ((prompt.run, small.args(), large.args()),
+                    (att.run_shared, gs.args() + [gs.start.cuda(), gs.len.cuda()],
+                     gl.args() + [gl.start.cuda(), gl.len.cuda()])):
+        want = bits(h(*x)).clone()
+        out = torch.zeros_like(x[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            h(*x, o=out)
+        refused = torch.cuda.CUDAGraph()
+        big = torch.zeros_like(y[0])
+        with torch.cuda.graph(refused):
+            with pytest.raises(bg.BiGemmError) as e:
+                h(*y, o=big)
+        assert e.value.code == bg.BI_GEMM_ERR_SCRATCH_LIMIT
+        runs.append((h, x, y, want, out, graph))
+    for h, x, y, want, out, graph in runs:
+        big = bits(h(*y)).clone()
+        junk = [torch.full((1 << 22,), 0x7F7F7F7F, dtype=torch.int32, device="cuda") for _ in range(8)]
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), want)
+        assert torch.equal(bits(h(*y)), big)
+        del junk
+    assert prompt.device_error() == 0 and att.device_error() == 0
+    prompt.close()
+    att.close()
+
+
+def test_waits_that_run_out_are_reported_and_the_handles_survive():
+    """Failure injection (test controls): block 0 of each kernel loads nothing, its waits end after
+    50 ms, the call reports BI_GEMM_ERR_TIMEOUT, and the next ordinary call gives the golden bits."""
+    L, P, V = Controls().L, ctypes.c_void_p, ctypes.c_void_p
+    I64, U64 = ctypes.c_int64, ctypes.c_uint64
+    ptr = lambda t: V(t.data_ptr())
+    # prompt
+    pk = Pack([(i, 200, 100) for i in range(3)], 8, 2, 128, 16)
+    product = BiPromptAttention(8, 2, 128, 16)
+    golden = bits(pk.run(product))
+    q, qs, q0, kc, vc, table, mp = pk.args()
+    o = torch.zeros_like(q)
+    h = P()
+    L.bi_ctl_prompt_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, ctypes.c_float]
+    L.bi_ctl_prompt_run.argtypes = [P, P, I64, P, P, I64, P, P, I64, P, I64, I64, P, P]
+    L.bi_ctl_prompt_stall.argtypes = [P, P, I64, P, P, I64, P, P, I64, P, I64, I64, P, U64, P]
+    L.bi_ctl_prompt_get_device_error.argtypes = L.bi_ctl_qkrope_get_device_error.argtypes = [P, P]
+    L.bi_ctl_prompt_destroy.argtypes = L.bi_ctl_qkrope_destroy.argtypes = [P]
+    assert L.bi_ctl_prompt_create(ctypes.byref(h), 8, 2, 128, 16, product.scale) == 0
+    args = (ptr(q), q.shape[0], ptr(qs), ptr(q0), 3, ptr(kc), ptr(vc), kc.shape[0], ptr(table), table.shape[1], mp, ptr(o))
+    assert L.bi_ctl_prompt_stall(h, *args, 50_000_000, stream_ptr()) == 0
+    assert L.bi_ctl_prompt_get_device_error(h, stream_ptr()) == bg.BI_GEMM_ERR_TIMEOUT
+    assert L.bi_ctl_prompt_run(h, *args, stream_ptr()) == 0
+    assert L.bi_ctl_prompt_get_device_error(h, stream_ptr()) == 0
+    assert torch.equal(bits(o), golden)
+    assert L.bi_ctl_prompt_destroy(h) == 0
+    product.close()
+    # the groups of a shared prefix
+    gr = Groups([(1200, [3, 9, 70])], 8, 2, 128, 16)
+    a, gs, gl = gr.args(), gr.start.cuda(), gr.len.cuda()
+    h = P()
+    assert L.bi_ctl_attention_create(ctypes.byref(h), 8, 2, 128, 16, ctypes.c_float(128**-0.5), 0) == 0
+    L.bi_ctl_attention_shared_stall.argtypes = [P, P, I64, P, P, P, P, I64, P, I64, I64, I64, P, P, I64, P, U64, P]
+    o = torch.zeros_like(a[0])
+    args = (ptr(a[0]), 3, ptr(a[1]), ptr(a[2]), ptr(a[3]), ptr(a[4]), a[3].shape[0], ptr(a[5]), 3, a[5].shape[1], a[6])
+    assert L.bi_ctl_attention_shared_stall(h, *args, ptr(gs), ptr(gl), 1, ptr(o), 50_000_000, stream_ptr()) == 0
+    assert L.bi_ctl_attention_get_device_error(h, stream_ptr()) == bg.BI_GEMM_ERR_TIMEOUT
+    assert L.bi_ctl_attention_run(h, *args, ptr(o), stream_ptr()) == 0
+    assert L.bi_ctl_attention_get_device_error(h, stream_ptr()) == 0
+    plain = BiAttention(8, 2, 128, 16)
+    assert torch.equal(bits(o), bits(plain.run_shared(*a, gs, gl)))
+    L.bi_ctl_attention_destroy(h)
+    # the form for many tokens of the append
+    rope = BiQkRope(2, 1, 64, 16)
+    T = 4 * rope.config["ring_ctas"]
+    r = make_rope(T, 2, 1, 64, 16, 64, far=2500)
+    h = P()
+    L.bi_ctl_qkrope_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, I64, ctypes.c_int32, ctypes.c_float]
+    L.bi_ctl_qkrope_stall.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, P, P, I64, P, I64, I64, P, U64, P]
+    assert L.bi_ctl_qkrope_create(ctypes.byref(h), 2, 1, 64, 16, 64, 0, 1e-6) == 0
+    q = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert L.bi_ctl_qkrope_stall(h, ptr(r["qkv"]), T, 4 * 64, ptr(r["gq"]), ptr(r["gk"]), ptr(r["cos_sin"]), 2500,
+                                 ptr(r["q_seq"]), ptr(r["q_pos"]), ptr(r["k_cache"]), ptr(r["v_cache"]),
+                                 r["k_cache"].shape[0], ptr(r["page_table"]), 3, r["page_table"].shape[1], ptr(q),
+                                 50_000_000, stream_ptr()) == 0
+    assert L.bi_ctl_qkrope_get_device_error(h, stream_ptr()) == bg.BI_GEMM_ERR_TIMEOUT
+    assert L.bi_ctl_qkrope_get_device_error(h, stream_ptr()) == 0
+    assert L.bi_ctl_qkrope_destroy(h) == 0
+    assert rope.run(**r).shape == (T, 2, 64) and rope.device_error() == 0
+    rope.close()
+    plain.close()
