@@ -110,9 +110,9 @@ int bi_attention_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, ui
  *
  * group_start int32 [num_groups + 1], ascending, and group_len int32 [num_groups]: DEVICE pointers,
  * 4-byte aligned.  Caught by the kernels, as BI_GEMM_ERR_INVALID_ARG from
- * bi_attention_get_device_error with the group's outputs undefined: a group_start that descends or
- * leaves [0, T], a negative group_len, page tables that differ within a shared split.  num_groups
- * >= 0; all else as bi_attention_run, but for the workspace: run_shared has its own, grown by
+ * bi_attention_get_device_error: a group_start that descends or leaves [0, T] or a negative
+ * group_len (nothing is shared then, the outputs are bi_attention_run's), and page tables that
+ * differ within a shared split (the group's outputs are then undefined).  num_groups >= 0; all else as bi_attention_run, but for the workspace: run_shared has its own, grown by
  * cudaMalloc (BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph that needs more than
  * an earlier call of its size left; a graph stays valid when later calls grow it).  Queues four
  * kernels: a plan, the tokens' own units, the groups' units beside them, the merge. */

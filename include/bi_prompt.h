@@ -37,7 +37,8 @@
  *   - Inputs the host cannot see (a q_start that descends or leaves [0, T], a negative q_pos0, a
  *     last position above max_pos or past max_pages pages, a page outside [0, num_pages)) are
  *     caught by the kernels: the sequence's output is then undefined (it is not computed, or a bad
- *     page's rows count as zeros) and bi_prompt_get_device_error reports BI_GEMM_ERR_INVALID_ARG.
+ *     page's rows count as zeros; of a q_start that descends nothing is computed) and
+ *     bi_prompt_get_device_error reports BI_GEMM_ERR_INVALID_ARG.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).  A handle is
  *     not thread-safe and must not be used on two streams at once; captured calls of one handle
  *     share its workspace, so their graphs must not run at the same time.
@@ -77,8 +78,9 @@ int bi_prompt_create(bi_prompt_t* out, int64_t num_q_heads, int64_t num_kv_heads
  * The run grows the handle's workspace (cudaMalloc) when T or num_seqs outgrow it (BI_GEMM_ERR_OOM
  * if that fails; BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph, which uses what
  * an earlier call of its size left; a graph stays valid when later calls grow the workspace), then
- * queues two kernels: a plan of the units (longest first) and the attention.  Asynchronous.  The kernel's waits are bounded (2 s): past the limit the block
- * stops, its output is undefined and bi_prompt_get_device_error reports BI_GEMM_ERR_TIMEOUT. */
+ * queues two kernels: a plan of the units (longest first) and the attention.  Asynchronous.  The
+ * kernel's waits are bounded (2 s): past the limit the block stops, its output is undefined and
+ * bi_prompt_get_device_error reports BI_GEMM_ERR_TIMEOUT. */
 int bi_prompt_run(bi_prompt_t h, const void* q, int64_t T, const int32_t* q_start, const int32_t* q_pos0,
                   int64_t num_seqs, const void* k_cache, const void* v_cache, int64_t num_pages,
                   const int32_t* page_table, int64_t max_pages, int64_t max_pos, void* o, void* stream);

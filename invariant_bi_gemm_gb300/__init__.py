@@ -1,15 +1,17 @@
-"""Python binding of the batch-invariant GEMM library (libbi_gemm.so, C ABI in include/bi_gemm.h
-and include/bi_rmsnorm.h).
+"""Python binding of the batch-invariant operators (libbi_gemm.so, C ABI in include/bi_gemm.h,
+bi_rmsnorm.h, bi_prenorm.h, bi_qkrope.h, bi_prompt.h and bi_attention.h).
 
-Argument marshalling only: every step of y = x·W (and of the RMSNorm) runs in the CUDA kernels of
+Argument marshalling only: every step of y = x·W (and of the other operators) runs in the CUDA kernels of
 ``csrc/``.  PyTorch supplies device memory and streams.  There is no CPU or
 PyTorch fallback: importing this module fails if the library has not been built
 (``python -m invariant_bi_gemm_gb300.build``), and every call that the library
 refuses raises ``BiGemmError``.
 
 Low-level functions carry the C names (``bi_gemm_create``, ``bi_gemm_run``, ...,
-``bi_rmsnorm_run``) and take raw device pointers; ``BiGemm`` and ``BiRmsNorm`` wrap them
-for torch tensors.
+``bi_rmsnorm_run``) and take raw device pointers; ``BiGemm``, ``BiRmsNorm``, ``BiPreNorm`` and,
+around one paged KV cache, ``BiQkRope`` (norm, rotation, append), ``BiPromptAttention`` and
+``BiAttention`` (single tokens; ``run_shared`` for tokens behind a common prefix) wrap them for
+torch tensors.
 """
 from __future__ import annotations
 
@@ -596,6 +598,7 @@ class BiAttention:
         self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
         self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
         self.handle = bi_attention_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale, split_size)
+        self._device = _device_of_handle()
 
     @property
     def config(self) -> dict:
@@ -644,7 +647,7 @@ class BiAttention:
         for positions 0 .. group_len[g] - 1 (int32 [groups]).  The prefix is read once per group;
         the result has the bits of run()."""
         import torch
-        T, index, o = _check_queries(q, o, self.Hq, self.D)
+        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, (self.page_size, self.Hkv, self.D), index)
         groups, i32 = group_len.shape[0], torch.int32
         _check_tensor("q_seq", q_seq, i32, (T,), index)
@@ -708,12 +711,19 @@ def _check_cache(k_cache, v_cache, page_table, page_shape, index: int):
     return shape[0], table[0], table[1]
 
 
-def _check_queries(q, o, Hq: int, D: int):
-    """q [T, Hq, D] bf16 and o like it (made where it is None).  Returns (T, device index, o)."""
+def _device_of_handle() -> int:
+    """The device a handle made now belongs to."""
+    import torch
+    return torch.cuda.current_device()
+
+
+def _check_queries(q, o, Hq: int, D: int, device: int):
+    """q [T, Hq, D] bf16 and o like it (made where it is None) on the handle's device.  Returns (T,
+    device index, o)."""
     import torch
     shape, index = q.shape, q.get_device()
-    if len(shape) != 3 or shape[1] != Hq or shape[2] != D or index < 0:
-        raise ValueError("q must be a CUDA tensor [T, num_q_heads, head_dim]")
+    if len(shape) != 3 or shape[1] != Hq or shape[2] != D or index != device:
+        raise ValueError(f"q must be a tensor [T, num_q_heads, head_dim] on cuda:{device}")
     _check_tensor("q", q, torch.bfloat16, shape, index)
     if o is None:
         o = torch.empty_like(q)
@@ -738,6 +748,7 @@ class BiQkRope:
         self.rot_dim = int(rot_dim) if rot_dim is not None else self.D
         self._width, self._page_shape = (self.Hq + 2 * self.Hkv) * self.D, (self.page_size, self.Hkv, self.D)
         self.handle = bi_qkrope_create(self.Hq, self.Hkv, self.D, self.page_size, self.rot_dim, interleaved, eps)
+        self._device = _device_of_handle()
 
     @property
     def config(self) -> dict:
@@ -746,8 +757,9 @@ class BiQkRope:
     def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
         import torch
         bf16, shape, index, width = torch.bfloat16, qkv.shape, qkv.get_device(), self._width
-        if len(shape) != 2 or shape[1] != width or qkv.dtype is not bf16 or index < 0:
-            raise ValueError("qkv must be a bf16 CUDA tensor [T, (num_q_heads + 2 num_kv_heads) head_dim]")
+        if len(shape) != 2 or shape[1] != width or qkv.dtype is not bf16 or index != self._device:
+            raise ValueError(f"qkv must be a bf16 tensor [T, (num_q_heads + 2 num_kv_heads) head_dim] on "
+                             f"cuda:{self._device}")
         T, stride = shape[0], width
         if not qkv.is_contiguous():
             stride, inner = qkv.stride()
@@ -815,6 +827,7 @@ class BiPromptAttention:
         self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
         self._page_shape = (self.page_size, self.Hkv, self.D)
         self.handle = bi_prompt_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale)
+        self._device = _device_of_handle()
 
     @property
     def config(self) -> dict:
@@ -822,7 +835,7 @@ class BiPromptAttention:
 
     def run(self, q, q_start, q_pos0, k_cache, v_cache, page_table, max_pos: int, o=None, stream=None):
         import torch
-        T, index, o = _check_queries(q, o, self.Hq, self.D)
+        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         _check_tensor("q_start", q_start, torch.int32, (seqs + 1,), index)
         _check_tensor("q_pos0", q_pos0, torch.int32, (seqs,), index)

@@ -1679,7 +1679,6 @@ int attention_run_shared(bi_attention* h, const void* q, int64_t T, const int32_
   sp.c.Hkv = h->Hkv;
   sp.c.page_size = h->page_size;
   sp.num_groups = num_groups;
-  sp.cap = w.cap;
   sp.cols = w.cols;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -47,45 +47,61 @@ struct SharedParams {
   int4* srec;                  // [cap] (first token, tokens, split, token whose pages are read)
   int32_t* count;              // [1] records
   tc::Cache c;
-  int64_t num_groups, cap;
+  int64_t num_groups;
   int32_t stall;               // failure injection (test controls only): this block loads no keys
   int32_t cols;                // columns of a unit at most: 128, or 64 above splits of 512
 };
 
-constexpr int kPlanTokens = 1024;
+constexpr int kPlanTokens = 1024;             // tokens (and groups) that the plan keeps in shared memory
 
 // One block: per token the splits that its group computes, the units of the groups, then the
-// records of all other units in the form that the attention kernels read.
+// records of all other units in the form that the attention kernels read.  Bound by latency: what the
+// first 1024 tokens and groups say is loaded at once, the rest works from shared memory, and a warp
+// writes one token's records at a time.  (With groups read when they were met and a token's records
+// written by the warp that scanned it, a call of 64 tokens behind a prefix of 8192 took 65.8 us, now 60.9.)
 __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp) {
   __shared__ int32_t warp_sums[32];
   __shared__ int32_t carry;
   __shared__ int32_t nrec;
-  __shared__ int32_t spos[kPlanTokens], snsh[kPlanTokens];   // the first tokens' positions (-1: bad), shares
+  __shared__ int32_t gs[kPlanTokens + 1], gl[kPlanTokens];   // the first groups
+  // of 1024 tokens: request, position (-1: cannot be served), shared splits, first own unit, own units
+  __shared__ int32_t sb[kPlanTokens], spos[kPlanTokens], snsh[kPlanTokens], sat[kPlanTokens], sn[kPlanTokens];
   const Params& p = sp.a;
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   if (tid == 0) carry = 0, nrec = 0;
-  // a token's position, -1 where it cannot be served
-  auto position = [&](int64_t t) {
-    const int32_t b = p.q_seq[t], pos = p.q_pos[t];
-    return b >= 0 && b < p.B && pos >= 0 && pos <= p.max_pos && int64_t(pos / p.page_size) < p.max_pages ? pos : -1;
+  auto served = [&](int32_t b, int32_t pos) {
+    return b >= 0 && b < p.B && pos >= 0 && pos <= p.max_pos && int64_t(pos / p.page_size) < p.max_pages;
   };
-  // the thread's token of the first 1024: read once, ahead of everything that depends on the groups
+  auto position = [&](int64_t t) {
+    const int32_t pos = p.q_pos[t];
+    return served(p.q_seq[t], pos) ? pos : -1;
+  };
   const int32_t b0 = tid < p.T ? p.q_seq[tid] : -1, p0 = tid < p.T ? p.q_pos[tid] : -1;
-  spos[tid] = b0 >= 0 && b0 < p.B && p0 >= 0 && p0 <= p.max_pos && int64_t(p0 / p.page_size) < p.max_pages ? p0 : -1;
+  // Ranges that leave [0, T] or descend may overlap: then nothing is shared, and every token is served
+  // by units of its own.
+  bool bad = false;
+  for (int64_t g = tid; g < sp.num_groups; g += 1024) {
+    const int32_t s = sp.group_start[g], e = sp.group_start[g + 1], len = sp.group_len[g];
+    bad |= s < 0 || e < s || e > p.T || len < 0;
+    if (g < kPlanTokens) {
+      gs[g] = s, gl[g] = len;
+      if (g + 1 == sp.num_groups || g + 1 == kPlanTokens) gs[g + 1] = e;
+    }
+  }
+  spos[tid] = served(b0, p0) ? p0 : -1;
   snsh[tid] = 0;
   for (int64_t t = tid; t < p.T; t += 1024) sp.nsh[t] = 0;
-  __syncthreads();
+  bad = __syncthreads_or(bad) != 0;
+  if (bad && tid == 0) atomicOr(p.status, kErrInput);
   const int32_t G = p.Hq / p.Hkv, per = sp.cols / G;     // tokens of a unit
   // a warp per group, or 32 / groups warps that share out its rows of units where there are few
   const int wpg = sp.num_groups < 32 ? 32 / int(sp.num_groups) : 1, wi = warp % wpg;
-  for (int64_t g = warp / wpg; g < sp.num_groups; g += 32 / wpg) {
-    const int32_t s = sp.group_start[g], e = sp.group_start[g + 1], len = sp.group_len[g];
-    if (s < 0 || e < s || e > p.T || len < 0) {
-      if (lane == 0) atomicOr(p.status, kErrInput);
-      continue;
-    }
+  for (int64_t g = warp / wpg; g < sp.num_groups && !bad; g += 32 / wpg) {
+    const bool near = g < kPlanTokens;
+    const int32_t s = near ? gs[g] : sp.group_start[g], e = near ? gs[g + 1] : sp.group_start[g + 1];
+    const int32_t len = near ? gl[g] : sp.group_len[g];
     if (e - s < 2) continue;                             // (alone: its own units serve it as well)
     for (int32_t t0 = s + wi * per; t0 < e; t0 += wpg * per) {
       const int32_t n = min(per, e - t0);
@@ -99,37 +115,35 @@ __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp
         most = max(most, x);
         if (k == 0) first = x;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+      most = int32_t(__reduce_max_sync(0xFFFFFFFFu, unsigned(most)));
       first = __shfl_sync(0xFFFFFFFFu, first, 0);        // the first token's, which mostly shares all
       __syncwarp();
       int32_t at = 0;
-      if (lane == 0) at = atomicAdd(&nrec, most);
+      if (lane == 0 && most > 0) at = atomicAdd(&nrec, most);
       at = __shfl_sync(0xFFFFFFFFu, at, 0);
       for (int32_t sx = lane; sx < most; sx += 32) {
         int32_t src = t0;
         if (first <= sx)
           while (sp.nsh[src] <= sx) ++src;               // (ends: a token has `most`)
-        if (at + sx < sp.cap) sp.srec[at + sx] = make_int4(t0, n, sx, src);
-        else atomicOr(p.status, kErrInput);              // (only from a group_start that descends)
+        sp.srec[at + sx] = make_int4(t0, n, sx, src);
       }
     }
   }
   __syncthreads();
-  if (tid == 0) sp.count[0] = int32_t(min(int64_t(nrec), sp.cap));
+  if (tid == 0) sp.count[0] = nrec;                      // (at most sp.cap: the groups are disjoint)
   for (int64_t base = 0; base < p.T; base += 1024) {
     const int64_t t = base + tid;
-    int32_t n = 0, b = 0, pos = 0, sh = 0;
+    int32_t n = 0;
     if (t < p.T) {
-      b = base == 0 ? b0 : p.q_seq[t];
-      pos = base == 0 ? p0 : p.q_pos[t];
+      const int32_t b = base == 0 ? b0 : p.q_seq[t], pos = base == 0 ? p0 : p.q_pos[t];
       if (b < 0 || b >= p.B || pos < 0 || int64_t(pos / p.page_size) >= p.max_pages) {
         atomicOr(p.status, kErrInput);
       } else if (pos > p.max_pos) {
         atomicOr(p.status, kErrBound);
       } else {
-        sh = base == 0 ? snsh[tid] : sp.nsh[t];
+        const int32_t sh = base == 0 ? snsh[tid] : sp.nsh[t];
         n = (splits_of(pos, p.split) - sh) * p.Hkv;
+        sb[tid] = b, spos[tid] = pos, snsh[tid] = sh;
       }
     }
     int32_t x = n;
@@ -152,15 +166,14 @@ __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp
     __syncthreads();
     const int32_t incl = carry + x + (warp > 0 ? warp_sums[warp - 1] : 0);
     if (t < p.T) p.cum[t] = incl - n;
-    for (int k = 0; k < 32; ++k) {
-      const int32_t nk = __shfl_sync(0xFFFFFFFFu, n, k), sk = __shfl_sync(0xFFFFFFFFu, incl - n, k);
-      const int32_t bk = __shfl_sync(0xFFFFFFFFu, b, k), pk = __shfl_sync(0xFFFFFFFFu, pos, k);
-      const int32_t hk = __shfl_sync(0xFFFFFFFFu, sh, k);
-      const int32_t tk = int32_t(base + warp * 32 + k);
-      for (int32_t r = lane; r < nk; r += 32) p.urec[sk + r] = make_int4(tk, bk, pk, hk * p.Hkv + r);
-    }
+    sat[tid] = incl - n, sn[tid] = n;
     __syncthreads();
     if (tid == 1023) carry = incl;
+    const int here = int(min(int64_t(1024), p.T - base));
+    for (int k = warp; k < here; k += 32) {
+      const int32_t nk = sn[k], at = sat[k], r0 = snsh[k] * p.Hkv;
+      for (int32_t r = lane; r < nk; r += 32) p.urec[at + r] = make_int4(int32_t(base) + k, sb[k], spos[k], r0 + r);
+    }
     __syncthreads();
   }
   if (tid == 0) p.cum[p.T] = carry;

@@ -56,12 +56,11 @@ struct Params {
   const int32_t* q_start;
   const int32_t* q_pos0;
   uint16_t* o;
-  int32_t* cum;             // [B + 1] tiles of the sequences before b
   int2* rec;                // [tiles] (sequence, tile of its request), longest first
   uint32_t* counter;        // [2]: tiles planned, units taken
   uint32_t* status;
   Cache c;
-  int64_t T, B, cap_tiles;
+  int64_t T, B;
   int32_t max_pos, Hq;
   int32_t stall;            // failure injection (test controls only): this block loads nothing
   uint64_t timeout_ns;
@@ -132,13 +131,17 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) 
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins; i += 1024) bins[i] = 0;
   __syncthreads();
+  bool descends = false;
   auto bin_of = [&](int32_t tile) { return kBins - 1 - min(kBins - 1, int32_t(int64_t(tile) * up / kBlockPos)); };
   for (int64_t b = tid; b < p.B; b += 1024) {
     int32_t first;
     const int32_t n = tiles_of(p, b, up, &first);
     if (n > 0) atomicAdd(&bins[bin_of(first + n - 1)], n);
+    descends |= p.q_start[b + 1] < p.q_start[b];         // (reported by tiles_of)
   }
-  __syncthreads();
+  // Sequences of an ascending q_start are disjoint and have at most cap_tiles tiles; of one that descends
+  // nothing is computed.
+  descends = __syncthreads_or(descends) != 0;
   int32_t total;
   {                                           // exclusive scan of the bins, two per thread
     const int32_t a0 = bins[2 * tid], a1 = bins[2 * tid + 1];
@@ -166,22 +169,16 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) 
     total = warp_sums[31];
     __syncthreads();
   }
-  // Ascending q_start gives at most cap_tiles; a table that descends and climbs again may claim more.
-  if (total < 0 || total > p.cap_tiles) {
-    if (tid == 0) atomicOr(p.status, kErrInput);
-    total = int32_t(p.cap_tiles);
-  }
-  for (int64_t b = warp; b < p.B; b += 32) {
+  for (int64_t b = warp; b < p.B && !descends; b += 32) {
     int32_t first, at = 0;
     const int32_t n = tiles_of(p, b, up, &first);
     if (n == 0) continue;
     if (lane == 0) at = atomicAdd(&bins[bin_of(first + n - 1)], n);
     at = __shfl_sync(0xFFFFFFFFu, at, 0);
-    for (int32_t k = lane; k < n; k += 32)
-      if (at + k >= 0 && at + k < p.cap_tiles) p.rec[at + k] = make_int2(int32_t(b), first + n - 1 - k);
+    for (int32_t k = lane; k < n; k += 32) p.rec[at + k] = make_int2(int32_t(b), first + n - 1 - k);
   }
   if (tid == 0) {
-    p.counter[0] = uint32_t(total);
+    p.counter[0] = descends ? 0u : uint32_t(total);
     p.counter[1] = 0u;
   }
 }
@@ -343,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             u.nb[i] = t1 >= u.first && t0 <= u.last ? t0 / kBlockPos + 1 : 0;
           }
           if (lane == 0) id = atomicAdd(p.counter + 1, 1u);       // the next one, ahead of its use
-          if (u.nb[0] == 0 && u.nb[1] == 0) continue;             // (only from a q_start that descends)
         }
         const uint32_t us = nun % kUnitSlots;
         if (nun >= kUnitSlots) {
@@ -772,7 +768,7 @@ struct bi_prompt {
 namespace {
 
 struct PromptWs {
-  size_t counter, cum, rec, total;
+  size_t counter, rec, total;
   int64_t cap_tiles;
 };
 
@@ -780,8 +776,7 @@ PromptWs prompt_layout(const bi_prompt* h, int64_t T, int64_t B) {
   PromptWs w;
   w.cap_tiles = T / h->kern.up + 2 * B;     // a sequence of n tokens touches at most n / up + 2 units
   w.counter = 0;
-  w.cum = 256;
-  w.rec = w.cum + biprompt::align256(size_t(B + 1) * sizeof(int32_t));
+  w.rec = 256;
   w.total = w.rec + biprompt::align256(size_t(w.cap_tiles) * sizeof(int2));
   return w;
 }
@@ -893,7 +888,6 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
   p.q_pos0 = q_pos0;
   p.o = static_cast<uint16_t*>(o);
   p.counter = reinterpret_cast<uint32_t*>(ws + w.counter);
-  p.cum = reinterpret_cast<int32_t*>(ws + w.cum);
   p.rec = reinterpret_cast<int2*>(ws + w.rec);
   p.status = h->d_status;
   p.c.kc = static_cast<const uint16_t*>(k_cache);
@@ -905,7 +899,6 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
   p.c.page_size = h->page_size;
   p.T = T;
   p.B = B;
-  p.cap_tiles = w.cap_tiles;
   p.max_pos = int32_t(max_pos);
   p.Hq = h->Hq;
   p.stall = stall;

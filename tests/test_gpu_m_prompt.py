@@ -245,6 +245,8 @@ def test_bad_inputs_are_reported(what):
         assert torch.equal(bits(o)[:70], good[:70]) and torch.equal(bits(o)[160:], good[160:])
     if what == "past the end":
         assert torch.equal(bits(o)[:160], good[:160]) and bool((o[160:] == 0).all())
+    if what == "descending":                   # sequences that overlap: none is computed
+        assert bool((o == 0).all())
     assert torch.equal(bits(pk.run(h)), good)
     h.close()
 

@@ -195,8 +195,37 @@ def test_bad_groups_are_reported(what):
     assert h.device_error() == bg.BI_GEMM_ERR_INVALID_ARG and h.device_error() == 0
     if what in ("past the end", "negative length", "page"):
         assert torch.equal(bits(o)[:3], good[:3])
+    if what in ("descending", "past the end", "negative length"):      # nothing is shared
+        assert torch.equal(bits(o), good)
     gr.start, gr.len, gr.table, gr.q_pos = start, length, table, pos
     assert torch.equal(gr.both(h)[1], good)
+    h.close()
+
+
+def test_overlapping_groups():
+    """Groups that climb, fall back and climb again claim the same tokens twice: reported, and every
+    token is served by units of its own."""
+    gr = Groups([(1100, [3, 40, 5]), (1500, [1, 2, 7, 9])], 8, 2, 64, 16)
+    h = BiAttention(8, 2, 64, 16)
+    good = gr.both(h)[0]
+    for starts, lens in (([0, 3, 0, 7, 3, 7], [1100, 5, 0, 5, 1500]), ([3, 7, 0, 3], [1500, 0, 1100]),
+                         ([0, 7, 6, 7], [1100, 0, 700]), ([0] + [7, 0] * 40, [600] * 80)):
+        start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        o = h.run_shared(*gr.args(), start, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        assert h.device_error() == bg.BI_GEMM_ERR_INVALID_ARG and h.device_error() == 0
+        assert torch.equal(bits(o), good)
+    h.close()
+
+
+@pytest.mark.parametrize("groups", [1, 5, 31, 33, 1023, 1024, 1025, 1500])
+def test_many_groups(groups):
+    """Group tables and batches on both sides of what the plan keeps in shared memory, some groups empty."""
+    rng = np.random.default_rng(groups)
+    gr = Groups([(260, [int(rng.integers(1, 200)) for _ in range(int(rng.integers(1, 4)))]) for _ in range(groups)],
+                4, 2, 64, 16)
+    h = BiAttention(4, 2, 64, 16, split_size=128)
+    got = gr.both(h)
+    assert torch.equal(got[0], got[1]) and h.device_error() == 0
     h.close()
 
 

@@ -250,3 +250,18 @@ def test_waits_that_run_out_are_reported_and_the_handles_survive():
     assert rope.run(**r).shape == (T, 2, 64) and rope.device_error() == 0
     rope.close()
     plain.close()
+
+
+def test_tensors_of_another_device_are_refused():
+    """Pointers of another GPU never reach a kernel of the handle's."""
+    rope, prompt, att = BiQkRope(8, 2, 64, 16), BiPromptAttention(8, 2, 64, 16), BiAttention(8, 2, 64, 16)
+    for op in (rope, prompt, att):
+        op._device += 1                        # (as if it had been made there)
+    gr, pk, x = Groups([(600, [3, 4])], 8, 2, 64, 16), Pack([(0, 7, 0)], 8, 2, 64, 16), torch.zeros
+    with pytest.raises(ValueError):
+        att.run_shared(*gr.args(), gr.start.cuda(), gr.len.cuda())
+    with pytest.raises(ValueError):
+        prompt.run(*pk.args())
+    with pytest.raises(ValueError):
+        rope.run(x(1, 768, dtype=torch.bfloat16, device="cuda"), None, None, x(1, 64, device="cuda"), i32(0), i32(0),
+                 *[t.cuda() for t in (pk.kc, pk.vc, pk.table)])
