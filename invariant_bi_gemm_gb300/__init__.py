@@ -598,7 +598,7 @@ class BiAttention:
         self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
         self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
         self.handle = bi_attention_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale, split_size)
-        self._device = _device_of_handle()
+        self._device = _handle_device()
 
     @property
     def config(self) -> dict:
@@ -646,10 +646,9 @@ class BiAttention:
         group_start[g + 1] - 1 (int32 [groups + 1], ascending), whose requests name the same pages
         for positions 0 .. group_len[g] - 1 (int32 [groups]).  The prefix is read once per group;
         the result has the bits of run()."""
-        import torch
         T, index, o = _check_queries(q, o, self.Hq, self.D, self._device)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, (self.page_size, self.Hkv, self.D), index)
-        groups, i32 = group_len.shape[0], torch.int32
+        groups, i32 = group_len.shape[0], _torch.i32
         _check_tensor("q_seq", q_seq, i32, (T,), index)
         _check_tensor("q_pos", q_pos, i32, (T,), index)
         _check_tensor("group_len", group_len, i32, (groups,), index)
@@ -679,17 +678,38 @@ class BiAttention:
             pass
 
 
+class _Torch:
+    """What the calls around the paged cache need of torch, looked up once (the module itself does not
+    import it): these calls are on the path of a single token's step."""
+
+    def __init__(self):
+        import torch
+        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.empty_like, self.current_stream = torch.empty_like, torch._C._cuda_getCurrentRawStream
+        self.current_device = torch.cuda.current_device
+
+
+_torch = None
+
+
+def _handle_device() -> int:
+    """The device a handle made now belongs to."""
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch.current_device()
+
+
 def _stream_of(stream, index: int) -> int:
     """The cudaStream_t of a stream argument; the device's current stream for None."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _torch.current_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check_tensor(name: str, t, dtype, shape, index: int) -> None:
-    """t: a contiguous tensor of this dtype and shape on CUDA device `index`.  (These checks are on
-    the path of a single token's step: plain attributes, no objects built unless something is wrong.)"""
+    """t: a contiguous tensor of this dtype and shape on CUDA device `index`.  (Plain attributes, no
+    objects built unless something is wrong.)"""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
@@ -698,37 +718,29 @@ def _check_tensor(name: str, t, dtype, shape, index: int) -> None:
 def _check_cache(k_cache, v_cache, page_table, page_shape, index: int):
     """The paged cache of one layer: k_cache, v_cache [pages, page_size, Hkv, D] bf16, page_table
     [num_seqs, max_pages] int32.  Returns (pages, num_seqs, max_pages)."""
-    import torch
     shape = k_cache.shape
     if len(shape) != 4 or shape[1:] != page_shape:
         raise ValueError(f"k_cache must be [pages, page_size, num_kv_heads, head_dim] = [pages, {page_shape}]")
-    _check_tensor("k_cache", k_cache, torch.bfloat16, shape, index)
-    _check_tensor("v_cache", v_cache, torch.bfloat16, shape, index)
+    _check_tensor("k_cache", k_cache, _torch.bf16, shape, index)
+    _check_tensor("v_cache", v_cache, _torch.bf16, shape, index)
     table = page_table.shape
     if len(table) != 2:
         raise ValueError("page_table must be [num_seqs, max_pages]")
-    _check_tensor("page_table", page_table, torch.int32, table, index)
+    _check_tensor("page_table", page_table, _torch.i32, table, index)
     return shape[0], table[0], table[1]
-
-
-def _device_of_handle() -> int:
-    """The device a handle made now belongs to."""
-    import torch
-    return torch.cuda.current_device()
 
 
 def _check_queries(q, o, Hq: int, D: int, device: int):
     """q [T, Hq, D] bf16 and o like it (made where it is None) on the handle's device.  Returns (T,
     device index, o)."""
-    import torch
     shape, index = q.shape, q.get_device()
     if len(shape) != 3 or shape[1] != Hq or shape[2] != D or index != device:
         raise ValueError(f"q must be a tensor [T, num_q_heads, head_dim] on cuda:{device}")
-    _check_tensor("q", q, torch.bfloat16, shape, index)
+    _check_tensor("q", q, _torch.bf16, shape, index)
     if o is None:
-        o = torch.empty_like(q)
+        o = _torch.empty_like(q)
     else:
-        _check_tensor("o", o, torch.bfloat16, shape, index)
+        _check_tensor("o", o, _torch.bf16, shape, index)
     return shape[0], index, o
 
 
@@ -748,15 +760,15 @@ class BiQkRope:
         self.rot_dim = int(rot_dim) if rot_dim is not None else self.D
         self._width, self._page_shape = (self.Hq + 2 * self.Hkv) * self.D, (self.page_size, self.Hkv, self.D)
         self.handle = bi_qkrope_create(self.Hq, self.Hkv, self.D, self.page_size, self.rot_dim, interleaved, eps)
-        self._device = _device_of_handle()
+        self._device = _handle_device()
 
     @property
     def config(self) -> dict:
         return bi_qkrope_get_config(self.handle)
 
     def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
-        import torch
-        bf16, shape, index, width = torch.bfloat16, qkv.shape, qkv.get_device(), self._width
+        bf16, i32 = _torch.bf16, _torch.i32
+        shape, index, width = qkv.shape, qkv.get_device(), self._width
         if len(shape) != 2 or shape[1] != width or qkv.dtype is not bf16 or index != self._device:
             raise ValueError(f"qkv must be a bf16 tensor [T, (num_q_heads + 2 num_kv_heads) head_dim] on "
                              f"cuda:{self._device}")
@@ -776,12 +788,12 @@ class BiQkRope:
         angles = cos_sin.shape
         if len(angles) != 2 or angles[1] != self.rot_dim:
             raise ValueError("cos_sin must be [positions, rot_dim]")
-        _check_tensor("cos_sin", cos_sin, torch.float32, angles, index)
-        _check_tensor("q_seq", q_seq, torch.int32, (T,), index)
-        _check_tensor("q_pos", q_pos, torch.int32, (T,), index)
+        _check_tensor("cos_sin", cos_sin, _torch.f32, angles, index)
+        _check_tensor("q_seq", q_seq, i32, (T,), index)
+        _check_tensor("q_pos", q_pos, i32, (T,), index)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         if q_out is None:
-            q_out = torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device)
+            q_out = qkv.new_empty(T, self.Hq, self.D)
         else:
             _check_tensor("q_out", q_out, bf16, (T, self.Hq, self.D), index)
         _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), angles[0],
@@ -827,18 +839,17 @@ class BiPromptAttention:
         self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
         self._page_shape = (self.page_size, self.Hkv, self.D)
         self.handle = bi_prompt_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale)
-        self._device = _device_of_handle()
+        self._device = _handle_device()
 
     @property
     def config(self) -> dict:
         return bi_prompt_get_config(self.handle)
 
     def run(self, q, q_start, q_pos0, k_cache, v_cache, page_table, max_pos: int, o=None, stream=None):
-        import torch
         T, index, o = _check_queries(q, o, self.Hq, self.D, self._device)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
-        _check_tensor("q_start", q_start, torch.int32, (seqs + 1,), index)
-        _check_tensor("q_pos0", q_pos0, torch.int32, (seqs,), index)
+        _check_tensor("q_start", q_start, _torch.i32, (seqs + 1,), index)
+        _check_tensor("q_pos0", q_pos0, _torch.i32, (seqs,), index)
         _check(library().bi_prompt_run(self.handle, q.data_ptr(), T, q_start.data_ptr(), q_pos0.data_ptr(), seqs,
                                        k_cache.data_ptr(), v_cache.data_ptr(), pages, page_table.data_ptr(), per,
                                        max_pos, o.data_ptr(), _stream_of(stream, index)), "bi_prompt_run")

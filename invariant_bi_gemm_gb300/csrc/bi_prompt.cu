@@ -62,7 +62,7 @@ struct Params {
   Cache c;
   int64_t T, B;
   int32_t max_pos, Hq;
-  int32_t stall;            // failure injection (test controls only): this block loads nothing
+  int32_t stall;            // failure injection (test controls only): nothing is loaded for this sequence
   uint64_t timeout_ns;
   float scale_log2;
 };
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(empty(s), (n / NS - 1) & 1u, sy));
         if (!ok) return false;
       }
-      if (int(blockIdx.x) == p.stall) return true;
+      if (u.b == p.stall) return true;
       if constexpr (kTma) {
         load_block_tma<D>(dst, full(s), values ? &tmv : &tmk, p.c, box, u.kh, lane);
       } else {
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && j == 0) {                                     // the queries behind the first key block
             if (nun > 0) ok = __all_sync(0xFFFFFFFFu, wait_bar(q_empty, (nun - 1) & 1u, sy));
             if (!ok) break;
-            if (lane == 0 && int(blockIdx.x) != p.stall) {
+            if (lane == 0 && u.b != p.stall) {
               ptx::mbar_arrive_expect_tx(q_full, uint32_t((u.nb[0] > 0) + (u.nb[1] > 0)) * C::TILE_BYTES);
               for (int t = 0; t < 2; ++t)
                 if (u.nb[t] > 0)
@@ -841,7 +841,7 @@ BI_GEMM_API int bi_prompt_workspace_size(bi_prompt_t h, int64_t T, int64_t num_s
 
 namespace {
 
-// bi_prompt_run with the failure injection of the test controls (stall: that block loads no keys) and
+// bi_prompt_run with the failure injection of the test controls (stall >= 0: nothing is loaded for that sequence) and
 // the limit of the waits.
 int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, const int32_t* q_pos0, int64_t B,
                const void* k_cache, const void* v_cache, int64_t num_pages, const int32_t* page_table,

@@ -2,7 +2,8 @@
  * bi_paged_controls.h — TEST-ONLY entry points of libbi_gemm_controls.so for the operators around the
  * paged cache: this library's own copies (a handle made here is used only here) and failure
  * injection.  Each *_stall is the product's run (same arguments and codes) with block 0 of the
- * kernel never issuing its loads and the waits limited to timeout_ns (> 0): the block's waits
+ * kernel (of the prompts' kernel, whose blocks take their units as they come: every block with a
+ * unit of sequence 0) never issuing its loads and the waits limited to timeout_ns (> 0): the block's waits
  * expire, it stops, and *_get_device_error then reads BI_GEMM_ERR_TIMEOUT; outputs are undefined
  * and the handle stays usable.  No GPU fault is raised.
  */
