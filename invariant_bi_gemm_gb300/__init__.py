@@ -685,7 +685,8 @@ class _Torch:
     def __init__(self):
         import torch
         self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
-        self.empty_like, self.current_stream = torch.empty_like, torch._C._cuda_getCurrentRawStream
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.current_stream = torch._C._cuda_getCurrentRawStream
         self.current_device = torch.cuda.current_device
 
 
@@ -793,7 +794,7 @@ class BiQkRope:
         _check_tensor("q_pos", q_pos, i32, (T,), index)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         if q_out is None:
-            q_out = qkv.new_empty(T, self.Hq, self.D)
+            q_out = _torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device)
         else:
             _check_tensor("q_out", q_out, bf16, (T, self.Hq, self.D), index)
         _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), angles[0],
