@@ -1407,11 +1407,12 @@ namespace {
 // bi_attention_run with the failure injection of the test controls (stall_block >= 0: that
 // block of the TMA kernel never issues its first load), the limit of the ring waits, and the
 // kernel choice (0: automatic; 1: the TMA page-box kernel where the handle has it; 2: the
-// row-copy kernel), which the test controls use to run both kernels on the same calls.
+// row-copy kernel), which the test controls use to run both kernels on the same calls.  `own`: the
+// workspace of a run_shared that shares nothing.
 int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_seq, const int32_t* q_pos,
                   const void* k_cache, const void* v_cache, int64_t num_pages, const int32_t* page_table,
                   int64_t num_seqs, int64_t max_pages, int64_t max_pos, void* o, void* stream, int32_t stall_block,
-                  uint64_t timeout_ns, int32_t kernel_choice = 0) {
+                  uint64_t timeout_ns, int32_t kernel_choice = 0, biattn_tc::Workspace* own = nullptr) {
   if (!h || T < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || max_pos < 0) return BI_GEMM_ERR_INVALID_ARG;
   if (T == 0) return BI_GEMM_OK;
   if (T > (int64_t(1) << 24) || max_pos >= (int64_t(1) << 30) ||
@@ -1432,7 +1433,9 @@ int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_se
   if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WsLayout w = layout_of(h, T, max_pos);
-  if (w.total > h->ws_bytes) {
+  if (own) {
+    if (const int rc = own->need(w.total, st)) return rc;
+  } else if (w.total > h->ws_bytes) {
     if (h->ws) cudaFreeAsync(h->ws, st);
     h->ws = nullptr;
     h->ws_bytes = 0;
@@ -1444,7 +1447,7 @@ int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_se
     h->ws = p;
     h->ws_bytes = w.total;
   }
-  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  uint8_t* ws = static_cast<uint8_t*>(own ? own->at : h->ws);
   biattn::Params p;
   std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const uint16_t*>(q);
@@ -1593,23 +1596,29 @@ int attention_run_shared(bi_attention* h, const void* q, int64_t T, const int32_
                          uint64_t timeout_ns) {
   if (!h || T < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || max_pos < 0 || num_groups < 0)
     return BI_GEMM_ERR_INVALID_ARG;
-  // without a group, or a bound that leaves no whole split before a token's own, nothing is shared
-  if (T == 0 || num_groups == 0 || max_pos < h->split)
-    return bi_attention_run(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages,
-                            max_pos, o, stream);
   if (T > (int64_t(1) << 24) || max_pos >= (int64_t(1) << 30) || num_groups > (int64_t(1) << 24) ||
       T * h->Hkv * (max_pos / h->split + 1) >= (int64_t(1) << 31))   // unit indices are int32
     return BI_GEMM_ERR_UNSUPPORTED;
+  if (T > 0 && num_groups > 0 && (!group_start || !group_len)) return BI_GEMM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(group_len)) & 3u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  // Nothing is shared without a group, or under a bound that leaves no whole split before a token's own,
+  // or where all units run in one round of the decode's resident blocks: two launches then take less time
+  // than four, however much is shared (32/8 heads of 128: 4 tokens behind 1500 positions, 128 units, 17.6 us
+  // against 22.9 shared; 8 behind 3500, 512 units, 24.5 against 23.7; 8 behind 8192, 1088 units, two rounds,
+  // 50.4 against 30.0).
+  const int64_t one_round = h->tma4 ? h->tma4_ctas : h->tma ? h->tma_ctas : h->max_ctas;
+  if (T == 0 || num_groups == 0 || max_pos < h->split || T * h->Hkv * (max_pos / h->split + 1) <= one_round)
+    return attention_run(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages, max_pos,
+                         o, stream, -1, timeout_ns, 0, &h->shared_ws);
   const SharedWs w = shared_layout(h, T, max_pos, num_groups);
   if (w.cap * h->Hkv >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
-  if (!q || !q_seq || !q_pos || !k_cache || !v_cache || !page_table || !o || !group_start || !group_len)
-    return BI_GEMM_ERR_INVALID_ARG;
+  if (!q || !q_seq || !q_pos || !k_cache || !v_cache || !page_table || !o) return BI_GEMM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(o) | reinterpret_cast<uintptr_t>(k_cache) |
        reinterpret_cast<uintptr_t>(v_cache)) & 15u)
     return BI_GEMM_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(q_seq) | reinterpret_cast<uintptr_t>(q_pos) |
-       reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(group_start) |
-       reinterpret_cast<uintptr_t>(group_len)) & 3u)
+       reinterpret_cast<uintptr_t>(page_table)) & 3u)
     return BI_GEMM_ERR_ALIGNMENT;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {

@@ -16,8 +16,8 @@
 //
 // Bound: for many tokens the tensor cores (6 D operations per query row and key, a third of them for
 // the weights' low part) and the softmax's instructions, for few the load of the prefix.  Measured at
-// 32/8 heads of 128: 64 tokens behind 8192 positions 61 us for the whole call (bi_attention_run 214), of
-// which the groups' units alone 32; 256 tokens behind 16384 348 us, units alone 177.
+// 32/8 heads of 128: 64 tokens behind 8192 positions 61 us for the whole call (bi_attention_run 308), of
+// which the groups' units alone 32; 256 tokens behind 16384 348 us (2319), units alone 177.
 //
 // Warps (640 threads, one block per SM): 0 loads (queries, then K1 .. K(n-1), K0, V0 .. V(n-1)
 // through a ring), 1 issues the MMAs, 2 and 3 check that the group's page tables agree, 4 - 19

@@ -62,7 +62,8 @@ class Groups:
         self.q_pos = torch.tensor([p for _, p in tokens], dtype=torch.int32)
         self.q = rn(len(tokens), Hq, D)
         self.start, self.len = torch.tensor(start, dtype=torch.int32), torch.tensor(share, dtype=torch.int32)
-        self.max_pos = int(self.q_pos.max())
+        # (a bound that is loose enough for a call of few tokens to share as well)
+        self.max_pos = max(int(self.q_pos.max()), 1024 * (1024 // (len(tokens) * Hkv) + 1))
 
     def args(self):
         return [x.cuda() for x in (self.q, self.q_seq, self.q_pos, self.kc, self.vc, self.table)] + [self.max_pos]
@@ -199,6 +200,24 @@ def test_bad_groups_are_reported(what):
         assert torch.equal(bits(o), good)
     gr.start, gr.len, gr.table, gr.q_pos = start, length, table, pos
     assert torch.equal(gr.both(h)[1], good)
+    h.close()
+
+
+@pytest.mark.parametrize("page", [16, 12])
+def test_both_sides_of_the_rule(page):
+    """Calls whose units all run at once are not shared, the next larger ones are: the same bits, and a
+    bad table of groups is only looked at where it is used."""
+    gr = Groups([(1100, [3, 40, 5, 9])], 8, 2, 64, page)
+    h = BiAttention(8, 2, 64, page)
+    want = gr.both(h)[0]
+    a, good, bad = gr.args()[:-1], gr.start.cuda(), (gr.start + 1).cuda()
+    seen = []
+    for bound in (1200, 512 * 56, 512 * 75, 512 * 76, 512 * 110, 512 * 400):
+        assert torch.equal(bits(h.run_shared(*a, bound, good, gr.len.cuda())), want)
+        assert h.device_error() == 0
+        assert torch.equal(bits(h.run_shared(*a, bound, bad, gr.len.cuda())), want)
+        seen.append(h.device_error())
+    assert seen[0] == 0 and seen[-1] == bg.BI_GEMM_ERR_INVALID_ARG and sorted(seen, reverse=True) == seen
     h.close()
 
 

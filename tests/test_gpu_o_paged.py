@@ -80,7 +80,9 @@ def test_prompt_then_forked_samples(Hq, Hkv, D, page, n):
         pos = torch.full((samples,), n + t, dtype=torch.int32, device="cuda")
         q = rope.run(rn(samples, width), gq, gk, cs, seqs, pos, kc, vc, tables)
         args = (q, seqs, pos, kc, vc, tables, n + t)
-        o = att.run_shared(*args, i32(0, samples), i32(whole * page))
+        # (as it is, and under a bound so loose that the few samples share)
+        o = att.run_shared(*args[:-1], 1 << 17, i32(0, samples), i32(whole * page))
+        assert torch.equal(bits(o), bits(att.run_shared(*args, i32(0, samples), i32(whole * page))))
         assert torch.equal(bits(o), bits(att.run(*args)))
         for b in range(samples):
             val, a, e = attention64(q[b:b + 1], flat(kc, tables[b], n + t + 1), flat(vc, tables[b], n + t + 1), att.scale)
@@ -113,7 +115,8 @@ def test_caches_past_32_bit_offsets(page):
     assert torch.equal(bits(o[0]), bits(o[1]))
     two = [torch.cat([t, t]) for t in (near, far)]
     pos, seq = i32(n - 1, n - 2), i32(0, 1)
-    s = [att.run_shared(q[:2].contiguous(), seq, pos, kc, vc, t, n - 1, i32(0, 2), i32(1024)) for t in two]
+    # (the bound is loose, so that two tokens share)
+    s = [att.run_shared(q[:2].contiguous(), seq, pos, kc, vc, t, 1 << 17, i32(0, 2), i32(1024)) for t in two]
     assert torch.equal(bits(s[0]), bits(s[1]))
     assert torch.equal(bits(s[0]), bits(att.run(q[:2].contiguous(), seq, pos, kc, vc, two[0], n - 1)))
     qkv = torch.randn(n, 3 * Hq * D, generator=g, device="cuda").to(torch.bfloat16)
