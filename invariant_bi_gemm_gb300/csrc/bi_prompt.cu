@@ -16,7 +16,8 @@
 // the tensor cores work for the other.  Tiles and blocks are cut at multiples of their size in the
 // request's own positions, so a row's arithmetic never depends on the chunk it came in.
 //
-// Warps (384 threads, one block per SM, persistent; units, longest first, from a counter):
+// Warps (384 threads, one block per SM; a unit each, or, where there are more, persistent blocks that take
+// planned units, longest first, from a counter):
 //   0       takes units, loads the tiles' queries (TMA box: 64 dims x G heads x positions) and the
 //           key blocks, page by page, into the ring (K0, V0, K1, V1, ...)
 //   1       issues the MMAs:  S = Q K^T (both operands in shared memory), O += P V (P in TMEM)
@@ -58,7 +59,7 @@ struct Params {
   const int32_t* q_pos0;
   uint16_t* o;
   int2* rec;                // [tiles] (sequence, tile of its request), longest first
-  uint32_t* counter;        // [2]: tiles planned, units taken
+  uint32_t* counter;        // [2]: tiles planned, units taken; NULL: no plan, a block per unit
   uint32_t* status;
   Cache c;
   int64_t T, B;
@@ -182,6 +183,37 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p, int32_t up) 
     p.counter[0] = descends ? 0u : uint32_t(total);
     p.counter[1] = 0u;
   }
+}
+
+// The record of tile `rank` without a plan (the whole warp): sequences in their order, a sequence's tiles
+// from its last; sequence -1 past the last tile, or where q_start descends.
+__device__ __forceinline__ int2 find_tile(const Params& p, int32_t up, int32_t rank, int lane) {
+  int2 r = make_int2(-1, 0);
+  int32_t before = 0;
+  bool descends = false;
+  for (int64_t b0 = 0; b0 < p.B; b0 += 32) {
+    const int64_t b = b0 + lane;
+    int32_t n = 0, first = 0;
+    if (b < p.B) {
+      n = tiles_of(p, b, up, &first);
+      descends |= p.q_start[b + 1] < p.q_start[b];
+    }
+    int32_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int32_t at = rank - (before + x - n);          // among the tiles of the lane's sequence
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at >= 0 && at < n);
+    if (hit) {
+      const int src = __ffs(int(hit)) - 1;
+      r.x = int32_t(b0) + src;
+      r.y = __shfl_sync(0xFFFFFFFFu, first + n - 1 - at, src);
+    }
+    before += __shfl_sync(0xFFFFFFFFu, x, 31);
+  }
+  return __any_sync(0xFFFFFFFFu, descends) ? make_int2(-1, 0) : r;
 }
 
 // ------------------------------------------------------------------ attention
@@ -315,11 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp == 0) {
       // ------------------------------------------------------------ units, queries, keys
-      const int32_t total = int32_t(p.counter[0]);
+      const bool planned = p.counter != nullptr;
+      const int2 only = planned ? make_int2(-1, 0) : find_tile(p, C::UP, int32_t(blockIdx.x) / p.c.Hkv, lane);
+      const int32_t total = planned ? int32_t(p.counter[0]) : only.x >= 0 ? int32_t(gridDim.x) : 0;
       bool ok = true;
       uint32_t seq = 0, nun = 0;               // ring loads and units so far
-      uint32_t id = 0;
-      if (lane == 0) id = atomicAdd(p.counter + 1, 1u);
+      uint32_t id = blockIdx.x;
+      if (planned && lane == 0) id = atomicAdd(p.counter + 1, 1u);
       while (ok) {
         id = __shfl_sync(0xFFFFFFFFu, id, 0);
         Unit u;
@@ -327,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         u.row0 = u.base = u.first = u.last = u.kh = u.nb[0] = u.nb[1] = 0;
         const int64_t rank = int64_t(id) / p.c.Hkv;
         if (rank < total) {
-          const int2 r = p.rec[rank];
+          const int2 r = planned ? p.rec[rank] : only;
           u.b = r.x;
           u.kh = int32_t(int64_t(id) - rank * p.c.Hkv);
           const int32_t s = p.q_start[r.x];
@@ -340,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t t0 = u.base + i * C::P, t1 = t0 + C::P - 1;
             u.nb[i] = t1 >= u.first && t0 <= u.last ? t0 / kBlockPos + 1 : 0;
           }
-          if (lane == 0) id = atomicAdd(p.counter + 1, 1u);       // the next one, ahead of its use
+          if (lane == 0) id = planned ? atomicAdd(p.counter + 1, 1u) : 0xFFFFFFFFu;   // the next one, ahead of its use
         }
         const uint32_t us = nun % kUnitSlots;
         if (nun >= kUnitSlots) {
@@ -771,14 +805,20 @@ namespace {
 struct PromptWs {
   size_t counter, rec, total;
   int64_t cap_tiles;
+  bool planned;
 };
 
 PromptWs prompt_layout(const bi_prompt* h, int64_t T, int64_t B) {
   PromptWs w;
   w.cap_tiles = T / h->kern.up + 2 * B;     // a sequence of n tokens touches at most n / up + 2 units
+  // Where every unit has a block of its own at once, each block finds its unit itself, and the plan's
+  // launch and workspace are spared (37 tokens, 32/8 heads of 128: 9.3 us, 11.6 with a plan; 3 chunks of
+  // 200 to 700 behind 28000, 16/2 heads of 64: 243 against 247).  With more units than blocks the plan's
+  // order pays: the longest units start first and blocks take the next as they end.
+  w.planned = w.cap_tiles * h->Hkv > h->num_sms;
   w.counter = 0;
   w.rec = 256;
-  w.total = w.rec + biprompt::align256(size_t(w.cap_tiles) * sizeof(int2));
+  w.total = w.planned ? w.rec + biprompt::align256(size_t(w.cap_tiles) * sizeof(int2)) : 0;
   return w;
 }
 
@@ -888,8 +928,8 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
   p.q_start = q_start;
   p.q_pos0 = q_pos0;
   p.o = static_cast<uint16_t*>(o);
-  p.counter = reinterpret_cast<uint32_t*>(ws + w.counter);
-  p.rec = reinterpret_cast<int2*>(ws + w.rec);
+  p.counter = w.planned ? reinterpret_cast<uint32_t*>(ws + w.counter) : nullptr;
+  p.rec = w.planned ? reinterpret_cast<int2*>(ws + w.rec) : nullptr;
   p.status = h->d_status;
   p.c.kc = static_cast<const uint16_t*>(k_cache);
   p.c.vc = static_cast<const uint16_t*>(v_cache);
@@ -917,7 +957,8 @@ int prompt_run(bi_prompt* h, const void* q, int64_t T, const int32_t* q_start, c
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(1024);
   void* pargs[2] = {&p, &up};
-  cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&biprompt::plan_kernel), pargs);
+  cudaError_t e = cudaSuccess;
+  if (w.planned) e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&biprompt::plan_kernel), pargs);
   if (e == cudaSuccess) {
     void* args[5] = {&tmq, &tmk, &tmv, &tmo, &p};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(w.cap_tiles * h->Hkv, h->num_sms)));

@@ -251,6 +251,29 @@ def test_bad_inputs_are_reported(what):
     h.close()
 
 
+@pytest.mark.parametrize("num_seqs", [1, 3, 31, 33, 70])
+def test_empty_sequences_around_and_the_plan(num_seqs):
+    """A sequence keeps its bits among empty ones, in calls so small that no plan is made and in calls
+    with one, wherever it stands."""
+    rows = [(i, 0, 0) for i in range(num_seqs)]
+    for at in {0, num_seqs // 2, num_seqs - 1}:
+        for others in (0, 40):
+            seqs = list(rows)
+            seqs[at] = (at, 75, 30)
+            pk = Pack(seqs + [(num_seqs + i, 90, 11 * i) for i in range(others)], 8, 1, 64, 16)
+            one = Pack([(at, 75, 30)], 8, 1, 64, 16)
+            h = BiPromptAttention(8, 1, 64, 16)
+            q, qs, q0, kc, vc, table, mp = pk.args()
+            got = bits(h.run(q, qs, q0, kc, vc, table, mp))
+            lo, hi = int(pk.q_start[at]), int(pk.q_start[at + 1])
+            alone = h.run(q[lo:hi].contiguous(), torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda"),
+                          q0[at:at + 1].contiguous(), kc, vc, table[at:at + 1].contiguous(), mp)
+            assert h.device_error() == 0
+            assert torch.equal(got[lo:hi], bits(alone)) and hi - lo == 75
+            one.check(one.run(h), h.scale)
+            h.close()
+
+
 def test_refusals():
     pk = Pack([(0, 7, 0), (1, 9, 4)], 8, 2, 64, 16)
     h = BiPromptAttention(8, 2, 64, 16)

@@ -161,9 +161,11 @@ def test_graphs_outlive_the_growth_of_their_workspace():
     grown it; a capture that would have to grow it is refused and the handle goes on."""
     small, large = Pack([(0, 60, 0)], 8, 2, 64, 16), Pack([(i, 200 + i, 0) for i in range(40)], 8, 2, 64, 16)
     gs, gl = Groups([(600, [3, 4])], 8, 2, 64, 16), Groups([(3000, [1 + i for i in range(60)])], 8, 2, 64, 16)
-    prompt, att = BiPromptAttention(8, 2, 64, 16), BiAttention(8, 2, 64, 16)
+    middle = Pack([(i, 100, 7 * i) for i in range(24)], 8, 2, 64, 16)
+    prompt, second, att = BiPromptAttention(8, 2, 64, 16), BiPromptAttention(8, 2, 64, 16), BiAttention(8, 2, 64, 16)
+    assert prompt.workspace_size(60, 1) == 0 < prompt.workspace_size(2400, 24) < prompt.workspace_size(8780, 40)
     runs = []
-    for h, x, y in ((prompt.run, small.args(), large.args()),
+    for h, x, y in ((prompt.run, small.args(), large.args()), (second.run, middle.args(), large.args()),
                     (att.run_shared, gs.args() + [gs.start.cuda(), gs.len.cuda()],
                      gl.args() + [gl.start.cuda(), gl.len.cuda()])):
         want = bits(h(*x)).clone()
@@ -187,9 +189,9 @@ def test_graphs_outlive_the_growth_of_their_workspace():
         assert torch.equal(bits(out), want)
         assert torch.equal(bits(h(*y)), big)
         del junk
-    assert prompt.device_error() == 0 and att.device_error() == 0
-    prompt.close()
-    att.close()
+    for h in (prompt, second, att):
+        assert h.device_error() == 0
+        h.close()
 
 
 def test_waits_that_run_out_are_reported_and_the_handles_survive():
