@@ -95,7 +95,8 @@ class bi_attention_config(ctypes.Structure):
 
 class bi_qkrope_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "page_size", "rot_dim",
-                                              "interleaved", "threads", "tokens_per_block", "ring_tokens", "ring_ctas")]
+                                              "interleaved", "threads", "tokens_per_block", "ring_tokens", "ring_ctas",
+                                              "ring_from")]
 
 
 class bi_prompt_config(ctypes.Structure):

@@ -4,7 +4,7 @@
 //
 // Bound: HBM bandwidth (every element read once, written once) beside the instructions, about eight
 // operations an element; one launch's latency for a few tokens.  Measured at 32/8 heads of 128: 1 token
-// 2.8 us, 64 tokens 2.9, 8192 tokens 43 (206 MB: 4.8 TB/s, 0.71 of a plain copy's rate).  A head of D elements belongs to D / 8
+// 2.8 us, 64 tokens 2.9, 8192 tokens 42 (206 MB: 4.9 TB/s, 0.73 of a plain copy's rate).  A head of D elements belongs to D / 8
 // lanes, eight elements each: two runs of four that are rotation partners (dimensions 4 j and
 // 4 j + rot / 2 on), or eight neighbours for an interleaved handle, so that a rotation needs no other
 // lane and its arithmetic goes two values an instruction.  A token has a power of two of such lane
@@ -39,7 +39,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;                // heads a lane group holds at a time
 constexpr int kMaxRing = 16;             // stages of the ring
-constexpr int kRingBytes = 72 * 1024;    // shared memory of a block's ring at most: three blocks per SM
+constexpr int kRingBytes = 54 * 1024;    // shared memory of a block's ring at most: four blocks per SM
+constexpr int kRingRows = 40 * 1024;     // bytes of rows that a block of it has to have
 constexpr uint32_t kErrInput = 1u;       // q_seq, q_pos or the page table's extent
 constexpr uint32_t kErrPage = 2u;        // page outside [0, num_pages)
 
@@ -252,9 +253,10 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
 // The form for many tokens: persistent blocks; a warp ahead of the others looks up 32 tokens' slots at a
 // time and copies their rows and angles into a ring (cp.async.bulk), so that several rows per block are
 // on their way whatever the lookups take.  (A block per token is up for 4 us, a third of it with loads
-// in flight: 55 us for 8192 tokens of 32/8 heads of 128.)
+// in flight: 52 us for 8192 tokens of 32/8 heads of 128, now 42.  With a larger ring and three blocks per SM
+// it took 43.5, with five, and registers spilled, 47.)
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads + 32, 3) qkrope_ring_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads + 32, 4) qkrope_ring_kernel(const Params p) {
   constexpr int LANES = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxRing];
@@ -361,7 +363,8 @@ struct bi_qkrope {
   float eps = 0.0f;
   int device = 0, groups_log2 = 0, per_block = 0;
   int ring = 0, ring_ctas = 0;      // stages and resident blocks of the form for many tokens (0: none),
-  int team_log2 = 0;                // and its warps per token
+  int team_log2 = 0;                // its warps per token
+  int ring_from = 0;                // and the tokens from which it runs
   size_t ring_smem = 0;
   uint32_t* d_status = nullptr;
 };
@@ -419,6 +422,8 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
       return BI_GEMM_ERR_CUDA;
     }
     h->ring_ctas = per_sm * sms;
+    const int64_t row = int64_t(heads) * h->D * 2;
+    h->ring_from = int((int64_t(biqkr::kRingRows) * h->ring_ctas + row - 1) / row);
   }
   if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
@@ -486,9 +491,11 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   p.eps = h->eps;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  // The ring from four tokens per resident block on: 32/8 heads of 128, 912 tokens 6.6 us against 6.3
-  // with a block per token, 8192 tokens 41.5 against 55.5.
-  const bool ring = h->ring > 0 && T >= 4 * int64_t(h->ring_ctas);
+  // The ring from 40 KB of rows per resident block on, where its start is paid for (us, ring against a
+  // block per token or few): 32/8 heads of 128 (12 KB a token), 1216 tokens 9.8 against 9.4, 2432 16.5
+  // against 17.7, 8192 42.0 against 52.3; 16/8 of 128, 2432 11.3 against 11.2, 4096 16.9 against 17.8;
+  // 16/2 of 64, 8192 15.2 against 14.9, 12000 19.6 against 19.9.
+  const bool ring = h->ring_from > 0 && T >= h->ring_from;
   p.ring = h->ring;
   p.team_log2 = h->team_log2;
   p.stall = stall;
@@ -550,6 +557,7 @@ BI_GEMM_API int bi_qkrope_get_config(bi_qkrope_t h, bi_qkrope_config* c) {
   c->tokens_per_block = h->per_block;
   c->ring_tokens = h->ring;
   c->ring_ctas = h->ring_ctas;
+  c->ring_from = h->ring_from;
   return BI_GEMM_OK;
 }
 

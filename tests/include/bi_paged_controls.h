@@ -41,7 +41,7 @@ int bi_ctl_attention_shared_stall(bi_attention_t h, const void* q, int64_t T, co
 
 int bi_ctl_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
                          int64_t page_size, int64_t rot_dim, int32_t interleaved, float eps);
-/* The form for many tokens stalls (T at least four times the configuration's ring_ctas). */
+/* The form for many tokens stalls (T at least the configuration's ring_from). */
 int bi_ctl_qkrope_stall(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq,
                         const void* gk, const float* cos_sin, int64_t num_positions, const int32_t* q_seq,
                         const int32_t* q_pos, void* k_cache, void* v_cache, int64_t num_pages,

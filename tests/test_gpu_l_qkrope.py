@@ -69,12 +69,16 @@ def reference(a, Hq, Hkv, D, page, rot, interleaved):
     (5, 1, 1, 64, 1, 16, True, True, 0),
     (130, 40, 40, 128, 64, 96, False, True, 0),          # more heads than a block holds at once
     (9, 3, 1, 64, 12, 48, False, False, 24),
-    (6001, 16, 4, 64, 16, 64, False, True, 8),           # the form for many tokens
+    (6001, 16, 4, 64, 16, 64, False, True, 8),           # many tokens, and the form for them
     (5000, 8, 2, 128, 7, 64, True, True, 0),
     (4001, 2, 1, 64, 32, 32, True, False, 0),
+    (8900, 16, 4, 64, 16, 64, False, True, 8),
+    (8903, 8, 2, 128, 7, 64, True, True, 0),
+    (2500, 32, 8, 128, 16, 128, False, True, 0),
+    (49001, 2, 1, 64, 32, 32, True, False, 0),
 ])
 def test_every_element(T, Hq, Hkv, D, page, rot, inter, norm, pad):
-    a = make(T, Hq, Hkv, D, page, rot, norm=norm, pad=pad, far=2500)
+    a = make(T, Hq, Hkv, D, page, rot, norm=norm, pad=pad, far=max(2500, T // 3 + 1))
     kc0, vc0 = a["k_cache"].clone(), a["v_cache"].clone()
     h = BiQkRope(Hq, Hkv, D, page, rot_dim=rot, eps=EPS, interleaved=inter)
     q = h.run(**a)
@@ -108,9 +112,9 @@ def test_token_independent_of_its_batch():
 def test_token_independent_of_the_form():
     """Tokens of a call large enough for the form for many tokens, alone and in calls on both sides of
     the border between the forms: the same bits; bad tokens among them are reported and left out."""
-    h = BiQkRope(4, 2, 64, 16, eps=EPS)
-    border = 4 * h.config["ring_ctas"]
-    a = make(border + 3, 4, 2, 64, 16, 64, far=4000)
+    h = BiQkRope(16, 2, 64, 16, eps=EPS)
+    border = h.config["ring_from"]
+    a = make(border + 3, 16, 2, 64, 16, 64, far=4000)
     q = h.run(**a).clone()
     kc = a["k_cache"].clone()
     cut = lambda lo, hi: dict(a, qkv=a["qkv"][lo:hi], q_seq=a["q_seq"][lo:hi], q_pos=a["q_pos"][lo:hi])

@@ -237,22 +237,22 @@ def test_waits_that_run_out_are_reported_and_the_handles_survive():
     assert torch.equal(bits(o), bits(plain.run_shared(*a, gs, gl)))
     L.bi_ctl_attention_destroy(h)
     # the form for many tokens of the append
-    rope = BiQkRope(2, 1, 64, 16)
-    T = 4 * rope.config["ring_ctas"]
-    r = make_rope(T, 2, 1, 64, 16, 64, far=2500)
+    rope = BiQkRope(16, 8, 128, 16)
+    T = rope.config["ring_from"]
+    r = make_rope(T, 16, 8, 128, 16, 128, far=2500)
     h = P()
     L.bi_ctl_qkrope_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, I64, ctypes.c_int32, ctypes.c_float]
     L.bi_ctl_qkrope_stall.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, P, P, I64, P, I64, I64, P, U64, P]
-    assert L.bi_ctl_qkrope_create(ctypes.byref(h), 2, 1, 64, 16, 64, 0, 1e-6) == 0
-    q = torch.zeros(T, 2, 64, dtype=torch.bfloat16, device="cuda")
-    assert L.bi_ctl_qkrope_stall(h, ptr(r["qkv"]), T, 4 * 64, ptr(r["gq"]), ptr(r["gk"]), ptr(r["cos_sin"]), 2500,
+    assert L.bi_ctl_qkrope_create(ctypes.byref(h), 16, 8, 128, 16, 128, 0, 1e-6) == 0
+    q = torch.zeros(T, 16, 128, dtype=torch.bfloat16, device="cuda")
+    assert L.bi_ctl_qkrope_stall(h, ptr(r["qkv"]), T, 32 * 128, ptr(r["gq"]), ptr(r["gk"]), ptr(r["cos_sin"]), 2500,
                                  ptr(r["q_seq"]), ptr(r["q_pos"]), ptr(r["k_cache"]), ptr(r["v_cache"]),
                                  r["k_cache"].shape[0], ptr(r["page_table"]), 3, r["page_table"].shape[1], ptr(q),
                                  50_000_000, stream_ptr()) == 0
     assert L.bi_ctl_qkrope_get_device_error(h, stream_ptr()) == bg.BI_GEMM_ERR_TIMEOUT
     assert L.bi_ctl_qkrope_get_device_error(h, stream_ptr()) == 0
     assert L.bi_ctl_qkrope_destroy(h) == 0
-    assert rope.run(**r).shape == (T, 2, 64) and rope.device_error() == 0
+    assert rope.run(**r).shape == (T, 16, 128) and rope.device_error() == 0
     rope.close()
     plain.close()
 
