@@ -1576,12 +1576,24 @@ SharedWs shared_layout(const bi_attention* h, int64_t T, int64_t max_pos, int64_
   return w;
 }
 
+// Nothing is shared without a group, or under a bound that leaves no whole split before a token's own,
+// or where all units run in one round of the decode's resident blocks: two launches then take less time
+// than four, however much is shared (32/8 heads of 128: 4 tokens behind 1500 positions, 128 units, 17.6 us
+// against 22.9 shared; 8 behind 3500, 512 units, 24.5 against 23.7; 8 behind 8192, 1088 units, two rounds,
+// 50.4 against 30.0).
+bool shares(const bi_attention* h, int64_t T, int64_t max_pos, int64_t num_groups) {
+  const int64_t one_round = h->tma4 ? h->tma4_ctas : h->tma ? h->tma_ctas : h->max_ctas;
+  return num_groups > 0 && max_pos >= h->split && T * h->Hkv * (max_pos / h->split + 1) > one_round;
+}
+
 }  // namespace
 
 BI_GEMM_API int bi_attention_shared_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, int64_t num_groups,
                                                    uint64_t* bytes) {
   if (!h || !bytes || T < 0 || max_pos < 0 || num_groups < 0) return BI_GEMM_ERR_INVALID_ARG;
-  *bytes = T == 0 ? 0 : uint64_t(shared_layout(h, T, max_pos, num_groups).total);
+  *bytes = T == 0 ? 0
+           : shares(h, T, max_pos, num_groups) ? uint64_t(shared_layout(h, T, max_pos, num_groups).total)
+                                               : uint64_t(layout_of(h, T, max_pos).total);
   return BI_GEMM_OK;
 }
 
@@ -1602,13 +1614,7 @@ int attention_run_shared(bi_attention* h, const void* q, int64_t T, const int32_
   if (T > 0 && num_groups > 0 && (!group_start || !group_len)) return BI_GEMM_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(group_len)) & 3u)
     return BI_GEMM_ERR_ALIGNMENT;
-  // Nothing is shared without a group, or under a bound that leaves no whole split before a token's own,
-  // or where all units run in one round of the decode's resident blocks: two launches then take less time
-  // than four, however much is shared (32/8 heads of 128: 4 tokens behind 1500 positions, 128 units, 17.6 us
-  // against 22.9 shared; 8 behind 3500, 512 units, 24.5 against 23.7; 8 behind 8192, 1088 units, two rounds,
-  // 50.4 against 30.0).
-  const int64_t one_round = h->tma4 ? h->tma4_ctas : h->tma ? h->tma_ctas : h->max_ctas;
-  if (T == 0 || num_groups == 0 || max_pos < h->split || T * h->Hkv * (max_pos / h->split + 1) <= one_round)
+  if (!shares(h, T, max_pos, num_groups))
     return attention_run(h, q, T, q_seq, q_pos, k_cache, v_cache, num_pages, page_table, num_seqs, max_pages, max_pos,
                          o, stream, -1, timeout_ns, 0, &h->shared_ws);
   const SharedWs w = shared_layout(h, T, max_pos, num_groups);

@@ -261,7 +261,8 @@ def test_refusals_and_empty_calls():
     assert torch.equal(bits(h.run_shared(*a, s[:1], n[:0])), want)          # no group
     empty = [a[0][:0], a[1][:0], a[2][:0]] + a[3:]
     assert h.run_shared(*empty, torch.zeros(2, dtype=torch.int32, device="cuda"), n).shape[0] == 0
-    assert h.shared_workspace_size(2, 600, 1) > h.workspace_size(2, 600)
+    assert h.shared_workspace_size(2, 600, 1) == h.workspace_size(2, 600)          # (nothing is shared)
+    assert h.shared_workspace_size(200, 9000, 1) > h.workspace_size(200, 9000)
     h.close()
 
 
