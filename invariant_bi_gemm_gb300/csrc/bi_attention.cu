@@ -1033,10 +1033,12 @@ __global__ void __launch_bounds__(kMergeThreads, kMergeBatch <= 4 ? 4 : 2) merge
   // kernel does not write them, and this grid starts only after each of its blocks has passed its
   // own wait for the kernels before it, so they are complete and visible (read from L2).
   const int32_t b = __ldcg(p.q_seq + t), pos = __ldcg(p.q_pos + t);
+  // Every unit's partial results are complete and visible.  Blocks with nothing to merge wait as well: a
+  // kernel behind this one waits for this grid alone, which must not end before the units it follows.
+  ptx::grid_dependency_wait();
   if (b < 0 || b >= p.B || pos < 0 || int64_t(pos / p.page_size) >= p.max_pages) return;
   const int32_t n = splits_of(pos, p.split);
   if (n == 1 || pos > p.max_pos) return;    // written directly / refused by the plan
-  ptx::grid_dependency_wait();   // every unit's partial results are complete and visible
   const int64_t slot0 = job * int64_t(p.max_splits);
   const int32_t c = (n + 3) / 4;
   const int pr = slice * kMergePairs + int(threadIdx.x >> 2), q = int(threadIdx.x & 3);

@@ -270,3 +270,29 @@ def test_tensors_of_another_device_are_refused():
     with pytest.raises(ValueError):
         rope.run(x(1, 768, dtype=torch.bfloat16, device="cuda"), None, None, x(1, 64, device="cuda"), i32(0), i32(0),
                  *[t.cuda() for t in (pk.kc, pk.vc, pk.table)])
+
+
+def test_appends_right_behind_a_call_that_merges_nothing():
+    """Contexts of one split, whose outputs need no merge: keys and values appended over them by the next
+    kernel of the stream, which starts as early as it may, change nothing that was asked before."""
+    Hq, Hkv, D, page, T = 32, 8, 128, 16, 2048
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    att, rope = BiAttention(Hq, Hkv, D, page), BiQkRope(Hq, Hkv, D, page)
+    pages = T * 512 // page
+    kc, vc, q = rn(pages, page, Hkv, D), rn(pages, page, Hkv, D), rn(T, Hq, D)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(T, -1).contiguous()
+    seq = torch.arange(T, dtype=torch.int32, device="cuda")
+    last = torch.full((T,), 511, dtype=torch.int32, device="cuda")
+    qkv, cs = rn(T, (Hq + 2 * Hkv) * D), torch.rand(512, D, generator=g, device="cuda")
+    want = bits(att.run(q, seq, last, kc, vc, table, 511)).clone()
+    old = [c.clone() for c in (kc, vc)]
+    for step in range(6):
+        o = att.run(q, seq, last, kc, vc, table, 511)
+        rope.run(qkv, None, None, cs, seq, last - 100 * (step % 2), kc, vc, table)      # inside the contexts
+        assert torch.equal(bits(o), want), step
+        for c, was in zip((kc, vc), old):
+            c.copy_(was)
+    assert att.device_error() == 0 and rope.device_error() == 0
+    att.close()
+    rope.close()
