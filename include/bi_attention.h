@@ -78,7 +78,7 @@ int bi_attention_create(bi_attention_t* out, int64_t num_q_heads, int64_t num_kv
  * grows the handle's workspace (stream-ordered cudaMallocAsync) when T or max_pos outgrow it
  * (BI_GEMM_ERR_OOM if that fails), then queues three kernels on `stream`: a plan of the
  * (token, KV head, split) units, the attention of every unit, and the merge of the splits of
- * tokens that have more than one.  Asynchronous.
+ * tokens that have more than one (none where max_pos leaves one split).  Asynchronous.
  *
  * Two attention kernels, with the same arithmetic and the same bits: for page sizes 8, 16, 32
  * and 64 (a 64-position stage is whole pages) a producer warp loads every page's rows of a KV

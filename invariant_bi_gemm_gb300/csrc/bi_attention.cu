@@ -1533,7 +1533,7 @@ int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_se
                                        : (inl ? h->kern.tma_inline : h->kern.tma))
                            : (inl ? h->kern.fn_inline : h->kern.fn);
   cudaError_t e = cudaLaunchKernelExC(&cfg, fn, use_tma ? targs : args);
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && p.max_splits > 1) {   // (one split at most: every output is written directly)
     cfg.gridDim = dim3(unsigned(T * h->Hkv * h->kern.merge_slices));
     cfg.blockDim = dim3(biattn::kMergeThreads);
     cfg.dynamicSmemBytes = 0;

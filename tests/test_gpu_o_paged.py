@@ -272,7 +272,8 @@ def test_tensors_of_another_device_are_refused():
                  *[t.cuda() for t in (pk.kc, pk.vc, pk.table)])
 
 
-def test_appends_right_behind_a_call_that_merges_nothing():
+@pytest.mark.parametrize("bound", [511, 4000])
+def test_appends_right_behind_a_call_that_merges_nothing(bound):
     """Contexts of one split, whose outputs need no merge: keys and values appended over them by the next
     kernel of the stream, which starts as early as it may, change nothing that was asked before."""
     Hq, Hkv, D, page, T = 32, 8, 128, 16, 2048
@@ -285,10 +286,10 @@ def test_appends_right_behind_a_call_that_merges_nothing():
     seq = torch.arange(T, dtype=torch.int32, device="cuda")
     last = torch.full((T,), 511, dtype=torch.int32, device="cuda")
     qkv, cs = rn(T, (Hq + 2 * Hkv) * D), torch.rand(512, D, generator=g, device="cuda")
-    want = bits(att.run(q, seq, last, kc, vc, table, 511)).clone()
+    want = bits(att.run(q, seq, last, kc, vc, table, bound)).clone()
     old = [c.clone() for c in (kc, vc)]
     for step in range(6):
-        o = att.run(q, seq, last, kc, vc, table, 511)
+        o = att.run(q, seq, last, kc, vc, table, bound)
         rope.run(qkv, None, None, cs, seq, last - 100 * (step % 2), kc, vc, table)      # inside the contexts
         assert torch.equal(bits(o), want), step
         for c, was in zip((kc, vc), old):
