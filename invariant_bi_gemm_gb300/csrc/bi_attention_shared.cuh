@@ -458,7 +458,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t tl = tmem + (uint32_t(w4 * 32) << 16);
     float* mine = msm + 32 * i;
     float* red = reinterpret_cast<float*>(smem + C::OFF_RED) + 128 * i;      // [4][32]
-    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory"); };
+    auto group_sync = [&]() {       // (aligned: the warp's lanes arrive together)
+      __syncwarp();
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
+    };
     // this position's row of the weights' buffer
     const uint32_t prow = sbase + uint32_t(C::OFF_P + pos * 128);
     uint32_t nu = 0, np = 0;

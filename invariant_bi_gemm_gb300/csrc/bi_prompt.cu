@@ -592,7 +592,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + uint32_t(i * 128), to = tmem + lane_base + uint32_t(256 + i * D);
     const uint32_t out_row = sbase + uint32_t(C::OFF_OUT + i * 128 * 128 + r * 128);
-    auto tile_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory"); };
+    // (aligned, as the tensor memory instructions are: the warp's lanes have to arrive together, and come
+    // from branches and loops of their own length)
+    auto tile_sync = [&]() {
+      __syncwarp();
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
+    };
     uint32_t ns = 0, nt = 0;                       // blocks and units of this tile
     Unit u;
     bool ok = true;
@@ -682,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) ok = wait_bar(o_done(i), nt & 1u, sy);
       if (bar_or(1 + i, !ok)) break;
+      __syncwarp();                                // (the wait lets lanes go one by one)
       ++nt;
       ptx::tc_fence_after();
       const bool store = pos >= u.first && pos <= u.last;
@@ -710,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[e] = __float_as_uint(__fadd_rn(__uint_as_float(o[e]), __uint_as_float(uint32_t(v[e]) << 16)));
           }
         }
+        __syncwarp();                           // (a row's loop ends at its own position)
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
@@ -735,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) ptx::st_global_v4(orow + c + 8 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
+        __syncwarp();
       }
       ptx::tc_fence_before();
     }
@@ -746,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t t0 = ptx::globaltimer();
     while (ptx::globaltimer() - t0 < 2000000ull) {
     }
+    __syncwarp();
   }
   if (warp == 1) ptx::tmem_dealloc(tmem, 512);
 }

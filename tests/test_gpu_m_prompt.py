@@ -205,6 +205,27 @@ def test_values_that_are_not_finite_count_where_they_are_seen():
     h.close()
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 4, 128), (4, 2, 64), (8, 2, 128), (8, 1, 64), (8, 1, 128), (2, 2, 64)])
+@pytest.mark.parametrize("page", [16, 12])
+def test_infinite_values_in_whole_and_cut_tiles(Hq, Hkv, D, page):
+    """An infinite value now and then, each in a dimension of its own, so that the rows of a warp add
+    back different numbers of them, in tiles that leave whole and in tiles cut by the chunk's ends."""
+    pk = Pack([(0, 300, 0), (1, 70, 45), (2, 33, 300)], Hq, Hkv, D, page)
+    h = BiPromptAttention(Hq, Hkv, D, page)
+    clean = pk.run(h).cpu()
+    want = torch.zeros(clean.shape, dtype=torch.bool)
+    for b, (_, n, ctx) in enumerate(pk.seqs):
+        lo = int(pk.q_start[b])
+        for k, p in enumerate(range(0, n + ctx, 37)):
+            d = (29 * k) % D
+            pk.vc[pk.table[b, p // page].long(), p % page, Hkv - 1, d] = float("inf")
+            want[lo + max(p - ctx, 0):lo + n, Hq - Hq // Hkv:, d] = True
+    o = pk.run(h).cpu()
+    assert torch.equal(o == float("inf"), want)
+    assert torch.equal(bits(o[~want]), bits(clean[~want]))
+    h.close()
+
+
 def test_rows_outside_the_sequences_and_empty_calls():
     pk = Pack([(0, 70, 0), (1, 0, 0), (2, 30, 5)], 8, 2, 128, 16, lead=11, tail=23)
     h = BiPromptAttention(8, 2, 128, 16)
