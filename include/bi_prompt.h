@@ -25,7 +25,9 @@
  * serves single tokens, keeps 16 bits of every weight and sums in another order.
  *
  * Values that are not finite count where they are seen and nowhere else: a key or value at a
- * position behind p (or in an unused slot of a page) never reaches o[t].
+ * position behind p (or in an unused slot of a page) never reaches o[t].  An infinite value that is
+ * seen under a weight that has underflowed to zero leaves an infinity or a NaN: which of the two is,
+ * like every other bit, a function of q[t], p and K_b, V_b[0..p] alone.
  *
  * Conventions (as in bi_gemm.h, whose BI_GEMM_* return codes these functions use):
  *   - q [T, num_q_heads, head_dim] and o likewise, bf16 row-major; k_cache, v_cache

@@ -24,7 +24,10 @@
 //   2       loads the value blocks (two warps, since a box takes about 48 clocks to issue)
 //   3       cleans the value blocks on the diagonal: rows a query must not see meet weights of zero,
 //           and zero times a value that is not finite is not zero.  Those values become zeros; for
-//           the rows that do see them, the epilogue adds them back (bad_v)
+//           the rows that do see them, the epilogue adds them back (bad_v).  With one query head per
+//           KV head the unit's two tiles end in different blocks; both tiles' rows then have the first
+//           of them cleaned.  It is the block of the unit's first position, whichever tiles the chunk
+//           fills: an infinite value added back is infinite, and one that meets a weight of zero is not
 //   4 - 11  softmax, a warpgroup per tile, a thread per row: S from TMEM, P to TMEM over S's columns
 // TMEM (512 columns): S0 / P0, S1 / P1 (128 each), O0, O1 (D each).
 #include <cuda.h>
@@ -77,6 +80,9 @@ struct Unit {
   int32_t b, kh;
   int32_t nb[2];       // key blocks of each tile (0: none of its rows belong to the chunk)
 };
+
+// The block from which a unit's values are cleaned, a function of its place in the request alone.
+__device__ __forceinline__ int32_t first_dirty(int32_t base) { return base / kBlockPos; }
 
 template <int D_, int G_>
 struct Cfg {
@@ -459,9 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         // One unit; false once a wait gave up.
-        auto unit = [&](const int32_t nb0, const int32_t nb1) {
+        auto unit = [&](const int32_t nb0, const int32_t nb1, const int32_t dirty) {
           const int32_t nb = max(nb0, nb1);
-          const int32_t dirty = (nb0 > 0 ? nb0 : nb1) - 1;           // cleaned from this block on
           if (!wait_bar(q_full, nu & 1u, sy) || !wait_bar(full(st), ph, sy)) return false;
           ptx::tc_fence_after();
           issued = true;
@@ -513,9 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t us = un % kUnitSlots;
           if (!wait_bar(unit_full(us), (un / kUnitSlots) & 1u, sy)) break;
           const int32_t b = units[us].b, nb0 = units[us].nb[0], nb1 = units[us].nb[1];
+          const int32_t dirty = first_dirty(units[us].base);
           ptx::mbar_arrive(unit_empty(us));
           ++un;
-          if (b < 0 || !unit(nb0, nb1)) break;
+          if (b < 0 || !unit(nb0, nb1, dirty)) break;
         }
       }
       if (lead && issued) {          // no MMA of ours may be in flight when TMEM is released
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok && next_unit(u)) {
         const int32_t nb = max(u.nb[0], u.nb[1]);
-        const int32_t dirty = (u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1;
+        const int32_t dirty = first_dirty(u.base);
         // Every load is waited for in turn and released, so that a parity is never a lap off.
         for (int32_t x = 0; x < 2 * nb && ok; ++x) {
           const uint32_t vs = seq + uint32_t(x);
@@ -704,9 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_ld_32x32b_x32(to + uint32_t(c), o);
         ptx::tmem_wait_ld();
         if (dirty && store) {
-          // values on the diagonal that are not finite: a weight is positive, so each stands for itself
-          const int32_t d0 = ((u.nb[0] > 0 ? u.nb[0] : u.nb[1]) - 1) * kBlockPos;
-          for (int32_t k = d0; k <= pos; ++k) {
+          // values of the cleaned blocks that are not finite: each counts as itself, as under a positive
+          // weight (also where the weight has underflowed to zero)
+          for (int32_t k = first_dirty(u.base) * kBlockPos; k <= pos; ++k) {
             const int64_t page = p.c.table[int64_t(u.b) * p.c.max_pages + k / p.c.page_size];
             if (page < 0 || page >= p.c.num_pages) continue;
             const uint16_t* v = p.c.vc + ((page * p.c.page_size + k % p.c.page_size) * p.c.Hkv + u.kh) * D + c;

@@ -226,6 +226,44 @@ def test_infinite_values_in_whole_and_cut_tiles(Hq, Hkv, D, page):
     h.close()
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 4, 128), (2, 2, 64), (4, 2, 128), (8, 1, 64)])
+def test_infinite_values_under_weights_of_zero_do_not_show_the_chunk(Hq, Hkv, D):
+    """Scores so sharp that most weights underflow to zero, and infinite values of both signs and NaN
+    under them: a row's bits are those of the whole prompt in every chunk, one that begins in a unit's
+    second tile (position 130 of units of 256) among them."""
+    n = 700
+    pk = Pack([(0, n, 0)], Hq, Hkv, D, 16)
+    for p, d, x in ((50, 7, "inf"), (127, 8, "-inf"), (128, 9, "inf"), (200, 10, "nan"), (300, 11, "-inf"),
+                    (383, 12, "inf"), (390, 13, "inf"), (640, 14, "-inf")):
+        pk.vc[pk.table[0, p // 16].long(), p % 16, :, d] = float(x)
+    h = BiPromptAttention(Hq, Hkv, D, 16, scale=4.0)
+    whole = pk.run(h)
+    assert bool(whole.isinf().any()) and bool(whole.isnan().any())
+    q = pk.q
+    for lo, hi in ((130, 256), (130, 700), (1, 140), (128, 129), (127, 128), (255, 512), (385, 390), (300, 700), (641, 642)):
+        pk.q = q[lo:hi].contiguous()
+        pk.q_start, pk.q_pos0 = torch.tensor([0, hi - lo], dtype=torch.int32), torch.tensor([lo], dtype=torch.int32)
+        assert torch.equal(bits(pk.run(h)), bits(whole[lo:hi])), (lo, hi)
+    h.close()
+
+
+def test_zeros_of_both_signs_do_not_show_the_chunk():
+    """Values of minus zero, and values of either sign behind a row: the sign of a row's zeros does not
+    depend on what stands in the cache behind it."""
+    Hq, Hkv, D, n = 4, 4, 64, 200
+    pk = Pack([(0, n, 0)], Hq, Hkv, D, 16)
+    h = BiPromptAttention(Hq, Hkv, D, 16)
+    at = lambda p: (pk.table[0, p // 16].long(), p % 16)
+    got = []
+    for sign in (1.0, -1.0):
+        for p in range(n):
+            pk.vc[at(p)[0], at(p)[1], :, 3] = -0.0 if p < 100 else sign
+            pk.vc[at(p)[0], at(p)[1], :, 4] = 0.0 if p < 100 else sign
+        got.append(bits(pk.run(h))[:100].clone())
+    assert torch.equal(got[0], got[1])
+    h.close()
+
+
 def test_rows_outside_the_sequences_and_empty_calls():
     pk = Pack([(0, 70, 0), (1, 0, 0), (2, 30, 5)], 8, 2, 128, 16, lead=11, tail=23)
     h = BiPromptAttention(8, 2, 128, 16)
