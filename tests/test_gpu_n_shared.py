@@ -119,6 +119,64 @@ def test_long_prefix_and_fp64(Hq, Hkv, D):
     h.close()
 
 
+def _page_factors(gr, page, f):
+    """Multiplies every page's keys by f(position of its first slot)."""
+    k = gr.kc.float()
+    done = set()
+    for row in gr.table.tolist():
+        for i, pg in enumerate(row):
+            if pg >= 0 and pg not in done:
+                done.add(pg)
+                k[pg] *= f(i * page)
+    gr.kc = k.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("what", ["scale 4", "scale 16", "growing keys", "wide", "cancelling", "denormal", "far splits"])
+@pytest.mark.parametrize("Hq,Hkv,D,split", [(8, 8, 64, 128), (16, 2, 64, 1024), (4, 4, 128, 512), (8, 1, 128, 128),
+                                            (8, 1, 64, 512), (4, 4, 128, 1024), (32, 8, 128, 512)])
+def test_bits_of_run_on_harsh_inputs(Hq, Hkv, D, split, what):
+    """Scores of hundreds, whose weights underflow or are denormal; keys that grow with their position;
+    keys and values over many powers of two; sums that cancel; denormal inputs; splits whose maxima lie
+    hundreds of powers of two apart: the bits of run, none of them a NaN."""
+    page = 16
+    g = torch.Generator().manual_seed(11)
+    gr = Groups([(2 * split + 77, [1 + 29 * i for i in range(21)]), (split + 16, [3, 40])], Hq, Hkv, D, page)
+    power = lambda x, lo, hi: (x.float() * torch.exp2(torch.randint(lo, hi + 1, x.shape, generator=g).float())).to(
+        torch.bfloat16)
+    scale = D**-0.5
+    if what.startswith("scale"):
+        scale = float(what.split()[1])
+    elif what == "growing keys":
+        _page_factors(gr, page, lambda p: 1 + p / 200)
+        scale = 0.5
+    elif what == "wide":
+        gr.kc, gr.vc, gr.q = power(gr.kc, -12, 6), power(gr.vc, -60, 60), power(gr.q, -6, 2)
+    elif what == "cancelling":
+        gr.kc[..., 1::2] = gr.kc[..., ::2]                       # (pairs of equal keys under opposite queries)
+        gr.q[..., 1::2] = -gr.q[..., ::2] * (1 + 2.0**-7 * (gr.q[..., ::2] > 0))
+        gr.vc[:, 1::2] = -gr.vc[:, ::2]                          # (neighbours of opposite values)
+        gr.kc, gr.vc = power(gr.kc, 0, 6), power(gr.vc, 0, 8)
+    elif what == "denormal":
+        tiny = lambda x: torch.where(x.isnan(), x, torch.randint(-127, 128, x.shape, generator=g).to(torch.bfloat16) * 2.0**-133)
+        gr.vc = tiny(gr.vc)
+        gr.kc[..., ::2] = tiny(gr.kc)[..., ::2]
+        gr.q[0] = tiny(gr.q[0])
+    else:
+        gr.q[..., 0] = 16.0
+        apart = {0: 0.0, 1: 120.0, 2: -120.0, 3: 60.0}
+        k = gr.kc.clone()
+        for row in gr.table.tolist():
+            for i, pg in enumerate(row):
+                if pg >= 0:
+                    k[pg, :, :, 0] = apart[i * page // split % 4]
+        gr.kc = k
+    h = BiAttention(Hq, Hkv, D, page, scale=scale, split_size=split)
+    plain, shared = gr.both(h)
+    assert not bool(plain.view(torch.bfloat16).isnan().any())
+    assert torch.equal(plain, shared)
+    h.close()
+
+
 def test_tokens_of_one_request_and_positions_inside_the_prefix():
     """A group may hold a chunk of a request and tokens whose position lies inside the prefix: each
     shares the splits before its own."""
