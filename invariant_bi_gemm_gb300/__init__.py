@@ -11,7 +11,9 @@ Low-level functions carry the C names (``bi_gemm_create``, ``bi_gemm_run``, ...,
 ``bi_rmsnorm_run``) and take raw device pointers; ``BiGemm``, ``BiRmsNorm``, ``BiPreNorm`` and,
 around one paged KV cache, ``BiQkRope`` (norm, rotation, append), ``BiPromptAttention`` and
 ``BiAttention`` (single tokens; ``run_shared`` for tokens behind a common prefix) wrap them for
-torch tensors.
+torch tensors.  Their calls run on `stream` (a torch stream or a cudaStream_t value; the current
+stream for None); an output that a call makes itself is memory of that stream, and work of another one
+on it is ordered by the caller.
 """
 from __future__ import annotations
 
@@ -179,6 +181,26 @@ def library() -> ctypes.CDLL:
 def _check(rc: int, where: str) -> None:
     if rc != BI_GEMM_OK:
         raise BiGemmError(rc, where)
+
+
+def _new_output(make, stream, device):
+    """An output that a call on `stream` makes itself.  Its memory comes from that stream's pool: a
+    block of the current stream's may still be in use by work queued there.  The current stream counts as a
+    user of it, so that it is not given out again before what is queued there when it is dropped is over
+    (ordering that work behind the call is the caller's, as with any other stream)."""
+    if stream is None:
+        return make()
+    import torch
+    current = torch.cuda.current_stream(device)
+    if not hasattr(stream, "cuda_stream"):
+        number = int(stream)                    # 0 and 1 are names of the default stream
+        stream = torch.cuda.default_stream(device) if number in (0, 1) else torch.cuda.ExternalStream(number, device)
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)
+    return t
 
 
 # --------------------------------------------------------------------- C names
@@ -460,7 +482,7 @@ class BiGemm:
         if want is None and (x.element_size() != 1 or W.element_size() != 1):
             raise ValueError("E4M3 inputs (1 byte per element) expected")
         if y is None:
-            y = torch.empty((M, self.N), dtype=self.out_dtype(), device=x.device)
+            y = _new_output(lambda: torch.empty((M, self.N), dtype=self.out_dtype(), device=x.device), stream, x.device)
         if tuple(y.shape) != (M, self.N) or y.dtype != self.out_dtype() or not y.is_contiguous():
             raise ValueError("y must be a contiguous [M, N] tensor of the output dtype")
         scales = None
@@ -496,14 +518,14 @@ class BiGemm:
         M = sum(int(b.shape[0]) for b in blocks)
         dev = blocks[0].device
         if x_out is None:
-            x_out = torch.empty((M, self.K), dtype=blocks[0].dtype, device=dev)
+            x_out = _new_output(lambda: torch.empty((M, self.K), dtype=blocks[0].dtype, device=dev), stream, dev)
         if fp8:
             if sx_blocks is None or sw is None:
                 raise ValueError("MXFP8 needs sx_blocks and sw")
             if sx_out is None:
-                sx_out = torch.empty((M, self.K // 32), dtype=torch.uint8, device=dev)
+                sx_out = _new_output(lambda: torch.empty((M, self.K // 32), dtype=torch.uint8, device=dev), stream, dev)
         if y is None:
-            y = torch.empty((M, self.N), dtype=self.out_dtype(), device=dev)
+            y = _new_output(lambda: torch.empty((M, self.N), dtype=self.out_dtype(), device=dev), stream, dev)
         if tuple(x_out.shape) != (M, self.K) or tuple(y.shape) != (M, self.N):
             raise ValueError("x_out [M, K] and y [M, N] expected")
         arr = (bi_gemm_block * nb)()
@@ -564,7 +586,7 @@ class BiRmsNorm:
             raise ValueError("x and g must be contiguous CUDA tensors")
         M = int(x.shape[0])
         if y is None:
-            y = torch.empty((M, self.d), dtype=torch.bfloat16, device=x.device)
+            y = _new_output(lambda: torch.empty((M, self.d), dtype=torch.bfloat16, device=x.device), stream, x.device)
         if tuple(y.shape) != (M, self.d) or y.dtype != torch.bfloat16 or not y.is_contiguous():
             raise ValueError("y must be a contiguous [M, d] bf16 tensor")
         if stream is None:
@@ -622,7 +644,7 @@ class BiAttention:
         if tuple(q_seq.shape) != (T,) or tuple(q_pos.shape) != (T,) or page_table.dim() != 2:
             raise ValueError("q_seq, q_pos [T]; page_table [num_seqs, max_pages]")
         if o is None:
-            o = torch.empty_like(q)
+            o = _new_output(lambda: torch.empty_like(q), stream, q.device)
         if o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
             raise ValueError("o must be a contiguous bf16 tensor shaped like q")
         if stream is None:
@@ -647,7 +669,7 @@ class BiAttention:
         group_start[g + 1] - 1 (int32 [groups + 1], ascending), whose requests name the same pages
         for positions 0 .. group_len[g] - 1 (int32 [groups]).  The prefix is read once per group;
         the result has the bits of run()."""
-        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device)
+        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device, stream)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, (self.page_size, self.Hkv, self.D), index)
         groups, i32 = group_len.shape[0], _torch.i32
         _check_tensor("q_seq", q_seq, i32, (T,), index)
@@ -732,15 +754,15 @@ def _check_cache(k_cache, v_cache, page_table, page_shape, index: int):
     return shape[0], table[0], table[1]
 
 
-def _check_queries(q, o, Hq: int, D: int, device: int):
-    """q [T, Hq, D] bf16 and o like it (made where it is None) on the handle's device.  Returns (T,
-    device index, o)."""
+def _check_queries(q, o, Hq: int, D: int, device: int, stream):
+    """q [T, Hq, D] bf16 and o like it (made for `stream` where it is None) on the handle's device.
+    Returns (T, device index, o)."""
     shape, index = q.shape, q.get_device()
     if len(shape) != 3 or shape[1] != Hq or shape[2] != D or index != device:
         raise ValueError(f"q must be a tensor [T, num_q_heads, head_dim] on cuda:{device}")
     _check_tensor("q", q, _torch.bf16, shape, index)
     if o is None:
-        o = _torch.empty_like(q)
+        o = _torch.empty_like(q) if stream is None else _new_output(lambda: _torch.empty_like(q), stream, q.device)
     else:
         _check_tensor("o", o, _torch.bf16, shape, index)
     return shape[0], index, o
@@ -795,7 +817,8 @@ class BiQkRope:
         _check_tensor("q_pos", q_pos, i32, (T,), index)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         if q_out is None:
-            q_out = _torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device)
+            q_out = _new_output(lambda: _torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device), stream,
+                                qkv.device)
         else:
             _check_tensor("q_out", q_out, bf16, (T, self.Hq, self.D), index)
         _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), angles[0],
@@ -848,7 +871,7 @@ class BiPromptAttention:
         return bi_prompt_get_config(self.handle)
 
     def run(self, q, q_start, q_pos0, k_cache, v_cache, page_table, max_pos: int, o=None, stream=None):
-        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device)
+        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device, stream)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         _check_tensor("q_start", q_start, _torch.i32, (seqs + 1,), index)
         _check_tensor("q_pos0", q_pos0, _torch.i32, (seqs,), index)
@@ -902,7 +925,7 @@ class BiPreNorm:
             raise ValueError("x and W must be contiguous CUDA tensors")
         M = int(x.shape[0])
         if y is None:
-            y = torch.empty((M, self.N), dtype=torch.float32, device=x.device)
+            y = _new_output(lambda: torch.empty((M, self.N), dtype=torch.float32, device=x.device), stream, x.device)
         if tuple(y.shape) != (M, self.N) or y.dtype != torch.float32 or not y.is_contiguous():
             raise ValueError("y must be a contiguous [M, N] fp32 tensor")
         if stream is None:
