@@ -112,9 +112,10 @@ int bi_attention_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, ui
  * 4-byte aligned.  Caught by the kernels, as BI_GEMM_ERR_INVALID_ARG from
  * bi_attention_get_device_error: a group_start that descends or leaves [0, T] or a negative
  * group_len (nothing is shared then, the outputs are bi_attention_run's), and page tables that
- * differ within a shared split (the group's outputs are then undefined).  num_groups >= 0; all else as bi_attention_run, but for the workspace: run_shared has its own, grown by
- * cudaMalloc (BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph that needs more than
- * an earlier call of its size left; a graph stays valid when later calls grow it).  Queues four
+ * differ within a shared split (the group's outputs are then undefined).  num_groups >= 0; all else
+ * as bi_attention_run, but for the workspace: run_shared has its own, grown in stream order
+ * (BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph that needs more than an earlier
+ * call of its size left; a graph stays valid when later calls grow it).  Queues four
  * kernels: a plan, the tokens' own units, the groups' units beside them, the merge.  A call whose
  * units (T x KV heads x splits up to max_pos) all run at once, four or fewer per SM, is faster
  * unshared: it is served by bi_attention_run's kernels and its groups are not looked at. */
@@ -124,7 +125,9 @@ int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const in
                             int64_t max_pages, int64_t max_pos, const int32_t* group_start,
                             const int32_t* group_len, int64_t num_groups, void* o, void* stream);
 
-/* Workspace bytes of a run_shared with T tokens, the bound max_pos and num_groups groups. */
+/* Workspace bytes that a run_shared with T tokens, the bound max_pos and num_groups groups needs.  The
+ * handle holds up to twice what a run has needed, at most 64 MiB more, and the smaller ones that
+ * captured calls use. */
 int bi_attention_shared_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, int64_t num_groups,
                                        uint64_t* bytes);
 

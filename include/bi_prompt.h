@@ -77,18 +77,19 @@ int bi_prompt_create(bi_prompt_t* out, int64_t num_q_heads, int64_t num_kv_heads
 
 /* o = attention(q) for the T packed query tokens of num_seqs sequences.  max_pos: an upper bound
  * (on the host) of every position; it changes no result.  T = 0 or num_seqs = 0 queues nothing.
- * The run grows the handle's workspace (cudaMalloc) when T or num_seqs outgrow it (BI_GEMM_ERR_OOM
- * if that fails; BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph, which uses what
- * an earlier call of its size left; a graph stays valid when later calls grow the workspace), then
- * queues two kernels: a plan of the units (longest first) and the attention.  A call with fewer
- * units than the GPU has SMs needs neither plan nor workspace.  Asynchronous.  The
- * kernel's waits are bounded (2 s): past the limit the block stops, its output is undefined and
+ * The run grows the handle's workspace (stream-ordered cudaMallocAsync) when T or num_seqs outgrow
+ * it (BI_GEMM_ERR_OOM if that fails; BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph,
+ * which uses what an earlier call of its size left; a graph stays valid when later calls grow the
+ * workspace), then queues two kernels: a plan of the units (longest first) and the attention.  A call
+ * that can have no more units than the GPU has SMs needs neither plan nor workspace.  Asynchronous.
+ * The kernel's waits are bounded (2 s): past the limit the block stops, its output is undefined and
  * bi_prompt_get_device_error reports BI_GEMM_ERR_TIMEOUT. */
 int bi_prompt_run(bi_prompt_t h, const void* q, int64_t T, const int32_t* q_start, const int32_t* q_pos0,
                   int64_t num_seqs, const void* k_cache, const void* v_cache, int64_t num_pages,
                   const int32_t* page_table, int64_t max_pages, int64_t max_pos, void* o, void* stream);
 
-/* Workspace bytes a run with T tokens in num_seqs sequences needs (0 for few). */
+/* Workspace bytes a run with T tokens in num_seqs sequences needs (0 for few).  The handle holds up to
+ * twice what a run has needed, at most 64 MiB more, and the smaller ones that captured calls use. */
 int bi_prompt_workspace_size(bi_prompt_t h, int64_t T, int64_t num_seqs, uint64_t* bytes);
 
 /* Synchronise `stream`; BI_GEMM_ERR_TIMEOUT if a bounded wait expired, else

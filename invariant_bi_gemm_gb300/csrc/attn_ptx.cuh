@@ -292,36 +292,51 @@ __device__ __forceinline__ void load_block_rows(uint32_t dst, const uint16_t* ba
 // Page sizes whose blocks are whole TMA boxes: powers of two from 8 (one 1024-byte swizzle atom) up.
 inline bool tma_page_size(int64_t ps) { return ps >= 8 && (ps & (ps - 1)) == 0; }
 
-// A handle's device scratch.  It grows to what a call needs, at least to twice what it was, and earlier
-// blocks live until the handle does: a graph captured with one of them may still be replayed.
+// A handle's device scratch, grown in stream order.  A block that a captured call uses lives until the
+// handle does, since the graph may still be replayed; any other is freed behind the calls that used it.
 struct Workspace {
+  // growth doubles up to this step, so that a bound that climbs with every call does not move the
+  // scratch at each, and no handle holds more than this beyond what a call has asked for
+  static constexpr size_t kStep = size_t(64) << 20;
   void* at = nullptr;
   size_t bytes = 0;
+  bool captured = false;        // a captured call uses `at`
   std::vector<void*> earlier;
 
-  // A call being captured cannot allocate for good: it uses what earlier calls (or a reserve) left.
+  // A call being captured cannot allocate for good: it uses what earlier calls left.
   int need(size_t n, cudaStream_t st) {
-    if (n <= bytes) return BI_GEMM_OK;
+    if (n == 0) return BI_GEMM_OK;
     cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) {
       cudaGetLastError();
       return BI_GEMM_ERR_CUDA;
     }
+    if (n <= bytes) {
+      captured |= capturing != cudaStreamCaptureStatusNone;
+      return BI_GEMM_OK;
+    }
     if (capturing != cudaStreamCaptureStatusNone) return BI_GEMM_ERR_SCRATCH_LIMIT;
-    const size_t size = n > 2 * bytes ? n : 2 * bytes;
-    void* p = nullptr;
-    if (cudaMalloc(&p, size) != cudaSuccess) {
-      cudaGetLastError();
-      return BI_GEMM_ERR_OOM;
-    }
     try {
-      if (at) earlier.push_back(at);
+      if (captured) earlier.reserve(earlier.size() + 1);
     } catch (...) {
-      cudaFree(p);
       return BI_GEMM_ERR_OOM;
     }
+    const size_t step = bytes + (bytes < kStep ? bytes : kStep);
+    size_t size = n > step ? n : step;
+    void* p = allocate(size, st);
+    if (!p && size > n) p = allocate(size = n, st);
+    if (!p && at && !captured) {          // the block that it replaces may be the room it needs
+      cudaFreeAsync(at, st);
+      at = nullptr;
+      bytes = 0;
+      p = allocate(size, st);
+    }
+    if (!p) return BI_GEMM_ERR_OOM;
+    if (captured) earlier.push_back(at);
+    else if (at) cudaFreeAsync(at, st);
     at = p;
     bytes = size;
+    captured = false;
     return BI_GEMM_OK;
   }
   void release() {
@@ -329,7 +344,16 @@ struct Workspace {
     for (void* p : earlier) cudaFree(p);
     at = nullptr;
     bytes = 0;
+    captured = false;
     earlier.clear();
+  }
+  static void* allocate(size_t n, cudaStream_t st) {
+    void* p = nullptr;
+    if (cudaMallocAsync(&p, n, st) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    return p;
   }
 };
 

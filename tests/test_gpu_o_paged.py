@@ -194,6 +194,54 @@ def test_graphs_outlive_the_growth_of_their_workspace():
         h.close()
 
 
+def _held(f):
+    """Device memory that f() left allocated outside torch."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.mem_get_info()[0]
+    f()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    return before - torch.cuda.mem_get_info()[0]
+
+
+def test_growth_holds_no_more_than_its_step():
+    """A bound that climbs call by call: the handle ends up with the workspace that the last call needs
+    and one step of growth (64 MiB, and what the driver rounds up), not with every earlier one."""
+    gr = Groups([(600, [3 + i for i in range(64)])], 32, 8, 128, 16)
+    att, a = BiAttention(32, 8, 128, 16), gr.args()[:-1]
+    extra = (gr.start.cuda(), gr.len.cuda())
+    out = torch.empty_like(a[0])
+    att.run_shared(*a, 8191, *extra, o=out)
+    bounds = [512 * n - 1 for n in range(40, 321, 40)]
+    need = att.shared_workspace_size(64, bounds[-1], 1)
+    assert need > 300 << 20
+    held = _held(lambda: [att.run_shared(*a, b, *extra, o=out) for b in bounds])
+    assert held <= need + (64 << 20) + (64 << 20), (held, need)
+    want = bits(att.run(*a, 8191))
+    assert torch.equal(bits(att.run_shared(*a, bounds[-1], *extra)), want) and att.device_error() == 0
+    att.close()
+
+
+def test_growth_keeps_what_captured_calls_use():
+    """Large workspaces: one that a captured call uses outlives the growth, and the graph its bits."""
+    gr = Groups([(600, [3 + i for i in range(64)])], 32, 8, 128, 16)
+    att, a = BiAttention(32, 8, 128, 16), gr.args()[:-1]
+    extra = (gr.start.cuda(), gr.len.cuda())
+    want = bits(att.run_shared(*a, 512 * 100, *extra)).clone()
+    out = torch.zeros_like(a[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        att.run_shared(*a, 512 * 100, *extra, o=out)
+    for n in (150, 250, 350):
+        assert torch.equal(bits(att.run_shared(*a, 512 * n, *extra)), want)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out), want) and att.device_error() == 0
+    att.close()
+
+
 def test_waits_that_run_out_are_reported_and_the_handles_survive():
     """Failure injection (test controls): block 0 of each kernel loads nothing, its waits end after
     50 ms, the call reports BI_GEMM_ERR_TIMEOUT, and the next ordinary call gives the golden bits."""
