@@ -1562,7 +1562,7 @@ namespace {
 struct SharedWs {
   WsLayout base;
   size_t nsh, srec, count, total;
-  int64_t cap;      // unit records: a group of n tokens has at most n / (tokens of a unit) + 1 rows of units
+  int64_t cap;      // unit records: a group of n > 1 tokens has at most n / (tokens of a unit) + 1 rows of units
   int32_t cols;
 };
 
@@ -1570,7 +1570,8 @@ SharedWs shared_layout(const bi_attention* h, int64_t T, int64_t max_pos, int64_
   SharedWs w;
   w.base = layout_of(h, T, max_pos);
   w.cols = h->split <= 512 ? 128 : 64;      // (blocks of a split) x columns fit the 512 of tensor memory
-  w.cap = (T / (w.cols / h->G) + num_groups) * (max_pos / h->split);
+  // (a group of fewer than two tokens has none)
+  w.cap = (T / (w.cols / h->G) + std::min(num_groups, T / 2)) * (max_pos / h->split);
   w.nsh = w.base.total;
   w.srec = w.nsh + biattn::align256(size_t(T) * sizeof(int32_t));
   w.count = w.srec + biattn::align256(size_t(w.cap) * sizeof(int4));
@@ -1578,14 +1579,14 @@ SharedWs shared_layout(const bi_attention* h, int64_t T, int64_t max_pos, int64_
   return w;
 }
 
-// Nothing is shared without a group, or under a bound that leaves no whole split before a token's own,
+// Nothing is shared without a group or by one token, or under a bound that leaves no whole split before a token's own,
 // or where all units run in one round of the decode's resident blocks: two launches then take less time
 // than four, however much is shared (32/8 heads of 128: 4 tokens behind 1500 positions, 128 units, 17.6 us
 // against 22.9 shared; 8 behind 3500, 512 units, 24.5 against 23.7; 8 behind 8192, 1088 units, two rounds,
 // 50.4 against 30.0).
 bool shares(const bi_attention* h, int64_t T, int64_t max_pos, int64_t num_groups) {
   const int64_t one_round = h->tma4 ? h->tma4_ctas : h->tma ? h->tma_ctas : h->max_ctas;
-  return num_groups > 0 && max_pos >= h->split && T * h->Hkv * (max_pos / h->split + 1) > one_round;
+  return T > 1 && num_groups > 0 && max_pos >= h->split && T * h->Hkv * (max_pos / h->split + 1) > one_round;
 }
 
 }  // namespace

@@ -306,6 +306,30 @@ def test_many_groups(groups):
     h.close()
 
 
+def test_a_long_table_of_empty_groups():
+    """Groups that hold no two tokens share nothing and need no room: a table padded with 2^18 of them
+    is served like the one without, and asks for no more workspace than the tokens can fill."""
+    gr = Groups([(1100, [3, 40, 5]), (1500, [1, 2, 7, 9])], 8, 2, 64, 16)
+    h = BiAttention(8, 2, 64, 16)
+    want = gr.both(h)[0]
+    n = 1 << 18
+    start = torch.full((n + 1,), 7, dtype=torch.int32)
+    length = torch.zeros(n, dtype=torch.int32)
+    start[:3], length[:2] = gr.start, gr.len
+    assert torch.equal(bits(h.run_shared(*gr.args(), start.cuda(), length.cuda())), want)
+    assert h.device_error() == 0
+    # one token, under a bound that would have more of them share
+    one = [x[:1].contiguous() for x in gr.args()[:3]] + gr.args()[3:-1]
+    assert torch.equal(bits(h.run_shared(*one, 1 << 20, torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                                         gr.len[:1].cuda())), want[:1])
+    assert h.device_error() == 0
+    # (seven tokens make at most three groups of two or more)
+    assert h.shared_workspace_size(7, 1 << 20, n) == h.shared_workspace_size(7, 1 << 20, 3)
+    bound = (1 << 29) - 1                      # 2^20 splits: room for a unit of every group was refused
+    assert h.shared_workspace_size(7, bound, n) == h.shared_workspace_size(7, bound, 3)
+    h.close()
+
+
 def test_refusals_and_empty_calls():
     gr = Groups([(600, [3, 4])], 8, 2, 64, 16)
     h = BiAttention(8, 2, 64, 16)
