@@ -116,9 +116,10 @@ int bi_attention_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, ui
  * as bi_attention_run, but for the workspace: run_shared has its own, grown in stream order
  * (BI_GEMM_ERR_SCRATCH_LIMIT in a call being captured into a graph that needs more than an earlier
  * call of its size left; a graph stays valid when later calls grow it).  Queues four
- * kernels: a plan, the tokens' own units, the groups' units beside them, the merge.  A call whose
- * units (T x KV heads x splits up to max_pos) all run at once, four or fewer per SM, is faster
- * unshared: it is served by bi_attention_run's kernels and its groups are not looked at. */
+ * kernels: a plan, the tokens' own units, the groups' units (which start as the own units' blocks
+ * leave SMs to them), the merge.  A call of one token, or whose units (T x KV heads x splits up to
+ * max_pos) the handle's blocks of bi_attention_run hold all at once, is faster unshared: it is
+ * served by bi_attention_run's kernels and its groups are not looked at. */
 int bi_attention_run_shared(bi_attention_t h, const void* q, int64_t T, const int32_t* q_seq,
                             const int32_t* q_pos, const void* k_cache, const void* v_cache,
                             int64_t num_pages, const int32_t* page_table, int64_t num_seqs,

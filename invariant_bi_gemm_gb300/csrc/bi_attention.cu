@@ -1579,13 +1579,18 @@ SharedWs shared_layout(const bi_attention* h, int64_t T, int64_t max_pos, int64_
   return w;
 }
 
-// Nothing is shared without a group or by one token, or under a bound that leaves no whole split before a token's own,
-// or where all units run in one round of the decode's resident blocks: two launches then take less time
-// than four, however much is shared (32/8 heads of 128: 4 tokens behind 1500 positions, 128 units, 17.6 us
-// against 22.9 shared; 8 behind 3500, 512 units, 24.5 against 23.7; 8 behind 8192, 1088 units, two rounds,
-// 50.4 against 30.0).
+// Nothing is shared without a group or by one token, or under a bound that leaves no whole split before a
+// token's own, or where all units run in one round of the decode's resident blocks: two launches then take
+// less time than four, however much is shared.  The blocks counted are those of the kernel for the handle's
+// pages: the TMA kernel's (32/8 heads of 128: 4 tokens behind 1500 positions, 128 units, 17.6 us against
+// 22.9 shared; 8 behind 3500, 512 units, 24.5 against 23.7; 8 behind 8192, 1088 units, two rounds, 50.4
+// against 30.0), or, for pages that are copied by rows, the row-copy kernel's (16/2 heads of 64, pages of
+// 12, five blocks per SM: 4 tokens of 94 splits, 752 units, 31.5 against 67.6 shared, 16 of 22, 28.0 against
+// 34.7; 16 of 24, two rounds, 40.2 against 34.9).
 bool shares(const bi_attention* h, int64_t T, int64_t max_pos, int64_t num_groups) {
-  const int64_t one_round = h->tma4 ? h->tma4_ctas : h->tma ? h->tma_ctas : h->max_ctas;
+  const int64_t one_round = h->tma4  ? h->tma4_ctas
+                            : h->tma ? h->tma_ctas
+                                     : (T <= biattn::kInlinePlanMaxT ? h->max_ctas_inline : h->max_ctas);
   return T > 1 && num_groups > 0 && max_pos >= h->split && T * h->Hkv * (max_pos / h->split + 1) > one_round;
 }
 

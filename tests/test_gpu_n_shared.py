@@ -279,6 +279,17 @@ def test_both_sides_of_the_rule(page):
     h.close()
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page,T,splits", [(16, 2, 64, 12, 4, 94), (16, 2, 64, 12, 16, 22), (8, 8, 64, 12, 16, 5)])
+def test_what_run_serves_in_one_round_is_not_shared(Hq, Hkv, D, page, T, splits):
+    """For pages that are copied by rows the rule counts the blocks of the kernel that run takes (five per
+    SM here, 760 for 640 to 752 units), so that no call is shared whose units those hold at once."""
+    h = BiAttention(Hq, Hkv, D, page)
+    assert 608 < T * Hkv * splits <= 760
+    assert h.shared_workspace_size(T, 512 * splits - 1, 1) == h.workspace_size(T, 512 * splits - 1)
+    assert h.shared_workspace_size(T, 512 * 2 * splits - 1, 1) > h.workspace_size(T, 512 * 2 * splits - 1)
+    h.close()
+
+
 def test_overlapping_groups():
     """Groups that climb, fall back and climb again claim the same tokens twice: reported, and every
     token is served by units of its own."""
