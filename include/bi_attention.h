@@ -76,7 +76,9 @@ int bi_attention_create(bi_attention_t* out, int64_t num_q_heads, int64_t num_kv
 /* o = attention(q) for T query tokens.  max_pos: an upper bound (on the host) of every q_pos;
  * it sizes the workspace and the grid and changes no result.  T = 0 queues nothing.  The run
  * grows the handle's workspace (stream-ordered cudaMallocAsync) when T or max_pos outgrow it
- * (BI_GEMM_ERR_OOM if that fails), then queues three kernels on `stream`: a plan of the
+ * (BI_GEMM_ERR_OOM if that fails; in a call being captured into a graph that an earlier call of its
+ * size did not make room for, the graph allocates its own at every launch; a graph stays valid when
+ * later calls grow the workspace), then queues three kernels on `stream`: a plan of the
  * (token, KV head, split) units, the attention of every unit, and the merge of the splits of
  * tokens that have more than one (none where max_pos leaves one split).  Asynchronous.
  *
@@ -93,7 +95,8 @@ int bi_attention_run(bi_attention_t h, const void* q, int64_t T, const int32_t* 
                      int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
                      int64_t max_pages, int64_t max_pos, void* o, void* stream);
 
-/* Workspace bytes a run with T tokens and the bound max_pos needs. */
+/* Workspace bytes a run with T tokens and the bound max_pos needs.  The handle holds up to twice what
+ * a run has needed, at most 64 MiB more, and the smaller ones that captured calls use. */
 int bi_attention_workspace_size(bi_attention_t h, int64_t T, int64_t max_pos, uint64_t* bytes);
 
 /* bi_attention_run for a batch whose tokens come in groups with a common prefix (a system prompt,

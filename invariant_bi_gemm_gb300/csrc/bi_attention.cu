@@ -1230,10 +1230,8 @@ struct bi_attention {
   size_t tma4_smem = 0;
   biattn::KernelInfo kern;
   biattn::SharedInfo shared;
-  biattn_tc::Workspace shared_ws;   // run_shared's own
   uint32_t* d_status = nullptr;
-  void* ws = nullptr;
-  size_t ws_bytes = 0;
+  biattn_tc::Workspace ws, shared_ws;   // run's, run_shared's
 };
 
 namespace {
@@ -1435,21 +1433,16 @@ int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_se
   if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WsLayout w = layout_of(h, T, max_pos);
-  if (own) {
-    if (const int rc = own->need(w.total, st)) return rc;
-  } else if (w.total > h->ws_bytes) {
-    if (h->ws) cudaFreeAsync(h->ws, st);
-    h->ws = nullptr;
-    h->ws_bytes = 0;
-    void* p = nullptr;
-    if (cudaMallocAsync(&p, w.total, st) != cudaSuccess) {
-      cudaGetLastError();
-      return BI_GEMM_ERR_OOM;
-    }
-    h->ws = p;
-    h->ws_bytes = w.total;
+  // A captured run that needs more than earlier calls left has the graph allocate and free it: memory
+  // that is there while the graph runs alone, so the handle does not keep it.
+  biattn_tc::Workspace& space = own ? *own : h->ws;
+  void* in_graph = nullptr;
+  if (const int rc = space.need(w.total, st)) {
+    if (own || rc != BI_GEMM_ERR_SCRATCH_LIMIT) return rc;
+    in_graph = biattn_tc::Workspace::allocate(w.total, st);
+    if (!in_graph) return BI_GEMM_ERR_OOM;
   }
-  uint8_t* ws = static_cast<uint8_t*>(own ? own->at : h->ws);
+  uint8_t* ws = static_cast<uint8_t*>(in_graph ? in_graph : space.at);
   biattn::Params p;
   std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const uint16_t*>(q);
@@ -1503,7 +1496,10 @@ int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_se
                        biattn::encode_cache(&tmv, v_cache, rows, h->Hkv, h->D, h->page_size);
   if (!p.inline_plan) {
     biattn::plan_kernel<<<1, 1024, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return BI_GEMM_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) {
+      if (in_graph) cudaFreeAsync(in_graph, st);
+      return BI_GEMM_ERR_CUDA;
+    }
   }
   const int64_t units = T * h->Hkv * int64_t(p.max_splits);
   void* args[1] = {&p};
@@ -1539,6 +1535,10 @@ int attention_run(bi_attention* h, const void* q, int64_t T, const int32_t* q_se
     cfg.dynamicSmemBytes = 0;
     // at most four splits per group: the instantiation with more resident blocks
     e = cudaLaunchKernelExC(&cfg, (p.max_splits + 3) / 4 <= 4 ? h->kern.merge : h->kern.merge_long, args);
+  }
+  if (in_graph) {
+    const cudaError_t f = cudaFreeAsync(in_graph, st);
+    if (e == cudaSuccess) e = f;
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -1787,7 +1787,7 @@ BI_GEMM_API int bi_attention_get_config(bi_attention_t h, bi_attention_config* c
 
 BI_GEMM_API int bi_attention_destroy(bi_attention_t h) {
   if (!h) return BI_GEMM_OK;
-  if (h->ws) cudaFree(h->ws);
+  h->ws.release();
   h->shared_ws.release();
   if (h->d_status) cudaFree(h->d_status);
   delete h;

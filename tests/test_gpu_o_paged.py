@@ -242,6 +242,41 @@ def test_growth_keeps_what_captured_calls_use():
     att.close()
 
 
+def test_captured_runs_and_the_workspace_of_run():
+    """BiAttention.run captured by a handle that has not run before, captured again after smaller calls,
+    and grown between the replays: graphs and calls give the bits of a handle that is never captured."""
+    gr = Groups([(3000, [3 + 5 * i for i in range(40)])], 8, 2, 64, 16)
+    few, many = [x[:5].contiguous() for x in gr.args()[:3]] + gr.args()[3:], gr.args()
+    plain, att = BiAttention(8, 2, 64, 16), BiAttention(8, 2, 64, 16)
+    want = [bits(plain.run(*a)).clone() for a in (few, many)]
+    out = [torch.zeros_like(a[0]) for a in (few, many, few)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(3)]
+
+    def replay(k):
+        out[k].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        return torch.equal(bits(out[k]), want[k % 2])
+
+    with torch.cuda.graph(graphs[0]):
+        att.run(*few, o=out[0])                       # nothing has run: the graph's own memory
+    assert torch.equal(bits(att.run(*few)), want[0])
+    assert replay(0) and replay(0)
+    with torch.cuda.graph(graphs[1]):
+        att.run(*many, o=out[1])                      # more than there is
+    with torch.cuda.graph(graphs[2]):
+        att.run(*few, o=out[2])                       # what there is
+    assert replay(1) and replay(2) and replay(1)
+    for _ in range(2):
+        assert torch.equal(bits(att.run(*many)), want[1])                # grows past what graph 2 uses
+        junk = [torch.full((1 << 22,), 0x7F7F7F7F, dtype=torch.int32, device="cuda") for _ in range(8)]
+        assert replay(2) and replay(0) and replay(1)
+        del junk
+    assert torch.equal(bits(att.run(*few)), want[0]) and att.device_error() == 0
+    att.close()
+    plain.close()
+
+
 def test_waits_that_run_out_are_reported_and_the_handles_survive():
     """Failure injection (test controls): block 0 of each kernel loads nothing, its waits end after
     50 ms, the call reports BI_GEMM_ERR_TIMEOUT, and the next ordinary call gives the golden bits."""
