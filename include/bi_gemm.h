@@ -73,7 +73,9 @@ enum {
   BI_GEMM_ERR_TIMEOUT = -6,      /* a bounded in-kernel wait expired (reported by
                                     bi_gemm_get_device_error)                               */
   BI_GEMM_ERR_SCRATCH_LIMIT = -7 /* bi_gemm_run_noalloc: the run needs more scratch than its
-                                    fixed array holds                                       */
+                                    fixed array holds; bi_prompt_run and
+                                    bi_attention_run_shared in a call being captured: more
+                                    workspace than earlier calls left                       */
 };
 
 /* Create a handle for y = x·W with fixed K and N.  Selects and records the single kernel

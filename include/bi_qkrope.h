@@ -31,7 +31,7 @@
  *     the kernel: the token's q_out row and slot are left as they were and
  *     bi_qkrope_get_device_error reports BI_GEMM_ERR_INVALID_ARG.
  *   - The (request, position) pairs of a call name different slots.  Two tokens of one call on the
- *     same slot leave it with 16-byte pieces of either.
+ *     same slot leave it with 8-byte pieces of either.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).  A handle keeps
  *     no workspace, only its status word; it is not thread-safe.
  */

@@ -663,7 +663,9 @@ BI_GEMM_API const char* bi_gemm_strerror(int code) {
     case BI_GEMM_ERR_CUDA: return "CUDA runtime error";
     case BI_GEMM_ERR_OOM: return "workspace allocation failed";
     case BI_GEMM_ERR_TIMEOUT: return "bounded in-kernel wait expired";
-    case BI_GEMM_ERR_SCRATCH_LIMIT: return "problem too large for the fixed scratch of bi_gemm_run_noalloc";
+    case BI_GEMM_ERR_SCRATCH_LIMIT:
+      return "scratch too small: a run past the fixed array of bi_gemm_run_noalloc, or a captured call that needs "
+             "more workspace than earlier calls left";
     default: return "unknown error code";
   }
 }

@@ -93,6 +93,11 @@ def test_shared_attention_null_arguments():
     assert L.bi_attention_shared_workspace_size(None, 1, 1, 1, ctypes.byref(b)) == INVALID
 
 
+def test_the_scratch_limit_names_captured_calls():
+    """The prompt and shared-prefix calls return it too, and have no fixed array."""
+    assert "captured" in bg.bi_gemm_strerror(bg.BI_GEMM_ERR_SCRATCH_LIMIT)
+
+
 def test_controls_symbols_exported():
     declared = [n for n in _declared("bi_paged_controls.h") if n.startswith("bi_ctl_")]
     assert len(declared) == 10
