@@ -817,8 +817,8 @@ class BiQkRope:
         _check_tensor("q_pos", q_pos, i32, (T,), index)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
         if q_out is None:
-            q_out = _new_output(lambda: _torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device), stream,
-                                qkv.device)
+            make = lambda: _torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device)
+            q_out = make() if stream is None else _new_output(make, stream, qkv.device)
         else:
             _check_tensor("q_out", q_out, bf16, (T, self.Hq, self.D), index)
         _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), angles[0],
