@@ -12,12 +12,12 @@
 // by tcgen05.mma (128 positions or dimensions on its rows, the columns on its N) where they use
 // mma.sync m16n8k16.  The two instructions accumulate a step of sixteen alike: measured, no bit of
 // 6.5 million sums of 64 to 4096 products differed, over normal, wide-range, cancelling and
-// denormal inputs, and the tests hold whole calls to it.
+// denormal inputs, and the tests hold whole calls to it on such inputs.
 //
 // Bound: for many tokens the tensor cores (6 D operations per query row and key, a third of them for
 // the weights' low part) and the softmax's instructions, for few the load of the prefix.  Measured at
 // 32/8 heads of 128: 64 tokens behind 8192 positions 61 us for the whole call (bi_attention_run 308), of
-// which the groups' units alone 32; 256 tokens behind 16384 348 us (2319), units alone 177.
+// which the groups' units alone 32; 256 tokens behind 16384 350 us (2319), units alone 177.
 //
 // Warps (640 threads, one block per SM): 0 loads (queries, then K1 .. K(n-1), K0, V0 .. V(n-1)
 // through a ring), 1 issues the MMAs, 2 and 3 check that the group's page tables agree, 4 - 19
@@ -60,7 +60,7 @@ constexpr int kPlanTokens = 1024;             // tokens (and groups) that the pl
 // records of all other units in the form that the attention kernels read.  Bound by latency: what the
 // first 1024 tokens and groups say is loaded at once, the rest works from shared memory, and a warp
 // writes one token's records at a time.  (With groups read when they were met and a token's records
-// written by the warp that scanned it, a call of 64 tokens behind a prefix of 8192 took 65.8 us, now 60.9.)
+// written by the warp that scanned it, a call of 64 tokens behind a prefix of 8192 took 65.8 us, then 60.9.)
 __global__ void __launch_bounds__(1024) plan_shared_kernel(const SharedParams sp) {
   __shared__ int32_t warp_sums[32];
   __shared__ int32_t carry;

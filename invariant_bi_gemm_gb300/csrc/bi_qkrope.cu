@@ -4,8 +4,8 @@
 //
 // Bound: HBM bandwidth (every element read once, written once) beside the instructions, about eight
 // operations an element; one launch's latency for a few tokens.  Measured at 32/8 heads of 128: 1 token
-// 2.8 us, 64 tokens 2.9, 8192 tokens 42 (206 MB: 4.9 TB/s, 0.73 of a plain copy's rate).  A head of D elements belongs to D / 8
-// lanes, eight elements each: two runs of four that are rotation partners (dimensions 4 j and
+// 3.0 us, 64 tokens 2.9, 8192 tokens 41.3 (206 MB: 5.0 TB/s, 0.74 of a plain copy's rate).  A head of D
+// elements belongs to D / 8 lanes, eight elements each: two runs of four that are rotation partners (dimensions 4 j and
 // 4 j + rot / 2 on), or eight neighbours for an interleaved handle, so that a rotation needs no other
 // lane and its arithmetic goes two values an instruction.  A token has a power of two of such lane
 // groups, each with up to kHeads heads at a time in registers: their loads are issued before the
