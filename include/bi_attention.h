@@ -38,7 +38,8 @@
  *     above max_pos) are caught by the kernels: the token's output is then undefined and
  *     bi_attention_get_device_error reports BI_GEMM_ERR_INVALID_ARG.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).  A handle is
- *     not thread-safe and must not be used on two streams at once.
+ *     not thread-safe and must not be used on two streams at once; captured calls of one handle
+ *     share its workspace, so their graphs must not run at the same time.
  */
 #ifndef BI_ATTENTION_H
 #define BI_ATTENTION_H

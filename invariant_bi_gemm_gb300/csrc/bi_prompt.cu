@@ -13,10 +13,11 @@
 // PFLOP/s, 0.82 to 0.84 of the measured dense peak), 24 prompts of 1 to 2000 tokens 271 to 273 us (1.16
 // PFLOP/s); 8192 tokens 344 us, 782 in pages of 12, whose rows are copied one by one; 8192 tokens of 32/8
 // heads of 64, with twice the exponentials per operation, 304 us (0.91 PFLOP/s).
-// Tile: 128 rows = 128 / G positions x the G query heads of a KV head, so a block of keys is loaded once for all its heads and a short chunk still fills rows.  A unit is two tiles (256 / G
-// positions) that share every key and value block and take turns: while one tile's softmax runs,
-// the tensor cores work for the other.  Tiles and blocks are cut at multiples of their size in the
-// request's own positions, so a row's arithmetic never depends on the chunk it came in.
+// Tile: 128 rows = 128 / G positions x the G query heads of a KV head, so a block of keys is loaded once
+// for all its heads and a short chunk still fills rows.  A unit is two tiles (256 / G positions) that
+// share every key and value block and take turns: while one tile's softmax runs, the tensor cores work
+// for the other.  Tiles and blocks are cut at multiples of their size in the request's own positions, so
+// a row's arithmetic never depends on the chunk it came in.
 //
 // Warps (384 threads, one block per SM; a unit each, or, where there are more, persistent blocks that take
 // planned units, longest first, from a counter):
