@@ -6,7 +6,10 @@
 //     P = 2^(s - m),   l += sum P,   O += bf16(P) V;     when m rises, l and O shrink by 2^(m_old - m)
 // and o = O / l.  One pass over keys and values; scores and weights never leave the SM.  m rises only
 // when a block's maximum passes it by more than 8 (a weight is then at most 2^8, and the product's
-// relative rounding is the same), so O is rescaled rarely.  The rule looks at the row alone.
+// relative rounding is the same), so O is rescaled rarely.  The rule looks at the row alone.  P is rounded
+// to bf16 for the product because the tensor cores take operands of 16 bits beside bf16 values: a second
+// part, as the decode keeps, would be half as many MMAs again in a kernel that they bound.  l sums P as it is, so
+// the error against 64 bits is 1.2 to 1.44 times that of weights of 32 bits.
 //
 // Bound: the tensor cores, 4 D operations per query row and key, beside 16-bit operands that stay on
 // chip.  Measured at 32/8 heads of 128: a prompt of 16384 tokens 1366 to 1406 us (1.56 to 1.61
