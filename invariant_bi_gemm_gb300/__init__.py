@@ -1,5 +1,5 @@
 """Python binding of the batch-invariant operators (libbi_gemm.so, C ABI in include/bi_gemm.h,
-bi_rmsnorm.h, bi_prenorm.h, bi_qkrope.h, bi_prompt.h and bi_attention.h).
+bi_rmsnorm.h, bi_prenorm.h, bi_qkrope.h, bi_prompt.h, bi_attention.h and bi_fp4.h).
 
 Argument marshalling only: every step of y = x·W (and of the other operators) runs in the CUDA kernels of
 ``csrc/``.  PyTorch supplies device memory and streams.  There is no CPU or
@@ -11,7 +11,7 @@ Low-level functions carry the C names (``bi_gemm_create``, ``bi_gemm_run``, ...,
 ``bi_rmsnorm_run``) and take raw device pointers; ``BiGemm``, ``BiRmsNorm``, ``BiPreNorm`` and,
 around one paged KV cache, ``BiQkRope`` (norm, rotation, append), ``BiPromptAttention`` and
 ``BiAttention`` (single tokens; ``run_shared`` for tokens behind a common prefix) wrap them for
-torch tensors.  Their calls run on `stream` (a torch stream or a cudaStream_t value; the current
+torch tensors, and so do ``BiQuant4`` and ``BiGemm4`` (matrices in 4 bits).  Their calls run on `stream` (a torch stream or a cudaStream_t value; the current
 stream for None); an output that a call makes itself is memory of that stream, and work of another one
 on it is ordered by the caller.
 """
@@ -28,6 +28,8 @@ BI_MXFP8E4M3_OUT_BF16 = 2
 BI_SCALES_NONE = 0
 BI_SCALES_E8M0_K32 = 1
 BI_GEMM_FLAG_STATIC_W = 1
+BI_MXFP4 = 0
+BI_NVFP4 = 1
 
 BI_GEMM_OK = 0
 BI_GEMM_ERR_INVALID_ARG = -1
@@ -58,6 +60,10 @@ QKROPE_EXPORTED_SYMBOLS = ("bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_d
 ATTENTION_EXPORTED_SYMBOLS = ("bi_attention_create", "bi_attention_run", "bi_attention_workspace_size",
                               "bi_attention_get_device_error", "bi_attention_get_config", "bi_attention_destroy",
                               "bi_attention_run_shared", "bi_attention_shared_workspace_size")
+# every symbol include/bi_fp4.h declares
+FP4_EXPORTED_SYMBOLS = ("bi_quant4_create", "bi_quant4_scale_bytes", "bi_quant4_run", "bi_quant4_expand",
+                        "bi_quant4_get_config", "bi_quant4_destroy", "bi_gemm4_create", "bi_gemm4_run",
+                        "bi_gemm4_get_device_error", "bi_gemm4_get_config", "bi_gemm4_destroy")
 
 
 class BiGemmError(RuntimeError):
@@ -110,6 +116,15 @@ class bi_prenorm_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("K", "N", "chunk", "splits", "tile_rows")]
 
 
+class bi_quant4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("K", "format", "block", "threads")]
+
+
+class bi_gemm4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("K", "N", "format", "out_f32", "tile_rows", "tile_cols", "stages",
+                                              "max_groups", "few_rows", "few_cols", "smem_bytes")]
+
+
 def _load() -> ctypes.CDLL:
     path = _build.lib_path("libbi_gemm.so")
     if not os.path.exists(path):
@@ -157,11 +172,22 @@ def _load() -> ctypes.CDLL:
     L.bi_prompt_get_device_error.argtypes = [P, P]
     L.bi_prompt_get_config.argtypes = [P, ctypes.POINTER(bi_prompt_config)]
     L.bi_prompt_destroy.argtypes = [P]
+    L.bi_quant4_create.argtypes = [ctypes.POINTER(P), I64, ctypes.c_int32, ctypes.c_float]
+    L.bi_quant4_scale_bytes.argtypes = [P, I64, ctypes.POINTER(ctypes.c_uint64)]
+    L.bi_quant4_run.argtypes = [P, P, I64, I64, P, P, P]
+    L.bi_quant4_expand.argtypes = [P, P, P, I64, P, P]
+    L.bi_quant4_get_config.argtypes = [P, ctypes.POINTER(bi_quant4_config)]
+    L.bi_quant4_destroy.argtypes = [P]
+    L.bi_gemm4_create.argtypes = [ctypes.POINTER(P), I64, I64, ctypes.c_int32, ctypes.c_int32]
+    L.bi_gemm4_run.argtypes = [P, P, P, I64, P, P, ctypes.c_float, P, P]
+    L.bi_gemm4_get_device_error.argtypes = [P, P]
+    L.bi_gemm4_get_config.argtypes = [P, ctypes.POINTER(bi_gemm4_config)]
+    L.bi_gemm4_destroy.argtypes = [P]
     for n in ("bi_gemm_create", "bi_gemm_create_ex", "bi_gemm_run", "bi_gemm_run_noalloc", "bi_gemm_run_gathered",
               "bi_gemm_get_device_error",
               "bi_gemm_destroy", "bi_gemm_get_config", "bi_gemm_workspace_size", "bi_gemm_version") + \
             RMSNORM_EXPORTED_SYMBOLS + ATTENTION_EXPORTED_SYMBOLS + PRENORM_EXPORTED_SYMBOLS + QKROPE_EXPORTED_SYMBOLS + \
-            PROMPT_EXPORTED_SYMBOLS:
+            PROMPT_EXPORTED_SYMBOLS + FP4_EXPORTED_SYMBOLS:
         getattr(L, n).restype = I32
     return L
 
@@ -438,6 +464,66 @@ def bi_prenorm_destroy(h: int) -> None:
     _check(library().bi_prenorm_destroy(ctypes.c_void_p(h)), "bi_prenorm_destroy")
 
 
+def bi_quant4_create(K: int, format: int, tensor_scale: float = 1.0) -> int:
+    """Returns the handle (an opaque integer); raises BiGemmError on refusal."""
+    h = ctypes.c_void_p()
+    _check(library().bi_quant4_create(ctypes.byref(h), int(K), int(format), float(tensor_scale)), "bi_quant4_create")
+    return h.value
+
+
+def bi_quant4_scale_bytes(h: int, M: int) -> int:
+    b = ctypes.c_uint64()
+    _check(library().bi_quant4_scale_bytes(ctypes.c_void_p(h), int(M), ctypes.byref(b)), "bi_quant4_scale_bytes")
+    return b.value
+
+
+def bi_quant4_run(h: int, x: int, M: int, x_stride: int, codes: int, scales: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_quant4_run(h, x, M, x_stride, codes, scales, stream), "bi_quant4_run")
+
+
+def bi_quant4_expand(h: int, codes: int, scales: int, M: int, y: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_quant4_expand(h, codes, scales, M, y, stream), "bi_quant4_expand")
+
+
+def bi_quant4_get_config(h: int) -> dict:
+    c = bi_quant4_config()
+    _check(library().bi_quant4_get_config(ctypes.c_void_p(h), ctypes.byref(c)), "bi_quant4_get_config")
+    return {n: getattr(c, n) for n, _ in bi_quant4_config._fields_}
+
+
+def bi_quant4_destroy(h: int) -> None:
+    _check(library().bi_quant4_destroy(ctypes.c_void_p(h)), "bi_quant4_destroy")
+
+
+def bi_gemm4_create(K: int, N: int, format: int, out_f32: bool = False) -> int:
+    """Returns the handle (an opaque integer); raises BiGemmError on refusal."""
+    h = ctypes.c_void_p()
+    _check(library().bi_gemm4_create(ctypes.byref(h), int(K), int(N), int(format), int(bool(out_f32))),
+           "bi_gemm4_create")
+    return h.value
+
+
+def bi_gemm4_run(h: int, x: int, sx: int, M: int, w: int, sw: int, alpha: float, y: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_gemm4_run(h, x, sx, M, w, sw, alpha, y, stream), "bi_gemm4_run")
+
+
+def bi_gemm4_get_device_error(h: int, stream: int = 0) -> int:
+    return library().bi_gemm4_get_device_error(ctypes.c_void_p(h), ctypes.c_void_p(stream))
+
+
+def bi_gemm4_get_config(h: int) -> dict:
+    c = bi_gemm4_config()
+    _check(library().bi_gemm4_get_config(ctypes.c_void_p(h), ctypes.byref(c)), "bi_gemm4_get_config")
+    return {n: getattr(c, n) for n, _ in bi_gemm4_config._fields_}
+
+
+def bi_gemm4_destroy(h: int) -> None:
+    _check(library().bi_gemm4_destroy(ctypes.c_void_p(h)), "bi_gemm4_destroy")
+
+
 # --------------------------------------------------------------------- torch wrappers
 
 _DTYPES = {"bf16": BI_BF16_OUT_BF16, "bf16_f32": BI_BF16_OUT_F32, "mxfp8": BI_MXFP8E4M3_OUT_BF16}
@@ -707,7 +793,7 @@ class _Torch:
 
     def __init__(self):
         import torch
-        self.bf16, self.f32, self.i32 = torch.bfloat16, torch.float32, torch.int32
+        self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
         self.empty, self.empty_like = torch.empty, torch.empty_like
         self.current_stream = torch._C._cuda_getCurrentRawStream
         self.current_device = torch.cuda.current_device
@@ -737,6 +823,16 @@ def _check_tensor(name: str, t, dtype, shape, index: int) -> None:
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
+
+
+def _take(name: str, t, dtype, shape, index: int, stream, device):
+    """The output t, checked, or a new one (made for `stream`) where it is None."""
+    if t is not None:
+        _check_tensor(name, t, dtype, shape, index)
+        return t
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    return _new_output(lambda: _torch.empty(shape, dtype=dtype, device=device), stream, device)
 
 
 def _check_cache(k_cache, v_cache, page_table, page_shape, index: int):
@@ -903,6 +999,133 @@ class BiPromptAttention:
             pass
 
 
+_FP4 = {"mxfp4": (BI_MXFP4, 32), "nvfp4": (BI_NVFP4, 16)}
+
+
+def _scale_tiles(rows: int, K: int, block: int):
+    """Shape of the scales of `rows` rows: tiles of 128 rows x 4 scales, row r's scale c at
+    [r // 128, c // 4, r % 32, r // 32 % 4, c % 4]."""
+    return (-(-rows // 128), K // (4 * block), 32, 4, 4)
+
+
+class BiQuant4:
+    """Rows of bf16 in 4 bits, on torch tensors (include/bi_fp4.h has the definition).
+
+    kind "mxfp4" (E2M1 codes, a power of two per 32 elements) or "nvfp4" (an E4M3 scale per 16, times the
+    constant tensor_scale).  run(x [M, K] bf16, rows may be strided) returns codes uint8 [M, K / 2] and
+    scales uint8 in tiles [ceil(M / 128), K / (4 block), 32, 4, 4] (the bytes of rows past M are left as they
+    were, undefined in new scales): the operands of BiGemm4.  expand() gives the values back as bf16.
+    """
+
+    def __init__(self, K: int, kind: str = "nvfp4", tensor_scale: float = 1.0):
+        if kind not in _FP4:
+            raise ValueError("kind: 'mxfp4' or 'nvfp4'")
+        self.K, self.kind, self.tensor_scale = int(K), kind, float(tensor_scale)
+        fmt, self.block = _FP4[kind]
+        self.handle = bi_quant4_create(self.K, fmt, self.tensor_scale)
+        self._device = _handle_device()
+
+    @property
+    def config(self) -> dict:
+        return bi_quant4_get_config(self.handle)
+
+    def run(self, x, codes=None, scales=None, stream=None):
+        shape, index, K = x.shape, x.get_device(), self.K
+        if len(shape) != 2 or shape[1] != K or x.dtype is not _torch.bf16 or index != self._device:
+            raise ValueError(f"x must be a bf16 tensor [M, {K}] on cuda:{self._device}")
+        M, stride = shape[0], K
+        if not x.is_contiguous():
+            stride, inner = x.stride()
+            if inner != 1 or stride < K:
+                raise ValueError("x rows must be contiguous and must not overlap")
+        codes = _take("codes", codes, _torch.u8, (M, K // 2), index, stream, x.device)
+        scales = _take("scales", scales, _torch.u8, _scale_tiles(M, K, self.block), index, stream, x.device)
+        _check(library().bi_quant4_run(self.handle, x.data_ptr(), M, stride, codes.data_ptr(), scales.data_ptr(),
+                                       _stream_of(stream, index)), "bi_quant4_run")
+        return codes, scales
+
+    __call__ = run
+
+    def expand(self, codes, scales, y=None, stream=None):
+        """The values [M, K] bf16 that codes and scales stand for."""
+        index = codes.get_device()
+        if len(codes.shape) != 2 or index != self._device:
+            raise ValueError(f"codes must be a tensor [M, K / 2] on cuda:{self._device}")
+        M = codes.shape[0]
+        _check_tensor("codes", codes, _torch.u8, (M, self.K // 2), index)
+        _check_tensor("scales", scales, _torch.u8, _scale_tiles(M, self.K, self.block), index)
+        y = _take("y", y, _torch.bf16, (M, self.K), index, stream, codes.device)
+        _check(library().bi_quant4_expand(self.handle, codes.data_ptr(), scales.data_ptr(), M, y.data_ptr(),
+                                          _stream_of(stream, index)), "bi_quant4_expand")
+        return y
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            bi_quant4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class BiGemm4:
+    """y = alpha x w^T of two matrices in 4 bits for fixed (K, N), on torch tensors (include/bi_fp4.h).
+
+    x [M, K / 2], w [N, K / 2] codes and sx, sw their scales in tiles, all uint8 as BiQuant4.run makes them (both
+    of this handle's kind); y [M, N] bf16 or, with out="f32", fp32.  alpha carries the tensor scales of "nvfp4".
+    """
+
+    def __init__(self, K: int, N: int, kind: str = "nvfp4", out: str = "bf16"):
+        if kind not in _FP4 or out not in ("bf16", "f32"):
+            raise ValueError("kind: 'mxfp4' or 'nvfp4'; out: 'bf16' or 'f32'")
+        self.K, self.N, self.kind, self.out = int(K), int(N), kind, out
+        fmt, self.block = _FP4[kind]
+        self.handle = bi_gemm4_create(self.K, self.N, fmt, out == "f32")
+        self._device = _handle_device()
+        self._w, self._sw = (self.N, self.K // 2), _scale_tiles(self.N, self.K, self.block)
+        self._dtype = _torch.f32 if out == "f32" else _torch.bf16
+
+    @property
+    def config(self) -> dict:
+        return bi_gemm4_get_config(self.handle)
+
+    def run(self, x, sx, w, sw, alpha: float = 1.0, y=None, stream=None):
+        index, u8 = x.get_device(), _torch.u8
+        if len(x.shape) != 2 or index != self._device:
+            raise ValueError(f"x must be a tensor [M, K / 2] on cuda:{self._device}")
+        M = x.shape[0]
+        _check_tensor("x", x, u8, (M, self.K // 2), index)
+        _check_tensor("sx", sx, u8, _scale_tiles(M, self.K, self.block), index)
+        _check_tensor("w", w, u8, self._w, index)
+        _check_tensor("sw", sw, u8, self._sw, index)
+        y = _take("y", y, self._dtype, (M, self.N), index, stream, x.device)
+        _check(library().bi_gemm4_run(self.handle, x.data_ptr(), sx.data_ptr(), M, w.data_ptr(), sw.data_ptr(), alpha,
+                                      y.data_ptr(), _stream_of(stream, index)), "bi_gemm4_run")
+        return y
+
+    __call__ = run
+
+    def device_error(self, stream=None) -> int:
+        s = 0
+        if stream is not None:
+            s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return bi_gemm4_get_device_error(self.handle, s)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            bi_gemm4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 class BiPreNorm:
     """mHC pre-norm projection y = RMSNorm(x) . W (fp32 out) on torch tensors: x [M, K] bf16,
     W [K, N] bf16 (a norm weight folded into W's rows)."""
@@ -949,6 +1172,9 @@ class BiPreNorm:
 
 
 __all__ = [
+    "BiQuant4", "bi_quant4_create", "bi_quant4_scale_bytes", "bi_quant4_run", "bi_quant4_expand", "bi_quant4_get_config",
+    "bi_quant4_destroy", "bi_quant4_config", "BiGemm4", "bi_gemm4_create", "bi_gemm4_run", "bi_gemm4_get_device_error",
+    "bi_gemm4_get_config", "bi_gemm4_destroy", "bi_gemm4_config", "FP4_EXPORTED_SYMBOLS", "BI_MXFP4", "BI_NVFP4",
     "BiPromptAttention", "bi_prompt_create", "bi_prompt_run", "bi_prompt_workspace_size", "bi_prompt_get_device_error",
     "bi_prompt_get_config", "bi_prompt_destroy", "bi_prompt_config", "PROMPT_EXPORTED_SYMBOLS",
     "BiQkRope", "bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",

@@ -1,0 +1,495 @@
+// bi_gemm4.cu — batch-invariant product of two matrices in 4 bits, y = alpha x w^T, for sm_103a (TMA, tcgen05
+// block-scaled MMAs, TMEM).  Implements the product of include/bi_fp4.h.
+//
+// Every element of y is summed by one sequence of tcgen05.mma instructions, 64 elements of K each, ascending: a
+// function of K alone.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+
+#include "../../include/bi_fp4.h"
+#include "attn_ptx.cuh"
+#include "fp4.cuh"
+
+#ifndef BI_GEMM_API
+#define BI_GEMM_API extern "C" __attribute__((visibility("default")))
+#endif
+
+namespace big4 {
+
+namespace ptx = bigemm::ptx;
+using biattn_tc::Sync;
+using biattn_tc::wait_bar;
+
+constexpr int kStageK = 256;              // elements of K a stage: one 128-byte swizzle row
+constexpr uint64_t kTimeoutNs = biattn_tc::kTimeoutNs;
+
+struct Params {
+  uint32_t* status;
+  int32_t M, N, K;
+  int32_t m_tiles, n_tiles, kblocks;
+  int32_t x_rows;           // rows of an x box
+  int32_t group_m;          // raster: M tiles of a group (N tiles vary slowest within it)
+  float alpha;
+  int32_t stall;            // failure injection (test controls only): nothing is loaded
+  uint64_t timeout_ns;
+};
+
+template <bool kNv>
+__device__ __forceinline__ void mma4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: E2M1 x E2M1, both along K, E8M0 or E4M3 scales.
+template <bool kNv>
+constexpr __host__ __device__ uint32_t idesc4(int M, int N) {
+  return (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (kNv ? 0u : 1u << 23) | (uint32_t(M >> 4) << 24);
+}
+
+// Matrix descriptors: rows of 128 bytes, 128-byte swizzle, groups of 8 rows 1024 bytes apart; a block of scales,
+// 32 rows of 16 bytes, no swizzle.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t a) { return biattn_tc::sdesc_sw128(a, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_scales(uint32_t a) {
+  return uint64_t((a & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (1ull << 46);
+}
+
+// ------------------------------------------------------------------ the form for many rows
+
+template <bool kNv_, bool kF32_>
+struct Wide {
+  static constexpr bool kNv = kNv_, kF32 = kF32_;
+  static constexpr int TM = 256, TN = 256;             // of y per CTA pair
+  static constexpr int TILES_K = kNv ? 4 : 2;          // scale tiles (of 4 scales) a stage
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
+  static constexpr int SFA_BYTES = TILES_K * 512, SFB_BYTES = 2 * TILES_K * 512;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int STAGES = 5;
+  static constexpr int SF_COLS = TILES_K * 12;         // TMEM columns of a stage's scales: x 4, w 8 a tile
+  static constexpr int SF_COL0 = TN;
+  static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "tensor memory");
+  static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, THREADS = 384;
+  static constexpr int OUT = kF32 ? 4 : 2;
+  static constexpr int STG_BYTES = 32 * 32 * OUT;
+  static constexpr int STG_BUFS = kF32 ? 1 : 2;
+  static constexpr int OFF_B = STAGES * A_BYTES;
+  static constexpr int OFF_SF = OFF_B + STAGES * B_BYTES;
+  static constexpr int OFF_STG = OFF_SF + STAGES * (SFA_BYTES + SFB_BYTES);
+  static_assert(OFF_STG % 1024 == 0, "swizzle atoms");
+  static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * STG_BUFS * STG_BYTES;
+  static constexpr int SMEM = OFF_BAR + (2 * STAGES + 3) * 8 + 16 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                const __grid_constant__ CUtensorMap msx, const __grid_constant__ CUtensorMap msw,
+                const __grid_constant__ CUtensorMap my, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };
+  const uint32_t tfull = bars + 16u * C::STAGES, tempty = tfull + 8, drain = tfull + 16;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + (2 * C::STAGES + 3) * 8);
+  volatile uint32_t* gave_up = misc + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int group = blockIdx.x / 2, groups = gridDim.x / 2, units = p.m_tiles * p.n_tiles;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(empty(s), 1);
+    }
+    ptx::mbar_init(tfull, 1);
+    ptx::mbar_init(tempty, 2 * C::EPI_WARPS);
+    ptx::mbar_init(drain, 1);
+    *gave_up = 0u;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(misc), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();                   // the peer's barriers are there and its TMEM is allocated
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const Sync sy{gave_up, p.status, p.timeout_ns};
+  auto place = [&](int u, int& m, int& n) {
+    // groups of group_m M tiles; within a group N slowest, so that the tiles in work share W
+    const int per = p.group_m * p.n_tiles, g = u / per, r = u - g * per;
+    const int gm = min(p.group_m, p.m_tiles - g * p.group_m);
+    n = r / gm;
+    m = g * p.group_m + (r - n * gm);
+  };
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- loads
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const uint32_t x_bytes = uint32_t(p.x_rows) * 128u + C::SFA_BYTES, w_bytes = C::B_BYTES + C::SFB_BYTES;
+    for (int u = group; u < units && ok; u += groups) {
+      int m, n;
+      place(u, m, n);
+      const int row0 = m * C::TM + int(rank) * 128, col0 = n * C::TN;
+      const bool mine = row0 < p.M, peers = m * C::TM + 128 < p.M;    // rows past M are not loaded
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!wait_bar(empty(s), ph ^ 1u, sy)) {
+          ok = false;
+          break;
+        }
+        if (!p.stall) {
+          const uint32_t fb = ptx::mapa_shared(full(s), 0);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), x_bytes * (peers ? 2u : 1u) + 2u * w_bytes);
+          const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
+          if (mine) {
+            ptx::tma_load_2d_pair(base + uint32_t(s) * C::A_BYTES, &mx, fb, kb * 128, row0);
+            ptx::tma_load_2d_pair(sf, &msx, fb, kb * (C::TILES_K * 64), row0 / 128);
+          }
+          ptx::tma_load_2d_pair(base + C::OFF_B + uint32_t(s) * C::B_BYTES, &mw, fb, kb * 128, col0 + int(rank) * 128);
+          ptx::tma_load_2d_pair(sf + C::SFA_BYTES, &msw, fb, kb * (C::TILES_K * 64), col0 / 128);
+        }
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---------------------------------------------------------------- products (leader)
+    int s = 0;
+    uint32_t ph = 0, tph = 0;
+    bool ok = true, issued = false;
+    for (int u = group; u < units && ok; u += groups) {
+      if (!wait_bar(tempty, tph ^ 1u, sy)) {
+        ok = false;
+        break;
+      }
+      tph ^= 1u;
+      ptx::tc_fence_after();
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!wait_bar(full(s), ph, sy)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t a = base + uint32_t(s) * C::A_BYTES, b = base + C::OFF_B + uint32_t(s) * C::B_BYTES;
+        const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
+        const uint32_t ta = tmem + C::SF_COL0 + uint32_t(s) * C::SF_COLS, tb = ta + C::TILES_K * 4;
+        // scales: x's tiles of this CTA's rows, w's of all 256 columns (a tile's halves side by side)
+#pragma unroll
+        for (int t = 0; t < C::TILES_K; ++t) {
+          ptx::tc_cp_32x128b_x4_pair(ta + 4u * t, desc_scales(sf + 512u * t));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            ptx::tc_cp_32x128b_x4_pair(tb + 8u * t + 4u * h,
+                                       desc_scales(sf + C::SFA_BYTES + uint32_t(h * C::TILES_K + t) * 512u));
+        }
+        const int steps = min(4, (p.K - kb * kStageK) / 64);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < steps) {
+            const int t = C::kNv ? k : k >> 1;
+            const uint32_t id = C::kNv ? 0u : uint32_t(k & 1) * 2u;
+            mma4_pair<C::kNv>(tmem, desc_rows(a + 32u * k), desc_rows(b + 32u * k),
+                              idesc4<C::kNv>(C::TM, C::TN) | (id << 4) | (id << 29), ta + 4u * t, tb + 8u * t,
+                              kb != 0 || k != 0 ? 1u : 0u);
+          }
+        }
+        issued = true;
+        ptx::tc_commit_pair_mc(empty(s), 0x3);
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+      if (ok) ptx::tc_commit_pair_mc(tfull, 0x3);
+    }
+    if (!ok && issued) {                 // what was issued ends before TMEM is released
+      ptx::tc_commit_pair_mc(drain, 0x1);
+      volatile uint32_t never = 0;
+      wait_bar(drain, 0u, Sync{&never, p.status, p.timeout_ns});
+    }
+  } else if (warp >= C::EPI_WARP0) {
+    // ---------------------------------------------------------------- results
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int e = warp - C::EPI_WARP0, q = warp & 3, half = e >> 2;
+    const uint32_t stg = base + C::OFF_STG + uint32_t(e) * (C::STG_BUFS * C::STG_BYTES);
+    uint32_t tph = 0;
+    int buf = 0;
+    for (int u = group; u < units; u += groups) {
+      int m, n;
+      place(u, m, n);
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(tfull, tph, sy))) break;
+      tph ^= 1u;
+      ptx::tc_fence_after();
+      const int row0 = m * C::TM + int(rank) * 128 + q * 32, col0 = n * C::TN + half * 128;
+      const int chunks = row0 < p.M ? max(0, min(4, (p.N - col0 + 31) / 32)) : 0;
+      uint32_t r[4][32];
+      const uint32_t from = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * 128);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < chunks) ptx::tmem_ld_32x32b_x32(from + 32u * c, r[c]);
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {                   // the accumulator is free (the leader waits for both CTAs)
+        ptx::fence_release_shared();
+        ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(tempty, 0));
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= chunks) continue;
+        const uint32_t dst = stg + uint32_t(buf) * C::STG_BYTES;
+        if (lane == 0) ptx::bulk_wait_read<C::STG_BUFS - 1>();
+        __syncwarp();
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = __fmul_rn(__uint_as_float(r[c][i]), p.alpha);
+        if constexpr (C::kF32) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            ptx::st_shared_v4(dst + lane * 128 + ((v ^ (lane & 7)) << 4), __float_as_uint(f[4 * v]),
+                              __float_as_uint(f[4 * v + 1]), __float_as_uint(f[4 * v + 2]), __float_as_uint(f[4 * v + 3]));
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            ptx::st_shared_v4(dst + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), ptx::pack_bf16x2(f[8 * v], f[8 * v + 1]),
+                              ptx::pack_bf16x2(f[8 * v + 2], f[8 * v + 3]), ptx::pack_bf16x2(f[8 * v + 4], f[8 * v + 5]),
+                              ptx::pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(&my, dst, col0 + c * 32, row0);
+          ptx::bulk_commit();
+        }
+        if (++buf == C::STG_BUFS) buf = 0;
+      }
+    }
+    if (lane == 0) ptx::bulk_wait_read<0>();
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *gave_up) {    // let every copy in flight land before the block leaves
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 2000000ull) {
+    }
+  }
+  __syncwarp();
+  ptx::cluster_sync();                   // neither CTA leaves while the pair still works
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// A matrix of `rows` x `cols` elements, rows `pitch` bytes apart, in boxes of box_rows x box_cols.
+bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* at, uint64_t rows, uint64_t cols, uint64_t pitch,
+            uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+  auto fn = biattn_tc::encode_fn();
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_cols, box_rows}, ones[2] = {1, 1};
+  return fn && fn(m, type, 2, const_cast<void*>(at), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Kernel {
+  const void* wide = nullptr;
+  int wide_smem = 0, stages = 0, tiles_k = 0;
+};
+template <bool kNv, bool kF32>
+Kernel kernel() {
+  using W = Wide<kNv, kF32>;
+  Kernel k;
+  k.wide = reinterpret_cast<const void*>(&wide_kernel<W>);
+  k.wide_smem = W::SMEM;
+  k.stages = W::STAGES;
+  k.tiles_k = W::TILES_K;
+  return k;
+}
+inline Kernel select(bool nv, bool f32) {
+  if (nv) return f32 ? kernel<true, true>() : kernel<true, false>();
+  return f32 ? kernel<false, true>() : kernel<false, false>();
+}
+
+}  // namespace big4
+
+struct bi_gemm4 {
+  int64_t K = 0, N = 0;
+  bool nv = false, f32 = false;
+  int device = 0, max_groups = 0;
+  big4::Kernel kern;
+  uint32_t* d_status = nullptr;
+};
+
+BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t format, int32_t out_f32) {
+  if (!out) return BI_GEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (K <= 0 || N <= 0 || (format != BI_MXFP4 && format != BI_NVFP4) || out_f32 < 0 || out_f32 > 1)
+    return BI_GEMM_ERR_INVALID_ARG;
+  if (K % 128 != 0 || K > (1 << 24) || N % 8 != 0 || N > (1 << 24)) return BI_GEMM_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (const int rc = bifp4::check_device(&dev)) return rc;
+  if (!biattn_tc::encode_fn()) return BI_GEMM_ERR_CUDA;
+  const big4::Kernel k = big4::select(format == BI_NVFP4, out_f32 != 0);
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaFuncSetAttribute(k.wide, cudaFuncAttributeMaxDynamicSharedMemorySize, k.wide_smem) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  bi_gemm4* h = new (std::nothrow) bi_gemm4();
+  if (!h) return BI_GEMM_ERR_OOM;
+  h->K = K;
+  h->N = N;
+  h->nv = format == BI_NVFP4;
+  h->f32 = out_f32 != 0;
+  h->device = dev;
+  h->kern = k;
+  // pairs that are resident at once (a pair needs two SMs of one cluster)
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(unsigned(sms / 2 * 2));
+  cfg.blockDim = dim3(384);
+  cfg.dynamicSmemBytes = size_t(k.wide_smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, k.wide, &cfg) != cudaSuccess || clusters < 1 ||
+      cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
+      cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
+    cudaGetLastError();
+    if (h->d_status) cudaFree(h->d_status);
+    delete h;
+    return BI_GEMM_ERR_CUDA;
+  }
+  h->max_groups = clusters;
+  *out = h;
+  return BI_GEMM_OK;
+}
+
+namespace {
+
+// bi_gemm4_run with the failure injection of the test controls (stall: nothing is loaded) and the limit of
+// the waits.
+int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void* w, const void* sw, float alpha, void* y,
+              void* stream, int32_t stall, uint64_t timeout_ns) {
+  if (!h || M < 0 || !std::isfinite(alpha)) return BI_GEMM_ERR_INVALID_ARG;
+  if (M == 0) return BI_GEMM_OK;
+  if (!x || !sx || !w || !sw || !y) return BI_GEMM_ERR_INVALID_ARG;
+  if (M >= (int64_t(1) << 31) - 256) return BI_GEMM_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(sx) | reinterpret_cast<uintptr_t>(w) |
+       reinterpret_cast<uintptr_t>(sw) | reinterpret_cast<uintptr_t>(y)) & 15u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
+  const int64_t m_tiles = (M + 255) / 256, n_tiles = (h->N + 255) / 256;
+  if (m_tiles * n_tiles >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  big4::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.status = h->d_status;
+  p.M = int32_t(M);
+  p.N = int32_t(h->N);
+  p.K = int32_t(h->K);
+  p.m_tiles = int32_t(m_tiles);
+  p.n_tiles = int32_t(n_tiles);
+  p.kblocks = int32_t((h->K + big4::kStageK - 1) / big4::kStageK);
+  p.x_rows = int32_t(std::min<int64_t>(128, (M + 7) / 8 * 8));
+  p.group_m = 16;
+  p.alpha = alpha;
+  p.stall = stall;
+  p.timeout_ns = timeout_ns;
+  const uint64_t tiles = uint64_t(h->K) / (h->nv ? 64 : 128);     // scale tiles of a row of tiles
+  const uint32_t tiles_k = uint32_t(h->kern.tiles_k);
+  CUtensorMap mx, mw, msx, msw, my;
+  using namespace big4;
+  if (!encode(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, uint64_t(M), uint64_t(h->K / 2), uint64_t(h->K / 2),
+              uint32_t(p.x_rows), 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, uint64_t(h->N), uint64_t(h->K / 2), uint64_t(h->K / 2), 128, 128,
+              CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode(&msx, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, sx, uint64_t((M + 127) / 128), tiles * 64, tiles * 512, 1,
+              tiles_k * 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode(&msw, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, sw, uint64_t((h->N + 127) / 128), tiles * 64, tiles * 512, 2,
+              tiles_k * 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode(&my, h->f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, uint64_t(M),
+              uint64_t(h->N), uint64_t(h->N) * (h->f32 ? 4 : 2), 32, 32,
+              h->f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return BI_GEMM_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(m_tiles * n_tiles, h->max_groups)));
+  cfg.blockDim = dim3(384);
+  cfg.dynamicSmemBytes = size_t(h->kern.wide_smem);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[6] = {&mx, &mw, &msx, &msw, &my, &p};
+  if (cudaLaunchKernelExC(&cfg, h->kern.wide, args) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  return BI_GEMM_OK;
+}
+
+}  // namespace
+
+BI_GEMM_API int bi_gemm4_run(bi_gemm4_t h, const void* x, const void* sx, int64_t M, const void* w, const void* sw,
+                             float alpha, void* y, void* stream) {
+  return gemm4_run(h, x, sx, M, w, sw, alpha, y, stream, 0, big4::kTimeoutNs);
+}
+
+BI_GEMM_API int bi_gemm4_get_device_error(bi_gemm4_t h, void* stream) {
+  if (!h) return BI_GEMM_ERR_INVALID_ARG;
+  return bifp4::read_status(h->d_status, static_cast<cudaStream_t>(stream), biattn_tc::kErrTimeout);
+}
+
+BI_GEMM_API int bi_gemm4_get_config(bi_gemm4_t h, bi_gemm4_config* c) {
+  if (!h || !c) return BI_GEMM_ERR_INVALID_ARG;
+  std::memset(c, 0, sizeof(*c));
+  c->K = int32_t(h->K);
+  c->N = int32_t(h->N);
+  c->format = h->nv ? BI_NVFP4 : BI_MXFP4;
+  c->out_f32 = h->f32;
+  c->tile_rows = c->tile_cols = 256;
+  c->stages = h->kern.stages;
+  c->max_groups = h->max_groups;
+  c->smem_bytes = h->kern.wide_smem;
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_gemm4_destroy(bi_gemm4_t h) {
+  if (!h) return BI_GEMM_OK;
+  if (h->d_status) cudaFree(h->d_status);
+  delete h;
+  return BI_GEMM_OK;
+}
