@@ -76,6 +76,18 @@ int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride,
                   void* k_cache, void* v_cache, int64_t num_pages, const int32_t* page_table, int64_t num_seqs,
                   int64_t max_pages, void* q_out, void* stream);
 
+/* bi_qkrope_run into a cache in 4 bits, the layout that bi_attention4.h reads (q_out is bi_qkrope_run's):
+ * a key head, rounded to bf16 as above, and a value head are quantised in the BI_NVFP4 format of bi_fp4.h with the
+ * tensor scales k_scale and v_scale (in [2^-64, 2^64], else BI_GEMM_ERR_INVALID_ARG) and go to the slot's rows of
+ * k_codes, v_codes [num_pages, page_size, Hkv, D / 2] and k_scales, v_scales [num_pages, page_size, Hkv, D / 16]
+ * (uint8, 16-byte aligned).  So the cache holds the quantised rows of the one that bi_qkrope_run would fill, bit
+ * for bit.  Two tokens of one call on the same slot leave it with pieces of either. */
+int bi_qkrope_run4(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq, const void* gk,
+                   const float* cos_sin, int64_t num_positions, const int32_t* q_seq, const int32_t* q_pos,
+                   void* k_codes, void* k_scales, void* v_codes, void* v_scales, float k_scale, float v_scale,
+                   int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages, void* q_out,
+                   void* stream);
+
 /* Synchronise `stream`; BI_GEMM_ERR_TIMEOUT if a bounded wait (2 s) expired, else
  * BI_GEMM_ERR_INVALID_ARG if a kernel caught a bad input, since the last call (the status is then
  * cleared); BI_GEMM_ERR_CUDA if synchronisation failed; else BI_GEMM_OK. */

@@ -1,5 +1,5 @@
 """Python binding of the batch-invariant operators (libbi_gemm.so, C ABI in include/bi_gemm.h,
-bi_rmsnorm.h, bi_prenorm.h, bi_qkrope.h, bi_prompt.h, bi_attention.h and bi_fp4.h).
+bi_rmsnorm.h, bi_prenorm.h, bi_qkrope.h, bi_prompt.h, bi_attention.h, bi_fp4.h and bi_attention4.h).
 
 Argument marshalling only: every step of y = x·W (and of the other operators) runs in the CUDA kernels of
 ``csrc/``.  PyTorch supplies device memory and streams.  There is no CPU or
@@ -11,7 +11,8 @@ Low-level functions carry the C names (``bi_gemm_create``, ``bi_gemm_run``, ...,
 ``bi_rmsnorm_run``) and take raw device pointers; ``BiGemm``, ``BiRmsNorm``, ``BiPreNorm`` and,
 around one paged KV cache, ``BiQkRope`` (norm, rotation, append), ``BiPromptAttention`` and
 ``BiAttention`` (single tokens; ``run_shared`` for tokens behind a common prefix) wrap them for
-torch tensors, and so do ``BiQuant4`` and ``BiGemm4`` (matrices in 4 bits).  Their calls run on `stream` (a torch stream or a cudaStream_t value; the current
+torch tensors, and so do, in 4 bits, ``BiQuant4`` and ``BiGemm4`` (matrices), ``BiQkRope.run4`` and
+``BiAttention4`` (the cache).  Their calls run on `stream` (a torch stream or a cudaStream_t value; the current
 stream for None); an output that a call makes itself is memory of that stream, and work of another one
 on it is ordered by the caller.
 """
@@ -55,7 +56,7 @@ PROMPT_EXPORTED_SYMBOLS = ("bi_prompt_create", "bi_prompt_run", "bi_prompt_works
                            "bi_prompt_get_device_error", "bi_prompt_get_config", "bi_prompt_destroy")
 # every symbol include/bi_qkrope.h declares
 QKROPE_EXPORTED_SYMBOLS = ("bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",
-                           "bi_qkrope_destroy")
+                           "bi_qkrope_destroy", "bi_qkrope_run4")
 # every symbol include/bi_attention.h declares
 ATTENTION_EXPORTED_SYMBOLS = ("bi_attention_create", "bi_attention_run", "bi_attention_workspace_size",
                               "bi_attention_get_device_error", "bi_attention_get_config", "bi_attention_destroy",
@@ -64,6 +65,11 @@ ATTENTION_EXPORTED_SYMBOLS = ("bi_attention_create", "bi_attention_run", "bi_att
 FP4_EXPORTED_SYMBOLS = ("bi_quant4_create", "bi_quant4_scale_bytes", "bi_quant4_run", "bi_quant4_expand",
                         "bi_quant4_get_config", "bi_quant4_destroy", "bi_gemm4_create", "bi_gemm4_run",
                         "bi_gemm4_get_device_error", "bi_gemm4_get_config", "bi_gemm4_destroy")
+
+# every symbol include/bi_attention4.h declares
+ATTENTION4_EXPORTED_SYMBOLS = ("bi_attention4_create", "bi_attention4_run", "bi_attention4_workspace_size",
+                               "bi_attention4_expand", "bi_attention4_get_device_error", "bi_attention4_get_config",
+                               "bi_attention4_destroy")
 
 
 class BiGemmError(RuntimeError):
@@ -125,6 +131,11 @@ class bi_gemm4_config(ctypes.Structure):
                                               "max_groups", "few_rows", "few_cols", "smem_bytes")]
 
 
+class bi_attention4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_q_heads", "num_kv_heads", "head_dim", "page_size", "split_size",
+                                              "threads", "max_ctas", "tokens_per_launch")]
+
+
 def _load() -> ctypes.CDLL:
     path = _build.lib_path("libbi_gemm.so")
     if not os.path.exists(path):
@@ -183,11 +194,20 @@ def _load() -> ctypes.CDLL:
     L.bi_gemm4_get_device_error.argtypes = [P, P]
     L.bi_gemm4_get_config.argtypes = [P, ctypes.POINTER(bi_gemm4_config)]
     L.bi_gemm4_destroy.argtypes = [P]
+    F = ctypes.c_float
+    L.bi_qkrope_run4.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, P, P, P, P, F, F, I64, P, I64, I64, P, P]
+    L.bi_attention4_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, F, F, F, I64]
+    L.bi_attention4_run.argtypes = [P, P, I64, P, P, P, P, P, P, I64, P, I64, I64, I64, P, P]
+    L.bi_attention4_workspace_size.argtypes = [P, I64, I64, ctypes.POINTER(ctypes.c_uint64)]
+    L.bi_attention4_expand.argtypes = [P, P, P, P, P, I64, P, I64, P, P, P]
+    L.bi_attention4_get_device_error.argtypes = [P, P]
+    L.bi_attention4_get_config.argtypes = [P, ctypes.POINTER(bi_attention4_config)]
+    L.bi_attention4_destroy.argtypes = [P]
     for n in ("bi_gemm_create", "bi_gemm_create_ex", "bi_gemm_run", "bi_gemm_run_noalloc", "bi_gemm_run_gathered",
               "bi_gemm_get_device_error",
               "bi_gemm_destroy", "bi_gemm_get_config", "bi_gemm_workspace_size", "bi_gemm_version") + \
             RMSNORM_EXPORTED_SYMBOLS + ATTENTION_EXPORTED_SYMBOLS + PRENORM_EXPORTED_SYMBOLS + QKROPE_EXPORTED_SYMBOLS + \
-            PROMPT_EXPORTED_SYMBOLS + FP4_EXPORTED_SYMBOLS:
+            PROMPT_EXPORTED_SYMBOLS + FP4_EXPORTED_SYMBOLS + ATTENTION4_EXPORTED_SYMBOLS:
         getattr(L, n).restype = I32
     return L
 
@@ -391,6 +411,16 @@ def bi_qkrope_run(h: int, qkv: int, T: int, qkv_stride: int, gq: int | None, gk:
     _check(rc, "bi_qkrope_run")
 
 
+def bi_qkrope_run4(h: int, qkv: int, T: int, qkv_stride: int, gq: int | None, gk: int | None, cos_sin: int,
+                   num_positions: int, q_seq: int, q_pos: int, k_codes: int, k_scales: int, v_codes: int, v_scales: int,
+                   k_scale: float, v_scale: float, num_pages: int, page_table: int, num_seqs: int, max_pages: int,
+                   q_out: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_qkrope_run4(h, qkv, T, qkv_stride, gq, gk, cos_sin, num_positions, q_seq, q_pos, k_codes, k_scales,
+                                    v_codes, v_scales, k_scale, v_scale, num_pages, page_table, num_seqs, max_pages,
+                                    q_out, stream), "bi_qkrope_run4")
+
+
 def bi_qkrope_get_device_error(h: int, stream: int = 0) -> int:
     return library().bi_qkrope_get_device_error(ctypes.c_void_p(h), ctypes.c_void_p(stream))
 
@@ -462,6 +492,52 @@ def bi_prenorm_get_config(h: int) -> dict:
 
 def bi_prenorm_destroy(h: int) -> None:
     _check(library().bi_prenorm_destroy(ctypes.c_void_p(h)), "bi_prenorm_destroy")
+
+
+def bi_attention4_create(num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, scale: float,
+                         k_scale: float = 1.0, v_scale: float = 1.0, split_size: int = 0) -> int:
+    """Returns the handle (an opaque integer); raises BiGemmError on refusal."""
+    h = ctypes.c_void_p()
+    _check(library().bi_attention4_create(ctypes.byref(h), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                          int(page_size), float(scale), float(k_scale), float(v_scale),
+                                          int(split_size)), "bi_attention4_create")
+    return h.value
+
+
+def bi_attention4_run(h: int, q: int, T: int, q_seq: int, q_pos: int, k_codes: int, k_scales: int, v_codes: int,
+                      v_scales: int, num_pages: int, page_table: int, num_seqs: int, max_pages: int, max_pos: int,
+                      o: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_attention4_run(h, q, T, q_seq, q_pos, k_codes, k_scales, v_codes, v_scales, num_pages, page_table,
+                                       num_seqs, max_pages, max_pos, o, stream), "bi_attention4_run")
+
+
+def bi_attention4_workspace_size(h: int, T: int, max_pos: int) -> int:
+    b = ctypes.c_uint64()
+    _check(library().bi_attention4_workspace_size(ctypes.c_void_p(h), int(T), int(max_pos), ctypes.byref(b)),
+           "bi_attention4_workspace_size")
+    return b.value
+
+
+def bi_attention4_expand(h: int, k_codes: int, k_scales: int, v_codes: int, v_scales: int, num_pages: int, pages: int,
+                         n: int, k_out: int, v_out: int, stream: int) -> None:
+    """Raw-pointer call (device addresses, stream a cudaStream_t value)."""
+    _check(library().bi_attention4_expand(h, k_codes, k_scales, v_codes, v_scales, num_pages, pages, n, k_out, v_out,
+                                          stream), "bi_attention4_expand")
+
+
+def bi_attention4_get_device_error(h: int, stream: int = 0) -> int:
+    return library().bi_attention4_get_device_error(ctypes.c_void_p(h), ctypes.c_void_p(stream))
+
+
+def bi_attention4_get_config(h: int) -> dict:
+    c = bi_attention4_config()
+    _check(library().bi_attention4_get_config(ctypes.c_void_p(h), ctypes.byref(c)), "bi_attention4_get_config")
+    return {n: getattr(c, n) for n, _ in bi_attention4_config._fields_}
+
+
+def bi_attention4_destroy(h: int) -> None:
+    _check(library().bi_attention4_destroy(ctypes.c_void_p(h)), "bi_attention4_destroy")
 
 
 def bi_quant4_create(K: int, format: int, tensor_scale: float = 1.0) -> int:
@@ -850,6 +926,31 @@ def _check_cache(k_cache, v_cache, page_table, page_shape, index: int):
     return shape[0], table[0], table[1]
 
 
+def _check_codes(k_codes, k_scales, v_codes, v_scales, page_shape, index: int) -> int:
+    """The paged cache of one layer in 4 bits: codes [pages, page_size, Hkv, D / 2] and scales [.., D / 16], uint8.
+    Returns its pages."""
+    page, heads, D = page_shape
+    shape, u8 = k_codes.shape, _torch.u8
+    if len(shape) != 4 or shape[1:] != (page, heads, D // 2):
+        raise ValueError(f"k_codes must be [pages, page_size, num_kv_heads, head_dim / 2] = [pages, {page}, {heads}, {D // 2}]")
+    scales = (shape[0], page, heads, D // 16)
+    _check_tensor("k_codes", k_codes, u8, shape, index)
+    _check_tensor("v_codes", v_codes, u8, shape, index)
+    _check_tensor("k_scales", k_scales, u8, scales, index)
+    _check_tensor("v_scales", v_scales, u8, scales, index)
+    return shape[0]
+
+
+def _check_cache4(k_codes, k_scales, v_codes, v_scales, page_table, page_shape, index: int):
+    """_check_cache for a cache in 4 bits."""
+    pages = _check_codes(k_codes, k_scales, v_codes, v_scales, page_shape, index)
+    table = page_table.shape
+    if len(table) != 2:
+        raise ValueError("page_table must be [num_seqs, max_pages]")
+    _check_tensor("page_table", page_table, _torch.i32, table, index)
+    return pages, table[0], table[1]
+
+
 def _check_queries(q, o, Hq: int, D: int, device: int, stream):
     """q [T, Hq, D] bf16 and o like it (made for `stream` where it is None) on the handle's device.
     Returns (T, device index, o)."""
@@ -886,7 +987,9 @@ class BiQkRope:
     def config(self) -> dict:
         return bi_qkrope_get_config(self.handle)
 
-    def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
+    def _rows(self, qkv, gq, gk, cos_sin, q_seq, q_pos, q_out, stream):
+        """The arguments that say nothing of the cache, checked: (device index, tokens, row stride, gq, gk, positions,
+        q_out)."""
         bf16, i32 = _torch.bf16, _torch.i32
         shape, index, width = qkv.shape, qkv.get_device(), self._width
         if len(shape) != 2 or shape[1] != width or qkv.dtype is not bf16 or index != self._device:
@@ -911,16 +1014,29 @@ class BiQkRope:
         _check_tensor("cos_sin", cos_sin, _torch.f32, angles, index)
         _check_tensor("q_seq", q_seq, i32, (T,), index)
         _check_tensor("q_pos", q_pos, i32, (T,), index)
+        q_out = _take("q_out", q_out, bf16, (T, self.Hq, self.D), index, stream, qkv.device)
+        return index, T, stride, wq, wk, angles[0], q_out
+
+    def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
+        index, T, stride, wq, wk, positions, q_out = self._rows(qkv, gq, gk, cos_sin, q_seq, q_pos, q_out, stream)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
-        if q_out is None:
-            make = lambda: _torch.empty((T, self.Hq, self.D), dtype=bf16, device=qkv.device)
-            q_out = make() if stream is None else _new_output(make, stream, qkv.device)
-        else:
-            _check_tensor("q_out", q_out, bf16, (T, self.Hq, self.D), index)
-        _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), angles[0],
+        _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions,
                                        q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                        pages, page_table.data_ptr(), seqs, per, q_out.data_ptr(),
                                        _stream_of(stream, index)), "bi_qkrope_run")
+        return q_out
+
+    def run4(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_codes, k_scales, v_codes, v_scales, page_table,
+             k_scale: float = 1.0, v_scale: float = 1.0, q_out=None, stream=None):
+        """run() into a cache in 4 bits (BiAttention4's): keys and values quantised with the tensor scales k_scale
+        and v_scale, the codes and scales that BiQuant4 "nvfp4" gives the rows that run() would store."""
+        index, T, stride, wq, wk, positions, q_out = self._rows(qkv, gq, gk, cos_sin, q_seq, q_pos, q_out, stream)
+        pages, seqs, per = _check_cache4(k_codes, k_scales, v_codes, v_scales, page_table, self._page_shape, index)
+        _check(library().bi_qkrope_run4(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions,
+                                        q_seq.data_ptr(), q_pos.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(),
+                                        v_codes.data_ptr(), v_scales.data_ptr(), k_scale, v_scale, pages,
+                                        page_table.data_ptr(), seqs, per, q_out.data_ptr(), _stream_of(stream, index)),
+               "bi_qkrope_run4")
         return q_out
 
     __call__ = run
@@ -990,6 +1106,78 @@ class BiPromptAttention:
     def close(self) -> None:
         if getattr(self, "handle", None):
             bi_prompt_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class BiAttention4:
+    """Batch-invariant decode attention over a paged KV cache in 4 bits, on torch tensors (include/bi_attention4.h).
+
+    q [T, Hq, D] bf16; k_codes, v_codes [pages, page_size, Hkv, D / 2] and k_scales, v_scales [pages, page_size, Hkv,
+    D / 16] uint8, filled by BiQkRope.run4; k_scale, v_scale: the tensor scales they were made with; page_table
+    int32 [num_seqs, max_pages]; q_seq, q_pos int32 [T] (request and position of each query token; a token at
+    -1 sees nothing and gets zeros).  max_pos: an upper bound of every position.
+    """
+
+    def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, scale: float | None = None,
+                 k_scale: float = 1.0, v_scale: float = 1.0, split_size: int = 0):
+        self.Hq, self.Hkv, self.D, self.page_size = int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size)
+        self.scale = float(scale) if scale is not None else float(head_dim) ** -0.5
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self._page_shape = (self.page_size, self.Hkv, self.D)
+        self.handle = bi_attention4_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale, self.k_scale,
+                                           self.v_scale, split_size)
+        self._device = _handle_device()
+
+    @property
+    def config(self) -> dict:
+        return bi_attention4_get_config(self.handle)
+
+    def run(self, q, q_seq, q_pos, k_codes, k_scales, v_codes, v_scales, page_table, max_pos: int, o=None, stream=None):
+        T, index, o = _check_queries(q, o, self.Hq, self.D, self._device, stream)
+        pages, seqs, per = _check_cache4(k_codes, k_scales, v_codes, v_scales, page_table, self._page_shape, index)
+        _check_tensor("q_seq", q_seq, _torch.i32, (T,), index)
+        _check_tensor("q_pos", q_pos, _torch.i32, (T,), index)
+        _check(library().bi_attention4_run(self.handle, q.data_ptr(), T, q_seq.data_ptr(), q_pos.data_ptr(),
+                                           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                           v_scales.data_ptr(), pages, page_table.data_ptr(), seqs, per, max_pos,
+                                           o.data_ptr(), _stream_of(stream, index)), "bi_attention4_run")
+        return o
+
+    __call__ = run
+
+    def expand(self, k_codes, k_scales, v_codes, v_scales, pages, k=None, v=None, stream=None):
+        """The values k, v [n, page_size, Hkv, D] bf16 of the cache's pages `pages` (int32 [n]; page i of the result
+        is left as it was, undefined in a new one, where the entry is -1)."""
+        index, n = k_codes.get_device(), pages.shape[0]
+        if index != self._device:
+            raise ValueError(f"k_codes must be a tensor on cuda:{self._device}")
+        count = _check_codes(k_codes, k_scales, v_codes, v_scales, self._page_shape, index)
+        _check_tensor("pages", pages, _torch.i32, (n,), index)
+        k = _take("k", k, _torch.bf16, (n, *self._page_shape), index, stream, k_codes.device)
+        v = _take("v", v, _torch.bf16, (n, *self._page_shape), index, stream, k_codes.device)
+        _check(library().bi_attention4_expand(self.handle, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                              v_scales.data_ptr(), count, pages.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                              _stream_of(stream, index)), "bi_attention4_expand")
+        return k, v
+
+    def device_error(self, stream=None) -> int:
+        s = 0
+        if stream is not None:
+            s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return bi_attention4_get_device_error(self.handle, s)
+
+    def workspace_size(self, T: int, max_pos: int) -> int:
+        return bi_attention4_workspace_size(self.handle, T, max_pos)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            bi_attention4_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
@@ -1175,6 +1363,9 @@ __all__ = [
     "BiQuant4", "bi_quant4_create", "bi_quant4_scale_bytes", "bi_quant4_run", "bi_quant4_expand", "bi_quant4_get_config",
     "bi_quant4_destroy", "bi_quant4_config", "BiGemm4", "bi_gemm4_create", "bi_gemm4_run", "bi_gemm4_get_device_error",
     "bi_gemm4_get_config", "bi_gemm4_destroy", "bi_gemm4_config", "FP4_EXPORTED_SYMBOLS", "BI_MXFP4", "BI_NVFP4",
+    "BiAttention4", "bi_attention4_create", "bi_attention4_run", "bi_attention4_workspace_size", "bi_attention4_expand",
+    "bi_attention4_get_device_error", "bi_attention4_get_config", "bi_attention4_destroy", "bi_attention4_config",
+    "ATTENTION4_EXPORTED_SYMBOLS", "bi_qkrope_run4",
     "BiPromptAttention", "bi_prompt_create", "bi_prompt_run", "bi_prompt_workspace_size", "bi_prompt_get_device_error",
     "bi_prompt_get_config", "bi_prompt_destroy", "bi_prompt_config", "PROMPT_EXPORTED_SYMBOLS",
     "BiQkRope", "bi_qkrope_create", "bi_qkrope_run", "bi_qkrope_get_device_error", "bi_qkrope_get_config",

@@ -2,7 +2,8 @@
 
 Produces, under ``invariant_bi_gemm_gb300/_build/``:
   libbi_gemm.so           the product (C ABI of include/bi_gemm.h, bi_rmsnorm.h, bi_attention.h,
-                          bi_prenorm.h, bi_qkrope.h, bi_prompt.h, bi_fp4.h)
+                          bi_prenorm.h, bi_qkrope.h, bi_prompt.h, bi_fp4.h,
+                          bi_attention4.h)
   libbi_gemm_controls.so  test-only negative controls and failure injection
 
 Both are compiled in parallel; a library is rebuilt when any source is newer.
@@ -23,7 +24,8 @@ ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 TARGETS = {
     "libbi_gemm.so": ("bi_gemm.cu", "bi_rmsnorm.cu", "bi_attention.cu", "bi_prenorm.cu", "bi_qkrope.cu",
-                      "bi_prompt.cu", "bi_quant4.cu", "bi_gemm4.cu"),
+                      "bi_prompt.cu", "bi_quant4.cu", "bi_gemm4.cu",
+                      "bi_attention4.cu"),
     "libbi_gemm_controls.so": ("bi_gemm_controls.cu",),
 }
 

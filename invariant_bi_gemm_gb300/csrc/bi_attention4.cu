@@ -1,0 +1,819 @@
+// bi_attention4.cu — batch-invariant decode attention over a paged KV cache in 4 bits, and the expansion of its
+// pages, for sm_103a.  Implements include/bi_attention4.h.
+//
+// A unit is (token, split, KV head); a block of four warps runs it.  Warp w takes the 32-position steps w, w + 4,
+// ... of the split through a ring of its own (cp.async, no barrier with the other warps), keeps a running maximum
+// reference, sum and the weighted values of its positions, and the four are merged in order at the unit's end.
+//
+// Per step, with g = lane / 4 and t = lane % 4 (mma.sync m16n8k16, f16 in, fp32 accumulate; the G <= 8 query
+// heads of the KV head on the columns):
+//   scores  S^T = K Q^T: 16 positions on the rows.  The order of the products' dimensions is free as long as both
+//           operands agree, so lane t takes a quarter of a row, whole 16-byte chunks: eight codes become four f16
+//           pairs by cvt, times their block's scale (exact: 2 + 4 significant bits).
+//   weights P = 2^(s - m + 7) in fp32, rounded to f16 and transposed in registers (movmatrix).
+//   values  O^T += V^T P^T: 16 dimensions on the rows, 16 positions deep.  Lane g owns D / 8 consecutive
+//           dimensions, lane t the positions 2t, 2t + 1, 2t + 8, 2t + 9 of each sixteen: the codes of two
+//           positions are interleaved before cvt, so that a pair of f16 is one dimension at two positions.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+
+#include "../../include/bi_attention4.h"
+#include "attn_ptx.cuh"
+#include "fp4.cuh"
+
+#ifndef BI_GEMM_API
+#define BI_GEMM_API extern "C" __attribute__((visibility("default")))
+#endif
+
+namespace biattn4 {
+
+namespace ptx = bigemm::ptx;
+using biattn_tc::ex2;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStep = 32;                 // positions of a step
+constexpr int kRing = 3;                  // steps of a warp's ring
+constexpr int kBlocksPerSm = 3;
+constexpr int kTokens = 1024;             // of a launch
+constexpr int kHeads = 8;                 // columns of the MMA
+constexpr int kDefaultSplit = 512;
+constexpr int kMergeWarps = 8;
+constexpr float kLift = 7.0f;             // weights are 2^7 at the reference, 2^15 at most
+constexpr float kSlack = 8.0f;            // the reference moves when a score passes it by more
+constexpr uint32_t kErrInput = 1u, kErrPage = 2u, kErrBound = 4u;
+
+struct Params {
+  const uint16_t* q;
+  const int32_t* q_seq;
+  const int32_t* q_pos;
+  const uint8_t* kc;
+  const uint8_t* ks;
+  const uint8_t* vc;
+  const uint8_t* vs;
+  const int32_t* table;
+  uint16_t* o;
+  float* part;        // [T, Hkv, max_splits, G, D] partial weighted sums
+  float* ml;          // [T, Hkv, max_splits, G, 2] (reference, sum)
+  uint32_t* status;
+  int64_t num_pages, max_pages, B;
+  int32_t T, Hq, Hkv, G, page_size, split, max_splits, max_pos;
+  uint32_t page_mul;  // pos / page_size = pos * page_mul >> page_shift for pos < 2^30
+  int32_t page_shift;
+  float c;            // scale * k_scale * log2(e)
+  float v_scale;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int CODES = D / 2, SCALES = D / 16;           // bytes of a row
+  // rows of values lie 16 bytes further apart than they are long, so that the rows 0, 2, 4, 6 that a load takes at
+  // once are on different banks
+  static constexpr int VROW = CODES + 16;
+  static constexpr int OFF_V = kStep * CODES, OFF_KS = OFF_V + kStep * VROW, OFF_VS = OFF_KS + kStep * SCALES;
+  static constexpr int STEP = OFF_VS + kStep * SCALES;
+  static constexpr int RING = kRing * STEP;                      // of a warp
+  static constexpr int OFF_ML = kWarps * RING;
+  static constexpr int OFF_CUM = OFF_ML + kWarps * kHeads * 8;
+  static constexpr int OFF_O = (OFF_CUM + (kTokens + 1 + kWarps) * 4 + 15) / 16 * 16;
+  static_assert(STEP % 16 == 0 && OFF_ML % 16 == 0, "alignment");
+  // The warps' parts meet in shared memory, eight heads in two halves of the dimensions: three blocks fit an SM.
+  __host__ __device__ static constexpr int halves(int G) { return G == 8 ? 2 : 1; }
+  __host__ __device__ static constexpr int row(int G) { return D / halves(G) + 4; }   // floats of a head
+  static constexpr int smem(int G) { return OFF_O + kWarps * G * row(G) * 4; }
+};
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct Unit {
+  int32_t t, kh, split, b, first, last;   // positions first .. last of request b (last < first: none)
+};
+
+// Splits of a token: one for an empty place, none for one that cannot be served (which `report` says).
+__device__ __forceinline__ int32_t splits_of(const Params& p, int32_t b, int32_t pos, bool report) {
+  if (pos == -1) return 1;
+  uint32_t bad = 0;
+  if (b < 0 || b >= p.B || pos < 0 || int64_t(pos / p.page_size) >= p.max_pages) bad = kErrInput;
+  else if (pos > p.max_pos) bad = kErrBound;
+  if (bad && report) atomicOr(p.status, bad);
+  return bad ? 0 : pos / p.split + 1;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int32_t* cum = reinterpret_cast<int32_t*>(smem + C::OFF_CUM);
+  int32_t* sums = cum + kTokens + 1;
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // first unit (of one KV head) of every token
+  int32_t carry = 0;
+  for (int base = 0; base < p.T; base += kThreads) {
+    const int i = base + tid;
+    const int32_t n = i < p.T ? splits_of(p, p.q_seq[i], p.q_pos[i], blockIdx.x == 0) : 0;
+    int32_t x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int32_t before = carry;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int32_t s = sums[w];
+      if (w < warp) before += s;
+      carry += s;
+    }
+    if (i < p.T) cum[i] = before + x - n;
+    __syncthreads();
+  }
+  if (tid == 0) cum[p.T] = carry;
+  __syncthreads();
+  const int64_t units = int64_t(carry) * p.Hkv;
+
+  auto find = [&](int64_t u) {
+    Unit r;
+    const int32_t v = int32_t(u / p.Hkv);
+    r.kh = int32_t(u - int64_t(v) * p.Hkv);
+    int lo = 0, hi = p.T;                                // cum[lo] <= v < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= v) lo = mid;
+      else hi = mid;
+    }
+    r.t = lo;
+    r.split = v - cum[lo];
+    r.b = __ldg(p.q_seq + lo);
+    r.first = r.split * p.split;
+    r.last = min(__ldg(p.q_pos + lo), r.first + p.split - 1);
+    return r;
+  };
+
+  // ---- this warp's loads, ahead of its products by up to kRing steps and across units
+  const uint32_t ring = ptx::smem_u32(smem) + uint32_t(warp) * C::RING;
+  int64_t lu = blockIdx.x;                               // unit of the next load
+  Unit L{};
+  int32_t lpos = 0;                                      // its position
+  int lslot = 0;
+  bool lmore = lu < units;
+  // Makes L the next unit (from lu on) in which this warp has a step.
+  auto seek = [&]() {
+    while (lu < units) {
+      L = find(lu);
+      lpos = L.first + warp * kStep;
+      if (lpos <= L.last) return;
+      lu += gridDim.x;
+    }
+    lmore = false;
+  };
+  auto issue = [&]() {
+    if (lmore) {
+      const uint32_t dst = ring + uint32_t(lslot) * C::STEP;
+      // a lane looks one position up; a row's place comes from its lane
+      const int32_t pos = lpos + lane;
+      int64_t at = -1;
+      if (pos <= L.last) {
+        const int32_t pg = int32_t((uint64_t(uint32_t(pos)) * p.page_mul) >> p.page_shift);
+        const int64_t page = __ldg(p.table + int64_t(L.b) * p.max_pages + pg);
+        if (page >= 0 && page < p.num_pages)
+          at = ((page * p.page_size + (pos - pg * p.page_size)) * p.Hkv + L.kh);
+        else
+          atomicOr(p.status, kErrPage);
+      }
+      constexpr int CH = C::CODES / 16, ROWS = 32 / CH;   // 16-byte chunks of a row, rows an instruction
+#pragma unroll
+      for (int i = 0; i < kStep / ROWS; ++i) {
+        const int row = i * ROWS + lane / CH, ch = lane % CH;
+        const int64_t a = __shfl_sync(0xFFFFFFFFu, at, row);
+        const uint32_t n = a >= 0 ? 16u : 0u;
+        const int64_t off = a >= 0 ? a * C::CODES + ch * 16 : 0;
+        ptx::cp_async_16(dst + uint32_t(row * C::CODES + ch * 16), p.kc + off, n);
+        ptx::cp_async_16(dst + C::OFF_V + uint32_t(row * C::VROW + ch * 16), p.vc + off, n);
+      }
+      const uint32_t n = at >= 0 ? uint32_t(C::SCALES) : 0u;
+      const int64_t off = at >= 0 ? at * C::SCALES : 0;
+      if constexpr (D == 128) {
+        cp_async_8(dst + C::OFF_KS + lane * 8, p.ks + off, n);
+        cp_async_8(dst + C::OFF_VS + lane * 8, p.vs + off, n);
+      } else {
+        ptx::cp_async_4(dst + C::OFF_KS + lane * 4, p.ks + off, n);
+        ptx::cp_async_4(dst + C::OFF_VS + lane * 4, p.vs + off, n);
+      }
+      if (++lslot == kRing) lslot = 0;
+      lpos += kWarps * kStep;
+      if (lpos > L.last) {
+        lu += gridDim.x;
+        seek();
+      }
+    }
+    ptx::cp_async_commit();
+  };
+  if (lmore) seek();
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue();
+
+  // ---- products
+  int slot = 0;
+  float* so = reinterpret_cast<float*>(smem + C::OFF_O);
+  float* sml = reinterpret_cast<float*>(smem + C::OFF_ML);
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const Unit U = find(u);
+    // the query in f16, relative to its head's largest element
+    uint32_t qf[D / 8];
+    float fac[2] = {0.0f, 0.0f};
+    {
+      const uint16_t* src = p.q + (int64_t(U.t) * p.Hq + U.kh * p.G + g) * D + t4 * (D / 4);
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 v = g < p.G ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+        qf[4 * i] = v.x, qf[4 * i + 1] = v.y, qf[4 * i + 2] = v.z, qf[4 * i + 3] = v.w;
+      }
+      most = bifp4::most_of(qf, D / 8);
+      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+      most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+      // times 2^11 / 2^exponent of the largest element (within fp32's range): sizes below 2^12
+      const int e = min(max(int(most >> 7), 12), 254);
+      const float up = __uint_as_float(uint32_t(265 - e) << 23), down = __uint_as_float(uint32_t(e - 11) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        qf[i] = pack_f16x2(__uint_as_float(qf[i] << 16) * up, __uint_as_float(qf[i] & 0xFFFF0000u) * up);
+      // the factors of the two heads whose scores this lane has
+      fac[0] = __fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4), p.c);
+      fac[1] = __fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4), p.c);
+    }
+    float acc[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    for (int32_t pos = U.first + warp * kStep; pos <= U.last; pos += kWarps * kStep) {
+      issue();
+      ptx::cp_async_wait<kRing - 1>();
+      __syncwarp();
+      const uint32_t src = ring + uint32_t(slot) * C::STEP;
+      if (++slot == kRing) slot = 0;
+      float s[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {                       // sixteen positions
+        s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
+        constexpr int W = D / 32;                         // words of codes a lane has of a row
+        uint32_t w[2][W], sc[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 16 * h + 8 * r + g;
+          const uint32_t a = src + uint32_t(row * C::CODES + t4 * (C::CODES / 4));
+          if constexpr (D == 128) {
+            uint32_t v[4];
+            biattn_tc::ld_shared_v4(a, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[r][i] = v[i];
+            const uint32_t b = bifp4::e4m3_pair(ld_shared_u16(src + C::OFF_KS + uint32_t(row * 8 + 2 * t4)));
+            sc[r][0] = __byte_perm(b, b, 0x1010), sc[r][1] = __byte_perm(b, b, 0x3232);
+          } else {
+            const uint2 v = ld_shared_v2(a);
+            w[r][0] = v.x, w[r][1] = v.y;
+            const uint32_t b = bifp4::e4m3_pair(ld_shared_u8(src + C::OFF_KS + uint32_t(row * 4 + t4)));
+            sc[r][0] = sc[r][1] = __byte_perm(b, b, 0x1010);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          uint32_t x[4], y[4];
+          bifp4::values8(w[0][i], x);
+          bifp4::values8(w[1][i], y);
+          const int k = i * 2 / W;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = mul_f16x2(x[j], sc[0][k]), y[j] = mul_f16x2(y[j], sc[1][k]);
+          mma(s[h], x[0], y[0], x[1], y[1], qf[4 * i], qf[4 * i + 1]);
+          mma(s[h], x[2], y[2], x[3], y[3], qf[4 * i + 2], qf[4 * i + 3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[h][j] = __fmul_rn(s[h][j], fac[j & 1]);
+      }
+      if (pos + kStep - 1 > U.last) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (pos + 16 * h + 8 * (j >> 1) + g > U.last) s[h][j] = -INFINITY;
+      }
+      bool move = false;
+      float top[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        top[j] = fmaxf(fmaxf(s[0][j], s[0][j + 2]), fmaxf(s[1][j], s[1][j + 2]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], o));
+        move |= top[j] > m[j] + kSlack;
+      }
+      if (__any_sync(0xFFFFFFFFu, move)) {                // (a head's rule looks at that head alone)
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool mv = top[j] > m[j] + kSlack;
+          f[j] = mv ? ex2(m[j] - top[j]) : 1.0f;
+          if (mv) m[j] = top[j];
+          l[j] *= f[j];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] *= f[j & 1];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[h][j] = ex2(__fadd_rn(__fsub_rn(s[h][j], m[j & 1]), kLift));
+        l[0] += s[h][0] + s[h][2];
+        l[1] += s[h][1] + s[h][3];
+        const uint32_t b0 = transposed(pack_f16x2(s[h][0], s[h][1])), b1 = transposed(pack_f16x2(s[h][2], s[h][3]));
+        constexpr int W = D / 64;                         // words of codes a lane has of a row
+        uint32_t w[4][W], sc[2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * h + 2 * t4 + (r & 1) + 8 * (r >> 1);
+          const uint32_t a = src + C::OFF_V + uint32_t(row * C::VROW + g * (C::CODES / 8));
+          if constexpr (D == 128) {
+            const uint2 v = ld_shared_v2(a);
+            w[r][0] = v.x, w[r][1] = v.y;
+          } else {
+            w[r][0] = ptx::ld_shared_u32(a);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = 16 * h + 2 * t4 + 8 * r;
+          const uint32_t a = src + C::OFF_VS + uint32_t(row * C::SCALES + (D == 128 ? g : g >> 1));
+          sc[r] = bifp4::e4m3_pair(ld_shared_u8(a) | ld_shared_u8(a + C::SCALES) << 8);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          // even and odd dimensions of the lane's eight, a pair of positions each
+          uint32_t x0[4], x1[4], y0[4], y1[4];
+          constexpr uint32_t LO = 0x0F0F0F0Fu;
+          bifp4::values8((w[0][i] & LO) | ((w[1][i] << 4) & ~LO), x0);
+          bifp4::values8(((w[0][i] >> 4) & LO) | (w[1][i] & ~LO), x1);
+          bifp4::values8((w[2][i] & LO) | ((w[3][i] << 4) & ~LO), y0);
+          bifp4::values8(((w[2][i] >> 4) & LO) | (w[3][i] & ~LO), y1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma(acc[4 * i + j], mul_f16x2(x0[j], sc[0]), mul_f16x2(x1[j], sc[0]), mul_f16x2(y0[j], sc[1]),
+                mul_f16x2(y1[j], sc[1]), b0, b1);
+        }
+      }
+      __syncwarp();                                       // the slot may be refilled
+    }
+    // ---- the four warps' parts, in order
+    const bool alone = U.split == 0 && U.last == __ldg(p.q_pos + U.t);
+    const int halves = C::halves(p.G), dims = D / halves, orow = C::row(p.G);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[j] = __fadd_rn(l[j], __shfl_xor_sync(0xFFFFFFFFu, l[j], o));
+      const int head = 2 * t4 + j;
+      if (g == 0 && head < p.G) {
+        sml[(warp * kHeads + head) * 2] = m[j];
+        sml[(warp * kHeads + head) * 2 + 1] = l[j];
+      }
+    }
+    for (int half = 0; half < halves; ++half) {
+      const int d0 = g * (D / 8) - half * dims;           // this lane's first dimension within the half
+      if (d0 >= 0 && d0 < dims) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int head = 2 * t4 + j;
+          if (head < p.G) {
+            float* dst = so + (warp * p.G + head) * orow + d0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+              *reinterpret_cast<float4*>(dst + 4 * i) =
+                  make_float4(acc[2 * i][j], acc[2 * i][j + 2], acc[2 * i + 1][j], acc[2 * i + 1][j + 2]);
+          }
+        }
+      }
+      __syncthreads();
+      for (int it = tid; it < p.G * (dims / 4); it += kThreads) {
+        const int head = it / (dims / 4), d = (it - head * (dims / 4)) * 4;
+        float M = -INFINITY, Ls = 0.0f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[(w * kHeads + head) * 2]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = sml[(w * kHeads + head) * 2], lw = sml[(w * kHeads + head) * 2 + 1];
+          // (a warp without a step has a sum of 0; one whose scores are all -inf or NaN has a NaN)
+          const float f = mw == -INFINITY ? (lw == 0.0f ? 0.0f : NAN) : ex2(__fsub_rn(mw, M));
+          const float4 v = *reinterpret_cast<const float4*>(so + (w * p.G + head) * orow + d);
+          Ls = __fmaf_rn(lw, f, Ls);
+          A.x = __fmaf_rn(v.x, f, A.x);
+          A.y = __fmaf_rn(v.y, f, A.y);
+          A.z = __fmaf_rn(v.z, f, A.z);
+          A.w = __fmaf_rn(v.w, f, A.w);
+        }
+        const int at_d = half * dims + d;
+        if (alone) {
+          const float f = U.last < 0 ? 0.0f : __fdiv_rn(p.v_scale, Ls);
+          const uint2 out = U.last < 0 ? make_uint2(0u, 0u)
+                                       : make_uint2(ptx::pack_bf16x2(__fmul_rn(A.x, f), __fmul_rn(A.y, f)),
+                                                    ptx::pack_bf16x2(__fmul_rn(A.z, f), __fmul_rn(A.w, f)));
+          *reinterpret_cast<uint2*>(p.o + (int64_t(U.t) * p.Hq + U.kh * p.G + head) * D + at_d) = out;
+        } else {
+          const int64_t at = ((int64_t(U.t) * p.Hkv + U.kh) * p.max_splits + U.split) * p.G + head;
+          *reinterpret_cast<float4*>(p.part + at * D + at_d) = A;
+          if (at_d == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, Ls);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  ptx::cp_async_wait<0>();
+}
+
+// Splits of a token's query head, a block each: warp w sums the w-th of eight consecutive groups of ceil(n / 8)
+// splits, ascending; the groups are added in order.
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p) {
+  constexpr int PER = D / 32;                             // dimensions a lane
+  __shared__ float sums[kMergeWarps][D];
+  __shared__ float2 mls[kMergeWarps];
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int32_t t = int32_t(blockIdx.x / p.Hq), h = int32_t(blockIdx.x - uint32_t(t) * p.Hq);
+  const int32_t n = splits_of(p, p.q_seq[t], p.q_pos[t], false);
+  if (n <= 1) return;                                     // written by its unit, or refused
+  const int32_t kh = h / p.G, hd = h - kh * p.G;
+  const int64_t slot0 = (int64_t(t) * p.Hkv + kh) * p.max_splits * p.G + hd;
+  const int32_t c = (n + kMergeWarps - 1) / kMergeWarps, s0 = min(n, warp * c), s1 = min(n, s0 + c);
+  const float2* mlp = reinterpret_cast<const float2*>(p.ml) + slot0;
+  float M = -INFINITY;
+  for (int32_t s = s0 + lane; s < s1; s += 32) M = fmaxf(M, mlp[int64_t(s) * p.G].x);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float L = 0.0f, A[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) A[i] = 0.0f;
+  constexpr int BATCH = 8;
+  for (int32_t b = s0; b < s1; b += BATCH) {
+    float2 ml[BATCH];
+    float v[BATCH][PER];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (b + i < s1) {
+        ml[i] = mlp[int64_t(b + i) * p.G];
+        const float* src = p.part + (slot0 + int64_t(b + i) * p.G) * D + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[i][0] = x.x, v[i][1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (b + i < s1) {
+        const float f = ex2(__fsub_rn(ml[i].x, M));
+        L = __fmaf_rn(ml[i].y, f, L);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) A[j] = __fmaf_rn(v[i][j], f, A[j]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) sums[warp][lane * PER + j] = A[j];
+  if (lane == 0) mls[warp] = make_float2(M, L);
+  __syncthreads();
+  if (int(threadIdx.x) < D / 2) {
+    float top = -INFINITY, Ls = 0.0f, a0 = 0.0f, a1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, mls[w].x);
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      if (w * c < n) {                                    // (a group of no splits adds nothing)
+        const float f = ex2(__fsub_rn(mls[w].x, top));
+        Ls = __fmaf_rn(mls[w].y, f, Ls);
+        a0 = __fmaf_rn(sums[w][2 * threadIdx.x], f, a0);
+        a1 = __fmaf_rn(sums[w][2 * threadIdx.x + 1], f, a1);
+      }
+    }
+    const float f = __fdiv_rn(p.v_scale, Ls);
+    *reinterpret_cast<uint32_t*>(p.o + (int64_t(t) * p.Hq + h) * D + 2 * threadIdx.x) =
+        ptx::pack_bf16x2(__fmul_rn(a0, f), __fmul_rn(a1, f));
+  }
+}
+
+struct ExpandParams {
+  const uint8_t* kc;
+  const uint8_t* ks;
+  const uint8_t* vc;
+  const uint8_t* vs;
+  const int32_t* pages;
+  uint16_t* ko;
+  uint16_t* vo;
+  uint32_t* status;
+  int64_t num_pages, blocks;              // blocks of sixteen elements in all
+  int64_t per_page;                       // and of a page
+  float k_scale, v_scale;
+};
+
+__global__ void __launch_bounds__(256) expand_kernel(const ExpandParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.blocks) return;
+  const int64_t n = i / p.per_page, r = i - n * p.per_page;
+  const int64_t page = p.pages[n];
+  if (page < 0 || page >= p.num_pages) {
+    if (page != -1 && r == 0) atomicOr(p.status, kErrPage);
+    return;
+  }
+  const int64_t at = page * p.per_page + r;
+  const uint2 kc = *reinterpret_cast<const uint2*>(p.kc + at * 8), vc = *reinterpret_cast<const uint2*>(p.vc + at * 8);
+  const float ks = bifp4::scale_value<true>(p.ks[at], p.k_scale), vs = bifp4::scale_value<true>(p.vs[at], p.v_scale);
+  uint32_t out[8];
+  bifp4::values_bf16(kc.x, ks, out);
+  bifp4::values_bf16(kc.y, ks, out + 4);
+  uint4* dst = reinterpret_cast<uint4*>(p.ko + i * 16);
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  bifp4::values_bf16(vc.x, vs, out);
+  bifp4::values_bf16(vc.y, vs, out + 4);
+  dst = reinterpret_cast<uint4*>(p.vo + i * 16);
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+inline const void* attn_of(int D) {
+  return D == 128 ? reinterpret_cast<const void*>(&attn_kernel<128>) : reinterpret_cast<const void*>(&attn_kernel<64>);
+}
+inline const void* merge_of(int D) {
+  return D == 128 ? reinterpret_cast<const void*>(&merge_kernel<128>) : reinterpret_cast<const void*>(&merge_kernel<64>);
+}
+
+}  // namespace biattn4
+
+struct bi_attention4 {
+  int Hq = 0, Hkv = 0, D = 0, G = 0, page_size = 0, split = 0;
+  float scale = 0.0f, k_scale = 1.0f, v_scale = 1.0f;
+  int device = 0, max_ctas = 0, smem = 0;
+  uint32_t* d_status = nullptr;
+  biattn_tc::Workspace ws;
+};
+
+BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
+                                     int64_t page_size, float scale, float k_scale, float v_scale, int64_t split_size) {
+  if (!out) return BI_GEMM_ERR_INVALID_ARG;
+  *out = nullptr;
+  auto fine = [](float s) { return s >= 0x1p-64f && s <= 0x1p64f; };
+  if (!std::isfinite(scale) || scale <= 0.0f || !fine(k_scale) || !fine(v_scale)) return BI_GEMM_ERR_INVALID_ARG;
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 || split_size < 0)
+    return BI_GEMM_ERR_INVALID_ARG;
+  const int64_t split = split_size ? split_size : biattn4::kDefaultSplit;
+  if (num_q_heads % num_kv_heads != 0 || num_q_heads > 4096 || page_size > (1 << 20) || split % 128 != 0 || split > 4096 ||
+      (head_dim != 64 && head_dim != 128))
+    return BI_GEMM_ERR_UNSUPPORTED;
+  const int64_t G = num_q_heads / num_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return BI_GEMM_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0, per_sm = 0;
+  if (const int rc = bifp4::check_device(&dev)) return rc;
+  const int smem = head_dim == 128 ? biattn4::Cfg<128>::smem(int(G)) : biattn4::Cfg<64>::smem(int(G));
+  // (the attribute is the kernel's, shared by every handle of the head size: the most any of them needs)
+  const int most = head_dim == 128 ? std::max(biattn4::Cfg<128>::smem(4), biattn4::Cfg<128>::smem(8))
+                                   : std::max(biattn4::Cfg<64>::smem(4), biattn4::Cfg<64>::smem(8));
+  const void* fn = biattn4::attn_of(int(head_dim));
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biattn4::kThreads, smem) != cudaSuccess || per_sm < 1) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  bi_attention4* h = new (std::nothrow) bi_attention4();
+  if (!h) return BI_GEMM_ERR_OOM;
+  h->Hq = int(num_q_heads);
+  h->Hkv = int(num_kv_heads);
+  h->D = int(head_dim);
+  h->G = int(G);
+  h->page_size = int(page_size);
+  h->split = int(split);
+  h->scale = scale;
+  h->k_scale = k_scale;
+  h->v_scale = v_scale;
+  h->device = dev;
+  h->max_ctas = per_sm * sms;
+  h->smem = smem;
+  if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
+      cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
+    cudaGetLastError();
+    if (h->d_status) cudaFree(h->d_status);
+    delete h;
+    return BI_GEMM_ERR_CUDA;
+  }
+  *out = h;
+  return BI_GEMM_OK;
+}
+
+namespace {
+
+struct Layout4 {
+  int64_t splits;
+  size_t part, total;      // bytes of the partial sums, and with the references and sums behind them
+};
+Layout4 layout4_of(const bi_attention4* h, int64_t T, int64_t max_pos) {
+  Layout4 w{max_pos / h->split + 1, 0, 0};
+  if (w.splits > 1) {
+    const size_t slots = size_t(std::min<int64_t>(T, biattn4::kTokens)) * h->Hkv * size_t(w.splits) * h->G;
+    w.part = slots * h->D * sizeof(float);
+    w.total = w.part + slots * 2 * sizeof(float);
+  }
+  return w;
+}
+
+}  // namespace
+
+BI_GEMM_API int bi_attention4_workspace_size(bi_attention4_t h, int64_t T, int64_t max_pos, uint64_t* bytes) {
+  if (!h || !bytes || T < 0 || max_pos < -1) return BI_GEMM_ERR_INVALID_ARG;
+  *bytes = T == 0 || max_pos < 0 ? 0 : uint64_t(layout4_of(h, T, max_pos).total);
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t* q_seq, const int32_t* q_pos,
+                                  const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                                  int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
+                                  int64_t max_pos, void* o, void* stream) {
+  if (!h || T < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || max_pos < -1) return BI_GEMM_ERR_INVALID_ARG;
+  if (T == 0) return BI_GEMM_OK;
+  if (T > (int64_t(1) << 24) || max_pos >= (int64_t(1) << 30)) return BI_GEMM_ERR_UNSUPPORTED;
+  if (!q || !q_seq || !q_pos || !k_codes || !k_scales || !v_codes || !v_scales || !page_table || !o)
+    return BI_GEMM_ERR_INVALID_ARG;
+  auto bits = [](const void* a) { return reinterpret_cast<uintptr_t>(a); };
+  if ((bits(q) | bits(o) | bits(k_codes) | bits(k_scales) | bits(v_codes) | bits(v_scales)) & 15u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  if ((bits(q_seq) | bits(q_pos) | bits(page_table)) & 3u) return BI_GEMM_ERR_ALIGNMENT;
+  const Layout4 w = layout4_of(h, T, std::max<int64_t>(max_pos, 0));
+  const int64_t per_token = int64_t(h->Hkv) * w.splits;
+  if (per_token * std::min<int64_t>(T, biattn4::kTokens) >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (const int rc = h->ws.need(w.total, st)) return rc;
+  biattn4::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.kc = static_cast<const uint8_t*>(k_codes);
+  p.ks = static_cast<const uint8_t*>(k_scales);
+  p.vc = static_cast<const uint8_t*>(v_codes);
+  p.vs = static_cast<const uint8_t*>(v_scales);
+  p.table = page_table;
+  p.part = static_cast<float*>(h->ws.at);
+  p.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(h->ws.at) + w.part);
+  p.status = h->d_status;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.B = num_seqs;
+  p.Hq = h->Hq;
+  p.Hkv = h->Hkv;
+  p.G = h->G;
+  p.page_size = h->page_size;
+  p.split = h->split;
+  p.max_splits = int32_t(w.splits);
+  p.max_pos = int32_t(max_pos);
+  int log2 = 0;
+  while ((1 << log2) < h->page_size) ++log2;
+  p.page_shift = 30 + log2;
+  p.page_mul = uint32_t((uint64_t(1) << p.page_shift) / uint64_t(h->page_size) + 1);
+  p.c = float(double(h->scale) * double(h->k_scale) * 1.4426950408889634);
+  p.v_scale = h->v_scale;
+  for (int64_t t0 = 0; t0 < T; t0 += biattn4::kTokens) {
+    p.T = int32_t(std::min<int64_t>(biattn4::kTokens, T - t0));
+    p.q = static_cast<const uint16_t*>(q) + t0 * h->Hq * h->D;
+    p.o = static_cast<uint16_t*>(o) + t0 * h->Hq * h->D;
+    p.q_seq = q_seq + t0;
+    p.q_pos = q_pos + t0;
+    const int64_t units = int64_t(p.T) * per_token;
+    if (const int rc = bifp4::launch(biattn4::attn_of(h->D), unsigned(std::min<int64_t>(units, h->max_ctas)),
+                                     biattn4::kThreads, size_t(h->smem), st, &p))
+      return rc;
+    if (w.splits > 1)
+      if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(int64_t(p.T) * h->Hq), 32 * biattn4::kMergeWarps, 0,
+                                       st, &p))
+        return rc;
+  }
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_attention4_expand(bi_attention4_t h, const void* k_codes, const void* k_scales, const void* v_codes,
+                                     const void* v_scales, int64_t num_pages, const int32_t* pages, int64_t n, void* k_out,
+                                     void* v_out, void* stream) {
+  if (!h || num_pages < 0 || n < 0) return BI_GEMM_ERR_INVALID_ARG;
+  if (n == 0) return BI_GEMM_OK;
+  if (!k_codes || !k_scales || !v_codes || !v_scales || !pages || !k_out || !v_out) return BI_GEMM_ERR_INVALID_ARG;
+  auto bits = [](const void* a) { return reinterpret_cast<uintptr_t>(a); };
+  if ((bits(k_codes) | bits(k_scales) | bits(v_codes) | bits(v_scales) | bits(k_out) | bits(v_out)) & 15u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  if (bits(pages) & 3u) return BI_GEMM_ERR_ALIGNMENT;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return BI_GEMM_ERR_CUDA;
+  }
+  if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
+  biattn4::ExpandParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kc = static_cast<const uint8_t*>(k_codes);
+  p.ks = static_cast<const uint8_t*>(k_scales);
+  p.vc = static_cast<const uint8_t*>(v_codes);
+  p.vs = static_cast<const uint8_t*>(v_scales);
+  p.pages = pages;
+  p.ko = static_cast<uint16_t*>(k_out);
+  p.vo = static_cast<uint16_t*>(v_out);
+  p.status = h->d_status;
+  p.num_pages = num_pages;
+  p.per_page = int64_t(h->page_size) * h->Hkv * (h->D / 16);
+  if (n > (int64_t(1) << 31) / p.per_page * 256) return BI_GEMM_ERR_UNSUPPORTED;
+  p.blocks = n * p.per_page;
+  p.k_scale = h->k_scale;
+  p.v_scale = h->v_scale;
+  if ((p.blocks + 255) / 256 >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  return bifp4::launch(reinterpret_cast<const void*>(&biattn4::expand_kernel), unsigned((p.blocks + 255) / 256), 256, 0,
+                       static_cast<cudaStream_t>(stream), &p);
+}
+
+BI_GEMM_API int bi_attention4_get_device_error(bi_attention4_t h, void* stream) {
+  if (!h) return BI_GEMM_ERR_INVALID_ARG;
+  return bifp4::read_status(h->d_status, static_cast<cudaStream_t>(stream), 0u);
+}
+
+BI_GEMM_API int bi_attention4_get_config(bi_attention4_t h, bi_attention4_config* c) {
+  if (!h || !c) return BI_GEMM_ERR_INVALID_ARG;
+  c->num_q_heads = h->Hq;
+  c->num_kv_heads = h->Hkv;
+  c->head_dim = h->D;
+  c->page_size = h->page_size;
+  c->split_size = h->split;
+  c->threads = biattn4::kThreads;
+  c->max_ctas = h->max_ctas;
+  c->tokens_per_launch = biattn4::kTokens;
+  return BI_GEMM_OK;
+}
+
+BI_GEMM_API int bi_attention4_destroy(bi_attention4_t h) {
+  if (!h) return BI_GEMM_OK;
+  h->ws.release();
+  if (h->d_status) cudaFree(h->d_status);
+  delete h;
+  return BI_GEMM_OK;
+}

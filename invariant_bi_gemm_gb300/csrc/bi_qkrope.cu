@@ -20,6 +20,7 @@
 
 #include "../../include/bi_qkrope.h"
 #include "attn_ptx.cuh"
+#include "fp4.cuh"
 
 #ifndef BI_GEMM_API
 #define BI_GEMM_API extern "C" __attribute__((visibility("default")))
@@ -64,6 +65,11 @@ struct Params {
   int32_t stall;            // failure injection (test controls only): this block of it loads nothing
   uint64_t timeout_ns;      // limit of its waits
   float eps;
+  uint8_t* kc4;             // the cache in 4 bits: codes and scales, and the tensor scales
+  uint8_t* ks4;
+  uint8_t* vc4;
+  uint8_t* vs4;
+  float k_scale, v_scale;
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -173,6 +179,64 @@ struct Lane {
     b = make_uint2(narrow(x[2]), narrow(x[3]));
   }
 
+  // Where the lane's two runs of head h are loaded from: its own, but eight neighbours of a value head that is
+  // about to be quantised.
+  template <bool kFour>
+  __device__ __forceinline__ int first(const Params& p, int h) const {
+    return kFour && h >= p.Hq + p.Hkv ? 8 * l : da;
+  }
+  template <bool kFour>
+  __device__ __forceinline__ int second(const Params& p, int h) const {
+    return kFour && h >= p.Hq + p.Hkv ? 8 * l + 4 : db;
+  }
+
+  // Head h of a token for a cache in 4 bits: queries as in `finish`; keys, rounded to bf16 as they are there, and
+  // values as E2M1 codes with a scale per sixteen, two lanes.
+  __device__ __forceinline__ void finish4(const Params& p, int h, int64_t t, int64_t slot, bool store, uint2 a,
+                                          uint2 b) const {
+    if (h < p.Hq) {
+      head(p, false, a, b);
+      if (store) {
+        uint16_t* dst = p.q_out + (t * p.Hq + h) * D;
+        *reinterpret_cast<uint2*>(dst + da) = a;
+        *reinterpret_cast<uint2*>(dst + db) = b;
+      }
+      return;
+    }
+    const bool key = h < p.Hq + p.Hkv;
+    uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    if (key) {
+      head(p, true, a, b);
+      w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
+      if constexpr (!kInterleaved) {
+        // from a lane's two runs to eight neighbours: dimensions 8 l .. 8 l + 3 and 8 l + 4 .. 8 l + 7 are runs of two
+        // neighbouring lanes, their first ones in the first half of the rotated dimensions, their second ones behind
+        const bool late = turned && 8 * l >= half;
+        const int from = !turned ? l : late ? 2 * l - half / 4 : 2 * l, next = turned ? from + 1 : l;
+        const uint32_t a0 = __shfl_sync(mask, a.x, from, LANES), a1 = __shfl_sync(mask, a.y, from, LANES);
+        const uint32_t b0 = __shfl_sync(mask, b.x, from, LANES), b1 = __shfl_sync(mask, b.y, from, LANES);
+        const uint32_t a2 = __shfl_sync(mask, a.x, next, LANES), a3 = __shfl_sync(mask, a.y, next, LANES);
+        const uint32_t b2 = __shfl_sync(mask, b.x, next, LANES), b3 = __shfl_sync(mask, b.y, next, LANES);
+        if (turned) {
+          w[0] = late ? b0 : a0, w[1] = late ? b1 : a1;
+          w[2] = late ? b2 : a2, w[3] = late ? b3 : a3;
+        }
+      }
+    }
+    uint32_t most = bifp4::most_of(w, 4);
+    most = max(most, __shfl_xor_sync(mask, most, 1));
+    const float g = key ? p.k_scale : p.v_scale;
+    const bifp4::Scale s = bifp4::nvfp4_scale(most, g, __fmul_rn(6.0f, g));
+    uint32_t word = s.byte << (8 * ((l >> 1) & 3));       // four blocks' scales to one lane of eight
+    word |= __shfl_xor_sync(mask, word, 2);
+    word |= __shfl_xor_sync(mask, word, 4);
+    if (store) {
+      const int64_t row = slot * p.Hkv + (h - p.Hq - (key ? 0 : p.Hkv));
+      *reinterpret_cast<uint32_t*>((key ? p.kc4 : p.vc4) + row * (D / 2) + 4 * l) = bifp4::quantise8<true>(w, s);
+      if ((l & 7) == 0) *reinterpret_cast<uint32_t*>((key ? p.ks4 : p.vs4) + row * (D / 16) + l / 2) = word;
+    }
+  }
+
   // Head h of a token: computed, and stored in q_out (row t) or the token's slot.
   __device__ __forceinline__ void finish(const Params& p, int h, int64_t t, int64_t slot, bool store, uint2 a,
                                          uint2 b) const {
@@ -206,7 +270,7 @@ __device__ __forceinline__ int64_t slot_of(const Params& p, int32_t b, int32_t p
 }
 
 // A block per token or few: the form for few tokens.
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kFour>
 __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
   constexpr int LANES = D / 8;
   // Programmatic dependent launch: the block may start while the previous kernel finishes and
@@ -228,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
     for (int k = 0; k < kHeads; ++k) {
       const int h = h0 + k * groups;
       if (h < H) {
-        ra[k] = *reinterpret_cast<const uint2*>(row + h * D + ln.da);
-        rb[k] = *reinterpret_cast<const uint2*>(row + h * D + ln.db);
+        ra[k] = *reinterpret_cast<const uint2*>(row + h * D + ln.template first<kFour>(p, h));
+        rb[k] = *reinterpret_cast<const uint2*>(row + h * D + ln.template second<kFour>(p, h));
       }
     }
   };
@@ -243,7 +307,8 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
     for (int k = 0; k < kHeads; ++k) {
       const int h = h0 + k * groups;
       if (h >= H) break;
-      ln.finish(p, h, t, slot, slot >= 0, ra[k], rb[k]);
+      if constexpr (kFour) ln.finish4(p, h, t, slot, slot >= 0, ra[k], rb[k]);
+      else ln.finish(p, h, t, slot, slot >= 0, ra[k], rb[k]);
     }
     if (h0 + kHeads * groups >= H) break;
     load(h0 + kHeads * groups);
@@ -255,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
 // on their way whatever the lookups take.  (A block per token is up for 4 us, a third of it with loads
 // in flight: 52 us for 8192 tokens of 32/8 heads of 128, now 42.  With a larger ring and three blocks per SM
 // it took 43.5, with five, and registers spilled, 47.)
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kFour>
 __global__ void __launch_bounds__(kThreads + 32, 4) qkrope_ring_kernel(const Params p) {
   constexpr int LANES = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -329,9 +394,12 @@ __global__ void __launch_bounds__(kThreads + 32, 4) qkrope_ring_kernel(const Par
       if (slot >= 0) {
         ln.angles(reinterpret_cast<const float*>(stage + row_bytes));
         const uint16_t* row = reinterpret_cast<const uint16_t*>(stage);
-        for (int h = g; h < H; h += groups)
-          ln.finish(p, h, t, slot, true, *reinterpret_cast<const uint2*>(row + h * D + ln.da),
-                    *reinterpret_cast<const uint2*>(row + h * D + ln.db));
+        for (int h = g; h < H; h += groups) {
+          const uint2 a = *reinterpret_cast<const uint2*>(row + h * D + ln.template first<kFour>(p, h));
+          const uint2 b = *reinterpret_cast<const uint2*>(row + h * D + ln.template second<kFour>(p, h));
+          if constexpr (kFour) ln.finish4(p, h, t, slot, true, a, b);
+          else ln.finish(p, h, t, slot, true, a, b);
+        }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty + 8 * s);
@@ -347,13 +415,19 @@ __global__ void __launch_bounds__(kThreads + 32, 4) qkrope_ring_kernel(const Par
 }
 
 using Kernel = void (*)(const Params);
+template <bool kFour>
 inline Kernel kernel_of(int D, bool interleaved) {
-  if (D == 128) return interleaved ? qkrope_kernel<128, true> : qkrope_kernel<128, false>;
-  return interleaved ? qkrope_kernel<64, true> : qkrope_kernel<64, false>;
+  if (D == 128) return interleaved ? qkrope_kernel<128, true, kFour> : qkrope_kernel<128, false, kFour>;
+  return interleaved ? qkrope_kernel<64, true, kFour> : qkrope_kernel<64, false, kFour>;
 }
+template <bool kFour>
 inline Kernel ring_kernel_of(int D, bool interleaved) {
-  if (D == 128) return interleaved ? qkrope_ring_kernel<128, true> : qkrope_ring_kernel<128, false>;
-  return interleaved ? qkrope_ring_kernel<64, true> : qkrope_ring_kernel<64, false>;
+  if (D == 128) return interleaved ? qkrope_ring_kernel<128, true, kFour> : qkrope_ring_kernel<128, false, kFour>;
+  return interleaved ? qkrope_ring_kernel<64, true, kFour> : qkrope_ring_kernel<64, false, kFour>;
+}
+inline Kernel kernel_of(int D, bool interleaved, bool ring, bool four) {
+  if (ring) return four ? ring_kernel_of<true>(D, interleaved) : ring_kernel_of<false>(D, interleaved);
+  return four ? kernel_of<true>(D, interleaved) : kernel_of<false>(D, interleaved);
 }
 
 }  // namespace biqkr
@@ -362,6 +436,7 @@ struct bi_qkrope {
   int Hq = 0, Hkv = 0, D = 0, page_size = 0, rot = 0, interleaved = 0;
   float eps = 0.0f;
   int device = 0, groups_log2 = 0, per_block = 0;
+  int ring_ctas4 = 0;               // resident blocks of that form for a cache in 4 bits
   int ring = 0, ring_ctas = 0;      // stages and resident blocks of the form for many tokens (0: none),
   int team_log2 = 0;                // its warps per token
   int ring_from = 0;                // and the tokens from which it runs
@@ -410,18 +485,24 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
     int sms = 0, per_sm = 0;
     h->ring = ring;
     h->ring_smem = ring * stage;
-    const auto fn = biqkr::ring_kernel_of(h->D, interleaved != 0);
+    const auto fn = biqkr::kernel_of(h->D, interleaved != 0, true, false);
+    const auto fn4 = biqkr::kernel_of(h->D, interleaved != 0, true, true);
+    int per_sm4 = 0;
     // (the attribute is the kernel's, shared by every handle: the most any of them needs)
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, biqkr::kRingBytes) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biqkr::kThreads + 32, h->ring_smem) !=
             cudaSuccess ||
-        per_sm < 1) {
+        cudaFuncSetAttribute(fn4, cudaFuncAttributeMaxDynamicSharedMemorySize, biqkr::kRingBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm4, fn4, biqkr::kThreads + 32, h->ring_smem) !=
+            cudaSuccess ||
+        per_sm < 1 || per_sm4 < 1) {
       cudaGetLastError();
       delete h;
       return BI_GEMM_ERR_CUDA;
     }
     h->ring_ctas = per_sm * sms;
+    h->ring_ctas4 = per_sm4 * sms;
     const int64_t row = int64_t(heads) * h->D * 2;
     h->ring_from = int((int64_t(biqkr::kRingRows) * h->ring_ctas + row - 1) / row);
   }
@@ -438,22 +519,35 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
 
 namespace {
 
-// bi_qkrope_run with the failure injection of the test controls (stall >= 0: that block of the form for
-// many tokens loads nothing) and the limit of its waits.
+// A cache in 4 bits.
+struct Four {
+  void *kc, *ks, *vc, *vs;
+  float k_scale, v_scale;
+};
+
+// bi_qkrope_run, or with `four` bi_qkrope_run4 (k_cache and v_cache are not used), with the failure injection of
+// the test controls (stall >= 0: that block of the form for many tokens loads nothing) and the limit of its waits.
 int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq, const void* gk,
                const float* cos_sin, int64_t num_positions, const int32_t* q_seq, const int32_t* q_pos, void* k_cache,
                void* v_cache, int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
-               void* q_out, void* stream, int32_t stall, uint64_t timeout_ns) {
+               void* q_out, void* stream, int32_t stall, uint64_t timeout_ns, const Four* four = nullptr) {
   if (!h || T < 0 || num_positions < 0 || num_pages < 0 || num_seqs < 0 || max_pages < 0 || !gq != !gk)
     return BI_GEMM_ERR_INVALID_ARG;
+  if (four) {
+    auto fine = [](float s) { return s >= 0x1p-64f && s <= 0x1p64f; };
+    if (!fine(four->k_scale) || !fine(four->v_scale)) return BI_GEMM_ERR_INVALID_ARG;
+  }
   if (T == 0) return BI_GEMM_OK;
-  if (!qkv || !cos_sin || !q_seq || !q_pos || !k_cache || !v_cache || !page_table || !q_out)
-    return BI_GEMM_ERR_INVALID_ARG;
+  if (!qkv || !cos_sin || !q_seq || !q_pos || !page_table || !q_out) return BI_GEMM_ERR_INVALID_ARG;
+  if (four ? !four->kc || !four->ks || !four->vc || !four->vs : !k_cache || !v_cache) return BI_GEMM_ERR_INVALID_ARG;
   if (qkv_stride % 8 != 0 || qkv_stride < int64_t(h->Hq + 2 * h->Hkv) * h->D || T > (int64_t(1) << 30))
     return BI_GEMM_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(qkv) | reinterpret_cast<uintptr_t>(gq) | reinterpret_cast<uintptr_t>(gk) |
        reinterpret_cast<uintptr_t>(cos_sin) | reinterpret_cast<uintptr_t>(k_cache) |
        reinterpret_cast<uintptr_t>(v_cache) | reinterpret_cast<uintptr_t>(q_out)) & 15u)
+    return BI_GEMM_ERR_ALIGNMENT;
+  if (four && ((reinterpret_cast<uintptr_t>(four->kc) | reinterpret_cast<uintptr_t>(four->ks) |
+                reinterpret_cast<uintptr_t>(four->vc) | reinterpret_cast<uintptr_t>(four->vs)) & 15u))
     return BI_GEMM_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(q_seq) | reinterpret_cast<uintptr_t>(q_pos) |
        reinterpret_cast<uintptr_t>(page_table)) & 3u)
@@ -489,6 +583,14 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   p.rot = h->rot;
   p.groups_log2 = h->groups_log2;
   p.eps = h->eps;
+  if (four) {
+    p.kc4 = static_cast<uint8_t*>(four->kc);
+    p.ks4 = static_cast<uint8_t*>(four->ks);
+    p.vc4 = static_cast<uint8_t*>(four->vc);
+    p.vs4 = static_cast<uint8_t*>(four->vs);
+    p.k_scale = four->k_scale;
+    p.v_scale = four->v_scale;
+  }
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   // The ring from 40 KB of rows per resident block on, where its start is paid for (us, ring against a
@@ -500,7 +602,7 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   p.team_log2 = h->team_log2;
   p.stall = stall;
   p.timeout_ns = timeout_ns;
-  cfg.gridDim = dim3(unsigned(ring ? h->ring_ctas : (T + h->per_block - 1) / h->per_block));
+  cfg.gridDim = dim3(unsigned(ring ? (four ? h->ring_ctas4 : h->ring_ctas) : (T + h->per_block - 1) / h->per_block));
   cfg.blockDim = dim3(biqkr::kThreads + (ring ? 32 : 0));
   cfg.dynamicSmemBytes = ring ? h->ring_smem : 0;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -509,7 +611,7 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const auto fn = ring ? biqkr::ring_kernel_of(h->D, h->interleaved != 0) : biqkr::kernel_of(h->D, h->interleaved != 0);
+  const auto fn = biqkr::kernel_of(h->D, h->interleaved != 0, ring, four != nullptr);
   if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
@@ -526,6 +628,16 @@ BI_GEMM_API int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t
                               void* stream) {
   return qkrope_run(h, qkv, T, qkv_stride, gq, gk, cos_sin, num_positions, q_seq, q_pos, k_cache, v_cache, num_pages,
                     page_table, num_seqs, max_pages, q_out, stream, -1, biattn_tc::kTimeoutNs);
+}
+
+BI_GEMM_API int bi_qkrope_run4(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq,
+                               const void* gk, const float* cos_sin, int64_t num_positions, const int32_t* q_seq,
+                               const int32_t* q_pos, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                               float k_scale, float v_scale, int64_t num_pages, const int32_t* page_table,
+                               int64_t num_seqs, int64_t max_pages, void* q_out, void* stream) {
+  const Four four{k_codes, k_scales, v_codes, v_scales, k_scale, v_scale};
+  return qkrope_run(h, qkv, T, qkv_stride, gq, gk, cos_sin, num_positions, q_seq, q_pos, nullptr, nullptr, num_pages,
+                    page_table, num_seqs, max_pages, q_out, stream, -1, biattn_tc::kTimeoutNs, &four);
 }
 
 BI_GEMM_API int bi_qkrope_get_device_error(bi_qkrope_t h, void* stream) {

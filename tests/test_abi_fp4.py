@@ -13,18 +13,36 @@ from test_abi import _declared, _structs
 INVALID, UNSUPPORTED = bg.BI_GEMM_ERR_INVALID_ARG, bg.BI_GEMM_ERR_UNSUPPORTED
 
 
-def test_header_symbols_exported():
-    declared = _declared("bi_fp4.h")
-    assert set(declared) == set(bg.FP4_EXPORTED_SYMBOLS)
+@pytest.mark.parametrize("header,names", [("bi_fp4.h", bg.FP4_EXPORTED_SYMBOLS),
+                                          ("bi_attention4.h", bg.ATTENTION4_EXPORTED_SYMBOLS)])
+def test_header_symbols_exported(header, names):
+    declared = _declared(header)
+    assert set(declared) == set(names)
     L = ctypes.CDLL(bgbuild.lib_path("libbi_gemm.so"))
     for name in declared:
         assert hasattr(L, name), name
 
 
-@pytest.mark.parametrize("name", ["bi_quant4_config", "bi_gemm4_config"])
-def test_binding_structs_match_the_header(name):
-    assert [n for _, n in _structs("bi_fp4.h")[name]] == [n for n, _ in getattr(bg, name)._fields_]
-    assert all(t == "int32_t" for t, _ in _structs("bi_fp4.h")[name])
+@pytest.mark.parametrize("header,name", [("bi_fp4.h", "bi_quant4_config"), ("bi_fp4.h", "bi_gemm4_config"),
+                                         ("bi_attention4.h", "bi_attention4_config")])
+def test_binding_structs_match_the_header(header, name):
+    assert [n for _, n in _structs(header)[name]] == [n for n, _ in getattr(bg, name)._fields_]
+    assert all(t == "int32_t" for t, _ in _structs(header)[name])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,scale,ks,vs,split,want", [
+    (0, 8, 128, 16, 0.1, 1, 1, 0, INVALID), (32, 8, 128, 0, 0.1, 1, 1, 0, INVALID), (32, 8, 128, 16, 0.0, 1, 1, 0, INVALID),
+    (32, 8, 128, 16, float("nan"), 1, 1, 0, INVALID), (32, 8, 128, 16, 0.1, 0, 1, 0, INVALID),
+    (32, 8, 128, 16, 0.1, 1, float("inf"), 0, INVALID), (32, 8, 128, 16, 0.1, 1, 2.0 ** 65, 0, INVALID),
+    (32, 8, 128, 16, 0.1, 1, 1, -128, INVALID), (32, 8, 96, 16, 0.1, 1, 1, 0, UNSUPPORTED),
+    (32, 2, 128, 16, 0.1, 1, 1, 0, UNSUPPORTED), (12, 4, 128, 16, 0.1, 1, 1, 0, UNSUPPORTED),
+    (32, 8, 128, 16, 0.1, 1, 1, 64, UNSUPPORTED), (32, 8, 128, 16, 0.1, 1, 1, 8192, UNSUPPORTED),
+    (32, 8, 128, (1 << 20) + 1, 0.1, 1, 1, 0, UNSUPPORTED),
+])
+def test_attention4_create_refuses_before_touching_cuda(Hq, Hkv, D, page, scale, ks, vs, split, want):
+    h = ctypes.c_void_p()
+    assert bg.library().bi_attention4_create(ctypes.byref(h), Hq, Hkv, D, page, scale, ks, vs, split) == want
+    assert h.value is None
 
 
 @pytest.mark.parametrize("K,fmt,g,want", [
@@ -56,6 +74,15 @@ def test_null_arguments():
     assert L.bi_quant4_scale_bytes(None, 1, None) == INVALID
     assert L.bi_quant4_get_config(None, None) == INVALID
     assert L.bi_quant4_destroy(None) == bg.BI_GEMM_OK
+    assert L.bi_attention4_create(None, 32, 8, 128, 16, 0.1, 1.0, 1.0, 0) == INVALID
+    assert L.bi_attention4_run(None, None, 1, *[None] * 6, 1, None, 1, 1, 1, None, None) == INVALID
+    assert L.bi_attention4_expand(None, *[None] * 4, 1, None, 1, None, None, None) == INVALID
+    assert L.bi_attention4_workspace_size(None, 1, 1, None) == INVALID
+    assert L.bi_attention4_get_device_error(None, None) == INVALID
+    assert L.bi_attention4_get_config(None, None) == INVALID
+    assert L.bi_attention4_destroy(None) == bg.BI_GEMM_OK
+    assert L.bi_qkrope_run4(None, None, 1, 6144, None, None, None, 1, *[None] * 6, 1.0, 1.0, 1, None, 1, 1, None,
+                            None) == INVALID
     assert L.bi_gemm4_create(None, 256, 64, 1, 0) == INVALID
     assert L.bi_gemm4_run(None, None, None, 1, None, None, 1.0, None, None) == INVALID
     assert L.bi_gemm4_get_device_error(None, None) == INVALID
