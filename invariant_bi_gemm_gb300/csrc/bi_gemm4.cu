@@ -30,9 +30,12 @@ constexpr int kStageK = 256;              // elements of K a stage: one 128-byte
 constexpr uint64_t kTimeoutNs = biattn_tc::kTimeoutNs;
 
 struct Params {
+  const uint8_t* sx;
+  const uint8_t* sw;
   uint32_t* status;
   int32_t M, N, K;
   int32_t m_tiles, n_tiles, kblocks;
+  int32_t tiles;            // scale tiles along K
   int32_t x_rows;           // rows of an x box
   int32_t group_m;          // raster: M tiles of a group (N tiles vary slowest within it)
   float alpha;
@@ -63,11 +66,56 @@ constexpr __host__ __device__ uint32_t idesc4(int M, int N) {
   return (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (kNv ? 0u : 1u << 23) | (uint32_t(M >> 4) << 24);
 }
 
-// Matrix descriptors: rows of 128 bytes, 128-byte swizzle, groups of 8 rows 1024 bytes apart; a block of scales,
-// 32 rows of 16 bytes, no swizzle.
+// Matrix descriptor: rows of 128 bytes, 128-byte swizzle, groups of 8 rows 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_rows(uint32_t a) { return biattn_tc::sdesc_sw128(a, 16, 1024); }
-__device__ __forceinline__ uint64_t desc_scales(uint32_t a) {
-  return uint64_t((a & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (1ull << 46);
+
+template <bool kNv>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                     uint32_t accumulate) {
+  if constexpr (kNv)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes), counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Scales go to tensor memory through registers: a tile of 128 rows x 4 scales (512 bytes, 16 for each of 32 lanes)
+// becomes four columns, which every quarter of the lanes has to hold.  Four warps write a quarter each.  (tcgen05.cp
+// does it in one instruction, but in the pipe of the MMAs: about 60 clocks a tile, so that 12 tiles for four MMAs
+// made a product of 8192 x 4096 x 14336 take 310 us against 171 without any.)
+// N tiles (2, 4 or 8; the i-th at smem + offset(i)) are read, and become 4 N columns.
+template <int N, class F>
+__device__ __forceinline__ void read_tiles(uint32_t (&w)[4 * N], uint32_t smem, int lane, F offset) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t v[4];
+    biattn_tc::ld_shared_v4(smem + uint32_t(offset(i)) + uint32_t(lane) * 16, v);
+    w[4 * i] = v[0], w[4 * i + 1] = v[1], w[4 * i + 2] = v[2], w[4 * i + 3] = v[3];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_tiles(uint32_t taddr, const uint32_t* w) {
+  if constexpr (N == 8) biattn_tc::tmem_st_x32(taddr, w);
+  else if constexpr (N == 4) biattn_tc::tmem_st_x16(taddr, w);
+  else tmem_st_x8(taddr, w);
 }
 
 // ------------------------------------------------------------------ the form for many rows
@@ -84,7 +132,10 @@ struct Wide {
   static constexpr int SF_COLS = TILES_K * 12;         // TMEM columns of a stage's scales: x 4, w 8 a tile
   static constexpr int SF_COL0 = TN;
   static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "tensor memory");
-  static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, THREADS = 384;
+  // warps: 0 loads, 1 products, 4 .. 7 scales, 8 .. 15 results; the first two warpgroups give registers to the others
+  static constexpr int SF_WARP0 = 4, EPI_WARPS = 8, EPI_WARP0 = 8, THREADS = 512;
+  static constexpr int REGS_LOW = 64, REGS_HIGH = 192;
+  static_assert((REGS_LOW + REGS_HIGH) * 256 <= 65536, "register split exceeds the launch's registers");
   static constexpr int OUT = kF32 ? 4 : 2;
   static constexpr int STG_BYTES = 32 * 32 * OUT;
   static constexpr int STG_BUFS = kF32 ? 1 : 2;
@@ -93,30 +144,35 @@ struct Wide {
   static constexpr int OFF_STG = OFF_SF + STAGES * (SFA_BYTES + SFB_BYTES);
   static_assert(OFF_STG % 1024 == 0, "swizzle atoms");
   static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * STG_BUFS * STG_BYTES;
-  static constexpr int SMEM = OFF_BAR + (2 * STAGES + 3) * 8 + 16 + 1024;
+  static constexpr int BARS = 4 * STAGES + 3;
+  static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                const __grid_constant__ CUtensorMap msx, const __grid_constant__ CUtensorMap msw,
                 const __grid_constant__ CUtensorMap my, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
-  auto full = [&](int s) { return bars + 8u * s; };
-  auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };
-  const uint32_t tfull = bars + 16u * C::STAGES, tempty = tfull + 8, drain = tfull + 16;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + (2 * C::STAGES + 3) * 8);
+  auto full = [&](int s) { return bars + 8u * s; };                        // the leader's: both CTAs' codes are there, and
+                                                                          // their scales in tensor memory
+  auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };         // the stage's products are done
+  auto sfull = [&](int s) { return bars + 8u * (2 * C::STAGES + s); };     // this CTA's scales are in shared memory
+  auto sempty = [&](int s) { return bars + 8u * (3 * C::STAGES + s); };    // and have been read from there
+  const uint32_t tfull = bars + 32u * C::STAGES, tempty = tfull + 8, drain = tfull + 16;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
   volatile uint32_t* gave_up = misc + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const int group = blockIdx.x / 2, groups = gridDim.x / 2, units = p.m_tiles * p.n_tiles;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(full(s), 1 + 8);
       ptx::mbar_init(empty(s), 1);
+      ptx::mbar_init(sfull(s), 1);
+      ptx::mbar_init(sempty(s), 4);
     }
     ptx::mbar_init(tfull, 1);
     ptx::mbar_init(tempty, 2 * C::EPI_WARPS);
@@ -142,13 +198,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     n = r / gm;
     m = g * p.group_m + (r - n * gm);
   };
+  if (warp < C::EPI_WARP0) {
+  ptx::setmaxnreg_dec<C::REGS_LOW>();
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- loads
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const uint32_t x_bytes = uint32_t(p.x_rows) * 128u + C::SFA_BYTES, w_bytes = C::B_BYTES + C::SFB_BYTES;
+    const uint32_t x_bytes = uint32_t(p.x_rows) * 128u;
     for (int u = group; u < units && ok; u += groups) {
       int m, n;
       place(u, m, n);
@@ -161,19 +219,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         if (!p.stall) {
           const uint32_t fb = ptx::mapa_shared(full(s), 0);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), x_bytes * (peers ? 2u : 1u) + 2u * w_bytes);
-          const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
-          if (mine) {
-            ptx::tma_load_2d_pair(base + uint32_t(s) * C::A_BYTES, &mx, fb, kb * 128, row0);
-            ptx::tma_load_2d_pair(sf, &msx, fb, kb * (C::TILES_K * 64), row0 / 128);
-          }
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), x_bytes * (peers ? 2u : 1u) + 2u * C::B_BYTES);
+          if (mine) ptx::tma_load_2d_pair(base + uint32_t(s) * C::A_BYTES, &mx, fb, kb * 128, row0);
           ptx::tma_load_2d_pair(base + C::OFF_B + uint32_t(s) * C::B_BYTES, &mw, fb, kb * 128, col0 + int(rank) * 128);
-          ptx::tma_load_2d_pair(sf + C::SFA_BYTES, &msw, fb, kb * (C::TILES_K * 64), col0 / 128);
         }
         if (++s == C::STAGES) s = 0, ph ^= 1u;
       }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (warp == 2 && lane == 0) {
+    // ---------------------------------------------------------------- scales, in a ring of their own: a stage of them is free
+    // as soon as it has been read, so that they are ahead of the codes and their way through the registers is
+    // not in the products' (one ring for both: 310 us for 8192 x 4096 x 14336)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = group; u < units && ok; u += groups) {
+      int m, n;
+      place(u, m, n);
+      const int row0 = m * C::TM + int(rank) * 128, col0 = n * C::TN;
+      const bool mine = row0 < p.M, wide = col0 + 128 < p.N;          // tiles of rows past M and N are not there
+      const uint8_t* sx = p.sx + int64_t(row0 / 128) * p.tiles * 512;
+      const uint8_t* sw = p.sw + int64_t(col0 / 128) * p.tiles * 512;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!wait_bar(sempty(s), ph ^ 1u, sy)) {
+          ok = false;
+          break;
+        }
+        if (!p.stall) {
+          const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
+          const int t0 = kb * C::TILES_K;
+          const uint32_t bytes = uint32_t(min(C::TILES_K, p.tiles - t0)) * 512u;
+          ptx::mbar_arrive_expect_tx(sfull(s), bytes * (1u + (mine ? 1u : 0u) + (wide ? 1u : 0u)));
+          if (mine) bulk_load(sf, sx + int64_t(t0) * 512, bytes, sfull(s));
+          bulk_load(sf + C::SFA_BYTES, sw + int64_t(t0) * 512, bytes, sfull(s));
+          if (wide) bulk_load(sf + C::SFA_BYTES + C::TILES_K * 512, sw + (int64_t(p.tiles) + t0) * 512, bytes, sfull(s));
+        }
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+    }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---------------------------------------------------------------- products (leader)
     int s = 0;
@@ -193,17 +278,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         ptx::tc_fence_after();
         const uint32_t a = base + uint32_t(s) * C::A_BYTES, b = base + C::OFF_B + uint32_t(s) * C::B_BYTES;
-        const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
         const uint32_t ta = tmem + C::SF_COL0 + uint32_t(s) * C::SF_COLS, tb = ta + C::TILES_K * 4;
-        // scales: x's tiles of this CTA's rows, w's of all 256 columns (a tile's halves side by side)
-#pragma unroll
-        for (int t = 0; t < C::TILES_K; ++t) {
-          ptx::tc_cp_32x128b_x4_pair(ta + 4u * t, desc_scales(sf + 512u * t));
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            ptx::tc_cp_32x128b_x4_pair(tb + 8u * t + 4u * h,
-                                       desc_scales(sf + C::SFA_BYTES + uint32_t(h * C::TILES_K + t) * 512u));
-        }
         const int steps = min(4, (p.K - kb * kStageK) / 64);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -226,7 +301,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
       volatile uint32_t never = 0;
       wait_bar(drain, 0u, Sync{&never, p.status, p.timeout_ns});
     }
-  } else if (warp >= C::EPI_WARP0) {
+  } else if (warp >= C::SF_WARP0) {
+    // ---------------------------------------------------------------- scales to tensor memory: x's tiles of this CTA's rows,
+    // w's of all 256 columns (a tile's halves side by side)
+    const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = group; u < units && ok; u += groups) {
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(sfull(s), ph, sy));
+        if (!ok) break;
+        const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
+        const uint32_t ta = tmem + quarter + C::SF_COL0 + uint32_t(s) * C::SF_COLS, tb = ta + C::TILES_K * 4;
+        uint32_t wa[4 * C::TILES_K], wb[8 * C::TILES_K];
+        read_tiles<C::TILES_K>(wa, sf, lane, [](int i) { return i * 512; });
+        read_tiles<2 * C::TILES_K>(wb, sf + C::SFA_BYTES, lane,
+                                   [](int i) { return ((i & 1) * C::TILES_K + (i >> 1)) * 512; });
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sempty(s));
+        // the columns' last products are done
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(empty(s), ph ^ 1u, sy));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        store_tiles<C::TILES_K>(ta, wa);
+        store_tiles<2 * C::TILES_K>(tb, wb);
+        biattn_tc::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::fence_release_shared();
+          ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(full(s), 0));
+        }
+        if (++s == C::STAGES) s = 0, ph ^= 1u;
+      }
+    }
+  }
+  } else {
+    ptx::setmaxnreg_inc<C::REGS_HIGH>();
     // ---------------------------------------------------------------- results
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int e = warp - C::EPI_WARP0, q = warp & 3, half = e >> 2;
@@ -301,6 +413,250 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
+// ------------------------------------------------------------------ the form for few rows
+//
+// The operands change places: rows of w on the 128 rows of the MMA, up to 256 rows of x on its columns, so that a CTA
+// alone takes 32, 64 or 128 columns of y and as many of them as there are SMs share the reading of w.  The sums have the
+// wide form's bits: an element is the same sequence of 64-element products, and neither the place of its row and
+// column in an instruction nor the instruction's extent enters (compared over every shape that the tests run).
+//
+// A CTA's R rows of w take the MMA's rows that they have in their tile of 128 (so that a tile of scales serves as it
+// is); the other rows multiply whatever the neighbouring stages hold, and are not stored.
+
+constexpr int kFewMaxStages = 14;
+constexpr int kFewThreads = 256;          // warps: 0 loads, 1 products, 4 .. 7 scales and results
+
+struct FewParams {
+  Params p;
+  int32_t rows;             // R
+  int32_t cols;             // columns of the MMA: rows of x of a tile, a multiple of 16
+  int32_t stages;
+  int32_t tmem_cols;
+  int32_t off_w, off_sf, off_stg, off_bar;   // shared memory: x ring at 0, w ring, scales ring, staging, barriers
+  int32_t sf_x;             // bytes of a stage's scales of x (behind those of w)
+};
+
+template <bool kNv, bool kF32>
+struct Few {
+  static constexpr int TILES_K = kNv ? 4 : 2;
+  static constexpr int OUT = kF32 ? 4 : 2, STG_BYTES = 32 * 32 * OUT;      // of a warp
+};
+
+template <bool kNv, bool kF32>
+__global__ void __launch_bounds__(kFewThreads)
+    few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+               const __grid_constant__ CUtensorMap my, const FewParams f) {
+  using C = Few<kNv, kF32>;
+  const Params& p = f.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = ptx::smem_u32(smem), bars = base + uint32_t(f.off_bar);
+  const int NS = f.stages;
+  auto full = [&](int s) { return bars + 8u * s; };                        // codes and scales are in shared memory
+  auto ready = [&](int s) { return bars + 8u * (kFewMaxStages + s); };     // and the scales in tensor memory
+  auto empty = [&](int s) { return bars + 8u * (2 * kFewMaxStages + s); }; // the stage's products are done
+  const uint32_t tfull = bars + 24u * kFewMaxStages, tempty = tfull + 8, drain = tfull + 16;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + f.off_bar + (3 * kFewMaxStages + 3) * 8);
+  volatile uint32_t* gave_up = misc + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = p.m_tiles * p.n_tiles;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      ptx::mbar_init(full(s), 1);
+      ptx::mbar_init(ready(s), 4);
+      ptx::mbar_init(empty(s), 1);
+    }
+    ptx::mbar_init(tfull, 1);
+    ptx::mbar_init(tempty, 4);
+    ptx::mbar_init(drain, 1);
+    *gave_up = 0u;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(misc), uint32_t(f.tmem_cols));
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const Sync sy{gave_up, p.status, p.timeout_ns};
+  const uint32_t sf_bytes = C::TILES_K * 512u + uint32_t(f.sf_x);          // of a stage
+  const uint32_t sf_col0 = uint32_t(f.cols), sf_cols = C::TILES_K * (f.cols > 128 ? 12u : 8u);
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- loads
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const int n = u / p.m_tiles, row0 = (u - n * p.m_tiles) * f.cols, col0 = n * f.rows;
+      const uint8_t* sx = p.sx + int64_t(row0 / 128) * p.tiles * 512;
+      const uint8_t* sw = p.sw + int64_t(col0 / 128) * p.tiles * 512;
+      const int left = p.M - row0;
+      const bool second = f.cols > 128 && left > 128;
+      // few rows' scales are the first bytes of their tile (16 a row up to 32 rows)
+      const uint32_t part = left <= 32 ? uint32_t(left) * 16u : 512u;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!wait_bar(empty(s), ph ^ 1u, sy)) {
+          ok = false;
+          break;
+        }
+        if (!p.stall) {
+          const int t0 = kb * C::TILES_K, nt = min(C::TILES_K, p.tiles - t0);
+          const uint32_t bytes = uint32_t(nt) * 512u, sf = base + uint32_t(f.off_sf) + uint32_t(s) * sf_bytes;
+          ptx::mbar_arrive_expect_tx(full(s), uint32_t(p.x_rows + f.rows) * 128u + bytes + uint32_t(nt) * part +
+                                                  (second ? bytes : 0u));
+          ptx::tma_load_2d(base + uint32_t(f.off_w) + uint32_t(s * f.rows) * 128u, &mw, full(s), kb * 128, col0);
+          ptx::tma_load_2d(base + uint32_t(s * f.cols) * 128u, &mx, full(s), kb * 128, row0);
+          bulk_load(sf, sw + int64_t(t0) * 512, bytes, full(s));
+          const uint32_t sfx = sf + C::TILES_K * 512u;
+          if (part == 512u) {
+            bulk_load(sfx, sx + int64_t(t0) * 512, bytes, full(s));
+          } else {
+            for (int t = 0; t < nt; ++t) bulk_load(sfx + uint32_t(t) * 512u, sx + int64_t(t0 + t) * 512, part, full(s));
+          }
+          if (second) bulk_load(sfx + C::TILES_K * 512u, sx + (int64_t(p.tiles) + t0) * 512, bytes, full(s));
+        }
+        if (++s == NS) s = 0, ph ^= 1u;
+      }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  } else if (warp == 1 && lane == 0) {
+    // ---------------------------------------------------------------- products
+    int s = 0;
+    uint32_t ph = 0, tph = 0;
+    bool ok = true, issued = false;
+    const uint32_t id0 = idesc4<kNv>(128, 0) | (uint32_t(f.cols >> 3) << 17);
+    const uint32_t wide = f.cols > 128 ? 8u : 4u;          // columns of a tile of x's scales
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const int col0 = u / p.m_tiles * f.rows;
+      if (!wait_bar(tempty, tph ^ 1u, sy)) {
+        ok = false;
+        break;
+      }
+      tph ^= 1u;
+      ptx::tc_fence_after();
+      const uint32_t shift = uint32_t(col0 & 127) * 128u;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!wait_bar(full(s), ph, sy) || !wait_bar(ready(s), ph, sy)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t a = base + uint32_t(f.off_w) + uint32_t(s * f.rows) * 128u - shift, b = base + uint32_t(s * f.cols) * 128u;
+        const uint32_t ta = tmem + sf_col0 + uint32_t(s) * sf_cols, tb = ta + C::TILES_K * 4;
+        const int steps = min(4, (p.K - kb * kStageK) / 64);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k < steps) {
+            const int t = kNv ? k : k >> 1;
+            const uint32_t id = kNv ? 0u : uint32_t(k & 1) * 2u;
+            mma4<kNv>(tmem, desc_rows(a + 32u * k), desc_rows(b + 32u * k), id0 | (id << 4) | (id << 29), ta + 4u * t,
+                      tb + wide * t, kb != 0 || k != 0 ? 1u : 0u);
+          }
+        }
+        issued = true;
+        ptx::tc_commit(empty(s));
+        if (++s == NS) s = 0, ph ^= 1u;
+      }
+      if (ok) ptx::tc_commit(tfull);
+    }
+    if (!ok && issued) {                 // what was issued ends before TMEM is released
+      ptx::tc_commit(drain);
+      volatile uint32_t never = 0;
+      wait_bar(drain, 0u, Sync{&never, p.status, p.timeout_ns});
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- scales to tensor memory, then the unit's results
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int q = warp - 4;
+    const uint32_t quarter = uint32_t(q * 32) << 16, stg = base + uint32_t(f.off_stg + q * C::STG_BYTES);
+    int s = 0;
+    uint32_t ph = 0, tph = 0;
+    bool ok = true, stored = false;
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(full(s), ph, sy));
+        if (!ok) break;
+        const uint32_t sf = base + uint32_t(f.off_sf) + uint32_t(s) * sf_bytes, sfx = sf + C::TILES_K * 512u;
+        const uint32_t ta = tmem + quarter + sf_col0 + uint32_t(s) * sf_cols, tb = ta + C::TILES_K * 4;
+        uint32_t wa[4 * C::TILES_K], wb[4 * C::TILES_K];
+        read_tiles<C::TILES_K>(wa, sf, lane, [](int i) { return i * 512; });
+        if (f.cols <= 128) {
+          read_tiles<C::TILES_K>(wb, sfx, lane, [](int i) { return i * 512; });
+          store_tiles<C::TILES_K>(ta, wa);
+          store_tiles<C::TILES_K>(tb, wb);
+        } else {
+          uint32_t w2[8 * C::TILES_K];
+          read_tiles<2 * C::TILES_K>(w2, sfx, lane, [](int i) { return ((i & 1) * C::TILES_K + (i >> 1)) * 512; });
+          store_tiles<C::TILES_K>(ta, wa);
+          store_tiles<2 * C::TILES_K>(tb, w2);
+        }
+        biattn_tc::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ready(s));
+        if (++s == NS) s = 0, ph ^= 1u;
+      }
+      if (!ok) break;
+      const int n = u / p.m_tiles, row0 = (u - n * p.m_tiles) * f.cols, col0 = n * f.rows;
+      if (!__all_sync(0xFFFFFFFFu, wait_bar(tfull, tph, sy))) break;
+      tph ^= 1u;
+      ptx::tc_fence_after();
+      // this warp's 32 rows of the MMA are columns of y where they are the CTA's
+      const int col = (col0 & ~127) + q * 32;
+      const bool mine = col >= col0 && col < col0 + f.rows && col < p.N;
+      const int chunks = mine ? (min(f.cols, p.M - row0) + 31) / 32 : 0;
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t r[32];
+        ptx::tmem_ld_32x32b_x32(tmem + quarter + 32u * c, r);
+        ptx::tmem_wait_ld();
+        if (lane == 0 && stored) ptx::bulk_wait_read<0>();
+        __syncwarp();
+        // a lane has a column of y: 32 of its rows
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float v = __fmul_rn(__uint_as_float(r[i]), p.alpha);
+          if constexpr (kF32) {
+            ptx::st_shared_u32(stg + uint32_t(i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4), __float_as_uint(v));
+          } else {
+            const uint16_t h = uint16_t(ptx::pack_bf16x2(v, v));
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(stg + uint32_t(i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2)),
+                         "h"(h)
+                         : "memory");
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(&my, stg, col, row0 + 32 * c);
+          ptx::bulk_commit();
+        }
+        stored = true;
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(tempty);
+    }
+    if (lane == 0) ptx::bulk_wait_read<0>();
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *gave_up) {    // let every copy in flight land before the block leaves
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < 2000000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, uint32_t(f.tmem_cols));
+  }
+}
+
 // ------------------------------------------------------------------ host
 
 // A matrix of `rows` x `cols` elements, rows `pitch` bytes apart, in boxes of box_rows x box_cols.
@@ -315,16 +671,17 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* at, uint64_t r
 
 struct Kernel {
   const void* wide = nullptr;
-  int wide_smem = 0, stages = 0, tiles_k = 0;
+  const void* few = nullptr;
+  int wide_smem = 0, stages = 0;
 };
 template <bool kNv, bool kF32>
 Kernel kernel() {
   using W = Wide<kNv, kF32>;
   Kernel k;
   k.wide = reinterpret_cast<const void*>(&wide_kernel<W>);
+  k.few = reinterpret_cast<const void*>(&few_kernel<kNv, kF32>);
   k.wide_smem = W::SMEM;
   k.stages = W::STAGES;
-  k.tiles_k = W::TILES_K;
   return k;
 }
 inline Kernel select(bool nv, bool f32) {
@@ -332,12 +689,37 @@ inline Kernel select(bool nv, bool f32) {
   return f32 ? kernel<false, true>() : kernel<false, false>();
 }
 
+constexpr int kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024;
+
+// Layout of the form for few rows with `per_sm` CTAs an SM: as deep a ring as shared and tensor memory hold; its
+// bytes of shared memory, 0 where fewer than three stages fit.
+int few_layout(FewParams& f, bool nv, bool f32, int per_sm) {
+  const int tiles = nv ? 4 : 2, sf_cols = tiles * (f.cols > 128 ? 12 : 8);
+  f.tmem_cols = 512 / (per_sm > 2 ? 4 : per_sm);
+  f.sf_x = tiles * 512 * (f.cols > 128 ? 2 : 1);
+  const int stg = 4 * 32 * 32 * (f32 ? 4 : 2), bar = (3 * kFewMaxStages + 3) * 8 + 16;
+  const int stage = (f.cols + f.rows) * 128 + tiles * 512 + f.sf_x;
+  const int room = std::min(kSmemBlock, kSmemSm / per_sm - 1024) - 1024 - stg - bar;
+  // The MMA reads 128 rows around a CTA's own: up to 128 - R before the ring of w (the x ring, filled up to them) and
+  // behind it.
+  const int margin = (128 - f.rows) * 128;
+  f.stages = std::min(std::min(kFewMaxStages, (f.tmem_cols - f.cols) / sf_cols), room / stage);
+  for (; f.stages >= 3; --f.stages) {
+    f.off_w = std::max(f.stages * f.cols * 128, margin);
+    f.off_sf = f.off_w + f.stages * f.rows * 128;
+    f.off_stg = (f.off_sf + std::max(f.stages * (tiles * 512 + f.sf_x), margin) + 1023) / 1024 * 1024;
+    f.off_bar = f.off_stg + stg;
+    if (f.off_bar + bar - stg - bar <= room) return f.off_bar + bar + 1024;
+  }
+  return 0;
+}
+
 }  // namespace big4
 
 struct bi_gemm4 {
   int64_t K = 0, N = 0;
   bool nv = false, f32 = false;
-  int device = 0, max_groups = 0;
+  int device = 0, max_groups = 0, sms = 0;
   big4::Kernel kern;
   uint32_t* d_status = nullptr;
 };
@@ -353,7 +735,8 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
   if (!biattn_tc::encode_fn()) return BI_GEMM_ERR_CUDA;
   const big4::Kernel k = big4::select(format == BI_NVFP4, out_f32 != 0);
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaFuncSetAttribute(k.wide, cudaFuncAttributeMaxDynamicSharedMemorySize, k.wide_smem) != cudaSuccess) {
+      cudaFuncSetAttribute(k.wide, cudaFuncAttributeMaxDynamicSharedMemorySize, k.wide_smem) != cudaSuccess ||
+      cudaFuncSetAttribute(k.few, cudaFuncAttributeMaxDynamicSharedMemorySize, big4::kSmemBlock) != cudaSuccess) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -365,11 +748,12 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
   h->f32 = out_f32 != 0;
   h->device = dev;
   h->kern = k;
+  h->sms = sms;
   // pairs that are resident at once (a pair needs two SMs of one cluster)
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(unsigned(sms / 2 * 2));
-  cfg.blockDim = dim3(384);
+  cfg.blockDim = dim3(512);
   cfg.dynamicSmemBytes = size_t(k.wide_smem);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -393,6 +777,18 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
 
 namespace {
 
+// Whether a call of M rows takes the form for few rows, and its layout.  Both forms give the same bits.
+bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, int& smem) {
+  if (M > 256) return false;
+  f.cols = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  f.rows = 128;
+  while (f.rows > 32 && (h->N + f.rows - 1) / f.rows < h->sms * 9 / 10) f.rows /= 2;
+  const int64_t units = (h->N + f.rows - 1) / f.rows;
+  per_sm = units > h->sms && f.cols <= 128 ? 2 : 1;
+  smem = big4::few_layout(f, h->nv, h->f32, per_sm);
+  return smem > 0;
+}
+
 // bi_gemm4_run with the failure injection of the test controls (stall: nothing is loaded) and the limit of
 // the waits.
 int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void* w, const void* sw, float alpha, void* y,
@@ -410,51 +806,53 @@ int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void*
     return BI_GEMM_ERR_CUDA;
   }
   if (dev != h->device) return BI_GEMM_ERR_INVALID_ARG;
-  const int64_t m_tiles = (M + 255) / 256, n_tiles = (h->N + 255) / 256;
-  if (m_tiles * n_tiles >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
-  big4::Params p;
-  std::memset(&p, 0, sizeof(p));
+  using namespace big4;
+  FewParams f;
+  std::memset(&f, 0, sizeof(f));
+  Params& p = f.p;
+  p.sx = static_cast<const uint8_t*>(sx);
+  p.sw = static_cast<const uint8_t*>(sw);
   p.status = h->d_status;
   p.M = int32_t(M);
   p.N = int32_t(h->N);
   p.K = int32_t(h->K);
-  p.m_tiles = int32_t(m_tiles);
-  p.n_tiles = int32_t(n_tiles);
-  p.kblocks = int32_t((h->K + big4::kStageK - 1) / big4::kStageK);
-  p.x_rows = int32_t(std::min<int64_t>(128, (M + 7) / 8 * 8));
+  p.kblocks = int32_t((h->K + kStageK - 1) / kStageK);
+  p.tiles = int32_t(h->K / (h->nv ? 64 : 128));
   p.group_m = 16;
   p.alpha = alpha;
   p.stall = stall;
   p.timeout_ns = timeout_ns;
-  const uint64_t tiles = uint64_t(h->K) / (h->nv ? 64 : 128);     // scale tiles of a row of tiles
-  const uint32_t tiles_k = uint32_t(h->kern.tiles_k);
-  CUtensorMap mx, mw, msx, msw, my;
-  using namespace big4;
+  int per_sm = 0, smem = 0;
+  const bool few = few_choice(h, M, f, per_sm, smem);
+  const int64_t m_tiles = few ? (M + f.cols - 1) / f.cols : (M + 255) / 256;
+  const int64_t n_tiles = few ? (h->N + f.rows - 1) / f.rows : (h->N + 255) / 256;
+  if (m_tiles * n_tiles >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  p.m_tiles = int32_t(m_tiles);
+  p.n_tiles = int32_t(n_tiles);
+  p.x_rows = int32_t(std::min<int64_t>(few ? f.cols : 128, (M + 7) / 8 * 8));
+  CUtensorMap mx, mw, my;
   if (!encode(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, uint64_t(M), uint64_t(h->K / 2), uint64_t(h->K / 2),
               uint32_t(p.x_rows), 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, uint64_t(h->N), uint64_t(h->K / 2), uint64_t(h->K / 2), 128, 128,
-              CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode(&msx, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, sx, uint64_t((M + 127) / 128), tiles * 64, tiles * 512, 1,
-              tiles_k * 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode(&msw, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, sw, uint64_t((h->N + 127) / 128), tiles * 64, tiles * 512, 2,
-              tiles_k * 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, uint64_t(h->N), uint64_t(h->K / 2), uint64_t(h->K / 2),
+              few ? uint32_t(f.rows) : 128u, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&my, h->f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, uint64_t(M),
               uint64_t(h->N), uint64_t(h->N) * (h->f32 ? 4 : 2), 32, 32,
               h->f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return BI_GEMM_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(m_tiles * n_tiles, h->max_groups)));
-  cfg.blockDim = dim3(384);
-  cfg.dynamicSmemBytes = size_t(h->kern.wide_smem);
+  cfg.gridDim = dim3(unsigned(few ? std::min<int64_t>(m_tiles * n_tiles, int64_t(per_sm) * h->sms)
+                                  : 2 * std::min<int64_t>(m_tiles * n_tiles, h->max_groups)));
+  cfg.blockDim = dim3(few ? kFewThreads : 512);
+  cfg.dynamicSmemBytes = size_t(few ? smem : h->kern.wide_smem);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* args[6] = {&mx, &mw, &msx, &msw, &my, &p};
-  if (cudaLaunchKernelExC(&cfg, h->kern.wide, args) != cudaSuccess) {
+  void* args[4] = {&mx, &mw, &my, few ? static_cast<void*>(&f) : static_cast<void*>(&p)};
+  if (cudaLaunchKernelExC(&cfg, few ? h->kern.few : h->kern.wide, args) != cudaSuccess) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -483,6 +881,7 @@ BI_GEMM_API int bi_gemm4_get_config(bi_gemm4_t h, bi_gemm4_config* c) {
   c->tile_rows = c->tile_cols = 256;
   c->stages = h->kern.stages;
   c->max_groups = h->max_groups;
+  c->few_rows = 256;
   c->smem_bytes = h->kern.wide_smem;
   return BI_GEMM_OK;
 }
