@@ -81,8 +81,8 @@ typedef struct {
   int32_t K, N, format, out_f32;
   int32_t tile_rows, tile_cols;  /* of y per CTA pair, and                                    */
   int32_t stages, max_groups;    /* the pipeline's depth and the pairs at most                 */
-  int32_t few_rows;              /* up to this M the form for few rows runs: the same bits     */
-  int32_t few_cols;              /* and its columns of y per CTA                               */
+  int32_t few_rows;              /* up to this M, and for larger ones whose tiles are no more
+                                    than the SMs, a form of smaller tiles runs: the same bits  */
   int32_t smem_bytes;
 } bi_gemm4_config;
 

@@ -128,7 +128,7 @@ class bi_quant4_config(ctypes.Structure):
 
 class bi_gemm4_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("K", "N", "format", "out_f32", "tile_rows", "tile_cols", "stages",
-                                              "max_groups", "few_rows", "few_cols", "smem_bytes")]
+                                              "max_groups", "few_rows", "smem_bytes")]
 
 
 class bi_attention4_config(ctypes.Structure):

@@ -68,6 +68,10 @@ constexpr __host__ __device__ uint32_t idesc4(int M, int N) {
 
 // Matrix descriptor: rows of 128 bytes, 128-byte swizzle, groups of 8 rows 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_rows(uint32_t a) { return biattn_tc::sdesc_sw128(a, 16, 1024); }
+// A tile of scales, 32 rows of 16 bytes, no swizzle: tcgen05.cp makes four columns of it.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t a) {
+  return uint64_t((a & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (1ull << 46);
+}
 
 template <bool kNv>
 __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -92,32 +96,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// Scales go to tensor memory through registers: a tile of 128 rows x 4 scales (512 bytes, 16 for each of 32 lanes)
-// becomes four columns, which every quarter of the lanes has to hold.  Four warps write a quarter each.  (tcgen05.cp
-// does it in one instruction, but in the pipe of the MMAs: about 60 clocks a tile, so that 12 tiles for four MMAs
-// made a product of 8192 x 4096 x 14336 take 310 us against 171 without any.)
-// N tiles (2, 4 or 8; the i-th at smem + offset(i)) are read, and become 4 N columns.
-template <int N, class F>
-__device__ __forceinline__ void read_tiles(uint32_t (&w)[4 * N], uint32_t smem, int lane, F offset) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t v[4];
-    biattn_tc::ld_shared_v4(smem + uint32_t(offset(i)) + uint32_t(lane) * 16, v);
-    w[4 * i] = v[0], w[4 * i + 1] = v[1], w[4 * i + 2] = v[2], w[4 * i + 3] = v[3];
-  }
-}
-template <int N>
-__device__ __forceinline__ void store_tiles(uint32_t taddr, const uint32_t* w) {
-  if constexpr (N == 8) biattn_tc::tmem_st_x32(taddr, w);
-  else if constexpr (N == 4) biattn_tc::tmem_st_x16(taddr, w);
-  else tmem_st_x8(taddr, w);
-}
-
 // ------------------------------------------------------------------ the form for many rows
 
 template <bool kNv_, bool kF32_>
@@ -132,10 +110,7 @@ struct Wide {
   static constexpr int SF_COLS = TILES_K * 12;         // TMEM columns of a stage's scales: x 4, w 8 a tile
   static constexpr int SF_COL0 = TN;
   static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "tensor memory");
-  // warps: 0 loads, 1 products, 4 .. 7 scales, 8 .. 15 results; the first two warpgroups give registers to the others
-  static constexpr int SF_WARP0 = 4, EPI_WARPS = 8, EPI_WARP0 = 8, THREADS = 512;
-  static constexpr int REGS_LOW = 64, REGS_HIGH = 192;
-  static_assert((REGS_LOW + REGS_HIGH) * 256 <= 65536, "register split exceeds the launch's registers");
+  static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, THREADS = 384;       // warps: 0 loads, 1 products, 4 .. results
   static constexpr int OUT = kF32 ? 4 : 2;
   static constexpr int STG_BYTES = 32 * 32 * OUT;
   static constexpr int STG_BUFS = kF32 ? 1 : 2;
@@ -144,7 +119,7 @@ struct Wide {
   static constexpr int OFF_STG = OFF_SF + STAGES * (SFA_BYTES + SFB_BYTES);
   static_assert(OFF_STG % 1024 == 0, "swizzle atoms");
   static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * STG_BUFS * STG_BYTES;
-  static constexpr int BARS = 4 * STAGES + 3;
+  static constexpr int BARS = 2 * STAGES + 3;
   static constexpr int SMEM = OFF_BAR + BARS * 8 + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory");
 };
@@ -152,27 +127,26 @@ struct Wide {
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     wide_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                const __grid_constant__ CUtensorMap msx, const __grid_constant__ CUtensorMap msw,
                 const __grid_constant__ CUtensorMap my, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = ptx::smem_u32(smem), bars = base + C::OFF_BAR;
-  auto full = [&](int s) { return bars + 8u * s; };                        // the leader's: both CTAs' codes are there, and
-                                                                          // their scales in tensor memory
+  auto full = [&](int s) { return bars + 8u * s; };                        // the leader's: both CTAs' operands are there
   auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };         // the stage's products are done
-  auto sfull = [&](int s) { return bars + 8u * (2 * C::STAGES + s); };     // this CTA's scales are in shared memory
-  auto sempty = [&](int s) { return bars + 8u * (3 * C::STAGES + s); };    // and have been read from there
-  const uint32_t tfull = bars + 32u * C::STAGES, tempty = tfull + 8, drain = tfull + 16;
+  const uint32_t tfull = bars + 16u * C::STAGES, tempty = tfull + 8, drain = tfull + 16;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::BARS * 8);
   volatile uint32_t* gave_up = misc + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
+  // One lane of a warp loads, or issues the products.  elect.sync names it: the compiler then keeps the operands of
+  // TMA and MMA instructions in uniform registers (with `lane == 0` a product cost about 180 clocks to issue).
+  const bool lead = biattn_tc::elect_one();
   const int group = blockIdx.x / 2, groups = gridDim.x / 2, units = p.m_tiles * p.n_tiles;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full(s), 1 + 8);
+      ptx::mbar_init(full(s), 1);
       ptx::mbar_init(empty(s), 1);
-      ptx::mbar_init(sfull(s), 1);
-      ptx::mbar_init(sempty(s), 4);
     }
     ptx::mbar_init(tfull, 1);
     ptx::mbar_init(tempty, 2 * C::EPI_WARPS);
@@ -198,15 +172,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     n = r / gm;
     m = g * p.group_m + (r - n * gm);
   };
-  if (warp < C::EPI_WARP0) {
-  ptx::setmaxnreg_dec<C::REGS_LOW>();
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && lead) {
     // ---------------------------------------------------------------- loads
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const uint32_t x_bytes = uint32_t(p.x_rows) * 128u;
+    const uint32_t x_bytes = uint32_t(p.x_rows) * 128u + C::SFA_BYTES, w_bytes = C::B_BYTES + C::SFB_BYTES;
     for (int u = group; u < units && ok; u += groups) {
       int m, n;
       place(u, m, n);
@@ -219,47 +191,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         if (!p.stall) {
           const uint32_t fb = ptx::mapa_shared(full(s), 0);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), x_bytes * (peers ? 2u : 1u) + 2u * C::B_BYTES);
-          if (mine) ptx::tma_load_2d_pair(base + uint32_t(s) * C::A_BYTES, &mx, fb, kb * 128, row0);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), x_bytes * (peers ? 2u : 1u) + 2u * w_bytes);
+          const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
+          if (mine) {
+            ptx::tma_load_2d_pair(base + uint32_t(s) * C::A_BYTES, &mx, fb, kb * 128, row0);
+            ptx::tma_load_2d_pair(sf, &msx, fb, kb * (C::TILES_K * 64), row0 / 128);
+          }
           ptx::tma_load_2d_pair(base + C::OFF_B + uint32_t(s) * C::B_BYTES, &mw, fb, kb * 128, col0 + int(rank) * 128);
+          ptx::tma_load_2d_pair(sf + C::SFA_BYTES, &msw, fb, kb * (C::TILES_K * 64), col0 / 128);
         }
         if (++s == C::STAGES) s = 0, ph ^= 1u;
       }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  } else if (warp == 2 && lane == 0) {
-    // ---------------------------------------------------------------- scales, in a ring of their own: a stage of them is free
-    // as soon as it has been read, so that they are ahead of the codes and their way through the registers is
-    // not in the products' (one ring for both: 310 us for 8192 x 4096 x 14336)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int u = group; u < units && ok; u += groups) {
-      int m, n;
-      place(u, m, n);
-      const int row0 = m * C::TM + int(rank) * 128, col0 = n * C::TN;
-      const bool mine = row0 < p.M, wide = col0 + 128 < p.N;          // tiles of rows past M and N are not there
-      const uint8_t* sx = p.sx + int64_t(row0 / 128) * p.tiles * 512;
-      const uint8_t* sw = p.sw + int64_t(col0 / 128) * p.tiles * 512;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        if (!wait_bar(sempty(s), ph ^ 1u, sy)) {
-          ok = false;
-          break;
-        }
-        if (!p.stall) {
-          const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
-          const int t0 = kb * C::TILES_K;
-          const uint32_t bytes = uint32_t(min(C::TILES_K, p.tiles - t0)) * 512u;
-          ptx::mbar_arrive_expect_tx(sfull(s), bytes * (1u + (mine ? 1u : 0u) + (wide ? 1u : 0u)));
-          if (mine) bulk_load(sf, sx + int64_t(t0) * 512, bytes, sfull(s));
-          bulk_load(sf + C::SFA_BYTES, sw + int64_t(t0) * 512, bytes, sfull(s));
-          if (wide) bulk_load(sf + C::SFA_BYTES + C::TILES_K * 512, sw + (int64_t(p.tiles) + t0) * 512, bytes, sfull(s));
-        }
-        if (++s == C::STAGES) s = 0, ph ^= 1u;
-      }
-    }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && lead && rank == 0) {
     // ---------------------------------------------------------------- products (leader)
     int s = 0;
     uint32_t ph = 0, tph = 0;
@@ -278,7 +223,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         ptx::tc_fence_after();
         const uint32_t a = base + uint32_t(s) * C::A_BYTES, b = base + C::OFF_B + uint32_t(s) * C::B_BYTES;
+        const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
         const uint32_t ta = tmem + C::SF_COL0 + uint32_t(s) * C::SF_COLS, tb = ta + C::TILES_K * 4;
+        // scales: x's tiles of each CTA's rows, w's of all 256 columns (a tile's halves side by side)
+#pragma unroll
+        for (int t = 0; t < C::TILES_K; ++t) {
+          ptx::tc_cp_32x128b_x4_pair(ta + 4u * t, desc_scales(sf + 512u * t));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            ptx::tc_cp_32x128b_x4_pair(tb + 8u * t + 4u * h,
+                                       desc_scales(sf + C::SFA_BYTES + uint32_t(h * C::TILES_K + t) * 512u));
+        }
         const int steps = min(4, (p.K - kb * kStageK) / 64);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -301,44 +256,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
       volatile uint32_t never = 0;
       wait_bar(drain, 0u, Sync{&never, p.status, p.timeout_ns});
     }
-  } else if (warp >= C::SF_WARP0) {
-    // ---------------------------------------------------------------- scales to tensor memory: x's tiles of this CTA's rows,
-    // w's of all 256 columns (a tile's halves side by side)
-    const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
-    int s = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int u = group; u < units && ok; u += groups) {
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(sfull(s), ph, sy));
-        if (!ok) break;
-        const uint32_t sf = base + C::OFF_SF + uint32_t(s) * (C::SFA_BYTES + C::SFB_BYTES);
-        const uint32_t ta = tmem + quarter + C::SF_COL0 + uint32_t(s) * C::SF_COLS, tb = ta + C::TILES_K * 4;
-        uint32_t wa[4 * C::TILES_K], wb[8 * C::TILES_K];
-        read_tiles<C::TILES_K>(wa, sf, lane, [](int i) { return i * 512; });
-        read_tiles<2 * C::TILES_K>(wb, sf + C::SFA_BYTES, lane,
-                                   [](int i) { return ((i & 1) * C::TILES_K + (i >> 1)) * 512; });
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(sempty(s));
-        // the columns' last products are done
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(empty(s), ph ^ 1u, sy));
-        if (!ok) break;
-        ptx::tc_fence_after();
-        store_tiles<C::TILES_K>(ta, wa);
-        store_tiles<2 * C::TILES_K>(tb, wb);
-        biattn_tc::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::fence_release_shared();
-          ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(full(s), 0));
-        }
-        if (++s == C::STAGES) s = 0, ph ^= 1u;
-      }
-    }
-  }
-  } else {
-    ptx::setmaxnreg_inc<C::REGS_HIGH>();
+  } else if (warp >= C::EPI_WARP0) {
     // ---------------------------------------------------------------- results
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int e = warp - C::EPI_WARP0, q = warp & 3, half = e >> 2;
@@ -353,39 +271,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
       ptx::tc_fence_after();
       const int row0 = m * C::TM + int(rank) * 128 + q * 32, col0 = n * C::TN + half * 128;
       const int chunks = row0 < p.M ? max(0, min(4, (p.N - col0 + 31) / 32)) : 0;
-      uint32_t r[4][32];
       const uint32_t from = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * 128);
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) ptx::tmem_ld_32x32b_x32(from + 32u * c, r[c]);
-      ptx::tmem_wait_ld();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {                   // the accumulator is free (the leader waits for both CTAs)
-        ptx::fence_release_shared();
-        ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(tempty, 0));
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= chunks) continue;
+      auto release = [&]() {             // the accumulator is free (the leader waits for both CTAs)
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::fence_release_shared();
+          ptx::mbar_arrive_remote_relaxed(ptx::mapa_shared(tempty, 0));
+        }
+      };
+      auto store = [&](int c, const uint32_t (&w)[16 * C::OUT / 2]) {
         const uint32_t dst = stg + uint32_t(buf) * C::STG_BYTES;
         if (lane == 0) ptx::bulk_wait_read<C::STG_BUFS - 1>();
         __syncwarp();
-        float f[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = __fmul_rn(__uint_as_float(r[c][i]), p.alpha);
-        if constexpr (C::kF32) {
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            ptx::st_shared_v4(dst + lane * 128 + ((v ^ (lane & 7)) << 4), __float_as_uint(f[4 * v]),
-                              __float_as_uint(f[4 * v + 1]), __float_as_uint(f[4 * v + 2]), __float_as_uint(f[4 * v + 3]));
-        } else {
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            ptx::st_shared_v4(dst + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), ptx::pack_bf16x2(f[8 * v], f[8 * v + 1]),
-                              ptx::pack_bf16x2(f[8 * v + 2], f[8 * v + 3]), ptx::pack_bf16x2(f[8 * v + 4], f[8 * v + 5]),
-                              ptx::pack_bf16x2(f[8 * v + 6], f[8 * v + 7]));
-        }
+        for (int v = 0; v < 2 * C::OUT; ++v)              // rows of 128 or 64 bytes in their swizzle
+          ptx::st_shared_v4(dst + uint32_t(C::kF32 ? lane * 128 + ((v ^ (lane & 7)) << 4)
+                                                   : lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4)),
+                            w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -393,6 +296,38 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
           ptx::bulk_commit();
         }
         if (++buf == C::STG_BUFS) buf = 0;
+      };
+      if constexpr (C::kF32) {
+        if (chunks == 0) release();
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t r[32];
+          ptx::tmem_ld_32x32b_x32(from + 32u * c, r);
+          ptx::tmem_wait_ld();
+          if (c + 1 == chunks) release();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), p.alpha));
+          store(c, r);
+        }
+      } else {
+        // the warp's whole share leaves tensor memory, rounded, before any of it is stored
+        uint32_t pk[4][16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < chunks) {
+            uint32_t r[32];
+            ptx::tmem_ld_32x32b_x32(from + 32u * c, r);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[c][i] = ptx::pack_bf16x2_ordered(__fmul_rn(__uint_as_float(r[2 * i]), p.alpha),
+                                                  __fmul_rn(__uint_as_float(r[2 * i + 1]), p.alpha));
+          }
+        }
+        release();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < chunks) store(c, pk[c]);
       }
     }
     if (lane == 0) ptx::bulk_wait_read<0>();
@@ -415,16 +350,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
 
 // ------------------------------------------------------------------ the form for few rows
 //
-// The operands change places: rows of w on the 128 rows of the MMA, up to 256 rows of x on its columns, so that a CTA
+// The operands change places: rows of w on the 128 rows of the MMA, up to 128 rows of x on its columns, so that a CTA
 // alone takes 32, 64 or 128 columns of y and as many of them as there are SMs share the reading of w.  The sums have the
 // wide form's bits: an element is the same sequence of 64-element products, and neither the place of its row and
 // column in an instruction nor the instruction's extent enters (compared over every shape that the tests run).
 //
 // A CTA's R rows of w take the MMA's rows that they have in their tile of 128 (so that a tile of scales serves as it
-// is); the other rows multiply whatever the neighbouring stages hold, and are not stored.
+// is); the other rows multiply whatever the neighbouring slots hold, and are not stored.  A stage is two slots of 256
+// elements of K: a turn of the loading loop costs about 250 clocks besides its copies, of 28 each.
 
-constexpr int kFewMaxStages = 14;
-constexpr int kFewThreads = 256;          // warps: 0 loads, 1 products, 4 .. 7 scales and results
+constexpr int kSlots = 2;                 // of a stage
+constexpr int kFewMaxStages = 8;
+constexpr int kFewCols = 128;             // rows of x at most
+constexpr int kFewThreads = 256;          // warps: 0 loads, 1 products, 4 .. 7 results
 
 struct FewParams {
   Params p;
@@ -433,12 +371,13 @@ struct FewParams {
   int32_t stages;
   int32_t tmem_cols;
   int32_t off_w, off_sf, off_stg, off_bar;   // shared memory: x ring at 0, w ring, scales ring, staging, barriers
-  int32_t sf_x;             // bytes of a stage's scales of x (behind those of w)
 };
 
 template <bool kNv, bool kF32>
 struct Few {
-  static constexpr int TILES_K = kNv ? 4 : 2;
+  static constexpr int TILES_K = kNv ? 4 : 2;                // scale tiles of a slot
+  static constexpr int SF_BYTES = kSlots * TILES_K * 512;    // of a stage and operand
+  static constexpr int SF_COLS = TILES_K * 8;                // TMEM columns of a slot's scales
   static constexpr int OUT = kF32 ? 4 : 2, STG_BYTES = 32 * 32 * OUT;      // of a warp
 };
 
@@ -452,18 +391,17 @@ __global__ void __launch_bounds__(kFewThreads)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t base = ptx::smem_u32(smem), bars = base + uint32_t(f.off_bar);
   const int NS = f.stages;
-  auto full = [&](int s) { return bars + 8u * s; };                        // codes and scales are in shared memory
-  auto ready = [&](int s) { return bars + 8u * (kFewMaxStages + s); };     // and the scales in tensor memory
-  auto empty = [&](int s) { return bars + 8u * (2 * kFewMaxStages + s); }; // the stage's products are done
-  const uint32_t tfull = bars + 24u * kFewMaxStages, tempty = tfull + 8, drain = tfull + 16;
-  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + f.off_bar + (3 * kFewMaxStages + 3) * 8);
+  auto full = [&](int s) { return bars + 8u * s; };                        // codes and scales are there
+  auto empty = [&](int s) { return bars + 8u * (kFewMaxStages + s); };     // the stage's products are done
+  const uint32_t tfull = bars + 16u * kFewMaxStages, tempty = tfull + 8, drain = tfull + 16;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + f.off_bar + (2 * kFewMaxStages + 3) * 8);
   volatile uint32_t* gave_up = misc + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const bool lead = biattn_tc::elect_one();               // (as above)
   const int units = p.m_tiles * p.n_tiles;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       ptx::mbar_init(full(s), 1);
-      ptx::mbar_init(ready(s), 4);
       ptx::mbar_init(empty(s), 1);
     }
     ptx::mbar_init(tfull, 1);
@@ -482,9 +420,7 @@ __global__ void __launch_bounds__(kFewThreads)
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
   const Sync sy{gave_up, p.status, p.timeout_ns};
-  const uint32_t sf_bytes = C::TILES_K * 512u + uint32_t(f.sf_x);          // of a stage
-  const uint32_t sf_col0 = uint32_t(f.cols), sf_cols = C::TILES_K * (f.cols > 128 ? 12u : 8u);
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && lead) {
     // ---------------------------------------------------------------- loads
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int s = 0;
@@ -494,42 +430,37 @@ __global__ void __launch_bounds__(kFewThreads)
       const int n = u / p.m_tiles, row0 = (u - n * p.m_tiles) * f.cols, col0 = n * f.rows;
       const uint8_t* sx = p.sx + int64_t(row0 / 128) * p.tiles * 512;
       const uint8_t* sw = p.sw + int64_t(col0 / 128) * p.tiles * 512;
-      const int left = p.M - row0;
-      const bool second = f.cols > 128 && left > 128;
-      // few rows' scales are the first bytes of their tile (16 a row up to 32 rows)
-      const uint32_t part = left <= 32 ? uint32_t(left) * 16u : 512u;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = 0; kb < p.kblocks; kb += kSlots) {
         if (!wait_bar(empty(s), ph ^ 1u, sy)) {
           ok = false;
           break;
         }
         if (!p.stall) {
-          const int t0 = kb * C::TILES_K, nt = min(C::TILES_K, p.tiles - t0);
-          const uint32_t bytes = uint32_t(nt) * 512u, sf = base + uint32_t(f.off_sf) + uint32_t(s) * sf_bytes;
-          ptx::mbar_arrive_expect_tx(full(s), uint32_t(p.x_rows + f.rows) * 128u + bytes + uint32_t(nt) * part +
-                                                  (second ? bytes : 0u));
-          ptx::tma_load_2d(base + uint32_t(f.off_w) + uint32_t(s * f.rows) * 128u, &mw, full(s), kb * 128, col0);
-          ptx::tma_load_2d(base + uint32_t(s * f.cols) * 128u, &mx, full(s), kb * 128, row0);
-          bulk_load(sf, sw + int64_t(t0) * 512, bytes, full(s));
-          const uint32_t sfx = sf + C::TILES_K * 512u;
-          if (part == 512u) {
-            bulk_load(sfx, sx + int64_t(t0) * 512, bytes, full(s));
-          } else {
-            for (int t = 0; t < nt; ++t) bulk_load(sfx + uint32_t(t) * 512u, sx + int64_t(t0 + t) * 512, part, full(s));
+          const int t0 = kb * C::TILES_K, slots = min(kSlots, p.kblocks - kb);
+          const uint32_t bytes = uint32_t(min(kSlots * C::TILES_K, p.tiles - t0)) * 512u;
+          const uint32_t sf = base + uint32_t(f.off_sf) + uint32_t(s) * (2u * C::SF_BYTES);
+          ptx::mbar_arrive_expect_tx(full(s), uint32_t((p.x_rows + f.rows) * slots) * 128u + 2u * bytes);
+#pragma unroll
+          for (int j = 0; j < kSlots; ++j) {
+            if (j < slots) {
+              const int at = s * kSlots + j;
+              ptx::tma_load_2d(base + uint32_t(f.off_w) + uint32_t(at * f.rows) * 128u, &mw, full(s), (kb + j) * 128, col0);
+              ptx::tma_load_2d(base + uint32_t(at * f.cols) * 128u, &mx, full(s), (kb + j) * 128, row0);
+            }
           }
-          if (second) bulk_load(sfx + C::TILES_K * 512u, sx + (int64_t(p.tiles) + t0) * 512, bytes, full(s));
+          bulk_load(sf, sw + int64_t(t0) * 512, bytes, full(s));
+          bulk_load(sf + C::SF_BYTES, sx + int64_t(t0) * 512, bytes, full(s));
         }
         if (++s == NS) s = 0, ph ^= 1u;
       }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && lead) {
     // ---------------------------------------------------------------- products
     int s = 0;
     uint32_t ph = 0, tph = 0;
     bool ok = true, issued = false;
     const uint32_t id0 = idesc4<kNv>(128, 0) | (uint32_t(f.cols >> 3) << 17);
-    const uint32_t wide = f.cols > 128 ? 8u : 4u;          // columns of a tile of x's scales
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const int col0 = u / p.m_tiles * f.rows;
       if (!wait_bar(tempty, tph ^ 1u, sy)) {
@@ -539,22 +470,35 @@ __global__ void __launch_bounds__(kFewThreads)
       tph ^= 1u;
       ptx::tc_fence_after();
       const uint32_t shift = uint32_t(col0 & 127) * 128u;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        if (!wait_bar(full(s), ph, sy) || !wait_bar(ready(s), ph, sy)) {
+      for (int kb = 0; kb < p.kblocks; kb += kSlots) {
+        if (!wait_bar(full(s), ph, sy)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t a = base + uint32_t(f.off_w) + uint32_t(s * f.rows) * 128u - shift, b = base + uint32_t(s * f.cols) * 128u;
-        const uint32_t ta = tmem + sf_col0 + uint32_t(s) * sf_cols, tb = ta + C::TILES_K * 4;
-        const int steps = min(4, (p.K - kb * kStageK) / 64);
+        const uint32_t sf = base + uint32_t(f.off_sf) + uint32_t(s) * (2u * C::SF_BYTES);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k < steps) {
-            const int t = kNv ? k : k >> 1;
-            const uint32_t id = kNv ? 0u : uint32_t(k & 1) * 2u;
-            mma4<kNv>(tmem, desc_rows(a + 32u * k), desc_rows(b + 32u * k), id0 | (id << 4) | (id << 29), ta + 4u * t,
-                      tb + wide * t, kb != 0 || k != 0 ? 1u : 0u);
+        for (int j = 0; j < kSlots; ++j) {
+          const int at = s * kSlots + j;
+          const uint32_t a = base + uint32_t(f.off_w) + uint32_t(at * f.rows) * 128u - shift;
+          const uint32_t b = base + uint32_t(at * f.cols) * 128u;
+          const uint32_t ta = tmem + uint32_t(f.cols + at * C::SF_COLS), tb = ta + C::TILES_K * 4;
+          const int steps = min(4, (p.K - (kb + j) * kStageK) / 64);
+          if (steps > 0) {
+#pragma unroll
+            for (int t = 0; t < C::TILES_K; ++t) {
+              ptx::tc_cp_32x128b_x4(ta + 4u * t, desc_scales(sf + uint32_t(j * C::TILES_K + t) * 512u));
+              ptx::tc_cp_32x128b_x4(tb + 4u * t, desc_scales(sf + C::SF_BYTES + uint32_t(j * C::TILES_K + t) * 512u));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k < steps) {
+              const int t = kNv ? k : k >> 1;
+              const uint32_t id = kNv ? 0u : uint32_t(k & 1) * 2u;
+              mma4<kNv>(tmem, desc_rows(a + 32u * k), desc_rows(b + 32u * k), id0 | (id << 4) | (id << 29), ta + 4u * t,
+                        tb + 4u * t, kb + j != 0 || k != 0 ? 1u : 0u);
+            }
           }
         }
         issued = true;
@@ -569,38 +513,13 @@ __global__ void __launch_bounds__(kFewThreads)
       wait_bar(drain, 0u, Sync{&never, p.status, p.timeout_ns});
     }
   } else if (warp >= 4) {
-    // ---------------------------------------------------------------- scales to tensor memory, then the unit's results
+    // ---------------------------------------------------------------- results
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int q = warp - 4;
     const uint32_t quarter = uint32_t(q * 32) << 16, stg = base + uint32_t(f.off_stg + q * C::STG_BYTES);
-    int s = 0;
-    uint32_t ph = 0, tph = 0;
-    bool ok = true, stored = false;
-    for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-      for (int kb = 0; kb < p.kblocks; ++kb) {
-        ok = __all_sync(0xFFFFFFFFu, wait_bar(full(s), ph, sy));
-        if (!ok) break;
-        const uint32_t sf = base + uint32_t(f.off_sf) + uint32_t(s) * sf_bytes, sfx = sf + C::TILES_K * 512u;
-        const uint32_t ta = tmem + quarter + sf_col0 + uint32_t(s) * sf_cols, tb = ta + C::TILES_K * 4;
-        uint32_t wa[4 * C::TILES_K], wb[4 * C::TILES_K];
-        read_tiles<C::TILES_K>(wa, sf, lane, [](int i) { return i * 512; });
-        if (f.cols <= 128) {
-          read_tiles<C::TILES_K>(wb, sfx, lane, [](int i) { return i * 512; });
-          store_tiles<C::TILES_K>(ta, wa);
-          store_tiles<C::TILES_K>(tb, wb);
-        } else {
-          uint32_t w2[8 * C::TILES_K];
-          read_tiles<2 * C::TILES_K>(w2, sfx, lane, [](int i) { return ((i & 1) * C::TILES_K + (i >> 1)) * 512; });
-          store_tiles<C::TILES_K>(ta, wa);
-          store_tiles<2 * C::TILES_K>(tb, w2);
-        }
-        biattn_tc::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ready(s));
-        if (++s == NS) s = 0, ph ^= 1u;
-      }
-      if (!ok) break;
+    uint32_t tph = 0;
+    bool stored = false;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const int n = u / p.m_tiles, row0 = (u - n * p.m_tiles) * f.cols, col0 = n * f.rows;
       if (!__all_sync(0xFFFFFFFFu, wait_bar(tfull, tph, sy))) break;
       tph ^= 1u;
@@ -692,24 +611,23 @@ inline Kernel select(bool nv, bool f32) {
 constexpr int kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024;
 
 // Layout of the form for few rows with `per_sm` CTAs an SM: as deep a ring as shared and tensor memory hold; its
-// bytes of shared memory, 0 where fewer than three stages fit.
+// bytes of shared memory, 0 where fewer than two stages fit.
 int few_layout(FewParams& f, bool nv, bool f32, int per_sm) {
-  const int tiles = nv ? 4 : 2, sf_cols = tiles * (f.cols > 128 ? 12 : 8);
-  f.tmem_cols = 512 / (per_sm > 2 ? 4 : per_sm);
-  f.sf_x = tiles * 512 * (f.cols > 128 ? 2 : 1);
-  const int stg = 4 * 32 * 32 * (f32 ? 4 : 2), bar = (3 * kFewMaxStages + 3) * 8 + 16;
-  const int stage = (f.cols + f.rows) * 128 + tiles * 512 + f.sf_x;
+  const int tiles = nv ? 4 : 2, sf = 2 * kSlots * tiles * 512;
+  f.tmem_cols = 512 / per_sm;
+  const int stg = 4 * 32 * 32 * (f32 ? 4 : 2), bar = (2 * kFewMaxStages + 3) * 8 + 16;
   const int room = std::min(kSmemBlock, kSmemSm / per_sm - 1024) - 1024 - stg - bar;
   // The MMA reads 128 rows around a CTA's own: up to 128 - R before the ring of w (the x ring, filled up to them) and
   // behind it.
   const int margin = (128 - f.rows) * 128;
-  f.stages = std::min(std::min(kFewMaxStages, (f.tmem_cols - f.cols) / sf_cols), room / stage);
-  for (; f.stages >= 3; --f.stages) {
-    f.off_w = std::max(f.stages * f.cols * 128, margin);
-    f.off_sf = f.off_w + f.stages * f.rows * 128;
-    f.off_stg = (f.off_sf + std::max(f.stages * (tiles * 512 + f.sf_x), margin) + 1023) / 1024 * 1024;
+  f.stages = std::min(kFewMaxStages, (f.tmem_cols - f.cols) / (kSlots * tiles * 8));
+  for (; f.stages >= 2; --f.stages) {
+    const int slots = f.stages * kSlots;
+    f.off_w = std::max(slots * f.cols * 128, margin);
+    f.off_sf = f.off_w + slots * f.rows * 128;
+    f.off_stg = (f.off_sf + std::max(f.stages * sf, margin) + 1023) / 1024 * 1024;
     f.off_bar = f.off_stg + stg;
-    if (f.off_bar + bar - stg - bar <= room) return f.off_bar + bar + 1024;
+    if (f.off_stg <= room) return f.off_bar + bar + 1024;
   }
   return 0;
 }
@@ -753,7 +671,7 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(unsigned(sms / 2 * 2));
-  cfg.blockDim = dim3(512);
+  cfg.blockDim = dim3(384);
   cfg.dynamicSmemBytes = size_t(k.wide_smem);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -777,14 +695,20 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
 
 namespace {
 
-// Whether a call of M rows takes the form for few rows, and its layout.  Both forms give the same bits.
+// Whether a call of M rows takes the form for few rows, and its layout.  Both forms give the same bits.  Measured with
+// nvfp4 (us; this form in tiles of 128 x 128 against pairs of 256 x 256): 256 x 4096 x 4096 (M, K, N) 8.8 against 10.2, 512 x
+// 4096 x 4096 8.3 against 9.8, 777 x 2176 x 1000 6.7 against 7.7, 4096 x 1024 x 256 5.2 against 6.2, and with more tiles than
+// SMs 256 x 4096 x 14336 15.6 against 12.1: a call takes it where its tiles run all at once.  Fewer columns of y a CTA
+// where that leaves half the SMs without work: 300 x 4096 x 1024 8.2 with 128, 7.7 with 32; 128 x 4096 x 4096 8.7 and 7.9; and
+// two CTAs an SM for many columns and a handful of rows: 1 x 4096 x 28672 14.0 with one, 13.1 with two.
 bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, int& smem) {
-  if (M > 256) return false;
-  f.cols = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  f.cols = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int64_t m_tiles = (M + f.cols - 1) / f.cols;
+  auto units = [&]() { return (h->N + f.rows - 1) / f.rows * m_tiles; };
   f.rows = 128;
-  while (f.rows > 32 && (h->N + f.rows - 1) / f.rows < h->sms * 9 / 10) f.rows /= 2;
-  const int64_t units = (h->N + f.rows - 1) / f.rows;
-  per_sm = units > h->sms && f.cols <= 128 ? 2 : 1;
+  if (M > big4::kFewCols && units() > h->sms) return false;
+  while (f.rows > 32 && units() < h->sms / (M > big4::kFewCols ? 3 : 2)) f.rows /= 2;
+  per_sm = units() > h->sms && f.cols <= 32 ? 2 : 1;
   smem = big4::few_layout(f, h->nv, h->f32, per_sm);
   return smem > 0;
 }
@@ -830,11 +754,17 @@ int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void*
   p.m_tiles = int32_t(m_tiles);
   p.n_tiles = int32_t(n_tiles);
   p.x_rows = int32_t(std::min<int64_t>(few ? f.cols : 128, (M + 7) / 8 * 8));
-  CUtensorMap mx, mw, my;
+  CUtensorMap mx, mw, msx, msw, my;
+  const uint64_t tiles = uint64_t(p.tiles);
+  const uint32_t tiles_k = h->nv ? 4 : 2;
   if (!encode(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, uint64_t(M), uint64_t(h->K / 2), uint64_t(h->K / 2),
               uint32_t(p.x_rows), 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, uint64_t(h->N), uint64_t(h->K / 2), uint64_t(h->K / 2),
               few ? uint32_t(f.rows) : 128u, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      (!few && (!encode(&msx, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, sx, uint64_t((M + 127) / 128), tiles * 64, tiles * 512, 1,
+                        tiles_k * 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                !encode(&msw, CU_TENSOR_MAP_DATA_TYPE_FLOAT64, sw, uint64_t((h->N + 127) / 128), tiles * 64, tiles * 512, 2,
+                        tiles_k * 64, CU_TENSOR_MAP_SWIZZLE_NONE))) ||
       !encode(&my, h->f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, uint64_t(M),
               uint64_t(h->N), uint64_t(h->N) * (h->f32 ? 4 : 2), 32, 32,
               h->f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
@@ -843,7 +773,7 @@ int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void*
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(unsigned(few ? std::min<int64_t>(m_tiles * n_tiles, int64_t(per_sm) * h->sms)
                                   : 2 * std::min<int64_t>(m_tiles * n_tiles, h->max_groups)));
-  cfg.blockDim = dim3(few ? kFewThreads : 512);
+  cfg.blockDim = dim3(few ? kFewThreads : 384);
   cfg.dynamicSmemBytes = size_t(few ? smem : h->kern.wide_smem);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -851,8 +781,9 @@ int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void*
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* args[4] = {&mx, &mw, &my, few ? static_cast<void*>(&f) : static_cast<void*>(&p)};
-  if (cudaLaunchKernelExC(&cfg, few ? h->kern.few : h->kern.wide, args) != cudaSuccess) {
+  void* few_args[4] = {&mx, &mw, &my, &f};
+  void* wide_args[6] = {&mx, &mw, &msx, &msw, &my, &p};
+  if (cudaLaunchKernelExC(&cfg, few ? h->kern.few : h->kern.wide, few ? few_args : wide_args) != cudaSuccess) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -881,7 +812,7 @@ BI_GEMM_API int bi_gemm4_get_config(bi_gemm4_t h, bi_gemm4_config* c) {
   c->tile_rows = c->tile_cols = 256;
   c->stages = h->kern.stages;
   c->max_groups = h->max_groups;
-  c->few_rows = 256;
+  c->few_rows = big4::kFewCols;
   c->smem_bytes = h->kern.wide_smem;
   return BI_GEMM_OK;
 }
