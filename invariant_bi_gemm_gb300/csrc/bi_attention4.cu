@@ -37,9 +37,9 @@ using biattn_tc::ex2;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 32;                 // positions of a step
-constexpr int kRing = 3;                  // steps of a warp's ring
-constexpr int kBlocksPerSm = 3;
-constexpr int kTokens = 1024;             // of a launch
+constexpr int kRing = 2;                  // steps of a warp's ring
+constexpr int kBlocksPerSm = 4;
+constexpr int kTokens = 512;              // of a launch
 constexpr int kHeads = 8;                 // columns of the MMA
 constexpr int kDefaultSplit = 512;
 constexpr int kMergeWarps = 8;
@@ -79,16 +79,24 @@ struct Cfg {
   static constexpr int RING = kRing * STEP;                      // of a warp
   static constexpr int OFF_ML = kWarps * RING;
   static constexpr int OFF_CUM = OFF_ML + kWarps * kHeads * 8;
-  static constexpr int OFF_O = (OFF_CUM + (kTokens + 1 + kWarps) * 4 + 15) / 16 * 16;
+  static constexpr int OFF_O = (OFF_CUM + (3 * kTokens + 1 + kWarps) * 4 + 15) / 16 * 16;
   static_assert(STEP % 16 == 0 && OFF_ML % 16 == 0, "alignment");
-  // The warps' parts meet in shared memory, eight heads in two halves of the dimensions: three blocks fit an SM.
+  // The warps' parts meet in shared memory, eight heads in two halves of the dimensions: four blocks fit an SM.
   __host__ __device__ static constexpr int halves(int G) { return G == 8 ? 2 : 1; }
   __host__ __device__ static constexpr int row(int G) { return D / halves(G) + 4; }   // floats of a head
   static constexpr int smem(int G) { return OFF_O + kWarps * G * row(G) * 4; }
 };
 
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
 }
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -148,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   using C = Cfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
   int32_t* cum = reinterpret_cast<int32_t*>(smem + C::OFF_CUM);
-  int32_t* sums = cum + kTokens + 1;
+  int32_t* seqs = cum + kTokens + 1;                     // the tokens' requests and positions
+  int32_t* poss = seqs + kTokens;
+  int32_t* sums = poss + kTokens;
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -156,7 +166,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   int32_t carry = 0;
   for (int base = 0; base < p.T; base += kThreads) {
     const int i = base + tid;
-    const int32_t n = i < p.T ? splits_of(p, p.q_seq[i], p.q_pos[i], blockIdx.x == 0) : 0;
+    int32_t n = 0;
+    if (i < p.T) {
+      seqs[i] = p.q_seq[i];
+      poss[i] = p.q_pos[i];
+      n = splits_of(p, seqs[i], poss[i], blockIdx.x == 0);
+    }
     int32_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -177,12 +192,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   }
   if (tid == 0) cum[p.T] = carry;
   __syncthreads();
-  const int64_t units = int64_t(carry) * p.Hkv;
+  const int32_t units = carry * p.Hkv;
 
-  auto find = [&](int64_t u) {
+  auto find = [&](int32_t u) {
     Unit r;
-    const int32_t v = int32_t(u / p.Hkv);
-    r.kh = int32_t(u - int64_t(v) * p.Hkv);
+    const int32_t v = u / p.Hkv;
+    r.kh = u - v * p.Hkv;
     int lo = 0, hi = p.T;                                // cum[lo] <= v < cum[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -191,25 +206,40 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
     }
     r.t = lo;
     r.split = v - cum[lo];
-    r.b = __ldg(p.q_seq + lo);
+    r.b = seqs[lo];
     r.first = r.split * p.split;
-    r.last = min(__ldg(p.q_pos + lo), r.first + p.split - 1);
+    r.last = min(poss[lo], r.first + p.split - 1);
     return r;
   };
 
-  // ---- this warp's loads, ahead of its products by up to kRing steps and across units
+  // ---- this warp's loads, ahead of its products by kRing steps and across units
   const uint32_t ring = ptx::smem_u32(smem) + uint32_t(warp) * C::RING;
-  int64_t lu = blockIdx.x;                               // unit of the next load
+  constexpr int CH = C::CODES / 16, ROWS = 32 / CH;      // 16-byte chunks of a row, rows an instruction
+  const int row = lane / CH, ch = lane % CH;
+  const uint8_t* kc = p.kc + ch * 16;
+  const uint8_t* vc = p.vc + ch * 16;
+  const uint32_t to_k = uint32_t(row * C::CODES + ch * 16), to_v = uint32_t(C::OFF_V + row * C::VROW + ch * 16);
+  int32_t lu = blockIdx.x;                               // unit of the next load
   Unit L{};
   int32_t lpos = 0;                                      // its position
+  int32_t lpage = 0, lrow = 0;                           // this lane's page there, fetched ahead, and row of the page
   int lslot = 0;
   bool lmore = lu < units;
+  auto fetch = [&]() {
+    const int32_t pos = min(lpos + lane, L.last);
+    const int32_t pg = int32_t((uint64_t(uint32_t(pos)) * p.page_mul) >> p.page_shift);
+    lrow = pos - pg * p.page_size;
+    lpage = __ldg(p.table + int64_t(L.b) * p.max_pages + pg);
+  };
   // Makes L the next unit (from lu on) in which this warp has a step.
   auto seek = [&]() {
     while (lu < units) {
       L = find(lu);
       lpos = L.first + warp * kStep;
-      if (lpos <= L.last) return;
+      if (lpos <= L.last) {
+        fetch();
+        return;
+      }
       lu += gridDim.x;
     }
     lmore = false;
@@ -217,39 +247,39 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   auto issue = [&]() {
     if (lmore) {
       const uint32_t dst = ring + uint32_t(lslot) * C::STEP;
-      // a lane looks one position up; a row's place comes from its lane
-      const int32_t pos = lpos + lane;
-      int64_t at = -1;
-      if (pos <= L.last) {
-        const int32_t pg = int32_t((uint64_t(uint32_t(pos)) * p.page_mul) >> p.page_shift);
-        const int64_t page = __ldg(p.table + int64_t(L.b) * p.max_pages + pg);
-        if (page >= 0 && page < p.num_pages)
-          at = ((page * p.page_size + (pos - pg * p.page_size)) * p.Hkv + L.kh);
-        else
-          atomicOr(p.status, kErrPage);
-      }
-      constexpr int CH = C::CODES / 16, ROWS = 32 / CH;   // 16-byte chunks of a row, rows an instruction
+      // a lane looks one position up; a row's place comes from its lane (fewer than 2^32 - 1 rows of a head: the host)
+      const bool here = lpos + lane <= L.last, good = lpage >= 0 && lpage < p.num_pages;
+      uint32_t at = uint32_t((int64_t(lpage) * p.page_size + lrow) * p.Hkv + L.kh);
+      if (__all_sync(0xFFFFFFFFu, here && good)) {
 #pragma unroll
-      for (int i = 0; i < kStep / ROWS; ++i) {
-        const int row = i * ROWS + lane / CH, ch = lane % CH;
-        const int64_t a = __shfl_sync(0xFFFFFFFFu, at, row);
-        const uint32_t n = a >= 0 ? 16u : 0u;
-        const int64_t off = a >= 0 ? a * C::CODES + ch * 16 : 0;
-        ptx::cp_async_16(dst + uint32_t(row * C::CODES + ch * 16), p.kc + off, n);
-        ptx::cp_async_16(dst + C::OFF_V + uint32_t(row * C::VROW + ch * 16), p.vc + off, n);
-      }
-      const uint32_t n = at >= 0 ? uint32_t(C::SCALES) : 0u;
-      const int64_t off = at >= 0 ? at * C::SCALES : 0;
-      if constexpr (D == 128) {
-        cp_async_8(dst + C::OFF_KS + lane * 8, p.ks + off, n);
-        cp_async_8(dst + C::OFF_VS + lane * 8, p.vs + off, n);
+        for (int i = 0; i < kStep / ROWS; ++i) {
+          const uint64_t off = uint64_t(__shfl_sync(0xFFFFFFFFu, at, i * ROWS + row)) * C::CODES;
+          cp_async_16(dst + to_k + uint32_t(i * ROWS * C::CODES), kc + off);
+          cp_async_16(dst + to_v + uint32_t(i * ROWS * C::VROW), vc + off);
+        }
+        cp_async<C::SCALES>(dst + C::OFF_KS + lane * C::SCALES, p.ks + uint64_t(at) * C::SCALES);
+        cp_async<C::SCALES>(dst + C::OFF_VS + lane * C::SCALES, p.vs + uint64_t(at) * C::SCALES);
       } else {
-        ptx::cp_async_4(dst + C::OFF_KS + lane * 4, p.ks + off, n);
-        ptx::cp_async_4(dst + C::OFF_VS + lane * 4, p.vs + off, n);
+        // the last step of a token, or a page that is not there: zeros in its place
+        if (here && !good) atomicOr(p.status, kErrPage);
+        if (!(here && good)) at = 0xFFFFFFFFu;
+#pragma unroll 1
+        for (int i = 0; i < kStep / ROWS; ++i) {
+          const uint32_t a = __shfl_sync(0xFFFFFFFFu, at, i * ROWS + row), n = a != 0xFFFFFFFFu ? 16u : 0u;
+          const uint64_t off = n ? uint64_t(a) * C::CODES : 0;
+          ptx::cp_async_16(dst + to_k + uint32_t(i * ROWS * C::CODES), kc + off, n);
+          ptx::cp_async_16(dst + to_v + uint32_t(i * ROWS * C::VROW), vc + off, n);
+        }
+        const uint32_t n = at != 0xFFFFFFFFu ? uint32_t(C::SCALES) : 0u;
+        const uint64_t off = n ? uint64_t(at) * C::SCALES : 0;
+        cp_async_zfill<C::SCALES>(dst + C::OFF_KS + lane * C::SCALES, p.ks + off, n);
+        cp_async_zfill<C::SCALES>(dst + C::OFF_VS + lane * C::SCALES, p.vs + off, n);
       }
       if (++lslot == kRing) lslot = 0;
       lpos += kWarps * kStep;
-      if (lpos > L.last) {
+      if (lpos <= L.last) {
+        fetch();
+      } else {
         lu += gridDim.x;
         seek();
       }
@@ -257,14 +287,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
     ptx::cp_async_commit();
   };
   if (lmore) seek();
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) issue();
+#pragma unroll 1
+  for (int i = 0; i < kRing; ++i) issue();
 
   // ---- products
   int slot = 0;
   float* so = reinterpret_cast<float*>(smem + C::OFF_O);
   float* sml = reinterpret_cast<float*>(smem + C::OFF_ML);
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  for (int32_t u = blockIdx.x; u < units; u += gridDim.x) {
     const Unit U = find(u);
     // the query in f16, relative to its head's largest element
     uint32_t qf[D / 8];
@@ -287,16 +317,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
       for (int i = 0; i < D / 8; ++i)
         qf[i] = pack_f16x2(__uint_as_float(qf[i] << 16) * up, __uint_as_float(qf[i] & 0xFFFF0000u) * up);
       // the factors of the two heads whose scores this lane has
-      fac[0] = __fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4), p.c);
-      fac[1] = __fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4), p.c);
+      // (above zero, so that a hidden position's -inf stays one)
+      fac[0] = fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4), p.c), 1e-45f);
+      fac[1] = fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4), p.c), 1e-45f);
     }
+    // (the reference m is a product's sum as it comes from the MMA; the difference to it is taken before the factor, so
+    // that it is exact near the reference however large the scores are)
     float acc[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
     for (int32_t pos = U.first + warp * kStep; pos <= U.last; pos += kWarps * kStep) {
-      issue();
       ptx::cp_async_wait<kRing - 1>();
       __syncwarp();
       const uint32_t src = ring + uint32_t(slot) * C::STEP;
@@ -336,8 +368,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
           mma(s[h], x[0], y[0], x[1], y[1], qf[4 * i], qf[4 * i + 1]);
           mma(s[h], x[2], y[2], x[3], y[3], qf[4 * i + 2], qf[4 * i + 3]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[h][j] = __fmul_rn(s[h][j], fac[j & 1]);
       }
       if (pos + kStep - 1 > U.last) {
 #pragma unroll
@@ -353,14 +383,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
         top[j] = fmaxf(fmaxf(s[0][j], s[0][j + 2]), fmaxf(s[1][j], s[1][j + 2]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], o));
-        move |= top[j] > m[j] + kSlack;
+        move |= __fmul_rn(__fsub_rn(top[j], m[j]), fac[j]) > kSlack;
       }
       if (__any_sync(0xFFFFFFFFu, move)) {                // (a head's rule looks at that head alone)
         float f[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const bool mv = top[j] > m[j] + kSlack;
-          f[j] = mv ? ex2(m[j] - top[j]) : 1.0f;
+          const bool mv = __fmul_rn(__fsub_rn(top[j], m[j]), fac[j]) > kSlack;
+          f[j] = mv ? ex2(__fmul_rn(__fsub_rn(m[j], top[j]), fac[j])) : 1.0f;
           if (mv) m[j] = top[j];
           l[j] *= f[j];
         }
@@ -372,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[h][j] = ex2(__fadd_rn(__fsub_rn(s[h][j], m[j & 1]), kLift));
+        for (int j = 0; j < 4; ++j) s[h][j] = ex2(__fmaf_rn(__fsub_rn(s[h][j], m[j & 1]), fac[j & 1], kLift));
         l[0] += s[h][0] + s[h][2];
         l[1] += s[h][1] + s[h][3];
         const uint32_t b0 = transposed(pack_f16x2(s[h][0], s[h][1])), b1 = transposed(pack_f16x2(s[h][2], s[h][3]));
@@ -411,9 +441,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
         }
       }
       __syncwarp();                                       // the slot may be refilled
+      issue();
     }
     // ---- the four warps' parts, in order
-    const bool alone = U.split == 0 && U.last == __ldg(p.q_pos + U.t);
+    const bool alone = U.split == 0 && U.last == poss[U.t];
     const int halves = C::halves(p.G), dims = D / halves, orow = C::row(p.G);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -421,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
       for (int o = 4; o < 32; o <<= 1) l[j] = __fadd_rn(l[j], __shfl_xor_sync(0xFFFFFFFFu, l[j], o));
       const int head = 2 * t4 + j;
       if (g == 0 && head < p.G) {
-        sml[(warp * kHeads + head) * 2] = m[j];
+        sml[(warp * kHeads + head) * 2] = __fmul_rn(m[j], fac[j]);
         sml[(warp * kHeads + head) * 2 + 1] = l[j];
       }
     }
@@ -703,6 +734,7 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
   const Layout4 w = layout4_of(h, T, std::max<int64_t>(max_pos, 0));
   const int64_t per_token = int64_t(h->Hkv) * w.splits;
   if (per_token * std::min<int64_t>(T, biattn4::kTokens) >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  if (num_pages > int64_t(0xFFFFFFFE) / h->page_size / h->Hkv) return BI_GEMM_ERR_UNSUPPORTED;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();

@@ -325,6 +325,8 @@ def test_queries_that_are_not_finite_and_zero_queries():
     assert torch.isnan(o[0, 3]).all() and not torch.isnan(o[1]).any() and not torch.isnan(o[0, 4:]).any()
     _, v = rows_of(four, table, 0, 50, 16, 1.0, 1.0)
     assert ((o[0, 6].double() - v[:, 1].mean(0)).abs() <= 2.0 ** -7 * v[:, 1].abs().mean(0)).all()
+    tiny = bg.BiAttention4(8, 2, 64, 16, k_scale=2.0 ** -64)       # a factor that underflows
+    assert torch.equal(tiny.run(q, seq, pos, *four, table, 49)[0, 6], o[0, 6])
 
 
 def test_bad_places_are_reported():
