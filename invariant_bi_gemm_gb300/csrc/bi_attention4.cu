@@ -100,8 +100,7 @@ __device__ __forceinline__ void cp_async_zfill(uint32_t dst, const void* src, ui
 }
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -121,24 +120,8 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
 struct Unit {
-  int32_t t, kh, split, b, first, last;   // positions first .. last of request b (last < first: none)
+  int32_t v, t, split, first, last;   // the v-th (token, split) and its positions (last < first: none)
 };
 
 // Splits of a token: one for an empty place, none for one that cannot be served (which `report` says).
@@ -192,24 +175,33 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   }
   if (tid == 0) cum[p.T] = carry;
   __syncthreads();
-  const int32_t units = carry * p.Hkv;
 
-  auto find = [&](int32_t u) {
-    Unit r;
-    const int32_t v = u / p.Hkv;
-    r.kh = u - v * p.Hkv;
-    int lo = 0, hi = p.T;                                // cum[lo] <= v < cum[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid] <= v) lo = mid;
-      else hi = mid;
+  // Block (chain, kh) takes a run of consecutive (token, split) of its head, so that a token's query is prepared once
+  // for its splits there; the blocks of a chain's heads read neighbouring rows at the same time.
+  const int32_t kh = int32_t(blockIdx.x % uint32_t(p.Hkv)), chain = int32_t(blockIdx.x / uint32_t(p.Hkv));
+  const int32_t chains = int32_t(gridDim.x / uint32_t(p.Hkv));
+  const int32_t v_end = int32_t(int64_t(carry) * (chain + 1) / chains);
+  auto locate = [&](Unit& r) {                           // t: cum[t] <= v < cum[t + 1]
+    for (;;) {
+      const int i = r.t + 1 + lane;
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, i >= p.T || cum[i] > r.v);
+      if (past) {
+        r.t += __ffs(past) - 1;
+        break;
+      }
+      r.t += 32;
     }
-    r.t = lo;
-    r.split = v - cum[lo];
-    r.b = seqs[lo];
+    r.split = r.v - cum[r.t];
     r.first = r.split * p.split;
-    r.last = min(poss[lo], r.first + p.split - 1);
-    return r;
+    r.last = min(poss[r.t], r.first + p.split - 1);
+  };
+  auto start = [&](Unit& r) {
+    r.v = int32_t(int64_t(carry) * chain / chains);
+    r.t = 0;
+    if (r.v < v_end) locate(r);
+  };
+  auto advance = [&](Unit& r) {
+    if (++r.v < v_end) locate(r);
   };
 
   // ---- this warp's loads, ahead of its products by kRing steps and across units
@@ -219,28 +211,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   const uint8_t* kc = p.kc + ch * 16;
   const uint8_t* vc = p.vc + ch * 16;
   const uint32_t to_k = uint32_t(row * C::CODES + ch * 16), to_v = uint32_t(C::OFF_V + row * C::VROW + ch * 16);
-  int32_t lu = blockIdx.x;                               // unit of the next load
-  Unit L{};
+  Unit L;                                                // unit of the next load
   int32_t lpos = 0;                                      // its position
   int32_t lpage = 0, lrow = 0;                           // this lane's page there, fetched ahead, and row of the page
   int lslot = 0;
-  bool lmore = lu < units;
+  bool lmore = true;
   auto fetch = [&]() {
     const int32_t pos = min(lpos + lane, L.last);
     const int32_t pg = int32_t((uint64_t(uint32_t(pos)) * p.page_mul) >> p.page_shift);
     lrow = pos - pg * p.page_size;
-    lpage = __ldg(p.table + int64_t(L.b) * p.max_pages + pg);
+    lpage = __ldg(p.table + int64_t(seqs[L.t]) * p.max_pages + pg);
   };
-  // Makes L the next unit (from lu on) in which this warp has a step.
+  // Makes L the next unit (from itself on) in which this warp has a step.
   auto seek = [&]() {
-    while (lu < units) {
-      L = find(lu);
+    while (L.v < v_end) {
       lpos = L.first + warp * kStep;
       if (lpos <= L.last) {
         fetch();
         return;
       }
-      lu += gridDim.x;
+      advance(L);
     }
     lmore = false;
   };
@@ -249,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
       const uint32_t dst = ring + uint32_t(lslot) * C::STEP;
       // a lane looks one position up; a row's place comes from its lane (fewer than 2^32 - 1 rows of a head: the host)
       const bool here = lpos + lane <= L.last, good = lpage >= 0 && lpage < p.num_pages;
-      uint32_t at = uint32_t((int64_t(lpage) * p.page_size + lrow) * p.Hkv + L.kh);
+      uint32_t at = uint32_t((int64_t(lpage) * p.page_size + lrow) * p.Hkv + kh);
       if (__all_sync(0xFFFFFFFFu, here && good)) {
 #pragma unroll
         for (int i = 0; i < kStep / ROWS; ++i) {
@@ -280,13 +270,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
       if (lpos <= L.last) {
         fetch();
       } else {
-        lu += gridDim.x;
+        advance(L);
         seek();
       }
     }
     ptx::cp_async_commit();
   };
-  if (lmore) seek();
+  start(L);
+  seek();
 #pragma unroll 1
   for (int i = 0; i < kRing; ++i) issue();
 
@@ -294,13 +285,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   int slot = 0;
   float* so = reinterpret_cast<float*>(smem + C::OFF_O);
   float* sml = reinterpret_cast<float*>(smem + C::OFF_ML);
-  for (int32_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const Unit U = find(u);
+  int32_t token = -1;
+  uint32_t qf[D / 8];
+  float fac[2] = {0.0f, 0.0f};
+  Unit U;
+  for (start(U); U.v < v_end; advance(U)) {
     // the query in f16, relative to its head's largest element
-    uint32_t qf[D / 8];
-    float fac[2] = {0.0f, 0.0f};
-    {
-      const uint16_t* src = p.q + (int64_t(U.t) * p.Hq + U.kh * p.G + g) * D + t4 * (D / 4);
+    if (U.t != token) {
+      token = U.t;
+      const uint16_t* src = p.q + (int64_t(U.t) * p.Hq + kh * p.G + g) * D + t4 * (D / 4);
       uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
@@ -331,40 +324,41 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
     for (int32_t pos = U.first + warp * kStep; pos <= U.last; pos += kWarps * kStep) {
       ptx::cp_async_wait<kRing - 1>();
       __syncwarp();
-      const uint32_t src = ring + uint32_t(slot) * C::STEP;
+      const uint8_t* src = smem + warp * C::RING + slot * C::STEP;
       if (++slot == kRing) slot = 0;
+      // scores: two sixteens of positions side by side, for two chains of products
+      constexpr int W = D / 32;                           // words of codes a lane has of a row
       float s[2][4];
+      uint32_t kw[4][W], ksc[4][2];                       // rows g, g + 8, g + 16, g + 24
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {                       // sixteen positions
-        s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
-        constexpr int W = D / 32;                         // words of codes a lane has of a row
-        uint32_t w[2][W], sc[2][2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = 16 * h + 8 * r + g;
-          const uint32_t a = src + uint32_t(row * C::CODES + t4 * (C::CODES / 4));
-          if constexpr (D == 128) {
-            uint32_t v[4];
-            biattn_tc::ld_shared_v4(a, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[r][i] = v[i];
-            const uint32_t b = bifp4::e4m3_pair(ld_shared_u16(src + C::OFF_KS + uint32_t(row * 8 + 2 * t4)));
-            sc[r][0] = __byte_perm(b, b, 0x1010), sc[r][1] = __byte_perm(b, b, 0x3232);
-          } else {
-            const uint2 v = ld_shared_v2(a);
-            w[r][0] = v.x, w[r][1] = v.y;
-            const uint32_t b = bifp4::e4m3_pair(ld_shared_u8(src + C::OFF_KS + uint32_t(row * 4 + t4)));
-            sc[r][0] = sc[r][1] = __byte_perm(b, b, 0x1010);
-          }
+      for (int r = 0; r < 4; ++r) {
+        const int at = 8 * r + g;
+        if constexpr (D == 128) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src + at * C::CODES + t4 * 16);
+          kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
+          const uint32_t b = bifp4::e4m3_pair(*reinterpret_cast<const uint16_t*>(src + C::OFF_KS + at * 8 + 2 * t4));
+          ksc[r][0] = __byte_perm(b, b, 0x1010), ksc[r][1] = __byte_perm(b, b, 0x3232);
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + at * C::CODES + t4 * 8);
+          kw[r][0] = v.x, kw[r][1] = v.y;
+          const uint32_t b = bifp4::e4m3_pair(src[C::OFF_KS + at * 4 + t4]);
+          ksc[r][0] = ksc[r][1] = __byte_perm(b, b, 0x1010);
         }
+      }
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[h][j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           uint32_t x[4], y[4];
-          bifp4::values8(w[0][i], x);
-          bifp4::values8(w[1][i], y);
+          bifp4::values8(kw[2 * h][i], x);
+          bifp4::values8(kw[2 * h + 1][i], y);
           const int k = i * 2 / W;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = mul_f16x2(x[j], sc[0][k]), y[j] = mul_f16x2(y[j], sc[1][k]);
+          for (int j = 0; j < 4; ++j) x[j] = mul_f16x2(x[j], ksc[2 * h][k]), y[j] = mul_f16x2(y[j], ksc[2 * h + 1][k]);
           mma(s[h], x[0], y[0], x[1], y[1], qf[4 * i], qf[4 * i + 1]);
           mma(s[h], x[2], y[2], x[3], y[3], qf[4 * i + 2], qf[4 * i + 3]);
         }
@@ -410,20 +404,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
         uint32_t w[4][W], sc[2];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * h + 2 * t4 + (r & 1) + 8 * (r >> 1);
-          const uint32_t a = src + C::OFF_V + uint32_t(row * C::VROW + g * (C::CODES / 8));
+          const int at = 16 * h + 2 * t4 + (r & 1) + 8 * (r >> 1);
+          const uint8_t* a = src + C::OFF_V + at * C::VROW + g * (C::CODES / 8);
           if constexpr (D == 128) {
-            const uint2 v = ld_shared_v2(a);
+            const uint2 v = *reinterpret_cast<const uint2*>(a);
             w[r][0] = v.x, w[r][1] = v.y;
           } else {
-            w[r][0] = ptx::ld_shared_u32(a);
+            w[r][0] = *reinterpret_cast<const uint32_t*>(a);
           }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = 16 * h + 2 * t4 + 8 * r;
-          const uint32_t a = src + C::OFF_VS + uint32_t(row * C::SCALES + (D == 128 ? g : g >> 1));
-          sc[r] = bifp4::e4m3_pair(ld_shared_u8(a) | ld_shared_u8(a + C::SCALES) << 8);
+          const uint8_t* a = src + C::OFF_VS + (16 * h + 2 * t4 + 8 * r) * C::SCALES + (D == 128 ? g : g >> 1);
+          sc[r] = bifp4::e4m3_pair(uint32_t(a[0]) | uint32_t(a[C::SCALES]) << 8);
         }
 #pragma unroll
         for (int i = 0; i < W; ++i) {
@@ -496,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
           const uint2 out = U.last < 0 ? make_uint2(0u, 0u)
                                        : make_uint2(ptx::pack_bf16x2(__fmul_rn(A.x, f), __fmul_rn(A.y, f)),
                                                     ptx::pack_bf16x2(__fmul_rn(A.z, f), __fmul_rn(A.w, f)));
-          *reinterpret_cast<uint2*>(p.o + (int64_t(U.t) * p.Hq + U.kh * p.G + head) * D + at_d) = out;
+          *reinterpret_cast<uint2*>(p.o + (int64_t(U.t) * p.Hq + kh * p.G + head) * D + at_d) = out;
         } else {
-          const int64_t at = ((int64_t(U.t) * p.Hkv + U.kh) * p.max_splits + U.split) * p.G + head;
+          const int64_t at = ((int64_t(U.t) * p.Hkv + kh) * p.max_splits + U.split) * p.G + head;
           *reinterpret_cast<float4*>(p.part + at * D + at_d) = A;
           if (at_d == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, Ls);
         }
@@ -775,9 +768,8 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
     p.o = static_cast<uint16_t*>(o) + t0 * h->Hq * h->D;
     p.q_seq = q_seq + t0;
     p.q_pos = q_pos + t0;
-    const int64_t units = int64_t(p.T) * per_token;
-    if (const int rc = bifp4::launch(biattn4::attn_of(h->D), unsigned(std::min<int64_t>(units, h->max_ctas)),
-                                     biattn4::kThreads, size_t(h->smem), st, &p))
+    const int64_t chains = std::min<int64_t>(int64_t(p.T) * w.splits, std::max(1, h->max_ctas / h->Hkv));
+    if (const int rc = bifp4::launch(biattn4::attn_of(h->D), unsigned(chains * h->Hkv), biattn4::kThreads, size_t(h->smem), st, &p))
       return rc;
     if (w.splits > 1)
       if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(int64_t(p.T) * h->Hq), 32 * biattn4::kMergeWarps, 0,
