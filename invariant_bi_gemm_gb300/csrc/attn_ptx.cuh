@@ -339,7 +339,10 @@ struct Workspace {
     captured = false;
     return BI_GEMM_OK;
   }
+  // cudaFree does not wait for the users of memory that came from cudaMallocAsync, and a handle may be dropped right
+  // behind its last call.
   void release() {
+    if (at || !earlier.empty()) cudaDeviceSynchronize();
     if (at) cudaFree(at);
     for (void* p : earlier) cudaFree(p);
     at = nullptr;

@@ -486,7 +486,8 @@ def test_workspace_graphs_and_streams():
     q, seq, pos, four, table = case(Hq, Hkv, D, page, lengths)
     want = bg.BiAttention4(Hq, Hkv, D, page).run(q, seq, pos, *four, table, 2999)
     att = bg.BiAttention4(Hq, Hkv, D, page)
-    assert att.workspace_size(3, 511) == 0 and att.workspace_size(3, 2999) > 0 and att.workspace_size(0, 10) == 0
+    assert att.workspace_size(3, 2999) > att.workspace_size(3, 511) > att.workspace_size(0, 10) == 0
+    assert bg.BiAttention4(8, 8, D, page).workspace_size(3, 255) == 0        # one part
     torch.cuda.synchronize()
     with pytest.raises(bg.BiGemmError) as e:           # a captured call that nothing made room for
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
@@ -508,6 +509,24 @@ def test_workspace_graphs_and_streams():
     other = att.run(q, seq, pos, *four, table, 2999, stream=s)
     s.synchronize()
     assert torch.equal(other, want)
+
+
+def test_a_handle_dropped_right_behind_its_call():
+    """Its workspace outlives the call: the results are those of a handle that stays."""
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    lengths = [6000, 20, 5000, 6000]
+    q, seq, pos, four, table = case(Hq, Hkv, D, page, lengths)
+    att, pre = bg.BiAttention4(Hq, Hkv, D, page), bg.BiPromptAttention(Hq, Hkv, D, page)
+    k, v = att.expand(*four, torch.arange(four[0].shape[0], device="cuda", dtype=torch.int32))
+    keep = bg.BiAttention(Hq, Hkv, D, page)
+    start, first = i32([0, 4]), i32([5996])
+    calls = (lambda h: h.run(q, seq, pos, *four, table, 5999), lambda h: h.run(q, seq, pos, k, v, table, 5999),
+             lambda h: h.run(q, start, first, k, v, table[:1].contiguous(), 5999))
+    for call, handle, make in zip(calls, (att, keep, pre), (bg.BiAttention4, bg.BiAttention, bg.BiPromptAttention)):
+        want = call(handle)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            assert torch.equal(call(make(Hq, Hkv, D, page)), want)
 
 
 def test_steps_back_to_back_without_a_wait():
