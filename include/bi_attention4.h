@@ -19,15 +19,14 @@
  *
  * A token with q_pos[t] = -1 sees no position: its output is zeros (an empty place of a padded batch).
  *
- * Batch invariance: the keys 0..p are cut at multiples of split_size; the positions of a split, sixteen at a time, go
- * to its 8 / HB parts in turn (HB: the largest of 8, 4, 2, 1 that divides num_kv_heads), a part takes its own in
- * ascending order, and the n parts are merged as eight consecutive groups of ceil(n / 8), ascending, then group by
- * group: all of it a function of p and the handle.  o[t] is a function of q[t], p and K_b, V_b[0..p], bit for bit,
- * whatever else the call holds.  Arithmetic: codes times scales exactly in f16; queries in f16 relative to their
- * head's largest element (a bf16 element at least 2^-25 of it is exact, any other within 2^-36 of it); scores on the
- * tensor cores in fp32; weights exp2 of the score less a running reference of the maximum (moved when passed by more
- * than 8), summed in fp32, rounded to f16 (11 bits) for the product with the values, fp32 accumulation; fp32 merges and
- * division; one bf16 rounding at the end.
+ * Batch invariance: the keys 0..p are cut at multiples of split_size, a split is four interleaved sequences of
+ * 32 positions in ascending order, merged in order, and the n splits are merged as eight consecutive groups of
+ * ceil(n / 8), ascending, then group by group: all of it a function of p.  o[t] is a function of q[t], p and
+ * K_b, V_b[0..p], bit for bit, whatever else the call holds.  Arithmetic: codes times scales exactly in f16;
+ * queries in f16 relative to their head's largest element (a bf16 element at least 2^-25 of it is exact, any
+ * other within 2^-36 of it); scores on the tensor cores in fp32; weights exp2 of the score less a running
+ * reference of the maximum (moved when passed by more than 8), summed in fp32, rounded to f16 (11 bits) for
+ * the product with the values, fp32 accumulation; fp32 merges and division; one bf16 rounding at the end.
  *
  * Conventions (as in bi_gemm.h, whose BI_GEMM_* return codes these functions use):
  *   - q, o bf16 [T, num_q_heads, head_dim]; page_table int32 [num_seqs, max_pages] (entry -1 = no page); q_seq,
@@ -63,8 +62,8 @@ typedef struct {
 } bi_attention4_config;
 
 /* Create a handle.  Requirements (else BI_GEMM_ERR_UNSUPPORTED): head_dim 64 or 128; num_q_heads /
- * num_kv_heads in {1, 2, 4, 8}; num_q_heads <= 4096; page_size 1 .. 2^20; split_size (0 = 256 for each of a
- * split's parts) a multiple of 128 up to 4096; an sm_103 device.  scale finite and > 0, k_scale and v_scale in [2^-64, 2^64] (else
+ * num_kv_heads in {1, 2, 4, 8}; num_q_heads <= 4096; page_size 1 .. 2^20; split_size (0 = 512) a multiple of
+ * 128 up to 4096; an sm_103 device.  scale finite and > 0, k_scale and v_scale in [2^-64, 2^64] (else
  * BI_GEMM_ERR_INVALID_ARG).  Checks on the arguments come before any CUDA call.  *out is NULL on failure. */
 int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
                          int64_t page_size, float scale, float k_scale, float v_scale, int64_t split_size);
@@ -75,8 +74,7 @@ int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_
  * being captured into a graph that needs more than an earlier call left; a graph stays valid when later
  * calls grow it), then queues the attention and, where max_pos leaves more than one split, the merge (of
  * each 512 tokens).  num_pages x page_size x num_kv_heads below 2^32 - 1, max_pos below 2^30 (else
- * BI_GEMM_ERR_UNSUPPORTED).  Asynchronous.  The waits inside a block are bounded (2 s): past the limit it stops, its
- * output is undefined and bi_attention4_get_device_error reports BI_GEMM_ERR_TIMEOUT. */
+ * BI_GEMM_ERR_UNSUPPORTED).  Asynchronous; nothing in it waits for another block. */
 int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t* q_seq, const int32_t* q_pos,
                       const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
                       int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
@@ -93,9 +91,8 @@ int bi_attention4_expand(bi_attention4_t h, const void* k_codes, const void* k_s
                          const void* v_scales, int64_t num_pages, const int32_t* pages, int64_t n, void* k_out,
                          void* v_out, void* stream);
 
-/* Synchronise `stream`; BI_GEMM_ERR_TIMEOUT if a bounded wait expired, else BI_GEMM_ERR_INVALID_ARG if a kernel
- * caught a bad input, since the last call (the status is then cleared); BI_GEMM_ERR_CUDA if synchronisation failed;
- * else BI_GEMM_OK. */
+/* Synchronise `stream`; BI_GEMM_ERR_INVALID_ARG if a kernel caught a bad input since the last call (the
+ * status is then cleared); BI_GEMM_ERR_CUDA if synchronisation failed; else BI_GEMM_OK. */
 int bi_attention4_get_device_error(bi_attention4_t h, void* stream);
 
 int bi_attention4_get_config(bi_attention4_t h, bi_attention4_config* c);

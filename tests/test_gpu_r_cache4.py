@@ -486,8 +486,7 @@ def test_workspace_graphs_and_streams():
     q, seq, pos, four, table = case(Hq, Hkv, D, page, lengths)
     want = bg.BiAttention4(Hq, Hkv, D, page).run(q, seq, pos, *four, table, 2999)
     att = bg.BiAttention4(Hq, Hkv, D, page)
-    assert att.workspace_size(3, 2999) > att.workspace_size(3, 511) > att.workspace_size(0, 10) == 0
-    assert bg.BiAttention4(8, 8, D, page).workspace_size(3, 255) == 0        # one part
+    assert att.workspace_size(3, 511) == 0 and att.workspace_size(3, 2999) > 0 and att.workspace_size(0, 10) == 0
     torch.cuda.synchronize()
     with pytest.raises(bg.BiGemmError) as e:           # a captured call that nothing made room for
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
