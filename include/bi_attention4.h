@@ -20,8 +20,8 @@
  * A token with q_pos[t] = -1 sees no position: its output is zeros (an empty place of a padded batch).
  *
  * Batch invariance: the keys 0..p are cut at multiples of split_size, a split is four interleaved sequences of
- * 32 positions in ascending order, merged in order, and the n splits are merged as eight consecutive groups of
- * ceil(n / 8), ascending, then group by group: all of it a function of p.  o[t] is a function of q[t], p and
+ * 32 positions in ascending order, merged in order, and the n splits are merged in ascending order, above 16 of them
+ * as eight consecutive groups of ceil(n / 8) and then group by group: all of it a function of p.  o[t] is a function of q[t], p and
  * K_b, V_b[0..p], bit for bit, whatever else the call holds.  Arithmetic: codes times scales exactly in f16;
  * queries in f16 relative to their head's largest element (a bf16 element at least 2^-25 of it is exact, any
  * other within 2^-36 of it); scores on the tensor cores in fp32; weights exp2 of the score less a running

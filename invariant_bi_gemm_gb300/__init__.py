@@ -870,7 +870,7 @@ class _Torch:
     def __init__(self):
         import torch
         self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.empty, self.empty_like, self.device = torch.empty, torch.empty_like, torch.device
         self.current_stream = torch._C._cuda_getCurrentRawStream
         self.current_device = torch.cuda.current_device
 
@@ -884,6 +884,12 @@ def _handle_device() -> int:
     if _torch is None:
         _torch = _Torch()
     return _torch.current_device()
+
+
+def _handle_devices():
+    """The same as (index, torch.device)."""
+    index = _handle_device()
+    return index, _torch.device("cuda", index)
 
 
 def _stream_of(stream, index: int) -> int:
@@ -981,7 +987,8 @@ class BiQkRope:
         self.rot_dim = int(rot_dim) if rot_dim is not None else self.D
         self._width, self._page_shape = (self.Hq + 2 * self.Hkv) * self.D, (self.page_size, self.Hkv, self.D)
         self.handle = bi_qkrope_create(self.Hq, self.Hkv, self.D, self.page_size, self.rot_dim, interleaved, eps)
-        self._device = _handle_device()
+        self._device, self._on = _handle_devices()
+        self._run, self._run4 = library().bi_qkrope_run, library().bi_qkrope_run4
 
     @property
     def config(self) -> dict:
@@ -1014,16 +1021,17 @@ class BiQkRope:
         _check_tensor("cos_sin", cos_sin, _torch.f32, angles, index)
         _check_tensor("q_seq", q_seq, i32, (T,), index)
         _check_tensor("q_pos", q_pos, i32, (T,), index)
-        q_out = _take("q_out", q_out, bf16, (T, self.Hq, self.D), index, stream, qkv.device)
+        q_out = _take("q_out", q_out, bf16, (T, self.Hq, self.D), index, stream, self._on)
         return index, T, stride, wq, wk, angles[0], q_out
 
     def run(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_cache, v_cache, page_table, q_out=None, stream=None):
         index, T, stride, wq, wk, positions, q_out = self._rows(qkv, gq, gk, cos_sin, q_seq, q_pos, q_out, stream)
         pages, seqs, per = _check_cache(k_cache, v_cache, page_table, self._page_shape, index)
-        _check(library().bi_qkrope_run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions,
-                                       q_seq.data_ptr(), q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                       pages, page_table.data_ptr(), seqs, per, q_out.data_ptr(),
-                                       _stream_of(stream, index)), "bi_qkrope_run")
+        rc = self._run(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions, q_seq.data_ptr(),
+                       q_pos.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), pages, page_table.data_ptr(), seqs, per,
+                       q_out.data_ptr(), _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_qkrope_run")
         return q_out
 
     def run4(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_codes, k_scales, v_codes, v_scales, page_table,
@@ -1032,11 +1040,11 @@ class BiQkRope:
         and v_scale, the codes and scales that BiQuant4 "nvfp4" gives the rows that run() would store."""
         index, T, stride, wq, wk, positions, q_out = self._rows(qkv, gq, gk, cos_sin, q_seq, q_pos, q_out, stream)
         pages, seqs, per = _check_cache4(k_codes, k_scales, v_codes, v_scales, page_table, self._page_shape, index)
-        _check(library().bi_qkrope_run4(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions,
-                                        q_seq.data_ptr(), q_pos.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(),
-                                        v_codes.data_ptr(), v_scales.data_ptr(), k_scale, v_scale, pages,
-                                        page_table.data_ptr(), seqs, per, q_out.data_ptr(), _stream_of(stream, index)),
-               "bi_qkrope_run4")
+        rc = self._run4(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions, q_seq.data_ptr(),
+                        q_pos.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                        k_scale, v_scale, pages, page_table.data_ptr(), seqs, per, q_out.data_ptr(), _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_qkrope_run4")
         return q_out
 
     __call__ = run
@@ -1132,7 +1140,8 @@ class BiAttention4:
         self._page_shape = (self.page_size, self.Hkv, self.D)
         self.handle = bi_attention4_create(self.Hq, self.Hkv, self.D, self.page_size, self.scale, self.k_scale,
                                            self.v_scale, split_size)
-        self._device = _handle_device()
+        self._device, self._on = _handle_devices()
+        self._run, self._expand = library().bi_attention4_run, library().bi_attention4_expand
 
     @property
     def config(self) -> dict:
@@ -1143,10 +1152,11 @@ class BiAttention4:
         pages, seqs, per = _check_cache4(k_codes, k_scales, v_codes, v_scales, page_table, self._page_shape, index)
         _check_tensor("q_seq", q_seq, _torch.i32, (T,), index)
         _check_tensor("q_pos", q_pos, _torch.i32, (T,), index)
-        _check(library().bi_attention4_run(self.handle, q.data_ptr(), T, q_seq.data_ptr(), q_pos.data_ptr(),
-                                           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                           v_scales.data_ptr(), pages, page_table.data_ptr(), seqs, per, max_pos,
-                                           o.data_ptr(), _stream_of(stream, index)), "bi_attention4_run")
+        rc = self._run(self.handle, q.data_ptr(), T, q_seq.data_ptr(), q_pos.data_ptr(), k_codes.data_ptr(),
+                       k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), pages, page_table.data_ptr(), seqs, per,
+                       max_pos, o.data_ptr(), _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_attention4_run")
         return o
 
     __call__ = run
@@ -1159,11 +1169,12 @@ class BiAttention4:
             raise ValueError(f"k_codes must be a tensor on cuda:{self._device}")
         count = _check_codes(k_codes, k_scales, v_codes, v_scales, self._page_shape, index)
         _check_tensor("pages", pages, _torch.i32, (n,), index)
-        k = _take("k", k, _torch.bf16, (n, *self._page_shape), index, stream, k_codes.device)
-        v = _take("v", v, _torch.bf16, (n, *self._page_shape), index, stream, k_codes.device)
-        _check(library().bi_attention4_expand(self.handle, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                              v_scales.data_ptr(), count, pages.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                              _stream_of(stream, index)), "bi_attention4_expand")
+        k = _take("k", k, _torch.bf16, (n, *self._page_shape), index, stream, self._on)
+        v = _take("v", v, _torch.bf16, (n, *self._page_shape), index, stream, self._on)
+        rc = self._expand(self.handle, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), count,
+                          pages.data_ptr(), n, k.data_ptr(), v.data_ptr(), _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_attention4_expand")
         return k, v
 
     def device_error(self, stream=None) -> int:
@@ -1211,7 +1222,8 @@ class BiQuant4:
         self.K, self.kind, self.tensor_scale = int(K), kind, float(tensor_scale)
         fmt, self.block = _FP4[kind]
         self.handle = bi_quant4_create(self.K, fmt, self.tensor_scale)
-        self._device = _handle_device()
+        self._device, self._on = _handle_devices()
+        self._run, self._expand = library().bi_quant4_run, library().bi_quant4_expand
 
     @property
     def config(self) -> dict:
@@ -1226,10 +1238,11 @@ class BiQuant4:
             stride, inner = x.stride()
             if inner != 1 or stride < K:
                 raise ValueError("x rows must be contiguous and must not overlap")
-        codes = _take("codes", codes, _torch.u8, (M, K // 2), index, stream, x.device)
-        scales = _take("scales", scales, _torch.u8, _scale_tiles(M, K, self.block), index, stream, x.device)
-        _check(library().bi_quant4_run(self.handle, x.data_ptr(), M, stride, codes.data_ptr(), scales.data_ptr(),
-                                       _stream_of(stream, index)), "bi_quant4_run")
+        codes = _take("codes", codes, _torch.u8, (M, K // 2), index, stream, self._on)
+        scales = _take("scales", scales, _torch.u8, _scale_tiles(M, K, self.block), index, stream, self._on)
+        rc = self._run(self.handle, x.data_ptr(), M, stride, codes.data_ptr(), scales.data_ptr(), _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_quant4_run")
         return codes, scales
 
     __call__ = run
@@ -1242,9 +1255,10 @@ class BiQuant4:
         M = codes.shape[0]
         _check_tensor("codes", codes, _torch.u8, (M, self.K // 2), index)
         _check_tensor("scales", scales, _torch.u8, _scale_tiles(M, self.K, self.block), index)
-        y = _take("y", y, _torch.bf16, (M, self.K), index, stream, codes.device)
-        _check(library().bi_quant4_expand(self.handle, codes.data_ptr(), scales.data_ptr(), M, y.data_ptr(),
-                                          _stream_of(stream, index)), "bi_quant4_expand")
+        y = _take("y", y, _torch.bf16, (M, self.K), index, stream, self._on)
+        rc = self._expand(self.handle, codes.data_ptr(), scales.data_ptr(), M, y.data_ptr(), _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_quant4_expand")
         return y
 
     def close(self) -> None:
@@ -1272,7 +1286,8 @@ class BiGemm4:
         self.K, self.N, self.kind, self.out = int(K), int(N), kind, out
         fmt, self.block = _FP4[kind]
         self.handle = bi_gemm4_create(self.K, self.N, fmt, out == "f32")
-        self._device = _handle_device()
+        self._device, self._on = _handle_devices()
+        self._run = library().bi_gemm4_run
         self._w, self._sw = (self.N, self.K // 2), _scale_tiles(self.N, self.K, self.block)
         self._dtype = _torch.f32 if out == "f32" else _torch.bf16
 
@@ -1289,9 +1304,11 @@ class BiGemm4:
         _check_tensor("sx", sx, u8, _scale_tiles(M, self.K, self.block), index)
         _check_tensor("w", w, u8, self._w, index)
         _check_tensor("sw", sw, u8, self._sw, index)
-        y = _take("y", y, self._dtype, (M, self.N), index, stream, x.device)
-        _check(library().bi_gemm4_run(self.handle, x.data_ptr(), sx.data_ptr(), M, w.data_ptr(), sw.data_ptr(), alpha,
-                                      y.data_ptr(), _stream_of(stream, index)), "bi_gemm4_run")
+        y = _take("y", y, self._dtype, (M, self.N), index, stream, self._on)
+        rc = self._run(self.handle, x.data_ptr(), sx.data_ptr(), M, w.data_ptr(), sw.data_ptr(), alpha, y.data_ptr(),
+                       _stream_of(stream, index))
+        if rc:
+            _check(rc, "bi_gemm4_run")
         return y
 
     __call__ = run

@@ -502,31 +502,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   ptx::cp_async_wait<0>();
 }
 
-// Splits of a token's query head, a block each: warp w sums the w-th of eight consecutive groups of ceil(n / 8)
-// splits, ascending; the groups are added in order.
+// Up to kSolo splits of a token's query head are summed in ascending order by one warp (eight heads a block: a block a
+// head took 51 us for 8192 heads of 9 splits); more of them as eight consecutive groups of ceil(n / 8) by the
+// warps of a block, ascending, the groups added in order.  n depends on the token's position alone.
+constexpr int kSolo = 16;
+
+// Splits s0 .. s1 - 1 of the head whose first is slot0, in order: the largest reference and, relative to it, the sum of the
+// sums and this lane's dimensions.
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p) {
-  constexpr int PER = D / 32;                             // dimensions a lane
-  __shared__ float sums[kMergeWarps][D];
-  __shared__ float2 mls[kMergeWarps];
-  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int32_t t = int32_t(blockIdx.x / p.Hq), h = int32_t(blockIdx.x - uint32_t(t) * p.Hq);
-  const int32_t n = splits_of(p, p.q_seq[t], p.q_pos[t], false);
-  if (n <= 1) return;                                     // written by its unit, or refused
-  const int32_t kh = h / p.G, hd = h - kh * p.G;
-  const int64_t slot0 = (int64_t(t) * p.Hkv + kh) * p.max_splits * p.G + hd;
-  const int32_t c = (n + kMergeWarps - 1) / kMergeWarps, s0 = min(n, warp * c), s1 = min(n, s0 + c);
+__device__ __forceinline__ void sum_splits(const Params& p, int64_t slot0, int32_t s0, int32_t s1, int lane, float& M, float& L,
+                                           float (&A)[D / 32]) {
+  constexpr int PER = D / 32, BATCH = 8;
   const float2* mlp = reinterpret_cast<const float2*>(p.ml) + slot0;
-  float M = -INFINITY;
+  M = -INFINITY;
   for (int32_t s = s0 + lane; s < s1; s += 32) M = fmaxf(M, mlp[int64_t(s) * p.G].x);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  float L = 0.0f, A[PER];
+  L = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) A[i] = 0.0f;
-  constexpr int BATCH = 8;
   for (int32_t b = s0; b < s1; b += BATCH) {
     float2 ml[BATCH];
     float v[BATCH][PER];
@@ -554,6 +548,40 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p)
       }
     }
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p) {
+  constexpr int PER = D / 32;                             // dimensions a lane
+  __shared__ float sums[kMergeWarps][D];
+  __shared__ float2 mls[kMergeWarps];
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int32_t t = int32_t(blockIdx.x / p.Hq);
+  int32_t h = int32_t(blockIdx.x - uint32_t(t) * p.Hq);
+  const int32_t n = splits_of(p, p.q_seq[t], p.q_pos[t], false);
+  if (n <= 1) return;                                     // written by its unit, or refused
+  const bool solo = n <= kSolo;
+  if (solo) {
+    if (h % kMergeWarps != 0) return;
+    h += warp;
+    if (h >= p.Hq) return;
+  }
+  const int32_t kh = h / p.G, hd = h - kh * p.G;
+  const int64_t slot0 = (int64_t(t) * p.Hkv + kh) * p.max_splits * p.G + hd;
+  const int32_t c = (n + kMergeWarps - 1) / kMergeWarps;
+  const int32_t s0 = solo ? 0 : min(n, warp * c), s1 = solo ? n : min(n, s0 + c);
+  float M, L, A[PER];
+  sum_splits<D>(p, slot0, s0, s1, lane, M, L, A);
+  uint16_t* o = p.o + (int64_t(t) * p.Hq + h) * D;
+  if (solo) {
+    const float f = __fdiv_rn(p.v_scale, L);
+#pragma unroll
+    for (int j = 0; j < PER; j += 2)
+      *reinterpret_cast<uint32_t*>(o + lane * PER + j) = ptx::pack_bf16x2(__fmul_rn(A[j], f), __fmul_rn(A[j + 1], f));
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < PER; ++j) sums[warp][lane * PER + j] = A[j];
   if (lane == 0) mls[warp] = make_float2(M, L);
@@ -572,10 +600,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p)
       }
     }
     const float f = __fdiv_rn(p.v_scale, Ls);
-    *reinterpret_cast<uint32_t*>(p.o + (int64_t(t) * p.Hq + h) * D + 2 * threadIdx.x) =
-        ptx::pack_bf16x2(__fmul_rn(a0, f), __fmul_rn(a1, f));
+    *reinterpret_cast<uint32_t*>(o + 2 * threadIdx.x) = ptx::pack_bf16x2(__fmul_rn(a0, f), __fmul_rn(a1, f));
   }
 }
+
+constexpr int kExpand = 4;                // pieces a thread expands
 
 struct ExpandParams {
   const uint8_t* kc;
@@ -586,7 +615,7 @@ struct ExpandParams {
   uint16_t* ko;
   uint16_t* vo;
   uint32_t* status;
-  int64_t num_pages, blocks;              // blocks of sixteen elements in all
+  int64_t num_pages, pieces;              // pieces of eight elements in all
   int64_t per_page;                       // and of a page
   float k_scale, v_scale;
 };
@@ -594,28 +623,38 @@ struct ExpandParams {
 __global__ void __launch_bounds__(256) expand_kernel(const ExpandParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= p.blocks) return;
-  const int64_t n = i / p.per_page, r = i - n * p.per_page;
-  const int64_t page = p.pages[n];
-  if (page < 0 || page >= p.num_pages) {
-    if (page != -1 && r == 0) atomicOr(p.status, kErrPage);
-    return;
+  // eight elements a thread: half a block, so that a warp's stores are whole lines
+  int64_t at[kExpand];
+  uint32_t kc[kExpand], vc[kExpand], ks[kExpand], vs[kExpand];
+  const int64_t first = int64_t(blockIdx.x) * (256 * kExpand) + threadIdx.x;
+#pragma unroll
+  for (int u = 0; u < kExpand; ++u) {
+    const int64_t i = first + u * 256;
+    at[u] = -1;
+    if (i < p.pieces) {
+      const int64_t n = i / p.per_page, r = i - n * p.per_page;
+      const int64_t page = p.pages[n];
+      if (page >= 0 && page < p.num_pages) {
+        at[u] = page * p.per_page + r;
+        kc[u] = reinterpret_cast<const uint32_t*>(p.kc)[at[u]];
+        vc[u] = reinterpret_cast<const uint32_t*>(p.vc)[at[u]];
+        ks[u] = p.ks[at[u] >> 1];
+        vs[u] = p.vs[at[u] >> 1];
+      } else if (page != -1 && r == 0) {
+        atomicOr(p.status, kErrPage);
+      }
+    }
   }
-  const int64_t at = page * p.per_page + r;
-  const uint2 kc = *reinterpret_cast<const uint2*>(p.kc + at * 8), vc = *reinterpret_cast<const uint2*>(p.vc + at * 8);
-  const float ks = bifp4::scale_value<true>(p.ks[at], p.k_scale), vs = bifp4::scale_value<true>(p.vs[at], p.v_scale);
-  uint32_t out[8];
-  bifp4::values_bf16(kc.x, ks, out);
-  bifp4::values_bf16(kc.y, ks, out + 4);
-  uint4* dst = reinterpret_cast<uint4*>(p.ko + i * 16);
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
-  bifp4::values_bf16(vc.x, vs, out);
-  bifp4::values_bf16(vc.y, vs, out + 4);
-  dst = reinterpret_cast<uint4*>(p.vo + i * 16);
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+  for (int u = 0; u < kExpand; ++u) {
+    if (at[u] < 0) continue;
+    const int64_t i = first + u * 256;
+    uint32_t out[4];
+    bifp4::values_bf16(kc[u], bifp4::scale_value<true>(ks[u], p.k_scale), out);
+    *reinterpret_cast<uint4*>(p.ko + i * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+    bifp4::values_bf16(vc[u], bifp4::scale_value<true>(vs[u], p.v_scale), out);
+    *reinterpret_cast<uint4*>(p.vo + i * 8) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
 }
 
 inline const void* attn_of(int D) {
@@ -806,13 +845,15 @@ BI_GEMM_API int bi_attention4_expand(bi_attention4_t h, const void* k_codes, con
   p.vo = static_cast<uint16_t*>(v_out);
   p.status = h->d_status;
   p.num_pages = num_pages;
-  p.per_page = int64_t(h->page_size) * h->Hkv * (h->D / 16);
-  if (n > (int64_t(1) << 31) / p.per_page * 256) return BI_GEMM_ERR_UNSUPPORTED;
-  p.blocks = n * p.per_page;
+  p.per_page = int64_t(h->page_size) * h->Hkv * (h->D / 8);
+  constexpr int64_t kBlock = 256 * biattn4::kExpand;
+  if (n > ((int64_t(1) << 31) - 1) / p.per_page * kBlock) return BI_GEMM_ERR_UNSUPPORTED;
+  p.pieces = n * p.per_page;
   p.k_scale = h->k_scale;
   p.v_scale = h->v_scale;
-  if ((p.blocks + 255) / 256 >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
-  return bifp4::launch(reinterpret_cast<const void*>(&biattn4::expand_kernel), unsigned((p.blocks + 255) / 256), 256, 0,
+  const int64_t blocks = (p.pieces + kBlock - 1) / kBlock;
+  if (blocks >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
+  return bifp4::launch(reinterpret_cast<const void*>(&biattn4::expand_kernel), unsigned(blocks), 256, 0,
                        static_cast<cudaStream_t>(stream), &p);
 }
 

@@ -70,6 +70,7 @@ struct Params {
   uint8_t* vc4;
   uint8_t* vs4;
   float k_scale, v_scale;
+  float k_inv, v_inv;       // reciprocals of six times those
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -226,7 +227,7 @@ struct Lane {
     uint32_t most = bifp4::most_of(w, 4);
     most = max(most, __shfl_xor_sync(mask, most, 1));
     const float g = key ? p.k_scale : p.v_scale;
-    const bifp4::Scale s = bifp4::nvfp4_scale(most, g, __fmul_rn(6.0f, g));
+    const bifp4::Scale s = bifp4::nvfp4_scale(most, g, __fmul_rn(6.0f, g), key ? p.k_inv : p.v_inv);
     uint32_t word = s.byte << (8 * ((l >> 1) & 3));       // four blocks' scales to one lane of eight
     word |= __shfl_xor_sync(mask, word, 2);
     word |= __shfl_xor_sync(mask, word, 4);
@@ -271,7 +272,7 @@ __device__ __forceinline__ int64_t slot_of(const Params& p, int32_t b, int32_t p
 
 // A block per token or few: the form for few tokens.
 template <int D, bool kInterleaved, bool kFour>
-__global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kFour ? 2 : 4) qkrope_kernel(const Params p) {
   constexpr int LANES = D / 8;
   // Programmatic dependent launch: the block may start while the previous kernel finishes and
   // waits for it (and its memory) before its first global access.
@@ -590,6 +591,8 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
     p.vs4 = static_cast<uint8_t*>(four->vs);
     p.k_scale = four->k_scale;
     p.v_scale = four->v_scale;
+    p.k_inv = 1.0f / (6.0f * four->k_scale);
+    p.v_inv = 1.0f / (6.0f * four->v_scale);
   }
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));

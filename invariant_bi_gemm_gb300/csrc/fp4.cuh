@@ -72,15 +72,22 @@ struct Scale {
   bool zero;          // every code is 0
   bool wide;          // above the largest scale: a quotient may be out of the range that in_units corrects
 };
-__device__ __forceinline__ Scale nvfp4_scale(uint32_t amax_bits, float g, float six_g) {
+// q = x / d for a d whose reciprocal r is known to an ulp: the product with r, corrected by its remainder (exact).  What
+// is representable comes out exact, so that ties are seen as such.
+__device__ __forceinline__ float divided(float x, float d, float r) {
+  const float q = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+// (inv_six_g: the rounded reciprocal of six_g)
+__device__ __forceinline__ Scale nvfp4_scale(uint32_t amax_bits, float g, float six_g, float inv_six_g) {
   Scale s;
-  const float most = __fdiv_rn(__uint_as_float(amax_bits << 16), six_g);
-  s.byte = e4m3_of(most);
-  s.wide = most > 448.0f;
+  const float amax = __uint_as_float(amax_bits << 16);
+  s.wide = !(__fmul_rn(amax, inv_six_g) <= 448.0f);
+  s.byte = s.wide ? 0x7Eu : e4m3_of(divided(amax, six_g, inv_six_g));
   s.unit = __fmul_rn(f16_lo(e4m3_pair(s.byte)), g);
   s.zero = s.byte == 0u;
   if (amax_bits >= 0x7F80u) s.byte = kNanE4M3, s.zero = true;
-  s.inv = __frcp_rn(s.unit);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inv) : "f"(s.unit));
   return s;
 }
 __device__ __forceinline__ Scale mxfp4_scale(uint32_t amax_bits) {
@@ -94,15 +101,27 @@ __device__ __forceinline__ Scale mxfp4_scale(uint32_t amax_bits) {
   if (s.zero) s.byte = kNanE8M0;
   return s;
 }
-// x / unit, correctly rounded: the product with the rounded reciprocal, corrected by its remainder (exact).  A
-// quotient on the border of two codes is representable, so that ties are seen as such.
+// The places of two bf16 values (a word) on the codes' grid: x / unit.
 template <bool kNv>
-__device__ __forceinline__ float in_units(float x, const Scale& s) {
-  if constexpr (!kNv) return __fmul_rn(x, s.inv);
-  if (s.wide) return __fdiv_rn(x, s.unit);
-  const float q = __fmul_rn(x, s.inv);
-  const float y = __fmaf_rn(__fmaf_rn(-q, s.unit, x), s.inv, q);
-  return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));   // (a zero keeps its sign)
+__device__ __forceinline__ void in_units(uint32_t w, const Scale& s, float& lo, float& hi) {
+  const uint32_t a = w << 16, b = w & 0xFFFF0000u;
+  if constexpr (!kNv) {
+    lo = __fmul_rn(__uint_as_float(a), s.inv), hi = __fmul_rn(__uint_as_float(b), s.inv);
+  } else if (s.wide) {                                // (out of the range that `divided` corrects)
+    lo = __fdiv_rn(__uint_as_float(a), s.unit), hi = __fdiv_rn(__uint_as_float(b), s.unit);
+  } else {
+    // `divided`, both at a time; a zero keeps its sign
+    uint64_t x, r, d, q, e;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(a), "r"(b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s.inv));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(-s.unit));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(d), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q));
+    uint32_t y, z;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(y), "=r"(z) : "l"(q));
+    lo = __uint_as_float(y | (a & 0x80000000u)), hi = __uint_as_float(z | (b & 0x80000000u));
+  }
 }
 
 // Largest size, as bits, among the bf16 pairs of w (a NaN is above every number).
@@ -130,8 +149,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t* w, const Scale& s)
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = in_units<kNv>(__uint_as_float(w[i] << 16), s);
-    v[2 * i + 1] = in_units<kNv>(__uint_as_float(w[i] & 0xFFFF0000u), s);
+    in_units<kNv>(w[i], s, v[2 * i], v[2 * i + 1]);
   }
   return codes8(v);
 }
