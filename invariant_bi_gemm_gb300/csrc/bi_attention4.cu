@@ -60,9 +60,10 @@ struct Params {
   float* part;        // [T, Hkv, max_splits, G, D] partial weighted sums
   float* ml;          // [T, Hkv, max_splits, G, 2] (reference, sum)
   uint32_t* status;
-  int64_t num_pages, max_pages, B;
+  int64_t max_pages, B;
+  uint32_t num_pages;
   int32_t T, Hq, Hkv, G, page_size, split, max_splits, max_pos;
-  uint32_t page_mul;  // pos / page_size = pos * page_mul >> page_shift for pos < 2^30
+  uint32_t page_mul;  // pos / page_size = 4 pos * page_mul >> (32 + page_shift) for pos < 2^30
   int32_t page_shift;
   float c;            // scale * k_scale * log2(e)
   float v_scale;
@@ -216,17 +217,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   int32_t lpage = 0, lrow = 0;                           // this lane's page there, fetched ahead, and row of the page
   int lslot = 0;
   bool lmore = true;
+  const int32_t* ltable = p.table;                       // its request's row of the page table
   auto fetch = [&]() {
-    const int32_t pos = min(lpos + lane, L.last);
-    const int32_t pg = int32_t((uint64_t(uint32_t(pos)) * p.page_mul) >> p.page_shift);
-    lrow = pos - pg * p.page_size;
-    lpage = __ldg(p.table + int64_t(seqs[L.t]) * p.max_pages + pg);
+    const uint32_t pos = uint32_t(min(lpos + lane, L.last)), pg = __umulhi(pos << 2, p.page_mul) >> p.page_shift;
+    lrow = int32_t(pos - pg * uint32_t(p.page_size));
+    lpage = __ldg(ltable + pg);
   };
   // Makes L the next unit (from itself on) in which this warp has a step.
   auto seek = [&]() {
     while (L.v < v_end) {
       lpos = L.first + warp * kStep;
       if (lpos <= L.last) {
+        ltable = p.table + int64_t(seqs[L.t]) * p.max_pages;
         fetch();
         return;
       }
@@ -238,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
     if (lmore) {
       const uint32_t dst = ring + uint32_t(lslot) * C::STEP;
       // a lane looks one position up; a row's place comes from its lane (fewer than 2^32 - 1 rows of a head: the host)
-      const bool here = lpos + lane <= L.last, good = lpage >= 0 && lpage < p.num_pages;
-      uint32_t at = uint32_t((int64_t(lpage) * p.page_size + lrow) * p.Hkv + kh);
+      const bool here = lpos + lane <= L.last, good = uint32_t(lpage) < p.num_pages;
+      uint32_t at = (uint32_t(lpage) * uint32_t(p.page_size) + uint32_t(lrow)) * uint32_t(p.Hkv) + uint32_t(kh);
       if (__all_sync(0xFFFFFFFFu, here && good)) {
 #pragma unroll
         for (int i = 0; i < kStep / ROWS; ++i) {
@@ -785,7 +787,7 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
   p.part = static_cast<float*>(h->ws.at);
   p.ml = reinterpret_cast<float*>(static_cast<uint8_t*>(h->ws.at) + w.part);
   p.status = h->d_status;
-  p.num_pages = num_pages;
+  p.num_pages = uint32_t(num_pages);      // (below 2^32 - 1, see above; a table's entry is below 2^31)
   p.max_pages = max_pages;
   p.B = num_seqs;
   p.Hq = h->Hq;
@@ -797,8 +799,8 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
   p.max_pos = int32_t(max_pos);
   int log2 = 0;
   while ((1 << log2) < h->page_size) ++log2;
-  p.page_shift = 30 + log2;
-  p.page_mul = uint32_t((uint64_t(1) << p.page_shift) / uint64_t(h->page_size) + 1);
+  p.page_shift = log2;
+  p.page_mul = uint32_t((uint64_t(1) << (30 + log2)) / uint64_t(h->page_size) + 1);
   p.c = float(double(h->scale) * double(h->k_scale) * 1.4426950408889634);
   p.v_scale = h->v_scale;
   for (int64_t t0 = 0; t0 < T; t0 += biattn4::kTokens) {

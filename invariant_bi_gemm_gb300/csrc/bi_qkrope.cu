@@ -272,7 +272,7 @@ __device__ __forceinline__ int64_t slot_of(const Params& p, int32_t b, int32_t p
 
 // A block per token or few: the form for few tokens.
 template <int D, bool kInterleaved, bool kFour>
-__global__ void __launch_bounds__(kThreads, kFour ? 2 : 4) qkrope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
   constexpr int LANES = D / 8;
   // Programmatic dependent launch: the block may start while the previous kernel finishes and
   // waits for it (and its memory) before its first global access.
