@@ -17,11 +17,13 @@
 #include "bi_attention.cu"
 #include "bi_prompt.cu"
 #include "bi_qkrope.cu"
+#include "bi_gemm4.cu"
 
 #include <cuda_bf16.h>
 
 #include "../../tests/include/bi_gemm_controls.h"
 #include "../../tests/include/bi_paged_controls.h"
+#include "../../tests/include/bi_fp4_controls.h"
 
 #define BI_CTL_API extern "C" __attribute__((visibility("default")))
 
@@ -257,3 +259,34 @@ BI_CTL_API int bi_ctl_qkrope_get_device_error(bi_qkrope_t h, void* stream) {
 }
 
 BI_CTL_API int bi_ctl_qkrope_destroy(bi_qkrope_t h) { return bi_qkrope_destroy(h); }
+
+// The operators in 4 bits.
+BI_CTL_API int bi_ctl_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t format, int32_t out_f32) {
+  return bi_gemm4_create(out, K, N, format, out_f32);
+}
+
+BI_CTL_API int bi_ctl_gemm4_run(bi_gemm4_t h, const void* x, const void* sx, int64_t M, const void* w, const void* sw,
+                                float alpha, void* y, void* stream) {
+  return bi_gemm4_run(h, x, sx, M, w, sw, alpha, y, stream);
+}
+
+BI_CTL_API int bi_ctl_gemm4_stall(bi_gemm4_t h, const void* x, const void* sx, int64_t M, const void* w, const void* sw,
+                                  float alpha, void* y, uint64_t timeout_ns, void* stream) {
+  if (timeout_ns == 0) return BI_GEMM_ERR_INVALID_ARG;
+  return gemm4_run(h, x, sx, M, w, sw, alpha, y, stream, 1, timeout_ns);
+}
+
+BI_CTL_API int bi_ctl_gemm4_get_device_error(bi_gemm4_t h, void* stream) { return bi_gemm4_get_device_error(h, stream); }
+
+BI_CTL_API int bi_ctl_gemm4_destroy(bi_gemm4_t h) { return bi_gemm4_destroy(h); }
+
+BI_CTL_API int bi_ctl_qkrope_stall4(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq,
+                                    const void* gk, const float* cos_sin, int64_t num_positions, const int32_t* q_seq,
+                                    const int32_t* q_pos, void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                                    float k_scale, float v_scale, int64_t num_pages, const int32_t* page_table,
+                                    int64_t num_seqs, int64_t max_pages, void* q_out, uint64_t timeout_ns, void* stream) {
+  if (timeout_ns == 0) return BI_GEMM_ERR_INVALID_ARG;
+  const Four four{k_codes, k_scales, v_codes, v_scales, k_scale, v_scale};
+  return qkrope_run(h, qkv, T, qkv_stride, gq, gk, cos_sin, num_positions, q_seq, q_pos, nullptr, nullptr, num_pages,
+                    page_table, num_seqs, max_pages, q_out, stream, 0, timeout_ns, &four);
+}

@@ -1,11 +1,14 @@
 """Matrices in 4 bits (include/bi_fp4.h): quantisation against the format's definition bit by bit, the values
 back, the product against 64-bit sums, and batch invariance of both."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import fp4_ref as ref
 import invariant_bi_gemm_gb300 as bg
+from gpu_util import Controls, stream_ptr
 
 pytestmark = pytest.mark.gpu
 KINDS = ("mxfp4", "nvfp4")
@@ -254,3 +257,31 @@ def test_sizes_of_nothing_and_refusals():
         q.run(xb[:, :K])
     with pytest.raises(ValueError):
         q.run(xb[:, :K].t())
+
+
+@pytest.mark.parametrize("M", [20, 700])
+def test_waits_of_both_forms_end(M):
+    """Failure injection (test controls): nothing is loaded, every wait ends after 50 ms, and the handle serves the next
+    call as if nothing had been."""
+    K, N = 1024, 4096
+    x, sx, _ = operand(M, K, "nvfp4", 1)
+    w, sw, _ = operand(N, K, "nvfp4", 2)
+    g = bg.BiGemm4(K, N)
+    assert (M > g.config["few_rows"]) == (M == 700)
+    want = g.run(x, sx, w, sw)
+    L, P, I64, I32, F = Controls().L, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+    L.bi_ctl_gemm4_create.argtypes = [ctypes.POINTER(P), I64, I64, I32, I32]
+    L.bi_ctl_gemm4_run.argtypes = [P, P, P, I64, P, P, F, P, P]
+    L.bi_ctl_gemm4_stall.argtypes = [P, P, P, I64, P, P, F, P, ctypes.c_uint64, P]
+    L.bi_ctl_gemm4_get_device_error.argtypes, L.bi_ctl_gemm4_destroy.argtypes = [P, P], [P]
+    h, y = P(), torch.zeros_like(want)
+    assert L.bi_ctl_gemm4_create(ctypes.byref(h), K, N, bg.BI_NVFP4, 0) == 0
+    a = (h, x.data_ptr(), sx.data_ptr(), M, w.data_ptr(), sw.data_ptr(), 1.0, y.data_ptr())
+    for _ in range(2):
+        assert L.bi_ctl_gemm4_stall(*a, 50_000_000, stream_ptr()) == 0
+        assert L.bi_ctl_gemm4_get_device_error(h, stream_ptr()) == bg.BI_GEMM_ERR_TIMEOUT
+        assert L.bi_ctl_gemm4_run(*a, stream_ptr()) == 0
+        assert L.bi_ctl_gemm4_get_device_error(h, stream_ptr()) == 0
+        assert torch.equal(y, want)
+        y.zero_()
+    assert L.bi_ctl_gemm4_destroy(h) == 0

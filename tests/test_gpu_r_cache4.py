@@ -1,6 +1,7 @@
 """The paged cache in 4 bits (include/bi_attention4.h, bi_qkrope_run4): the append against the bf16 append bit by bit,
 attention against 64-bit sums over the values that the cache stands for, bits across batches and pages, places
 that nothing may see, expansion, and the operators together."""
+import ctypes
 import math
 
 import numpy as np
@@ -9,6 +10,8 @@ import torch
 
 import fp4_ref as ref
 import invariant_bi_gemm_gb300 as bg
+from gpu_util import Controls, stream_ptr
+from test_gpu_p_streams import owner
 
 pytestmark = pytest.mark.gpu
 CPU = torch.device("cpu")
@@ -572,3 +575,74 @@ def test_sizes_of_nothing_and_refusals():
     with pytest.raises(bg.BiGemmError):
         att.run(**{**good, "max_pos": -2})
     assert math.isclose(att.scale, D ** -0.5)
+
+
+def test_the_appends_waits_end():
+    """Failure injection (test controls): block 0 of the form for many tokens loads nothing; its waits end after 50 ms."""
+    Hq, Hkv, D, page = 16, 8, 128, 16
+    L, P, I64 = Controls().L, ctypes.c_void_p, ctypes.c_int64
+    L.bi_ctl_qkrope_create.argtypes = [ctypes.POINTER(P), I64, I64, I64, I64, I64, ctypes.c_int32, ctypes.c_float]
+    L.bi_ctl_qkrope_stall4.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, P, P, P, P, ctypes.c_float, ctypes.c_float, I64, P,
+                                       I64, I64, P, ctypes.c_uint64, P]
+    L.bi_ctl_qkrope_get_device_error.argtypes, L.bi_ctl_qkrope_destroy.argtypes = [P, P], [P]
+    rope = bg.BiQkRope(Hq, Hkv, D, page)
+    T = rope.config["ring_from"] + 5
+    table, pages = table_of([-(-T // page)])
+    four = empty_cache4(pages, page, Hkv, D)
+    qkv = torch.randn((T, (Hq + 2 * Hkv) * D), device="cuda").to(torch.bfloat16)
+    cs, seq, pos = cos_sin(T, D), torch.zeros(T, dtype=torch.int32, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+    q = torch.zeros((T, Hq, D), dtype=torch.bfloat16, device="cuda")
+    h = P()
+    assert L.bi_ctl_qkrope_create(ctypes.byref(h), Hq, Hkv, D, page, D, 0, 1e-6) == 0
+    assert L.bi_ctl_qkrope_stall4(h, qkv.data_ptr(), T, qkv.shape[1], None, None, cs.data_ptr(), T, seq.data_ptr(),
+                                  pos.data_ptr(), *[a.data_ptr() for a in four], 1.0, 1.0, pages, table.data_ptr(), 1,
+                                  table.shape[1], q.data_ptr(), 50_000_000, stream_ptr()) == 0
+    assert L.bi_ctl_qkrope_get_device_error(h, stream_ptr()) == bg.BI_GEMM_ERR_TIMEOUT
+    assert L.bi_ctl_qkrope_get_device_error(h, stream_ptr()) == 0
+    assert L.bi_ctl_qkrope_destroy(h) == 0
+    assert torch.equal(rope.run4(qkv, None, None, cs, seq, pos, *four, table), rope.run4(qkv, None, None, cs, seq, pos, *four, table))
+    assert rope.device_error() == bg.BI_GEMM_OK
+
+
+def test_tensors_of_another_device_are_refused():
+    """Pointers of another GPU never reach a kernel of the handle's."""
+    q, seq, pos, four, table = case(8, 2, 64, 16, [50, 40])
+    att, rope, quant, gemm = bg.BiAttention4(8, 2, 64, 16), bg.BiQkRope(8, 2, 64, 16), bg.BiQuant4(128), bg.BiGemm4(128, 64)
+    codes, scales = quant.run(torch.zeros((3, 128), dtype=torch.bfloat16, device="cuda"))
+    for op in (att, rope, quant, gemm):
+        op._device += 1                        # (as if it had been made there)
+    qkv = torch.zeros((2, 12 * 64), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: att.run(q, seq, pos, *four, table, 49), lambda: att.expand(*four, i32([0])),
+                 lambda: rope.run4(qkv, None, None, cos_sin(64, 64), seq, pos, *four, table),
+                 lambda: quant.run(torch.zeros((3, 128), dtype=torch.bfloat16, device="cuda")),
+                 lambda: quant.expand(codes, scales), lambda: gemm.run(codes, scales, codes, scales)):
+        with pytest.raises(ValueError):
+            call()
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+@pytest.mark.parametrize("which", ["quant", "expand", "gemm", "append", "attend", "pages"])
+def test_outputs_belong_to_the_stream_that_writes_them(which, as_number):
+    """Outputs that a call makes itself, on a stream that is not the current one: memory of that stream."""
+    q, seq, pos, four, table = case(8, 2, 64, 16, [700, 40])
+    att, rope, quant, gemm = bg.BiAttention4(8, 2, 64, 16), bg.BiQkRope(8, 2, 64, 16), bg.BiQuant4(256), bg.BiGemm4(256, 96)
+    x = torch.randn((5, 256), device="cuda").to(torch.bfloat16)
+    codes, scales = quant.run(x)
+    w, sw = quant.run(torch.randn((96, 256), device="cuda").to(torch.bfloat16))
+    qkv, cs = torch.randn((2, 12 * 64), device="cuda").to(torch.bfloat16), cos_sin(704, 64)
+    calls = {"quant": lambda s: quant.run(x, stream=s)[:1], "expand": lambda s: [quant.expand(codes, scales, stream=s)],
+             "gemm": lambda s: [gemm.run(codes, scales, w, sw, stream=s)],
+             "append": lambda s: [rope.run4(qkv, None, None, cs, seq, pos, *four, table, stream=s)],
+             "attend": lambda s: [att.run(q, seq, pos, *four, table, 699, stream=s)],
+             "pages": lambda s: att.expand(*four, table[1, :3].contiguous(), stream=s)}
+    call = calls[which]
+    want = [o.clone() for o in call(None)]
+    torch.cuda.synchronize()
+    side, current = torch.cuda.Stream(), torch.cuda.current_stream()
+    for o in [*call(None), *call(current), *call(current.cuda_stream)]:
+        assert owner(o) == current.cuda_stream
+    torch.cuda.synchronize()
+    got = call(side.cuda_stream if as_number else side)
+    side.synchronize()
+    for o, was in zip(got, want):
+        assert owner(o) == side.cuda_stream and torch.equal(o, was)
