@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
     *gave_up = 0u;
     ptx::fence_barrier_init();
     ptx::fence_proxy_async_smem();
+    for (const CUtensorMap* m : {&mx, &mw, &msx, &msw, &my}) ptx::prefetch_tensormap(m);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(misc), 512);
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(kFewThreads)
     *gave_up = 0u;
     ptx::fence_barrier_init();
     ptx::fence_proxy_async_smem();
+    for (const CUtensorMap* m : {&mx, &mw, &my}) ptx::prefetch_tensormap(m);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(misc), uint32_t(f.tmem_cols));
