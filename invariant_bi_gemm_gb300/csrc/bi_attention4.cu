@@ -849,7 +849,7 @@ BI_GEMM_API int bi_attention4_expand(bi_attention4_t h, const void* k_codes, con
   p.num_pages = num_pages;
   p.per_page = int64_t(h->page_size) * h->Hkv * (h->D / 8);
   constexpr int64_t kBlock = 256 * biattn4::kExpand;
-  if (n > ((int64_t(1) << 31) - 1) / p.per_page * kBlock) return BI_GEMM_ERR_UNSUPPORTED;
+  if (n > (((int64_t(1) << 31) - 1) * kBlock) / p.per_page) return BI_GEMM_ERR_UNSUPPORTED;
   p.pieces = n * p.per_page;
   p.k_scale = h->k_scale;
   p.v_scale = h->v_scale;

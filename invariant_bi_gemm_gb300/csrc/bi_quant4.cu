@@ -34,7 +34,9 @@ struct Params {
   uint16_t* y;
   int64_t pieces;                        // of sixteen elements, in all
   int64_t stride;                        // of x, in elements
-  int32_t per_row;                       // pieces of a row
+  int32_t per_row;                       // pieces of a row: 8 .. 2^20
+  uint32_t row_mul;                      // i / per_row = i * row_mul >> row_shift for i < 2^21
+  int32_t row_shift;
   float g, six_g, inv_six_g;
 };
 
@@ -43,19 +45,34 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int c, int per_tile_row
   return ((r >> 7) * per_tile_row + (c >> 2)) * 512 + int64_t((r & 31) * 16 + ((r >> 5) & 3) * 4);
 }
 
+// Where a block's pieces lie: its first one's row by one division, the others' by a multiplication.
+struct Place {
+  int64_t row0;
+  uint32_t rest;
+  __device__ __forceinline__ Place(const Params& p, int64_t first) {
+    row0 = p.pieces >> 32 ? first / p.per_row : int64_t(uint32_t(first) / uint32_t(p.per_row));
+    rest = uint32_t(first - row0 * p.per_row);
+  }
+  __device__ __forceinline__ void operator()(const Params& p, uint32_t off, int64_t& row, int& piece) const {
+    const uint32_t i = rest + off, r = uint32_t(uint64_t(i) * p.row_mul >> p.row_shift);
+    row = row0 + r;
+    piece = int(i - r * uint32_t(p.per_row));
+  }
+};
+
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t first = int64_t(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+  const Place place(p, int64_t(blockIdx.x) * (kThreads * kUnroll));
   uint32_t w[kUnroll][8];
   int64_t row[kUnroll];
   int piece[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int64_t i = first + u * kThreads;
-    row[u] = i < p.pieces ? i / p.per_row : 0;
-    piece[u] = int(i - row[u] * p.per_row);
+    place(p, threadIdx.x + u * kThreads, row[u], piece[u]);
     if (i < p.pieces) {
       const uint4* src = reinterpret_cast<const uint4*>(p.x + row[u] * p.stride + piece[u] * 16);
       const uint4 a = src[0], b = src[1];
@@ -97,13 +114,16 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t first = int64_t(blockIdx.x) * (kThreads * 2 * kUnroll) + threadIdx.x, halves = 2 * p.pieces;
+  const Place place(p, int64_t(blockIdx.x) * (kThreads * kUnroll));
   uint32_t codes[2 * kUnroll], byte[2 * kUnroll];
 #pragma unroll
   for (int u = 0; u < 2 * kUnroll; ++u) {
     const int64_t i = first + u * kThreads;
     if (i < halves) {
-      const int64_t row = (i >> 1) / p.per_row;
-      const int piece = int((i >> 1) - row * p.per_row), c = kNv ? piece : piece >> 1;
+      int64_t row;
+      int piece;
+      place(p, (threadIdx.x + u * kThreads) >> 1, row, piece);
+      const int c = kNv ? piece : piece >> 1;
       codes[u] = reinterpret_cast<const uint32_t*>(p.codes)[i];
       byte[u] = p.scales[scale_word(row, c, kNv ? p.per_row >> 2 : p.per_row >> 3) + (c & 3)];
     }
@@ -165,7 +185,12 @@ int quant4_launch(bi_quant4* h, const void* fn, biq4::Params& p, int64_t M, void
   p.g = h->g;
   p.six_g = 6.0f * h->g;
   p.inv_six_g = 1.0f / p.six_g;
+  int log2 = 0;
+  while ((1 << log2) < p.per_row) ++log2;
+  p.row_shift = 21 + log2;
+  p.row_mul = uint32_t((uint64_t(1) << p.row_shift) / uint64_t(p.per_row) + 1);
   const int64_t per_block = biq4::kThreads * biq4::kUnroll, blocks = (p.pieces + per_block - 1) / per_block;
+  static_assert(biq4::kThreads * biq4::kUnroll < (1 << 20), "Place: offsets below 2^21");
   if (blocks >= (int64_t(1) << 31)) return BI_GEMM_ERR_UNSUPPORTED;
   return bifp4::launch(fn, unsigned(blocks), biq4::kThreads, 0, static_cast<cudaStream_t>(stream), &p);
 }
