@@ -357,10 +357,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
 // column in an instruction nor the instruction's extent enters (compared over every shape that the tests run).
 //
 // A CTA's R rows of w take the MMA's rows that they have in their tile of 128 (so that a tile of scales serves as it
-// is); the other rows multiply whatever the neighbouring slots hold, and are not stored.  A stage is two slots of 256
-// elements of K: a turn of the loading loop costs about 250 clocks besides its copies, of 28 each.
+// is); the other rows multiply whatever the neighbouring slots hold, and are not stored.
+//
+// A stage is two or four slots of 256 elements of K.  A turn of the loading loop costs about 250 clocks besides its
+// copies, of 28 each; one of the issuing loop about 160 besides its products, of 40 each (128 rows of 32 bytes from
+// shared memory, however few columns meet them), and its scales' copies, of 11: for 1 x 14336 x 4096 these, not the loads,
+// take the time (9.7 us without the products, 13.5 with them; two loading warps 8.0 and 13.7).  Four slots are taken
+// where three such stages fit: 13.5 -> 12.3 us there, 64 x 14336 x 4096 14.3 -> 13.2, 16 x 32768 x 2048 30.8 -> 27.2; with
+// two stages 64 x 4096 x 14336 9.4 -> 11.0, with one 1 x 512 x 4096 2.7 -> 2.9.
 
-constexpr int kSlots = 2;                 // of a stage
 constexpr int kFewMaxStages = 8;
 constexpr int kFewCols = 128;             // rows of x at most
 constexpr int kFewThreads = 256;          // warps: 0 loads, 1 products, 4 .. 7 results
@@ -369,24 +374,25 @@ struct FewParams {
   Params p;
   int32_t rows;             // R
   int32_t cols;             // columns of the MMA: rows of x of a tile, a multiple of 16
-  int32_t stages;
+  int32_t slots, stages;
   int32_t tmem_cols;
   int32_t off_w, off_sf, off_stg, off_bar;   // shared memory: x ring at 0, w ring, scales ring, staging, barriers
 };
 
-template <bool kNv, bool kF32>
+template <bool kNv, bool kF32, int kSlots_>
 struct Few {
+  static constexpr int kSlots = kSlots_;                     // of a stage
   static constexpr int TILES_K = kNv ? 4 : 2;                // scale tiles of a slot
   static constexpr int SF_BYTES = kSlots * TILES_K * 512;    // of a stage and operand
   static constexpr int SF_COLS = TILES_K * 8;                // TMEM columns of a slot's scales
   static constexpr int OUT = kF32 ? 4 : 2, STG_BYTES = 32 * 32 * OUT;      // of a warp
 };
 
-template <bool kNv, bool kF32>
+template <bool kNv, bool kF32, int kSlots>
 __global__ void __launch_bounds__(kFewThreads)
     few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                const __grid_constant__ CUtensorMap my, const FewParams f) {
-  using C = Few<kNv, kF32>;
+  using C = Few<kNv, kF32, kSlots>;
   const Params& p = f.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -592,7 +598,7 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* at, uint64_t r
 
 struct Kernel {
   const void* wide = nullptr;
-  const void* few = nullptr;
+  const void* few[2] = {nullptr, nullptr};   // two and four slots
   int wide_smem = 0, stages = 0;
 };
 template <bool kNv, bool kF32>
@@ -600,7 +606,8 @@ Kernel kernel() {
   using W = Wide<kNv, kF32>;
   Kernel k;
   k.wide = reinterpret_cast<const void*>(&wide_kernel<W>);
-  k.few = reinterpret_cast<const void*>(&few_kernel<kNv, kF32>);
+  k.few[0] = reinterpret_cast<const void*>(&few_kernel<kNv, kF32, 2>);
+  k.few[1] = reinterpret_cast<const void*>(&few_kernel<kNv, kF32, 4>);
   k.wide_smem = W::SMEM;
   k.stages = W::STAGES;
   return k;
@@ -612,19 +619,20 @@ inline Kernel select(bool nv, bool f32) {
 
 constexpr int kSmemSm = 228 * 1024, kSmemBlock = 227 * 1024;
 
-// Layout of the form for few rows with `per_sm` CTAs an SM: as deep a ring as shared and tensor memory hold; its
-// bytes of shared memory, 0 where fewer than two stages fit.
-int few_layout(FewParams& f, bool nv, bool f32, int per_sm) {
-  const int tiles = nv ? 4 : 2, sf = 2 * kSlots * tiles * 512;
+// Layout of the form for few rows with `per_sm` CTAs an SM and stages of n slots: as deep a ring as shared and tensor
+// memory hold; its bytes of shared memory, 0 where fewer than `least` stages fit.
+int few_layout(FewParams& f, bool nv, bool f32, int per_sm, int n, int least) {
+  const int tiles = nv ? 4 : 2, sf = 2 * n * tiles * 512;
+  f.slots = n;
   f.tmem_cols = 512 / per_sm;
   const int stg = 4 * 32 * 32 * (f32 ? 4 : 2), bar = (2 * kFewMaxStages + 3) * 8 + 16;
   const int room = std::min(kSmemBlock, kSmemSm / per_sm - 1024) - 1024 - stg - bar;
   // The MMA reads 128 rows around a CTA's own: up to 128 - R before the ring of w (the x ring, filled up to them) and
   // behind it.
   const int margin = (128 - f.rows) * 128;
-  f.stages = std::min(kFewMaxStages, (f.tmem_cols - f.cols) / (kSlots * tiles * 8));
-  for (; f.stages >= 2; --f.stages) {
-    const int slots = f.stages * kSlots;
+  f.stages = std::min(kFewMaxStages, (f.tmem_cols - f.cols) / (n * tiles * 8));
+  for (; f.stages >= least; --f.stages) {
+    const int slots = f.stages * n;
     f.off_w = std::max(slots * f.cols * 128, margin);
     f.off_sf = f.off_w + slots * f.rows * 128;
     f.off_stg = (f.off_sf + std::max(f.stages * sf, margin) + 1023) / 1024 * 1024;
@@ -656,7 +664,8 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
   const big4::Kernel k = big4::select(format == BI_NVFP4, out_f32 != 0);
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaFuncSetAttribute(k.wide, cudaFuncAttributeMaxDynamicSharedMemorySize, k.wide_smem) != cudaSuccess ||
-      cudaFuncSetAttribute(k.few, cudaFuncAttributeMaxDynamicSharedMemorySize, big4::kSmemBlock) != cudaSuccess) {
+      cudaFuncSetAttribute(k.few[0], cudaFuncAttributeMaxDynamicSharedMemorySize, big4::kSmemBlock) != cudaSuccess ||
+      cudaFuncSetAttribute(k.few[1], cudaFuncAttributeMaxDynamicSharedMemorySize, big4::kSmemBlock) != cudaSuccess) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -711,7 +720,8 @@ bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, i
   if (M > big4::kFewCols && units() > h->sms) return false;
   while (f.rows > 32 && units() < h->sms / (M > big4::kFewCols ? 3 : 2)) f.rows /= 2;
   per_sm = units() > h->sms && f.cols <= 32 ? 2 : 1;
-  smem = big4::few_layout(f, h->nv, h->f32, per_sm);
+  smem = h->K > 4 * big4::kStageK ? big4::few_layout(f, h->nv, h->f32, per_sm, 4, 3) : 0;
+  if (!smem) smem = big4::few_layout(f, h->nv, h->f32, per_sm, 2, 2);
   return smem > 0;
 }
 
@@ -785,7 +795,7 @@ int gemm4_run(bi_gemm4* h, const void* x, const void* sx, int64_t M, const void*
   cfg.numAttrs = 1;
   void* few_args[4] = {&mx, &mw, &my, &f};
   void* wide_args[6] = {&mx, &mw, &msx, &msw, &my, &p};
-  if (cudaLaunchKernelExC(&cfg, few ? h->kern.few : h->kern.wide, few ? few_args : wide_args) != cudaSuccess) {
+  if (cudaLaunchKernelExC(&cfg, few ? h->kern.few[f.slots / 4] : h->kern.wide, few ? few_args : wide_args) != cudaSuccess) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
