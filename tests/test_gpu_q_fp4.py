@@ -170,6 +170,25 @@ def test_a_rows_bits_do_not_depend_on_the_batch(kind, K, N):
                 assert torch.equal(y.view(torch.uint8), whole[first:first + M].contiguous().view(torch.uint8)), (M, first)
 
 
+@pytest.mark.parametrize("out", ("bf16", "f32"))
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("K,N", [(5760, 4104), (2176, 4104), (1152, 9736)])
+def test_large_and_small_tiles_have_the_same_bits(kind, K, N, out):
+    """700 rows in tiles of 256 x 256 on CTA pairs; 1 to 128 of them in the smaller tiles, in stages of four and of two
+    slots whose last ones are not full."""
+    x, sx, _ = operand(700, K, kind, 3, -6, 6)
+    w, sw, _ = operand(N, K, kind, 4, -6, 6)
+    raw = ref.from_tiles(host(sx), 700)
+    g = bg.BiGemm4(K, N, kind, out)
+    assert -(-700 // 128) * -(-N // 128) > torch.cuda.get_device_properties(0).multi_processor_count
+    whole = g.run(x, sx, w, sw)
+    for M in (1, 20, 64, 100, 128):
+        for first in (0, 700 - M):
+            part = torch.from_numpy(ref.to_tiles(raw[first:first + M], 0x11)).cuda()
+            y = g.run(x[first:first + M].contiguous(), part, w, sw)
+            assert torch.equal(y.view(torch.uint8), whole[first:first + M].contiguous().view(torch.uint8)), (M, first)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M", [5, 200])
 def test_a_nan_stays_in_its_row_and_column(kind, M):
