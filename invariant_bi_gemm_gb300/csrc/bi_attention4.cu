@@ -41,6 +41,7 @@ constexpr int kRing = 2;                  // steps of a warp's ring
 constexpr int kBlocksPerSm = 4;
 constexpr int kTokens = 512;              // of a launch
 constexpr int kHeads = 8;                 // columns of the MMA
+constexpr int kGroup = 4;                 // KV heads of the larger blocks
 constexpr int kDefaultSplit = 512;
 constexpr int kMergeWarps = 8;
 constexpr float kLift = 7.0f;             // weights are 2^7 at the reference, 2^15 at most
@@ -69,8 +70,10 @@ struct Params {
   float v_scale;
 };
 
-template <int D>
+// HB: KV heads of a block, four warps each.
+template <int D, int HB>
 struct Cfg {
+  static constexpr int THREADS = kThreads * HB;
   static constexpr int CODES = D / 2, SCALES = D / 16;           // bytes of a row
   // rows of values lie 16 bytes further apart than they are long, so that the rows 0, 2, 4, 6 that a load takes at
   // once are on different banks
@@ -78,14 +81,14 @@ struct Cfg {
   static constexpr int OFF_V = kStep * CODES, OFF_KS = OFF_V + kStep * VROW, OFF_VS = OFF_KS + kStep * SCALES;
   static constexpr int STEP = OFF_VS + kStep * SCALES;
   static constexpr int RING = kRing * STEP;                      // of a warp
-  static constexpr int OFF_ML = kWarps * RING;
-  static constexpr int OFF_CUM = OFF_ML + kWarps * kHeads * 8;
-  static constexpr int OFF_O = (OFF_CUM + (3 * kTokens + 1 + kWarps) * 4 + 15) / 16 * 16;
+  static constexpr int OFF_ML = HB * kWarps * RING;
+  static constexpr int OFF_CUM = OFF_ML + HB * kWarps * kHeads * 8;
+  static constexpr int OFF_O = (OFF_CUM + (3 * kTokens + 1 + HB * kWarps) * 4 + 15) / 16 * 16;
   static_assert(STEP % 16 == 0 && OFF_ML % 16 == 0, "alignment");
   // The warps' parts meet in shared memory, eight heads in two halves of the dimensions: four blocks fit an SM.
   __host__ __device__ static constexpr int halves(int G) { return G == 8 ? 2 : 1; }
   __host__ __device__ static constexpr int row(int G) { return D / halves(G) + 4; }   // floats of a head
-  static constexpr int smem(int G) { return OFF_O + kWarps * G * row(G) * 4; }
+  static constexpr int smem(int G) { return OFF_O + HB * kWarps * G * row(G) * 4; }
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
@@ -116,6 +119,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Both halves of a times the lower or upper half of b.
+template <int kHalf>
+__device__ __forceinline__ uint32_t mul_f16x2_by(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kHalf == 0)
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {l, l};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 t;\n\tmov.b32 {l, h}, %2;\n\tmov.b32 t, {h, h};\n\tmul.rn.f16x2 %0, %1, t;\n\t}"
+        : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -135,21 +150,26 @@ __device__ __forceinline__ int32_t splits_of(const Params& p, int32_t b, int32_t
   return bad ? 0 : pos / p.split + 1;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Params p) {
-  using C = Cfg<D>;
+// kTwin: up to four heads, each on two of the MMA's columns.
+template <int D, bool kTwin, int HB>
+__global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(const Params p) {
+  using C = Cfg<D, HB>;
+  constexpr int HEADS = kTwin ? 1 : 2;                   // whose scores and sums a lane has
+  constexpr int TILES = kTwin ? D / 32 : D / 16;         // of the weighted values
   extern __shared__ __align__(128) uint8_t smem[];
   int32_t* cum = reinterpret_cast<int32_t*>(smem + C::OFF_CUM);
   int32_t* seqs = cum + kTokens + 1;                     // the tokens' requests and positions
   int32_t* poss = seqs + kTokens;
   int32_t* sums = poss + kTokens;
-  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int lane = int(threadIdx.x) & 31, g = lane >> 2, t4 = lane & 3;
+  const int group = HB == 1 ? 0 : int(threadIdx.x) / kThreads;   // its KV head of the block's
+  const int tid = int(threadIdx.x) - group * kThreads, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // first unit (of one KV head) of every token
   int32_t carry = 0;
-  for (int base = 0; base < p.T; base += kThreads) {
-    const int i = base + tid;
+  for (int base = 0; base < p.T; base += C::THREADS) {
+    const int i = base + int(threadIdx.x);
     int32_t n = 0;
     if (i < p.T) {
       seqs[i] = p.q_seq[i];
@@ -162,25 +182,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
       const int32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) sums[warp] = x;
+    if (lane == 31) sums[group * kWarps + warp] = x;
     __syncthreads();
     int32_t before = carry;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < HB * kWarps; ++w) {
       const int32_t s = sums[w];
-      if (w < warp) before += s;
+      if (w < group * kWarps + warp) before += s;
       carry += s;
     }
     if (i < p.T) cum[i] = before + x - n;
     __syncthreads();
   }
-  if (tid == 0) cum[p.T] = carry;
+  if (threadIdx.x == 0) cum[p.T] = carry;
   __syncthreads();
 
   // Block (chain, kh) takes a run of consecutive (token, split) of its head, so that a token's query is prepared once
   // for its splits there; the blocks of a chain's heads read neighbouring rows at the same time.
-  const int32_t kh = int32_t(blockIdx.x % uint32_t(p.Hkv)), chain = int32_t(blockIdx.x / uint32_t(p.Hkv));
-  const int32_t chains = int32_t(gridDim.x / uint32_t(p.Hkv));
+  const uint32_t across = uint32_t(p.Hkv) / HB;          // blocks of a chain
+  const int32_t kh = int32_t(blockIdx.x % across) * HB + group, chain = int32_t(blockIdx.x / across);
+  const int32_t chains = int32_t(gridDim.x / across);
   const int32_t v_end = int32_t(int64_t(carry) * (chain + 1) / chains);
   auto locate = [&](Unit& r) {                           // t: cum[t] <= v < cum[t + 1]
     for (;;) {
@@ -206,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   };
 
   // ---- this warp's loads, ahead of its products by kRing steps and across units
-  const uint32_t ring = ptx::smem_u32(smem) + uint32_t(warp) * C::RING;
+  const uint32_t ring = ptx::smem_u32(smem) + uint32_t(group * kWarps + warp) * C::RING;
   constexpr int CH = C::CODES / 16, ROWS = 32 / CH;      // 16-byte chunks of a row, rows an instruction
   const int row = lane / CH, ch = lane % CH;
   const uint8_t* kc = p.kc + ch * 16;
@@ -284,22 +305,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
   for (int i = 0; i < kRing; ++i) issue();
 
   // ---- products
+  auto meet = [&]() {                                    // the four warps of a head
+    if constexpr (HB == 1)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kThreads) : "memory");
+  };
   int slot = 0;
-  float* so = reinterpret_cast<float*>(smem + C::OFF_O);
-  float* sml = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* so = reinterpret_cast<float*>(smem + C::OFF_O) + group * kWarps * p.G * C::row(p.G);
+  float* sml = reinterpret_cast<float*>(smem + C::OFF_ML) + group * kWarps * kHeads * 2;
   int32_t token = -1;
   uint32_t qf[D / 8];
-  float fac[2] = {0.0f, 0.0f};
+  float fac[HEADS];
+  const int column = kTwin ? g >> 1 : g;                 // the head of this lane's column
+  // (kTwin) the weights of two positions, one in either half, to the half that the column's dimensions are in
+  const uint32_t even = g & 1 ? 0x1044u : 0x4410u, odd = g & 1 ? 0x3244u : 0x4432u;
   Unit U;
   for (start(U); U.v < v_end; advance(U)) {
     // the query in f16, relative to its head's largest element
     if (U.t != token) {
       token = U.t;
-      const uint16_t* src = p.q + (int64_t(U.t) * p.Hq + kh * p.G + g) * D + t4 * (D / 4);
+      const uint16_t* src = p.q + (int64_t(U.t) * p.Hq + kh * p.G + column) * D + t4 * (D / 4);
       uint32_t most = 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const uint4 v = g < p.G ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+        const uint4 v = column < p.G ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
         qf[4 * i] = v.x, qf[4 * i + 1] = v.y, qf[4 * i + 2] = v.z, qf[4 * i + 3] = v.w;
       }
       most = bifp4::most_of(qf, D / 8);
@@ -311,40 +341,41 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         qf[i] = pack_f16x2(__uint_as_float(qf[i] << 16) * up, __uint_as_float(qf[i] & 0xFFFF0000u) * up);
-      // the factors of the two heads whose scores this lane has
+      // the factors of the heads whose scores this lane has
       // (above zero, so that a hidden position's -inf stays one)
-      fac[0] = fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4), p.c), 1e-45f);
-      fac[1] = fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4), p.c), 1e-45f);
+#pragma unroll
+      for (int j = 0; j < HEADS; ++j)
+        fac[j] = fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4 * j), p.c), 1e-45f);
     }
     // (the reference m is a product's sum as it comes from the MMA; the difference to it is taken before the factor, so
     // that it is exact near the reference however large the scores are)
-    float acc[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float acc[TILES][4], m[HEADS], l[HEADS];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
+    for (int j = 0; j < HEADS; ++j) m[j] = -INFINITY, l[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
     for (int32_t pos = U.first + warp * kStep; pos <= U.last; pos += kWarps * kStep) {
       ptx::cp_async_wait<kRing - 1>();
       __syncwarp();
-      const uint8_t* src = smem + warp * C::RING + slot * C::STEP;
+      const uint8_t* src = smem + (group * kWarps + warp) * C::RING + slot * C::STEP;
       if (++slot == kRing) slot = 0;
       // scores: two sixteens of positions side by side, for two chains of products
       constexpr int W = D / 32;                           // words of codes a lane has of a row
       float s[2][4];
-      uint32_t kw[4][W], ksc[4][2];                       // rows g, g + 8, g + 16, g + 24
+      uint32_t kw[4][W], ksc[4];                          // rows g, g + 8, g + 16, g + 24
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int at = 8 * r + g;
         if constexpr (D == 128) {
           const uint4 v = *reinterpret_cast<const uint4*>(src + at * C::CODES + t4 * 16);
           kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
-          const uint32_t b = bifp4::e4m3_pair(*reinterpret_cast<const uint16_t*>(src + C::OFF_KS + at * 8 + 2 * t4));
-          ksc[r][0] = __byte_perm(b, b, 0x1010), ksc[r][1] = __byte_perm(b, b, 0x3232);
+          ksc[r] = bifp4::e4m3_pair(*reinterpret_cast<const uint16_t*>(src + C::OFF_KS + at * 8 + 2 * t4));
         } else {
           const uint2 v = *reinterpret_cast<const uint2*>(src + at * C::CODES + t4 * 8);
           kw[r][0] = v.x, kw[r][1] = v.y;
-          const uint32_t b = bifp4::e4m3_pair(src[C::OFF_KS + at * 4 + t4]);
-          ksc[r][0] = ksc[r][1] = __byte_perm(b, b, 0x1010);
+          ksc[r] = bifp4::e4m3_pair(src[C::OFF_KS + at * 4 + t4]);
         }
       }
 #pragma unroll
@@ -358,11 +389,36 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
           uint32_t x[4], y[4];
           bifp4::values8(kw[2 * h][i], x);
           bifp4::values8(kw[2 * h + 1][i], y);
-          const int k = i * 2 / W;
+          // (D = 128: 32 dimensions a lane, two blocks)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = mul_f16x2(x[j], ksc[2 * h][k]), y[j] = mul_f16x2(y[j], ksc[2 * h + 1][k]);
+          for (int j = 0; j < 4; ++j) {
+            if (D == 64 || i < 2) {
+              x[j] = mul_f16x2_by<0>(x[j], ksc[2 * h]), y[j] = mul_f16x2_by<0>(y[j], ksc[2 * h + 1]);
+            } else {
+              x[j] = mul_f16x2_by<1>(x[j], ksc[2 * h]), y[j] = mul_f16x2_by<1>(y[j], ksc[2 * h + 1]);
+            }
+          }
           mma(s[h], x[0], y[0], x[1], y[1], qf[4 * i], qf[4 * i + 1]);
           mma(s[h], x[2], y[2], x[3], y[3], qf[4 * i + 2], qf[4 * i + 3]);
+        }
+      }
+      constexpr int VW = D / 64;                          // words of codes a lane has of a row of values
+      uint32_t vw[kTwin ? 4 : 1][2][VW], vsc[kTwin ? 4 : 1];
+      if constexpr (kTwin) {                              // (asked for before they are needed)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint8_t* a = src + C::OFF_V + (8 * q + 2 * t4 + r) * C::VROW + g * (C::CODES / 8);
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(a);
+              vw[q][r][0] = v.x, vw[q][r][1] = v.y;
+            } else {
+              vw[q][r][0] = *reinterpret_cast<const uint32_t*>(a);
+            }
+          }
+          const uint8_t* a = src + C::OFF_VS + (8 * q + 2 * t4) * C::SCALES + (D == 128 ? g : g >> 1);
+          vsc[q] = bifp4::e4m3_pair(uint32_t(a[0]) | uint32_t(a[C::SCALES]) << 8);
         }
       }
       if (pos + kStep - 1 > U.last) {
@@ -373,79 +429,101 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
             if (pos + 16 * h + 8 * (j >> 1) + g > U.last) s[h][j] = -INFINITY;
       }
       bool move = false;
-      float top[2];
+      float top[HEADS];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < HEADS; ++j) {
         top[j] = fmaxf(fmaxf(s[0][j], s[0][j + 2]), fmaxf(s[1][j], s[1][j + 2]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], o));
         move |= __fmul_rn(__fsub_rn(top[j], m[j]), fac[j]) > kSlack;
       }
       if (__any_sync(0xFFFFFFFFu, move)) {                // (a head's rule looks at that head alone)
-        float f[2];
+        float f[HEADS];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < HEADS; ++j) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], o));
           const bool mv = __fmul_rn(__fsub_rn(top[j], m[j]), fac[j]) > kSlack;
           f[j] = mv ? ex2(__fmul_rn(__fsub_rn(m[j], top[j]), fac[j])) : 1.0f;
           if (mv) m[j] = top[j];
           l[j] *= f[j];
         }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < TILES; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] *= f[j & 1];
+          for (int j = 0; j < 4; ++j) acc[i][j] *= f[j & (HEADS - 1)];
       }
+      if constexpr (kTwin) {
+        // (columns 2 t4 and 2 t4 + 1 are one head's: s[h][j] and s[h][j + 1] are equal)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int q = 0; q < 4; ++q) {                     // eight positions
+          const float e = ex2(__fmaf_rn(__fsub_rn(s[q >> 1][2 * (q & 1)], m[0]), fac[0], kLift));
+          l[0] += e;
+          const uint32_t b = transposed(pack_f16x2(e, e));
+          const uint32_t b0 = __byte_perm(b, 0u, even), b1 = __byte_perm(b, 0u, odd);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[h][j] = ex2(__fmaf_rn(__fsub_rn(s[h][j], m[j & 1]), fac[j & 1], kLift));
-        l[0] += s[h][0] + s[h][2];
-        l[1] += s[h][1] + s[h][3];
-        const uint32_t b0 = transposed(pack_f16x2(s[h][0], s[h][1])), b1 = transposed(pack_f16x2(s[h][2], s[h][3]));
-        constexpr int W = D / 64;                         // words of codes a lane has of a row
-        uint32_t w[4][W], sc[2];
+          for (int i = 0; i < VW; ++i) {
+            uint32_t x[4], y[4];
+            bifp4::values8(vw[q][0][i], x);
+            bifp4::values8(vw[q][1][i], y);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = 16 * h + 2 * t4 + (r & 1) + 8 * (r >> 1);
-          const uint8_t* a = src + C::OFF_V + at * C::VROW + g * (C::CODES / 8);
-          if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(a);
-            w[r][0] = v.x, w[r][1] = v.y;
-          } else {
-            w[r][0] = *reinterpret_cast<const uint32_t*>(a);
+            for (int j = 0; j < 2; ++j)
+              mma(acc[2 * i + j], mul_f16x2_by<0>(x[2 * j], vsc[q]), mul_f16x2_by<0>(x[2 * j + 1], vsc[q]),
+                  mul_f16x2_by<1>(y[2 * j], vsc[q]), mul_f16x2_by<1>(y[2 * j + 1], vsc[q]), b0, b1);
           }
         }
+      } else {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint8_t* a = src + C::OFF_VS + (16 * h + 2 * t4 + 8 * r) * C::SCALES + (D == 128 ? g : g >> 1);
-          sc[r] = bifp4::e4m3_pair(uint32_t(a[0]) | uint32_t(a[C::SCALES]) << 8);
-        }
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          // even and odd dimensions of the lane's eight, a pair of positions each
-          uint32_t x0[4], x1[4], y0[4], y1[4];
-          constexpr uint32_t LO = 0x0F0F0F0Fu;
-          bifp4::values8((w[0][i] & LO) | ((w[1][i] << 4) & ~LO), x0);
-          bifp4::values8(((w[0][i] >> 4) & LO) | (w[1][i] & ~LO), x1);
-          bifp4::values8((w[2][i] & LO) | ((w[3][i] << 4) & ~LO), y0);
-          bifp4::values8(((w[2][i] >> 4) & LO) | (w[3][i] & ~LO), y1);
+          for (int j = 0; j < 4; ++j) s[h][j] = ex2(__fmaf_rn(__fsub_rn(s[h][j], m[j & (HEADS - 1)]), fac[j & (HEADS - 1)], kLift));
+          l[0] += s[h][0] + s[h][2];
+          l[HEADS - 1] += s[h][1] + s[h][3];
+          const uint32_t b0 = transposed(pack_f16x2(s[h][0], s[h][1])), b1 = transposed(pack_f16x2(s[h][2], s[h][3]));
+          constexpr int W = D / 64;                         // words of codes a lane has of a row
+          uint32_t w[4][W], sc[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma(acc[4 * i + j], mul_f16x2(x0[j], sc[0]), mul_f16x2(x1[j], sc[0]), mul_f16x2(y0[j], sc[1]),
-                mul_f16x2(y1[j], sc[1]), b0, b1);
+          for (int r = 0; r < 4; ++r) {
+            const int at = 16 * h + 2 * t4 + (r & 1) + 8 * (r >> 1);
+            const uint8_t* a = src + C::OFF_V + at * C::VROW + g * (C::CODES / 8);
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(a);
+              w[r][0] = v.x, w[r][1] = v.y;
+            } else {
+              w[r][0] = *reinterpret_cast<const uint32_t*>(a);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint8_t* a = src + C::OFF_VS + (16 * h + 2 * t4 + 8 * r) * C::SCALES + (D == 128 ? g : g >> 1);
+            sc[r] = bifp4::e4m3_pair(uint32_t(a[0]) | uint32_t(a[C::SCALES]) << 8);
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            // even and odd dimensions of the lane's eight, a pair of positions each
+            uint32_t x0[4], x1[4], y0[4], y1[4];
+            constexpr uint32_t LO = 0x0F0F0F0Fu;
+            bifp4::values8((w[0][i] & LO) | ((w[1][i] << 4) & ~LO), x0);
+            bifp4::values8(((w[0][i] >> 4) & LO) | (w[1][i] & ~LO), x1);
+            bifp4::values8((w[2][i] & LO) | ((w[3][i] << 4) & ~LO), y0);
+            bifp4::values8(((w[2][i] >> 4) & LO) | (w[3][i] & ~LO), y1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma(acc[4 * i + j], mul_f16x2(x0[j], sc[0]), mul_f16x2(x1[j], sc[0]), mul_f16x2(y0[j], sc[1]),
+                  mul_f16x2(y1[j], sc[1]), b0, b1);
+          }
         }
       }
       __syncwarp();                                       // the slot may be refilled
       issue();
     }
     // ---- the four warps' parts, in order
+    if constexpr (HB > 1) __syncthreads();               // (keeps the heads on neighbouring rows)
     const bool alone = U.split == 0 && U.last == poss[U.t];
     const int halves = C::halves(p.G), dims = D / halves, orow = C::row(p.G);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < HEADS; ++j) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[j] = __fadd_rn(l[j], __shfl_xor_sync(0xFFFFFFFFu, l[j], o));
-      const int head = 2 * t4 + j;
+      const int head = HEADS * t4 + j;
       if (g == 0 && head < p.G) {
         sml[(warp * kHeads + head) * 2] = __fmul_rn(m[j], fac[j]);
         sml[(warp * kHeads + head) * 2 + 1] = l[j];
@@ -455,18 +533,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
       const int d0 = g * (D / 8) - half * dims;           // this lane's first dimension within the half
       if (d0 >= 0 && d0 < dims) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int head = 2 * t4 + j;
+        for (int j = 0; j < HEADS; ++j) {
+          const int head = HEADS * t4 + j;
           if (head < p.G) {
             float* dst = so + (warp * p.G + head) * orow + d0;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              *reinterpret_cast<float4*>(dst + 4 * i) =
-                  make_float4(acc[2 * i][j], acc[2 * i][j + 2], acc[2 * i + 1][j], acc[2 * i + 1][j + 2]);
+            for (int i = 0; i < D / 32; ++i) {
+              if constexpr (kTwin)
+                *reinterpret_cast<float4*>(dst + 4 * i) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+              else
+                *reinterpret_cast<float4*>(dst + 4 * i) =
+                    make_float4(acc[2 * i][j], acc[2 * i][j + 2], acc[2 * i + 1][j], acc[2 * i + 1][j + 2]);
+            }
           }
         }
       }
-      __syncthreads();
+      meet();
       for (int it = tid; it < p.G * (dims / 4); it += kThreads) {
         const int head = it / (dims / 4), d = (it - head * (dims / 4)) * 4;
         float M = -INFINITY, Ls = 0.0f;
@@ -498,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(const Para
           if (at_d == 0) *reinterpret_cast<float2*>(p.ml + at * 2) = make_float2(M, Ls);
         }
       }
-      __syncthreads();
+      meet();
     }
   }
   ptx::cp_async_wait<0>();
@@ -659,8 +741,17 @@ __global__ void __launch_bounds__(256) expand_kernel(const ExpandParams p) {
   }
 }
 
-inline const void* attn_of(int D) {
-  return D == 128 ? reinterpret_cast<const void*>(&attn_kernel<128>) : reinterpret_cast<const void*>(&attn_kernel<64>);
+// With HB = 1 or kGroup KV heads a block (kGroup: heads of 128).
+template <bool kTwin>
+const void* attn_for(int D, int HB) {
+  if (D == 64) return reinterpret_cast<const void*>(&attn_kernel<64, kTwin, 1>);
+  return HB == 1 ? reinterpret_cast<const void*>(&attn_kernel<128, kTwin, 1>)
+                 : reinterpret_cast<const void*>(&attn_kernel<128, kTwin, kGroup>);
+}
+inline const void* attn_of(int D, int G, int HB) { return G <= 4 ? attn_for<true>(D, HB) : attn_for<false>(D, HB); }
+inline int smem_of(int D, int G, int HB) {
+  if (D == 64) return Cfg<64, 1>::smem(G);
+  return HB == 1 ? Cfg<128, 1>::smem(G) : Cfg<128, kGroup>::smem(G);
 }
 inline const void* merge_of(int D) {
   return D == 128 ? reinterpret_cast<const void*>(&merge_kernel<128>) : reinterpret_cast<const void*>(&merge_kernel<64>);
@@ -672,6 +763,7 @@ struct bi_attention4 {
   int Hq = 0, Hkv = 0, D = 0, G = 0, page_size = 0, split = 0;
   float scale = 0.0f, k_scale = 1.0f, v_scale = 1.0f;
   int device = 0, max_ctas = 0, smem = 0;
+  int sms = 0, group_ctas = 0, group_smem = 0;   // of the blocks of kGroup heads (0: they are not for this shape)
   uint32_t* d_status = nullptr;
   biattn_tc::Workspace ws;
 };
@@ -690,16 +782,28 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
     return BI_GEMM_ERR_UNSUPPORTED;
   const int64_t G = num_q_heads / num_kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return BI_GEMM_ERR_UNSUPPORTED;
-  int dev = 0, sms = 0, per_sm = 0;
+  int dev = 0, sms = 0;
   if (const int rc = bifp4::check_device(&dev)) return rc;
-  const int smem = head_dim == 128 ? biattn4::Cfg<128>::smem(int(G)) : biattn4::Cfg<64>::smem(int(G));
   // (the attribute is the kernel's, shared by every handle of the head size: the most any of them needs)
-  const int most = head_dim == 128 ? std::max(biattn4::Cfg<128>::smem(4), biattn4::Cfg<128>::smem(8))
-                                   : std::max(biattn4::Cfg<64>::smem(4), biattn4::Cfg<64>::smem(8));
-  const void* fn = biattn4::attn_of(int(head_dim));
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biattn4::kThreads, smem) != cudaSuccess || per_sm < 1) {
+  auto ready = [&](int HB, int& smem, int& ctas) {
+    const void* fn = biattn4::attn_of(int(head_dim), int(G), HB);
+    smem = biattn4::smem_of(int(head_dim), int(G), HB);
+    int per_sm = 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             biattn4::smem_of(int(head_dim), G <= 4 ? 4 : 8, HB)) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biattn4::kThreads * HB, smem) != cudaSuccess || per_sm < 1)
+      return false;
+    ctas = per_sm * sms;
+    return true;
+  };
+  // Blocks of four KV heads, for calls of many units (bi_attention4_run has their number): their warps read neighbouring
+  // 64-byte pieces of long rows at about the same time.  us, 8 KV heads of 128 (a block a head / four): 256 contexts of
+  // 4600 344 / 285, 64 of 4096 81 / 73, 128 of them at G = 8 186 / 167.  Rows of fewer or shorter heads gain nothing: 4 of 128
+  // 51 / 53, 8 of 64 29 / 32.
+  const bool grouped = head_dim == 128 && num_kv_heads >= 8 && num_kv_heads % biattn4::kGroup == 0;
+  int smem = 0, ctas = 0, group_smem = 0, group_ctas = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !ready(1, smem, ctas) ||
+      (grouped && !ready(biattn4::kGroup, group_smem, group_ctas))) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -715,8 +819,11 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
   h->k_scale = k_scale;
   h->v_scale = v_scale;
   h->device = dev;
-  h->max_ctas = per_sm * sms;
+  h->max_ctas = ctas;
   h->smem = smem;
+  h->sms = sms;
+  h->group_ctas = group_ctas;
+  h->group_smem = group_smem;
   if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
     cudaGetLastError();
@@ -809,8 +916,12 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
     p.o = static_cast<uint16_t*>(o) + t0 * h->Hq * h->D;
     p.q_seq = q_seq + t0;
     p.q_pos = q_pos + t0;
-    const int64_t chains = std::min<int64_t>(int64_t(p.T) * w.splits, std::max(1, h->max_ctas / h->Hkv));
-    if (const int rc = bifp4::launch(biattn4::attn_of(h->D), unsigned(chains * h->Hkv), biattn4::kThreads, size_t(h->smem), st, &p))
+    const int64_t units = int64_t(p.T) * w.splits;
+    // (us, a block a head / four: 8 x 4096, 512 heads' units, 17.9 / 17.5; 1 x 16384, 256 units, 13.8 / 15.7; 1 x 700 8.9 / 14.4)
+    const int HB = h->group_ctas && units * h->Hkv >= 3 * h->sms ? biattn4::kGroup : 1, across = h->Hkv / HB;
+    const int64_t chains = std::min<int64_t>(units, std::max(1, (HB == 1 ? h->max_ctas : h->group_ctas) / across));
+    if (const int rc = bifp4::launch(biattn4::attn_of(h->D, h->G, HB), unsigned(chains * across), biattn4::kThreads * HB,
+                                     size_t(HB == 1 ? h->smem : h->group_smem), st, &p))
       return rc;
     if (w.splits > 1)
       if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(int64_t(p.T) * h->Hq), 32 * biattn4::kMergeWarps, 0,

@@ -271,6 +271,29 @@ def test_a_tokens_bits_do_not_depend_on_the_call(Hq, Hkv, D, page):
     assert torch.equal(bg.BiAttention4(Hq, Hkv, D, other).run(q, seq, pos, *moved, t2, 2599), whole)
 
 
+@pytest.mark.parametrize("Hq,Hkv,page,split", [(32, 8, 16, 0), (8, 8, 12, 0), (64, 8, 16, 128), (48, 12, 64, 0), (32, 16, 1, 256)])
+def test_large_calls_have_the_bits_of_small_ones(Hq, Hkv, page, split):
+    """Batches whose blocks take four KV heads: ragged contexts, empty places, a token that cannot be served."""
+    D = 128
+    lengths = [1 + (37 * i * i) % 1500 for i in range(68)] + [0, 1501]
+    q, seq, pos, four, table = case(Hq, Hkv, D, page, lengths, 3)
+    att = bg.BiAttention4(Hq, Hkv, D, page, split_size=split)
+    whole = att.run(q, seq, pos, *four, table, 1500)
+    assert att.device_error() == bg.BI_GEMM_OK
+    for t in (0, 1, 5, 13, 31, 40, 66, 67, 68, 69):
+        one = att.run(q[t:t + 1], seq[t:t + 1], pos[t:t + 1], *four, table, max(lengths[t] - 1, 0))
+        assert torch.equal(one[0], whole[t]), t
+    some = torch.tensor([1, 40, 69], device="cuda")
+    want, a, e, total = attention64(q[some], seq[some], pos[some], four, table, page, att.scale, 1.0, 1.0)
+    assert ((whole[some].double() - want).abs() <= tolerance(want, a, e, total, D)).all()
+    seq2, pos2 = seq.clone(), pos.clone()
+    seq2[7], pos2[11] = 1000, 1501
+    o = att.run(q, seq2, pos2, *four, table, 1500)
+    assert att.device_error() == bg.BI_GEMM_ERR_INVALID_ARG
+    served = torch.tensor([t for t in range(70) if t not in (7, 11)], device="cuda")
+    assert torch.equal(o[served], whole[served])
+
+
 def test_many_tokens_of_few_requests():
     """More tokens than one launch serves, several of one request at consecutive positions, empty places between."""
     Hq, Hkv, D, page = 8, 2, 64, 16
