@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(256) expand_kernel(const ExpandParams p) {
     const int64_t i = first + u * 256;
     at[u] = -1;
     if (i < p.pieces) {
-      const int64_t n = i / p.per_page, r = i - n * p.per_page;
+      // (a page has no more pieces than the call)
+      const int64_t n = p.pieces >> 32 ? i / p.per_page : int64_t(uint32_t(i) / uint32_t(p.per_page)), r = i - n * p.per_page;
       const int64_t page = p.pages[n];
       if (page >= 0 && page < p.num_pages) {
         at[u] = page * p.per_page + r;
