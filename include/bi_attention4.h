@@ -57,7 +57,7 @@ typedef struct {
   int32_t num_q_heads, num_kv_heads, head_dim, page_size;
   int32_t split_size;       /* positions per split (fixed for the handle)                      */
   int32_t threads;          /* threads per block                                               */
-  int32_t max_ctas;         /* resident blocks                                                 */
+  int32_t max_ctas;         /* resident blocks of one KV head                                  */
   int32_t tokens_per_launch; /* calls of more tokens are served as several                      */
 } bi_attention4_config;
 

@@ -1,19 +1,36 @@
 // bi_attention4.cu — batch-invariant decode attention over a paged KV cache in 4 bits, and the expansion of its
 // pages, for sm_103a.  Implements include/bi_attention4.h.
 //
-// A unit is (token, split, KV head); a block of four warps runs it.  Warp w takes the 32-position steps w, w + 4,
+//   o_t = v_scale * sum_j w_j V_j / sum_j w_j,  w_j = 2^(c q_t . K_j - m),  c = scale k_scale log2(e)
+//
+// over the positions j of a token's request up to its own, K_j and V_j codes times block scales.
+//
+// A unit is (token, split, KV head); four warps run it.  Warp w takes the 32-position steps w, w + 4,
 // ... of the split through a ring of its own (cp.async, no barrier with the other warps), keeps a running maximum
 // reference, sum and the weighted values of its positions, and the four are merged in order at the unit's end.
 //
-// Per step, with g = lane / 4 and t = lane % 4 (mma.sync m16n8k16, f16 in, fp32 accumulate; the G <= 8 query
-// heads of the KV head on the columns):
+// Per step, with g = lane / 4 and t = lane % 4 (mma.sync m16n8k16, f16 in, fp32 accumulate; the query heads of
+// the KV head on the columns):
 //   scores  S^T = K Q^T: 16 positions on the rows.  The order of the products' dimensions is free as long as both
 //           operands agree, so lane t takes a quarter of a row, whole 16-byte chunks: eight codes become four f16
 //           pairs by cvt, times their block's scale (exact: 2 + 4 significant bits).
 //   weights P = 2^(s - m + 7) in fp32, rounded to f16 and transposed in registers (movmatrix).
-//   values  O^T += V^T P^T: 16 dimensions on the rows, 16 positions deep.  Lane g owns D / 8 consecutive
-//           dimensions, lane t the positions 2t, 2t + 1, 2t + 8, 2t + 9 of each sixteen: the codes of two
-//           positions are interleaved before cvt, so that a pair of f16 is one dimension at two positions.
+//   values  O^T += V^T P^T.  A code pair that cvt makes is two dimensions at one position, and the MMA sums over the pair.
+//           G <= 4: a head has two columns, and a weight stands in one half of its pair and zero in the other, so that one
+//           column gets the even dimensions and the other the odd ones (32 dimensions on the 16 rows, 8 positions deep).
+//           G = 8: the codes of two positions are interleaved before cvt, a pair is one dimension at two positions (16
+//           dimensions, 16 positions deep).  Lane g owns D / 8 consecutive dimensions either way.
+//
+// Tensor cores of the fifth generation would need codes and scales of the query too, of which eight bits would take four
+// products, and a value's block scales lie along the dimensions where the MMA's lie along the sum.
+//
+// Bound (256 contexts of 1000 to 8192, 32/8 heads of 128, 279 us, 4.6 TB/s, 0.68 of the bytes' time): the loads alone
+// take 250 us, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head: 240), the arithmetic
+// alone 230 at 270 instructions a sixteen of positions and head.  One token (700 positions: 8.8 us): the latencies of a
+// launch, a chain of steps and the merge's launch.
+// Tried: a loading warp for eight computing ones, a warp a head (largest call 355 when this form took 391, but 96
+// registers, and one token's 700 positions 18.6 us instead of 9.3); three blocks an SM with rings of three steps (no
+// change); splits of 256 positions (433 against 391, one token's 32768 21.4 against 18.5) and 1024 (379, 21.6).
 #include <cuda_runtime.h>
 
 #include <algorithm>

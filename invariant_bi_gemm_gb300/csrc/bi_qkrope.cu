@@ -192,7 +192,9 @@ struct Lane {
   }
 
   // Head h of a token for a cache in 4 bits: queries as in `finish`; keys, rounded to bf16 as they are there, and
-  // values as E2M1 codes with a scale per sixteen, two lanes.
+  // values as E2M1 codes with a scale per sixteen, two lanes.  Bound by instructions (ALUs busy for half the time): a
+  // lane's eight neighbours come from two other lanes by shuffles, and a block's scale wants a division.  8192 tokens of 32/8
+  // heads of 128, not normalised: 43.6 us, the bf16 cache 36.6 (with norms 53.5 and 41.4); 64 tokens 3.3 and 2.7.
   __device__ __forceinline__ void finish4(const Params& p, int h, int64_t t, int64_t slot, bool store, uint2 a,
                                           uint2 b) const {
     if (h < p.Hq) {
