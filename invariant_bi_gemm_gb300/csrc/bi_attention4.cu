@@ -25,7 +25,7 @@
 // products, and a value's block scales lie along the dimensions where the MMA's lie along the sum.
 //
 // Bound (256 contexts of 1000 to 8192, 32/8 heads of 128, 279 us, 4.6 TB/s, 0.68 of the bytes' time): the loads alone
-// take 250 us, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head: 240), the arithmetic
+// take 270 us, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head: 240), the arithmetic
 // alone 230 at 270 instructions a sixteen of positions and head.  One token (700 positions: 8.8 us): the latencies of a
 // launch, a chain of steps and the merge's launch.
 // Tried: a loading warp for eight computing ones, a warp a head (largest call 355 when this form took 391, but 96
