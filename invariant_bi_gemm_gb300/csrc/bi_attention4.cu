@@ -31,6 +31,9 @@
 // Tried: a loading warp for eight computing ones, a warp a head (largest call 355 when this form took 391, but 96
 // registers, and one token's 700 positions 18.6 us instead of 9.3); three blocks an SM with rings of three steps (no
 // change); splits of 256 positions (433 against 391, one token's 32768 21.4 against 18.5) and 1024 (379, 21.6).
+// For the blocks of four heads (285): one loading warp and rings that the heads share 421, four loading warps 333 (a stage
+// waits for the slowest of four heads); pairs of such blocks with a cluster barrier a unit 325.  The last block to arrive
+// merging a token's splits, instead of a second kernel: nothing for one token, 343 for the largest call (registers).
 #include <cuda_runtime.h>
 
 #include <algorithm>
