@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
   const uint8_t* kc = p.kc + ch * 16;
   const uint8_t* vc = p.vc + ch * 16;
   const uint32_t to_k = uint32_t(row * C::CODES + ch * 16), to_v = uint32_t(C::OFF_V + row * C::VROW + ch * 16);
-  Unit L;                                                // unit of the next load
+  Unit L = {};                                           // unit of the next load
   int32_t lpos = 0;                                      // its position
   int32_t lpage = 0, lrow = 0;                           // this lane's page there, fetched ahead, and row of the page
   int lslot = 0;
