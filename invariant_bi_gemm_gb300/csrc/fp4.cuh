@@ -70,7 +70,7 @@ struct Scale {
   uint32_t byte;
   float unit, inv;
   bool zero;          // every code is 0
-  bool wide;          // above the largest scale: a quotient may be out of the range that in_units corrects
+  bool wide;          // above the largest scale: a quotient may be far above the codes'
 };
 // q = x / d for a d whose reciprocal r is known to an ulp: the product with r, corrected by its remainder (exact).  What
 // is representable comes out exact, so that ties are seen as such.
@@ -107,8 +107,6 @@ __device__ __forceinline__ void in_units(uint32_t w, const Scale& s, float& lo, 
   const uint32_t a = w << 16, b = w & 0xFFFF0000u;
   if constexpr (!kNv) {
     lo = __fmul_rn(__uint_as_float(a), s.inv), hi = __fmul_rn(__uint_as_float(b), s.inv);
-  } else if (s.wide) {                                // (out of the range that `divided` corrects)
-    lo = __fdiv_rn(__uint_as_float(a), s.unit), hi = __fdiv_rn(__uint_as_float(b), s.unit);
   } else {
     // `divided`, both at a time; a zero keeps its sign
     uint64_t x, r, d, q, e;
@@ -146,11 +144,16 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t* w, const Scale& s)
     return r;
   }
   if (s.zero) return 0u;
+  uint32_t x[4] = {w[0], w[1], w[2], w[3]};
+  if (kNv && s.wide) {
+    // sizes from 8 units on become 8 units, a 6 all the same: quotients that `divided` corrects
+    const uint32_t most = __float_as_uint(__fmul_rn(8.0f, s.unit)) >> 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (x[i] & 0x80008000u) | __vminu2(x[i] & 0x7FFF7FFFu, most | most << 16);
+  }
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    in_units<kNv>(w[i], s, v[2 * i], v[2 * i + 1]);
-  }
+  for (int i = 0; i < 4; ++i) in_units<kNv>(x[i], s, v[2 * i], v[2 * i + 1]);
   return codes8(v);
 }
 

@@ -83,6 +83,25 @@ def test_strided_rows_and_bytes_of_rows_that_are_not_there(kind):
     assert (ref.from_tiles(host(scales), 128)[M:] == 0xAB).all()
 
 
+@pytest.mark.parametrize("g", [1.0, 0.37, 2.0 ** 64, 2.0 ** -64, 1.7 * 2.0 ** -60])
+@pytest.mark.parametrize("top", [3.3e38, 3000.0])
+def test_every_bf16_value_of_a_block_beyond_the_largest_scale(g, top):
+    """Each finite pattern of either sign in blocks whose largest element asks for a scale above 448 (top: as it is, or
+    3000 g, just above 448 * 6 g)."""
+    big = np.float32(min(top * g, 3.3e38) if top < 1e30 else top)
+    v = ref.bf16_values(np.arange(65536, dtype=np.uint32))
+    v = v[np.isfinite(v) & (np.abs(v) <= big)]
+    v = np.concatenate([v, np.zeros(-len(v) % 15, np.float32)]).reshape(-1, 15)
+    x = host(bf16(np.concatenate([np.full((len(v), 1), big, np.float32), v], 1)).float())
+    x = np.pad(x.reshape(-1), (0, -x.size % 1024)).reshape(-1, 1024)
+    codes, scales = bg.BiQuant4(1024, "nvfp4", g).run(bf16(x))
+    want, byte = ref.quantise(x, "nvfp4", g)
+    got_s = ref.from_tiles(host(scales), len(x))
+    assert np.array_equal(got_s, byte) and (got_s.reshape(-1)[:len(v)] == 0x7E).all()
+    got = ref.unpack(host(codes))
+    assert np.array_equal(got, want), np.argwhere(got != want)[:5]
+
+
 @pytest.mark.parametrize("kind,g", [("mxfp4", 1.0), ("nvfp4", 0.5), ("nvfp4", 0.37)])
 def test_expand_gives_the_values(kind, g):
     r = np.random.default_rng(5)
