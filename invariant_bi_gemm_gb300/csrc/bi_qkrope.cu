@@ -235,7 +235,7 @@ struct Lane {
     word |= __shfl_xor_sync(mask, word, 4);
     if (store) {
       const int64_t row = slot * p.Hkv + (h - p.Hq - (key ? 0 : p.Hkv));
-      *reinterpret_cast<uint32_t*>((key ? p.kc4 : p.vc4) + row * (D / 2) + 4 * l) = bifp4::quantise8<true>(w, s);
+      *reinterpret_cast<uint32_t*>((key ? p.kc4 : p.vc4) + row * (D / 2) + 4 * l) = bifp4::quantise8<true, false>(w, s);
       if ((l & 7) == 0) *reinterpret_cast<uint32_t*>((key ? p.ks4 : p.vs4) + row * (D / 16) + l / 2) = word;
     }
   }
