@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
 // in flight: 52 us for 8192 tokens of 32/8 heads of 128, now 42.  With a larger ring and three blocks per SM
 // it took 43.5, with five, and registers spilled, 47.)
 template <int D, bool kInterleaved, bool kFour>
-__global__ void __launch_bounds__(kThreads + 32, 4) qkrope_ring_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads + 32, kFour ? 3 : 4) qkrope_ring_kernel(const Params p) {
   constexpr int LANES = D / 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxRing];
