@@ -57,7 +57,7 @@ typedef struct {
   int32_t ring_tokens;        /* the form for many tokens: tokens on their way per block (0:
                                  rows too long for it), and its resident blocks              */
   int32_t ring_ctas;
-  int32_t ring_from;          /* the T from which it runs                                     */
+  int32_t ring_from;          /* the T from which it runs (bi_qkrope_run4's may be lower)     */
 } bi_qkrope_config;
 
 /* Create a handle.  Requirements: head_dim 64 or 128; rot_dim a multiple of 16, 16..head_dim;

@@ -41,7 +41,8 @@ constexpr int kThreads = 256;
 constexpr int kHeads = 4;                // heads a lane group holds at a time
 constexpr int kMaxRing = 16;             // stages of the ring
 constexpr int kRingBytes = 54 * 1024;    // shared memory of a block's ring at most: four blocks per SM
-constexpr int kRingRows = 40 * 1024;     // bytes of rows that a block of it has to have
+constexpr int kRingRows = 40 * 1024;     // bytes of rows that a block of it has to have,
+constexpr int kRingRows4 = 24 * 1024;    // and where keys and values are quantised
 constexpr uint32_t kErrInput = 1u;       // q_seq, q_pos or the page table's extent
 constexpr uint32_t kErrPage = 2u;        // page outside [0, num_pages)
 
@@ -194,7 +195,8 @@ struct Lane {
   // Head h of a token for a cache in 4 bits: queries as in `finish`; keys, rounded to bf16 as they are there, and
   // values as E2M1 codes with a scale per sixteen, two lanes.  Bound by instructions (ALUs busy for half the time): a
   // lane's eight neighbours come from two other lanes by shuffles, and a block's scale wants a division.  8192 tokens of 32/8
-  // heads of 128, not normalised: 43.6 us, the bf16 cache 36.6 (with norms 53.5 and 41.4); 64 tokens 3.3 and 2.7.
+  // heads of 128, not normalised: 37.9 us, the bf16 cache 36.6 (with norms 49.9 and 41.4); 64 tokens 2.9 and 2.7.  Three
+  // blocks an SM: with four, and a few registers spilled, 43.8 and 3.3.
   __device__ __forceinline__ void finish4(const Params& p, int h, int64_t t, int64_t slot, bool store, uint2 a,
                                           uint2 b) const {
     if (h < p.Hq) {
@@ -235,7 +237,7 @@ struct Lane {
     word |= __shfl_xor_sync(mask, word, 4);
     if (store) {
       const int64_t row = slot * p.Hkv + (h - p.Hq - (key ? 0 : p.Hkv));
-      *reinterpret_cast<uint32_t*>((key ? p.kc4 : p.vc4) + row * (D / 2) + 4 * l) = bifp4::quantise8<true, false>(w, s);
+      *reinterpret_cast<uint32_t*>((key ? p.kc4 : p.vc4) + row * (D / 2) + 4 * l) = bifp4::quantise8<true>(w, s);
       if ((l & 7) == 0) *reinterpret_cast<uint32_t*>((key ? p.ks4 : p.vs4) + row * (D / 16) + l / 2) = word;
     }
   }
@@ -274,7 +276,7 @@ __device__ __forceinline__ int64_t slot_of(const Params& p, int32_t b, int32_t p
 
 // A block per token or few: the form for few tokens.
 template <int D, bool kInterleaved, bool kFour>
-__global__ void __launch_bounds__(kThreads, 4) qkrope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kFour ? 3 : 4) qkrope_kernel(const Params p) {
   constexpr int LANES = D / 8;
   // Programmatic dependent launch: the block may start while the previous kernel finishes and
   // waits for it (and its memory) before its first global access.
@@ -442,7 +444,7 @@ struct bi_qkrope {
   int ring_ctas4 = 0;               // resident blocks of that form for a cache in 4 bits
   int ring = 0, ring_ctas = 0;      // stages and resident blocks of the form for many tokens (0: none),
   int team_log2 = 0;                // its warps per token
-  int ring_from = 0;                // and the tokens from which it runs
+  int ring_from = 0, ring_from4 = 0;   // and the tokens from which it runs
   size_t ring_smem = 0;
   uint32_t* d_status = nullptr;
 };
@@ -508,6 +510,7 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
     h->ring_ctas4 = per_sm4 * sms;
     const int64_t row = int64_t(heads) * h->D * 2;
     h->ring_from = int((int64_t(biqkr::kRingRows) * h->ring_ctas + row - 1) / row);
+    h->ring_from4 = int((int64_t(biqkr::kRingRows4) * h->ring_ctas4 + row - 1) / row);
   }
   if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
@@ -601,8 +604,11 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   // The ring from 40 KB of rows per resident block on, where its start is paid for (us, ring against a
   // block per token or few): 32/8 heads of 128 (12 KB a token), 1216 tokens 9.8 against 9.4, 2432 16.5
   // against 17.7, 8192 42.0 against 52.3; 16/8 of 128, 2432 11.3 against 11.2, 4096 16.9 against 17.8;
-  // 16/2 of 64, 8192 15.2 against 14.9, 12000 19.6 against 19.9.
-  const bool ring = h->ring_from > 0 && T >= h->ring_from;
+  // 16/2 of 64, 8192 15.2 against 14.9, 12000 19.6 against 19.9.  A cache in 4 bits, from 24 KB: 32/8 of 128, 700 tokens
+  // 6.2 against 5.6, 1000 8.0 against 8.6, 2000 13.0 against 15.6; 16/8 of 128, 1500 8.3 against 8.0, 2000 10.7 against 11.6;
+  // 16/2 of 64, 4000 8.3 against 7.9, 6000 11.1 against 11.9.
+  const int from = four ? h->ring_from4 : h->ring_from;
+  const bool ring = from > 0 && T >= from;
   p.ring = h->ring;
   p.team_log2 = h->team_log2;
   p.stall = stall;

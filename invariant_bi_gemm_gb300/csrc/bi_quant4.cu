@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
     uint32_t most = most_of(w[u], 8);
     if (!kNv) most = max(most, __shfl_xor_sync(mask, most, 1));
     const Scale s = kNv ? nvfp4_scale(most, p.g, p.six_g, p.inv_six_g) : mxfp4_scale(most);
-    const uint2 codes = make_uint2(quantise8<kNv, true>(w[u], s), quantise8<kNv, true>(w[u] + 4, s));
+    const uint2 codes = make_uint2(quantise8<kNv>(w[u], s), quantise8<kNv>(w[u] + 4, s));
     *reinterpret_cast<uint2*>(p.codes + (row[u] * p.per_row + piece[u]) * 8) = codes;
     // four scales to one lane
     if constexpr (kNv) {

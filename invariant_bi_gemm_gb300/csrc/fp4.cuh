@@ -101,14 +101,12 @@ __device__ __forceinline__ Scale mxfp4_scale(uint32_t amax_bits) {
   if (s.zero) s.byte = kNanE8M0;
   return s;
 }
-// The places of two bf16 values (a word) on the codes' grid: x / unit.  kDivide: of a wide block too.
-template <bool kNv, bool kDivide>
+// The places of two bf16 values (a word) on the codes' grid: x / unit.
+template <bool kNv>
 __device__ __forceinline__ void in_units(uint32_t w, const Scale& s, float& lo, float& hi) {
   const uint32_t a = w << 16, b = w & 0xFFFF0000u;
   if constexpr (!kNv) {
     lo = __fmul_rn(__uint_as_float(a), s.inv), hi = __fmul_rn(__uint_as_float(b), s.inv);
-  } else if (kDivide && s.wide) {
-    lo = __fdiv_rn(__uint_as_float(a), s.unit), hi = __fdiv_rn(__uint_as_float(b), s.unit);
   } else {
     // `divided`, both at a time; a zero keeps its sign
     uint64_t x, r, d, q, e;
@@ -133,9 +131,8 @@ __device__ __forceinline__ uint32_t most_of(const uint32_t* w, int n) {
 }
 
 // Eight bf16 values (four words) -> their codes.  A wide block's quotients are out of the range that `divided` corrects:
-// its values are clamped first (nvfp4, 14336 x 4096: 30.1 us, with a division in its place 32.4), or, where registers are
-// short, divided (the append of 8192 tokens and its expansion: 53.9 us, with the clamp, spilled, 59.8).
-template <bool kNv, bool kClamp>
+// its values are clamped first (nvfp4, 14336 x 4096: 30.1 us, with a division in its place 32.4).
+template <bool kNv>
 __device__ __forceinline__ uint32_t quantise8(const uint32_t* w, const Scale& s) {
   if (s.zero && kNv) {
     // zeros keep their sign; a block that is not finite has codes of 0
@@ -149,7 +146,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t* w, const Scale& s)
   }
   if (s.zero) return 0u;
   uint32_t x[4] = {w[0], w[1], w[2], w[3]};
-  if (kNv && kClamp && s.wide) {
+  if (kNv && s.wide) {
     // sizes from 8 units on become 8 units, a 6 all the same
     const uint32_t most = __float_as_uint(__fmul_rn(8.0f, s.unit)) >> 16;
 #pragma unroll
@@ -157,7 +154,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t* w, const Scale& s)
   }
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) in_units<kNv, !kClamp>(x[i], s, v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) in_units<kNv>(x[i], s, v[2 * i], v[2 * i + 1]);
   return codes8(v);
 }
 
