@@ -2,8 +2,8 @@
 // quantisation of include/bi_fp4.h.
 //
 // Bound: HBM bandwidth (2 bytes an element read, 0.53 or 0.56 written) and, close behind, the ALUs, which are busy for
-// 60 % of the time: 14336 x 4096 take 25 us with mxfp4 (5.9 TB/s), 32 with nvfp4 (whose scales want a division each),
-// and 24 back (6.1 TB/s).  A thread has sixteen consecutive
+// 60 % of the time: 14336 x 4096 take 25 us with mxfp4 (5.9 TB/s), 30 with nvfp4 (whose scales want a division each, and
+// whose elements another), and 24 back (6.1 TB/s).  Two pieces a thread: one 27.5 and 34, four 26 and 40.  A thread has sixteen consecutive
 // elements: a block of BI_NVFP4, half a block of BI_MXFP4 (the two halves meet in one shuffle).  K is a multiple of
 // 128, so the lanes that share a block, or the four scales that lie side by side in a tile and leave as one
 // 32-bit store, are always of one row, and threads run over the matrix without regard to where rows end.
