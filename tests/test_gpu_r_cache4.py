@@ -316,6 +316,40 @@ def test_many_tokens_of_few_requests():
     assert ((o[some].double() - want).abs() <= tolerance(want, a, e, total, D)).all()
 
 
+def test_many_tokens_in_blocks_of_four_heads():
+    """Three launches of such blocks, a captured call of them, and two handles at once on two streams."""
+    Hq, Hkv, D, page, T = 16, 8, 128, 16, 1100
+    table, pages = table_of([-(-1400 // page)] * 3)
+    four = random_cache(pages, page, Hkv, D, 4)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((T, Hq, D), generator=g, device="cuda").to(torch.bfloat16)
+    seq = (torch.arange(T, device="cuda") % 3).to(torch.int32)
+    pos = (torch.arange(T, device="cuda") * 7 % 1399).to(torch.int32)
+    pos[::11], seq[::11] = -1, 77
+    att, other = (bg.BiAttention4(Hq, Hkv, D, page) for _ in range(2))
+    o = att.run(q, seq, pos, *four, table, 1399)
+    assert att.device_error() == bg.BI_GEMM_OK
+    assert (o[::11] == 0).all()
+    for t in (1, 300, 511, 512, 513, 1023, 1024, 1025, 1099):
+        assert torch.equal(att.run(q[t:t + 1], seq[t:t + 1], pos[t:t + 1], *four, table, 1399)[0], o[t]), t
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(o)
+    with torch.cuda.graph(graph):
+        att.run(q, seq, pos, *four, table, 1399, o=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, o)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for k, h in enumerate((att, other)):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(h.run(q, seq, pos, *four, table, 1399))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, o) for xs in got for x in xs)
+
+
 def test_what_lies_behind_a_position_is_not_seen():
     """NaN scales in the same page behind the position, and in other pages."""
     q, seq, pos, four, table = case(32, 8, 128, 16, [100, 513, 7])
