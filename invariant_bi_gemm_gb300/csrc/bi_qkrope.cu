@@ -41,6 +41,7 @@ constexpr int kThreads = 256;
 constexpr int kHeads = 4;                // heads a lane group holds at a time
 constexpr int kMaxRing = 16;             // stages of the ring
 constexpr int kRingBytes = 54 * 1024;    // shared memory of a block's ring at most: four blocks per SM
+constexpr int kRingBytes4 = 72 * 1024;   // three, for a cache in 4 bits
 constexpr int kRingRows = 40 * 1024;     // bytes of rows that a block of it has to have,
 constexpr int kRingRows4 = 24 * 1024;    // and where keys and values are quantised
 constexpr uint32_t kErrInput = 1u;       // q_seq, q_pos or the page table's extent
@@ -441,11 +442,11 @@ struct bi_qkrope {
   int Hq = 0, Hkv = 0, D = 0, page_size = 0, rot = 0, interleaved = 0;
   float eps = 0.0f;
   int device = 0, groups_log2 = 0, per_block = 0;
-  int ring_ctas4 = 0;               // resident blocks of that form for a cache in 4 bits
   int ring = 0, ring_ctas = 0;      // stages and resident blocks of the form for many tokens (0: none),
   int team_log2 = 0;                // its warps per token
-  int ring_from = 0, ring_from4 = 0;   // and the tokens from which it runs
-  size_t ring_smem = 0;
+  int ring_from = 0;                // and the tokens from which it runs
+  int ring4 = 0, ring_ctas4 = 0, ring_from4 = 0;   // the same for a cache in 4 bits
+  size_t stage = 0;                 // bytes of a stage
   uint32_t* d_status = nullptr;
 };
 
@@ -486,32 +487,33 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
   const int ring = int(std::min<size_t>(biqkr::kMaxRing, biqkr::kRingBytes / stage));
   // warps per token: the power of two that leaves a lane group kHeads heads or fewer
   while (h->team_log2 < 3 && ((32 / (h->D / 8) * biqkr::kHeads) << h->team_log2) < heads) ++h->team_log2;
-  if (ring >= 3) {
+  // (three blocks an SM leave a cache in 4 bits more room: taken where a ring would not fit else.  64/8 heads of 128, us:
+  // 1000 tokens 12.9 without, 11.3 with one, 9000 85.9 and 63.1; 32/8, where both fit, 8192 38.4 with the larger, 37.9)
+  const int ring4 = ring >= 3 ? ring : int(std::min<size_t>(biqkr::kMaxRing, biqkr::kRingBytes4 / stage));
+  auto ready = [&](bool four, int stages, int room, int rows, int& ctas, int& from) {
+    if (stages < 3) return true;
+    const auto fn = biqkr::kernel_of(h->D, interleaved != 0, true, four);
     int sms = 0, per_sm = 0;
-    h->ring = ring;
-    h->ring_smem = ring * stage;
-    const auto fn = biqkr::kernel_of(h->D, interleaved != 0, true, false);
-    const auto fn4 = biqkr::kernel_of(h->D, interleaved != 0, true, true);
-    int per_sm4 = 0;
     // (the attribute is the kernel's, shared by every handle: the most any of them needs)
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, biqkr::kRingBytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biqkr::kThreads + 32, h->ring_smem) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(fn4, cudaFuncAttributeMaxDynamicSharedMemorySize, biqkr::kRingBytes) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm4, fn4, biqkr::kThreads + 32, h->ring_smem) !=
-            cudaSuccess ||
-        per_sm < 1 || per_sm4 < 1) {
-      cudaGetLastError();
-      delete h;
-      return BI_GEMM_ERR_CUDA;
-    }
-    h->ring_ctas = per_sm * sms;
-    h->ring_ctas4 = per_sm4 * sms;
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, room) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biqkr::kThreads + 32, stages * stage) != cudaSuccess ||
+        per_sm < 1)
+      return false;
+    ctas = per_sm * sms;
     const int64_t row = int64_t(heads) * h->D * 2;
-    h->ring_from = int((int64_t(biqkr::kRingRows) * h->ring_ctas + row - 1) / row);
-    h->ring_from4 = int((int64_t(biqkr::kRingRows4) * h->ring_ctas4 + row - 1) / row);
+    from = int((int64_t(rows) * ctas + row - 1) / row);
+    return true;
+  };
+  if (!ready(false, ring, biqkr::kRingBytes, biqkr::kRingRows, h->ring_ctas, h->ring_from) ||
+      !ready(true, ring4, biqkr::kRingBytes4, biqkr::kRingRows4, h->ring_ctas4, h->ring_from4)) {
+    cudaGetLastError();
+    delete h;
+    return BI_GEMM_ERR_CUDA;
   }
+  h->ring = ring >= 3 ? ring : 0;
+  h->ring4 = ring4;
+  h->stage = stage;
   if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
     cudaGetLastError();
@@ -609,13 +611,13 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   // 16/2 of 64, 4000 8.3 against 7.9, 6000 11.1 against 11.9.
   const int from = four ? h->ring_from4 : h->ring_from;
   const bool ring = from > 0 && T >= from;
-  p.ring = h->ring;
+  p.ring = four ? h->ring4 : h->ring;
   p.team_log2 = h->team_log2;
   p.stall = stall;
   p.timeout_ns = timeout_ns;
   cfg.gridDim = dim3(unsigned(ring ? (four ? h->ring_ctas4 : h->ring_ctas) : (T + h->per_block - 1) / h->per_block));
   cfg.blockDim = dim3(biqkr::kThreads + (ring ? 32 : 0));
-  cfg.dynamicSmemBytes = ring ? h->ring_smem : 0;
+  cfg.dynamicSmemBytes = ring ? size_t(p.ring) * h->stage : 0;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -51,6 +51,7 @@ def i32(a):
 # ------------------------------------------------------------------ append
 
 @pytest.mark.parametrize("Hq,Hkv,D,page,rot,inter,norm,T", [
+    (64, 8, 128, 16, 128, False, True, 800), (64, 8, 128, 16, 64, True, False, 1300),
     (32, 8, 128, 16, 128, False, True, 1), (32, 8, 128, 16, 128, False, False, 70), (32, 8, 128, 12, 128, True, True, 33),
     (16, 2, 64, 5, 32, False, True, 77), (16, 2, 64, 16, 64, True, False, 9), (4, 4, 128, 8, 64, False, True, 40),
     (8, 1, 128, 32, 16, False, True, 21), (8, 8, 64, 64, 48, False, False, 130), (4, 4, 128, 7, 96, False, True, 50),
