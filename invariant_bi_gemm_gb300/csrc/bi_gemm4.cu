@@ -727,7 +727,8 @@ namespace {
 // nvfp4 (us; this form in tiles of 128 x 128 against pairs of 256 x 256): 256 x 4096 x 4096 (M, K, N) 8.8 against 10.2, 512 x
 // 4096 x 4096 8.3 against 9.8, 777 x 2176 x 1000 6.7 against 7.7, 4096 x 1024 x 256 5.2 against 6.2, and with more tiles than
 // SMs 256 x 4096 x 14336 15.6 against 12.1: a call takes it where its tiles run all at once.  Fewer columns of y a CTA
-// where that leaves half the SMs without work: 300 x 4096 x 1024 8.2 with 128, 7.7 with 32; 128 x 4096 x 4096 8.7 and 7.9; and
+// where that leaves half the SMs without work: 300 x 4096 x 1024 8.2 with 128, 7.7 with 32; 128 x 4096 x 4096 8.7 and 7.9; 777 x 2176 x 1000 6.7
+// with 128, 6.2 with 64; and
 // two CTAs an SM for many columns and a handful of rows: 1 x 4096 x 28672 14.0 with one, 13.1 with two.
 bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, int& smem) {
   f.cols = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
@@ -735,7 +736,7 @@ bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, i
   auto units = [&]() { return (h->N + f.rows - 1) / f.rows * m_tiles; };
   f.rows = 128;
   if (M > big4::kFewCols && units() > h->sms) return false;
-  while (f.rows > 32 && units() < h->sms / (M > big4::kFewCols ? 3 : 2)) f.rows /= 2;
+  while (f.rows > 32 && units() < h->sms / 2) f.rows /= 2;
   per_sm = units() > h->sms && f.cols <= 32 ? 2 : 1;
   smem = h->K > 4 * big4::kStageK ? big4::few_layout(f, h->nv, h->f32, per_sm, 4, 3) : 0;
   if (!smem) smem = big4::few_layout(f, h->nv, h->f32, per_sm, 2, 2);
