@@ -654,6 +654,11 @@ __device__ __forceinline__ void sum_splits(const Params& p, int64_t slot0, int32
   }
 }
 
+// Blocks of a token: one for eight heads where no token of the call can have more than kSolo splits.
+__host__ __device__ constexpr uint32_t merge_blocks(int32_t Hq, int32_t max_splits) {
+  return uint32_t(max_splits <= kSolo ? (Hq + kMergeWarps - 1) / kMergeWarps : Hq);
+}
+
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p) {
   constexpr int PER = D / 32;                             // dimensions a lane
@@ -662,8 +667,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const Params p)
   const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int32_t t = int32_t(blockIdx.x / p.Hq);
-  int32_t h = int32_t(blockIdx.x - uint32_t(t) * p.Hq);
+  const uint32_t per = merge_blocks(p.Hq, p.max_splits);
+  const int32_t t = int32_t(blockIdx.x / per);
+  int32_t h = int32_t((blockIdx.x - uint32_t(t) * per) * (uint32_t(p.max_splits) <= kSolo ? kMergeWarps : 1));
   const int32_t n = splits_of(p, p.q_seq[t], p.q_pos[t], false);
   if (n <= 1) return;                                     // written by its unit, or refused
   const bool solo = n <= kSolo;
@@ -945,7 +951,7 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
                                      size_t(HB == 1 ? h->smem : h->group_smem), st, &p))
       return rc;
     if (w.splits > 1)
-      if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(int64_t(p.T) * h->Hq), 32 * biattn4::kMergeWarps, 0,
+      if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(p.T) * biattn4::merge_blocks(h->Hq, p.max_splits), 32 * biattn4::kMergeWarps, 0,
                                        st, &p))
         return rc;
   }
