@@ -24,16 +24,17 @@
 // Tensor cores of the fifth generation would need codes and scales of the query too, of which eight bits would take four
 // products, and a value's block scales lie along the dimensions where the MMA's lie along the sum.
 //
-// Bound (256 contexts of 1000 to 8192, 32/8 heads of 128, 279 us, 4.6 TB/s, 0.68 of the bytes' time): the loads alone
-// take 270 us, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head: 240), the arithmetic
-// alone 230 at 270 instructions a sixteen of positions and head.  One token (700 positions: 8.8 us): the latencies of a
-// launch, a chain of steps and the merge's launch.
+// Bound (256 contexts of 1000 to 8192, 32/8 heads of 128, 265 us, 4.9 TB/s, 0.72 of the bytes' rate): the loads alone
+// take nine tenths of it, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head a tenth less), the
+// arithmetic alone eight tenths at 270 instructions a sixteen of positions and head, the merge's launch 12 us.  One token (700
+// positions: 8.8 us): the latencies of a launch, a chain of steps and the merge's launch.
 // Tried: a loading warp for eight computing ones, a warp a head (largest call 355 when this form took 391, but 96
 // registers, and one token's 700 positions 18.6 us instead of 9.3); three blocks an SM with rings of three steps (no
 // change); splits of 256 positions (433 against 391, one token's 32768 21.4 against 18.5) and 1024 (379, 21.6).
 // For the blocks of four heads (285): one loading warp and rings that the heads share 421, four loading warps 333 (a stage
 // waits for the slowest of four heads); pairs of such blocks with a cluster barrier a unit 325.  The last block to arrive
 // merging a token's splits, instead of a second kernel: nothing for one token, 343 for the largest call (registers).
+// Splits joined in the block that runs them, the merge left with what chains cut: 1 % less.
 #include <cuda_runtime.h>
 
 #include <algorithm>
