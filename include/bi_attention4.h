@@ -72,9 +72,9 @@ int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_
  * workspace and changes no result.  T = 0 queues nothing.  The run grows the handle's workspace in stream
  * order when it needs more than before (BI_GEMM_ERR_OOM if that fails; BI_GEMM_ERR_SCRATCH_LIMIT in a call
  * being captured into a graph that needs more than an earlier call left; a graph stays valid when later
- * calls grow it), then queues the attention and, where max_pos leaves more than one split, the merge (of
- * each 512 tokens).  num_pages x page_size x num_kv_heads below 2^32 - 1, max_pos below 2^30 (else
- * BI_GEMM_ERR_UNSUPPORTED).  Asynchronous; nothing in it waits for another block. */
+ * calls grow it), then queues the attention and, where max_pos leaves more than one split and the
+ * splits' blocks do not merge among themselves, the merge (of each 512 tokens).  num_pages x page_size x num_kv_heads below 2^32 - 1, max_pos below 2^30 (else
+ * BI_GEMM_ERR_UNSUPPORTED).  Asynchronous; only the blocks of a cluster, which run together, wait for one another. */
 int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t* q_seq, const int32_t* q_pos,
                       const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
                       int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,

@@ -27,7 +27,7 @@
 // Bound (256 contexts of 1000 to 8192, 32/8 heads of 128, 265 us, 4.9 TB/s, 0.72 of the bytes' rate): the loads alone
 // take nine tenths of it, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head a tenth less), the
 // arithmetic alone eight tenths at 270 instructions a sixteen of positions and head, the merge's launch 12 us.  One token (700
-// positions: 8.8 us): the latencies of a launch, a chain of steps and the merge's launch.
+// positions: 7.9 us, 8.9 before its two splits merged in a cluster): the latencies of a launch, a lookup, a chain of steps.
 // Tried: a loading warp for eight computing ones, a warp a head (largest call 355 when this form took 391, but 96
 // registers, and one token's 700 positions 18.6 us instead of 9.3); three blocks an SM with rings of three steps (no
 // change); splits of 256 positions (433 against 391, one token's 32768 21.4 against 18.5) and 1024 (379, 21.6).
@@ -85,6 +85,7 @@ struct Params {
   int64_t max_pages, B;
   uint32_t num_pages;
   int32_t T, Hq, Hkv, G, page_size, split, max_splits, max_pos;
+  int32_t cluster;    // blocks of a (token, KV head), a split each, that merge among themselves (0: runs of units)
   uint32_t page_mul;  // pos / page_size = 4 pos * page_mul >> (32 + page_shift) for pos < 2^30
   int32_t page_shift;
   float c;            // scale * k_scale * log2(e)
@@ -157,6 +158,11 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+__device__ __forceinline__ float ld_cluster(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
 struct Unit {
   int32_t v, t, split, first, last;   // the v-th (token, split) and its positions (last < first: none)
 };
@@ -171,8 +177,9 @@ __device__ __forceinline__ int32_t splits_of(const Params& p, int32_t b, int32_t
   return bad ? 0 : pos / p.split + 1;
 }
 
-// kTwin: up to four heads, each on two of the MMA's columns.
-template <int D, bool kTwin, int HB>
+// kTwin: up to four heads, each on two of the MMA's columns.  kCluster: a block a split, the splits of a (token, KV head) in
+// a cluster that merges them.
+template <int D, bool kTwin, int HB, bool kCluster>
 __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(const Params p) {
   using C = Cfg<D, HB>;
   constexpr int HEADS = kTwin ? 1 : 2;                   // whose scores and sums a lane has
@@ -222,9 +229,19 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
   // Block (chain, kh) takes a run of consecutive (token, split) of its head, so that a token's query is prepared once
   // for its splits there; the blocks of a chain's heads read neighbouring rows at the same time.
   const uint32_t across = uint32_t(p.Hkv) / HB;          // blocks of a chain
-  const int32_t kh = int32_t(blockIdx.x % across) * HB + group, chain = int32_t(blockIdx.x / across);
+  const int32_t chain = int32_t(blockIdx.x / across);
   const int32_t chains = int32_t(gridDim.x / across);
-  const int32_t v_end = int32_t(int64_t(carry) * (chain + 1) / chains);
+  // In clusters a block has one unit, or none.
+  int32_t kh = int32_t(blockIdx.x % across) * HB + group, ct = 0, rank = 0, n_splits = 0;
+  int32_t v_end = int32_t(int64_t(carry) * (chain + 1) / chains);
+  if constexpr (kCluster) {
+    const int32_t place = int32_t(blockIdx.x) / p.cluster;
+    rank = int32_t(blockIdx.x) - place * p.cluster;
+    ct = place / p.Hkv;
+    kh = place - ct * p.Hkv;
+    n_splits = cum[ct + 1] - cum[ct];
+    v_end = cum[ct] + min(rank + 1, n_splits);
+  }
   auto locate = [&](Unit& r) {                           // t: cum[t] <= v < cum[t + 1]
     for (;;) {
       const int i = r.t + 1 + lane;
@@ -240,7 +257,7 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
     r.last = min(poss[r.t], r.first + p.split - 1);
   };
   auto start = [&](Unit& r) {
-    r.v = int32_t(int64_t(carry) * chain / chains);
+    r.v = kCluster ? cum[ct] + min(rank, n_splits) : int32_t(int64_t(carry) * chain / chains);
     r.t = 0;
     if (r.v < v_end) locate(r);
   };
@@ -596,6 +613,11 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
                                        : make_uint2(ptx::pack_bf16x2(__fmul_rn(A.x, f), __fmul_rn(A.y, f)),
                                                     ptx::pack_bf16x2(__fmul_rn(A.z, f), __fmul_rn(A.w, f)));
           *reinterpret_cast<uint2*>(p.o + (int64_t(U.t) * p.Hq + kh * p.G + head) * D + at_d) = out;
+        } else if (kCluster) {
+          // (the rings are done with)
+          float* keep = reinterpret_cast<float*>(smem);
+          *reinterpret_cast<float4*>(keep + head * D + at_d) = A;
+          if (at_d == 0) *reinterpret_cast<float2*>(keep + kHeads * D + 2 * head) = make_float2(M, Ls);
         } else {
           const int64_t at = ((int64_t(U.t) * p.Hkv + kh) * p.max_splits + U.split) * p.G + head;
           *reinterpret_cast<float4*>(p.part + at * D + at_d) = A;
@@ -606,9 +628,42 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
     }
   }
   ptx::cp_async_wait<0>();
+  if constexpr (kCluster) {
+    // The cluster's blocks have a split each: a warp a head sums them as merge_kernel would.
+    __syncwarp();
+    ptx::cluster_sync();
+    for (int hd = rank * kWarps + warp; n_splits > 1 && hd < p.G; hd += p.cluster * kWarps) {
+      constexpr int PER = D / 32;
+      const uint32_t keep = ptx::smem_u32(smem);
+      float mine = -INFINITY, sum = 0.0f;
+      if (lane < n_splits) {
+        const uint32_t at = ptx::mapa_shared(keep + uint32_t(kHeads * D + 2 * hd) * 4u, uint32_t(lane));
+        mine = ld_cluster(at), sum = ld_cluster(at + 4u);
+      }
+      float M = mine, L = 0.0f, A[PER];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+#pragma unroll
+      for (int j = 0; j < PER; ++j) A[j] = 0.0f;
+      for (int s = 0; s < n_splits; ++s) {
+        const uint32_t at = ptx::mapa_shared(keep + uint32_t(hd * D + lane * PER) * 4u, uint32_t(s));
+        const float f = ex2(__fsub_rn(__shfl_sync(0xFFFFFFFFu, mine, s), M));
+        L = __fmaf_rn(__shfl_sync(0xFFFFFFFFu, sum, s), f, L);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) A[j] = __fmaf_rn(ld_cluster(at + 4u * j), f, A[j]);
+      }
+      uint16_t* o = p.o + (int64_t(ct) * p.Hq + kh * p.G + hd) * D;
+      const float f = __fdiv_rn(p.v_scale, L);
+#pragma unroll
+      for (int j = 0; j < PER; j += 2)
+        *reinterpret_cast<uint32_t*>(o + lane * PER + j) = ptx::pack_bf16x2(__fmul_rn(A[j], f), __fmul_rn(A[j + 1], f));
+    }
+    __syncwarp();
+    ptx::cluster_sync();                                // nobody leaves while its splits are read
+  }
 }
 
-// Up to kSolo splits of a token's query head are summed in ascending order by one warp (eight heads a block: a block a
+// Up to kSolo splits of a token's query head are summed in ascending order by one warp (of a cluster's block, or here, eight heads a block: a block a
 // head took 51 us for 8192 heads of 9 splits); more of them as eight consecutive groups of ceil(n / 8) by the
 // warps of a block, ascending, the groups added in order.  n depends on the token's position alone.
 constexpr int kSolo = 16;
@@ -770,17 +825,20 @@ __global__ void __launch_bounds__(256) expand_kernel(const ExpandParams p) {
   }
 }
 
-// With HB = 1 or kGroup KV heads a block (kGroup: heads of 128).
+// With one KV head a block, in clusters or not (HB = 0, 1), or kGroup of them (heads of 128).
 template <bool kTwin>
 const void* attn_for(int D, int HB) {
-  if (D == 64) return reinterpret_cast<const void*>(&attn_kernel<64, kTwin, 1>);
-  return HB == 1 ? reinterpret_cast<const void*>(&attn_kernel<128, kTwin, 1>)
-                 : reinterpret_cast<const void*>(&attn_kernel<128, kTwin, kGroup>);
+  if (HB == 0)
+    return D == 64 ? reinterpret_cast<const void*>(&attn_kernel<64, kTwin, 1, true>)
+                   : reinterpret_cast<const void*>(&attn_kernel<128, kTwin, 1, true>);
+  if (D == 64) return reinterpret_cast<const void*>(&attn_kernel<64, kTwin, 1, false>);
+  return HB == 1 ? reinterpret_cast<const void*>(&attn_kernel<128, kTwin, 1, false>)
+                 : reinterpret_cast<const void*>(&attn_kernel<128, kTwin, kGroup, false>);
 }
 inline const void* attn_of(int D, int G, int HB) { return G <= 4 ? attn_for<true>(D, HB) : attn_for<false>(D, HB); }
 inline int smem_of(int D, int G, int HB) {
   if (D == 64) return Cfg<64, 1>::smem(G);
-  return HB == 1 ? Cfg<128, 1>::smem(G) : Cfg<128, kGroup>::smem(G);
+  return HB <= 1 ? Cfg<128, 1>::smem(G) : Cfg<128, kGroup>::smem(G);
 }
 inline const void* merge_of(int D) {
   return D == 128 ? reinterpret_cast<const void*>(&merge_kernel<128>) : reinterpret_cast<const void*>(&merge_kernel<64>);
@@ -820,7 +878,8 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
     int per_sm = 0;
     if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              biattn4::smem_of(int(head_dim), G <= 4 ? 4 : 8, HB)) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biattn4::kThreads * HB, smem) != cudaSuccess || per_sm < 1)
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, biattn4::kThreads * std::max(HB, 1), smem) != cudaSuccess ||
+        per_sm < 1)
       return false;
     ctas = per_sm * sms;
     return true;
@@ -830,9 +889,9 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
   // 4600 344 / 285, 64 of 4096 81 / 73, 128 of them at G = 8 186 / 167.  Rows of fewer or shorter heads gain nothing: 4 of 128
   // 51 / 53, 8 of 64 29 / 32.
   const bool grouped = head_dim == 128 && num_kv_heads >= 8 && num_kv_heads % biattn4::kGroup == 0;
-  int smem = 0, ctas = 0, group_smem = 0, group_ctas = 0;
+  int smem = 0, ctas = 0, group_smem = 0, group_ctas = 0, cluster_smem = 0, cluster_ctas = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !ready(1, smem, ctas) ||
-      (grouped && !ready(biattn4::kGroup, group_smem, group_ctas))) {
+      !ready(0, cluster_smem, cluster_ctas) || (grouped && !ready(biattn4::kGroup, group_smem, group_ctas))) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -949,10 +1008,17 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
     // (us, a block a head / four: 8 x 4096, 512 heads' units, 17.9 / 17.5; 1 x 16384, 256 units, 13.8 / 15.7; 1 x 700 8.9 / 14.4)
     const int HB = h->group_ctas && units * h->Hkv >= 3 * h->sms ? biattn4::kGroup : 1, across = h->Hkv / HB;
     const int64_t chains = std::min<int64_t>(units, std::max(1, (HB == 1 ? h->max_ctas : h->group_ctas) / across));
-    if (const int rc = bifp4::launch(biattn4::attn_of(h->D, h->G, HB), unsigned(chains * across), biattn4::kThreads * HB,
-                                     size_t(HB == 1 ? h->smem : h->group_smem), st, &p))
+    // Clusters of two or four splits' blocks, where they run in one round: no second kernel.  us, without / with: 1 x 700 8.9 /
+    // 7.9, 1 x 2000 9.3 / 8.3, 16 x 1000 14.1 / 11.9, 100 x 1000 at 8/1 heads 15.3 / 11.0; of eight: 1 x 4096 9.3 / 9.0, but 4 x 4096
+    // 12.6 / 13.7.
+    const int64_t S = w.splits <= 2 ? 2 : 4, blocks = int64_t(p.T) * h->Hkv * S;
+    const bool cluster = HB == 1 && w.splits > 1 && w.splits <= 4 && blocks <= h->max_ctas;
+    p.cluster = cluster ? int32_t(S) : 0;
+    if (const int rc = bifp4::launch(biattn4::attn_of(h->D, h->G, cluster ? 0 : HB), unsigned(cluster ? blocks : chains * across),
+                                     biattn4::kThreads * HB, size_t(HB == 1 ? h->smem : h->group_smem), st, &p,
+                                     unsigned(p.cluster)))
       return rc;
-    if (w.splits > 1)
+    if (w.splits > 1 && !cluster)
       if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(p.T) * biattn4::merge_blocks(h->Hq, p.max_splits), 32 * biattn4::kMergeWarps, 0,
                                        st, &p))
         return rc;

@@ -191,18 +191,22 @@ inline int check_device(int* dev) {
 }
 
 // A kernel of one parameter block, as a programmatic dependent of its predecessor.
-inline int launch(const void* fn, unsigned blocks, unsigned threads, size_t smem, cudaStream_t st, void* params) {
+inline int launch(const void* fn, unsigned blocks, unsigned threads, size_t smem, cudaStream_t st, void* params,
+                  unsigned cluster = 0) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster ? 2 : 1;
   void* args[1] = {params};
   if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
     cudaGetLastError();

@@ -295,6 +295,36 @@ def test_large_calls_have_the_bits_of_small_ones(Hq, Hkv, page, split):
     assert torch.equal(o[served], whole[served])
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(8, 2, 64, 12), (16, 2, 128, 16), (4, 4, 128, 5), (8, 1, 64, 16), (2, 2, 64, 64)])
+@pytest.mark.parametrize("longest", [1000, 2048])
+def test_splits_that_merge_in_clusters(Hq, Hkv, D, page, longest):
+    """Small calls of two to four splits, a block each: ragged contexts, empty places, tokens that cannot be served; the
+    bits of calls with a larger bound, which merge in a second kernel, and of a captured call."""
+    lengths = [longest, 1, 0, 512, 513, min(1025, longest), 37, 700, min(1536, longest), 2, 511, 999]
+    q, seq, pos, four, table = case(Hq, Hkv, D, page, lengths, 6)
+    att = bg.BiAttention4(Hq, Hkv, D, page)
+    o = att.run(q, seq, pos, *four, table, longest - 1)
+    assert att.device_error() == bg.BI_GEMM_OK
+    assert torch.equal(o, att.run(q, seq, pos, *four, table, 9000))
+    for t, n in enumerate(lengths):
+        assert torch.equal(att.run(q[t:t + 1], seq[t:t + 1], pos[t:t + 1], *four, table, longest - 1)[0], o[t]), t
+    want, a, e, total = attention64(q, seq, pos, four, table, page, att.scale, 1.0, 1.0)
+    assert ((o.double() - want).abs() <= tolerance(want, a, e, total, D)).all()
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(o)
+    with torch.cuda.graph(graph):
+        att.run(q, seq, pos, *four, table, longest - 1, o=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, o)
+    seq2, pos2 = seq.clone(), pos.clone()
+    seq2[0], pos2[7] = -3, longest
+    got = att.run(q, seq2, pos2, *four, table, longest - 1)
+    assert att.device_error() == bg.BI_GEMM_ERR_INVALID_ARG
+    served = torch.tensor([t for t in range(len(lengths)) if t not in (0, 7)], device="cuda")
+    assert torch.equal(got[served], o[served])
+
+
 def test_many_tokens_of_few_requests():
     """More tokens than one launch serves, several of one request at consecutive positions, empty places between."""
     Hq, Hkv, D, page = 8, 2, 64, 16
