@@ -143,7 +143,7 @@ int bi_attention_get_device_error(bi_attention_t h, void* stream);
 
 int bi_attention_get_config(bi_attention_t h, bi_attention_config* c);
 
-/* Release the handle and, behind everything that the device has queued, its workspace (NULL is a no-op).  Not to
+/* Release the handle and, behind everything that its device has queued, its workspace (NULL is a no-op).  Not to
  * be called while a stream is being captured. */
 int bi_attention_destroy(bi_attention_t h);
 

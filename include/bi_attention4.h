@@ -97,7 +97,7 @@ int bi_attention4_get_device_error(bi_attention4_t h, void* stream);
 
 int bi_attention4_get_config(bi_attention4_t h, bi_attention4_config* c);
 
-/* Release the handle and, behind everything that the device has queued, its workspace (NULL is a no-op).  Not to
+/* Release the handle and, behind everything that its device has queued, its workspace (NULL is a no-op).  Not to
  * be called while a stream is being captured. */
 int bi_attention4_destroy(bi_attention4_t h);
 

@@ -178,7 +178,7 @@ int bi_gemm_run_noalloc(bi_gemm_t h, const void* x, int64_t M, const void* W,
  * output is then undefined), or BI_GEMM_ERR_CUDA if synchronisation failed. */
 int bi_gemm_get_device_error(bi_gemm_t h, void* stream);
 
-/* Release the handle, its status word and its workspace (synchronises the device first).
+/* Release the handle, its status word and its workspace (synchronises its device first, whichever is current).
  * NULL is accepted. */
 int bi_gemm_destroy(bi_gemm_t h);
 

@@ -99,7 +99,7 @@ int bi_prompt_get_device_error(bi_prompt_t h, void* stream);
 
 int bi_prompt_get_config(bi_prompt_t h, bi_prompt_config* c);
 
-/* Release the handle and, behind everything that the device has queued, its workspace (NULL is a no-op).  Not to
+/* Release the handle and, behind everything that its device has queued, its workspace (NULL is a no-op).  Not to
  * be called while a stream is being captured. */
 int bi_prompt_destroy(bi_prompt_t h);
 

@@ -1787,8 +1787,8 @@ BI_GEMM_API int bi_attention_get_config(bi_attention_t h, bi_attention_config* c
 
 BI_GEMM_API int bi_attention_destroy(bi_attention_t h) {
   if (!h) return BI_GEMM_OK;
-  h->ws.release();
-  h->shared_ws.release();
+  h->ws.release(h->device);
+  h->shared_ws.release(h->device);
   if (h->d_status) cudaFree(h->d_status);
   delete h;
   return BI_GEMM_OK;

@@ -1085,7 +1085,7 @@ BI_GEMM_API int bi_attention4_get_config(bi_attention4_t h, bi_attention4_config
 
 BI_GEMM_API int bi_attention4_destroy(bi_attention4_t h) {
   if (!h) return BI_GEMM_OK;
-  h->ws.release();
+  h->ws.release(h->device);
   if (h->d_status) cudaFree(h->d_status);
   delete h;
   return BI_GEMM_OK;

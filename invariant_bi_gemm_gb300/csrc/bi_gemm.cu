@@ -26,6 +26,7 @@
 
 #include "../../include/bi_gemm.h"
 #include "bi_gemm_kernel.cuh"
+#include "workspace.cuh"
 
 #ifndef BI_GEMM_API
 #define BI_GEMM_API extern "C" __attribute__((visibility("default")))
@@ -509,10 +510,10 @@ BI_GEMM_API int bi_gemm_get_device_error(bi_gemm_t h, void* stream) {
 
 BI_GEMM_API int bi_gemm_destroy(bi_gemm_t h) {
   if (!h) return BI_GEMM_OK;
-  cudaDeviceSynchronize();
-  if (h->ws) cudaFree(h->ws);
-  if (h->d_status) cudaFree(h->d_status);
-  cudaGetLastError();
+  bigemm::behind(h->device, [h] {
+    if (h->ws) cudaFree(h->ws);
+    if (h->d_status) cudaFree(h->d_status);
+  });
   delete h;
   return BI_GEMM_OK;
 }

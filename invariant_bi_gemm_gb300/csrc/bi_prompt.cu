@@ -1037,7 +1037,7 @@ BI_GEMM_API int bi_prompt_get_config(bi_prompt_t h, bi_prompt_config* c) {
 
 BI_GEMM_API int bi_prompt_destroy(bi_prompt_t h) {
   if (!h) return BI_GEMM_OK;
-  h->ws.release();
+  h->ws.release(h->device);
   if (h->d_status) cudaFree(h->d_status);
   delete h;
   return BI_GEMM_OK;
