@@ -737,9 +737,13 @@ bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, i
   f.rows = 128;
   if (M > big4::kFewCols && units() > h->sms) return false;
   while (f.rows > 32 && units() < h->sms / 2) f.rows /= 2;
+  // (nvfp4 with fp32 results and 32 columns: two stages of two CTAs an SM do not fit, one CTA is taken)
   per_sm = units() > h->sms && f.cols <= 32 ? 2 : 1;
-  smem = h->K > 4 * big4::kStageK ? big4::few_layout(f, h->nv, h->f32, per_sm, 4, 3) : 0;
-  if (!smem) smem = big4::few_layout(f, h->nv, h->f32, per_sm, 2, 2);
+  for (smem = 0;; per_sm = 1) {
+    if (h->K > 4 * big4::kStageK) smem = big4::few_layout(f, h->nv, h->f32, per_sm, 4, 3);
+    if (!smem) smem = big4::few_layout(f, h->nv, h->f32, per_sm, 2, 2);
+    if (smem || per_sm == 1) break;
+  }
   return smem > 0;
 }
 

@@ -276,6 +276,25 @@ BI_CTL_API int bi_ctl_gemm4_stall(bi_gemm4_t h, const void* x, const void* sx, i
   return gemm4_run(h, x, sx, M, w, sw, alpha, y, stream, 1, timeout_ns);
 }
 
+BI_CTL_API int bi_ctl_gemm4_form(int64_t K, int64_t N, int32_t format, int32_t out_f32, int32_t sms, int64_t M,
+                                 int32_t* per_sm, int32_t* stages, int32_t* slots) {
+  if (K <= 0 || N <= 0 || sms <= 0 || M <= 0 || !per_sm || !stages || !slots) return BI_GEMM_ERR_INVALID_ARG;
+  bi_gemm4 h;
+  h.K = K;
+  h.N = N;
+  h.nv = format == BI_NVFP4;
+  h.f32 = out_f32 != 0;
+  h.sms = sms;
+  big4::FewParams f;
+  std::memset(&f, 0, sizeof(f));
+  int ctas = 0, smem = 0;
+  const bool few = few_choice(&h, M, f, ctas, smem);
+  *per_sm = few ? ctas : 0;
+  *stages = few ? f.stages : 0;
+  *slots = few ? f.slots : 0;
+  return few ? f.rows : 0;
+}
+
 BI_CTL_API int bi_ctl_gemm4_get_device_error(bi_gemm4_t h, void* stream) { return bi_gemm4_get_device_error(h, stream); }
 
 BI_CTL_API int bi_ctl_gemm4_destroy(bi_gemm4_t h) { return bi_gemm4_destroy(h); }

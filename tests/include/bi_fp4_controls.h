@@ -22,6 +22,10 @@ int bi_ctl_gemm4_run(bi_gemm4_t h, const void* x, const void* sx, int64_t M, con
                      void* y, void* stream);
 int bi_ctl_gemm4_stall(bi_gemm4_t h, const void* x, const void* sx, int64_t M, const void* w, const void* sw, float alpha,
                        void* y, uint64_t timeout_ns, void* stream);
+/* What a product of M rows runs as on a device of `sms` SMs, without touching one: rows of w a CTA in the form of smaller
+ * tiles, and its CTAs an SM, stages and slots a stage; 0 in the form of CTA pairs. */
+int bi_ctl_gemm4_form(int64_t K, int64_t N, int32_t format, int32_t out_f32, int32_t sms, int64_t M, int32_t* per_sm,
+                      int32_t* stages, int32_t* slots);
 int bi_ctl_gemm4_get_device_error(bi_gemm4_t h, void* stream);
 int bi_ctl_gemm4_destroy(bi_gemm4_t h);
 
