@@ -81,7 +81,9 @@ int bi_qkrope_run(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride,
  * tensor scales k_scale and v_scale (in [2^-64, 2^64], else BI_GEMM_ERR_INVALID_ARG) and go to the slot's rows of
  * k_codes, v_codes [num_pages, page_size, Hkv, D / 2] and k_scales, v_scales [num_pages, page_size, Hkv, D / 16]
  * (uint8, 16-byte aligned).  So the cache holds the quantised rows of the one that bi_qkrope_run would fill, bit
- * for bit.  Two tokens of one call on the same slot leave it with pieces of either. */
+ * for bit.  Two tokens of one call on the same slot leave it with pieces of either.
+ * A token with q_pos[t] = -1, whatever its q_seq, is an empty place of a padded batch, as bi_attention4_run has it:
+ * nothing is appended, its q_out row stays as it was, and no error is reported (bi_qkrope_run reports one). */
 int bi_qkrope_run4(bi_qkrope_t h, const void* qkv, int64_t T, int64_t qkv_stride, const void* gq, const void* gk,
                    const float* cos_sin, int64_t num_positions, const int32_t* q_seq, const int32_t* q_pos,
                    void* k_codes, void* k_scales, void* v_codes, void* v_scales, float k_scale, float v_scale,

@@ -1037,7 +1037,8 @@ class BiQkRope:
     def run4(self, qkv, gq, gk, cos_sin, q_seq, q_pos, k_codes, k_scales, v_codes, v_scales, page_table,
              k_scale: float = 1.0, v_scale: float = 1.0, q_out=None, stream=None):
         """run() into a cache in 4 bits (BiAttention4's): keys and values quantised with the tensor scales k_scale
-        and v_scale, the codes and scales that BiQuant4 "nvfp4" gives the rows that run() would store."""
+        and v_scale, the codes and scales that BiQuant4 "nvfp4" gives the rows that run() would store.  A token at -1 is
+        an empty place: nothing is appended, its row of q_out is left as it was (undefined in a new one)."""
         index, T, stride, wq, wk, positions, q_out = self._rows(qkv, gq, gk, cos_sin, q_seq, q_pos, q_out, stream)
         pages, seqs, per = _check_cache4(k_codes, k_scales, v_codes, v_scales, page_table, self._page_shape, index)
         rc = self._run4(self.handle, qkv.data_ptr(), T, stride, wq, wk, cos_sin.data_ptr(), positions, q_seq.data_ptr(),

@@ -261,8 +261,10 @@ struct Lane {
   }
 };
 
-// The cache slot of a token, -1 (and an error) where it has none.
+// The cache slot of a token, -1 where it has none: an error but for an empty place of a batch for a cache in 4 bits.
+template <bool kFour>
 __device__ __forceinline__ int64_t slot_of(const Params& p, int32_t b, int32_t pos) {
+  if (kFour && pos == -1) return -1;
   if (b < 0 || b >= p.B || pos < 0 || pos >= p.num_positions || int64_t(pos / p.page_size) >= p.max_pages) {
     atomicOr(p.status, kErrInput);
     return -1;
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kFour ? 3 : 4) qkrope_kernel(const P
   };
   load(g);
   const int32_t pos = p.q_pos[t];
-  const int64_t slot = slot_of(p, p.q_seq[t], pos);
+  const int64_t slot = slot_of<kFour>(p, p.q_seq[t], pos);
   if (slot >= 0) ln.angles(p.cs + int64_t(pos) * p.rot);
   // The loop is uniform over a lane group, not over a warp: a shuffle names its group's lanes.
   for (int h0 = g;; h0 += kHeads * groups) {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kThreads + 32, kFour ? 3 : 4) qkrope_ring_kern
       int32_t pos = -1;
       if (mine < p.T) {
         pos = p.q_pos[mine];
-        slot = slot_of(p, p.q_seq[mine], pos);
+        slot = slot_of<kFour>(p, p.q_seq[mine], pos);
       }
       for (int k = 0; k < 32 && t0 + k * step < p.T; ++k) {
         const int64_t t = t0 + k * step, sl = __shfl_sync(0xFFFFFFFFu, slot, k);
