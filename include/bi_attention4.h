@@ -80,7 +80,8 @@ int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t
                       int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
                       int64_t max_pos, void* o, void* stream);
 
-/* Workspace bytes a run with T tokens and the bound max_pos needs (0: none). */
+/* Workspace bytes a run with T tokens and the bound max_pos needs (0: none, where the bound leaves one split or the
+ * splits' blocks merge among themselves). */
 int bi_attention4_workspace_size(bi_attention4_t h, int64_t T, int64_t max_pos, uint64_t* bytes);
 
 /* k_out, v_out bf16 [n, page_size, num_kv_heads, head_dim]: the values of pages[i] (int32 [n], 4-byte aligned),

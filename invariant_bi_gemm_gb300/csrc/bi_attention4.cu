@@ -851,6 +851,7 @@ struct bi_attention4 {
   float scale = 0.0f, k_scale = 1.0f, v_scale = 1.0f;
   int device = 0, max_ctas = 0, smem = 0;
   int sms = 0, group_ctas = 0, group_smem = 0;   // of the blocks of kGroup heads (0: they are not for this shape)
+  int cluster_ctas[2] = {0, 0};                  // resident blocks in clusters of two and of four
   uint32_t* d_status = nullptr;
   biattn_tc::Workspace ws;
 };
@@ -889,9 +890,27 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
   // 4600 344 / 285, 64 of 4096 81 / 73, 128 of them at G = 8 186 / 167.  Rows of fewer or shorter heads gain nothing: 4 of 128
   // 51 / 53, 8 of 64 29 / 32.
   const bool grouped = head_dim == 128 && num_kv_heads >= 8 && num_kv_heads % biattn4::kGroup == 0;
-  int smem = 0, ctas = 0, group_smem = 0, group_ctas = 0, cluster_smem = 0, cluster_ctas = 0;
+  auto clusters = [&](int smem, int S, int& ctas) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(unsigned(S));
+    cfg.blockDim = dim3(biattn4::kThreads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(S);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, biattn4::attn_of(int(head_dim), int(G), 0), &cfg) != cudaSuccess) return false;
+    ctas = n * S;
+    return true;
+  };
+  int smem = 0, ctas = 0, group_smem = 0, group_ctas = 0, cluster_smem = 0, unused = 0, cluster_ctas[2] = {0, 0};
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !ready(1, smem, ctas) ||
-      !ready(0, cluster_smem, cluster_ctas) || (grouped && !ready(biattn4::kGroup, group_smem, group_ctas))) {
+      !ready(0, cluster_smem, unused) || !clusters(cluster_smem, 2, cluster_ctas[0]) ||
+      !clusters(cluster_smem, 4, cluster_ctas[1]) || (grouped && !ready(biattn4::kGroup, group_smem, group_ctas))) {
     cudaGetLastError();
     return BI_GEMM_ERR_CUDA;
   }
@@ -912,6 +931,8 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
   h->sms = sms;
   h->group_ctas = group_ctas;
   h->group_smem = group_smem;
+  h->cluster_ctas[0] = cluster_ctas[0];
+  h->cluster_ctas[1] = cluster_ctas[1];
   if (cudaMalloc(&h->d_status, sizeof(uint32_t)) != cudaSuccess ||
       cudaMemset(h->d_status, 0, sizeof(uint32_t)) != cudaSuccess) {
     cudaGetLastError();
@@ -925,14 +946,35 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
 
 namespace {
 
+// How a launch of T tokens and `splits` splits at most runs.
+struct Form4 {
+  int HB;                  // KV heads of a block
+  int32_t cluster;         // blocks of a cluster, whose splits merge there (0: none, the merge kernel does)
+  int64_t blocks;
+};
+Form4 form4_of(const bi_attention4* h, int64_t T, int64_t splits) {
+  const int64_t units = T * splits;
+  // (us, a block a head / four: 8 x 4096, 512 heads' units, 17.9 / 17.5; 1 x 16384, 256 units, 13.8 / 15.7; 1 x 700 8.9 / 14.4)
+  const int HB = h->group_ctas && units * h->Hkv >= 3 * h->sms ? biattn4::kGroup : 1, across = h->Hkv / HB;
+  // Clusters of two or four splits' blocks, where they run in one round: no second kernel.  us, without / with: 1 x 700 8.9 /
+  // 7.9, 1 x 2000 9.3 / 8.3, 16 x 1000 14.1 / 11.9, 100 x 1000 at 8/1 heads 15.3 / 11.0; of eight: 1 x 4096 9.3 / 9.0, but 4 x 4096
+  // 12.6 / 13.7.
+  const int64_t S = splits <= 2 ? 2 : 4;
+  if (HB == 1 && splits > 1 && splits <= 4 && T * h->Hkv * S <= h->cluster_ctas[S / 4]) return {1, int32_t(S), T * h->Hkv * S};
+  const int64_t chains = std::min<int64_t>(units, std::max(1, (HB == 1 ? h->max_ctas : h->group_ctas) / across));
+  return {HB, 0, chains * across};
+}
+
 struct Layout4 {
   int64_t splits;
   size_t part, total;      // bytes of the partial sums, and with the references and sums behind them
 };
 Layout4 layout4_of(const bi_attention4* h, int64_t T, int64_t max_pos) {
   Layout4 w{max_pos / h->split + 1, 0, 0};
-  if (w.splits > 1) {
-    const size_t slots = size_t(std::min<int64_t>(T, biattn4::kTokens)) * h->Hkv * size_t(w.splits) * h->G;
+  // (a call's first launch is its largest: where that merges in clusters, all do)
+  const int64_t first = std::min<int64_t>(T, biattn4::kTokens);
+  if (w.splits > 1 && !form4_of(h, first, w.splits).cluster) {
+    const size_t slots = size_t(first) * h->Hkv * size_t(w.splits) * h->G;
     w.part = slots * h->D * sizeof(float);
     w.total = w.part + slots * 2 * sizeof(float);
   }
@@ -1004,23 +1046,16 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
     p.o = static_cast<uint16_t*>(o) + t0 * h->Hq * h->D;
     p.q_seq = q_seq + t0;
     p.q_pos = q_pos + t0;
-    const int64_t units = int64_t(p.T) * w.splits;
-    // (us, a block a head / four: 8 x 4096, 512 heads' units, 17.9 / 17.5; 1 x 16384, 256 units, 13.8 / 15.7; 1 x 700 8.9 / 14.4)
-    const int HB = h->group_ctas && units * h->Hkv >= 3 * h->sms ? biattn4::kGroup : 1, across = h->Hkv / HB;
-    const int64_t chains = std::min<int64_t>(units, std::max(1, (HB == 1 ? h->max_ctas : h->group_ctas) / across));
-    // Clusters of two or four splits' blocks, where they run in one round: no second kernel.  us, without / with: 1 x 700 8.9 /
-    // 7.9, 1 x 2000 9.3 / 8.3, 16 x 1000 14.1 / 11.9, 100 x 1000 at 8/1 heads 15.3 / 11.0; of eight: 1 x 4096 9.3 / 9.0, but 4 x 4096
-    // 12.6 / 13.7.
-    const int64_t S = w.splits <= 2 ? 2 : 4, blocks = int64_t(p.T) * h->Hkv * S;
-    const bool cluster = HB == 1 && w.splits > 1 && w.splits <= 4 && blocks <= h->max_ctas;
-    p.cluster = cluster ? int32_t(S) : 0;
-    if (const int rc = bifp4::launch(biattn4::attn_of(h->D, h->G, cluster ? 0 : HB), unsigned(cluster ? blocks : chains * across),
-                                     biattn4::kThreads * HB, size_t(HB == 1 ? h->smem : h->group_smem), st, &p,
-                                     unsigned(p.cluster)))
+    const Form4 f = form4_of(h, p.T, w.splits);
+    p.cluster = f.cluster;
+    if (const int rc = bifp4::launch(biattn4::attn_of(h->D, h->G, f.cluster ? 0 : f.HB), unsigned(f.blocks),
+                                     biattn4::kThreads * f.HB, size_t(f.HB == 1 ? h->smem : h->group_smem), st, &p,
+                                     unsigned(f.cluster)))
       return rc;
-    if (w.splits > 1 && !cluster)
-      if (const int rc = bifp4::launch(biattn4::merge_of(h->D), unsigned(p.T) * biattn4::merge_blocks(h->Hq, p.max_splits), 32 * biattn4::kMergeWarps, 0,
-                                       st, &p))
+    if (w.splits > 1 && !f.cluster)
+      if (const int rc = bifp4::launch(biattn4::merge_of(h->D),
+                                       unsigned(p.T) * biattn4::merge_blocks(h->Hq, p.max_splits),
+                                       32 * biattn4::kMergeWarps, 0, st, &p))
         return rc;
   }
   return BI_GEMM_OK;
