@@ -63,8 +63,8 @@ typedef struct {
 
 /* Create a handle.  Requirements (else BI_GEMM_ERR_UNSUPPORTED): head_dim 64 or 128; num_q_heads /
  * num_kv_heads in {1, 2, 4, 8}; num_q_heads <= 4096; page_size 1 .. 2^20; split_size (0 = 512) a multiple of
- * 128 up to 4096; an sm_103 device.  scale finite and > 0, k_scale and v_scale in [2^-64, 2^64] (else
- * BI_GEMM_ERR_INVALID_ARG).  Checks on the arguments come before any CUDA call.  *out is NULL on failure. */
+ * 128 up to 4096; an sm_103 device.  scale finite and > 0, k_scale and v_scale in [2^-64, 2^64], scale k_scale log2(e)
+ * below 2^128 (else BI_GEMM_ERR_INVALID_ARG).  Checks on the arguments come before any CUDA call.  *out is NULL on failure. */
 int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
                          int64_t page_size, float scale, float k_scale, float v_scale, int64_t split_size);
 

@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -381,10 +382,11 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
       for (int i = 0; i < D / 8; ++i)
         qf[i] = pack_f16x2(__uint_as_float(qf[i] << 16) * up, __uint_as_float(qf[i] & 0xFFFF0000u) * up);
       // the factors of the heads whose scores this lane has
-      // (above zero, so that a hidden position's -inf stays one)
+      // (above zero, so that a hidden position's -inf stays one, and finite, so that a difference of zero stays one: queries
+      // beyond 2^116 / c whose large elements meet keys of zero)
 #pragma unroll
       for (int j = 0; j < HEADS; ++j)
-        fac[j] = fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4 * j), p.c), 1e-45f);
+        fac[j] = fminf(fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4 * j), p.c), 1e-45f), FLT_MAX);
     }
     // (the reference m is a product's sum as it comes from the MMA; the difference to it is taken before the factor, so
     // that it is exact near the reference however large the scores are)
@@ -856,12 +858,20 @@ struct bi_attention4 {
   biattn_tc::Workspace ws;
 };
 
+namespace {
+
+// The factor from a key's product with a query to the exponent of its weight.
+double factor4(float scale, float k_scale) { return double(scale) * double(k_scale) * 1.4426950408889634; }
+
+}  // namespace
+
 BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
                                      int64_t page_size, float scale, float k_scale, float v_scale, int64_t split_size) {
   if (!out) return BI_GEMM_ERR_INVALID_ARG;
   *out = nullptr;
   auto fine = [](float s) { return s >= 0x1p-64f && s <= 0x1p64f; };
-  if (!std::isfinite(scale) || scale <= 0.0f || !fine(k_scale) || !fine(v_scale)) return BI_GEMM_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.0f || !fine(k_scale) || !fine(v_scale) || factor4(scale, k_scale) > FLT_MAX)
+    return BI_GEMM_ERR_INVALID_ARG;
   if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 || split_size < 0)
     return BI_GEMM_ERR_INVALID_ARG;
   const int64_t split = split_size ? split_size : biattn4::kDefaultSplit;
@@ -1038,7 +1048,7 @@ BI_GEMM_API int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, c
   while ((1 << log2) < h->page_size) ++log2;
   p.page_shift = log2;
   p.page_mul = uint32_t((uint64_t(1) << (30 + log2)) / uint64_t(h->page_size) + 1);
-  p.c = float(double(h->scale) * double(h->k_scale) * 1.4426950408889634);
+  p.c = float(factor4(h->scale, h->k_scale));
   p.v_scale = h->v_scale;
   for (int64_t t0 = 0; t0 < T; t0 += biattn4::kTokens) {
     p.T = int32_t(std::min<int64_t>(biattn4::kTokens, T - t0));

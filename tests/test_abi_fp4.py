@@ -105,3 +105,14 @@ def test_the_tests_own_format():
     t = ref.to_tiles(s)
     for r, c in ((0, 0), (31, 3), (32, 4), (127, 7), (128, 0), (199, 5)):
         assert t[r // 128, c // 4, r % 32, r // 32 % 4, c % 4] == s[r, c]
+
+
+@pytest.mark.parametrize("scale,ks,fine", [(2.0 ** 100, 2.0 ** 64, False), (3e38, 1.0, False), (2.0 ** 64, 2.0 ** 64, False),
+                                           (2.0 ** 63, 2.0 ** 64, True), (2e38, 1.0, True), (1e-38, 2.0 ** -64, True)])
+def test_attention4_create_refuses_factors_beyond_fp32(scale, ks, fine):
+    """scale k_scale log2(e), the factor of every score, has to be a finite fp32 number; scales that it is for get as far
+    as the device (none here, or a handle)."""
+    h = ctypes.c_void_p()
+    rc = bg.library().bi_attention4_create(ctypes.byref(h), 32, 8, 128, 16, scale, ks, 1.0, 0)
+    assert (rc != INVALID) == fine
+    bg.library().bi_attention4_destroy(h)
