@@ -85,7 +85,7 @@ int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t
 int bi_attention4_workspace_size(bi_attention4_t h, int64_t T, int64_t max_pos, uint64_t* bytes);
 
 /* k_out, v_out bf16 [n, page_size, num_kv_heads, head_dim]: the values of pages[i] (int32 [n], 4-byte aligned),
- * i = 0 .. n - 1, for operators that read a bf16 cache (bi_prompt_run over a cached context: page i of the
+ * i = 0 .. n - 1, rounded as bi_quant4_expand rounds them, for operators that read a bf16 cache (bi_prompt_run over a cached context: page i of the
  * result is page i of its table).  An entry of -1 leaves page i as it was; any other outside [0, num_pages)
  * does too and is reported by bi_attention4_get_device_error.  One kernel; allocates nothing. */
 int bi_attention4_expand(bi_attention4_t h, const void* k_codes, const void* k_scales, const void* v_codes,

@@ -67,7 +67,8 @@ int bi_quant4_scale_bytes(bi_quant4_t h, int64_t M, uint64_t* bytes);
 int bi_quant4_run(bi_quant4_t h, const void* x, int64_t M, int64_t x_stride, void* codes, void* scales,
                   void* stream);
 
-/* y bf16 [M, K]: the values of codes and scales times the handle's tensor scale, rounded once. */
+/* y bf16 [M, K]: the values of codes and scales times the handle's tensor scale: scale g, then code times that, in fp32
+ * (exact where g is a power of two), then to bf16. */
 int bi_quant4_expand(bi_quant4_t h, const void* codes, const void* scales, int64_t M, void* y, void* stream);
 
 int bi_quant4_get_config(bi_quant4_t h, bi_quant4_config* c);

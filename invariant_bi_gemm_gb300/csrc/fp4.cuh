@@ -72,8 +72,10 @@ struct Scale {
   bool zero;          // every code is 0
   bool wide;          // above the largest scale: a quotient may be far above the codes'
 };
-// q = x / d for a d whose reciprocal r is known to an ulp: the product with r, corrected by its remainder (exact).  What
-// is representable comes out exact, so that ties are seen as such.
+// q = x / d for a d whose reciprocal r is known to an ulp: the product with r, corrected by its remainder, which is exact
+// (Markstein's correction of a quotient).  With a rounded reciprocal it is the rounded quotient; with one an ulp off it
+// still lies on the rounded quotient's side of every tie between codes, but for one divisor's mantissa (2^24 - 1, whose
+// rcp.approx is the reciprocal that does not miss: the tests have the proof and that divisor).
 __device__ __forceinline__ float divided(float x, float d, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
@@ -165,7 +167,7 @@ __device__ __forceinline__ float scale_value(uint32_t byte, float g) {
   return byte == kNanE8M0 ? __uint_as_float(0x7FC00000u)
                           : __uint_as_float(byte ? byte << 23 : 1u << 22);
 }
-// Eight codes times their scale, as bf16 pairs (rounded once).
+// Eight codes times their scale, as bf16 pairs (in fp32 and then bf16).
 __device__ __forceinline__ void values_bf16(uint32_t codes, float scale, uint32_t* out) {
   uint32_t h[4];
   values8(codes, h);
