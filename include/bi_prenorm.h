@@ -55,7 +55,8 @@ int bi_prenorm_run(bi_prenorm_t h, const void* x, int64_t M, const void* W, floa
 
 int bi_prenorm_get_config(bi_prenorm_t h, bi_prenorm_config* c);
 
-/* Release the handle and its workspace (NULL is a no-op). */
+/* Release the handle and, behind everything that its device has queued, its workspace (NULL is a no-op).  Not to
+ * be called while a stream is being captured. */
 int bi_prenorm_destroy(bi_prenorm_t h);
 
 #ifdef __cplusplus

@@ -23,6 +23,7 @@
 
 #include "../../include/bi_prenorm.h"
 #include "ptx.cuh"
+#include "workspace.cuh"
 
 #ifndef BI_GEMM_API
 #define BI_GEMM_API extern "C" __attribute__((visibility("default")))
@@ -329,7 +330,7 @@ BI_GEMM_API int bi_prenorm_get_config(bi_prenorm_t h, bi_prenorm_config* c) {
 
 BI_GEMM_API int bi_prenorm_destroy(bi_prenorm_t h) {
   if (!h) return BI_GEMM_OK;
-  if (h->ws) cudaFree(h->ws);
+  if (h->ws) bigemm::behind(h->device, [h] { cudaFree(h->ws); });
   delete h;
   return BI_GEMM_OK;
 }
