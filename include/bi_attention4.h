@@ -21,8 +21,8 @@
  *
  * Batch invariance: the keys 0..p are cut at multiples of split_size, a split is four interleaved sequences of
  * 32 positions in ascending order, merged in order, and the n splits are merged in ascending order, above 16 of them
- * as eight consecutive groups of ceil(n / 8) and then group by group: all of it a function of p.  o[t] is a function of q[t], p and
- * K_b, V_b[0..p], bit for bit, whatever else the call holds.  Arithmetic: codes times scales exactly in f16;
+ * as eight consecutive groups of ceil(n / 8) and then group by group: all of it a function of p.  o[t] is a function
+ * of q[t], p and K_b, V_b[0..p], bit for bit, whatever else the call holds.  Arithmetic: codes times scales exactly in f16;
  * queries in f16 relative to their head's largest element (a bf16 element at least 2^-25 of it is exact, any
  * other within 2^-36 of it); scores on the tensor cores in fp32; weights exp2 of the score less a running
  * reference of the maximum (moved when passed by more than 8), summed in fp32, rounded to f16 (11 bits) for
@@ -64,7 +64,8 @@ typedef struct {
 /* Create a handle.  Requirements (else BI_GEMM_ERR_UNSUPPORTED): head_dim 64 or 128; num_q_heads /
  * num_kv_heads in {1, 2, 4, 8}; num_q_heads <= 4096; page_size 1 .. 2^20; split_size (0 = 512) a multiple of
  * 128 up to 4096; an sm_103 device.  scale finite and > 0, k_scale and v_scale in [2^-64, 2^64], scale k_scale log2(e)
- * below 2^128 (else BI_GEMM_ERR_INVALID_ARG).  Checks on the arguments come before any CUDA call.  *out is NULL on failure. */
+ * below 2^128 (else BI_GEMM_ERR_INVALID_ARG).  Checks on the arguments come before any CUDA call.  *out is NULL on
+ * failure. */
 int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_kv_heads, int64_t head_dim,
                          int64_t page_size, float scale, float k_scale, float v_scale, int64_t split_size);
 
@@ -73,8 +74,9 @@ int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, int64_t num_
  * order when it needs more than before (BI_GEMM_ERR_OOM if that fails; BI_GEMM_ERR_SCRATCH_LIMIT in a call
  * being captured into a graph that needs more than an earlier call left; a graph stays valid when later
  * calls grow it), then queues the attention and, where max_pos leaves more than one split and the
- * splits' blocks do not merge among themselves, the merge (of each 512 tokens).  num_pages x page_size x num_kv_heads below 2^32 - 1, max_pos below 2^30 (else
- * BI_GEMM_ERR_UNSUPPORTED).  Asynchronous; only the blocks of a cluster, which run together, wait for one another. */
+ * splits' blocks do not merge among themselves, the merge (of each 512 tokens).  num_pages x page_size x num_kv_heads
+ * below 2^32 - 1, max_pos below 2^30 (else BI_GEMM_ERR_UNSUPPORTED).  Asynchronous; only the blocks of a cluster, which
+ * run together, wait for one another. */
 int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t* q_seq, const int32_t* q_pos,
                       const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
                       int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int64_t max_pages,
@@ -85,9 +87,9 @@ int bi_attention4_run(bi_attention4_t h, const void* q, int64_t T, const int32_t
 int bi_attention4_workspace_size(bi_attention4_t h, int64_t T, int64_t max_pos, uint64_t* bytes);
 
 /* k_out, v_out bf16 [n, page_size, num_kv_heads, head_dim]: the values of pages[i] (int32 [n], 4-byte aligned),
- * i = 0 .. n - 1, rounded as bi_quant4_expand rounds them, for operators that read a bf16 cache (bi_prompt_run over a cached context: page i of the
- * result is page i of its table).  An entry of -1 leaves page i as it was; any other outside [0, num_pages)
- * does too and is reported by bi_attention4_get_device_error.  One kernel; allocates nothing. */
+ * i = 0 .. n - 1, rounded as bi_quant4_expand rounds them, for operators that read a bf16 cache (bi_prompt_run over a
+ * cached context: page i of the result is page i of its table).  An entry of -1 leaves page i as it was; any other
+ * outside [0, num_pages) does too and is reported by bi_attention4_get_device_error.  One kernel; allocates nothing. */
 int bi_attention4_expand(bi_attention4_t h, const void* k_codes, const void* k_scales, const void* v_codes,
                          const void* v_scales, int64_t num_pages, const int32_t* pages, int64_t n, void* k_out,
                          void* v_out, void* stream);

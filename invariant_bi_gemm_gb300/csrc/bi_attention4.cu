@@ -15,26 +15,30 @@
 //           operands agree, so lane t takes a quarter of a row, whole 16-byte chunks: eight codes become four f16
 //           pairs by cvt, times their block's scale (exact: 2 + 4 significant bits).
 //   weights P = 2^(s - m + 7) in fp32, rounded to f16 and transposed in registers (movmatrix).
-//   values  O^T += V^T P^T.  A code pair that cvt makes is two dimensions at one position, and the MMA sums over the pair.
-//           G <= 4: a head has two columns, and a weight stands in one half of its pair and zero in the other, so that one
-//           column gets the even dimensions and the other the odd ones (32 dimensions on the 16 rows, 8 positions deep).
+//   values  O^T += V^T P^T.  A code pair that cvt makes is two dimensions at one position, and the MMA sums over the
+//           pair.  G <= 4: a head has two columns, and a weight stands in one half of its pair and zero in the other, so
+//           that one column gets the even dimensions and the other the odd ones (32 dimensions on the 16 rows, 8
+//           positions deep).
 //           G = 8: the codes of two positions are interleaved before cvt, a pair is one dimension at two positions (16
 //           dimensions, 16 positions deep).  Lane g owns D / 8 consecutive dimensions either way.
 //
-// Tensor cores of the fifth generation would need codes and scales of the query too, of which eight bits would take four
-// products, and a value's block scales lie along the dimensions where the MMA's lie along the sum.
+// Tensor cores of the fifth generation would need codes and scales of the query too, of which eight bits would take
+// four products, and a value's block scales lie along the dimensions where the MMA's lie along the sum.
 //
 // Bound (256 contexts of 1000 to 8192, 32/8 heads of 128, 265 us, 4.9 TB/s, 0.72 of the bytes' rate): the loads alone
-// take nine tenths of it, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head a tenth less), the
-// arithmetic alone eight tenths at 270 instructions a sixteen of positions and head, the merge's launch 12 us.  One token (700
-// positions: 7.9 us, 8.9 before its two splits merged in a cluster): the latencies of a launch, a lookup, a chain of steps.
-// Tried: a loading warp for eight computing ones, a warp a head (largest call 355 when this form took 391, but 96
-// registers, and one token's 700 positions 18.6 us instead of 9.3); three blocks an SM with rings of three steps (no
-// change); splits of 256 positions (433 against 391, one token's 32768 21.4 against 18.5) and 1024 (379, 21.6).
-// For the blocks of four heads (285): one loading warp and rings that the heads share 421, four loading warps 333 (a stage
-// waits for the slowest of four heads); pairs of such blocks with a cluster barrier a unit 325.  The last block to arrive
-// merging a token's splits, instead of a second kernel: nothing for one token, 343 for the largest call (registers).
-// Splits joined in the block that runs them, the merge left with what chains cut: 1 % less.
+// take nine tenths of it, a head's 64 bytes of every 512-byte row (the same bytes in rows of one KV head a tenth
+// less), the arithmetic alone eight tenths at 270 instructions a sixteen of positions and head, the merge's launch 12
+// us.  One token (700 positions: 7.9 us, 8.9 before its two splits merged in a cluster): the latencies of a launch, a
+// lookup, a chain of steps.  Between them no unit is full: 133 ragged contexts at 16/2 heads of 64 (27.5 us) have
+// ALUs at 37 % and DRAM at 26 % of their peaks with 23 % of the warps, 32 contexts of 1000 (16.6 us) 32 % and 27 %,
+// 128 of 4096 at 64/8 heads (156 us) 42 % and 54 %.  Tried: a loading warp for eight computing ones, a warp a head
+// (largest call 355 when this form took 391, but 96 registers, and one token's 700 positions 18.6 us instead of 9.3);
+// three blocks an SM with rings of three steps (no change); splits of 256 positions (433 against 391, one token's
+// 32768 21.4 against 18.5) and 1024 (379, 21.6).  For the blocks of four heads (285): one loading warp and rings that
+// the heads share 421, four loading warps 333 (a stage waits for the slowest of four heads); pairs of such blocks
+// with a cluster barrier a unit 325.  The last block to arrive merging a token's splits, instead of a second kernel:
+// nothing for one token, 343 for the largest call (registers).  Splits joined in the block that runs them, the merge
+// left with what chains cut: 1 % less.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -178,8 +182,8 @@ __device__ __forceinline__ int32_t splits_of(const Params& p, int32_t b, int32_t
   return bad ? 0 : pos / p.split + 1;
 }
 
-// kTwin: up to four heads, each on two of the MMA's columns.  kCluster: a block a split, the splits of a (token, KV head) in
-// a cluster that merges them.
+// kTwin: up to four heads, each on two of the MMA's columns.  kCluster: a block a split, the splits of a (token, KV
+// head) in a cluster that merges them.
 template <int D, bool kTwin, int HB, bool kCluster>
 __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(const Params p) {
   using C = Cfg<D, HB>;
@@ -194,8 +198,8 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
   const int group = HB == 1 ? 0 : int(threadIdx.x) / kThreads;   // its KV head of the block's
   const int tid = int(threadIdx.x) - group * kThreads, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (The next kernel is not asked for early: with its blocks waiting beside these, 133 ragged contexts at 16/2 heads of 64
-  // took 31 us instead of 27, 16 of 4096 at 32/8 of 128 26.8 instead of 26.0, and none less.)
+  // (The next kernel is not asked for early: with its blocks waiting beside these, 133 ragged contexts at 16/2 heads
+  // of 64 took 31 us instead of 27, 16 of 4096 at 32/8 of 128 26.8 instead of 26.0, and none less.)
   // first unit (of one KV head) of every token
   int32_t carry = 0;
   for (int base = 0; base < p.T; base += C::THREADS) {
@@ -382,8 +386,8 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
       for (int i = 0; i < D / 8; ++i)
         qf[i] = pack_f16x2(__uint_as_float(qf[i] << 16) * up, __uint_as_float(qf[i] & 0xFFFF0000u) * up);
       // the factors of the heads whose scores this lane has
-      // (above zero, so that a hidden position's -inf stays one, and finite, so that a difference of zero stays one: queries
-      // beyond 2^116 / c whose large elements meet keys of zero)
+      // (above zero, so that a hidden position's -inf stays one, and finite, so that a difference of zero stays one:
+      // queries beyond 2^116 / c whose large elements meet keys of zero)
 #pragma unroll
       for (int j = 0; j < HEADS; ++j)
         fac[j] = fminf(fmaxf(__fmul_rn(__shfl_sync(0xFFFFFFFFu, down, 8 * t4 + 4 * j), p.c), 1e-45f), FLT_MAX);
@@ -515,7 +519,10 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[h][j] = ex2(__fmaf_rn(__fsub_rn(s[h][j], m[j & (HEADS - 1)]), fac[j & (HEADS - 1)], kLift));
+          for (int j = 0; j < 4; ++j) {
+            const int k = j & (HEADS - 1);
+            s[h][j] = ex2(__fmaf_rn(__fsub_rn(s[h][j], m[k]), fac[k], kLift));
+          }
           l[0] += s[h][0] + s[h][2];
           l[HEADS - 1] += s[h][1] + s[h][3];
           const uint32_t b0 = transposed(pack_f16x2(s[h][0], s[h][1])), b1 = transposed(pack_f16x2(s[h][2], s[h][3]));
@@ -665,16 +672,17 @@ __global__ void __launch_bounds__(kThreads * HB, kBlocksPerSm / HB) attn_kernel(
   }
 }
 
-// Up to kSolo splits of a token's query head are summed in ascending order by one warp (of a cluster's block, or here, eight heads a block: a block a
-// head took 51 us for 8192 heads of 9 splits); more of them as eight consecutive groups of ceil(n / 8) by the
-// warps of a block, ascending, the groups added in order.  n depends on the token's position alone.
+// Up to kSolo splits of a token's query head are summed in ascending order by one warp (of a cluster's block, or here,
+// eight heads a block: a block a head took 51 us for 8192 heads of 9 splits); more of them as eight consecutive
+// groups of ceil(n / 8) by the warps of a block, ascending, the groups added in order.  n depends on the token's
+// position alone.
 constexpr int kSolo = 16;
 
-// Splits s0 .. s1 - 1 of the head whose first is slot0, in order: the largest reference and, relative to it, the sum of the
-// sums and this lane's dimensions.
+// Splits s0 .. s1 - 1 of the head whose first is slot0, in order: the largest reference and, relative to it, the sum
+// of the sums and this lane's dimensions.
 template <int D>
-__device__ __forceinline__ void sum_splits(const Params& p, int64_t slot0, int32_t s0, int32_t s1, int lane, float& M, float& L,
-                                           float (&A)[D / 32]) {
+__device__ __forceinline__ void sum_splits(const Params& p, int64_t slot0, int32_t s0, int32_t s1, int lane, float& M,
+                                           float& L, float (&A)[D / 32]) {
   constexpr int PER = D / 32, BATCH = 8;
   const float2* mlp = reinterpret_cast<const float2*>(p.ml) + slot0;
   M = -INFINITY;
@@ -895,10 +903,10 @@ BI_GEMM_API int bi_attention4_create(bi_attention4_t* out, int64_t num_q_heads, 
     ctas = per_sm * sms;
     return true;
   };
-  // Blocks of four KV heads, for calls of many units (bi_attention4_run has their number): their warps read neighbouring
-  // 64-byte pieces of long rows at about the same time.  us, 8 KV heads of 128 (a block a head / four): 256 contexts of
-  // 4600 344 / 285, 64 of 4096 81 / 73, 128 of them at G = 8 186 / 167.  Rows of fewer or shorter heads gain nothing: 4 of 128
-  // 51 / 53, 8 of 64 29 / 32.
+  // Blocks of four KV heads, for calls of many units (form4_of has their number): their warps read
+  // neighbouring 64-byte pieces of long rows at about the same time.  us, 8 KV heads of 128 (a block a head / four):
+  // 256 contexts of 4600 324 / 272, 64 of 4096 77 / 70, 128 of them at G = 8 167 / 156.  Rows of fewer or shorter
+  // heads gain nothing: 4 of 128 51 / 53, 8 of 64 29 / 32.
   const bool grouped = head_dim == 128 && num_kv_heads >= 8 && num_kv_heads % biattn4::kGroup == 0;
   auto clusters = [&](int smem, int S, int& ctas) {
     cudaLaunchConfig_t cfg;
@@ -964,13 +972,15 @@ struct Form4 {
 };
 Form4 form4_of(const bi_attention4* h, int64_t T, int64_t splits) {
   const int64_t units = T * splits;
-  // (us, a block a head / four: 8 x 4096, 512 heads' units, 17.9 / 17.5; 1 x 16384, 256 units, 13.8 / 15.7; 1 x 700 8.9 / 14.4)
+  // (us, a block a head / four: 32 x 1000, 512 heads' units, 16.3 / 16.6; 8 x 4096, 512 too, 17.8 / 17.0; 1 x 16384,
+  // 256, 14.3 / 15.6; 4 x 4096, 256 too, 13.1 / 15.6; 1 x 700 7.9 / 14.4)
   const int HB = h->group_ctas && units * h->Hkv >= 3 * h->sms ? biattn4::kGroup : 1, across = h->Hkv / HB;
-  // Clusters of two or four splits' blocks, where they run in one round: no second kernel.  us, without / with: 1 x 700 8.9 /
-  // 7.9, 1 x 2000 9.3 / 8.3, 16 x 1000 14.1 / 11.9, 100 x 1000 at 8/1 heads 15.3 / 11.0; of eight: 1 x 4096 9.3 / 9.0, but 4 x 4096
-  // 12.6 / 13.7.
+  // Clusters of two or four splits' blocks, where they run in one round: no second kernel.  us, without / with: 1 x
+  // 700 8.9 / 7.9, 1 x 2000 9.3 / 8.1, 16 x 1000 14.5 / 11.8, 100 x 1000 at 8/1 heads 15.9 / 11.4; of eight: 1 x 4096
+  // 9.3 / 9.0, but 4 x 4096 12.6 / 13.7.
   const int64_t S = splits <= 2 ? 2 : 4;
-  if (HB == 1 && splits > 1 && splits <= 4 && T * h->Hkv * S <= h->cluster_ctas[S / 4]) return {1, int32_t(S), T * h->Hkv * S};
+  if (HB == 1 && splits > 1 && splits <= 4 && T * h->Hkv * S <= h->cluster_ctas[S / 4])
+    return {1, int32_t(S), T * h->Hkv * S};
   const int64_t chains = std::min<int64_t>(units, std::max(1, (HB == 1 ? h->max_ctas : h->group_ctas) / across));
   return {HB, 0, chains * across};
 }

@@ -7,9 +7,12 @@
 // function of K alone.  fp32 accumulators in tensor memory; alpha and the rounding to bf16 come once, at the end.
 //
 // Two forms share the work, with the same bits.  Many rows: CTA pairs take 256 x 256 of y, bound by the tensor pipe:
-// 8192 x 4096 x 14336 (M, K, N) in 155 us with nvfp4 (6.2 PFLOP/s) and 150 with mxfp4 (6.4), where four times the
-// measured bf16 rate allows 125; 2048 rows 43 us.  Few rows: the operands change places, bound by the latency of one
-// CTA's chain of stages: one row by 4096 x 14336 in 8.2 us where its bytes take 4.9, 64 rows by 14336 x 4096 in 13.0.
+// 8192 x 4096 x 14336 (M, K, N) in 154 us with nvfp4 (6.2 PFLOP/s) and 149 with mxfp4 (6.4), where four times the
+// measured bf16 rate would allow 125 (the rate of these instructions by themselves was not measured, nor that of their
+// form of 96 elements); thousands of calls on end, at the power limit and 1770 MHz, 167 and 158.  2048 rows 43 us.  Few
+// rows: the operands change places, bound by the latency of one CTA's chain of stages: one row by 4096 x 14336 in 8.1
+// us where its bytes take 4.9, 64 rows by 14336 x 4096 (mxfp4) in 13.0.  By a vocabulary, bound by the bytes of w: 1,
+// 32 and 128 rows by 4096 x 128256 in 47, 49 and 56 us (0.94, 0.92 and 0.86 of the measured copy).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -106,14 +109,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // ------------------------------------------------------------------ the form for many rows
 //
-// A pair of CTAs, persistent; warp 0 of each loads its half of the codes (128-byte swizzle rows of 256 elements) and the
-// scales (tiles as they lie in memory, as boxes of 512-byte rows), the leader's warp 1 moves the scales to tensor memory
-// (tcgen05.cp) and issues the products, eight warps store.  One accumulator: 256 columns, and five stages' scales behind
-// it; the eight warps read it at once and hand it back before they round and store.  us for 8192 x 4096 x 14336, nvfp4:
-// 310 with the issuing thread chosen by its lane number, 206 with the scales stored to tensor memory by four warps, 157
-// with the thread named by elect.sync (operands in uniform registers) and the copies back; without copies of scales
-// 145, without loads 134.  Waits: every lane polls, backing off by the clock (one lane alone 228, suspended waits 210,
-// nanosleep 300); a wait with a cluster-wide acquire in the issuing thread 380.
+// A pair of CTAs, persistent; warp 0 of each loads its half of the codes (128-byte swizzle rows of 256 elements) and
+// the scales (tiles as they lie in memory, as boxes of 512-byte rows), the leader's warp 1 moves the scales to tensor
+// memory (tcgen05.cp) and issues the products, eight warps store.  One accumulator: 256 columns, and five stages'
+// scales behind it; the eight warps read it at once and hand it back before they round and store.  us for 8192 x 4096
+// x 14336, nvfp4: 310 with the issuing thread chosen by its lane number, 206 with the scales stored to tensor memory
+// by four warps, 157 with the thread named by elect.sync (operands in uniform registers) and the copies back; without
+// copies of scales 145, without loads 134.  Waits: every lane polls, backing off by the clock (one lane alone 228,
+// suspended waits 210, nanosleep 300); a wait with a cluster-wide acquire in the issuing thread 380.
 
 template <bool kNv_, bool kF32_>
 struct Wide {
@@ -369,8 +372,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
 // ------------------------------------------------------------------ the form for few rows
 //
 // The operands change places: rows of w on the 128 rows of the MMA, up to 128 rows of x on its columns, so that a CTA
-// alone takes 32, 64 or 128 columns of y and as many of them as there are SMs share the reading of w.  The sums have the
-// wide form's bits: an element is the same sequence of 64-element products, and neither the place of its row and
+// alone takes 32, 64 or 128 columns of y and as many of them as there are SMs share the reading of w.  The sums have
+// the wide form's bits: an element is the same sequence of 64-element products, and neither the place of its row and
 // column in an instruction nor the instruction's extent enters (compared over every shape that the tests run).
 //
 // A CTA's R rows of w take the MMA's rows that they have in their tile of 128 (so that a tile of scales serves as it
@@ -378,10 +381,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) __cluster_dims__(2, 1, 1)
 //
 // A stage is two or four slots of 256 elements of K.  A turn of the loading loop costs about 250 clocks besides its
 // copies, of 28 each; one of the issuing loop about 160 besides its products, of 40 each (128 rows of 32 bytes from
-// shared memory, however few columns meet them), and its scales' copies, of 11: for 1 x 14336 x 4096 these, not the loads,
-// take the time (9.7 us without the products, 13.5 with them; two loading warps 8.0 and 13.7).  Four slots are taken
-// where three such stages fit: 13.5 -> 12.3 us there, 64 x 14336 x 4096 14.3 -> 13.2, 16 x 32768 x 2048 30.8 -> 27.2; with
-// two stages 64 x 4096 x 14336 9.4 -> 11.0, with one 1 x 512 x 4096 2.7 -> 2.9.
+// shared memory, however few columns meet them), and its scales' copies, of 11: for 1 x 14336 x 4096 these, not the
+// loads, take the time (9.7 us without the products, 13.5 with them; two loading warps 8.0 and 13.7).  Four slots are
+// taken where three such stages fit: 13.5 -> 12.3 us there, 64 x 14336 x 4096 14.3 -> 13.1 (both mxfp4; nvfp4 takes
+// 14.0 and 14.4 with them), 16 x 32768 x 2048 30.8 -> 27.3 (nvfp4); with two stages 64 x 4096 x 14336 9.4 -> 11.0,
+// with one 1 x 512 x 4096 2.7 -> 2.9.
 
 constexpr int kFewMaxStages = 8;
 constexpr int kFewCols = 128;             // rows of x at most
@@ -724,12 +728,13 @@ BI_GEMM_API int bi_gemm4_create(bi_gemm4_t* out, int64_t K, int64_t N, int32_t f
 namespace {
 
 // Whether a call of M rows takes the form for few rows, and its layout.  Both forms give the same bits.  Measured with
-// nvfp4 (us; this form in tiles of 128 x 128 against pairs of 256 x 256): 256 x 4096 x 4096 (M, K, N) 8.8 against 10.2, 512 x
-// 4096 x 4096 8.3 against 9.8, 777 x 2176 x 1000 6.7 against 7.7, 4096 x 1024 x 256 5.2 against 6.2, and with more tiles than
-// SMs 256 x 4096 x 14336 15.6 against 12.1: a call takes it where its tiles run all at once.  Fewer columns of y a CTA
-// where that leaves half the SMs without work: 300 x 4096 x 1024 8.2 with 128, 7.7 with 32; 128 x 4096 x 4096 8.7 and 7.9; 777 x 2176 x 1000 6.7
-// with 128, 6.2 with 64; and
-// two CTAs an SM for many columns and a handful of rows: 1 x 4096 x 28672 14.0 with one, 13.1 with two.
+// nvfp4 (us; this form, in tiles of 128 rows of x, against pairs of 256 x 256): 256 x 4096 x 4096 (M, K, N) 7.9 against
+// 9.8, 512 x 4096 x 4096 8.4 against 9.8, 777 x 2176 x 1000 5.7 against 7.2, 4096 x 1024 x 256 4.5 against 5.5, and
+// with more tiles than SMs 256 x 4096 x 14336 14.7 against 11.3, 2048 x 4096 x 14336 69.6 against 42.6: a call takes
+// it where its tiles run all at once.  Fewer columns of y a CTA where 128 would leave half the SMs without work: 300
+// x 4096 x 1024 7.4 with 128, 7.0 with the rule's; 128 x 4096 x 4096 8.4 and 7.6; 777 x 2176 x 1000 6.0 and 5.7, with
+// fp32 results 7.0 and 5.8.  Two CTAs an SM for many columns and a handful of rows: 1 x 4096 x 28672 14.1 with one,
+// 13.3 with two.
 bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, int& smem) {
   f.cols = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const int64_t m_tiles = (M + f.cols - 1) / f.cols;
@@ -737,7 +742,8 @@ bool few_choice(const bi_gemm4* h, int64_t M, big4::FewParams& f, int& per_sm, i
   f.rows = 128;
   if (M > big4::kFewCols && units() > h->sms) return false;
   while (f.rows > 32 && units() < h->sms / 2) f.rows /= 2;
-  // (nvfp4 with fp32 results and 32 columns: two stages of two CTAs an SM do not fit, one CTA is taken)
+  // (nvfp4 with fp32 results and 32 columns: two stages of two CTAs an SM do not fit, one CTA is taken.  17 x 4096 x
+  // 20480 13.5 us, pairs 17.2; x 128256 50.0 and 57.7)
   per_sm = units() > h->sms && f.cols <= 32 ? 2 : 1;
   for (smem = 0;; per_sm = 1) {
     if (h->K > 4 * big4::kStageK) smem = big4::few_layout(f, h->nv, h->f32, per_sm, 4, 3);

@@ -194,10 +194,11 @@ struct Lane {
   }
 
   // Head h of a token for a cache in 4 bits: queries as in `finish`; keys, rounded to bf16 as they are there, and
-  // values as E2M1 codes with a scale per sixteen, two lanes.  Bound by instructions (ALUs busy for half the time): a
-  // lane's eight neighbours come from two other lanes by shuffles, and a block's scale wants a division.  8192 tokens of 32/8
-  // heads of 128, not normalised: 37.9 us, the bf16 cache 36.6 (with norms 49.9 and 41.4); 64 tokens 2.9 and 2.7.  Three
-  // blocks an SM: with four, and a few registers spilled, 43.8 and 3.3.
+  // values as E2M1 codes with a scale per sixteen, two lanes.  A lane's eight neighbours come from two other lanes by
+  // shuffles, and a block's scale wants a division: a head is a long chain of steps, of which a warp of the ring has
+  // one at a time.  No unit is full beside it: ALUs 50 % (with norms 42), DRAM 43 % (32), 38 % of the warps.  8192
+  // tokens of 32/8 heads of 128, not normalised: 37.9 us, the bf16 cache 36.6 (with norms 49.9 and 41.4); 64 tokens
+  // 2.9 and 2.7.  Three blocks an SM: with four, and a few registers spilled, 43.8 and 3.3.
   __device__ __forceinline__ void finish4(const Params& p, int h, int64_t t, int64_t slot, bool store, uint2 a,
                                           uint2 b) const {
     if (h < p.Hq) {
@@ -489,8 +490,9 @@ BI_GEMM_API int bi_qkrope_create(bi_qkrope_t* out, int64_t num_q_heads, int64_t 
   const int ring = int(std::min<size_t>(biqkr::kMaxRing, biqkr::kRingBytes / stage));
   // warps per token: the power of two that leaves a lane group kHeads heads or fewer
   while (h->team_log2 < 3 && ((32 / (h->D / 8) * biqkr::kHeads) << h->team_log2) < heads) ++h->team_log2;
-  // (three blocks an SM leave a cache in 4 bits more room: taken where a ring would not fit else.  64/8 heads of 128, us:
-  // 1000 tokens 12.9 without, 11.3 with one, 9000 85.9 and 63.1; 32/8, where both fit, 8192 38.4 with the larger, 37.9)
+  // (three blocks an SM leave a cache in 4 bits more room: taken where a ring would not fit else.  64/8 heads of 128,
+  // us: 1000 tokens 12.9 without, 11.3 with one, 9000 85.9 and 63.1; 32/8, where both fit, 8192 38.4 with the larger,
+  // 37.9)
   const int ring4 = ring >= 3 ? ring : int(std::min<size_t>(biqkr::kMaxRing, biqkr::kRingBytes4 / stage));
   auto ready = [&](bool four, int stages, int room, int rows, int& ctas, int& from) {
     if (stages < 3) return true;
@@ -608,9 +610,9 @@ int qkrope_run(bi_qkrope* h, const void* qkv, int64_t T, int64_t qkv_stride, con
   // The ring from 40 KB of rows per resident block on, where its start is paid for (us, ring against a
   // block per token or few): 32/8 heads of 128 (12 KB a token), 1216 tokens 9.8 against 9.4, 2432 16.5
   // against 17.7, 8192 42.0 against 52.3; 16/8 of 128, 2432 11.3 against 11.2, 4096 16.9 against 17.8;
-  // 16/2 of 64, 8192 15.2 against 14.9, 12000 19.6 against 19.9.  A cache in 4 bits, from 24 KB: 32/8 of 128, 700 tokens
-  // 6.2 against 5.6, 1000 8.0 against 8.6, 2000 13.0 against 15.6; 16/8 of 128, 1500 8.3 against 8.0, 2000 10.7 against 11.6;
-  // 16/2 of 64, 4000 8.3 against 7.9, 6000 11.1 against 11.9.
+  // 16/2 of 64, 8192 15.2 against 14.9, 12000 19.6 against 19.9.  A cache in 4 bits, from 24 KB: 32/8 of 128, 700
+  // tokens 6.2 against 5.6, 1000 8.0 against 8.6, 2000 13.0 against 15.6; 16/8 of 128, 1500 8.3 against 8.0, 2000
+  // 10.7 against 11.6; 16/2 of 64, 4000 8.3 against 7.9, 6000 11.1 against 11.9.
   const int from = four ? h->ring_from4 : h->ring_from;
   const bool ring = from > 0 && T >= from;
   p.ring = four ? h->ring4 : h->ring;

@@ -2,11 +2,12 @@
 // quantisation of include/bi_fp4.h.
 //
 // Bound: HBM bandwidth (2 bytes an element read, 0.53 or 0.56 written) and, close behind, the ALUs, which are busy for
-// 60 % of the time: 14336 x 4096 take 25 us with mxfp4 (5.9 TB/s), 30 with nvfp4 (whose scales want a division each, and
-// whose elements another), and 24 back (6.1 TB/s).  Two pieces a thread: one 27.5 and 34, four 26 and 40.  A thread has sixteen consecutive
-// elements: a block of BI_NVFP4, half a block of BI_MXFP4 (the two halves meet in one shuffle).  K is a multiple of
-// 128, so the lanes that share a block, or the four scales that lie side by side in a tile and leave as one
-// 32-bit store, are always of one row, and threads run over the matrix without regard to where rows end.
+// 60 % of the time: 14336 x 4096 take 25 us with mxfp4 (5.9 TB/s), 30 with nvfp4 (whose scales want a division each,
+// and whose elements another), and 24 back (6.1 TB/s).  Two pieces a thread: one 27.5 and 34, four 26 and 40.  A
+// thread has sixteen consecutive elements: a block of BI_NVFP4, half a block of BI_MXFP4 (the two halves meet in one
+// shuffle).  K is a multiple of 128, so the lanes that share a block, or the four scales that lie side by side in a
+// tile and leave as one 32-bit store, are always of one row, and threads run over the matrix without regard to where
+// rows end.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -110,7 +111,8 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
   }
 }
 
-// Eight elements a thread, so that a warp's stores are whole lines (sixteen: 30 us for 14336 x 4096, in halves of lines).
+// Eight elements a thread, so that a warp's stores are whole lines (sixteen: 30 us for 14336 x 4096, in halves of
+// lines).
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

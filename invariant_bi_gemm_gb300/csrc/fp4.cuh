@@ -72,10 +72,10 @@ struct Scale {
   bool zero;          // every code is 0
   bool wide;          // above the largest scale: a quotient may be far above the codes'
 };
-// q = x / d for a d whose reciprocal r is known to an ulp: the product with r, corrected by its remainder, which is exact
-// (Markstein's correction of a quotient).  With a rounded reciprocal it is the rounded quotient; with one an ulp off it
-// still lies on the rounded quotient's side of every tie between codes, but for one divisor's mantissa (2^24 - 1, whose
-// rcp.approx is the reciprocal that does not miss: the tests have the proof and that divisor).
+// q = x / d for a d whose reciprocal r is known to an ulp: the product with r, corrected by its remainder, which is
+// exact (Markstein's correction of a quotient).  With a rounded reciprocal it is the rounded quotient; with one an
+// ulp off it still lies on the rounded quotient's side of every tie between codes, but for one divisor's mantissa
+// (2^24 - 1, whose rcp.approx is the reciprocal that does not miss: the tests have the proof and that divisor).
 __device__ __forceinline__ float divided(float x, float d, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
@@ -132,8 +132,8 @@ __device__ __forceinline__ uint32_t most_of(const uint32_t* w, int n) {
   return max(m & 0xFFFFu, m >> 16);
 }
 
-// Eight bf16 values (four words) -> their codes.  A wide block's quotients are out of the range that `divided` corrects:
-// its values are clamped first (nvfp4, 14336 x 4096: 30.1 us, with a division in its place 32.4).
+// Eight bf16 values (four words) -> their codes.  A wide block's quotients are out of the range that `divided`
+// corrects: its values are clamped first (nvfp4, 14336 x 4096: 30.1 us, with a division in its place 32.4).
 template <bool kNv>
 __device__ __forceinline__ uint32_t quantise8(const uint32_t* w, const Scale& s) {
   if (s.zero && kNv) {

@@ -9,9 +9,9 @@
 
 namespace bigemm {
 
-// Gives a handle's memory back (`free_all`) behind everything that its device has queued: cudaFree does not wait for the
-// users of memory that came from cudaMallocAsync, and a handle may be dropped right behind its last call, with any
-// device current.  Where the device cannot be waited for the memory stays: better lost than freed under a kernel.
+// Gives a handle's memory back (`free_all`) behind everything that its device has queued: cudaFree does not wait for
+// the users of memory that came from cudaMallocAsync, and a handle may be dropped right behind its last call, with
+// any device current.  Where the device cannot be waited for the memory stays: better lost than freed under a kernel.
 template <class F>
 void behind(int device, F&& free_all) {
   int current = device;
