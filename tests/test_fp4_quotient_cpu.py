@@ -38,9 +38,10 @@ def side(q, tie):
 
 
 def test_only_one_divisor_can_change_a_code():
-    """x has 8 bits (bf16), the divisor d 24, its reciprocal r is within an ulp of 1 / d (PTX: rcp.approx).  The quotient is
-    near a tie only for the d around x / tie.  Among all of those, the corrected quotient is on another side than the rounded one
-    for one divisor's mantissa alone, 2^24 - 1, at the tie of 1/4 and with the smaller r; test_gpu_v_fp4_quotient.py runs it."""
+    """x has 8 bits (bf16), the divisor d 24, its reciprocal r is within an ulp of 1 / d (PTX: rcp.approx).  The quotient
+    is near a tie only for the d around x / tie.  Among all of those, the corrected quotient is on another side than the
+    rounded one for one divisor's mantissa alone, 2^24 - 1, at the tie of 1/4 and with the smaller r;
+    test_gpu_v_fp4_quotient.py runs it."""
     odd = set()
     for tie in TIES:
         for m in range(128, 256):

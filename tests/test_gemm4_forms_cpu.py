@@ -27,7 +27,8 @@ def test_few_rows_take_the_smaller_tiles(kind, f32):
             for N in (8, 128, 4096, 128 * sms - 8, 128 * sms, 128 * sms + 8, 19464, 20480, 32000, 128256, 1 << 24):
                 for K in (128, 1024, 1152, 4096, 14336):
                     rows, per_sm, stages, slots = form(K, N, kind, f32, M, sms)
-                    assert rows in (32, 64, 128) and per_sm in (1, 2) and stages >= 2 and slots in (2, 4), (sms, M, N, K)
+                    fine = rows in (32, 64, 128) and per_sm in (1, 2) and stages >= 2 and slots in (2, 4)
+                    assert fine, (sms, M, N, K)
 
 
 @pytest.mark.parametrize("kind", [bg.BI_MXFP4, bg.BI_NVFP4])

@@ -1,5 +1,5 @@
-"""The product in 4 bits in every form that a call can take: each row against 64-bit sums and, between the forms, bit for
-bit.  Which form a shape takes on this device is read through the test controls."""
+"""The product in 4 bits in every form that a call can take: each row against 64-bit sums and, between the forms, bit
+for bit.  Which form a shape takes on this device is read through the test controls."""
 import pytest
 import torch
 
@@ -34,7 +34,8 @@ def check_rows(y, vx, vw, K, out):
         assert off.max() <= 0, (c, float(off.max()), int((off > 0).sum()))
 
 
-# Rows past a tile's first half, past none of it (one CTA of the last pair has no rows), more M tiles than a raster's group.
+# Rows past a tile's first half, past none of it (one CTA of the last pair has no rows), more M tiles than a raster's
+# group.
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("M,K,N", [(257, 384, 10000), (300, 2176, 10248), (513, 128, 10000), (700, 640, 16392),

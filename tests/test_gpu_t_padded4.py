@@ -14,8 +14,9 @@ def blank(t, places):
     return t
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,page,inter,T", [(32, 8, 128, 16, False, 1), (32, 8, 128, 16, False, 37), (16, 2, 64, 12, True, 90),
-                                                   (64, 8, 128, 16, False, 900), (8, 8, 64, 16, True, 14000)])
+@pytest.mark.parametrize("Hq,Hkv,D,page,inter,T", [(32, 8, 128, 16, False, 1), (32, 8, 128, 16, False, 37),
+                                                   (16, 2, 64, 12, True, 90), (64, 8, 128, 16, False, 900),
+                                                   (8, 8, 64, 16, True, 14000)])
 def test_append_leaves_empty_places_alone(Hq, Hkv, D, page, inter, T):
     """Every third place is empty, requests out of range among them: the other tokens' rows and slots are those of a
     call without the empty ones, everything else stays, and nothing is reported.  Both forms of the append."""

@@ -74,8 +74,8 @@ def test_scratch_is_what_the_call_uses(Hq, Hkv, D):
 
 # ------------------------------------------------------------------ sizes
 
-# The query's size, k_scale and the softmax's scale, whose product leaves scores of ordinary size; the last two queries
-# are below the smallest factor's range, the last one of denormals.
+# The query's size, k_scale and the softmax's scale, whose product leaves scores of ordinary size; the last two
+# queries are below the smallest factor's range, the last one of denormals.
 SIZES = [(2.0 ** 100, 2.0 ** -64, 2.0 ** -34), (2.0 ** 120, 2.0 ** -60, 2.0 ** -58), (2.0 ** -100, 2.0 ** 64, 2.0 ** 38),
          (2.0 ** 60, 2.0 ** -1, 2.0 ** -57), (2.0 ** -120, 2.0 ** 64, 2.0 ** 58), (2.0 ** -128, 2.0 ** 64, 2.0 ** 62)]
 
@@ -108,8 +108,9 @@ def planted(q, four, table, n, page, seed):
     return at
 
 
-@pytest.mark.parametrize("spread,ks,scale", [(1e30, 2.0 ** -60, None), (2.0 ** 125, 2.0 ** -40, None), (1e-30, 2.0 ** 64, 2.0 ** 50),
-                                             (64.0, 1.0, 8.0), (2.0 ** 40, 2.0 ** 40, 2.0 ** 20)])
+@pytest.mark.parametrize("spread,ks,scale", [(1e30, 2.0 ** -60, None), (2.0 ** 125, 2.0 ** -40, None),
+                                             (1e-30, 2.0 ** 64, 2.0 ** 50), (64.0, 1.0, 8.0),
+                                             (2.0 ** 40, 2.0 ** 40, 2.0 ** 20)])
 @pytest.mark.parametrize("Hq,Hkv,D", [(16, 4, 128), (8, 1, 64), (2, 2, 128)])
 def test_one_key_takes_all_of_extreme_scores(spread, ks, scale, Hq, Hkv, D):
     """A key above the others by 1e2 to 1e37: the output is its value, rounded once to bf16 (2^-8) behind fp32 steps."""
@@ -128,8 +129,8 @@ def test_one_key_takes_all_of_extreme_scores(spread, ks, scale, Hq, Hkv, D):
 
 
 def test_a_factor_beyond_fp32():
-    """Queries whose largest element meets keys of 0 and whose others, 2^-24 of it, decide: scores are finite, the factor
-    from the products to them (2^129) is not."""
+    """Queries whose largest element meets keys of 0 and whose others, 2^-24 of it, decide: scores are finite, the
+    factor from the products to them (2^129) is not."""
     Hq, Hkv, D, n = 8, 2, 64, 700
     table, pages = table_of([-(-n // 16)])
     four = random_cache(pages, 16, Hkv, D, 3, 0x30, 0x38)

@@ -1,5 +1,5 @@
-"""How handles give their device memory back, without a GPU: csrc/workspace.cuh compiled against a CUDA runtime that only
-keeps a record of its calls."""
+"""How handles give their device memory back, without a GPU: csrc/workspace.cuh compiled against a CUDA runtime that
+only keeps a record of its calls."""
 import ctypes
 import os
 import subprocess
@@ -19,7 +19,11 @@ static void note(const char* what, long n) { record += what + std::to_string(n) 
 
 extern "C" {
 cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
-cudaError_t cudaSetDevice(int d) { if (failing == 2 && d) return cudaErrorInvalidDevice; device = d; return cudaSuccess; }
+cudaError_t cudaSetDevice(int d) {
+  if (failing == 2 && d) return cudaErrorInvalidDevice;
+  device = d;
+  return cudaSuccess;
+}
 cudaError_t cudaDeviceSynchronize() {
   if (failing == 1) return cudaErrorLaunchFailure;
   note("wait", device);
